@@ -15,6 +15,7 @@
 #include <vector>
 
 #include "../../include/kivi.h"
+#include "kivi_chunk.cuh"
 #include "kivi_internal.cuh"
 
 namespace {
@@ -48,6 +49,7 @@ struct kivi_cache {
     // which then becomes current (no CTA of the append waits for another).
     int *cnt;
     int parity;
+    float *chunk_part;   // split partials of the chunk attention
     std::vector<int> T, Tqk, Tqv;   // host mirror
     DecodePlan last_plan;
     bool profiling;
@@ -133,11 +135,12 @@ kivi_status check_shape(int b, int h_kv, int d, int k_bits, int v_bits, int G, i
 
 void free_dev(kivi_cache *c) {
     KiviDev &d = c->dv;
-    void *ps[] = {d.blk, d.Kf, d.Vf, c->cnt, d.status, d.part, d.merge_ticket, d.ml};
+    void *ps[] = {d.blk, d.Kf, d.Vf, c->cnt, d.status, d.part, d.merge_ticket, d.ml, c->chunk_part};
     for (void *p : ps)
         if (p) cudaFree(p);
     memset(&d, 0, sizeof d);
     c->cnt = nullptr;
+    c->chunk_part = nullptr;
 }
 
 void point_counters(kivi_cache *c) {
@@ -185,6 +188,60 @@ kivi_status check_append_args(kivi_cache *c, const void *k, const void *v) {
     return KIVI_OK;
 }
 
+kivi_status check_window(int window, int sinks) {
+    if (window < 0 || sinks < 0) {
+        set_err("window and sinks must not be negative");
+        return KIVI_ERR_INVALID_ARG;
+    }
+    return KIVI_OK;
+}
+
+// the cache's memory is on the current device
+kivi_status check_device(const kivi_cache *c) {
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev != c->device) {
+        set_err("the cache belongs to device %s%ld, which is not current", "", c->device);
+        return KIVI_ERR_INVALID_ARG;
+    }
+    return KIVI_OK;
+}
+
+// Checks a chunk's K, V and token counts and fills a's counters (a.hq is the
+// caller's); *maxn: the most tokens of a sequence.
+kivi_status check_chunk(kivi_cache *c, const void *K, const void *V, const int32_t *n, int n_stride, ChunkArgs &a,
+                        int *maxn) {
+    if (!n || n_stride < 0) {
+        set_err("n is null or n_stride negative");
+        return KIVI_ERR_INVALID_ARG;
+    }
+    if (n_stride > (1 << 26)) {
+        set_err("n_stride above 2^26");
+        return KIVI_ERR_UNSUPPORTED;
+    }
+    *maxn = 0;
+    for (int i = 0; i < c->g.b; ++i) {
+        if (n[i] < 0 || n[i] > n_stride) {
+            set_err("n[i] outside [0, n_stride] for i = %s%ld", "", i);
+            return KIVI_ERR_INVALID_ARG;
+        }
+        a.T[i] = c->T[i];
+        a.Tqk[i] = c->Tqk[i];
+        a.Tqv[i] = c->Tqv[i];
+        a.n[i] = n[i];
+        *maxn = n[i] > *maxn ? n[i] : *maxn;
+    }
+    a.n_stride = n_stride;
+    if (*maxn > 0 && (!K || !V)) {
+        set_err("K or V is null");
+        return KIVI_ERR_INVALID_ARG;
+    }
+    if (*maxn > 0 && (!aligned16(K) || !aligned16(V))) {
+        set_err("K and V must be 16-byte aligned");
+        return KIVI_ERR_INVALID_ARG;
+    }
+    return check_device(c);
+}
+
 // host mirror of one append (item 4's lazy maintenance, then the token)
 void advance_mirror(kivi_cache *c) {
     const int R = c->g.R;
@@ -218,9 +275,10 @@ kivi_status launch_append(kivi_cache *c, const void *k, const void *v, kivi_stre
 // Plan and launch the decode kernel; units come from (T, Tqk, Tqv).
 kivi_status launch_decode(kivi_cache *c, const void *q, int h_q, void *out, kivi_stream_t stream,
                           const int *T, const int *Tqk, const int *Tqv, const char *what,
-                          const ProbsOut *po = nullptr, const FusedStep *fs = nullptr) {
+                          const ProbsOut *po = nullptr, const FusedStep *fs = nullptr,
+                          Visible vis = Visible{0, 0}) {
     DecodeUnits units;
-    DecodePlan plan = kivi_plan_decode(c->g, h_q, T, Tqk, Tqv, c->num_sms, &units, fs != nullptr);
+    DecodePlan plan = kivi_plan_decode(c->g, h_q, T, Tqk, Tqv, c->num_sms, &units, fs != nullptr, vis);
     cudaEvent_t e0 = nullptr, e1 = nullptr;
     if (c->profiling && c->nprof < kMaxProfile) {
         if ((int)c->ev.size() < 2 * (c->nprof + 1)) {
@@ -239,7 +297,7 @@ kivi_status launch_decode(kivi_cache *c, const void *q, int h_q, void *out, kivi
     int maxT = 0;
     for (int i = 0; i < c->g.b; ++i) maxT = T[i] > maxT ? T[i] : maxT;
     cudaError_t e = kivi_launch_decode(c->g, c->dv, (const __half *)q, h_q, (__half *)out, plan, units,
-                                       (cudaStream_t)stream, e0, e1, po, maxT, fs);
+                                       (cudaStream_t)stream, e0, e1, po, maxT, fs, vis);
     if (e != cudaSuccess) return fail_cuda(c, e, what);
     c->last_plan = plan;
     return KIVI_OK;
@@ -302,6 +360,56 @@ kivi_status launch_fused_step(kivi_cache *c, const void *k, const void *v, const
     return KIVI_OK;
 }
 
+// kivi_prefill_attn and kivi_prefill_attn_window
+kivi_status prefill_attn(kivi_cache_t c, const void *q, const void *K, const void *V, const int32_t *t, int t_stride,
+                         int h_q, Visible vis, void *out, kivi_stream_t stream) {
+    kivi_status s = check_handle(c);
+    if (s != KIVI_OK) return s;
+    if (vis.window > 0 && (s = check_device(c)) != KIVI_OK) return s;
+    if (c->g.G > 64 || (c->g.d != 64 && c->g.d != 128)) {
+        set_err("prefill attention supports d 64 or 128 and G <= 64");
+        return KIVI_ERR_UNSUPPORTED;
+    }
+    if (h_q < c->g.h || h_q % c->g.h != 0 || h_q / c->g.h > KIVI_MAX_QPERKV) {
+        set_err("h_q must be a multiple of h_kv, at most %s%ld times it", "", KIVI_MAX_QPERKV);
+        return KIVI_ERR_INVALID_ARG;
+    }
+    if (!t || t_stride < 0) {
+        set_err("t is null or t_stride negative");
+        return KIVI_ERR_INVALID_ARG;
+    }
+    SeqLens lens;
+    int maxt = 0;
+    for (int i = 0; i < c->g.b; ++i) {
+        if (t[i] < 0 || t[i] > t_stride) {
+            set_err("t[i] outside [0, t_stride] for i = %s%ld", "", i);
+            return KIVI_ERR_INVALID_ARG;
+        }
+        if (t[i] > c->max_tokens) {
+            set_err("t[i] above max_tokens for i = %s%ld", "", i);
+            return KIVI_ERR_CAPACITY;
+        }
+        lens.t[i] = t[i];
+        maxt = t[i] > maxt ? t[i] : maxt;
+    }
+    if (maxt > 0 && (!q || !K || !V || !out)) {
+        set_err("q, K, V or out is null");
+        return KIVI_ERR_INVALID_ARG;
+    }
+    if (maxt > 0 && (!aligned16(q) || !aligned16(K) || !aligned16(V) || !aligned16(out))) {
+        set_err("q, K, V and out must be 16-byte aligned");
+        return KIVI_ERR_INVALID_ARG;
+    }
+    cudaError_t e = kivi_launch_prefill_attn(c->g, c->dv, (const __half *)q, (const __half *)K, (const __half *)V,
+                                             (__half *)out, lens, t_stride, h_q, (cudaStream_t)stream, vis);
+    if (e != cudaSuccess) return fail_cuda(c, e, "prefill_attn");
+    for (int i = 0; i < c->g.b; ++i) {
+        c->T[i] = t[i];
+        c->Tqk[i] = t[i] - t[i] % c->g.R;
+        c->Tqv[i] = t[i] > c->g.R ? t[i] - c->g.R : 0;
+    }
+    return KIVI_OK;
+}
 
 }  // namespace
 
@@ -341,6 +449,7 @@ kivi_status kivi_cache_create(int b, int h_kv, int d, int k_bits, int v_bits, in
     }
     c->magic = kMagic;
     c->poisoned = false;
+    c->chunk_part = nullptr;
     c->max_tokens = max_tokens;
     c->profiling = false;
     c->nprof = 0;
@@ -374,8 +483,10 @@ kivi_status kivi_cache_create(int b, int h_kv, int d, int k_bits, int v_bits, in
         {(void **)&dv.part, bh * KIVI_MAX_QPERKV * g.smax * (d + 4) * 4},
         {(void **)&dv.merge_ticket, bh * 4 * 4},
         {(void **)&dv.ml, bh * KIVI_MAX_QPERKV * 2 * 4},
+        {(void **)&c->chunk_part, kivi_chunk_partial_floats(d, c->num_sms) * 4},
     };
     for (auto &r : reqs) {
+        if (r.bytes == 0) continue;
         e = cudaMalloc(r.p, r.bytes);
         if (e == cudaSuccess) e = cudaMemset(*r.p, 0, r.bytes);
         if (e != cudaSuccess) {
@@ -470,51 +581,16 @@ kivi_status kivi_prefill(kivi_cache_t c, const void *K, const void *V, const int
 kivi_status kivi_prefill_attn(kivi_cache_t c, const void *q, const void *K, const void *V, const int32_t *t,
                               int t_stride, int h_q, void *out, kivi_stream_t stream) {
     g_err[0] = 0;
-    kivi_status s = check_handle(c);
+    return prefill_attn(c, q, K, V, t, t_stride, h_q, Visible{0, 0}, out, stream);
+}
+
+kivi_status kivi_prefill_attn_window(kivi_cache_t c, const void *q, const void *K, const void *V, const int32_t *t,
+                                     int t_stride, int h_q, int window, int sinks, void *out,
+                                     kivi_stream_t stream) {
+    g_err[0] = 0;
+    kivi_status s = check_window(window, sinks);
     if (s != KIVI_OK) return s;
-    if (c->g.G > 64 || (c->g.d != 64 && c->g.d != 128)) {
-        set_err("prefill attention supports d 64 or 128 and G <= 64");
-        return KIVI_ERR_UNSUPPORTED;
-    }
-    if (h_q < c->g.h || h_q % c->g.h != 0 || h_q / c->g.h > KIVI_MAX_QPERKV) {
-        set_err("h_q must be a multiple of h_kv, at most %s%ld times it", "", KIVI_MAX_QPERKV);
-        return KIVI_ERR_INVALID_ARG;
-    }
-    if (!t || t_stride < 0) {
-        set_err("t is null or t_stride negative");
-        return KIVI_ERR_INVALID_ARG;
-    }
-    SeqLens lens;
-    int maxt = 0;
-    for (int i = 0; i < c->g.b; ++i) {
-        if (t[i] < 0 || t[i] > t_stride) {
-            set_err("t[i] outside [0, t_stride] for i = %s%ld", "", i);
-            return KIVI_ERR_INVALID_ARG;
-        }
-        if (t[i] > c->max_tokens) {
-            set_err("t[i] above max_tokens for i = %s%ld", "", i);
-            return KIVI_ERR_CAPACITY;
-        }
-        lens.t[i] = t[i];
-        maxt = t[i] > maxt ? t[i] : maxt;
-    }
-    if (maxt > 0 && (!q || !K || !V || !out)) {
-        set_err("q, K, V or out is null");
-        return KIVI_ERR_INVALID_ARG;
-    }
-    if (maxt > 0 && (!aligned16(q) || !aligned16(K) || !aligned16(V) || !aligned16(out))) {
-        set_err("q, K, V and out must be 16-byte aligned");
-        return KIVI_ERR_INVALID_ARG;
-    }
-    cudaError_t e = kivi_launch_prefill_attn(c->g, c->dv, (const __half *)q, (const __half *)K, (const __half *)V,
-                                             (__half *)out, lens, t_stride, h_q, (cudaStream_t)stream);
-    if (e != cudaSuccess) return fail_cuda(c, e, "prefill_attn");
-    for (int i = 0; i < c->g.b; ++i) {
-        c->T[i] = t[i];
-        c->Tqk[i] = t[i] - t[i] % c->g.R;
-        c->Tqv[i] = t[i] > c->g.R ? t[i] - c->g.R : 0;
-    }
-    return KIVI_OK;
+    return prefill_attn(c, q, K, V, t, t_stride, h_q, Visible{window, sinks}, out, stream);
 }
 
 kivi_status kivi_append(kivi_cache_t c, const void *k, const void *v, kivi_stream_t stream) {
@@ -534,6 +610,86 @@ kivi_status kivi_decode_attn(kivi_cache_t c, const void *q, int h_q, void *out,
     s = check_decode_args(c, q, h_q, out);
     if (s != KIVI_OK) return s;
     return launch_decode(c, q, h_q, out, stream, c->T.data(), c->Tqk.data(), c->Tqv.data(), "decode_attn");
+}
+
+kivi_status kivi_decode_attn_window(kivi_cache_t c, const void *q, int h_q, int window, int sinks, void *out,
+                                    kivi_stream_t stream) {
+    g_err[0] = 0;
+    kivi_status s = check_handle(c);
+    if (s != KIVI_OK) return s;
+    s = check_window(window, sinks);
+    if (s != KIVI_OK) return s;
+    s = check_decode_args(c, q, h_q, out);
+    if (s != KIVI_OK) return s;
+    s = check_device(c);
+    if (s != KIVI_OK) return s;
+    return launch_decode(c, q, h_q, out, stream, c->T.data(), c->Tqk.data(), c->Tqv.data(), "decode_attn_window",
+                         nullptr, nullptr, Visible{window, sinks});
+}
+
+kivi_status kivi_chunk_attn(kivi_cache_t c, const void *q, const void *K, const void *V, const int32_t *n,
+                            int n_stride, int h_q, int window, int sinks, void *out, kivi_stream_t stream) {
+    g_err[0] = 0;
+    kivi_status s = check_handle(c);
+    if (s != KIVI_OK) return s;
+    if (c->g.d != 64 && c->g.d != 128) {
+        set_err("chunk attention supports d 64 or 128");
+        return KIVI_ERR_UNSUPPORTED;
+    }
+    if (h_q < c->g.h || h_q % c->g.h != 0 || h_q / c->g.h > KIVI_MAX_QPERKV) {
+        set_err("h_q must be a multiple of h_kv, at most %s%ld times it", "", KIVI_MAX_QPERKV);
+        return KIVI_ERR_INVALID_ARG;
+    }
+    s = check_window(window, sinks);
+    if (s != KIVI_OK) return s;
+    ChunkArgs a;
+    int maxn = 0;
+    s = check_chunk(c, K, V, n, n_stride, a, &maxn);
+    if (s != KIVI_OK) return s;
+    if (maxn == 0) return KIVI_OK;
+    if (!q || !out) {
+        set_err("q or out is null");
+        return KIVI_ERR_INVALID_ARG;
+    }
+    if (!aligned16(q) || !aligned16(out)) {
+        set_err("q and out must be 16-byte aligned");
+        return KIVI_ERR_INVALID_ARG;
+    }
+    a.hq = h_q;
+    a.vis = Visible{window, sinks};
+    cudaError_t e = kivi_launch_chunk_attn(c->g, c->dv, (const __half *)q, (const __half *)K, (const __half *)V,
+                                           (__half *)out, a, c->chunk_part, c->num_sms, (cudaStream_t)stream);
+    if (e != cudaSuccess) return fail_cuda(c, e, "chunk_attn");
+    return KIVI_OK;
+}
+
+kivi_status kivi_append_chunk(kivi_cache_t c, const void *K, const void *V, const int32_t *n, int n_stride,
+                              kivi_stream_t stream) {
+    g_err[0] = 0;
+    kivi_status s = check_handle(c);
+    if (s != KIVI_OK) return s;
+    ChunkArgs a;
+    int maxn = 0;
+    s = check_chunk(c, K, V, n, n_stride, a, &maxn);
+    if (s != KIVI_OK) return s;
+    for (int i = 0; i < c->g.b; ++i)
+        if (n[i] > c->max_tokens - c->T[i]) {
+            set_err("sequence %s%ld would exceed max_tokens", "", i);
+            return KIVI_ERR_CAPACITY;
+        }
+    if (maxn == 0) return KIVI_OK;
+    int *nxt = c->cnt + (size_t)(1 - c->parity) * 3 * c->g.b;
+    cudaError_t e = kivi_launch_append_chunk(c->g, c->dv, (const __half *)K, (const __half *)V, a, nxt,
+                                             (cudaStream_t)stream);
+    if (e != cudaSuccess) return fail_cuda(c, e, "append_chunk");
+    c->parity ^= 1;
+    point_counters(c);
+    for (int i = 0; i < c->g.b; ++i) {
+        c->Tqk[i] = chunk_tqk(a.T[i], a.Tqk[i], n[i], c->g.R);
+        c->Tqv[i] = chunk_tqv(a.T[i], a.Tqv[i], n[i], c->g.R);
+        c->T[i] += n[i];
+    }
+    return KIVI_OK;
 }
 
 kivi_status kivi_decode_attn_probs(kivi_cache_t c, const void *q, int h_q, void *out, float *probs,

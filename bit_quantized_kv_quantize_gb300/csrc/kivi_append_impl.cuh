@@ -11,6 +11,66 @@
 #pragma once
 #include "kivi_internal.cuh"
 
+// Quantize one staged round of keys of slice (i, j): tokens [ta, tb) (whole
+// groups, at most CH from the round's aligned start cs), token tau in row
+// tau - cs of xs (shared, [CH][d]); their groups' scales and zeros, then the
+// code words of the round's blocks, whose earlier tokens (below Tqk, the
+// quantized ones so far) keep their codes and whose later ones are zero.
+// s_ks: 3 (CH / G) d floats of shared memory.  G, d and the block's word
+// count are powers of two: indices are shifts and masks.  Called by every
+// thread of a CTA, the rows visible to all; the caller synchronizes before
+// it reuses the rows.
+__device__ __forceinline__ void pack_key_round(const KiviGeom &g, const KiviDev &dv, int i, int j, const __half *xs,
+                                               float *s_ks, int cs, int CH, int ta, int tb, int Tqk) {
+    const int d = g.d, G = g.G;
+    const int lgG = __ffs(G) - 1, lgd = __ffs(d) - 1, lgw = __ffs(g.kc_blk) - 1;
+    const int cph = 16 / g.kbits;
+    float *s_kz = s_ks + (CH / G) * d;
+    float *s_kr = s_kz + (CH / G) * d;
+    const int gr0 = ta >> lgG, ngr = (tb - ta) >> lgG;
+    for (int e = threadIdx.x; e < ngr * d; e += blockDim.x) {
+        const int gr = e >> lgd, c = e & (d - 1);
+        const __half *col = xs + (size_t)((gr0 + gr) * G - cs) * d + c;
+        float mn = __half2float(col[0]), mx = mn;
+        for (int k = 1; k < G; ++k) {
+            const float x = __half2float(col[(size_t)k * d]);
+            mn = fminf(mn, x);
+            mx = fmaxf(mx, x);
+        }
+        const QParams p = qparams(mn, mx, g.kbits);
+        ksz_store(g, dv.blk, i, j, gr0 + gr, c, p.s16, p.z16);
+        s_ks[e] = p.sf;
+        s_kz[e] = p.zf;
+        s_kr[e] = p.sf == 0.0f ? 0.0f : __frcp_rn(p.sf);
+    }
+    __syncthreads();
+    const int kb0 = cs / KIVI_KBLK, nkb = CH / KIVI_KBLK;
+    for (int e = threadIdx.x; e < nkb * g.kc_blk; e += blockDim.x) {
+        const int kb = kb0 + (e >> lgw), wb = e & (g.kc_blk - 1);
+        const int t0 = kb * KIVI_KBLK;
+        if (t0 >= tb || t0 + KIVI_KBLK <= ta) continue;   // no window token in this block
+        const KWord kw = kword_decode(wb, g.kbits);
+        uint32_t *kc = kc_words(g, dv.blk, i, j, kb);
+        const uint32_t old = t0 < Tqk ? kc[wb] : 0u;   // earlier tokens' codes stay
+        uint32_t word = 0;
+        for (int half = 0; half < 2; ++half) {
+            const int c = kw.c0 + half;
+            for (int r = 0; r < cph; ++r) {
+                const int tau = t0 + 8 * (kw.pos0 + r) + kw.g;
+                const int sh = 16 * half + r * g.kbits;
+                if (tau < Tqk) {
+                    word |= old & (((1u << g.kbits) - 1u) << sh);
+                } else if (tau < tb) {   // later tokens: zero
+                    const int sz = (((tau >> lgG) - gr0) << lgd) + c;
+                    word |= qcode_rcp(__half2float(xs[((tau - cs) << lgd) + c]), s_ks[sz], s_kz[sz],
+                                      s_kr[sz], g.kbits) << sh;
+                }
+            }
+        }
+        kc[wb] = word;
+    }
+}
+
 // Append the token (knew, vnew: fp16 [b][h][d]) to slice (i, j) whose
 // counters are T, Tqk, Tqv (in range).  Called by every thread of a CTA (any
 // block size); the counters themselves are left to the caller.
@@ -42,20 +102,15 @@ __device__ __forceinline__ void append_pair(const KiviGeom &g, const KiviDev &dv
         // (flush_round_tokens: whole groups and 64-token blocks): the
         // round's window rows come into shared memory with one round trip,
         // then its groups get their scale and zero and its blocks their
-        // code words.  Shared memory (dynamic, flush_smem_bytes): rows
-        // [CH][d] fp16, then s, z and RN(1 / s) [CH/G][d] fp32.  G, d and
-        // the block's word count are powers of two: indices are shifts and
-        // masks.
+        // code words (pack_key_round).  Shared memory (dynamic,
+        // flush_smem_bytes): rows [CH][d] fp16, then s, z and RN(1 / s)
+        // [CH/G][d] fp32.
         extern __shared__ __align__(16) unsigned char flush_smem[];
         const int G = g.G, CH = flush_round_tokens(g);
         const int CA = G > KIVI_KBLK ? G : KIVI_KBLK;   // alignment of a round's start
-        const int lgG = __ffs(G) - 1, lgd = __ffs(d) - 1, lgw = __ffs(g.kc_blk) - 1;
         __half *xs = reinterpret_cast<__half *>(flush_smem);
         float *s_ks = reinterpret_cast<float *>(flush_smem + (size_t)CH * d * 2);
-        float *s_kz = s_ks + (CH / G) * d;
-        float *s_kr = s_kz + (CH / G) * d;
         const int nv = d / 8;   // 16-byte pieces per row
-        const int cph = 16 / g.kbits;
         for (int cs = Tqk / CA * CA; cs < Tqk + R; cs += CH) {
             const int ta = max(cs, Tqk), tb = min(cs + CH, Tqk + R);   // multiples of G
             for (int e = threadIdx.x; e < (tb - ta) * nv; e += blockDim.x) {
@@ -64,48 +119,7 @@ __device__ __forceinline__ void append_pair(const KiviGeom &g, const KiviDev &dv
                     reinterpret_cast<const uint4 *>(kf + (size_t)(tau - Tqk) * d)[c8];
             }
             __syncthreads();
-            const int gr0 = ta >> lgG, ngr = (tb - ta) >> lgG;
-            for (int e = threadIdx.x; e < ngr * d; e += blockDim.x) {
-                const int gr = e >> lgd, c = e & (d - 1);
-                const __half *col = xs + (size_t)((gr0 + gr) * G - cs) * d + c;
-                float mn = __half2float(col[0]), mx = mn;
-                for (int k = 1; k < G; ++k) {
-                    const float x = __half2float(col[(size_t)k * d]);
-                    mn = fminf(mn, x);
-                    mx = fmaxf(mx, x);
-                }
-                const QParams p = qparams(mn, mx, g.kbits);
-                ksz_store(g, dv.blk, i, j, gr0 + gr, c, p.s16, p.z16);
-                s_ks[e] = p.sf;
-                s_kz[e] = p.zf;
-                s_kr[e] = p.sf == 0.0f ? 0.0f : __frcp_rn(p.sf);
-            }
-            __syncthreads();
-            const int kb0 = cs / KIVI_KBLK, nkb = CH / KIVI_KBLK;
-            for (int e = threadIdx.x; e < nkb * g.kc_blk; e += blockDim.x) {
-                const int kb = kb0 + (e >> lgw), wb = e & (g.kc_blk - 1);
-                const int t0 = kb * KIVI_KBLK;
-                if (t0 >= tb || t0 + KIVI_KBLK <= ta) continue;   // no window token in this block
-                const KWord kw = kword_decode(wb, g.kbits);
-                uint32_t *kc = kc_words(g, dv.blk, i, j, kb);
-                const uint32_t old = t0 < Tqk ? kc[wb] : 0u;   // earlier tokens' codes stay
-                uint32_t word = 0;
-                for (int half = 0; half < 2; ++half) {
-                    const int c = kw.c0 + half;
-                    for (int r = 0; r < cph; ++r) {
-                        const int tau = t0 + 8 * (kw.pos0 + r) + kw.g;
-                        const int sh = 16 * half + r * g.kbits;
-                        if (tau < Tqk) {
-                            word |= old & (((1u << g.kbits) - 1u) << sh);
-                        } else if (tau < tb) {   // later tokens: zero
-                            const int sz = (((tau >> lgG) - gr0) << lgd) + c;
-                            word |= qcode_rcp(__half2float(xs[((tau - cs) << lgd) + c]), s_ks[sz], s_kz[sz],
-                                              s_kr[sz], g.kbits) << sh;
-                        }
-                    }
-                }
-                kc[wb] = word;
-            }
+            pack_key_round(g, dv, i, j, xs, s_ks, cs, CH, ta, tb, Tqk);
             __syncthreads();   // the next chunk reuses the rows
         }
     }

@@ -2,7 +2,8 @@
 // kernel (kivi_decode_impl.cuh, instantiated per head dimension in
 // kivi_decode_d{64,128,256}.cu, and with the score output for the
 // attention weights in kivi_decode_probs_d{64,128,256}.cu; kivi_probs.cu
-// turns those scores into weights).
+// turns those scores into weights; with a sliding window in
+// kivi_decode_win_d{64,128,256}.cu).
 //
 // The kernel is persistent: a fixed grid of CTAs (two per SM) splits the
 // work units of all (sequence, kv head, head group) pairs evenly, so every
@@ -36,6 +37,13 @@ cudaError_t kivi_launch_decode_probs_d256(const KiviGeom &, const KiviDev &, con
                                           const DecodePlan &, const DecodeUnits &, const ProbsOut &,
                                           cudaStream_t);
 
+cudaError_t kivi_launch_decode_win_d64(const KiviGeom &, const KiviDev &, const __half *, int, __half *,
+                                      const DecodePlan &, const DecodeUnits &, const Visible &, cudaStream_t);
+cudaError_t kivi_launch_decode_win_d128(const KiviGeom &, const KiviDev &, const __half *, int, __half *,
+                                       const DecodePlan &, const DecodeUnits &, const Visible &, cudaStream_t);
+cudaError_t kivi_launch_decode_win_d256(const KiviGeom &, const KiviDev &, const __half *, int, __half *,
+                                       const DecodePlan &, const DecodeUnits &, const Visible &, cudaStream_t);
+
 namespace {
 int env_int(const char *name, int dflt) {
     const char *v = getenv(name);
@@ -57,7 +65,7 @@ int kivi_partial_slots(int b, int h, int num_sms) {
 }
 
 DecodePlan kivi_plan_decode(const KiviGeom &g, int hq, const int *T, const int *Tqk, const int *Tqv,
-                            int num_sms, DecodeUnits *units, bool fused) {
+                            int num_sms, DecodeUnits *units, bool fused, Visible vis) {
     DecodePlan p;
     const int hg = hq / g.h;
     p.qgroups = (hg + 3) / 4;
@@ -101,8 +109,9 @@ DecodePlan kivi_plan_decode(const KiviGeom &g, int hq, const int *T, const int *
     }
     units->start[0] = 0;
     for (int i = 0; i < g.b; ++i) {
-        const int nf = (Tqk[i] < Tqv[i] ? Tqk[i] : Tqv[i]) / KIVI_KBLK;
-        const int nb = (T[i] + KIVI_KBLK - 1) / KIVI_KBLK;
+        const BlockList bl = visible_blocks(vis, T[i] > 0 ? T[i] - 1 : 0);
+        const int nf = bl.virt((Tqk[i] < Tqv[i] ? Tqk[i] : Tqv[i]) / KIVI_KBLK);
+        const int nb = bl.virt((T[i] + KIVI_KBLK - 1) / KIVI_KBLK);
         int w = units->lead + nf + MW * (nb - nf) + tail;
         if (w < 1) w = 1;   // an empty sequence still gets its (zero) output written
         units->full[i] = nf;
@@ -138,8 +147,8 @@ DecodePlan kivi_plan_decode(const KiviGeom &g, int hq, const int *T, const int *
 cudaError_t kivi_launch_decode(const KiviGeom &g, const KiviDev &dv, const __half *q, int hq,
                                __half *out, const DecodePlan &plan, const DecodeUnits &units,
                                cudaStream_t st, cudaEvent_t ev0, cudaEvent_t ev1, const ProbsOut *po,
-                               int maxT, const FusedStep *fs) {
-    if (po && fs) return cudaErrorInvalidValue;
+                               int maxT, const FusedStep *fs, Visible vis) {
+    if ((po && fs) || (vis.window > 0 && (po || fs))) return cudaErrorInvalidValue;
     if (ev0) cudaEventRecord(ev0, st);
     cudaError_t e;
     if (fs) {
@@ -147,6 +156,12 @@ cudaError_t kivi_launch_decode(const KiviGeom &g, const KiviDev &dv, const __hal
         case 64: e = kivi_launch_decode_fused_d64(g, dv, q, hq, out, plan, units, *fs, st); break;
         case 128: e = kivi_launch_decode_fused_d128(g, dv, q, hq, out, plan, units, *fs, st); break;
         default: e = kivi_launch_decode_fused_d256(g, dv, q, hq, out, plan, units, *fs, st); break;
+        }
+    } else if (vis.window > 0) {
+        switch (g.d) {
+        case 64: e = kivi_launch_decode_win_d64(g, dv, q, hq, out, plan, units, vis, st); break;
+        case 128: e = kivi_launch_decode_win_d128(g, dv, q, hq, out, plan, units, vis, st); break;
+        default: e = kivi_launch_decode_win_d256(g, dv, q, hq, out, plan, units, vis, st); break;
         }
     } else if (po) {
         switch (g.d) {

@@ -29,63 +29,20 @@
 // log2(e) / sqrt(d)); the last CTA to finish a pair merges its partials
 // with log-sum-exp weights and writes the fp16 output.
 #pragma once
+#include "kivi_async.cuh"
 #include "kivi_internal.cuh"
 #include "kivi_mma.cuh"
+#include "kivi_unpack.cuh"
 
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kMaxWaitIters = 1 << 24;   // bounded mbarrier waits
 constexpr int kFastMerge = 16;   // partials a pair's final merge reads in one round trip ...
 constexpr int kFastMergeV = 4;   // ... with at most this many accumulators a thread
 
 // ---------------------------------------------------------------------------
-// PTX helpers
+// PTX helpers (mbarriers and plain bulk copies: kivi_async.cuh)
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ void mbar_init(uint64_t *bar, unsigned count) {
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count) : "memory");
-}
-
-__device__ __forceinline__ void fence_mbar_init() {
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-}
-
-__device__ __forceinline__ void fence_proxy_async() {
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
-
-__device__ __forceinline__ void mbar_expect_tx(uint64_t *bar, unsigned bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)),
-                 "r"(bytes)
-                 : "memory");
-}
-
-__device__ __forceinline__ bool mbar_try_wait(uint64_t *bar, unsigned phase) {
-    unsigned ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(phase)
-        : "memory");
-    return ok != 0;
-}
-
-// bounded wait: false if the barrier did not complete within the limit
-__device__ __forceinline__ bool mbar_wait(uint64_t *bar, unsigned phase) {
-    for (int it = 0; it < kMaxWaitIters; ++it)
-        if (mbar_try_wait(bar, phase)) return true;
-    return false;
-}
-
-__device__ __forceinline__ void bulk_g2s(void *dst, const void *src, unsigned bytes, uint64_t *bar) {
-    asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-            smem_u32(dst)),
-        "l"(src), "r"(bytes), "r"(smem_u32(bar))
-        : "memory");
-}
 // L2 eviction-priority policies: the streamed records are read once
 // (evict first); the tail data prefetched long before its use is kept
 // (evict last)
@@ -119,81 +76,6 @@ __device__ __forceinline__ uint32_t hmul2u(uint32_t a, uint32_t b) { return h2u(
 __device__ __forceinline__ uint32_t hfma2u(uint32_t a, uint32_t b, uint32_t c) {
     return h2u(__hfma2(u2h(a), u2h(b), u2h(c)));
 }
-
-// Unpack field r of both 16-bit halves of w as fp16 (off + code).  The field
-// is moved (by a shift shared between fields, or none) to a mantissa
-// position p of an fp16 constant whose exponent makes bit p weigh 1, and
-// or-ed into it: the value is 2^(10 - p) + code.
-//   keys:   p in {4, 6, 8} (offsets 64, 16, 4); the accumulator carries
-//           off * sum(q s), removed with the zero-point MMA's sum(q s) row;
-//           against score-sized sums this costs < 1e-4 relative.
-//   values: any p <= 8; the offset is subtracted in fp16 before the MMA
-//           (exact), because the weighted value sums can be far smaller
-//           than off * sum(p s).
-struct View {
-    int shl, shr;          // shift left / right applied to the word
-    uint32_t mask, magic;  // field mask at its target position, fp16 pattern of the offset
-    float off;
-};
-__host__ __device__ constexpr View at_pos(int p, int width, int shl, int shr) {
-    // field of `width` bits at mantissa bit p; fp16 2^(10 - p) = exponent field 25 - p
-    return View{shl, shr, (((1u << width) - 1u) << p) * 0x10001u, (uint32_t)(25 - p) * 0x04000400u,
-                (float)(1 << (10 - p))};
-}
-template <int BITS, bool KEY>
-__host__ __device__ constexpr View view_of(int r) {
-    if (BITS == 4) {
-        if (KEY)   // field bits [4r, 4r + 4) -> bits 6..9, offset 16
-            return r <= 1 ? at_pos(6, 4, 6 - 4 * r, 0) : at_pos(6, 4, 0, 4 * r - 6);
-        // values: slots 0, 1 in place (p = 0, 4); slots 2, 3 shifted to p = 4
-        return r == 0 ? at_pos(0, 4, 0, 0) : (r == 1 ? at_pos(4, 4, 0, 0) : at_pos(4, 4, 0, 4 * r - 4));
-    }
-    // 2-bit field bits [2r, 2r + 2)
-    if (KEY) {
-        switch (r) {
-        case 0: return at_pos(4, 2, 4, 0);
-        case 1: return at_pos(6, 2, 4, 0);
-        case 2: return at_pos(4, 2, 0, 0);
-        case 3: return at_pos(6, 2, 0, 0);
-        case 4: return at_pos(8, 2, 0, 0);
-        case 5: return at_pos(4, 2, 0, 6);
-        case 6: return at_pos(6, 2, 0, 6);
-        default: return at_pos(8, 2, 0, 6);
-        }
-    }
-    // values: slots 0..4 in place (p = 0, 2, 4, 6, 8); slots 5..7 via one shift
-    return r <= 4 ? at_pos(2 * r, 2, 0, 0) : at_pos(2 * r - 6, 2, 0, 6);
-}
-// (x & mask) | magic as one lop3 with both constants as immediates; the
-// plain C++ form compiles to two ALU instructions on this target.
-template <uint32_t MASK, uint32_t MAGIC>
-__device__ __forceinline__ uint32_t and_or(uint32_t x) {
-    uint32_t r;
-    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(x), "n"(MASK), "n"(MAGIC));
-    return r;
-}
-template <int BITS, bool KEY, int R>
-__device__ __forceinline__ uint32_t unpack_t(uint32_t w) {
-    constexpr View v = view_of<BITS, KEY>(R);
-    const uint32_t x = v.shl ? (w << v.shl) : (v.shr ? (w >> v.shr) : w);
-    return and_or<v.mask, v.magic>(x);
-}
-// runtime-looking slot index r (a constant once the caller's loops unroll)
-template <int BITS, bool KEY>
-__device__ __forceinline__ uint32_t unpack(uint32_t w, int r) {
-    switch (r) {
-    case 0: return unpack_t<BITS, KEY, 0>(w);
-    case 1: return unpack_t<BITS, KEY, 1>(w);
-    case 2: return unpack_t<BITS, KEY, 2>(w);
-    case 3: return unpack_t<BITS, KEY, 3>(w);
-    case 4: return unpack_t<BITS, KEY, (BITS == 2 ? 4 : 3)>(w);
-    case 5: return unpack_t<BITS, KEY, (BITS == 2 ? 5 : 3)>(w);
-    case 6: return unpack_t<BITS, KEY, (BITS == 2 ? 6 : 3)>(w);
-    default: return unpack_t<BITS, KEY, (BITS == 2 ? 7 : 3)>(w);
-    }
-}
-template <int BITS, bool KEY>
-__host__ __device__ constexpr float slot_offset(int r) { return view_of<BITS, KEY>(r).off; }
 
 // Value fields for the P.V contraction: off + code as fp16 (2-bit fields
 // at mantissa positions 6 and 8, offsets 16 and 4; 4-bit at position 4,
@@ -529,6 +411,7 @@ struct MixCtx {
     const unsigned char *krows, *vrows;  // window rows of tokens ka.., va.. (stride RS bytes)
     int ka, va, RS;
     const unsigned char *zrow;           // 2 d zero bytes
+    int lo, sinks;                       // WIN: tokens [sinks, lo) are hidden
 };
 __device__ __forceinline__ const __half *key_row(const MixCtx &m, int tau) {
     return reinterpret_cast<const __half *>(tau >= m.Tqk && tau < m.T ? m.krows + (size_t)(tau - m.ka) * m.RS
@@ -544,7 +427,9 @@ __device__ __forceinline__ uint32_t keep_halves(uint32_t x, bool lo, bool hi) {
 
 // PROBS: the block's scores (log2 units) of head tq also go to srow[0..63]
 // (tokens tb.. of that head's weights row; null for absent heads).
-template <int D, int KB, int VB, int SH, bool MIXED, bool PROBS>
+// WIN: the scores of tokens [mx.sinks, mx.lo) are masked; the block (MIXED:
+// the tile) holds at least one other token.
+template <int D, int KB, int VB, int SH, bool MIXED, bool PROBS, bool WIN>
 __device__ __forceinline__ void do_block(WarpAcc<D> &A, const uint32_t (&qB)[D / 16][2],
                                          const unsigned char *sb, float alpha, const MixCtx &mx, float *srow) {
     using RG = Rec<D, KB, VB, SH>;
@@ -670,6 +555,16 @@ __device__ __forceinline__ void do_block(WarpAcc<D> &A, const uint32_t (&qB)[D /
                 const int t0 = 16 * mm + gq;
                 if (!MIXED || mx.tb + t0 < mx.T) srow[t0] = p[mm][0];
                 if (!MIXED || mx.tb + t0 + 8 < mx.T) srow[t0 + 8] = p[mm][1];
+            }
+        }
+    }
+    if constexpr (WIN) {
+        if (mx.tb < mx.lo && mx.tb + KIVI_KBLK > mx.sinks) {   // a block the window's edge or the sinks' end cuts
+#pragma unroll
+            for (int mm = 0; mm < 4; ++mm) {
+                const int t0 = mx.tb + 16 * mm + gq;
+                if (t0 >= mx.sinks && t0 < mx.lo) p[mm][0] = -INFINITY;
+                if (t0 + 8 >= mx.sinks && t0 + 8 < mx.lo) p[mm][1] = -INFINITY;
             }
         }
     }
@@ -850,10 +745,14 @@ __host__ __device__ __forceinline__ int cta_of_unit(long long u, long long U, in
     return (int)(((u + 1) * C - 1) / U);
 }
 
-template <int D, int KB, int VB, int SH, bool PROBS, bool FUSED>
+// WIN: of each sequence only the blocks the newest token's query sees count
+// (its block list, computed alike by the plan): "block" indices below are
+// then positions in that list, and pblk gives the block itself.
+template <int D, int KB, int VB, int SH, bool PROBS, bool FUSED, bool WIN>
 __global__ void __launch_bounds__(256, 2)
     decode_kernel(KiviGeom g, KiviDev dv, const __half *__restrict__ q, int hq,
-                  __half *__restrict__ out, DecodePlan plan, DecodeUnits units, ProbsOut po, FusedStep fs) {
+                  __half *__restrict__ out, DecodePlan plan, DecodeUnits units, ProbsOut po, FusedStep fs,
+                  Visible vis) {
     extern __shared__ __align__(128) unsigned char smem[];
     constexpr int NJ = D / 16;
     const int nw = blockDim.x >> 5;
@@ -961,8 +860,14 @@ __global__ void __launch_bounds__(256, 2)
         const int Tqv0 = pop ? Tqv - 1 : Tqv;   // the value queue before this launch's pop
         // an appending sequence stages the popped token's block as a window
         // block: it counts its value queue before the pop
-        const int nfull = min(Tqk, app ? Tqv0 : Tqv) / KIVI_KBLK;
-        const int nblk = (T + KIVI_KBLK - 1) / KIVI_KBLK;
+        int nfull = min(Tqk, app ? Tqv0 : Tqv) / KIVI_KBLK;
+        int nblk = (T + KIVI_KBLK - 1) / KIVI_KBLK;
+        BlockList bl{0, 0, 0};
+        if constexpr (WIN) {
+            bl = visible_blocks(vis, max(T - 1, 0));
+            nfull = bl.virt(nfull);
+            nblk = bl.virt(nblk);
+        }
         const int nfh = units.full[i];
         const int MW = units.mixed_weight;
 
@@ -994,6 +899,7 @@ __global__ void __launch_bounds__(256, 2)
         const int m1 = b1 > nfh ? (b1 - nfh + MW - 1) / MW : 0;
         const int nL = nA + max(0, m1 - m0);
         auto blk = [&](int x) { return x < nA ? b0 + x : nfh + m0 + (x - nA); };
+        auto pblk = [&](int x) { return WIN ? bl.phys(blk(x)) : blk(x); };
         auto first_at_least = [&](int kb) {   // first x with blk(x) >= kb (blk increases)
             int lo = 0, hi = nL;
             while (lo < hi) {
@@ -1016,7 +922,7 @@ __global__ void __launch_bounds__(256, 2)
             // rows into L2 now
             const uint64_t keep = policy_evict_last();
             for (int x = xm; x < nD; ++x) {
-                const int kb = blk(x), tb = kb * KIVI_KBLK, te = min(tb + KIVI_KBLK, T);
+                const int kb = pblk(x), tb = kb * KIVI_KBLK, te = min(tb + KIVI_KBLK, T);
                 prefetch_l2(recs + (size_t)kb * RG::BYTES, (unsigned)RG::BYTES, keep);
                 prefetch_rows<D>(kwin, g.R, max(tb, Tqk), te, keep);
                 prefetch_rows<D>(vwin, g.R + 1, max(tb, Tqv), te, keep);
@@ -1035,7 +941,7 @@ __global__ void __launch_bounds__(256, 2)
                 more = false;
                 return;
             }
-            issue_block<RG::BYTES>(myregion + (size_t)islot * RG::BYTES, mybars + islot, recs, blk(x), pol_stream);
+            issue_block<RG::BYTES>(myregion + (size_t)islot * RG::BYTES, mybars + islot, recs, pblk(x), pol_stream);
             islot = next_slot(islot);
             ++issued;
         };
@@ -1077,7 +983,12 @@ __global__ void __launch_bounds__(256, 2)
             float *srow = nullptr;
             if constexpr (PROBS)   // the warp's consumed-th block is its grab of that index
                 if (prow) srow = prow + (size_t)blk(warp + nw * consumed) * KIVI_KBLK;
-            do_block<D, KB, VB, SH, false, PROBS>(A, qB, myregion + (size_t)rslot * RG::BYTES, alpha, mc, srow);
+            if constexpr (WIN) {
+                mc.tb = pblk(warp + nw * consumed) * KIVI_KBLK;
+                mc.lo = bl.lo;
+                mc.sinks = vis.sinks;
+            }
+            do_block<D, KB, VB, SH, false, PROBS, WIN>(A, qB, myregion + (size_t)rslot * RG::BYTES, alpha, mc, srow);
             __syncwarp();
             // Refill the slot just read.  Its packed data was only read (by
             // loads whose values the block has consumed): no proxy fence.
@@ -1120,14 +1031,14 @@ __global__ void __launch_bounds__(256, 2)
             if (warp == 0) {
                 unsigned bytes = 0;
                 for (int k = 0; k < nrb; ++k) {
-                    const int kb = blk(x0 + k), tb = kb * KIVI_KBLK, te = min(tb + KIVI_KBLK, tnew);
+                    const int kb = pblk(x0 + k), tb = kb * KIVI_KBLK, te = min(tb + KIVI_KBLK, tnew);
                     bytes += RG::BYTES + (rows_to_stage(max(tb, Tqk), te, g.R) +
                                          rows_to_stage(max(tb, Tqv), te, g.R + 1)) * 2 * D;
                     if (tnew < T && tnew >= tb && tnew < tb + KIVI_KBLK) bytes += 4 * D;
                 }
                 if (lane == 0) mbar_expect_tx(cbar, bytes);
                 for (int k = 0; k < nrb && lane == 0; ++k) {
-                    const int kb = blk(x0 + k), tb = kb * KIVI_KBLK, te = min(tb + KIVI_KBLK, tnew);
+                    const int kb = pblk(x0 + k), tb = kb * KIVI_KBLK, te = min(tb + KIVI_KBLK, tnew);
                     unsigned char *reg = ring + (size_t)k * mreg;
                     const int ka = max(tb, Tqk), va = max(tb, Tqv);
                     bulk_g2s(reg, recs + (size_t)kb * RG::BYTES, (unsigned)RG::BYTES, cbar);
@@ -1158,8 +1069,13 @@ __global__ void __launch_bounds__(256, 2)
             }
             for (int w4 = warp; w4 < 4 * nrb; w4 += nw) {
                 const int k = w4 >> 2, t = w4 & 3;
-                const int kb = blk(x0 + k), tb = kb * KIVI_KBLK;
+                const int kb = pblk(x0 + k), tb = kb * KIVI_KBLK;
                 if (tb + 16 * t >= T || dead) continue;
+                if constexpr (WIN) {
+                    if (tb + 16 * t >= vis.sinks && tb + 16 * t + 16 <= bl.lo) continue;   // a hidden tile
+                    mc.lo = bl.lo;
+                    mc.sinks = vis.sinks;
+                }
                 unsigned char *reg = ring + (size_t)k * mreg;
                 mc.tb = tb;
                 mc.tmask = 1 << t;
@@ -1172,7 +1088,7 @@ __global__ void __launch_bounds__(256, 2)
                 mc.va = tb;
                 mc.zrow = reg + RG::BYTES + (size_t)2 * KIVI_KBLK * RS;
                 mc.RS = RS;
-                do_block<D, KB, VB, SH, true, PROBS>(A, qB, reg, alpha, mc, PROBS && prow ? prow + tb : nullptr);
+                do_block<D, KB, VB, SH, true, PROBS, WIN>(A, qB, reg, alpha, mc, PROBS && prow ? prow + tb : nullptr);
             }
         }
         __syncthreads();   // the ring holds mixed data no longer needed
@@ -1451,10 +1367,10 @@ __global__ void __launch_bounds__(256, 2)
     }
 }
 
-template <int D, int KB, int VB, int SH, bool PROBS, bool FUSED>
+template <int D, int KB, int VB, int SH, bool PROBS, bool FUSED, bool WIN>
 cudaError_t launch_t(const KiviGeom &g, const KiviDev &dv, const __half *q, int hq, __half *out,
                      const DecodePlan &plan, const DecodeUnits &units, const ProbsOut &po, const FusedStep &fs,
-                     cudaStream_t st) {
+                     const Visible &vis, cudaStream_t st) {
     using RG = Rec<D, KB, VB, SH>;
     if (g.rec_bytes != RG::BYTES || g.off_ksz != RG::OFF_KSZ || g.off_vc != RG::OFF_VC ||
         g.off_vsz != RG::OFF_VSZ || g.vc_blk != RG::VC_BLK || g.vsz_blk != RG::VSZ_BLK)
@@ -1462,7 +1378,7 @@ cudaError_t launch_t(const KiviGeom &g, const KiviDev &dv, const __half *q, int 
     size_t rings = (size_t)plan.warps * warp_region(g, plan.stages);
     if (rings < mixed_region(g)) rings = mixed_region(g);
     const size_t smem = bar_region(plan.warps, plan.stages) + rings;
-    cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, KB, VB, SH, PROBS, FUSED>,
+    cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, KB, VB, SH, PROBS, FUSED, WIN>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     // programmatic dependent launch: the CTAs may be placed while the
@@ -1477,34 +1393,36 @@ cudaError_t launch_t(const KiviGeom &g, const KiviDev &dv, const __half *q, int 
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, decode_kernel<D, KB, VB, SH, PROBS, FUSED>, g, dv, q, hq, out, plan, units, po,
-                              fs);
+    return cudaLaunchKernelEx(&cfg, decode_kernel<D, KB, VB, SH, PROBS, FUSED, WIN>, g, dv, q, hq, out, plan, units, po,
+                              fs, vis);
 }
 
-template <int D, int KB, int VB, bool PROBS, bool FUSED>
+template <int D, int KB, int VB, bool PROBS, bool FUSED, bool WIN>
 cudaError_t launch_g(const KiviGeom &g, const KiviDev &dv, const __half *q, int hq, __half *out,
                      const DecodePlan &plan, const DecodeUnits &units, const ProbsOut &po, const FusedStep &fs,
-                     cudaStream_t st) {
+                     const Visible &vis, cudaStream_t st) {
     switch (g.G) {
-    case 16: return launch_t<D, KB, VB, 0, PROBS, FUSED>(g, dv, q, hq, out, plan, units, po, fs, st);
-    case 32: return launch_t<D, KB, VB, 1, PROBS, FUSED>(g, dv, q, hq, out, plan, units, po, fs, st);
-    case 64: return launch_t<D, KB, VB, 2, PROBS, FUSED>(g, dv, q, hq, out, plan, units, po, fs, st);
+    case 16: return launch_t<D, KB, VB, 0, PROBS, FUSED, WIN>(g, dv, q, hq, out, plan, units, po, fs, vis, st);
+    case 32: return launch_t<D, KB, VB, 1, PROBS, FUSED, WIN>(g, dv, q, hq, out, plan, units, po, fs, vis, st);
+    case 64: return launch_t<D, KB, VB, 2, PROBS, FUSED, WIN>(g, dv, q, hq, out, plan, units, po, fs, vis, st);
     default:
-        if constexpr (D >= 128) return launch_t<D, KB, VB, 3, PROBS, FUSED>(g, dv, q, hq, out, plan, units, po, fs, st);
+        if constexpr (D >= 128) return launch_t<D, KB, VB, 3, PROBS, FUSED, WIN>(g, dv, q, hq, out, plan, units, po, fs, vis, st);
         return cudaErrorInvalidValue;
     }
 }
 
-// PROBS: the weights variant; FUSED: the variant that appends (fs).
-template <int D, bool PROBS, bool FUSED = false>
+// PROBS: the weights variant; FUSED: the variant that appends (fs); WIN: the
+// variant with a sliding window (vis).
+template <int D, bool PROBS, bool FUSED = false, bool WIN = false>
 cudaError_t launch_d(const KiviGeom &g, const KiviDev &dv, const __half *q, int hq, __half *out,
                      const DecodePlan &plan, const DecodeUnits &units, const ProbsOut &po, cudaStream_t st,
-                     const FusedStep &fs = FusedStep{nullptr, nullptr, nullptr}) {
-    static_assert(!(PROBS && FUSED), "the weights variant does not append");
-    if (g.kbits == 2 && g.vbits == 2) return launch_g<D, 2, 2, PROBS, FUSED>(g, dv, q, hq, out, plan, units, po, fs, st);
-    if (g.kbits == 2 && g.vbits == 4) return launch_g<D, 2, 4, PROBS, FUSED>(g, dv, q, hq, out, plan, units, po, fs, st);
-    if (g.kbits == 4 && g.vbits == 2) return launch_g<D, 4, 2, PROBS, FUSED>(g, dv, q, hq, out, plan, units, po, fs, st);
-    return launch_g<D, 4, 4, PROBS, FUSED>(g, dv, q, hq, out, plan, units, po, fs, st);
+                     const FusedStep &fs = FusedStep{nullptr, nullptr, nullptr},
+                     const Visible &vis = Visible{0, 0}) {
+    static_assert(!(PROBS && FUSED) && !(WIN && (PROBS || FUSED)), "one variant at a time");
+    if (g.kbits == 2 && g.vbits == 2) return launch_g<D, 2, 2, PROBS, FUSED, WIN>(g, dv, q, hq, out, plan, units, po, fs, vis, st);
+    if (g.kbits == 2 && g.vbits == 4) return launch_g<D, 2, 4, PROBS, FUSED, WIN>(g, dv, q, hq, out, plan, units, po, fs, vis, st);
+    if (g.kbits == 4 && g.vbits == 2) return launch_g<D, 4, 2, PROBS, FUSED, WIN>(g, dv, q, hq, out, plan, units, po, fs, vis, st);
+    return launch_g<D, 4, 4, PROBS, FUSED, WIN>(g, dv, q, hq, out, plan, units, po, fs, vis, st);
 }
 
 }  // namespace

@@ -1,0 +1,10 @@
+// kivi_decode_win_d256.cu -- decode-attention kernels for head dimension 256
+// with a sliding window and sink tokens.
+#include "kivi_decode_impl.cuh"
+
+cudaError_t kivi_launch_decode_win_d256(const KiviGeom &g, const KiviDev &dv, const __half *q, int hq, __half *out,
+                                       const DecodePlan &plan, const DecodeUnits &units, const Visible &vis,
+                                       cudaStream_t st) {
+    return launch_d<256, false, false, true>(g, dv, q, hq, out, plan, units, ProbsOut{nullptr, nullptr, 0}, st,
+                                            FusedStep{nullptr, nullptr, nullptr}, vis);
+}

@@ -104,6 +104,33 @@ struct FusedStep {
     int *nxt;
 };
 
+// Which tokens a query at position p sees besides s <= p: with window > 0,
+// those with p - s < window or s < sinks; window 0: all of them.
+struct Visible {
+    int window, sinks;
+};
+// The 64-token blocks holding a token that some query at positions
+// [p0, p1] sees (0 <= p0 <= p1), as a list without the hidden stretch
+// between the sinks' blocks and the window's: blocks [0, ns), then
+// [ns + gap, ...).  Virtual index x of the list is block phys(x); virt(n)
+// is how many of its entries are blocks below n.
+struct BlockList {
+    int lo;    // the first token that p0's window sees
+    int ns, gap;
+    __host__ __device__ int phys(int x) const { return x < ns ? x : x + gap; }
+    __host__ __device__ int virt(int n) const { return n <= ns ? n : n - gap > ns ? n - gap : ns; }
+};
+__host__ __device__ __forceinline__ BlockList visible_blocks(const Visible &v, int p0) {
+    BlockList l{0, 0, 0};
+    if (v.window > 0 && p0 >= v.window) {
+        l.lo = p0 - v.window + 1;
+        l.ns = ((v.sinks < l.lo ? v.sinks : l.lo) + KIVI_KBLK - 1) / KIVI_KBLK;
+        const int wb = l.lo / KIVI_KBLK;
+        if (wb > l.ns) l.gap = wb - l.ns;
+    }
+    return l;
+}
+
 struct SeqLens {
     int t[KIVI_MAX_BATCH];
 };
@@ -339,10 +366,11 @@ cudaError_t kivi_launch_prefill(const KiviGeom &g, const KiviDev &dv, const __ha
 // The prefill with its causal attention (kivi_prefill_attn.cu): O = the
 // attention of Q over K, V (fp16 [b][hq][t_stride][d] and [b][h][t_stride][d])
 // and the cache filled as kivi_launch_prefill fills it.  d in {64, 128},
-// G <= 64 (cudaErrorInvalidValue otherwise).
+// G <= 64 (cudaErrorInvalidValue otherwise).  vis: what each query sees of
+// the tokens up to its own (the cache takes every token).
 cudaError_t kivi_launch_prefill_attn(const KiviGeom &g, const KiviDev &dv, const __half *Q, const __half *K,
                                      const __half *V, __half *O, const SeqLens &lens, int t_stride, int hq,
-                                     cudaStream_t st);
+                                     cudaStream_t st, Visible vis = Visible{0, 0});
 // nxt: the other counter set ([3][b]: T, Tqk, Tqv), which receives the
 // counters after the append (dv's set is left as it was).
 // only_flush: append only the sequences whose key window is full now (the
@@ -351,9 +379,10 @@ cudaError_t kivi_launch_append(const KiviGeom &g, const KiviDev &dv, const __hal
                                const __half *v, const AppendCounters &ac, int *nxt, cudaStream_t st,
                                bool only_flush = false);
 // The decode plan and its work units (kivi_decode.cu); fused: the launch
-// also appends the step's token (its plan charges the owners' appends).
+// also appends the step's token (its plan charges the owners' appends);
+// vis: only the visible blocks count.
 DecodePlan kivi_plan_decode(const KiviGeom &g, int hq, const int *T, const int *Tqk, const int *Tqv,
-                            int num_sms, DecodeUnits *units, bool fused = false);
+                            int num_sms, DecodeUnits *units, bool fused = false, Visible vis = Visible{0, 0});
 // partial slots per (sequence, query head) a cache of this shape allocates
 int kivi_partial_slots(int b, int h, int num_sms);
 // Scores left in po.p by the decode kernel's weights variant -> weights
@@ -366,7 +395,10 @@ cudaError_t kivi_launch_probs_finalize(const KiviGeom &g, const KiviDev &dv, int
 // (FusedStep).  Its units come from the counters after the append, except
 // that a sequence the launch appends counts its value queue before the pop
 // (the popped token's block is staged as a window block).
+// vis (window 0: everything; not with po or fs): the tokens the newest
+// token's query sees.
 cudaError_t kivi_launch_decode(const KiviGeom &g, const KiviDev &dv, const __half *q, int hq,
                                __half *out, const DecodePlan &plan, const DecodeUnits &units,
                                cudaStream_t st, cudaEvent_t ev0, cudaEvent_t ev1,
-                               const ProbsOut *po = nullptr, int maxT = 0, const FusedStep *fs = nullptr);
+                               const ProbsOut *po = nullptr, int maxT = 0, const FusedStep *fs = nullptr,
+                               Visible vis = Visible{0, 0});

@@ -7,7 +7,9 @@ fails to load, importing this module raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import math
 import os
 
 import numpy as np
@@ -23,7 +25,8 @@ EXPORTS = ["kivi_cache_create", "kivi_cache_destroy", "kivi_prefill", "kivi_appe
            "kivi_cache_export", "kivi_cache_check", "kivi_profile_enable", "kivi_profile_read",
            "kivi_decode_plan", "kivi_status_str", "kivi_last_error", "kivi_abi_version",
            "kivi_decode_attn_noalloc", "kivi_cache_export_records", "kivi_append_decode",
-           "kivi_decode_attn_probs", "kivi_plan_preview", "kivi_prefill_attn"]
+           "kivi_decode_attn_probs", "kivi_plan_preview", "kivi_prefill_attn", "kivi_prefill_attn_window",
+           "kivi_decode_attn_window", "kivi_chunk_attn", "kivi_append_chunk", "kivi_rope"]
 
 
 class KiviError(RuntimeError):
@@ -49,6 +52,11 @@ def _load():
     L.kivi_append.argtypes = [vp, vp, vp, vp]
     L.kivi_decode_attn.argtypes = [vp, vp, i32, vp, vp]
     L.kivi_decode_attn_probs.argtypes = [vp, vp, i32, vp, vp, vp, ctypes.c_int64, vp]
+    L.kivi_prefill_attn_window.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i32, vp, vp]
+    L.kivi_decode_attn_window.argtypes = [vp, vp, i32, i32, i32, vp, vp]
+    L.kivi_chunk_attn.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i32, vp, vp]
+    L.kivi_append_chunk.argtypes = [vp, vp, vp, vp, i32, vp]
+    L.kivi_rope.argtypes = [vp, vp] + [i32] * 5 + [vp] * 4 + [i32, i32, ctypes.c_float, i32, vp, vp, vp]
     L.kivi_plan_preview.argtypes = [i32] * 9 + [vp, vp, vp, i32, vp]
     L.kivi_cache_lengths.argtypes = [vp, vp, vp, vp]
     L.kivi_cache_export_sizes.argtypes = [vp, ctypes.POINTER(ctypes.c_size_t)]
@@ -101,6 +109,115 @@ def _dev_fp16(x, shape, name):
     return ctypes.c_void_p(x.data_ptr())
 
 
+def _on(stream):
+    """Context in which torch allocates (and launches) on `stream`."""
+    import torch
+    return torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext()
+
+
+def _counts(n, b, name="n"):
+    """Per-sequence counts as a contiguous int32 array."""
+    a = np.asarray(n)
+    if a.dtype.kind not in "iu" or a.ndim > 1 or (a.ndim == 1 and a.shape[0] not in (1, b)):
+        raise ValueError(f"{name} must be an integer or {b} integers")
+    if a.size and (int(a.min()) < -2**31 or int(a.max()) >= 2**31):
+        raise ValueError(f"{name} outside 32 bits")
+    return np.ascontiguousarray(np.broadcast_to(a.astype(np.int32), (b,)))
+
+
+def rope_frequencies(rot_dim, base=10000.0, scaling=None, factor=1.0, original_length=8192, beta_fast=32.0,
+                     beta_slow=1.0, low=1.0, high=4.0):
+    """Rotary frequencies (radians a position, float64 [rot_dim / 2]) and the
+    factor on the rotated channels, for Rope.
+
+    scaling: None, base ** (-2 m / rot_dim); "linear", divided by factor;
+    "ntk", the base raised so that the lowest frequency is divided by factor;
+    "yarn", divided by factor below beta_slow turns over original_length,
+    kept above beta_fast, a linear ramp (in m) between, and the rotated part
+    times 0.1 ln(factor) + 1; "bands", divided below `low` turns over
+    original_length, kept above `high`, linear (in turns) between."""
+    if rot_dim < 2 or rot_dim % 2 or not (base > 1 and factor >= 1):
+        raise ValueError("need an even rot_dim >= 2, base > 1 and factor >= 1")
+    m = np.arange(rot_dim // 2, dtype=np.float64)
+    f = float(base) ** (-2.0 * m / rot_dim)
+    if scaling is None:
+        return f, 1.0
+    if scaling == "linear":
+        return f / factor, 1.0
+    if scaling == "ntk":
+        if rot_dim < 4:
+            raise ValueError("ntk scaling needs rot_dim >= 4")
+        return (base * factor ** (rot_dim / (rot_dim - 2))) ** (-2.0 * m / rot_dim), 1.0
+    if scaling == "yarn":
+        at = [rot_dim * math.log(original_length / (r * 2 * math.pi)) / (2 * math.log(base))
+              for r in (beta_fast, beta_slow)]
+        lo, hi = max(math.floor(at[0]), 0), min(math.ceil(at[1]), rot_dim // 2 - 1)
+        ramp = np.clip((m - lo) / max(hi - lo, 1e-3), 0.0, 1.0)
+        return f / factor * ramp + f * (1 - ramp), 0.1 * math.log(factor) + 1.0
+    if scaling == "bands":
+        if not high > low:
+            raise ValueError("bands scaling needs high > low")
+        keep = np.clip((original_length * f / (2 * math.pi) - low) / (high - low), 0.0, 1.0)
+        return f / factor * (1 - keep) + f * keep, 1.0
+    raise ValueError(f"unknown scaling {scaling!r}")
+
+
+class Rope:
+    """Rotary positions for heads of dimension d: the first rot_dim channels
+    (default all) turn, pairs (m, m + rot_dim / 2) or, interleaved, (2 m,
+    2 m + 1), at the frequencies inv_freq (default base ** (-2 m / rot_dim);
+    rope_frequencies has the long-context scalings) times factor."""
+
+    def __init__(self, d, rot_dim=None, base=10000.0, interleaved=False, inv_freq=None, factor=1.0):
+        self.d, self.rot_dim = d, d if rot_dim is None else rot_dim
+        self.interleaved, self.factor = bool(interleaved), float(factor)
+        f = rope_frequencies(self.rot_dim, base)[0] if inv_freq is None else np.asarray(inv_freq, np.float64)
+        if f.shape != (self.rot_dim // 2,) or not np.all(np.isfinite(f)):
+            raise ValueError(f"inv_freq must be {self.rot_dim // 2} finite numbers")
+        self.inv_freq = f.copy()
+        # fractions of a turn, 2^64 = one turn
+        self._turns = np.array([int(round(x / (2 * math.pi) * 2.0**64)) % 2**64 for x in f.tolist()], np.uint64)
+
+    def apply(self, q, k, pos, n=None, q_out=None, k_out=None, inverse=False, stream=None):
+        """Rotate q (CUDA fp16 [b, h_q, t, d] or [b, h_q, d]) and k (same with
+        h_kv heads, or None).  pos: first position of each sequence (an
+        integer or b integers), or every position (CUDA int32 [b, t]).  n:
+        tokens of each sequence (default t; rows past them stay as they are in
+        the outputs, zero in new ones).  inverse: the transposed map.  Returns
+        (q_out, k_out), or q_out alone when k is None."""
+        import torch
+        if not isinstance(q, torch.Tensor) or q.dim() not in (3, 4):
+            raise ValueError("q must be a [b, heads, t, d] or [b, heads, d] tensor")
+        step = q.dim() == 3
+        b, hq, t = q.shape[0], q.shape[1], 1 if step else q.shape[2]
+        hk = 0 if k is None else k.shape[1]
+        shapes = [(b, h, self.d) if step else (b, h, t, self.d) for h in (hq, hk)]
+        qp = _dev_fp16(q, shapes[0], "q")
+        kp = _dev_fp16(k, shapes[1], "k") if k is not None else None
+        cnt = _counts(t if n is None else n, b)
+        pos0, posp = None, None
+        if isinstance(pos, torch.Tensor) and pos.is_cuda:
+            if pos.dtype != torch.int32 or tuple(pos.shape) != (b, t) or not pos.is_contiguous():
+                raise ValueError(f"pos must be a contiguous int32 tensor [{b}, {t}]")
+            posp = pos.data_ptr()
+        else:
+            pos0 = _counts(pos, b, "pos")
+        tensors = [x for x in (q, k, q_out, k_out, pos if posp else None) if x is not None]
+        if any(x.device != q.device for x in tensors):
+            raise ValueError("all tensors must be on one device")
+        with torch.cuda.device(q.device), _on(stream):
+            new = torch.empty_like if np.all(cnt == t) else torch.zeros_like
+            q_out = new(q) if q_out is None else q_out
+            k_out = new(k) if k_out is None and k is not None else k_out
+            qo = _dev_fp16(q_out, shapes[0], "q_out")
+            ko = _dev_fp16(k_out, shapes[1], "k_out") if k is not None else None
+            _check(lib.kivi_rope(qp, kp, b, hq, hk, t, self.d, cnt.ctypes.data,
+                                 None if pos0 is None else pos0.ctypes.data, posp, self._turns.ctypes.data,
+                                 self.rot_dim, int(self.interleaved), self.factor, int(bool(inverse)), qo, ko,
+                                 _stream(stream)))
+        return q_out if k is None else (q_out, k_out)
+
+
 class KiviCache:
     """A KIVI quantized KV cache of b sequences x h_kv heads on the current GPU."""
 
@@ -111,6 +228,8 @@ class KiviCache:
         self._h = ctypes.c_void_p()
         _check(lib.kivi_cache_create(b, h_kv, d, k_bits, v_bits, G, R, max_tokens,
                                      ctypes.byref(self._h)))
+        import torch
+        self._dev = torch.cuda.current_device()   # the handle's memory is there
 
     # -- lifecycle ---------------------------------------------------------
     def close(self):
@@ -137,10 +256,16 @@ class KiviCache:
         vp = _dev_fp16(V, (self.b, self.h_kv, ts, self.d), "V")
         _check(lib.kivi_prefill(self._h, kp, vp, t.ctypes.data, ts, _stream(stream)))
 
-    def prefill_attn(self, Q, K, V, t, out=None, stream=None):
+    def _here(self, *tensors):
+        """The tensors are on the cache's device."""
+        if any(x is not None and x.device.index != self._dev for x in tensors):
+            raise ValueError(f"tensors must be on the cache's device cuda:{self._dev}")
+
+    def prefill_attn(self, Q, K, V, t, out=None, stream=None, window=0, sinks=0):
         """prefill(K, V, t) and the prompt's causal attention: Q CUDA fp16
         [b, h_q, t_stride, d] -> out (same shape; rows past each sequence's
-        length untouched).  One launch."""
+        length untouched).  One launch.  With window > 0 a query sees only the
+        last `window` tokens up to its own and the sequence's first `sinks`."""
         import torch
         t = np.ascontiguousarray(np.broadcast_to(np.asarray(t, np.int32), (self.b,)))
         ts, hq = K.shape[2], Q.shape[1]
@@ -150,7 +275,61 @@ class KiviCache:
         if out is None:
             out = torch.zeros_like(Q)
         op = _dev_fp16(out, (self.b, hq, ts, self.d), "out")
-        _check(lib.kivi_prefill_attn(self._h, qp, kp, vp, t.ctypes.data, ts, hq, op, _stream(stream)))
+        if window or sinks:
+            self._here(Q, K, V, out)
+            _check(lib.kivi_prefill_attn_window(self._h, qp, kp, vp, t.ctypes.data, ts, hq, window, sinks, op,
+                                                _stream(stream)))
+        else:
+            _check(lib.kivi_prefill_attn(self._h, qp, kp, vp, t.ctypes.data, ts, hq, op, _stream(stream)))
+        return out
+
+    def _chunk(self, K, V, n):
+        if K.dim() != 4:
+            raise ValueError("K must be [b, h_kv, n_stride, d]")
+        ns = K.shape[2]
+        kp = _dev_fp16(K, (self.b, self.h_kv, ns, self.d), "K")
+        vp = _dev_fp16(V, (self.b, self.h_kv, ns, self.d), "V")
+        return kp, vp, _counts(n, self.b), ns
+
+    def chunk_attn(self, Q, K, V, n, window=0, sinks=0, out=None, stream=None):
+        """Attention of n new tokens of each sequence (an integer or b of
+        them) over the cache and the chunk itself: Q CUDA fp16 [b, h_q, ns, d],
+        K and V [b, h_kv, ns, d] -> out (rows past n untouched, zero in a new
+        tensor).  Does not append (append_chunk, extend)."""
+        import torch
+        kp, vp, cnt, ns = self._chunk(K, V, n)
+        hq = Q.shape[1]
+        qp = _dev_fp16(Q, (self.b, hq, ns, self.d), "Q")
+        with _on(stream):
+            if out is None:
+                out = torch.zeros_like(Q)
+            op = _dev_fp16(out, (self.b, hq, ns, self.d), "out")
+            self._here(Q, K, V, out)
+            _check(lib.kivi_chunk_attn(self._h, qp, kp, vp, cnt.ctypes.data, ns, hq, window, sinks, op,
+                                       _stream(stream)))
+        return out
+
+    def append_chunk(self, K, V, n, stream=None):
+        """Append n tokens of each sequence (an integer or b of them; K, V CUDA
+        fp16 [b, h_kv, ns, d]): n one-token appends in one call."""
+        kp, vp, cnt, ns = self._chunk(K, V, n)
+        self._here(K, V)
+        _check(lib.kivi_append_chunk(self._h, kp, vp, cnt.ctypes.data, ns, _stream(stream)))
+
+    def extend(self, Q, K, V, n, window=0, sinks=0, rope=None, out=None, stream=None):
+        """Take the next chunk of every sequence: rotate its queries and keys
+        at the positions behind the cached tokens (rope: a Rope, or None),
+        attend (chunk_attn; returns its out) and append it (append_chunk)."""
+        cnt = _counts(n, self.b)
+        T = self.lengths()[0]
+        if np.any(cnt > self.max_tokens - T):
+            raise CapacityError(3, f"sequence {int(np.argmax(cnt > self.max_tokens - T))} would exceed max_tokens")
+        self._here(Q, K, V, out)
+        with _on(stream):
+            if rope is not None:
+                Q, K = rope.apply(Q, K, T, n=cnt, stream=stream)
+            out = self.chunk_attn(Q, K, V, cnt, window, sinks, out, stream)
+            self.append_chunk(K, V, cnt, stream)
         return out
 
     def append(self, k, v, stream=None):
@@ -159,15 +338,21 @@ class KiviCache:
         vp = _dev_fp16(v, (self.b, self.h_kv, self.d), "v")
         _check(lib.kivi_append(self._h, kp, vp, _stream(stream)))
 
-    def decode(self, q, out=None, stream=None):
-        """q: CUDA fp16 [b, h_q, d] -> out CUDA fp16 [b, h_q, d]."""
+    def decode(self, q, out=None, stream=None, window=0, sinks=0):
+        """q: CUDA fp16 [b, h_q, d] -> out CUDA fp16 [b, h_q, d].  With
+        window > 0 the query sees only the last `window` tokens and the
+        sequence's first `sinks`."""
         import torch
         hq = q.shape[1]
         qp = _dev_fp16(q, (self.b, hq, self.d), "q")
         if out is None:
             out = torch.empty_like(q)
         op = _dev_fp16(out, (self.b, hq, self.d), "out")
-        _check(lib.kivi_decode_attn(self._h, qp, hq, op, _stream(stream)))
+        if window or sinks:
+            self._here(q, out)
+            _check(lib.kivi_decode_attn_window(self._h, qp, hq, window, sinks, op, _stream(stream)))
+        else:
+            _check(lib.kivi_decode_attn(self._h, qp, hq, op, _stream(stream)))
         return out
 
     def decode_probs(self, q, probs, mass=None, out=None, stream=None):

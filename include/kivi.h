@@ -99,6 +99,78 @@ kivi_status kivi_prefill(kivi_cache_t c, const void *K, const void *V, const int
 kivi_status kivi_prefill_attn(kivi_cache_t c, const void *q, const void *K, const void *V, const int32_t *t,
                               int t_stride, int h_q, void *out, kivi_stream_t stream);
 
+/* Sliding windows with sinks (kivi_prefill_attn_window,
+ * kivi_decode_attn_window, kivi_chunk_attn): with window > 0 the query at
+ * position p sees, of the tokens s <= p, those with p - s < window and the
+ * sequence's first `sinks` tokens (s < sinks).  window == 0: every token
+ * s <= p, whatever sinks says.  A token always sees itself.  Neither may be
+ * negative (KIVI_ERR_INVALID_ARG).  Inputs are finite also where they are
+ * hidden. */
+
+/* kivi_prefill_attn with a sliding window: out is the windowed attention of
+ * the prompt; the cache afterwards is the same (it takes every token).  Key
+ * tiles that no query of a tile sees are neither read nor multiplied. */
+kivi_status kivi_prefill_attn_window(kivi_cache_t c, const void *q, const void *K, const void *V, const int32_t *t,
+                                     int t_stride, int h_q, int window, int sinks, void *out,
+                                     kivi_stream_t stream);
+
+/* Attention of a chunk of new tokens over the cache as it stands and over
+ * the chunk itself: the next piece of a long prompt, or the tokens of a
+ * speculative step.  Sequence i brings n[i] tokens (n: HOST array of b
+ * int32, 0 <= n[i] <= n_stride) at positions T_i, T_i + 1, ...: K and V fp16
+ * [b][h_kv][n_stride][d], q and out fp16 [b][h_q][n_stride][d] (device,
+ * 16-byte aligned).  For token r < n[i], query head h (kv head
+ * h / (h_q / h_kv)):
+ *   out[i][h][r] = softmax over the visible tokens s <= T_i + r of the cache
+ *                  (quantized, then fp16: item 5) and the chunk (fp16)
+ * Rows r >= n[i] of out are not written; a sequence with n[i] = 0 is left
+ * out.  Read-only on the cache: kivi_append_chunk appends the tokens, so a
+ * rejected draft needs no undoing.  Scores accumulate in fp32; the restored
+ * keys and values (scale code + zero) and the softmax weights are rounded to
+ * fp16 before the products (|K|, |V| <= 32768, so that they stay finite).
+ * One launch, or two when few rows meet long sequences (their tokens are
+ * then split over CTAs and joined; a call's result is repeatable bit for
+ * bit).  Uses a buffer of the cache: calls on one cache that overlap on the
+ * GPU (two streams, or two captured graphs replayed at once) must not be
+ * issued.  A captured call replays with the counts and positions it was
+ * captured with.  Supports d 64 or 128 (KIVI_ERR_UNSUPPORTED otherwise) and
+ * n_stride <= 2^26; h_q a multiple of h_kv, at most 8 times it; the cache's
+ * device must be current (KIVI_ERR_INVALID_ARG). */
+kivi_status kivi_chunk_attn(kivi_cache_t c, const void *q, const void *K, const void *V, const int32_t *n,
+                            int n_stride, int h_q, int window, int sinks, void *out, kivi_stream_t stream);
+
+/* Append n[i] tokens to sequence i (0 leaves it as it is): K, V, n and
+ * n_stride as for kivi_chunk_attn, any d.  The cache afterwards is bitwise
+ * the one that n[i] calls of kivi_append for sequence i alone would leave.
+ * KIVI_ERR_CAPACITY (and nothing changes) if a sequence would exceed
+ * max_tokens.  Two launches at most, on `stream`. */
+kivi_status kivi_append_chunk(kivi_cache_t c, const void *K, const void *V, const int32_t *n, int n_stride,
+                              kivi_stream_t stream);
+
+/* Rotary positions of queries and keys, before they enter the calls above.
+ * Channel pair m < rot_dim / 2 of a token at position p turns by the angle
+ * p w_m: (x, y) -> factor (x cos - y sin, y cos + x sin).  interleaved == 0:
+ * pair m is channels (m, m + rot_dim / 2); else (2 m, 2 m + 1).  Channels
+ * from rot_dim on are copied.  inverse != 0 applies the transposed map (the
+ * angle negated): the gradient with respect to the input.
+ * q, q_out fp16 [b][h_q][n_stride][d], k, k_out fp16 [b][h_kv][n_stride][d]
+ * (device, 16-byte aligned; an output may be its input, but not overlap it
+ * otherwise; h_q or h_kv may be 0, its pointers are then not used).  Rows
+ * r >= n[i] (n: HOST array of b int32) are not written.  The position of
+ * token r of sequence i is pos0[i] + r (pos0: HOST array of b int32) or
+ * pos[i][r] (pos: DEVICE int32 [b][n_stride]); one of the two is NULL.  Any
+ * int32 position is valid.
+ * turns (HOST, rot_dim / 2 entries): w_m as a fraction of a full turn in
+ * fixed point, round(w_m / (2 pi) 2^64) mod 2^64; the angle is formed in
+ * 64-bit integers, so far positions lose nothing.  Frequency scaling for
+ * long contexts is a choice of the table (kivi.py: rope_frequencies).
+ * Sines and products in fp32, results rounded once.  One launch on the
+ * current device, no state.  Supports d 64, 128 or 256 and rot_dim a
+ * multiple of 16, at most d (KIVI_ERR_UNSUPPORTED otherwise). */
+kivi_status kivi_rope(const void *q, const void *k, int b, int h_q, int h_kv, int n_stride, int d, const int32_t *n,
+                      const int32_t *pos0, const int32_t *pos, const uint64_t *turns, int rot_dim, int interleaved,
+                      float factor, int inverse, void *q_out, void *k_out, kivi_stream_t stream);
+
 /* Append one token to every sequence: k and v fp16 [b][h_kv][d] (device).
  * First, per sequence, the maintenance of item 4 left over from the previous
  * step: the fp16 key block is quantized if it holds R keys, and the oldest
@@ -121,6 +193,13 @@ kivi_status kivi_append(kivi_cache_t c, const void *k, const void *v, kivi_strea
  * global memory is read before it has completed, so stream order holds. */
 kivi_status kivi_decode_attn(kivi_cache_t c, const void *q, int h_q, void *out,
                              kivi_stream_t stream);
+
+/* kivi_decode_attn with a sliding window and sinks: the query is the newest
+ * token's (position T_i - 1).  Blocks it does not see are not read.  With
+ * window == 0 the call is kivi_decode_attn.  The cache's device must be
+ * current (KIVI_ERR_INVALID_ARG). */
+kivi_status kivi_decode_attn_window(kivi_cache_t c, const void *q, int h_q, int window, int sinks, void *out,
+                                    kivi_stream_t stream);
 
 /* Decode attention with each token's attention weight: out as
  * kivi_decode_attn computes it (bitwise the same), and, for sequence i,
