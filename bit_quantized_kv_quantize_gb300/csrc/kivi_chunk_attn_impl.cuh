@@ -55,8 +55,8 @@ __device__ __forceinline__ uint32_t ck_affine(uint32_t x, float off, uint32_t s,
 }
 
 // K^ of a record's 64 tokens: chunk-major tile [64 tokens][D], 16-byte chunk
-// c of token r at byte c 1024 + r 16.  Warp w of the kCkDq takes the code
-// chunks w, w + kCkDq, ...; a lane's half2 (two channels of one token) are
+// c of token r at byte c 1024 + r 16.  Warp w of the kCkDq takes the
+// 16-channel steps w, w + kCkDq, ...; a lane's half2 (two channels of one token) are
 // the lanes t = 0..3 of one 16-byte chunk: 128 consecutive bytes a store.
 template <int D, int KB>
 __device__ __forceinline__ void dequant_keys(unsigned char *tile, const unsigned char *rec, int off_ksz, int lgG,
@@ -64,28 +64,40 @@ __device__ __forceinline__ void dequant_keys(unsigned char *tile, const unsigned
     const int lane = threadIdx.x & 31, gq = lane >> 2, tq = lane & 3;
     const __half *ksz = reinterpret_cast<const __half *>(rec + off_ksz) + tq * (D / 4);
     unsigned char *dst = tile + gq * 16 + tq * 4;
-    constexpr int JPC = KB == 2 ? 2 : 1;   // 16-channel steps a chunk of words covers
-    for (int ch = w; ch < D * KB / 64; ch += kCkDq) {
-        const uint4 w4 = *reinterpret_cast<const uint4 *>(rec + (size_t)ch * 512 + lane * 16);
+    constexpr int NW = KB / 2;   // words of a channel pair
+    // one 16-channel step a turn, not unrolled (see dequant_values)
+#pragma unroll 1
+    for (int j = w; j < D / 16; j += kCkDq) {
+        // every load before the first store: the compiler keeps their order
+        uint32_t W[2 * NW];
+        const unsigned char *pw = rec + (size_t)((j * 2 * NW) >> 2) * 512 + lane * 16 + ((j * 2 * NW) & 3) * 4;
+        if (KB == 2) {
+            const uint2 v = *reinterpret_cast<const uint2 *>(pw);
+            W[0] = v.x;
+            W[1] = v.y;
+        } else {
+            const uint4 v = *reinterpret_cast<const uint4 *>(pw);
+            W[0] = v.x;
+            W[1] = v.y;
+            W[NW] = v.z;
+            W[2 * NW - 1] = v.w;
+        }
+        uint2 sv[4], zv[4];
 #pragma unroll
-        for (int jj = 0; jj < JPC; ++jj) {
-            const int j = ch * JPC + jj;
-            const uint32_t W[2][2] = {{KB == 2 && jj ? w4.z : w4.x, w4.y}, {KB == 2 ? (jj ? w4.w : w4.y) : w4.z, w4.w}};
+        for (int qd = 0; qd < 4; ++qd) {   // 16 tokens share a group row
+            const __half *row = ksz + (((16 * qd) >> lgG) * 2) * D + 4 * j;
+            sv[qd] = *reinterpret_cast<const uint2 *>(row);
+            zv[qd] = *reinterpret_cast<const uint2 *>(row + D);
+        }
+        unsigned char *p = dst + (size_t)(2 * j) * (kCkKeys * 16);
 #pragma unroll
-            for (int qd = 0; qd < 4; ++qd) {   // 16 tokens share a group row
-                const __half *row = ksz + (((16 * qd) >> lgG) * 2) * D + 4 * j;
-                const uint2 s = *reinterpret_cast<const uint2 *>(row), z = *reinterpret_cast<const uint2 *>(row + D);
-#pragma unroll
-                for (int o = 0; o < 2; ++o) {
-                    const int pos = 2 * qd + o;
-                    const int wi = KB == 2 ? 0 : pos >> 2, r = KB == 2 ? pos : pos & 3;
-                    const float off = slot_offset<KB, true>(r);
-                    unsigned char *p = dst + (size_t)(2 * j) * (kCkKeys * 16) + pos * 128;
-                    *reinterpret_cast<uint32_t *>(p) = ck_affine(unpack<KB, true>(W[0][wi], r), off, s.x, z.x);
-                    *reinterpret_cast<uint32_t *>(p + kCkKeys * 16) =
-                        ck_affine(unpack<KB, true>(W[1][wi], r), off, s.y, z.y);
-                }
-            }
+        for (int pos = 0; pos < 8; ++pos) {
+            const int wi = KB == 2 ? 0 : pos >> 2, r = KB == 2 ? pos : pos & 3;
+            const float off = slot_offset<KB, true>(r);
+            const uint2 sc = sv[pos >> 1], z = zv[pos >> 1];
+            *reinterpret_cast<uint32_t *>(p + pos * 128) = ck_affine(unpack<KB, true>(W[wi], r), off, sc.x, z.x);
+            *reinterpret_cast<uint32_t *>(p + kCkKeys * 16 + pos * 128) =
+                ck_affine(unpack<KB, true>(W[NW + wi], r), off, sc.y, z.y);
         }
     }
 }
@@ -99,47 +111,82 @@ __device__ __forceinline__ void dequant_values(unsigned char *tile, const unsign
     constexpr int WL = D * VB / 64, CS = WL < 4 ? WL : 4, NWV = D * VB / 128, CPH = 16 / VB;
     const int lane = threadIdx.x & 31, gq = lane >> 2, tq = lane & 3;
     const int ngi = D >> lgG;
-    const uint32_t *words = reinterpret_cast<const uint32_t *>(rec + off_vc) + (size_t)w * (D * VB / 2);
+    const uint32_t *words = reinterpret_cast<const uint32_t *>(rec + off_vc) + (size_t)w * (D * VB / 2) + lane * CS;
     const __half *vsz = reinterpret_cast<const __half *>(rec + off_vsz) + (size_t)w * (2 * ngi * 16) + 4 * tq;
-    uint32_t W[WL];
-#pragma unroll
-    for (int c = 0; c < WL / CS; ++c) {
-        if (CS == 4) {
-            const uint4 v = *reinterpret_cast<const uint4 *>(words + c * 128 + lane * 4);
-            W[c * 4] = v.x;
-            W[c * 4 + 1] = v.y;
-            W[c * 4 + CS / 2] = v.z;
-            W[c * 4 + CS - 1] = v.w;
-        } else {
-            const uint2 v = *reinterpret_cast<const uint2 *>(words + c * 64 + lane * 2);
-            W[c * 2] = v.x;
-            W[c * 2 + 1] = v.y;
-        }
-    }
     unsigned char *dst = tile + (size_t)(2 * w) * (D * 16) + gq * 16 + tq * 4;
+    // one word (CPH channel steps of 8) a turn, not unrolled: short code
+    // stays in the instruction cache beside the softmax warps'
+#pragma unroll 1
+    for (int wi = 0; wi < NWV; ++wi, dst += CPH * 128) {
+        // every load before the first store: the compiler keeps their order
+        const int u1 = NWV + wi;   // tokens 2 t, 2 t + 1: word wi; + 8: word u1
+        const uint32_t W0 = words[wi / CS * 32 * CS + wi % CS], W1 = words[u1 / CS * 32 * CS + u1 % CS];
+        uint2 sv[CPH / 2], zv[CPH / 2];
 #pragma unroll
-    for (int q = 0; q < D / 16; ++q) {   // 16 channels share a group row
-        const int gi = (16 * q) >> lgG;
-        const uint2 s = *reinterpret_cast<const uint2 *>(vsz + gi * 16);
-        const uint2 z = *reinterpret_cast<const uint2 *>(vsz + (ngi + gi) * 16);
+        for (int q = 0; q < CPH / 2; ++q) {   // 16 channels share a group row
+            const int gi = (16 * (wi * (CPH / 2) + q)) >> lgG;
+            sv[q] = *reinterpret_cast<const uint2 *>(vsz + gi * 16);
+            zv[q] = *reinterpret_cast<const uint2 *>(vsz + (ngi + gi) * 16);
+        }
 #pragma unroll
-        for (int o = 0; o < 2; ++o) {
-            const int ci = 2 * q + o, wi = ci / CPH, r = ci % CPH;
+        for (int r = 0; r < CPH; ++r) {
             const float off = slot_offset<VB, false>(r);
-            *reinterpret_cast<uint32_t *>(dst + ci * 128) = ck_affine(unpack<VB, false>(W[wi], r), off, s.x, z.x);
-            *reinterpret_cast<uint32_t *>(dst + D * 16 + ci * 128) =
-                ck_affine(unpack<VB, false>(W[NWV + wi], r), off, s.y, z.y);
+            *reinterpret_cast<uint32_t *>(dst + r * 128) =
+                ck_affine(unpack<VB, false>(W0, r), off, sv[r >> 1].x, zv[r >> 1].x);
+            *reinterpret_cast<uint32_t *>(dst + D * 16 + r * 128) =
+                ck_affine(unpack<VB, false>(W1, r), off, sv[r >> 1].y, zv[r >> 1].y);
         }
     }
 }
 
+// position in a ring of stages, and the phase its next use completes
+struct CkRing {
+    int s = 0;
+    unsigned p = 0;
+    __device__ __forceinline__ void next(int n) {
+        if (++s == n) {
+            s = 0;
+            p ^= 1u;
+        }
+    }
+};
+
+// One dequantizing warp's share of the tiles [0, n) of a piece, all of them
+// fully quantized: the loop that most of a long cache runs in, kept apart
+// (and short) from the tiles with fp16 tokens.  False if a wait ran out.
+template <int D, int KB, int VB>
+__device__ __forceinline__ bool packed_tiles(int n, CkRing &t, CkRing &r, unsigned char *sK, unsigned char *sV,
+                                             const unsigned char *sR, const KiviGeom &g, int rs, int w, uint64_t *bT,
+                                             uint64_t *eT, uint64_t *bR, uint64_t *eR, const volatile int *abort) {
+    constexpr int TB = kCkKeys * D * 2;
+    const int lane = threadIdx.x & 31, lgG = __ffs(g.G) - 1;
+    for (int x = 0; x < n; ++x) {
+        const bool ok = (x < kCkStages || mbar_wait_ab(&eT[t.s], t.p ^ 1u, abort)) && mbar_wait_ab(&bR[r.s], r.p, abort);
+        if (!__all_sync(0xffffffffu, ok)) return false;
+        const unsigned char *rec = sR + (size_t)r.s * g.rec_bytes;
+        dequant_keys<D, KB>(sK + t.s * TB, rec, g.off_ksz, lgG, w);
+        dequant_values<D, VB>(sV + t.s * TB, rec, g.off_vc, g.off_vsz, lgG, w);
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) {
+            mbar_arrive(&bT[t.s]);
+            mbar_arrive(&eR[r.s]);
+        }
+        t.next(kCkStages);
+        r.next(rs);
+    }
+    return true;
+}
+
 // Warps: 4 NH of softmax (thread tid owns row tid mod 128 of slot tid / 128,
 // tensor-memory columns [256 slot, + 256): S / P buffers in 0-63 and 64-127,
-// O from 128), kCkDq dequantizing, one issuing S = Q K^T, one O += P V.
+// O from 128), kCkDq dequantizing, one issuing S = Q K^T, one O += P V, one
+// copying records (an issue and its wait take long enough to hold a
+// dequantizing warp back).
 // They meet on mbarriers (bounded waits): a tile's K^ / V^ written,
 // read (MMA commits), S done, P written, P V done; records landed and read.
 template <int D, int NH>
-__global__ void __launch_bounds__(32 * (4 * NH + kCkDq + 2), 1)
+__global__ void __launch_bounds__(32 * (4 * NH + kCkDq + 3), 1)
     chunk_attn_kernel(KiviGeom g, KiviDev dv, const __half *__restrict__ Q, const __half *__restrict__ Kn,
                       const __half *__restrict__ Vn, __half *__restrict__ O, const __grid_constant__ ChunkArgs a) {
     extern __shared__ __align__(128) unsigned char smem[];
@@ -147,10 +194,10 @@ __global__ void __launch_bounds__(32 * (4 * NH + kCkDq + 2), 1)
     constexpr unsigned QLBO = kCkRows * 16, KLBO = kCkKeys * 16, VLBO = D * 16;
     constexpr int NSW = 4 * NH, CR = NH * kCkRows, TS = kCkStages;
     unsigned char *sQ = smem, *sK = sQ + NH * QB, *sV = sK + TS * TB, *sR = sV + TS * TB;
-    __shared__ __align__(8) uint64_t bars[7 + 4 * TS + 2 * kCkMaxRaw];
-    uint64_t *const bS = bars, *const bF = bars + 2, *const bP = bars + 4, *const bK = bars + 6, *const bV = bK + TS,
-                    *const eK = bV + TS, *const eV = eK + TS, *const bR = eV + TS, *const eR = bR + kCkMaxRaw,
-                    *const bX = eR + kCkMaxRaw;
+    constexpr int NB = 7 + 2 * TS + 2 * kCkMaxRaw;
+    __shared__ __align__(8) uint64_t bars[NB];
+    uint64_t *const bS = bars, *const bF = bars + 2, *const bP = bars + 4, *const bT = bars + 6, *const eT = bT + TS,
+                    *const bR = eT + TS, *const eR = bR + kCkMaxRaw, *const bX = eR + kCkMaxRaw;
     __shared__ uint32_t s_taddr;
     __shared__ int s_abort;   // a wait ran out: every warp stops
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -182,8 +229,8 @@ __global__ void __launch_bounds__(32 * (4 * NH + kCkDq + 2), 1)
         return;
     }
     if (tid == 0) {
-        for (int k = 0; k < 7 + 4 * TS + 2 * kCkMaxRaw; ++k) {
-            const bool written = k >= 6 && k < 6 + 2 * TS, read_raw = k >= 6 + 4 * TS + kCkMaxRaw;
+        for (int k = 0; k < NB; ++k) {
+            const bool written = k >= 6 && k < 6 + TS, read_raw = k >= 6 + 2 * TS + kCkMaxRaw;
             mbar_init(&bars[k], k == 4 || k == 5 ? NSW : written || read_raw ? kCkDq : 1);
         }
         fence_mbar_init();
@@ -207,20 +254,41 @@ __global__ void __launch_bounds__(32 * (4 * NH + kCkDq + 2), 1)
     const uint32_t taddr = s_taddr;
     const volatile int *abort = &s_abort;
     bool ok = true;
-    auto ph = [](int x, int m) { return (unsigned)(x / m) & 1u; };   // phase of use x of one of m stages
-
-    if (warp == NSW + kCkDq) {
+    const int nraw = min(nx, max(0, bl.virt((max(Tqk, Tqv) + kCkKeys - 1) / kCkKeys) - x0));   // tiles with records
+    if (warp == NSW + kCkDq + 2) {
+        // ---- records (lane 0) ----
+        if (lane == 0) {
+            const unsigned char *recs = dv.blk + rec_off(g, i, j, 0);
+            CkRing r;
+            int x = 0;
+            for (; x < nraw; ++x, r.next(a.rs)) {
+                ok = x < a.rs || mbar_wait_ab(&eR[r.s], r.p ^ 1u, abort);   // read
+                if (!ok) break;
+                mbar_expect_tx(&bR[r.s], (unsigned)g.rec_bytes);
+                bulk_g2s(sR + (size_t)r.s * g.rec_bytes, recs + (size_t)(tile0(x) / kCkKeys) * g.rec_bytes,
+                         (unsigned)g.rec_bytes, &bR[r.s]);
+            }
+            if (!ok) {
+                s_abort = 1;
+                atomicOr(dv.status, KIVI_FLAG_WAIT);
+            }
+            // every copy has landed before shared memory is given up (bounded)
+            for (int y = max(0, x - a.rs); y < x; ++y) mbar_wait(&bR[y % a.rs], (unsigned)(y / a.rs) & 1u);
+        }
+        __syncwarp();
+    } else if (warp == NSW + kCkDq) {
         // ---- S = Q K^T (lane 0) ----
         if (lane == 0) {
             constexpr uint32_t ID_S = tc_idesc_f16(kCkRows, kCkKeys, 0);
-            int done = 0;
-            for (int x = 0; x < nx; ++x) {
-                // its K^ written, its S buffer free (P V of tile x - 2 read its weights there)
-                ok = mbar_wait_ab(&bK[x % TS], ph(x, TS), abort) &&
-                     (x < 2 || mbar_wait_ab(&bF[x & 1], ph(x - 2, 2), abort));
+            CkRing t;
+            int x = 0;
+            for (; x < nx; ++x, t.next(TS)) {
+                // its tile written, its S buffer free (P V of tile x - 2 read its weights there)
+                ok = mbar_wait_ab(&bT[t.s], t.p, abort) &&
+                     (x < 2 || mbar_wait_ab(&bF[x & 1], (unsigned)((x >> 1) + 1) & 1u, abort));
                 if (!ok) break;
                 tc_fence_after();
-                const unsigned char *k = sK + (x % TS) * TB;
+                const unsigned char *k = sK + t.s * TB;
 #pragma unroll
                 for (int e = 0; e < NH; ++e)
 #pragma unroll
@@ -228,29 +296,28 @@ __global__ void __launch_bounds__(32 * (4 * NH + kCkDq + 2), 1)
                         tc_mma_f16(taddr + 256 * e + 64 * (x & 1), tc_desc(sQ + e * QB + 2 * c * QLBO, QLBO, 128),
                                    tc_desc(k + 2 * c * KLBO, KLBO, 128), ID_S, c > 0);
                 tc_commit(&bS[x & 1]);
-                tc_commit(&eK[x % TS]);
-                done = x + 1;
             }
             if (!ok) {
                 s_abort = 1;
                 atomicOr(dv.status, KIVI_FLAG_WAIT);
             }
             // every commit has landed before shared memory is given up (bounded)
-            for (int x = max(0, done - 2); x < done; ++x) mbar_wait(&bS[x & 1], ph(x, 2));
-            for (int x = max(0, done - TS); x < done; ++x) mbar_wait(&eK[x % TS], ph(x, TS));
+            for (int y = max(0, x - 2); y < x; ++y) mbar_wait(&bS[y & 1], (unsigned)(y >> 1) & 1u);
         }
         __syncwarp();
     } else if (warp == NSW + kCkDq + 1) {
         // ---- O += P V (lane 0) ----
         if (lane == 0) {
             constexpr uint32_t ID_R = tc_idesc_f16(kCkRows, D, 1), ID_T = tc_idesc_f16(kCkRows, D, 0);
-            int done = 0;
-            for (int x = 0; x < nx; ++x) {
-                ok = mbar_wait_ab(&bP[x & 1], ph(x, 2), abort) && mbar_wait_ab(&bV[x % TS], ph(x, TS), abort);
+            CkRing t;
+            int x = 0;
+            for (; x < nx; ++x, t.next(TS)) {
+                const bool transposed = tile0(x) < Tqv;
+                // (its P written: S read the tile, which was written before)
+                ok = mbar_wait_ab(&bP[x & 1], (unsigned)(x >> 1) & 1u, abort) && mbar_wait_ab(&bT[t.s], t.p, abort);
                 if (!ok) break;
                 tc_fence_after();
-                const unsigned char *v = sV + (x % TS) * TB;
-                const bool transposed = tile0(x) < Tqv;
+                const unsigned char *v = sV + t.s * TB;
 #pragma unroll
                 for (int e = 0; e < NH; ++e)
 #pragma unroll
@@ -260,31 +327,22 @@ __global__ void __launch_bounds__(32 * (4 * NH + kCkDq + 2), 1)
                                                  : tc_desc(v + 256 * c, 128, KLBO),
                                       transposed ? ID_T : ID_R, x > 0 || c > 0);
                 tc_commit(&bF[x & 1]);
-                tc_commit(&eV[x % TS]);
-                done = x + 1;
+                tc_commit(&eT[t.s]);
             }
             if (!ok) {
                 s_abort = 1;
                 atomicOr(dv.status, KIVI_FLAG_WAIT);
             }
-            for (int x = max(0, done - 2); x < done; ++x) mbar_wait(&bF[x & 1], ph(x, 2));
-            for (int x = max(0, done - TS); x < done; ++x) mbar_wait(&eV[x % TS], ph(x, TS));
+            for (int y = max(0, x - 2); y < x; ++y) mbar_wait(&bF[y & 1], (unsigned)(y >> 1) & 1u);
+            for (int y = max(0, x - TS); y < x; ++y) mbar_wait(&eT[y % TS], (unsigned)(y / TS) & 1u);
         }
         __syncwarp();
     } else if (warp >= NSW) {
         // ---- K^ and V^ tiles ----
         const int w = warp - NSW, dt = tid - 32 * NSW;   // dt: 0 .. 127
         const int lgG = __ffs(g.G) - 1;
-        const int nraw = min(nx, max(0, bl.virt((max(Tqk, Tqv) + kCkKeys - 1) / kCkKeys) - x0));   // tiles with records
-        const unsigned char *recs = dv.blk + rec_off(g, i, j, 0);
         const __half *kwin = dv.Kf + kf_slice(g, i, j), *vwin = dv.Vf + vf_slice(g, i, j);
         const __half *kch = Kn + ((size_t)i * g.h + j) * a.n_stride * D, *vch = Vn + ((size_t)i * g.h + j) * a.n_stride * D;
-        auto issue_raw = [&](int x) {   // dt == 0
-            uint64_t *bar = &bR[x % a.rs];
-            mbar_expect_tx(bar, (unsigned)g.rec_bytes);
-            bulk_g2s(sR + (size_t)(x % a.rs) * g.rec_bytes, recs + (size_t)(tile0(x) / kCkKeys) * g.rec_bytes,
-                     (unsigned)g.rec_bytes, bar);
-        };
         // the dequantizing warps meet (a bounded wait, unlike a named barrier)
         int meets = 0;
         auto meet = [&]() {
@@ -292,32 +350,26 @@ __global__ void __launch_bounds__(32 * (4 * NH + kCkDq + 2), 1)
             if (lane == 0) mbar_arrive(bX);
             return __all_sync(0xffffffffu, mbar_wait_ab(bX, (unsigned)meets++ & 1u, abort)) != 0;
         };
-        int issued = 0;
-        if (dt == 0)
-            for (; issued < min(nraw, a.rs); ++issued) issue_raw(issued);
         // fp16 rows: token tau's row in the window or the chunk (zero past the chunk)
         auto row16 = [&](const __half *win, int ring, const __half *chk, int tau, int c) {
             const __half *src = tau < T ? win + (size_t)(tau % ring) * D : chk + (size_t)(tau - T) * D;
             return tau < T + n ? *reinterpret_cast<const uint4 *>(src + 8 * c) : make_uint4(0u, 0u, 0u, 0u);
         };
         constexpr int CPR = D / 8, RPT = kCkKeys * CPR / 128;   // 16-byte chunks a row; a thread's share of a tile
-        for (int x = 0; x < nx; ++x) {
-            const int tb = tile0(x), s = x % TS;
-            unsigned char *kt = sK + s * TB, *vt = sV + s * TB;
+        CkRing t, r;   // this tile's and record's stages
+        const int npk = min(nx, max(0, bl.virt(min(Tqk, Tqv) / kCkKeys) - x0));   // fully quantized tiles
+        if (g.kbits == 2)
+            ok = g.vbits == 2 ? packed_tiles<D, 2, 2>(npk, t, r, sK, sV, sR, g, a.rs, w, bT, eT, bR, eR, abort)
+                              : packed_tiles<D, 2, 4>(npk, t, r, sK, sV, sR, g, a.rs, w, bT, eT, bR, eR, abort);
+        else
+            ok = g.vbits == 2 ? packed_tiles<D, 4, 2>(npk, t, r, sK, sV, sR, g, a.rs, w, bT, eT, bR, eR, abort)
+                              : packed_tiles<D, 4, 4>(npk, t, r, sK, sV, sR, g, a.rs, w, bT, eT, bR, eR, abort);
+        // the others: some or all tokens in the window or the chunk
+        for (int x = npk; x < nx && ok; ++x, t.next(TS)) {
+            const int tb = tile0(x);
+            unsigned char *kt = sK + t.s * TB, *vt = sV + t.s * TB;
             const bool raw = x < nraw;
             const bool kq = tb < Tqk, kall = tb + kCkKeys <= Tqk, vq = tb < Tqv, vall = tb + kCkKeys <= Tqv;
-            // a record a few tiles ahead, into the stage that tile x - 1 has been read from
-            if (x > 0 && x - 1 + a.rs < nraw) {
-                if (dt == 0) {
-                    ok = mbar_wait_ab(&eR[(x - 1) % a.rs], ph(x - 1, a.rs), abort);
-                    if (ok) {
-                        issue_raw(x - 1 + a.rs);
-                        ++issued;
-                    }
-                }
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-            }
             uint4 kr[RPT], vr[RPT];   // fp16 tiles: loads in flight before the waits
             if (!kq)
 #pragma unroll
@@ -327,11 +379,10 @@ __global__ void __launch_bounds__(32 * (4 * NH + kCkDq + 2), 1)
 #pragma unroll
                 for (int k = 0; k < RPT; ++k)
                     vr[k] = row16(vwin, g.R + 1, vch, tb + (dt + 128 * k) / CPR, (dt + 128 * k) % CPR);
-            ok = (x < TS || mbar_wait_ab(&eK[s], ph(x - TS, TS), abort)) &&
-                 (!raw || mbar_wait_ab(&bR[x % a.rs], ph(x, a.rs), abort));
+            ok = (x < TS || mbar_wait_ab(&eT[t.s], t.p ^ 1u, abort)) && (!raw || mbar_wait_ab(&bR[r.s], r.p, abort));
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
-            const unsigned char *rec = sR + (size_t)(x % a.rs) * g.rec_bytes;
+            const unsigned char *rec = sR + (size_t)r.s * g.rec_bytes;
             if (kq) {
                 if (g.kbits == 2) dequant_keys<D, 2>(kt, rec, g.off_ksz, lgG, w);
                 else dequant_keys<D, 4>(kt, rec, g.off_ksz, lgG, w);
@@ -347,11 +398,6 @@ __global__ void __launch_bounds__(32 * (4 * NH + kCkDq + 2), 1)
                 for (int k = 0; k < RPT; ++k)
                     *reinterpret_cast<uint4 *>(kt + ((dt + 128 * k) % CPR) * KLBO + (dt + 128 * k) / CPR * 16) = kr[k];
             }
-            fence_proxy_async();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bK[s]);
-            ok = __all_sync(0xffffffffu, x < TS || mbar_wait_ab(&eV[s], ph(x - TS, TS), abort));
-            if (!ok) break;
             if (vq) {
                 if (g.vbits == 2) dequant_values<D, 2>(vt, rec, g.off_vc, g.off_vsz, lgG, w);
                 else dequant_values<D, 4>(vt, rec, g.off_vc, g.off_vsz, lgG, w);
@@ -375,16 +421,15 @@ __global__ void __launch_bounds__(32 * (4 * NH + kCkDq + 2), 1)
             fence_proxy_async();
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(&bV[s]);
-                if (raw) mbar_arrive(&eR[x % a.rs]);
+                mbar_arrive(&bT[t.s]);
+                if (raw) mbar_arrive(&eR[r.s]);
             }
+            if (raw) r.next(a.rs);
         }
         if (!ok && lane == 0) {
             s_abort = 1;
             atomicOr(dv.status, KIVI_FLAG_WAIT);
         }
-        if (dt == 0)   // every record copy has landed (bounded)
-            for (int x = max(0, issued - a.rs); x < issued; ++x) mbar_wait(&bR[x % a.rs], ph(x, a.rs));
         __syncwarp();
     } else {
         // ---- the softmax warps ----
@@ -398,7 +443,7 @@ __global__ void __launch_bounds__(32 * (4 * NH + kCkDq + 2), 1)
         float mref = -INFINITY, lsum = 0.f;   // the row's reference maximum (raw score units) and weight sum
         for (int x = 0; x < nx; ++x) {
             const int b = x & 1, key0 = tile0(x);
-            ok = __all_sync(0xffffffffu, mbar_wait_ab(&bS[b], ph(x, 2), abort));
+            ok = __all_sync(0xffffffffu, mbar_wait_ab(&bS[b], (unsigned)(x >> 1) & 1u, abort));
             if (!ok) break;
             tc_fence_after();
             const uint32_t tS = tH + 64 * b;
@@ -441,7 +486,7 @@ __global__ void __launch_bounds__(32 * (4 * NH + kCkDq + 2), 1)
             }
             lsum = lsum * alpha + ((l4[0] + l4[1]) + (l4[2] + l4[3]));
             if (x > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {   // rescale O, once P V of tile x - 1 is in
-                ok = __all_sync(0xffffffffu, mbar_wait_ab(&bF[b ^ 1], ph(x - 1, 2), abort));
+                ok = __all_sync(0xffffffffu, mbar_wait_ab(&bF[b ^ 1], (unsigned)((x - 1) >> 1) & 1u, abort));
                 if (!ok) break;
                 tc_fence_after();
 #pragma unroll
@@ -460,7 +505,7 @@ __global__ void __launch_bounds__(32 * (4 * NH + kCkDq + 2), 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&bP[b]);
         }
-        if (ok) ok = __all_sync(0xffffffffu, mbar_wait_ab(&bF[(nx - 1) & 1], ph(nx - 1, 2), abort));
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait_ab(&bF[(nx - 1) & 1], (unsigned)((nx - 1) >> 1) & 1u, abort));
         if (!ok) {
             if (lane == 0) {
                 s_abort = 1;
@@ -554,7 +599,7 @@ cudaError_t launch_chunk(const KiviGeom &g, const KiviDev &dv, const __half *Q, 
     const size_t smem = fixed + (size_t)a.rs * g.rec_bytes;
     cudaError_t e = cudaFuncSetAttribute(chunk_attn_kernel<D, NH>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    chunk_attn_kernel<D, NH><<<ctas, 32 * (4 * NH + kCkDq + 2), smem, st>>>(g, dv, Q, K, V, O, a);
+    chunk_attn_kernel<D, NH><<<ctas, 32 * (4 * NH + kCkDq + 3), smem, st>>>(g, dv, Q, K, V, O, a);
     e = cudaGetLastError();
     if (e != cudaSuccess || !join) return e;
     chunk_join_kernel<D><<<dim3((maxrows + 7) / 8, g.h, g.b), 256, 0, st>>>(g, O, a, NH * kCkRows);
