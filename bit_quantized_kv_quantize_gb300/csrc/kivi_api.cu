@@ -365,7 +365,14 @@ kivi_status prefill_attn(kivi_cache_t c, const void *q, const void *K, const voi
                          int h_q, Visible vis, void *out, kivi_stream_t stream) {
     kivi_status s = check_handle(c);
     if (s != KIVI_OK) return s;
-    if (vis.window > 0 && (s = check_device(c)) != KIVI_OK) return s;
+    if (vis.window > 0) {
+        s = check_device(c);
+        if (s != KIVI_OK) return s;
+        if (t_stride > 0 && (long long)c->g.b * c->g.h * t_stride >= (1LL << 31)) {
+            set_err("b h_kv t_stride must be below 2^31");
+            return KIVI_ERR_UNSUPPORTED;
+        }
+    }
     if (c->g.G > 64 || (c->g.d != 64 && c->g.d != 128)) {
         set_err("prefill attention supports d 64 or 128 and G <= 64");
         return KIVI_ERR_UNSUPPORTED;
@@ -400,8 +407,28 @@ kivi_status prefill_attn(kivi_cache_t c, const void *q, const void *K, const voi
         set_err("q, K, V and out must be 16-byte aligned");
         return KIVI_ERR_INVALID_ARG;
     }
-    cudaError_t e = kivi_launch_prefill_attn(c->g, c->dv, (const __half *)q, (const __half *)K, (const __half *)V,
-                                             (__half *)out, lens, t_stride, h_q, (cudaStream_t)stream, vis);
+    cudaError_t e;
+    if (vis.window > 0) {
+        // the cache by the prefill's pack kernels (an epilogue that packs in
+        // the attention's CTAs takes longer than it saves once the attention
+        // itself is short: 4k tokens of 32 heads, window 1024, 231 against
+        // 127 + 45 us), the attention as a chunk's with nothing cached
+        ChunkArgs a;
+        for (int i = 0; i < c->g.b; ++i) {
+            a.T[i] = a.Tqk[i] = a.Tqv[i] = 0;
+            a.n[i] = t[i];
+        }
+        a.n_stride = t_stride;
+        a.hq = h_q;
+        a.vis = vis;
+        e = kivi_launch_prefill(c->g, c->dv, (const __half *)K, (const __half *)V, lens, t_stride, (cudaStream_t)stream);
+        if (e == cudaSuccess)
+            e = kivi_launch_chunk_attn(c->g, c->dv, (const __half *)q, (const __half *)K, (const __half *)V,
+                                       (__half *)out, a, c->chunk_part, c->num_sms, (cudaStream_t)stream);
+    } else {
+        e = kivi_launch_prefill_attn(c->g, c->dv, (const __half *)q, (const __half *)K, (const __half *)V,
+                                     (__half *)out, lens, t_stride, h_q, (cudaStream_t)stream);
+    }
     if (e != cudaSuccess) return fail_cuda(c, e, "prefill_attn");
     for (int i = 0; i < c->g.b; ++i) {
         c->T[i] = t[i];
@@ -654,6 +681,10 @@ kivi_status kivi_chunk_attn(kivi_cache_t c, const void *q, const void *K, const 
     if (!aligned16(q) || !aligned16(out)) {
         set_err("q and out must be 16-byte aligned");
         return KIVI_ERR_INVALID_ARG;
+    }
+    if ((long long)c->g.b * c->g.h * n_stride >= (1LL << 31)) {
+        set_err("b h_kv n_stride must be below 2^31");
+        return KIVI_ERR_UNSUPPORTED;
     }
     a.hq = h_q;
     a.vis = Visible{window, sinks};

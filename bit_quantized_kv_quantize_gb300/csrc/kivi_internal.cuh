@@ -366,11 +366,10 @@ cudaError_t kivi_launch_prefill(const KiviGeom &g, const KiviDev &dv, const __ha
 // The prefill with its causal attention (kivi_prefill_attn.cu): O = the
 // attention of Q over K, V (fp16 [b][hq][t_stride][d] and [b][h][t_stride][d])
 // and the cache filled as kivi_launch_prefill fills it.  d in {64, 128},
-// G <= 64 (cudaErrorInvalidValue otherwise).  vis: what each query sees of
-// the tokens up to its own (the cache takes every token).
+// G <= 64 (cudaErrorInvalidValue otherwise).
 cudaError_t kivi_launch_prefill_attn(const KiviGeom &g, const KiviDev &dv, const __half *Q, const __half *K,
                                      const __half *V, __half *O, const SeqLens &lens, int t_stride, int hq,
-                                     cudaStream_t st, Visible vis = Visible{0, 0});
+                                     cudaStream_t st);
 // nxt: the other counter set ([3][b]: T, Tqk, Tqv), which receives the
 // counters after the append (dv's set is left as it was).
 // only_flush: append only the sequences whose key window is full now (the
