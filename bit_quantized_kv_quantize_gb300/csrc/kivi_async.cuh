@@ -41,6 +41,7 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t *bar, unsigned phase) {
 
 // bounded wait: false if the barrier did not complete within the limit
 __device__ __forceinline__ bool mbar_wait(uint64_t *bar, unsigned phase) {
+#pragma unroll 1
     for (int it = 0; it < kMaxWaitIters; ++it)
         if (mbar_try_wait(bar, phase)) return true;
     return false;
@@ -57,6 +58,7 @@ __device__ __forceinline__ void bulk_g2s(void *dst, const void *src, unsigned by
 // A wait that also gives up when another warp of the CTA has given up
 // (*abort set): false then, or after the iteration limit.
 __device__ __forceinline__ bool mbar_wait_ab(uint64_t *bar, unsigned phase, const volatile int *abort) {
+#pragma unroll 1   // (short code: the kernels wait in many places)
     for (int it = 0; it < kMaxWaitIters; ++it) {
         unsigned ok;
         asm volatile(

@@ -5,30 +5,51 @@
 
 // One chunk call (kernel parameters): per sequence the cache's counters and
 // the chunk's tokens, from the host mirror; the attention's work list: the
-// units of sequence i (each row tile of each kv head: kCkLead, then one a key
-// tile; ordered by row tile, then head) are [ustart[i], ustart[i + 1]).
+// units are each row tile of each kv head (kCkLead, then one a key tile; by
+// sequence, row tile, head), and CTA c takes those from cta[c] up to
+// cta[c + 1].
+constexpr int kCkMaxCtas = 256;
+struct ChunkPos {
+    long long u;    // units before it
+    int i, m, j;    // the row tile it lies in: sequence, row tile, kv head
+    int o;          // its offset there
+};
 struct ChunkArgs {
-    int hq, n_stride;
+    int hq, hg, n_stride;         // hg: query heads a kv head
+    unsigned hg_mul;              // ceil(2^32 / hg): x / hg = umulhi(x, hg_mul) for x < 2^29 (hg <= 8)
     int rs;           // record stages
+    int tile_rows, tile_blocks;   // rows of a row tile, 64-token blocks of a key tile
     Visible vis;
-    float *acc, *ml;  // partials: [2 CTAs][kCkTileRows][d] and [2 CTAs][kCkTileRows][2]
+    float *acc, *ml;  // partials: [2 CTAs][tile_rows][d] and [2 CTAs][tile_rows][2]
+    int ctas;
+    ChunkPos cta[kCkMaxCtas + 1];
     int T[KIVI_MAX_BATCH], Tqk[KIVI_MAX_BATCH], Tqv[KIVI_MAX_BATCH], n[KIVI_MAX_BATCH];
-    long long ustart[KIVI_MAX_BATCH + 1];
 };
 
-constexpr int kCkTileRows = 256;   // rows of a row tile
-constexpr int kCkLead = 4;         // units that stand for a row tile's fixed cost
+constexpr int kCkLead = 4;   // units that stand for a row tile's fixed cost
 
-// Row tiles of a kv head with hg query heads, and the key tiles (64-token
-// blocks) that row tile m of sequence i sees.
-__host__ __device__ __forceinline__ int chunk_row_tiles(int n, int hg) {
-    return (n * hg + kCkTileRows - 1) / kCkTileRows;
+// x / hg
+__host__ __device__ __forceinline__ int chunk_div(const ChunkArgs &a, int x) {
+#ifdef __CUDA_ARCH__
+    return a.hg == 1 ? x : (int)__umulhi((unsigned)x, a.hg_mul);
+#else
+    return x / a.hg;
+#endif
 }
-__host__ __device__ __forceinline__ int chunk_tiles(const ChunkArgs &a, int i, int m, int hg) {
-    const int r0 = m * kCkTileRows / hg, r1 = (m * kCkTileRows + kCkTileRows - 1) / hg;
+// Row tiles of sequence i's kv heads, and the 64-token blocks and key tiles
+// that its row tile m sees.
+__host__ __device__ __forceinline__ int chunk_row_tiles(const ChunkArgs &a, int i) {
+    return (a.n[i] * a.hg + a.tile_rows - 1) / a.tile_rows;
+}
+__host__ __device__ __forceinline__ int chunk_blocks(const ChunkArgs &a, int i, int m) {
+    const int r0 = chunk_div(a, m * a.tile_rows), r1 = chunk_div(a, m * a.tile_rows + a.tile_rows - 1);
     const int last = r1 < a.n[i] - 1 ? r1 : a.n[i] - 1;
     return visible_blocks(a.vis, a.T[i] + r0).virt((a.T[i] + last) / KIVI_KBLK + 1);
 }
+__host__ __device__ __forceinline__ int chunk_tiles(const ChunkArgs &a, int i, int m) {
+    return (chunk_blocks(a, i, m) + a.tile_blocks - 1) / a.tile_blocks;   // 1 or 2 blocks a tile
+}
+
 // Counters after n one-token appends (item 4's lazy maintenance: a full key
 // window flushes, and a value queue of R + 1 pops, at the start of the next
 // append).
@@ -43,8 +64,8 @@ __host__ __device__ __forceinline__ int chunk_tqv(int T, int Tqv, int n, int R) 
 
 // floats of the attention's partials buffer of a cache with head dimension d
 size_t kivi_chunk_partial_floats(int d, int num_sms);
-// The attention of the chunk (kivi_chunk_attn.cu).  a: everything but rs, acc,
-// ml, ustart.  d in {64, 128} (cudaErrorInvalidValue otherwise).
+// The attention of the chunk (kivi_chunk_attn.cu).  a: hq, n_stride, vis, T,
+// Tqk, Tqv and n.  d in {64, 128} (cudaErrorInvalidValue otherwise).
 cudaError_t kivi_launch_chunk_attn(const KiviGeom &g, const KiviDev &dv, const __half *Q, const __half *K,
                                    const __half *V, __half *O, ChunkArgs &a, float *partials, int num_sms,
                                    cudaStream_t st);

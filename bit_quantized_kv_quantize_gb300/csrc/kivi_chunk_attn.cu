@@ -4,6 +4,10 @@
 
 #include "kivi_chunk_attn_impl.cuh"
 
+// (kivi_chunk_few.cu)
+cudaError_t kivi_launch_chunk_few(const KiviGeom &, const KiviDev &, const __half *, const __half *, const __half *,
+                                  __half *, ChunkArgs &, int, cudaStream_t);
+
 namespace {
 
 template <int D>
@@ -17,7 +21,7 @@ cudaError_t launch_chunk(const KiviGeom &g, const KiviDev &dv, const __half *Q, 
     CUtensorMap tq, tk, tv;
     memset(&tq, 0, sizeof tq);   // unused with a head group that does not divide 128
     const long long rows = (long long)g.b * g.h * a.n_stride;
-    const int hg = a.hq / g.h;
+    const int hg = a.hg;
     cudaError_t e = make_tile_map(&tk, K, rows, D, kCkKeys);
     if (e == cudaSuccess && kCkRows % hg == 0)
         e = make_group_rows_map(&tq, Q, (long long)g.b * g.h, hg, a.n_stride, D);
@@ -26,21 +30,6 @@ cudaError_t launch_chunk(const KiviGeom &g, const KiviDev &dv, const __half *Q, 
         e = cudaFuncSetAttribute(chunk_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     chunk_attn_kernel<D><<<ctas, kCkThreads, smem, st>>>(g, dv, Q, K, V, O, tq, tk, tv, a);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    // does a CTA's range start behind the first tile of a row tile?
-    const long long U = a.ustart[g.b];
-    bool join = false;
-    long long P = 0;   // the first unit of (i, m)
-    for (int i = 0, c = 1; i < g.b && !join; ++i)
-        for (int m = 0; m < chunk_row_tiles(a.n[i], hg) && !join; ++m) {
-            const int w = kCkLead + chunk_tiles(a, i, m, hg);
-            const long long end = P + (long long)g.h * w;
-            for (; c < ctas && (long long)c * U / ctas < end; ++c) join |= ((long long)c * U / ctas - P) % w > kCkLead;
-            P = end;
-        }
-    if (!join) return cudaSuccess;
-    chunk_join_kernel<D><<<(ctas - 1) * (kCkTileRows / 32), 256, 0, st>>>(g, O, a, ctas);
     return cudaGetLastError();
 }
 
@@ -56,26 +45,55 @@ cudaError_t kivi_launch_chunk_attn(const KiviGeom &g, const KiviDev &dv, const _
     if (g.d != 64 && g.d != 128) return cudaErrorInvalidValue;
     if ((long long)g.b * g.h * a.n_stride >= (1LL << 31)) return cudaErrorInvalidValue;   // TMA row coordinates
     const int hg = a.hq / g.h;
+    a.hg = hg;
+    a.hg_mul = (unsigned)(((1ull << 32) + hg - 1) / hg);
     int maxrows = 0;
-    long long items = 0;
-    a.ustart[0] = 0;
-    for (int i = 0; i < g.b; ++i) {
-        const int mt = chunk_row_tiles(a.n[i], hg);
-        long long u = 0;
-        for (int m = 0; m < mt; ++m) u += kCkLead + chunk_tiles(a, i, m, hg);
-        a.ustart[i + 1] = a.ustart[i] + u * g.h;
-        items += (long long)mt * g.h;
-        maxrows = a.n[i] * hg > maxrows ? a.n[i] * hg : maxrows;
-    }
+    for (int i = 0; i < g.b; ++i) maxrows = a.n[i] * hg > maxrows ? a.n[i] * hg : maxrows;
     if (maxrows == 0) return cudaSuccess;
-    // One CTA an SM; where the row tiles are short (a CTA's share below 16
-    // units), one a row tile, or one a few of them: cutting them would cost
-    // more than it balances.
-    const long long U = a.ustart[g.b];
-    long long ctas = num_sms;
-    if (U < 16 * ctas) ctas = items < ctas ? items : ctas;
+    // Up to 64 rows a kv head: the transposed kernel, whose work follows the
+    // rows (4 tokens of 8 sequences over 32k: 244 us with 256-row tiles).
+    const bool few = maxrows <= 64;
+    a.tile_rows = !few ? kCkTileRows : maxrows <= 16 ? 16 : maxrows <= 32 ? 32 : 64;
+    a.tile_blocks = few ? 2 : 1;
+    long long items = 0, U = 0;
+    for (int i = 0; i < g.b; ++i) {
+        const int mt = chunk_row_tiles(a, i);
+        long long u = 0;
+        for (int m = 0; m < mt; ++m) u += kCkLead + chunk_tiles(a, i, m);
+        U += u * g.h;
+        items += (long long)mt * g.h;
+    }
+    // One CTA an SM, but no share below 2 kCkLead units unless the row tiles
+    // are that short: cutting them finer costs more than it shortens.
+    const long long sms = num_sms < kCkMaxCtas ? num_sms : kCkMaxCtas;
+    const long long want = U / (2 * kCkLead) > items ? U / (2 * kCkLead) : items;
+    const int ctas = (int)(want < sms ? want : sms);
+    // each CTA's first unit, and whether one lies behind the first key tile of
+    // a row tile (whose partials are then joined)
+    bool join = false;
+    long long P = 0;   // the first unit of (i, m)
+    int c = 0;
+    for (int i = 0; i < g.b; ++i)
+        for (int m = 0; m < chunk_row_tiles(a, i); ++m) {
+            const int w = kCkLead + chunk_tiles(a, i, m);
+            const long long end = P + (long long)g.h * w;
+            for (; c < ctas && (long long)c * U / ctas < end; ++c) {
+                const long long u = (long long)c * U / ctas;
+                a.cta[c] = ChunkPos{u, i, m, (int)((u - P) / w), (int)((u - P) % w)};
+                join |= a.cta[c].o > kCkLead;
+            }
+            P = end;
+        }
+    a.ctas = ctas;
+    a.cta[ctas] = ChunkPos{U, 0, 0, 0, 0};
     a.acc = partials;
     a.ml = partials + (size_t)2 * num_sms * kCkTileRows * g.d;
-    return g.d == 64 ? launch_chunk<64>(g, dv, Q, K, V, O, a, (int)ctas, st)
-                     : launch_chunk<128>(g, dv, Q, K, V, O, a, (int)ctas, st);
+    cudaError_t e = few ? kivi_launch_chunk_few(g, dv, Q, K, V, O, a, ctas, st)
+                    : g.d == 64 ? launch_chunk<64>(g, dv, Q, K, V, O, a, ctas, st)
+                                : launch_chunk<128>(g, dv, Q, K, V, O, a, ctas, st);
+    if (e != cudaSuccess || !join) return e;
+    const unsigned blocks = (unsigned)(ctas - 1) * (a.tile_rows / kJoinRows);
+    if (g.d == 64) chunk_join_kernel<64><<<blocks, 256, 0, st>>>(O, a);
+    else chunk_join_kernel<128><<<blocks, 256, 0, st>>>(O, a);
+    return cudaGetLastError();
 }

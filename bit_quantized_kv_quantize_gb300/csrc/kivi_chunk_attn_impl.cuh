@@ -43,35 +43,20 @@
 // CTAs share leaves unnormalized partials (max, sum, O), joined by a second
 // kernel.
 #pragma once
-#include <cuda_fp16.h>
-
-#include "kivi_async.cuh"
-#include "kivi_chunk.cuh"
-#include "kivi_internal.cuh"
-#include "kivi_mma.cuh"
+#include "kivi_chunk_tiles.cuh"
 #include "kivi_tcgen05.cuh"
 #include "kivi_tma.cuh"
-#include "kivi_unpack.cuh"
 
 namespace {
 
 constexpr int kCkRows = 128;     // rows of a slot
+constexpr int kCkTileRows = 2 * kCkRows;
 constexpr int kCkKeys = KIVI_KBLK;   // tokens of a tile
 constexpr int kCkStages = 3;     // K^ tiles, and V^ tiles, in flight
 constexpr int kCkMaxRaw = 8;     // records in flight
-constexpr int kCkDq = 4;         // dequantizing warps
+constexpr int kCkDq = kCkDqGroup;   // dequantizing warps
 constexpr int kCkOut = 8 * 32 * 64;   // a softmax warp's 32 rows x 32 columns of the output
 constexpr int kCkThreads = 32 * (8 + kCkDq + 3);
-constexpr unsigned kFull = 0xffffffffu;
-
-__device__ __forceinline__ uint32_t ck_pack(float lo, float hi) {
-    return h2u(__floats2half2_rn(lo, hi));
-}
-// s code + z of two values, the code from off + code (exact)
-__device__ __forceinline__ uint32_t ck_affine(uint32_t x, float off, uint32_t s, uint32_t z) {
-    return h2u(__hfma2(__hsub2(u2h(x), __float2half2_rn(off)), u2h(s), u2h(z)));
-}
-
 
 // {a, b} as one 64-bit operand of the packed fp32 instructions
 __device__ __forceinline__ unsigned long long ck_f2(float a, float b) {
@@ -93,190 +78,6 @@ __device__ __forceinline__ unsigned long long ck_add2(unsigned long long a, unsi
     return r;
 }
 
-// K^ of a record's 64 tokens: chunk-major tile [64 tokens][D], 16-byte chunk
-// c of token r at byte c 1024 + r 16.  Warp w of the kCkDq takes the
-// 16-channel steps w, w + kCkDq, ...; a lane's half2 (two channels of one token) are
-// the lanes t = 0..3 of one 16-byte chunk: 128 consecutive bytes a store.
-template <int D, int KB>
-__device__ __forceinline__ void dequant_keys(unsigned char *tile, const unsigned char *rec, int off_ksz, int lgG,
-                                             int w) {
-    const int lane = threadIdx.x & 31, gq = lane >> 2, tq = lane & 3;
-    const __half *ksz = reinterpret_cast<const __half *>(rec + off_ksz) + tq * (D / 4);
-    unsigned char *dst = tile + gq * 16 + tq * 4;
-    constexpr int NW = KB / 2;   // words of a channel pair
-    // one 16-channel step a turn, not unrolled (see dequant_values)
-#pragma unroll 1
-    for (int j = w; j < D / 16; j += kCkDq) {
-        // every load before the first store: the compiler keeps their order
-        uint32_t W[2 * NW];
-        const unsigned char *pw = rec + (size_t)((j * 2 * NW) >> 2) * 512 + lane * 16 + ((j * 2 * NW) & 3) * 4;
-        if (KB == 2) {
-            const uint2 v = *reinterpret_cast<const uint2 *>(pw);
-            W[0] = v.x;
-            W[1] = v.y;
-        } else {
-            const uint4 v = *reinterpret_cast<const uint4 *>(pw);
-            W[0] = v.x;
-            W[1] = v.y;
-            W[NW] = v.z;
-            W[2 * NW - 1] = v.w;
-        }
-        uint2 sv[4], zv[4];
-#pragma unroll
-        for (int qd = 0; qd < 4; ++qd) {   // 16 tokens share a group row
-            const __half *row = ksz + (((16 * qd) >> lgG) * 2) * D + 4 * j;
-            sv[qd] = *reinterpret_cast<const uint2 *>(row);
-            zv[qd] = *reinterpret_cast<const uint2 *>(row + D);
-        }
-        unsigned char *p = dst + (size_t)(2 * j) * (kCkKeys * 16);
-#pragma unroll
-        for (int pos = 0; pos < 8; ++pos) {
-            const int wi = KB == 2 ? 0 : pos >> 2, r = KB == 2 ? pos : pos & 3;
-            const float off = slot_offset<KB, true>(r);
-            const uint2 sc = sv[pos >> 1], z = zv[pos >> 1];
-            *reinterpret_cast<uint32_t *>(p + pos * 128) = ck_affine(unpack<KB, true>(W[wi], r), off, sc.x, z.x);
-            *reinterpret_cast<uint32_t *>(p + kCkKeys * 16 + pos * 128) =
-                ck_affine(unpack<KB, true>(W[NW + wi], r), off, sc.y, z.y);
-        }
-    }
-}
-
-// V^ of a record's 64 tokens, transposed: chunk-major tile [D channels][64
-// tokens], tokens 8 k .. 8 k + 7 of channel c at byte k D 16 + c 16.  Warp w
-// takes value block w (16 tokens).
-template <int D, int VB>
-__device__ __forceinline__ void dequant_values(unsigned char *tile, const unsigned char *rec, int off_vc, int off_vsz,
-                                               int lgG, int w) {
-    constexpr int WL = D * VB / 64, CS = WL < 4 ? WL : 4, NWV = D * VB / 128, CPH = 16 / VB;
-    const int lane = threadIdx.x & 31, gq = lane >> 2, tq = lane & 3;
-    const int ngi = D >> lgG;
-    const uint32_t *words = reinterpret_cast<const uint32_t *>(rec + off_vc) + (size_t)w * (D * VB / 2) + lane * CS;
-    const __half *vsz = reinterpret_cast<const __half *>(rec + off_vsz) + (size_t)w * (2 * ngi * 16) + 4 * tq;
-    unsigned char *dst = tile + (size_t)(2 * w) * (D * 16) + gq * 16 + tq * 4;
-    // one word (CPH channel steps of 8) a turn, not unrolled: short code
-    // stays in the instruction cache beside the softmax warps'
-#pragma unroll 1
-    for (int wi = 0; wi < NWV; ++wi, dst += CPH * 128) {
-        // every load before the first store: the compiler keeps their order
-        const int u1 = NWV + wi;   // tokens 2 t, 2 t + 1: word wi; + 8: word u1
-        const uint32_t W0 = words[wi / CS * 32 * CS + wi % CS], W1 = words[u1 / CS * 32 * CS + u1 % CS];
-        uint2 sv[CPH / 2], zv[CPH / 2];
-#pragma unroll
-        for (int q = 0; q < CPH / 2; ++q) {   // 16 channels share a group row
-            const int gi = (16 * (wi * (CPH / 2) + q)) >> lgG;
-            sv[q] = *reinterpret_cast<const uint2 *>(vsz + gi * 16);
-            zv[q] = *reinterpret_cast<const uint2 *>(vsz + (ngi + gi) * 16);
-        }
-#pragma unroll
-        for (int r = 0; r < CPH; ++r) {
-            const float off = slot_offset<VB, false>(r);
-            *reinterpret_cast<uint32_t *>(dst + r * 128) =
-                ck_affine(unpack<VB, false>(W0, r), off, sv[r >> 1].x, zv[r >> 1].x);
-            *reinterpret_cast<uint32_t *>(dst + D * 16 + r * 128) =
-                ck_affine(unpack<VB, false>(W1, r), off, sv[r >> 1].y, zv[r >> 1].y);
-        }
-    }
-}
-
-// position in a ring of stages, and the phase its next use completes
-struct CkRing {
-    int s = 0;
-    unsigned p = 0;
-    __device__ __forceinline__ void next(int n) {
-        if (++s == n) {
-            s = 0;
-            p ^= 1u;
-        }
-    }
-};
-
-// A CTA's share of one row tile.
-struct CkSeg {
-    int i, j, m;     // sequence, kv head, row tile
-    int T, n;        // cached tokens, chunk tokens
-    int row0, nrows; // first row, rows of (i, j)
-    int nt;          // its key tiles
-    int x0, nx;      // the CTA's of them
-    BlockList bl;
-    // first token of the CTA's tile x
-    __device__ __forceinline__ int key0(int x) const { return bl.phys(x0 + x) * kCkKeys; }
-};
-
-// Walks a CTA's unit range [u, u1): every warp runs the same walk.
-struct CkWalk {
-    long long u, u1;
-    int i, m, j;     // the row tile holding u ...
-    int o;           // ... and u's offset in it
-    __device__ __forceinline__ int weight(const KiviGeom &g, const ChunkArgs &a) const {
-        return kCkLead + chunk_tiles(a, i, m, a.hq / g.h);
-    }
-    __device__ __forceinline__ void start(const KiviGeom &g, const ChunkArgs &a, int c, int C) {
-        const long long U = a.ustart[g.b];
-        u = (long long)c * U / C;
-        u1 = (long long)(c + 1) * U / C;
-        int lo = 0;
-        for (int hi = g.b; hi - lo > 1;) {
-            const int mid = (lo + hi) >> 1;
-            if (a.ustart[mid] <= u) lo = mid; else hi = mid;
-        }
-        i = lo;
-        const int hg = a.hq / g.h, lane = threadIdx.x & 31, mt = chunk_row_tiles(a.n[i], hg);
-        long long rem = u - a.ustart[i];
-        for (m = 0;; m += 32) {   // 32 row tiles of every head at a time
-            const long long w = m + lane < mt ? (long long)g.h * (kCkLead + chunk_tiles(a, i, m + lane, hg)) : 0;
-            long long e = w;   // inclusive prefix
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const long long y = __shfl_up_sync(kFull, e, d);
-                if (lane >= d) e += y;
-            }
-            const unsigned past = __ballot_sync(kFull, e > rem);
-            if (past || m + 32 >= mt) {
-                const int l = past ? __ffs(past) - 1 : 31;
-                rem -= __shfl_sync(kFull, e - w, l);
-                m += l;
-                break;
-            }
-            rem -= __shfl_sync(kFull, e, 31);
-        }
-        const int w = weight(g, a);
-        j = (int)(rem / w);
-        o = (int)(rem % w);
-    }
-    // the next segment with tiles; false at the range's end
-    __device__ __forceinline__ bool next(const KiviGeom &g, const ChunkArgs &a, CkSeg &s) {
-        const int hg = a.hq / g.h;
-        while (u < u1) {
-            const int w = weight(g, a), o1 = (int)min((long long)w, o + (u1 - u));
-            const int x0 = max(o - kCkLead, 0), x1 = max(o1 - kCkLead, 0);
-            if (x1 > x0) {
-                s.i = i;
-                s.j = j;
-                s.m = m;
-                s.T = a.T[i];
-                s.n = a.n[i];
-                s.row0 = m * kCkTileRows;
-                s.nrows = s.n * hg;
-                s.nt = w - kCkLead;
-                s.x0 = x0;
-                s.nx = x1 - x0;
-                s.bl = visible_blocks(a.vis, s.T + s.row0 / hg);
-            }
-            u += o1 - o;
-            o = 0;
-            if (o1 == w && ++j == g.h) {
-                j = 0;
-                if (++m == chunk_row_tiles(a.n[i], hg)) {
-                    m = 0;
-                    do ++i; while (i < g.b && a.n[i] == 0);
-                }
-            }
-            if (x1 > x0) return true;
-        }
-        return false;
-    }
-};
-
 // One dequantizing warp's share of n tiles, all fully quantized: the loop that
 // most of a long cache runs in, kept apart (and short) from the tiles with
 // fp16 tokens.  t: the tile stages' position (tiles: tiles so far), r: the
@@ -292,7 +93,7 @@ __device__ __forceinline__ bool packed_tiles(int n, int &tiles, CkRing &t, CkRin
         bool ok = (tiles < kCkStages || mbar_wait_ab(&eK[t.s], t.p ^ 1u, abort)) && mbar_wait_ab(&bR[r.s], r.p, abort);
         if (!__all_sync(kFull, ok)) return false;
         const unsigned char *rec = sR + (size_t)r.s * g.rec_bytes;
-        dequant_keys<D, KB>(sK + t.s * TB, rec, g.off_ksz, lgG, w);
+        dequant_keys<D, KB, kCkKeys>(sK + t.s * TB, rec, g.off_ksz, lgG, w);
         fence_proxy_async();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bK[t.s]);
@@ -349,7 +150,7 @@ __global__ void __launch_bounds__(kCkThreads, 1)
     __shared__ uint32_t s_taddr;
     __shared__ int s_abort;   // a wait ran out: every warp stops
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int hg = a.hq / g.h;
+    const int hg = a.hg;
     const bool qtma = kCkRows % hg == 0;   // Q's row tiles are boxes of its array
     if (tid < NB) {
         mbar_init(&bars[tid], tid < N4 && !(qtma && tid < 2) ? 4 : 1);
@@ -364,7 +165,7 @@ __global__ void __launch_bounds__(kCkThreads, 1)
     const volatile int *abort = &s_abort;
     bool ok = true;
     CkWalk walk;
-    walk.start(g, a, blockIdx.x, gridDim.x);
+    walk.start(a, blockIdx.x);
     CkSeg sg = {};
     // the segment's first tiles have a record: how many
     auto raw_tiles = [&](int Tq) {
@@ -372,117 +173,114 @@ __global__ void __launch_bounds__(kCkThreads, 1)
     };
 
     if (warp == 8 + kCkDq) {
-        // ---- S = Q K^T (lane 0 issues) ----
+        // ---- S = Q K^T ----
         constexpr uint32_t ID_S = tc_idesc_f16(kCkRows, kCkKeys, 0);
         CkRing tk;
         int nk = 0;             // K tiles read
         int cs[2] = {0, 0};     // S of each slot
         unsigned qph[2] = {0, 0};
-        while (walk.next(g, a, sg)) {
-            if (lane == 0) {
-                const int slots = sg.nrows - sg.row0 > kCkRows ? 2 : 1;
-                if (qtma) {   // this segment's Q, once the last one's S is done
+        const uint64_t dq = tc_desc(sQ, QLBO, 128), dk = tc_desc(sK, KLBO, 128);
+        while (ok && walk.next(g, a, sg)) {
+            const int nx = __reduce_max_sync(kFull, sg.nx);   // (warp-uniform)
+            const int slots = __reduce_max_sync(kFull, sg.nrows - sg.row0 > kCkRows ? 2 : 1);
+            if (qtma) {   // this segment's Q, once the last one's S is done
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        if (e >= slots || !ok) continue;
-                        ok = cs[e] == 0 || mbar_wait_ab(&bS[2 * e + ((cs[e] - 1) & 1)], (unsigned)((cs[e] - 1) >> 1) & 1u, abort);
-                        if (ok) tma_rows(sQ + e * QB, &tmQ, (sg.row0 + e * kCkRows) / hg, sg.i * g.h + sg.j, &bQ[e], QB);
-                    }
+                for (int e = 0; e < 2; ++e) {
+                    if (e >= slots) continue;
+                    ok = __all_sync(kFull, ok && (cs[e] == 0 || mbar_wait_ab(&bS[2 * e + ((cs[e] - 1) & 1)],
+                                                                              (unsigned)((cs[e] - 1) >> 1) & 1u, abort)));
+                    if (ok && lane == 0)
+                        tma_rows(sQ + e * QB, &tmQ, chunk_div(a, sg.row0 + e * kCkRows), sg.i * g.h + sg.j, &bQ[e], QB);
                 }
-                for (int x = 0; x < sg.nx && ok; ++x) {
+            }
+            for (int x = 0; x < nx && ok; ++x) {
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        if (e >= slots || !ok) continue;
-                        // its Q and K written, its S buffer free (P V of the slot's
-                        // last tile but one, in this segment or before, read its
-                        // weights there)
-                        const int b = cs[e] & 1;
-                        ok = (x > 0 || mbar_wait_ab(&bQ[e], qph[e], abort)) &&
-                             (e > 0 || mbar_wait_ab(&bK[tk.s], tk.p, abort)) &&
-                             (cs[e] < 2 || mbar_wait_ab(&bF[2 * e + b], (unsigned)((cs[e] >> 1) + 1) & 1u, abort));
-                        if (!ok) continue;
-                        if (x == 0) qph[e] ^= 1u;
-                        ++cs[e];
-                        tc_fence_after();
+                for (int e = 0; e < 2; ++e) {
+                    if (e >= slots || !ok) continue;
+                    // its Q and K written, its S buffer free (P V of the slot's
+                    // last tile but one, in this segment or before, read its
+                    // weights there)
+                    const int b = cs[e] & 1;
+                    ok = (x > 0 || mbar_wait_ab(&bQ[e], qph[e], abort)) &&
+                         (e > 0 || mbar_wait_ab(&bK[tk.s], tk.p, abort)) &&
+                         (cs[e] < 2 || mbar_wait_ab(&bF[2 * e + b], (unsigned)((cs[e] >> 1) + 1) & 1u, abort));
+                    ok = __all_sync(kFull, ok);
+                    if (!ok) continue;
+                    if (x == 0) qph[e] ^= 1u;
+                    ++cs[e];
+                    tc_fence_after();
+                    const uint64_t d = dk + (uint32_t)(tk.s * (TB >> 4));
 #pragma unroll
-                        for (int c = 0; c < D / 16; ++c)
-                            tc_mma_f16(taddr + 256 * e + 64 * b, tc_desc(sQ + e * QB + 2 * c * QLBO, QLBO, 128),
-                                       tc_desc(sK + tk.s * TB + 2 * c * KLBO, KLBO, 128), ID_S, c > 0);
-                        tc_commit(&bS[2 * e + b]);
-                        if (e == slots - 1) {
-                            tc_commit(&eK[tk.s]);
-                            tk.next(KS);
-                            ++nk;
-                        }
+                    for (int c = 0; c < D / 16; ++c)
+                        tc_mma_f16_w(taddr + 256 * e + 64 * b, dq + ((e * QB + 2 * c * QLBO) >> 4), d + ((2 * c * KLBO) >> 4),
+                                     ID_S, c > 0);
+                    tc_commit_w(&bS[2 * e + b]);
+                    if (e == slots - 1) {
+                        tc_commit_w(&eK[tk.s]);
+                        tk.next(KS);
+                        ++nk;
                     }
                 }
             }
-            ok = __all_sync(kFull, ok);
-            if (!ok) break;
         }
-        if (lane == 0) {
-            if (!ok) {
-                s_abort = 1;
-                atomicOr(dv.status, KIVI_FLAG_WAIT);
-            }
-            // every commit has landed before shared memory is given up
-            // (bounded; a phase already seen returns at once)
+        if (!ok && lane == 0) {
+            s_abort = 1;
+            atomicOr(dv.status, KIVI_FLAG_WAIT);
+        }
+        // every commit has landed before shared memory is given up (bounded; a
+        // phase already seen returns at once)
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
-                for (int y = max(0, cs[e] - 2); y < cs[e]; ++y) mbar_wait(&bS[2 * e + (y & 1)], (unsigned)(y >> 1) & 1u);
-            for (int y = max(0, nk - KS); y < nk; ++y) mbar_wait(&eK[y % KS], (unsigned)(y / KS) & 1u);
-        }
+        for (int e = 0; e < 2; ++e)
+            for (int y = max(0, cs[e] - 2); y < cs[e]; ++y) mbar_wait(&bS[2 * e + (y & 1)], (unsigned)(y >> 1) & 1u);
+        for (int y = max(0, nk - KS); y < nk; ++y) mbar_wait(&eK[y % KS], (unsigned)(y / KS) & 1u);
         __syncwarp();
     } else if (warp == 8 + kCkDq + 1) {
-        // ---- O += P V (lane 0 issues) ----
+        // ---- O += P V ----
         constexpr uint32_t ID_R = tc_idesc_f16(kCkRows, D, 1), ID_T = tc_idesc_f16(kCkRows, D, 0);
         CkRing tv;
         int nv = 0;             // V tiles read
         int cp[2] = {0, 0};     // P V of each slot
-        while (walk.next(g, a, sg)) {
-            if (lane == 0) {
-                const int slots = sg.nrows - sg.row0 > kCkRows ? 2 : 1;
-                const int Tqv = a.Tqv[sg.i];
-                for (int x = 0; x < sg.nx && ok; ++x) {
-                    const bool transposed = sg.key0(x) < Tqv;
+        const uint64_t dt = tc_desc(sV, VLBO, 128), dr = tc_desc(sV, 128, KLBO);   // transposed, as rows
+        while (ok && walk.next(g, a, sg)) {
+            const int nx = __reduce_max_sync(kFull, sg.nx);
+            const int slots = __reduce_max_sync(kFull, sg.nrows - sg.row0 > kCkRows ? 2 : 1);
+            // tiles with quantized values hold V transposed: the first ones
+            const int nt = __reduce_max_sync(kFull, sg.bl.virt((a.Tqv[sg.i] + kCkKeys - 1) / kCkKeys) - sg.x0);
+            for (int x = 0; x < nx && ok; ++x) {
+                const uint64_t st = (uint32_t)(tv.s * (TB >> 4));
+                const uint64_t d = (x < nt ? dt : dr) + st, step = x < nt ? (2 * VLBO) >> 4 : 256 >> 4;
+                const uint32_t id = x < nt ? ID_T : ID_R;
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        if (e >= slots || !ok) continue;
-                        const int b = cp[e] & 1;
-                        ok = mbar_wait_ab(&bP[2 * e + b], (unsigned)(cp[e] >> 1) & 1u, abort) &&
-                             (e > 0 || mbar_wait_ab(&bV[tv.s], tv.p, abort));
-                        if (!ok) continue;
-                        ++cp[e];
-                        tc_fence_after();
-                        const unsigned char *v = sV + tv.s * TB;
-                        const uint32_t tO = taddr + 256 * e + 128, tP = taddr + 256 * e + 64 * b;
+                for (int e = 0; e < 2; ++e) {
+                    if (e >= slots || !ok) continue;
+                    const int b = cp[e] & 1;
+                    ok = mbar_wait_ab(&bP[2 * e + b], (unsigned)(cp[e] >> 1) & 1u, abort) &&
+                         (e > 0 || mbar_wait_ab(&bV[tv.s], tv.p, abort));
+                    ok = __all_sync(kFull, ok);
+                    if (!ok) continue;
+                    ++cp[e];
+                    tc_fence_after();
 #pragma unroll
-                        for (int c = 0; c < kCkKeys / 16; ++c)
-                            tc_mma_f16_ta(tO, tP + 8 * c,
-                                          transposed ? tc_desc(v + 2 * c * VLBO, VLBO, 128) : tc_desc(v + 256 * c, 128, KLBO),
-                                          transposed ? ID_T : ID_R, x > 0 || c > 0);
-                        tc_commit(&bF[2 * e + b]);
-                        if (e == slots - 1) {
-                            tc_commit(&eV[tv.s]);
-                            tv.next(KS);
-                            ++nv;
-                        }
+                    for (int c = 0; c < kCkKeys / 16; ++c)
+                        tc_mma_f16_ta_w(taddr + 256 * e + 128, taddr + 256 * e + 64 * b + 8 * c, d + c * step, id,
+                                        x > 0 || c > 0);
+                    tc_commit_w(&bF[2 * e + b]);
+                    if (e == slots - 1) {
+                        tc_commit_w(&eV[tv.s]);
+                        tv.next(KS);
+                        ++nv;
                     }
                 }
             }
-            ok = __all_sync(kFull, ok);
-            if (!ok) break;
         }
-        if (lane == 0) {
-            if (!ok) {
-                s_abort = 1;
-                atomicOr(dv.status, KIVI_FLAG_WAIT);
-            }
+        if (!ok && lane == 0) {
+            s_abort = 1;
+            atomicOr(dv.status, KIVI_FLAG_WAIT);
+        }
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
-                for (int y = max(0, cp[e] - 2); y < cp[e]; ++y) mbar_wait(&bF[2 * e + (y & 1)], (unsigned)(y >> 1) & 1u);
-            for (int y = max(0, nv - KS); y < nv; ++y) mbar_wait(&eV[y % KS], (unsigned)(y / KS) & 1u);
-        }
+        for (int e = 0; e < 2; ++e)
+            for (int y = max(0, cp[e] - 2); y < cp[e]; ++y) mbar_wait(&bF[2 * e + (y & 1)], (unsigned)(y >> 1) & 1u);
+        for (int y = max(0, nv - KS); y < nv; ++y) mbar_wait(&eV[y % KS], (unsigned)(y / KS) & 1u);
         __syncwarp();
     } else if (warp == 8 + kCkDq + 2) {
         // ---- records (lane 0 issues) ----
@@ -572,8 +370,7 @@ __global__ void __launch_bounds__(kCkThreads, 1)
                 }
                 const unsigned char *rec = sR + (size_t)r.s * g.rec_bytes;
                 if (kq) {
-                    if (g.kbits == 2) dequant_keys<D, 2>(kt, rec, g.off_ksz, lgG, w);
-                    else dequant_keys<D, 4>(kt, rec, g.off_ksz, lgG, w);
+                    dequant_keys_cold<D, kCkKeys>(kt, rec, g.kbits, g.off_ksz, lgG, w);
                     if (!kall) {   // its window and chunk tokens over the rest
                         if (!(ok = meet())) break;
                         for (int e = dt; e < (tb + kCkKeys - Tqk) * CPR; e += GT) {
@@ -596,8 +393,7 @@ __global__ void __launch_bounds__(kCkThreads, 1)
                 ok = __all_sync(kFull, tiles < KS || mbar_wait_ab(&eV[t.s], t.p ^ 1u, abort));
                 if (!ok) break;
                 if (vq) {
-                    if (g.vbits == 2) dequant_values<D, 2>(vt, rec, g.off_vc, g.off_vsz, lgG, w);
-                    else dequant_values<D, 4>(vt, rec, g.off_vc, g.off_vsz, lgG, w);
+                    dequant_values_cold<D>(vt, rec, g.vbits, g.off_vc, g.off_vsz, lgG, w);
                     if (!vall) {
                         if (!(ok = meet())) break;
                         for (int e = dt; e < (tb + kCkKeys - Tqv) * CPR; e += GT) {
@@ -662,9 +458,9 @@ __global__ void __launch_bounds__(kCkThreads, 1)
                     uint4 v[8];
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
-                        const int rw = min(srow + qr(k0 + k), sg.nrows - 1);
+                        const int rw = min(srow + qr(k0 + k), sg.nrows - 1), tok = chunk_div(a, rw);
                         v[k] = *reinterpret_cast<const uint4 *>(
-                            Q + (((size_t)sg.i * a.hq + sg.j * hg + rw % hg) * a.n_stride + rw / hg) * D + 8 * qc(k0 + k));
+                            Q + (((size_t)sg.i * a.hq + sg.j * hg + rw - tok * hg) * a.n_stride + tok) * D + 8 * qc(k0 + k));
                     }
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
@@ -676,8 +472,8 @@ __global__ void __launch_bounds__(kCkThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bQ[slot]);
             }
-            const int pos = sg.T + row / hg, ps0 = sg.T + srow / hg, ps1 = sg.T + (srow + kCkRows - 1) / hg;
-            const int lo = W > 0 ? pos - W : -1;   // tokens [sinks, lo] are hidden
+            const int pos = sg.T + chunk_div(a, row), ps0 = sg.T + chunk_div(a, srow),
+                      ps1 = sg.T + chunk_div(a, srow + kCkRows - 1);
             float mref = -INFINITY, lsum = 0.f;    // the row's reference maximum (raw score units) and weight sum
             for (int x = 0; x < sg.nx; ++x, ++cnt) {
                 const int b = cnt & 1, key0 = sg.key0(x);
@@ -690,10 +486,11 @@ __global__ void __launch_bounds__(kCkThreads, 1)
                 tc_wait_ld();
                 if (key0 + kCkKeys - 1 > ps0 || (W > 0 && key0 <= ps1 - W && key0 + kCkKeys > sinks)) {
                     // some row of the slot does not see the whole tile
+                    const uint32_t h0 = ck_hidden32(key0, pos, W, sinks), h1 = ck_hidden32(key0 + 32, pos, W, sinks);
 #pragma unroll
-                    for (int c = 0; c < 64; ++c) {
-                        const int key = key0 + c;
-                        if (key > pos || (key <= lo && key >= sinks)) r[c >> 5][c & 31] = 0xff800000u;
+                    for (int c = 0; c < 32; ++c) {
+                        if ((h0 >> c) & 1u) r[0][c] = 0xff800000u;
+                        if ((h1 >> c) & 1u) r[1][c] = 0xff800000u;
                     }
                 }
                 float m8[8];
@@ -773,8 +570,8 @@ __global__ void __launch_bounds__(kCkThreads, 1)
                 size_t orow[4];   // the rows this lane stores
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const int rw = min(row32 + 8 * k + q8, sg.nrows - 1);
-                    orow[k] = (((size_t)sg.i * a.hq + sg.j * hg + rw % hg) * a.n_stride + rw / hg) * D + 8 * c4;
+                    const int rw = min(row32 + 8 * k + q8, sg.nrows - 1), tok = chunk_div(a, rw);
+                    orow[k] = (((size_t)sg.i * a.hq + sg.j * hg + rw - tok * hg) * a.n_stride + tok) * D + 8 * c4;
                 }
 #pragma unroll 1
                 for (int c0 = 0; c0 < D; c0 += 32) {
@@ -808,55 +605,6 @@ __global__ void __launch_bounds__(kCkThreads, 1)
     tc_fence_before();
     __syncthreads();
     if (warp == 0) tc_dealloc(taddr, 512);
-}
-
-// Joins the partials of the row tiles that CTA boundaries cut, a block per
-// cut row tile and 32 of its rows (a warp takes rows w, w + 8, ...): weights
-// 2^(m_k - M), M the largest m.  Block x finds its row tile from the boundary
-// before CTA x / 8 + 1: the tile's first such boundary owns it.
-template <int D>
-__global__ void __launch_bounds__(256)
-    chunk_join_kernel(KiviGeom g, __half *__restrict__ O, const __grid_constant__ ChunkArgs a, int ctas) {
-    constexpr int V = D / 32;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int hg = a.hq / g.h, c = blockIdx.x / (kCkTileRows / 32) + 1;
-    CkWalk walk;
-    walk.start(g, a, c, ctas);
-    if (walk.o <= kCkLead) return;   // CTA c starts with a row tile of its own
-    const long long U = a.ustart[g.b], P = walk.u - walk.o;
-    const int w = walk.weight(g, a), i = walk.i, j = walk.j;
-    auto cta_of = [&](long long u) { return (int)(((u + 1) * ctas - 1) / U); };
-    const int c0 = cta_of(P + kCkLead), c1 = cta_of(P + w - 1);   // those with its tiles
-    if (c != c0 + 1) return;         // an earlier boundary owns the row tile
-    // CTA c0 holds its first tile and runs into it (slot 2 c + 1), the others
-    // start in it (slot 2 c)
-    const float2 *ml = reinterpret_cast<const float2 *>(a.ml);
-    const int nrows = min(a.n[i] * hg - walk.m * kCkTileRows, kCkTileRows);
-    for (int r = (blockIdx.x % (kCkTileRows / 32)) * 32 + warp; r < min(nrows, (int)(blockIdx.x % (kCkTileRows / 32)) * 32 + 32);
-         r += 8) {
-        auto part = [&](int k) { return (size_t)(2 * k + (k == c0 ? 1 : 0)) * kCkTileRows + r; };
-        float M = -INFINITY;
-        for (int k = c0 + lane; k <= c1; k += 32) M = fmaxf(M, ml[part(k)].x);
-#pragma unroll
-        for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
-        float L = 0.f, acc[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) acc[v] = 0.f;
-#pragma unroll 4
-        for (int k = c0; k <= c1; ++k) {
-            const float2 x = ml[part(k)];
-            const float wt = x.x == -INFINITY ? 0.f : ex2(x.x - M);   // (sees nothing of this share)
-            L = fmaf(wt, x.y, L);
-            const float *src = a.acc + part(k) * D + lane * V;
-#pragma unroll
-            for (int v = 0; v < V; ++v) acc[v] = fmaf(wt, src[v], acc[v]);
-        }
-        const float inv = 1.f / L;
-        const int row = walk.m * kCkTileRows + r;
-        __half *dst = O + (((size_t)i * a.hq + j * hg + row % hg) * a.n_stride + row / hg) * D + lane * V;
-#pragma unroll
-        for (int v = 0; v < V; v += 2) *reinterpret_cast<uint32_t *>(dst + v) = ck_pack(acc[v] * inv, acc[v + 1] * inv);
-    }
 }
 
 }  // namespace

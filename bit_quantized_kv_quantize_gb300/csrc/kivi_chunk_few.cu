@@ -1,0 +1,32 @@
+// kivi_chunk_few.cu -- launch of the chunk attention for few query rows
+// (kivi_chunk_few_impl.cuh).
+#include "kivi_chunk_few_impl.cuh"
+
+namespace {
+
+template <int D, int N>
+cudaError_t launch_few(const KiviGeom &g, const KiviDev &dv, const __half *Q, const __half *K, const __half *V,
+                       __half *O, ChunkArgs &a, int ctas, cudaStream_t st) {
+    const size_t fixed = (size_t)2 * kFwStages * kFwKeys * D * 2 + (size_t)N * D * 2 + (size_t)fw_bufs(N) * kFwKeys * N * 2;
+    a.rs = (int)((224 * 1024 - fixed) / g.rec_bytes);
+    if (a.rs > kFwMaxRaw) a.rs = kFwMaxRaw;
+    if (a.rs < 4) return cudaErrorInvalidValue;
+    const size_t smem = fixed + (size_t)a.rs * g.rec_bytes;
+    cudaError_t e = cudaFuncSetAttribute(chunk_few_kernel<D, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    chunk_few_kernel<D, N><<<ctas, fw_threads(N), smem, st>>>(g, dv, Q, K, V, O, a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t kivi_launch_chunk_few(const KiviGeom &g, const KiviDev &dv, const __half *Q, const __half *K,
+                                  const __half *V, __half *O, ChunkArgs &a, int ctas, cudaStream_t st) {
+    if (g.d == 64)
+        return a.tile_rows == 16   ? launch_few<64, 16>(g, dv, Q, K, V, O, a, ctas, st)
+               : a.tile_rows == 32 ? launch_few<64, 32>(g, dv, Q, K, V, O, a, ctas, st)
+                                   : launch_few<64, 64>(g, dv, Q, K, V, O, a, ctas, st);
+    return a.tile_rows == 16   ? launch_few<128, 16>(g, dv, Q, K, V, O, a, ctas, st)
+           : a.tile_rows == 32 ? launch_few<128, 32>(g, dv, Q, K, V, O, a, ctas, st)
+                               : launch_few<128, 64>(g, dv, Q, K, V, O, a, ctas, st);
+}
