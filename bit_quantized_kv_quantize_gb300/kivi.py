@@ -7,6 +7,7 @@ fails to load, importing this module raises.
 """
 from __future__ import annotations
 
+import array
 import contextlib
 import ctypes
 import math
@@ -86,8 +87,9 @@ def _check(rc: int):
 
 def _stream(stream):
     import torch
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is None:   # the current stream's handle, without an object for it
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream
 
 
 def _dev_f32_rows(x, lead, name):
@@ -116,13 +118,41 @@ def _on(stream):
 
 
 def _counts(n, b, name="n"):
-    """Per-sequence counts as a contiguous int32 array."""
-    a = np.asarray(n)
-    if a.dtype.kind not in "iu" or a.ndim > 1 or (a.ndim == 1 and a.shape[0] not in (1, b)):
+    """Per-sequence counts (an integer or b of them) as an array of C ints."""
+    if not isinstance(n, (int, list, tuple)) or isinstance(n, bool):
+        a = np.asarray(n)
+        if a.dtype.kind not in "iu" or a.ndim > 1:
+            raise ValueError(f"{name} must be an integer or {b} integers")
+        n = a.tolist()
+    if isinstance(n, int):
+        n = (n,) * b
+    if len(n) != b:
         raise ValueError(f"{name} must be an integer or {b} integers")
-    if a.size and (int(a.min()) < -2**31 or int(a.max()) >= 2**31):
-        raise ValueError(f"{name} outside 32 bits")
-    return np.ascontiguousarray(np.broadcast_to(a.astype(np.int32), (b,)))
+    try:
+        return array.array("i", n)
+    except TypeError:
+        raise ValueError(f"{name} must be an integer or {b} integers") from None
+    except OverflowError:
+        raise ValueError(f"{name} outside 32 bits") from None
+
+
+def _addr(a):
+    """Address of an array.array's items."""
+    return a.buffer_info()[0]
+
+
+def _rows16(x, shape, dev, name):
+    """Address of a contiguous CUDA fp16 tensor of this shape on device dev."""
+    import torch
+    if type(x) is not torch.Tensor and not isinstance(x, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if x.dtype is not torch.float16 or not x.is_cuda:
+        raise TypeError(f"{name} must be a CUDA float16 tensor")
+    if x.shape != shape or not x.is_contiguous():
+        raise ValueError(f"{name} must be contiguous with shape {tuple(shape)}, got {tuple(x.shape)}")
+    if x.get_device() != dev:
+        raise ValueError(f"{name} must be on device cuda:{dev}")
+    return x.data_ptr()
 
 
 def rope_frequencies(rot_dim, base=10000.0, scaling=None, factor=1.0, original_length=8192, beta_fast=32.0,
@@ -170,13 +200,13 @@ class Rope:
 
     def __init__(self, d, rot_dim=None, base=10000.0, interleaved=False, inv_freq=None, factor=1.0):
         self.d, self.rot_dim = d, d if rot_dim is None else rot_dim
-        self.interleaved, self.factor = bool(interleaved), float(factor)
+        self.interleaved, self.factor = int(bool(interleaved)), float(factor)
         f = rope_frequencies(self.rot_dim, base)[0] if inv_freq is None else np.asarray(inv_freq, np.float64)
         if f.shape != (self.rot_dim // 2,) or not np.all(np.isfinite(f)):
             raise ValueError(f"inv_freq must be {self.rot_dim // 2} finite numbers")
         self.inv_freq = f.copy()
         # fractions of a turn, 2^64 = one turn
-        self._turns = np.array([int(round(x / (2 * math.pi) * 2.0**64)) % 2**64 for x in f.tolist()], np.uint64)
+        self._turns = array.array("Q", [int(round(x / (2 * math.pi) * 2.0**64)) % 2**64 for x in f.tolist()])
 
     def apply(self, q, k, pos, n=None, q_out=None, k_out=None, inverse=False, stream=None):
         """Rotate q (CUDA fp16 [b, h_q, t, d] or [b, h_q, d]) and k (same with
@@ -188,34 +218,39 @@ class Rope:
         import torch
         if not isinstance(q, torch.Tensor) or q.dim() not in (3, 4):
             raise ValueError("q must be a [b, heads, t, d] or [b, heads, d] tensor")
-        step = q.dim() == 3
-        b, hq, t = q.shape[0], q.shape[1], 1 if step else q.shape[2]
+        if not q.is_cuda:
+            raise TypeError("q must be a CUDA float16 tensor")
+        dev = q.get_device()
+        if dev != torch.cuda.current_device():
+            with torch.cuda.device(dev):
+                return self.apply(q, k, pos, n, q_out, k_out, inverse, stream)
+        shape, step = q.shape, q.dim() == 3
+        b, hq, t = shape[0], shape[1], 1 if step else shape[2]
         hk = 0 if k is None else k.shape[1]
-        shapes = [(b, h, self.d) if step else (b, h, t, self.d) for h in (hq, hk)]
-        qp = _dev_fp16(q, shapes[0], "q")
-        kp = _dev_fp16(k, shapes[1], "k") if k is not None else None
+        qs = (b, hq, self.d) if step else (b, hq, t, self.d)
+        ks = (b, hk, self.d) if step else (b, hk, t, self.d)
+        qp, kp = _rows16(q, qs, dev, "q"), None if k is None else _rows16(k, ks, dev, "k")
         cnt = _counts(t if n is None else n, b)
-        pos0, posp = None, None
+        posp, pos0 = None, None
         if isinstance(pos, torch.Tensor) and pos.is_cuda:
-            if pos.dtype != torch.int32 or tuple(pos.shape) != (b, t) or not pos.is_contiguous():
-                raise ValueError(f"pos must be a contiguous int32 tensor [{b}, {t}]")
+            if pos.dtype is not torch.int32 or tuple(pos.shape) != (b, t) or not pos.is_contiguous() or pos.get_device() != dev:
+                raise ValueError(f"pos must be a contiguous int32 tensor [{b}, {t}] on device cuda:{dev}")
             posp = pos.data_ptr()
         else:
             pos0 = _counts(pos, b, "pos")
-        tensors = [x for x in (q, k, q_out, k_out, pos if posp else None) if x is not None]
-        if any(x.device != q.device for x in tensors):
-            raise ValueError("all tensors must be on one device")
-        with torch.cuda.device(q.device), _on(stream):
-            new = torch.empty_like if np.all(cnt == t) else torch.zeros_like
-            q_out = new(q) if q_out is None else q_out
-            k_out = new(k) if k_out is None and k is not None else k_out
-            qo = _dev_fp16(q_out, shapes[0], "q_out")
-            ko = _dev_fp16(k_out, shapes[1], "k_out") if k is not None else None
-            _check(lib.kivi_rope(qp, kp, b, hq, hk, t, self.d, cnt.ctypes.data,
-                                 None if pos0 is None else pos0.ctypes.data, posp, self._turns.ctypes.data,
-                                 self.rot_dim, int(self.interleaved), self.factor, int(bool(inverse)), qo, ko,
-                                 _stream(stream)))
+        if q_out is None or (k_out is None and k is not None):
+            new = torch.empty_like if n is None or min(cnt) == t else torch.zeros_like
+            with _on(stream):
+                q_out = new(q) if q_out is None else q_out
+                k_out = new(k) if k_out is None and k is not None else k_out
+        self._call(qp, kp, b, hq, hk, t, cnt, pos0, posp, inverse, _rows16(q_out, qs, dev, "q_out"),
+                   None if k is None else _rows16(k_out, ks, dev, "k_out"), _stream(stream))
         return q_out if k is None else (q_out, k_out)
+
+    def _call(self, qp, kp, b, hq, hk, t, cnt, pos0, posp, inverse, qo, ko, stream):
+        _check(lib.kivi_rope(qp, kp, b, hq, hk, t, self.d, _addr(cnt), None if pos0 is None else _addr(pos0), posp,
+                             _addr(self._turns), self.rot_dim, self.interleaved, self.factor, 1 if inverse else 0,
+                             qo, ko, stream))
 
 
 class KiviCache:
@@ -284,52 +319,64 @@ class KiviCache:
         return out
 
     def _chunk(self, K, V, n):
+        """Addresses of a chunk's keys and values, its counts and stride."""
         if K.dim() != 4:
             raise ValueError("K must be [b, h_kv, n_stride, d]")
-        ns = K.shape[2]
-        kp = _dev_fp16(K, (self.b, self.h_kv, ns, self.d), "K")
-        vp = _dev_fp16(V, (self.b, self.h_kv, ns, self.d), "V")
-        return kp, vp, _counts(n, self.b), ns
+        shape = (self.b, self.h_kv, K.shape[2], self.d)
+        return (_rows16(K, shape, self._dev, "K"), _rows16(V, shape, self._dev, "V"), _counts(n, self.b),
+                K.shape[2])
+
+    def _chunk_out(self, Q, ns, out, stream):
+        """Address of a chunk's queries, its output (a new one is zero) and that's address."""
+        import torch
+        if Q.dim() != 4:
+            raise ValueError("Q must be [b, h_q, n_stride, d]")
+        shape = (self.b, Q.shape[1], ns, self.d)
+        qp = _rows16(Q, shape, self._dev, "Q")
+        if out is None:
+            with _on(stream):
+                out = torch.zeros_like(Q)
+        return qp, out, _rows16(out, shape, self._dev, "out")
 
     def chunk_attn(self, Q, K, V, n, window=0, sinks=0, out=None, stream=None):
         """Attention of n new tokens of each sequence (an integer or b of
         them) over the cache and the chunk itself: Q CUDA fp16 [b, h_q, ns, d],
         K and V [b, h_kv, ns, d] -> out (rows past n untouched, zero in a new
         tensor).  Does not append (append_chunk, extend)."""
-        import torch
         kp, vp, cnt, ns = self._chunk(K, V, n)
-        hq = Q.shape[1]
-        qp = _dev_fp16(Q, (self.b, hq, ns, self.d), "Q")
-        with _on(stream):
-            if out is None:
-                out = torch.zeros_like(Q)
-            op = _dev_fp16(out, (self.b, hq, ns, self.d), "out")
-            self._here(Q, K, V, out)
-            _check(lib.kivi_chunk_attn(self._h, qp, kp, vp, cnt.ctypes.data, ns, hq, window, sinks, op,
-                                       _stream(stream)))
+        qp, out, op = self._chunk_out(Q, ns, out, stream)
+        _check(lib.kivi_chunk_attn(self._h, qp, kp, vp, _addr(cnt), ns, Q.shape[1], window, sinks, op,
+                                   _stream(stream)))
         return out
 
     def append_chunk(self, K, V, n, stream=None):
         """Append n tokens of each sequence (an integer or b of them; K, V CUDA
         fp16 [b, h_kv, ns, d]): n one-token appends in one call."""
         kp, vp, cnt, ns = self._chunk(K, V, n)
-        self._here(K, V)
-        _check(lib.kivi_append_chunk(self._h, kp, vp, cnt.ctypes.data, ns, _stream(stream)))
+        _check(lib.kivi_append_chunk(self._h, kp, vp, _addr(cnt), ns, _stream(stream)))
 
     def extend(self, Q, K, V, n, window=0, sinks=0, rope=None, out=None, stream=None):
         """Take the next chunk of every sequence: rotate its queries and keys
         at the positions behind the cached tokens (rope: a Rope, or None),
         attend (chunk_attn; returns its out) and append it (append_chunk)."""
-        cnt = _counts(n, self.b)
-        T = self.lengths()[0]
-        if np.any(cnt > self.max_tokens - T):
-            raise CapacityError(3, f"sequence {int(np.argmax(cnt > self.max_tokens - T))} would exceed max_tokens")
-        self._here(Q, K, V, out)
-        with _on(stream):
-            if rope is not None:
-                Q, K = rope.apply(Q, K, T, n=cnt, stream=stream)
-            out = self.chunk_attn(Q, K, V, cnt, window, sinks, out, stream)
-            self.append_chunk(K, V, cnt, stream)
+        import torch
+        kp, vp, cnt, ns = self._chunk(K, V, n)
+        T = array.array("i", bytes(4 * self.b))
+        _check(lib.kivi_cache_lengths(self._h, _addr(T), None, None))
+        for i in range(self.b):
+            if cnt[i] > self.max_tokens - T[i]:
+                raise CapacityError(3, f"sequence {i} would exceed max_tokens")
+        qp, out, op = self._chunk_out(Q, ns, out, stream)
+        hq, st, cp = Q.shape[1], _stream(stream), _addr(cnt)
+        if rope is not None:
+            if rope.d != self.d:
+                raise ValueError(f"rope is for heads of dimension {rope.d}")
+            with _on(stream):   # rows past n are not read
+                rq, rk = torch.empty_like(Q), torch.empty_like(K)
+            rope._call(qp, kp, self.b, hq, self.h_kv, ns, cnt, T, None, False, rq.data_ptr(), rk.data_ptr(), st)
+            qp, kp = rq.data_ptr(), rk.data_ptr()
+        _check(lib.kivi_chunk_attn(self._h, qp, kp, vp, cp, ns, hq, window, sinks, op, st))
+        _check(lib.kivi_append_chunk(self._h, kp, vp, cp, ns, st))
         return out
 
     def append(self, k, v, stream=None):
