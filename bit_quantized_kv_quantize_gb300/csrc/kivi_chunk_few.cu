@@ -7,14 +7,14 @@ namespace {
 template <int D, int N>
 cudaError_t launch_few(const KiviGeom &g, const KiviDev &dv, const __half *Q, const __half *K, const __half *V,
                        __half *O, ChunkArgs &a, int ctas, cudaStream_t st) {
-    const size_t fixed = (size_t)2 * kFwStages * kFwKeys * D * 2 + (size_t)N * D * 2 + (size_t)fw_bufs(N) * kFwKeys * N * 2;
+    const size_t fixed = (size_t)kFwStages * (fw_kb(D) + fw_vb(D)) + (size_t)N * D * 2 + (size_t)fw_bufs(N) * kFwKeys * N * 2;
     a.rs = (int)((224 * 1024 - fixed) / g.rec_bytes);
     if (a.rs > kFwMaxRaw) a.rs = kFwMaxRaw;
     if (a.rs < 4) return cudaErrorInvalidValue;
     const size_t smem = fixed + (size_t)a.rs * g.rec_bytes;
     cudaError_t e = cudaFuncSetAttribute(chunk_few_kernel<D, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    chunk_few_kernel<D, N><<<ctas, fw_threads(N), smem, st>>>(g, dv, Q, K, V, O, a);
+    chunk_few_kernel<D, N><<<ctas, kFwThreads, smem, st>>>(g, dv, Q, K, V, O, a);
     return cudaGetLastError();
 }
 

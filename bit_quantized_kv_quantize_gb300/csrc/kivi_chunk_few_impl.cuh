@@ -20,6 +20,12 @@
 // rescaled.  A thread keeps its own part of each row's sum; they are added up
 // at the end of the segment.
 //
+// The order of the channels in K^ and Q, and of the tokens in V^ and P^T, is
+// free as long as both operands keep it.  It is chosen so that a lane's
+// unpacked values of a record are 16 consecutive bytes of a tile (8 channels
+// of a token: fw_chan; 8 tokens of a channel: fw_tok), stored at once, where
+// the natural order takes four stores.
+//
 // V^ is always the [channels][tokens] tile here (the MMA's A operand); fp16
 // tokens of the windows and the chunk are written transposed, value by value
 // (a few tiles of a sequence).  P^T goes through shared memory as the B
@@ -34,14 +40,24 @@ namespace {
 constexpr int kFwKeys = 128;    // tokens of a tile (two blocks)
 constexpr int kFwStages = 2;    // K^ tiles, and V^ tiles, in flight
 constexpr int kFwMaxRaw = 12;   // records in flight
-// Dequantizing groups.  Four of them where the softmax warps' registers allow
-// it (80 a thread), else two (128): one group alone restores a block in about
-// 1200 cycles.
-__host__ __device__ constexpr int fw_groups(int N) { return N == 16 ? 4 : 2; }
-__host__ __device__ constexpr int fw_threads(int N) { return 32 * (4 + fw_groups(N) * kCkDqGroup + 3); }
+// Dequantizing warps: four for K^ and four for V^, block b of a CTA to warp b
+// mod 4 (a V^ stage is held until the softmax and O^T are through with it: K^
+// must not wait for that).  A warp restores a whole block in a short loop: with
+// a role a warp, straight-line code runs at the rate of instruction fetches
+// (measured: 7 cycles an instruction when four warps shared a block, each
+// running its part once).
+constexpr int kFwDq = 4;
+constexpr int kFwThreads = 32 * (4 + 2 * kFwDq + 3);
 // S^T and P^T buffers: tiles that the softmax may be apart from either MMA
 // (four hide the waits between the roles; with 64 rows there is room for two)
 __host__ __device__ constexpr int fw_bufs(int N) { return N == 64 ? 2 : 4; }
+// Bytes from a 16-byte chunk to the next along a row of K^, and of V^^T: 32
+// more than their rows take, so that the lanes of a store (2 rows of 4 chunks)
+// fall in different banks; bytes of a tile.
+constexpr int kFwKS = kFwKeys * 16 + 32;
+__host__ __device__ constexpr int fw_vs(int D) { return D * 16 + 32; }
+__host__ __device__ constexpr int fw_kb(int D) { return D / 8 * kFwKS; }
+__host__ __device__ constexpr int fw_vb(int D) { return kFwKeys / 8 * fw_vs(D); }
 constexpr float kFwUnset = 1e30f;   // minus the reference of a row that has seen nothing
 
 __device__ __forceinline__ float redux_max(float x) {
@@ -62,18 +78,162 @@ __device__ __forceinline__ bool fw_any(bool v) {
 }
 __device__ __forceinline__ void fw_sync() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
 
-// A dequantizing group's state.
-struct FwGroup {
-    int w, dt, lgG, meets;   // warp, thread of the group; log2 G; meetings so far
-    uint64_t *bX;
-    const volatile int *abort;
-    // the group's warps meet (a bounded wait, unlike a named barrier)
-    __device__ __forceinline__ bool meet() {
-        __syncwarp();
-        if ((threadIdx.x & 31) == 0) mbar_arrive(bX);
-        return __all_sync(kFull, mbar_wait_ab(bX, (unsigned)meets++ & 1u, abort)) != 0;
+// Position of channel c in a row of K^ and Q, of token r in a row of V^^T and
+// in P^T.
+__device__ __forceinline__ int fw_chan(int c) {
+    return (c & ~31) | ((c >> 1) & 3) << 3 | ((c >> 4) & 1) << 2 | ((c >> 3) & 1) << 1 | (c & 1);
+}
+__device__ __forceinline__ int fw_tok(int r) {
+    return (r & ~31) | ((r >> 1) & 3) << 3 | ((r >> 4) & 1) << 2 | ((r >> 3) & 1) << 1 | (r & 1);
+}
+
+// K^ of a record's 64 tokens (rows of the tile from `tile` on), channels in
+// fw_chan's order, by one warp: a turn restores 32 channels of 32 tokens, lane
+// (gq, tq) the 8 channels at position 8 tq of tokens 8 pos + gq.  LG: log2 of
+// the group size.
+template <int D, int KB, int LG>
+__device__ __forceinline__ void few_keys(unsigned char *tile, const unsigned char *rec) {
+    constexpr int KC = 2 * D * KB * 4;          // code bytes
+    constexpr int GH = LG >= 5 ? 1 : 2;         // groups 32 tokens span
+    const int lane = threadIdx.x & 31, gq = lane >> 2, tq = lane & 3;
+    const unsigned char *pw = rec + lane * 16;
+    const __half *ksz = reinterpret_cast<const __half *>(rec + KC) + tq * (D / 4);
+    unsigned char *dst = tile + (size_t)tq * kFwKS + gq * 16;
+#pragma unroll 1
+    for (int k = 0; k < D / 16; ++k) {
+        const int jp = k >> 1, th = k & 1;      // 32 channels, half of the tokens
+        // words of 16-channel steps 2 jp, 2 jp + 1: [step][hh], the half's codes lowest
+        uint32_t W[4];
+        if (KB == 2) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(pw + jp * 512);
+            W[0] = v.x >> (8 * th);
+            W[1] = v.y >> (8 * th);
+            W[2] = v.z >> (8 * th);
+            W[3] = v.w >> (8 * th);
+        } else {
+            const uint4 v = *reinterpret_cast<const uint4 *>(pw + jp * 1024);
+            const uint4 u = *reinterpret_cast<const uint4 *>(pw + jp * 1024 + 512);
+            W[0] = th ? v.y : v.x;
+            W[1] = th ? v.w : v.z;
+            W[2] = th ? u.y : u.x;
+            W[3] = th ? u.w : u.z;
+        }
+        uint4 sv[GH], zv[GH];                   // the lane's 8 channels' scales and zeros
+#pragma unroll
+        for (int q = 0; q < GH; ++q) {
+            const int row = LG >= 6 ? 0 : th * GH + q;
+            sv[q] = *reinterpret_cast<const uint4 *>(ksz + 8 * jp + 2 * row * D);
+            zv[q] = *reinterpret_cast<const uint4 *>(ksz + 8 * jp + (2 * row + 1) * D);
+        }
+        unsigned char *p = dst + jp * (4 * kFwKS) + th * 512;
+#pragma unroll
+        for (int pos = 0; pos < 4; ++pos) {
+            const uint4 sc = sv[pos * GH / 4], z = zv[pos * GH / 4];
+            const float off = slot_offset<KB, true>(pos);
+            *reinterpret_cast<uint4 *>(p + pos * 128) = make_uint4(
+                ck_affine(unpack<KB, true>(W[0], pos), off, sc.x, z.x), ck_affine(unpack<KB, true>(W[1], pos), off, sc.y, z.y),
+                ck_affine(unpack<KB, true>(W[2], pos), off, sc.z, z.z), ck_affine(unpack<KB, true>(W[3], pos), off, sc.w, z.w));
+        }
     }
-};
+}
+// V^^T of a record's 64 tokens, tokens in fw_tok's order (tile: the first
+// chunk of 8), by one warp: a turn restores 32 channels of 32 tokens, lane
+// (gq, tq) the tokens at position 8 tq of channels 8 ci + gq.  rv, rz: the
+// record's value codes, scales and zeros.
+template <int D, int VB, int LG>
+__device__ __forceinline__ void few_values(unsigned char *tile, const unsigned char *rv, const unsigned char *rz) {
+    constexpr int WL = D * VB / 64, CS = WL < 4 ? WL : 4, NWV = D * VB / 128, NGI = D >> LG, BW = D * VB / 2;
+    constexpr int GH = LG >= 5 ? 1 : 2;         // groups 32 channels span
+    const int lane = threadIdx.x & 31, gq = lane >> 2, tq = lane & 3;
+    const uint32_t *words = reinterpret_cast<const uint32_t *>(rv) + lane * CS;
+    const __half *vsz = reinterpret_cast<const __half *>(rz) + 4 * tq;
+    unsigned char *dst = tile + (size_t)tq * fw_vs(D) + gq * 16;
+#pragma unroll 1
+    for (int k = 0; k < D / 16; ++k) {
+        const int c4 = k >> 1, vp = k & 1;      // 32 channels, two value blocks
+        // the words of these channels (2 bits: half of a word), of tokens [block][p]
+        const int wi = VB == 2 ? c4 >> 1 : c4, sh = VB == 2 ? (c4 & 1) * 8 : 0;
+        uint32_t W[2][2];
+#pragma unroll
+        for (int v = 0; v < 2; ++v)
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                const int u = p * NWV + wi;
+                W[v][p] = words[(2 * vp + v) * BW + u / CS * 32 * CS + u % CS] >> sh;
+            }
+        uint2 sv[GH][2], zv[GH][2];
+#pragma unroll
+        for (int q = 0; q < GH; ++q)
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+                const __half *row = vsz + (2 * vp + v) * (2 * NGI * 16) + (LG >= 5 ? (32 * c4) >> LG : 2 * c4 + q) * 16;
+                sv[q][v] = *reinterpret_cast<const uint2 *>(row);
+                zv[q][v] = *reinterpret_cast<const uint2 *>(row + NGI * 16);
+            }
+        unsigned char *p = dst + vp * (4 * fw_vs(D)) + c4 * 512;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const float off = slot_offset<VB, false>(q);
+            const int e = q * GH / 4;
+            *reinterpret_cast<uint4 *>(p + q * 128) = make_uint4(ck_affine(unpack<VB, false>(W[0][0], q), off, sv[e][0].x, zv[e][0].x),
+                                                                 ck_affine(unpack<VB, false>(W[0][1], q), off, sv[e][0].y, zv[e][0].y),
+                                                                 ck_affine(unpack<VB, false>(W[1][0], q), off, sv[e][1].x, zv[e][1].x),
+                                                                 ck_affine(unpack<VB, false>(W[1][1], q), off, sv[e][1].y, zv[e][1].y));
+        }
+    }
+}
+// ... by the cache's bit widths and group size
+template <int D, int KB>
+__device__ __forceinline__ void few_keys_g(unsigned char *tile, const unsigned char *rec, int lgG) {
+    switch (lgG) {
+    case 4: few_keys<D, KB, 4>(tile, rec); break;
+    case 5: few_keys<D, KB, 5>(tile, rec); break;
+    default: few_keys<D, KB, 6>(tile, rec); break;   // one row of scales a record from G = 64 on
+    }
+}
+template <int D, int VB>
+__device__ __forceinline__ void few_values_g(unsigned char *tile, const unsigned char *rv, const unsigned char *rz,
+                                             int lgG) {
+    switch (lgG) {
+    case 4: few_values<D, VB, 4>(tile, rv, rz); break;
+    case 5: few_values<D, VB, 5>(tile, rv, rz); break;
+    case 6: few_values<D, VB, 6>(tile, rv, rz); break;
+    default:
+        if constexpr (D >= 128) few_values<D, VB, 7>(tile, rv, rz);
+        break;
+    }
+}
+template <int D>
+__device__ __forceinline__ void few_keys(const KiviGeom &g, unsigned char *tile, const unsigned char *rec, int lgG) {
+    if (g.kbits == 2) few_keys_g<D, 2>(tile, rec, lgG);
+    else few_keys_g<D, 4>(tile, rec, lgG);
+}
+template <int D>
+__device__ __forceinline__ void few_values(const KiviGeom &g, unsigned char *tile, const unsigned char *rec, int lgG) {
+    if (g.vbits == 2) few_values_g<D, 2>(tile, rec + g.off_vc, rec + g.off_vsz, lgG);
+    else few_values_g<D, 4>(tile, rec + g.off_vc, rec + g.off_vsz, lgG);
+}
+// ... out of line, for blocks that also hold fp16 tokens
+template <int D>
+__device__ __noinline__ void few_keys_cold(const KiviGeom &g, unsigned char *tile, const unsigned char *rec, int lgG) {
+    few_keys<D>(g, tile, rec, lgG);
+}
+template <int D>
+__device__ __noinline__ void few_values_cold(const KiviGeom &g, unsigned char *tile, const unsigned char *rec, int lgG) {
+    few_values<D>(g, tile, rec, lgG);
+}
+// 16 bytes of a row (channels 8 c ..) to their positions in row r of a tile
+// whose chunks are STEP bytes apart
+template <int STEP>
+__device__ __forceinline__ void fw_put(unsigned char *tile, int r, int c, const uint4 &v) {
+    const uint32_t h[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int p = fw_chan(8 * c + 2 * k);
+        *reinterpret_cast<uint32_t *>(tile + (p >> 3) * STEP + r * 16 + (p & 7) * 2) = h[k];
+    }
+}
+
 // 16 bytes of token tau's fp16 row, in the window or the chunk (zero past the
 // chunk; chunk0: the slice's first row in chk)
 template <int D>
@@ -83,56 +243,66 @@ __device__ __forceinline__ uint4 fw_row16(const CkSeg &sg, const __half *win, in
     return tau < sg.T + sg.n ? *reinterpret_cast<const uint4 *>(src + 8 * c) : make_uint4(0u, 0u, 0u, 0u);
 }
 // Block blk of the segment with some fp16 tokens (or past the list: then its
-// keys are left and its values zeroed, as their weights are zero).  False if
-// a wait ran out.
+// keys are left and its values zeroed, as their weights are zero), by one
+// warp; loads go out ahead of the stores.
 template <int D>
-__device__ __noinline__ bool cold_keys(FwGroup &f, const KiviGeom &g, const KiviDev &dv, const __half *Kn,
-                                       const ChunkArgs &a, const CkSeg &sg, int blk, unsigned char *kt,
-                                       const unsigned char *rec) {
-    constexpr int CPR = D / 8;
-    const int v = 2 * sg.x0 + blk, Tqk = a.Tqk[sg.i];
-    if (v >= sg.nb) return true;
+__device__ __noinline__ void cold_keys(const KiviGeom &g, const KiviDev &dv, const __half *Kn, const ChunkArgs &a,
+                                       const CkSeg &sg, int blk, unsigned char *kt, const unsigned char *rec) {
+    constexpr int CPR = D / 8, U = 8;
+    const int lane = threadIdx.x & 31, v = 2 * sg.x0 + blk, Tqk = a.Tqk[sg.i];
+    if (v >= sg.nb) return;
     const int tb = sg.bl.phys(v) * KIVI_KBLK, r0 = max(Tqk - tb, 0);   // rows below r0 are quantized
-    if (r0 > 0) dequant_keys_cold<D, kFwKeys>(kt, rec, g.kbits, g.off_ksz, f.lgG, f.w);
-    if (r0 >= KIVI_KBLK) return true;
-    if (r0 > 0 && !f.meet()) return false;
+    if (r0 > 0) few_keys<D>(g, kt, rec, __ffs(g.G) - 1);
+    __syncwarp();
     const __half *win = dv.Kf + kf_slice(g, sg.i, sg.j);
     const size_t chunk0 = ((size_t)sg.i * g.h + sg.j) * a.n_stride;
-    for (int e = f.dt; e < (KIVI_KBLK - r0) * CPR; e += 32 * kCkDqGroup) {
-        const int rr = r0 + e / CPR, c = e % CPR;
-        *reinterpret_cast<uint4 *>(kt + c * (kFwKeys * 16) + rr * 16) = fw_row16<D>(sg, win, g.R, Kn, chunk0, tb + rr, c);
+    for (int e0 = r0 * CPR + lane; e0 < KIVI_KBLK * CPR; e0 += 32 * U) {
+        uint4 x[U];
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int e = min(e0 + 32 * k, KIVI_KBLK * CPR - 1);
+            x[k] = fw_row16<D>(sg, win, g.R, Kn, chunk0, tb + e / CPR, e % CPR);
+        }
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int e = e0 + 32 * k;
+            if (e < KIVI_KBLK * CPR) fw_put<kFwKS>(kt, e / CPR, e % CPR, x[k]);
+        }
     }
-    return true;
 }
 template <int D>
-__device__ __noinline__ bool cold_values(FwGroup &f, const KiviGeom &g, const KiviDev &dv, const __half *Vn,
-                                         const ChunkArgs &a, const CkSeg &sg, int blk, unsigned char *vt,
-                                         const unsigned char *rec) {
-    constexpr int CPR = D / 8;
-    const int v = 2 * sg.x0 + blk, Tqv = a.Tqv[sg.i];
+__device__ __noinline__ void cold_values(const KiviGeom &g, const KiviDev &dv, const __half *Vn, const ChunkArgs &a,
+                                         const CkSeg &sg, int blk, unsigned char *vt, const unsigned char *rec) {
+    constexpr int CPR = D / 8, U = 8;
+    const int lane = threadIdx.x & 31, v = 2 * sg.x0 + blk, Tqv = a.Tqv[sg.i];
     if (v >= sg.nb) {
-        for (int e = f.dt; e < KIVI_KBLK / 8 * D; e += 32 * kCkDqGroup)
-            reinterpret_cast<uint4 *>(vt)[e] = make_uint4(0u, 0u, 0u, 0u);
-        return true;
+        for (int e = lane; e < KIVI_KBLK / 8 * (fw_vs(D) / 16); e += 32) reinterpret_cast<uint4 *>(vt)[e] = make_uint4(0u, 0u, 0u, 0u);
+        return;
     }
     const int tb = sg.bl.phys(v) * KIVI_KBLK, r0 = max(Tqv - tb, 0);
-    if (r0 > 0) dequant_values_cold<D>(vt, rec, g.vbits, g.off_vc, g.off_vsz, f.lgG, f.w);
-    if (r0 >= KIVI_KBLK) return true;
-    if (r0 > 0 && !f.meet()) return false;
+    if (r0 > 0) few_values<D>(g, vt, rec, __ffs(g.G) - 1);
+    __syncwarp();
     const __half *win = dv.Vf + vf_slice(g, sg.i, sg.j);
     const size_t chunk0 = ((size_t)sg.i * g.h + sg.j) * a.n_stride;
-    const int nr = KIVI_KBLK - r0;
-    for (int e = f.dt; e < nr * CPR; e += 32 * kCkDqGroup) {
-        // consecutive lanes take consecutive tokens
-        const int rr = r0 + e % nr, c = e / nr;
-        const uint4 u = fw_row16<D>(sg, win, g.R + 1, Vn, chunk0, tb + rr, c);
-        const uint32_t h[4] = {u.x, u.y, u.z, u.w};
-        unsigned char *dst = vt + (rr >> 3) * (D * 16) + c * 128 + (rr & 7) * 2;
+    // consecutive lanes take consecutive tokens
+    for (int e0 = lane; e0 < KIVI_KBLK * CPR; e0 += 32 * U) {
+        uint4 x[U];
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-            *reinterpret_cast<uint16_t *>(dst + k * 16) = (uint16_t)(h[k >> 1] >> (16 * (k & 1)));
+        for (int k = 0; k < U; ++k) {
+            const int e = e0 + 32 * k, rr = max(e & (KIVI_KBLK - 1), r0 & (KIVI_KBLK - 1));
+            x[k] = fw_row16<D>(sg, win, g.R + 1, Vn, chunk0, tb + rr, e / KIVI_KBLK);
+        }
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int e = e0 + 32 * k, rr = e & (KIVI_KBLK - 1), c = e / KIVI_KBLK, pos = fw_tok(rr);
+            if (rr < r0) continue;
+            const uint32_t h[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+            unsigned char *dst = vt + (pos >> 3) * fw_vs(D) + c * 128 + (pos & 7) * 2;
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                *reinterpret_cast<uint16_t *>(dst + q * 16) = (uint16_t)(h[q >> 1] >> (16 * (q & 1)));
+        }
     }
-    return true;
 }
 
 // A raise: the rows' maxima over the tile (tS: this warp's scores; hid: does
@@ -181,27 +351,27 @@ __device__ __noinline__ void rescale_out(uint32_t tO, const float *s_al) {
 }
 
 // Warps 0-3: softmax (thread t: token t of the tile, tensor-memory lane t;
-// channel t of O^T); then the dequantizing groups; then one warp each for
+// channel t of O^T); then the dequantizing warps; then one warp each for
 // S^T, O^T and the record copies.  Tensor memory: S^T buffers of N
 // columns from 0, then O^T.  Shared memory: K^ and V^ stages, Q [N][D], P^T
 // tiles [128][N], references and sums, records.
 template <int D, int N>
-__global__ void __launch_bounds__(fw_threads(N), 1)
+__global__ void __launch_bounds__(kFwThreads, 1)
     chunk_few_kernel(KiviGeom g, KiviDev dv, const __half *__restrict__ Q, const __half *__restrict__ Kn,
                      const __half *__restrict__ Vn, __half *__restrict__ O, const __grid_constant__ ChunkArgs a) {
     extern __shared__ __align__(128) unsigned char smem[];
-    constexpr int G = fw_groups(N), TB = kFwKeys * D * 2, KS = kFwStages, PB = kFwKeys * N * 2, QB = N * D * 2;
-    constexpr unsigned QLBO = N * 16, KLBO = kFwKeys * 16, VLBO = D * 16;
+    constexpr int KB = fw_kb(D), VB = fw_vb(D), KS = kFwStages, PB = kFwKeys * N * 2, QB = N * D * 2;
+    constexpr unsigned QLBO = N * 16, KLBO = kFwKS, VLBO = fw_vs(D);
     constexpr int BF = fw_bufs(N), TCOLS = N == 16 ? 128 : 256;   // (BF + 1) N columns, a power of two
     constexpr int LB = BF == 4 ? 2 : 1;                           // log2 of the buffers
-    unsigned char *sK = smem, *sV = sK + KS * TB, *sQ = sV + KS * TB, *sP = sQ + QB, *sR = sP + BF * PB;
-    // counts 8 (two groups): K and V tiles written; 4: Q, P [buffer], the
-    // groups' meetings, records read; 1: the others
-    constexpr int N8 = 2 * KS, N4 = N8 + 1 + BF + G + kFwMaxRaw, NB = N4 + 2 * BF + 2 * KS + kFwMaxRaw;
+    unsigned char *sK = smem, *sV = sK + KS * KB, *sQ = sV + KS * VB, *sP = sQ + QB, *sR = sP + BF * PB;
+    // counts 4 (the softmax warps): Q, P [buffer]; 2 (a tile's two warps, a
+    // record's): K and V tiles written, records read; 1: the others
+    constexpr int N4 = 1 + BF, N2 = N4 + 2 * KS + kFwMaxRaw, NB = N2 + 2 * BF + 2 * KS + kFwMaxRaw;
     __shared__ __align__(8) uint64_t bars[NB];
-    uint64_t *const bK = bars, *const bV = bK + KS, *const bQ = bars + N8, *const bP = bQ + 1, *const bX = bP + BF,
-                    *const eR = bX + G, *const bS = bars + N4, *const bF = bS + BF, *const eK = bF + BF,
-                    *const eV = eK + KS, *const bR = eV + KS;
+    uint64_t *const bQ = bars, *const bP = bars + 1, *const bK = bars + N4, *const bV = bK + KS, *const eR = bV + KS,
+                    *const bS = bars + N2, *const bF = bS + BF, *const eK = bF + BF, *const eV = eK + KS,
+                    *const bR = eV + KS;
     __shared__ uint32_t s_taddr;
     __shared__ int s_abort;
     __shared__ __align__(16) float s_ref[N];       // minus each row's reference (log2 units)
@@ -210,7 +380,7 @@ __global__ void __launch_bounds__(fw_threads(N), 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int hg = a.hg;
     if (tid < NB) {
-        mbar_init(&bars[tid], tid < N8 ? 8 : tid < N4 ? 4 : 1);
+        mbar_init(&bars[tid], tid < N4 ? 4 : tid < N2 ? 2 : 1);
         fence_mbar_init();
     }
     if (tid == 0) s_abort = 0;
@@ -224,7 +394,7 @@ __global__ void __launch_bounds__(fw_threads(N), 1)
     CkWalk walk;
     walk.start(a, blockIdx.x);
     CkSeg sg = {};
-    constexpr int WD = 4, WS = WD + G * kCkDqGroup;   // first dequantizing warp, the S^T warp
+    constexpr int WD = 4, WS = WD + 2 * kFwDq;   // first dequantizing warp, the S^T warp
     // The segment's blocks are [2 x0, nb): how many of them have a record.
     auto raw_blocks = [&](int Tq) {
         const int nb = min(2 * (sg.x0 + sg.nx), sg.nb);
@@ -247,7 +417,7 @@ __global__ void __launch_bounds__(fw_threads(N), 1)
                 ok = __all_sync(kFull, ok);
                 if (!ok) break;
                 tc_fence_after();
-                const uint64_t d = dk + (uint32_t)(t.s * (TB >> 4));
+                const uint64_t d = dk + (uint32_t)(t.s * (KB >> 4));
 #pragma unroll
                 for (int c = 0; c < D / 16; ++c)
                     tc_mma_f16_w(taddr + N * (cs & (BF - 1)), d + ((2 * c * KLBO) >> 4), dq + ((2 * c * QLBO) >> 4), ID, c > 0);
@@ -279,7 +449,7 @@ __global__ void __launch_bounds__(fw_threads(N), 1)
                 ok = __all_sync(kFull, ok);
                 if (!ok) break;
                 tc_fence_after();
-                const uint64_t d = dvd + (uint32_t)(t.s * (TB >> 4)), e = dp + (uint32_t)((cp & (BF - 1)) * (PB >> 4));
+                const uint64_t d = dvd + (uint32_t)(t.s * (VB >> 4)), e = dp + (uint32_t)((cp & (BF - 1)) * (PB >> 4));
 #pragma unroll
                 for (int c = 0; c < kFwKeys / 16; ++c)
                     tc_mma_f16_w(taddr + BF * N, d + ((2 * c * VLBO) >> 4), e + ((256 * c) >> 4), ID, x > 0 || c > 0);
@@ -322,60 +492,45 @@ __global__ void __launch_bounds__(fw_threads(N), 1)
         }
         __syncwarp();
     } else if (warp >= WD) {
-        // ---- K^ and V^^T: the CTA's tile y is restored by groups 2 y mod G
-        // and 2 y + 1 mod G, a block each ----
-        const int grp = (warp - WD) / kCkDqGroup, half = grp & 1;
-        FwGroup f;
-        f.w = (warp - WD) % kCkDqGroup;
-        f.dt = (tid - 32 * WD) & (32 * kCkDqGroup - 1);
-        f.lgG = __ffs(g.G) - 1;
-        f.meets = 0;
-        f.bX = &bX[grp];
-        f.abort = abort;
-        int tiles = 0, recs = 0;   // of the CTA so far
+        // ---- K^ (the first four warps) or V^^T (the others): the CTA's blocks,
+        // two a tile, in turn ----
+        const int w = (warp - WD) % kFwDq, lgG = __ffs(g.G) - 1;
+        const bool keys = warp < WD + kFwDq;
+        uint64_t *const bT = keys ? bK : bV, *const eT = keys ? eK : eV;   // the tile written, read
+        int tiles = 0;   // of the CTA so far
+        CkRing seg;      // the segment's first record's stage
         while (ok && walk.next(g, a, sg)) {
             const int nraw = raw_blocks(max(a.Tqk[sg.i], a.Tqv[sg.i]));
             const int npk = sg.bl.virt(min(a.Tqk[sg.i], a.Tqv[sg.i]) / KIVI_KBLK) - 2 * sg.x0;   // fully quantized blocks
-            // the segment's first tile of this group; its stage, and the
-            // record's (if any)
-            int x = ((grp >> 1) - tiles % (G / 2) + G / 2) % (G / 2);
-            for (; x < sg.nx; x += G / 2) {
-                const int y = tiles + x, st = y % KS, blk = 2 * x + half, rec = recs + blk, rst = rec % a.rs;
-                const unsigned tp = (unsigned)(y / KS) & 1u;
+            int blk = (w - 2 * tiles) & (kFwDq - 1);   // the segment's first block of this warp
+            CkRing r = seg;
+            r.skip(blk, a.rs);
+            for (; blk < 2 * sg.nx; blk += kFwDq, r.skip(kFwDq, a.rs)) {
+                const int y = tiles + (blk >> 1), st = y % KS, half = blk & 1;
                 const bool raw = blk < nraw;
-                unsigned char *kt = sK + st * TB + half * KIVI_KBLK * 16;
-                unsigned char *vt = sV + st * TB + half * (KIVI_KBLK / 8) * (int)VLBO;
-                const unsigned char *rp = sR + (size_t)rst * g.rec_bytes;
-                ok = (y < KS || mbar_wait_ab(&eK[st], tp ^ 1u, abort)) &&
-                     (!raw || mbar_wait_ab(&bR[rst], (unsigned)(rec / a.rs) & 1u, abort));
+                const unsigned char *rp = sR + (size_t)r.s * g.rec_bytes;
+                ok = (y < KS || mbar_wait_ab(&eT[st], (unsigned)(y / KS + 1) & 1u, abort)) &&
+                     (!raw || mbar_wait_ab(&bR[r.s], r.p, abort));
                 ok = __all_sync(kFull, ok);
                 if (!ok) break;
-                if (blk < npk) {
-                    if (g.kbits == 2) dequant_keys<D, 2, kFwKeys>(kt, rp, g.off_ksz, f.lgG, f.w);
-                    else dequant_keys<D, 4, kFwKeys>(kt, rp, g.off_ksz, f.lgG, f.w);
-                } else if (!(ok = cold_keys<D>(f, g, dv, Kn, a, sg, blk, kt, rp))) {
-                    break;
-                }
-                fence_proxy_async();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bK[st]);
-                ok = __all_sync(kFull, y < KS || mbar_wait_ab(&eV[st], tp ^ 1u, abort));
-                if (!ok) break;
-                if (blk < npk) {
-                    if (g.vbits == 2) dequant_values<D, 2>(vt, rp, g.off_vc, g.off_vsz, f.lgG, f.w);
-                    else dequant_values<D, 4>(vt, rp, g.off_vc, g.off_vsz, f.lgG, f.w);
-                } else if (!(ok = cold_values<D>(f, g, dv, Vn, a, sg, blk, vt, rp))) {
-                    break;
+                if (keys) {
+                    unsigned char *kt = sK + st * KB + half * KIVI_KBLK * 16;
+                    if (blk < npk) few_keys<D>(g, kt, rp, lgG);
+                    else cold_keys<D>(g, dv, Kn, a, sg, blk, kt, rp);
+                } else {
+                    unsigned char *vt = sV + st * VB + half * (KIVI_KBLK / 8) * (int)VLBO;
+                    if (blk < npk) few_values<D>(g, vt, rp, lgG);
+                    else cold_values<D>(g, dv, Vn, a, sg, blk, vt, rp);
                 }
                 fence_proxy_async();
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(&bV[st]);
-                    if (raw) mbar_arrive(&eR[rst]);
+                    mbar_arrive(&bT[st]);
+                    if (raw) mbar_arrive(&eR[r.s]);
                 }
             }
             tiles += sg.nx;
-            recs += nraw;
+            seg.skip(nraw, a.rs);
         }
         if (!ok && lane == 0) {
             s_abort = 1;
@@ -389,6 +544,7 @@ __global__ void __launch_bounds__(fw_threads(N), 1)
         const float sl2 = 1.4426950408889634f / sqrtf((float)D);   // log2(e) / sqrt(d)
         const int W = a.vis.window, sinks = a.vis.sinks;
         constexpr int CH = 16;   // columns at a time
+        const int kpos = fw_tok(tid);
         int cnt = 0;             // tiles so far
         while (walk.next(g, a, sg)) {
             // Q: row (r, e) from head e of token r; rows past the chunk are zero
@@ -401,7 +557,7 @@ __global__ void __launch_bounds__(fw_threads(N), 1)
                     v = *reinterpret_cast<const uint4 *>(
                         Q + (((size_t)sg.i * a.hq + sg.j * hg + rw - tok * hg) * a.n_stride + tok) * D + 8 * c);
                 }
-                *reinterpret_cast<uint4 *>(sQ + c * QLBO + q * 16) = v;
+                fw_put<N * 16>(sQ, q, c, v);
             }
             if (tid < N) s_ref[tid] = kFwUnset;
             fence_proxy_async();
@@ -421,18 +577,25 @@ __global__ void __launch_bounds__(fw_threads(N), 1)
                 tc_fence_after();
                 // some row does not see all of this warp's block
                 const bool cut = kb + KIVI_KBLK - 1 > p0 || (W > 0 && kb <= p1 - W && kb + KIVI_KBLK > sinks);
-                // 16 scores of this token in log2 units, masked
-                auto scores = [&](int c0, float (&s)[CH]) {
+                // 16 scores of this token as log2 weights against the rows'
+                // references, masked
+                auto scores = [&](int c0, float (&y)[CH]) {
                     uint32_t r[CH];
                     tc_ld16(tS + c0, r);
                     tc_wait_ld();
 #pragma unroll
-                    for (int c = 0; c < CH; ++c) s[c] = __uint_as_float(r[c]) * sl2;
+                    for (int c = 0; c < CH; c += 4) {
+                        const float4 ref = *reinterpret_cast<const float4 *>(s_ref + c0 + c);
+                        y[c] = fmaf(__uint_as_float(r[c]), sl2, ref.x);
+                        y[c + 1] = fmaf(__uint_as_float(r[c + 1]), sl2, ref.y);
+                        y[c + 2] = fmaf(__uint_as_float(r[c + 2]), sl2, ref.z);
+                        y[c + 3] = fmaf(__uint_as_float(r[c + 3]), sl2, ref.w);
+                    }
                     if (cut) {
                         const uint32_t h = ck_hidden16(key, c0, p0, e0, hg, W, sinks);
 #pragma unroll
                         for (int c = 0; c < CH; ++c)
-                            if ((h >> c) & 1u) s[c] = -INFINITY;
+                            if ((h >> c) & 1u) y[c] = -INFINITY;
                     }
                 };
                 float s[CH], up = -INFINITY;   // the most that a score lies above its reference
@@ -441,7 +604,7 @@ __global__ void __launch_bounds__(fw_threads(N), 1)
                     for (int c0 = 0; c0 < N; c0 += CH) {
                         scores(c0, s);
 #pragma unroll
-                        for (int c = 0; c < CH; ++c) up = fmaxf(up, s[c] + s_ref[c0 + c]);
+                        for (int c = 0; c < CH; ++c) up = fmaxf(up, s[c]);
                     }
                 const bool raise = fw_any(!ok || up > 8.f);
                 if (raise) {
@@ -470,14 +633,14 @@ __global__ void __launch_bounds__(fw_threads(N), 1)
                     uint32_t pw[CH / 2];
 #pragma unroll
                     for (int c = 0; c < CH; c += 2) {
-                        const float y0 = ex2(s[c] + s_ref[c0 + c]), y1 = ex2(s[c + 1] + s_ref[c0 + c + 1]);
+                        const float y0 = ex2(s[c]), y1 = ex2(s[c + 1]);
                         lsum[c0 + c] += y0;
                         lsum[c0 + c + 1] += y1;
                         pw[c / 2] = ck_pack(y0, y1);
                     }
 #pragma unroll
                     for (int k = 0; k < CH / 8; ++k)
-                        *reinterpret_cast<uint4 *>(sP + b * PB + ((c0 / 8 + k) * kFwKeys + tid) * 16) =
+                        *reinterpret_cast<uint4 *>(sP + b * PB + ((c0 / 8 + k) * kFwKeys + kpos) * 16) =
                             make_uint4(pw[4 * k], pw[4 * k + 1], pw[4 * k + 2], pw[4 * k + 3]);
                 }
                 fence_proxy_async();

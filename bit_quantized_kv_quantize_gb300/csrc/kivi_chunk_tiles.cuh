@@ -138,6 +138,9 @@ struct CkRing {
             p ^= 1u;
         }
     }
+    __device__ __forceinline__ void skip(int k, int n) {
+        for (s += k; s >= n; s -= n) p ^= 1u;
+    }
 };
 
 // A CTA's share of one row tile.

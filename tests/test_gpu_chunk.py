@@ -85,6 +85,72 @@ def test_chunk_attention(b, hq, h, d, kb, vb, G, Rw, T, steps, n, window, sinks)
     c.close()
 
 
+def _attention_case(b, hq, h, d, kb, vb, G, Rw, T, steps, n, window, sinks):
+    c, Q, Kn, Vn, keys, vals = _setup(b, hq, h, d, kb, vb, G, Rw, T, steps, n, 5 + d + G + sum(n))
+    out = c.chunk_attn(*_cuda(Q, Kn, Vn), n, window, sinks).float().cpu().numpy()
+    for i in range(b):
+        t = T[i] + steps
+        _, qk, qv = R.counters_after(T[i], *R.counters(T[i], Rw), steps, Rw)
+        for j in range(h):
+            k, v = R.restore(keys[i][j], vals[i][j], qk, qv, kb, vb, G)
+            k = np.concatenate([k, Kn[i, j, :n[i]].astype(np.float64)])
+            v = np.concatenate([v, Vn[i, j, :n[i]].astype(np.float64)])
+            see = R.visible(t + np.arange(n[i]), t + n[i], window, sinks)
+            for e in range(j * (hq // h), (j + 1) * (hq // h)):
+                ref, wabs, mag = R.attend(Q[i, e, :n[i]], k, v, see)
+                R.check_rounded(out[i, e, :n[i]], ref, wabs, mag, t + n[i], f"sequence {i} head {e}")
+    assert c.check() == 0
+    c.close()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("kb", [2, 4])
+@pytest.mark.parametrize("vb", [2, 4])
+@pytest.mark.parametrize("G", [16, 32, 64, 128])
+@pytest.mark.parametrize("n", [3, 45])
+def test_chunk_attention_formats(d, kb, vb, G, n):
+    """Every record format, with few rows and with many."""
+    if G > d:
+        pytest.skip("needs d % G == 0")
+    _attention_case(1, 4, 1, d, kb, vb, G, max(G, 32), [413], G // 8, [n], 0, 0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n,hq", [(1, 8), (2, 8), (5, 5), (8, 2), (16, 4), (13, 8), (17, 8), (64, 1)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (150, 70), (3, 0)])
+def test_chunk_attention_row_counts(n, hq, window, sinks):
+    """Row counts around the row tiles' sizes, even and odd numbers of blocks."""
+    _attention_case(2, hq, 1, 128, 2, 4, 32, 32, [700, 10], 1, [n, max(n - 1, 1)], window, sinks)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n", [2, 40])
+def test_growing_scores(n):
+    """Keys grow along the sequence, so the running maximum rises by far more
+    than 2^8 in weight again and again."""
+    from bit_quantized_kv_quantize_gb300 import kivi as K
+    rng = np.random.default_rng(4)
+    t, d = 1500, 64
+    Kh, Vh = (rng.standard_normal((1, 1, t, d)).astype(np.float16) for _ in range(2))
+    Kh[:] = np.abs(Kh) * (np.arange(t) / 150.0).astype(np.float16)[None, None, :, None]
+    Q = np.abs(rng.standard_normal((1, 2, n, d))).astype(np.float16)
+    Kn, Vn = (rng.standard_normal((1, 1, n, d)).astype(np.float16) for _ in range(2))
+    c = K.KiviCache(1, 1, d, 4, 4, 32, 64, t + n)
+    c.prefill(*_cuda(Kh, Vh), t)
+    out = c.chunk_attn(*_cuda(Q, Kn, Vn), n).float().cpu().numpy()
+    k, v = R.restore(Kh[0, 0], Vh[0, 0], *R.counters(t, 64), 4, 4, 32)
+    k, v = np.concatenate([k, Kn[0, 0].astype(np.float64)]), np.concatenate([v, Vn[0, 0].astype(np.float64)])
+    for e in range(2):
+        ref, wabs, mag = R.attend(Q[0, e], k, v, R.visible(t + np.arange(n), t + n, 0, 0))
+        got, h = out[0, e].astype(np.float64), 2.0 ** -11
+        # (the pointwise part of check_rounded: few tokens carry these rows, so
+        # their roundings do not average)
+        bound = wabs * (np.expm1(2 * h * mag)[:, None] + 2 * h + (t + n) * 2.0 ** -23) + np.abs(ref) * h
+        assert np.all(np.abs(got - ref) <= bound + wabs * (t + n) * 2.0 ** -25 + 2.0 ** -24)
+    c.close()
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("b,h,d,kb,vb,G,Rw,T,steps,n", [
     (1, 1, 64, 2, 2, 32, 32, [0], 0, 1),
