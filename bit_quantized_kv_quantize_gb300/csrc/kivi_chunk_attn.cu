@@ -50,10 +50,12 @@ cudaError_t kivi_launch_chunk_attn(const KiviGeom &g, const KiviDev &dv, const _
     int maxrows = 0;
     for (int i = 0; i < g.b; ++i) maxrows = a.n[i] * hg > maxrows ? a.n[i] * hg : maxrows;
     if (maxrows == 0) return cudaSuccess;
-    // Up to 64 rows a kv head: the transposed kernel, whose work follows the
-    // rows (4 tokens of 8 sequences over 32k: 244 us with 256-row tiles).
-    const bool few = maxrows <= 64;
-    a.tile_rows = !few ? kCkTileRows : maxrows <= 16 ? 16 : maxrows <= 32 ? 32 : 64;
+    // Up to 32 rows a kv head: the transposed kernel, whose work follows the
+    // rows.  Over 32k tokens of 8 sequences of 8 heads, in microseconds, it and
+    // 256-row tiles: 16 rows 149 and 235, 32 rows 190 and 235, 64 rows 270
+    // and 238.  (Over 1000 tokens, 32 rows: 38 and 33.)
+    const bool few = maxrows <= 32;
+    a.tile_rows = !few ? kCkTileRows : maxrows <= 16 ? 16 : 32;
     a.tile_blocks = few ? 2 : 1;
     long long items = 0, U = 0;
     for (int i = 0; i < g.b; ++i) {

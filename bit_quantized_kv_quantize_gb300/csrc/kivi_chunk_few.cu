@@ -7,7 +7,7 @@ namespace {
 template <int D, int N>
 cudaError_t launch_few(const KiviGeom &g, const KiviDev &dv, const __half *Q, const __half *K, const __half *V,
                        __half *O, ChunkArgs &a, int ctas, cudaStream_t st) {
-    const size_t fixed = (size_t)kFwStages * (fw_kb(D) + fw_vb(D)) + (size_t)N * D * 2 + (size_t)fw_bufs(N) * kFwKeys * N * 2;
+    const size_t fixed = (size_t)kFwStages * (fw_kb(D) + fw_vb(D)) + (size_t)N * D * 2 + (size_t)kFwBufs * kFwKeys * N * 2;
     a.rs = (int)((224 * 1024 - fixed) / g.rec_bytes);
     if (a.rs > kFwMaxRaw) a.rs = kFwMaxRaw;
     if (a.rs < 4) return cudaErrorInvalidValue;
@@ -23,10 +23,8 @@ cudaError_t launch_few(const KiviGeom &g, const KiviDev &dv, const __half *Q, co
 cudaError_t kivi_launch_chunk_few(const KiviGeom &g, const KiviDev &dv, const __half *Q, const __half *K,
                                   const __half *V, __half *O, ChunkArgs &a, int ctas, cudaStream_t st) {
     if (g.d == 64)
-        return a.tile_rows == 16   ? launch_few<64, 16>(g, dv, Q, K, V, O, a, ctas, st)
-               : a.tile_rows == 32 ? launch_few<64, 32>(g, dv, Q, K, V, O, a, ctas, st)
-                                   : launch_few<64, 64>(g, dv, Q, K, V, O, a, ctas, st);
-    return a.tile_rows == 16   ? launch_few<128, 16>(g, dv, Q, K, V, O, a, ctas, st)
-           : a.tile_rows == 32 ? launch_few<128, 32>(g, dv, Q, K, V, O, a, ctas, st)
-                               : launch_few<128, 64>(g, dv, Q, K, V, O, a, ctas, st);
+        return a.tile_rows == 16 ? launch_few<64, 16>(g, dv, Q, K, V, O, a, ctas, st)
+                                 : launch_few<64, 32>(g, dv, Q, K, V, O, a, ctas, st);
+    return a.tile_rows == 16 ? launch_few<128, 16>(g, dv, Q, K, V, O, a, ctas, st)
+                             : launch_few<128, 32>(g, dv, Q, K, V, O, a, ctas, st);
 }

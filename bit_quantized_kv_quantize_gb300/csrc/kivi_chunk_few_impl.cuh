@@ -5,7 +5,7 @@
 // With 128 query rows on the MMA's M side, a few rows leave most of the tensor
 // cores' and the softmax's work padding, and a tile takes about 1800 cycles
 // however few the rows.  Here the tokens are on the M side and the rows on N
-// (N = 16, 32 or 64):
+// (N = 16 or 32):
 //   S^T [128 tokens x N] = K^ Q^T,   O^T [d x N] += V^^T P^T,
 // so a tile of 128 tokens costs 16 MMAs of N columns, thread t of the softmax
 // owns token t and computes N weights, and what remains is restoring the
@@ -49,8 +49,8 @@ constexpr int kFwMaxRaw = 12;   // records in flight
 constexpr int kFwDq = 4;
 constexpr int kFwThreads = 32 * (4 + 2 * kFwDq + 3);
 // S^T and P^T buffers: tiles that the softmax may be apart from either MMA
-// (four hide the waits between the roles; with 64 rows there is room for two)
-__host__ __device__ constexpr int fw_bufs(int N) { return N == 64 ? 2 : 4; }
+// (four hide the waits between the roles)
+constexpr int kFwBufs = 4;
 // Bytes from a 16-byte chunk to the next along a row of K^, and of V^^T: 32
 // more than their rows take, so that the lanes of a store (2 rows of 4 chunks)
 // fall in different banks; bytes of a tile.
@@ -362,8 +362,8 @@ __global__ void __launch_bounds__(kFwThreads, 1)
     extern __shared__ __align__(128) unsigned char smem[];
     constexpr int KB = fw_kb(D), VB = fw_vb(D), KS = kFwStages, PB = kFwKeys * N * 2, QB = N * D * 2;
     constexpr unsigned QLBO = N * 16, KLBO = kFwKS, VLBO = fw_vs(D);
-    constexpr int BF = fw_bufs(N), TCOLS = N == 16 ? 128 : 256;   // (BF + 1) N columns, a power of two
-    constexpr int LB = BF == 4 ? 2 : 1;                           // log2 of the buffers
+    constexpr int BF = kFwBufs, LB = 2;             // buffers, log2 of them
+    constexpr int TCOLS = N == 16 ? 128 : 256;      // (BF + 1) N columns, a power of two
     unsigned char *sK = smem, *sV = sK + KS * KB, *sQ = sV + KS * VB, *sP = sQ + QB, *sR = sP + BF * PB;
     // counts 4 (the softmax warps): Q, P [buffer]; 2 (a tile's two warps, a
     // record's): K and V tiles written, records read; 1: the others
