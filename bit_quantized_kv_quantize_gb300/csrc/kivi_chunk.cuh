@@ -21,7 +21,6 @@ struct ChunkArgs {
     int tile_rows, tile_blocks;   // rows of a row tile, 64-token blocks of a key tile
     Visible vis;
     float *acc, *ml;  // partials: [2 CTAs][tile_rows][d] and [2 CTAs][tile_rows][2]
-    int ctas;
     ChunkPos cta[kCkMaxCtas + 1];
     int T[KIVI_MAX_BATCH], Tqk[KIVI_MAX_BATCH], Tqv[KIVI_MAX_BATCH], n[KIVI_MAX_BATCH];
 };

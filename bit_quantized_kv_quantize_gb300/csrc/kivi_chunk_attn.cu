@@ -47,9 +47,15 @@ cudaError_t kivi_launch_chunk_attn(const KiviGeom &g, const KiviDev &dv, const _
     const int hg = a.hq / g.h;
     a.hg = hg;
     a.hg_mul = (unsigned)(((1ull << 32) + hg - 1) / hg);
-    int maxrows = 0;
-    for (int i = 0; i < g.b; ++i) maxrows = a.n[i] * hg > maxrows ? a.n[i] * hg : maxrows;
+    int maxrows = 0, end = 0;
+    for (int i = 0; i < g.b; ++i) {
+        maxrows = a.n[i] * hg > maxrows ? a.n[i] * hg : maxrows;
+        end = a.T[i] + a.n[i] > end ? a.T[i] + a.n[i] : end;
+    }
     if (maxrows == 0) return cudaSuccess;
+    // a window that no position reaches is none (and would pass 32 bits below
+    // the first positions)
+    if (a.vis.window >= end) a.vis = Visible{0, 0};
     // Up to 32 rows a kv head: the transposed kernel, whose work follows the
     // rows.  Over 32k tokens of 8 sequences of 8 heads, in microseconds, it and
     // 256-row tiles: 16 rows 149 and 235, 32 rows 190 and 235, 64 rows 270
@@ -86,7 +92,6 @@ cudaError_t kivi_launch_chunk_attn(const KiviGeom &g, const KiviDev &dv, const _
             }
             P = end;
         }
-    a.ctas = ctas;
     a.cta[ctas] = ChunkPos{U, 0, 0, 0, 0};
     a.acc = partials;
     a.ml = partials + (size_t)2 * num_sms * kCkTileRows * g.d;

@@ -571,7 +571,7 @@ __global__ void __launch_bounds__(kFwThreads, 1)
             for (int c = 0; c < N; ++c) lsum[c] = 0.f;
             for (int x = 0; x < sg.nx; ++x, ++cnt) {
                 const int b = cnt & (BF - 1), v = 2 * (sg.x0 + x) + (tid >> 6);
-                const int kb = v < sg.nb ? sg.bl.phys(v) * KIVI_KBLK : 1 << 30, key = kb + (tid & 63);
+                const int kb = v < sg.nb ? sg.bl.phys(v) * KIVI_KBLK : 0x7fffff00, key = kb + (tid & 63);
                 const uint32_t tS = taddr + lane_off + N * b;
                 ok = ok && __all_sync(kFull, mbar_wait_ab(&bS[b], (unsigned)(cnt >> LB) & 1u, abort));
                 tc_fence_after();

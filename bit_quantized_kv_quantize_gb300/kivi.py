@@ -11,6 +11,7 @@ import array
 import contextlib
 import ctypes
 import math
+import operator
 import os
 
 import numpy as np
@@ -134,6 +135,12 @@ def _counts(n, b, name="n"):
         raise ValueError(f"{name} must be an integer or {b} integers") from None
     except OverflowError:
         raise ValueError(f"{name} outside 32 bits") from None
+
+
+def _visible(window, sinks):
+    """A window and a number of sinks as C ints; those past 32 bits mean the
+    same as the largest (or, negative, are refused alike)."""
+    return tuple(max(-1, min(operator.index(x), 2**31 - 1)) for x in (window, sinks))
 
 
 def _addr(a):
@@ -312,7 +319,7 @@ class KiviCache:
         op = _dev_fp16(out, (self.b, hq, ts, self.d), "out")
         if window or sinks:
             self._here(Q, K, V, out)
-            _check(lib.kivi_prefill_attn_window(self._h, qp, kp, vp, t.ctypes.data, ts, hq, window, sinks, op,
+            _check(lib.kivi_prefill_attn_window(self._h, qp, kp, vp, t.ctypes.data, ts, hq, *_visible(window, sinks), op,
                                                 _stream(stream)))
         else:
             _check(lib.kivi_prefill_attn(self._h, qp, kp, vp, t.ctypes.data, ts, hq, op, _stream(stream)))
@@ -345,7 +352,7 @@ class KiviCache:
         tensor).  Does not append (append_chunk, extend)."""
         kp, vp, cnt, ns = self._chunk(K, V, n)
         qp, out, op = self._chunk_out(Q, ns, out, stream)
-        _check(lib.kivi_chunk_attn(self._h, qp, kp, vp, _addr(cnt), ns, Q.shape[1], window, sinks, op,
+        _check(lib.kivi_chunk_attn(self._h, qp, kp, vp, _addr(cnt), ns, Q.shape[1], *_visible(window, sinks), op,
                                    _stream(stream)))
         return out
 
@@ -361,6 +368,7 @@ class KiviCache:
         attend (chunk_attn; returns its out) and append it (append_chunk)."""
         import torch
         kp, vp, cnt, ns = self._chunk(K, V, n)
+        win, snk = _visible(window, sinks)
         T = array.array("i", bytes(4 * self.b))
         _check(lib.kivi_cache_lengths(self._h, _addr(T), None, None))
         for i in range(self.b):
@@ -375,7 +383,7 @@ class KiviCache:
                 rq, rk = torch.empty_like(Q), torch.empty_like(K)
             rope._call(qp, kp, self.b, hq, self.h_kv, ns, cnt, T, None, False, rq.data_ptr(), rk.data_ptr(), st)
             qp, kp = rq.data_ptr(), rk.data_ptr()
-        _check(lib.kivi_chunk_attn(self._h, qp, kp, vp, cp, ns, hq, window, sinks, op, st))
+        _check(lib.kivi_chunk_attn(self._h, qp, kp, vp, cp, ns, hq, win, snk, op, st))
         _check(lib.kivi_append_chunk(self._h, kp, vp, cp, ns, st))
         return out
 
@@ -397,7 +405,7 @@ class KiviCache:
         op = _dev_fp16(out, (self.b, hq, self.d), "out")
         if window or sinks:
             self._here(q, out)
-            _check(lib.kivi_decode_attn_window(self._h, qp, hq, window, sinks, op, _stream(stream)))
+            _check(lib.kivi_decode_attn_window(self._h, qp, hq, *_visible(window, sinks), op, _stream(stream)))
         else:
             _check(lib.kivi_decode_attn(self._h, qp, hq, op, _stream(stream)))
         return out

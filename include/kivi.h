@@ -64,8 +64,9 @@ typedef enum {
  * holding up to max_tokens tokens per sequence; k_bits / v_bits per item 1,
  * group size G per items 2-3, residual length R per item 4.  All device
  * memory of the cache is allocated here (packed codes, fp16 scale/zero,
- * fp16 residual windows, counters, decode partials).  *out receives the
- * handle; release it with kivi_cache_destroy. */
+ * fp16 residual windows, counters, decode partials, and with d <= 128 the
+ * chunk attention's partials: 2 x SMs x 256 rows of d + 2 floats, 40 MB at
+ * d = 128).  *out receives the handle; release it with kivi_cache_destroy. */
 kivi_status kivi_cache_create(int b, int h_kv, int d, int k_bits, int v_bits, int G, int R,
                               int max_tokens, kivi_cache_t *out);
 
@@ -109,7 +110,9 @@ kivi_status kivi_prefill_attn(kivi_cache_t c, const void *q, const void *K, cons
 
 /* kivi_prefill_attn with a sliding window: out is the windowed attention of
  * the prompt; the cache afterwards is the same (it takes every token).  Key
- * tiles that no query of a tile sees are neither read nor multiplied. */
+ * tiles that no query of a tile sees are neither read nor multiplied.  With
+ * window > 0 several launches, which use the cache's buffer as
+ * kivi_chunk_attn's do; b h_kv t_stride below 2^31. */
 kivi_status kivi_prefill_attn_window(kivi_cache_t c, const void *q, const void *K, const void *V, const int32_t *t,
                                      int t_stride, int h_q, int window, int sinks, void *out,
                                      kivi_stream_t stream);
@@ -128,9 +131,8 @@ kivi_status kivi_prefill_attn_window(kivi_cache_t c, const void *q, const void *
  * rejected draft needs no undoing.  Scores accumulate in fp32; the restored
  * keys and values (scale code + zero) and the softmax weights are rounded to
  * fp16 before the products (|K|, |V| <= 32768, so that they stay finite).
- * One launch, or two when few rows meet long sequences (their tokens are
- * then split over CTAs and joined; a call's result is repeatable bit for
- * bit).  Uses a buffer of the cache: calls on one cache that overlap on the
+ * out overlaps no input.  One launch, or two when row tiles are split over
+ * CTAs and joined (a call's result is repeatable bit for bit).  Uses a buffer of the cache: calls on one cache that overlap on the
  * GPU (two streams, or two captured graphs replayed at once) must not be
  * issued.  A captured call replays with the counts and positions it was
  * captured with.  Supports d 64 or 128 (KIVI_ERR_UNSUPPORTED otherwise) and

@@ -350,3 +350,39 @@ def test_refusals():
     assert status(lambda: w.chunk_attn(x, x, x, 1)) == 2                # d = 256
     w.append_chunk(x, x, 4)
     w.close()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n", [3, 90])
+@pytest.mark.parametrize("window", [2**31 - 1, 2**31 - 64, 2**31, 2**40])
+def test_window_beyond_every_position(n, window):
+    """A window that no position reaches is no window, in every call; both
+    row-tile forms."""
+    import torch
+    from bit_quantized_kv_quantize_gb300 import kivi as K
+    rng = np.random.default_rng(window % 97 + n)
+    b, h, hq, d, t = 2, 2, 4, 64, 200
+    c = K.KiviCache(b, h, d, 2, 4, 32, 32, t + n)
+    Q, Kp, Vp = _cuda(*(rng.standard_normal((b, x, t, d)).astype(np.float16) for x in (hq, h, h)))
+    plain = c.prefill_attn(Q, Kp, Vp, t)
+    # (another kernel than the plain prompt's: each rounds the weights to fp16
+    # and its output, by 2^-11 of at most max |V|)
+    diff = (c.prefill_attn(Q, Kp, Vp, t, window=window).float() - plain.float()).abs().max()
+    assert diff <= 4 * 2.0 ** -11 * Vp.abs().max().float()
+    q = Q[:, :, :n].contiguous()
+    k, v = Kp[:, :, :n].contiguous(), Vp[:, :, :n].contiguous()
+    assert torch.equal(c.chunk_attn(q, k, v, n, window=window, sinks=2**31), c.chunk_attn(q, k, v, n))
+    assert torch.equal(c.decode(q[:, :, 0].contiguous(), window=window, sinks=2**40), c.decode(q[:, :, 0].contiguous()))
+    assert torch.equal(c.chunk_attn(q, k, v, n, window=7, sinks=2**32 + 1), c.chunk_attn(q, k, v, n, window=7, sinks=2**31 - 1))
+    for bad in (-1, -2**31, -2**32, -2**40):
+        with pytest.raises(K.KiviError):
+            c.chunk_attn(q, k, v, n, window=bad)
+        with pytest.raises(K.KiviError):
+            c.decode(q[:, :, 0].contiguous(), window=4, sinks=bad)
+        with pytest.raises(K.KiviError):
+            c.prefill_attn(Q, Kp, Vp, t, window=bad)
+    for bad in (4.0, "4", None):
+        with pytest.raises(TypeError):
+            c.chunk_attn(q, k, v, n, window=bad)
+    assert c.check() == 0
+    c.close()
