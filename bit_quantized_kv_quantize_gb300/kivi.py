@@ -315,7 +315,8 @@ class KiviCache:
         kp = _dev_fp16(K, (self.b, self.h_kv, ts, self.d), "K")
         vp = _dev_fp16(V, (self.b, self.h_kv, ts, self.d), "V")
         if out is None:
-            out = torch.zeros_like(Q)
+            with _on(stream):
+                out = torch.zeros_like(Q)
         op = _dev_fp16(out, (self.b, hq, ts, self.d), "out")
         if window or sinks:
             self._here(Q, K, V, out)
@@ -401,7 +402,8 @@ class KiviCache:
         hq = q.shape[1]
         qp = _dev_fp16(q, (self.b, hq, self.d), "q")
         if out is None:
-            out = torch.empty_like(q)
+            with _on(stream):
+                out = torch.empty_like(q)
         op = _dev_fp16(out, (self.b, hq, self.d), "out")
         if window or sinks:
             self._here(q, out)

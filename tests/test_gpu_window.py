@@ -137,3 +137,37 @@ def test_window_zero_is_everything_and_refusals():
             c.prefill_attn(qq, x, x, 150, **kw)
     assert c.lengths()[0].tolist() == [150]
     c.close()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("window", [0, 70])
+def test_other_stream_and_graph(window):
+    """A prompt and a step on a stream of their own, their outputs made there
+    too (the current stream is busy meanwhile), and captured and replayed."""
+    import torch
+    from bit_quantized_kv_quantize_gb300 import kivi as K
+    rng = np.random.default_rng(5)
+    b, h, hq, d, ts, t = 2, 2, 4, 64, 150, [150, 90]
+    c = K.KiviCache(b, h, d, 2, 2, 32, 64, 256)
+    Q, Kp, Vp = (torch.from_numpy(rng.standard_normal((b, x, ts, d)).astype(np.float16)).cuda() for x in (hq, h, h))
+    q = Q[:, :, 7].contiguous()
+    want, step = c.prefill_attn(Q, Kp, Vp, t, window=window, sinks=3), c.decode(q, window=window, sinks=3)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    torch.cuda._sleep(20_000_000)
+    got = c.prefill_attn(Q, Kp, Vp, t, stream=s, window=window, sinks=3)
+    dec = c.decode(q, stream=s, window=window, sinks=3)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and torch.equal(dec, step)
+    g = torch.cuda.CUDAGraph()
+    got.zero_()
+    with torch.cuda.graph(g):
+        c.prefill_attn(Q, Kp, Vp, t, out=got, window=window, sinks=3)
+        c.decode(q, out=dec, window=window, sinks=3)
+    for _ in range(2):
+        dec.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want) and torch.equal(dec, step)
+    assert c.check() == 0
+    c.close()
