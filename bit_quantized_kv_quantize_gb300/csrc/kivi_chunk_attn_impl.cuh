@@ -21,12 +21,13 @@
 // up to 1.2e-3 where keys have channels 8 times the others; an fp16 output
 // alone rounds by 2e-4).
 //
-// Pipeline.  A slot has two S buffers of 64 columns (P over the first 32) and
-// O.  One warp issues the S MMAs, up to two tiles ahead (once the P V that
-// reads a buffer's weights is done), another the P V MMAs, so that a wait of
-// one does not hold the other back; slots wait for their own work only.  (One 128-column buffer a slot, S
-// following P V, makes the softmax, P V and S of a slot a serial chain:
-// 5150 against 4400 cycles a 128-token tile pair, measured.)
+// Pipeline.  A slot has one S buffer of 64 columns, two P buffers of 32 and O.
+// The scores are read into registers at once, so S of the next tile runs
+// under the softmax of this one, and P V of the last tile too.  (With P
+// written over its scores in one of two S buffers, S of a tile had to wait for
+// P V of the last but one: 1100 cycles of softmax a tile and 600 of waiting
+// for scores, measured.)  A warp issues a slot's S MMAs, another both slots'
+// P V MMAs, so that a wait of one does not hold the others back.
 //
 // Records (packed codes, scales, zeros) come into a ring of shared-memory
 // stages, one bulk copy each, several ahead.  Four warps restore a tile: K^
@@ -56,7 +57,7 @@ constexpr int kCkStages = 3;     // K^ tiles, and V^ tiles, in flight
 constexpr int kCkMaxRaw = 8;     // records in flight
 constexpr int kCkDq = kCkDqGroup;   // dequantizing warps
 constexpr int kCkOut = 8 * 32 * 64;   // a softmax warp's 32 rows x 32 columns of the output
-constexpr int kCkThreads = 32 * (8 + kCkDq + 3);
+constexpr int kCkThreads = 32 * (8 + kCkDq + 4);
 
 // {a, b} as one 64-bit operand of the packed fp32 instructions
 __device__ __forceinline__ unsigned long long ck_f2(float a, float b) {
@@ -125,8 +126,9 @@ __device__ __forceinline__ void tma_rows(void *dst, const CUtensorMap *tm, int r
 }
 
 // Warps 0-7: softmax (thread tid owns row tid mod 128 of slot tid / 128,
-// tensor-memory columns [256 slot, + 256): S / P buffers in 0-63 and 64-127,
-// O from 128); 8-11: dequantizing; 12: S = Q K^T; 13: O += P V; 14: record copies.  They
+// tensor-memory columns [256 slot, + 256): S in 0-63, P buffers from 64 and 96,
+// O from 128); 8-11: dequantizing; 12, 13: S = Q K^T of a slot; 14: O += P V; 15:
+// record copies.  They
 // meet on mbarriers only (bounded waits): Q written; a K^ / V^ tile written
 // (four warps, or a TMA copy and three) and read (MMA commits); S done and P
 // written and P V done, per slot and buffer; records landed and read.
@@ -141,19 +143,20 @@ __global__ void __launch_bounds__(kCkThreads, 1)
     constexpr unsigned QLBO = kCkRows * 16, KLBO = kCkKeys * 16, VLBO = D * 16;
     unsigned char *sQ = smem, *sK = sQ + 2 * QB, *sV = sK + KS * TB, *sO = sV + KS * TB, *sR = sO + kCkOut;
     // counts 4 (a slot's or the dequantizing warps): Q [slot], P [slot][buffer],
-    // a meeting, K and V tiles written, records read; 1: the others
-    constexpr int N4 = 7 + 2 * KS + kCkMaxRaw, NB = N4 + 8 + 2 * KS + kCkMaxRaw;
+    // scores read [slot], a meeting, K and V tiles written, records read; 2
+    // (both slots' MMAs): K tiles read; 1: the others
+    constexpr int N4 = 9 + 2 * KS + kCkMaxRaw, N2 = N4 + KS, NB = N2 + 9 + KS + kCkMaxRaw;
     __shared__ __align__(8) uint64_t bars[NB];
-    uint64_t *const bQ = bars, *const bP = bars + 2, *const bX = bars + 6, *const bK = bars + 7, *const bV = bK + KS,
-                    *const eR = bV + KS, *const bS = bars + N4, *const bF = bS + 4, *const eK = bF + 4,
-                    *const eV = eK + KS, *const bR = eV + KS;
+    uint64_t *const bQ = bars, *const bP = bars + 2, *const bL = bars + 6, *const bX = bars + 8, *const bK = bars + 9,
+                    *const bV = bK + KS, *const eR = bV + KS, *const eK = bars + N4, *const bS = bars + N2,
+                    *const bF = bS + 2, *const bE = bF + 4, *const eV = bE + 3, *const bR = eV + KS;
     __shared__ uint32_t s_taddr;
     __shared__ int s_abort;   // a wait ran out: every warp stops
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int hg = a.hg;
     const bool qtma = kCkRows % hg == 0;   // Q's row tiles are boxes of its array
     if (tid < NB) {
-        mbar_init(&bars[tid], tid < N4 && !(qtma && tid < 2) ? 4 : 1);
+        mbar_init(&bars[tid], tid < N4 && !(qtma && tid < 2) ? 4 : tid >= N4 && tid < N2 ? 2 : 1);
         fence_mbar_init();
     }
     if (tid == 0) s_abort = 0;
@@ -172,73 +175,64 @@ __global__ void __launch_bounds__(kCkThreads, 1)
         return max(0, min(sg.x0 + sg.nx, sg.bl.virt((Tq + kCkKeys - 1) / kCkKeys)) - sg.x0);
     };
 
-    if (warp == 8 + kCkDq) {
-        // ---- S = Q K^T ----
+    if (warp == 8 + kCkDq || warp == 8 + kCkDq + 1) {
+        // ---- S = Q K^T of slot e ----
+        const int e = __shfl_sync(kFull, warp - (8 + kCkDq), 0);   // (warp-uniform)
+        int cnt = 0;            // S of the slot
+        CkRing t;
         constexpr uint32_t ID_S = tc_idesc_f16(kCkRows, kCkKeys, 0);
-        CkRing tk;
-        int nk = 0;             // K tiles read
-        int cs[2] = {0, 0};     // S of each slot
-        unsigned qph[2] = {0, 0};
-        const uint64_t dq = tc_desc(sQ, QLBO, 128), dk = tc_desc(sK, KLBO, 128);
+        unsigned qph = 0;
+        bool qin = false;       // a copy of Q may be in flight
+        const uint64_t dq = tc_desc(sQ + e * QB, QLBO, 128), dk = tc_desc(sK, KLBO, 128);
         while (ok && walk.next(g, a, sg)) {
-            const int nx = __reduce_max_sync(kFull, sg.nx);   // (warp-uniform)
-            const int slots = __reduce_max_sync(kFull, sg.nrows - sg.row0 > kCkRows ? 2 : 1);
-            if (qtma) {   // this segment's Q, once the last one's S is done
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    if (e >= slots) continue;
-                    ok = __all_sync(kFull, ok && (cs[e] == 0 || mbar_wait_ab(&bS[2 * e + ((cs[e] - 1) & 1)],
-                                                                              (unsigned)((cs[e] - 1) >> 1) & 1u, abort)));
-                    if (ok && lane == 0)
-                        tma_rows(sQ + e * QB, &tmQ, chunk_div(a, sg.row0 + e * kCkRows), sg.i * g.h + sg.j, &bQ[e], QB);
-                }
+            const int nx = __reduce_max_sync(kFull, sg.nx);
+            const bool mine = sg.nrows - sg.row0 > e * kCkRows;   // (a slot without rows only releases the tiles)
+            if (qtma && mine) {   // this segment's Q, once the last one's S is done
+                ok = __all_sync(kFull, cnt == 0 || mbar_wait_ab(&bS[e], (unsigned)(cnt - 1) & 1u, abort));
+                if (ok && lane == 0)
+                    tma_rows(sQ + e * QB, &tmQ, chunk_div(a, sg.row0 + e * kCkRows), sg.i * g.h + sg.j, &bQ[e], QB);
+                qin = ok;
             }
-            for (int x = 0; x < nx && ok; ++x) {
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    if (e >= slots || !ok) continue;
-                    // its Q and K written, its S buffer free (P V of the slot's
-                    // last tile but one, in this segment or before, read its
-                    // weights there)
-                    const int b = cs[e] & 1;
-                    ok = (x > 0 || mbar_wait_ab(&bQ[e], qph[e], abort)) &&
-                         (e > 0 || mbar_wait_ab(&bK[tk.s], tk.p, abort)) &&
-                         (cs[e] < 2 || mbar_wait_ab(&bF[2 * e + b], (unsigned)((cs[e] >> 1) + 1) & 1u, abort));
-                    ok = __all_sync(kFull, ok);
-                    if (!ok) continue;
-                    if (x == 0) qph[e] ^= 1u;
-                    ++cs[e];
-                    tc_fence_after();
-                    const uint64_t d = dk + (uint32_t)(tk.s * (TB >> 4));
-#pragma unroll
-                    for (int c = 0; c < D / 16; ++c)
-                        tc_mma_f16_w(taddr + 256 * e + 64 * b, dq + ((e * QB + 2 * c * QLBO) >> 4), d + ((2 * c * KLBO) >> 4),
-                                     ID_S, c > 0);
-                    tc_commit_w(&bS[2 * e + b]);
-                    if (e == slots - 1) {
-                        tc_commit_w(&eK[tk.s]);
-                        tk.next(KS);
-                        ++nk;
-                    }
+            for (int x = 0; x < nx && ok; ++x, t.next(KS)) {
+                // its Q and K written, its last scores read
+                ok = mbar_wait_ab(&bK[t.s], t.p, abort);
+                if (mine)
+                    ok = ok && (x > 0 || mbar_wait_ab(&bQ[e], qph, abort)) &&
+                         (cnt == 0 || mbar_wait_ab(&bL[e], (unsigned)(cnt - 1) & 1u, abort));
+                ok = __all_sync(kFull, ok);
+                if (!ok) break;
+                if (!mine) {
+                    if (lane == 0) mbar_arrive(&eK[t.s]);
+                    continue;
                 }
+                if (x == 0) {
+                    qph ^= 1u;
+                    qin = false;
+                }
+                ++cnt;
+                tc_fence_after();
+                const uint64_t d = dk + (uint32_t)(t.s * (TB >> 4));
+#pragma unroll
+                for (int c = 0; c < D / 16; ++c)
+                    tc_mma_f16_w(taddr + 256 * e, dq + ((2 * c * QLBO) >> 4), d + ((2 * c * KLBO) >> 4), ID_S, c > 0);
+                tc_commit_w(&bS[e]);
+                tc_commit_w(&eK[t.s]);
             }
         }
         if (!ok && lane == 0) {
             s_abort = 1;
             atomicOr(dv.status, KIVI_FLAG_WAIT);
         }
-        // every commit has landed before shared memory is given up (bounded; a
-        // phase already seen returns at once)
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-            for (int y = max(0, cs[e] - 2); y < cs[e]; ++y) mbar_wait(&bS[2 * e + (y & 1)], (unsigned)(y >> 1) & 1u);
-        for (int y = max(0, nk - KS); y < nk; ++y) mbar_wait(&eK[y % KS], (unsigned)(y / KS) & 1u);
+        // every MMA, commit and copy of this warp has landed before shared
+        // memory is given up (bounded)
+        if (qin) mbar_wait(&bQ[e], qph);
+        tc_commit_w(&bE[e]);
+        mbar_wait(&bE[e], 0u);
         __syncwarp();
-    } else if (warp == 8 + kCkDq + 1) {
+    } else if (warp == 8 + kCkDq + 2) {
         // ---- O += P V ----
         constexpr uint32_t ID_R = tc_idesc_f16(kCkRows, D, 1), ID_T = tc_idesc_f16(kCkRows, D, 0);
         CkRing tv;
-        int nv = 0;             // V tiles read
         int cp[2] = {0, 0};     // P V of each slot
         const uint64_t dt = tc_desc(sV, VLBO, 128), dr = tc_desc(sV, 128, KLBO);   // transposed, as rows
         while (ok && walk.next(g, a, sg)) {
@@ -262,13 +256,12 @@ __global__ void __launch_bounds__(kCkThreads, 1)
                     tc_fence_after();
 #pragma unroll
                     for (int c = 0; c < kCkKeys / 16; ++c)
-                        tc_mma_f16_ta_w(taddr + 256 * e + 128, taddr + 256 * e + 64 * b + 8 * c, d + c * step, id,
+                        tc_mma_f16_ta_w(taddr + 256 * e + 128, taddr + 256 * e + 64 + 32 * b + 8 * c, d + c * step, id,
                                         x > 0 || c > 0);
                     tc_commit_w(&bF[2 * e + b]);
                     if (e == slots - 1) {
                         tc_commit_w(&eV[tv.s]);
                         tv.next(KS);
-                        ++nv;
                     }
                 }
             }
@@ -277,12 +270,10 @@ __global__ void __launch_bounds__(kCkThreads, 1)
             s_abort = 1;
             atomicOr(dv.status, KIVI_FLAG_WAIT);
         }
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-            for (int y = max(0, cp[e] - 2); y < cp[e]; ++y) mbar_wait(&bF[2 * e + (y & 1)], (unsigned)(y >> 1) & 1u);
-        for (int y = max(0, nv - KS); y < nv; ++y) mbar_wait(&eV[y % KS], (unsigned)(y / KS) & 1u);
+        tc_commit_w(&bE[2]);
+        mbar_wait(&bE[2], 0u);
         __syncwarp();
-    } else if (warp == 8 + kCkDq + 2) {
+    } else if (warp == 8 + kCkDq + 3) {
         // ---- records (lane 0 issues) ----
         CkRing r;
         int issued = 0;
@@ -477,13 +468,16 @@ __global__ void __launch_bounds__(kCkThreads, 1)
             float mref = -INFINITY, lsum = 0.f;    // the row's reference maximum (raw score units) and weight sum
             for (int x = 0; x < sg.nx; ++x, ++cnt) {
                 const int b = cnt & 1, key0 = sg.key0(x);
-                ok = __all_sync(kFull, mbar_wait_ab(&bS[2 * slot + b], (unsigned)(cnt >> 1) & 1u, abort));
+                ok = __all_sync(kFull, mbar_wait_ab(&bS[slot], (unsigned)cnt & 1u, abort));
                 if (!ok) break;
                 tc_fence_after();
                 uint32_t r[2][32];   // this row's 64 scores
-                tc_ld32(tS + 64 * b, r[0]);
-                tc_ld32(tS + 64 * b + 32, r[1]);
+                tc_ld32(tS, r[0]);
+                tc_ld32(tS + 32, r[1]);
                 tc_wait_ld();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bL[slot]);
                 if (key0 + kCkKeys - 1 > ps0 || (W > 0 && key0 <= ps1 - W && key0 + kCkKeys > sinks)) {
                     // some row of the slot does not see the whole tile
                     const uint32_t h0 = ck_hidden32(key0, pos, W, sinks), h1 = ck_hidden32(key0 + 32, pos, W, sinks);
@@ -535,14 +529,17 @@ __global__ void __launch_bounds__(kCkThreads, 1)
                         tc_st32(tO + c0, o);
                     }
                 }
-                tc_st32(tS + 64 * b, pw);   // P over the first 32 columns of its S buffer
+                // this P buffer's last P V has read its weights
+                ok = cnt < 2 || __all_sync(kFull, mbar_wait_ab(&bF[2 * slot + b], (unsigned)((cnt >> 1) + 1) & 1u, abort));
+                if (!ok) break;
+                tc_fence_after();
+                tc_st32(tS + 64 + 32 * b, pw);
                 tc_wait_st();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bP[2 * slot + b]);
             }
-            // the last P V (the one before it ended before its S, which was waited
-            // for, was issued, or is waited for first)
+            // the last two P V
             for (int y = max(cnt - 2, cnt - sg.nx); y < cnt && ok; ++y)
                 ok = __all_sync(kFull, mbar_wait_ab(&bF[2 * slot + (y & 1)], (unsigned)(y >> 1) & 1u, abort));
             if (!ok) break;
