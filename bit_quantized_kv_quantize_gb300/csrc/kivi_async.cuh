@@ -39,6 +39,19 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t *bar, unsigned phase) {
     return ok != 0;
 }
 
+// whether the barrier has completed the phase (a poll: no wait)
+__device__ __forceinline__ bool mbar_test(uint64_t *bar, unsigned phase) {
+    unsigned ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(phase)
+        : "memory");
+    return ok != 0;
+}
+
 // bounded wait: false if the barrier did not complete within the limit
 __device__ __forceinline__ bool mbar_wait(uint64_t *bar, unsigned phase) {
 #pragma unroll 1

@@ -90,16 +90,24 @@ __device__ __forceinline__ bool packed_tiles(int n, int &tiles, CkRing &t, CkRin
                                              uint64_t *bR, uint64_t *eR, const volatile int *abort) {
     constexpr int TB = kCkKeys * D * 2;
     const int lane = threadIdx.x & 31, lgG = __ffs(g.G) - 1;
+    bool rk = false, rr = false;   // polled ahead: the K stage is free, the record is in
     for (int x = 0; x < n; ++x, ++tiles) {
-        bool ok = (tiles < kCkStages || mbar_wait_ab(&eK[t.s], t.p ^ 1u, abort)) && mbar_wait_ab(&bR[r.s], r.p, abort);
+        bool ok = (rk || tiles < kCkStages || mbar_wait_ab(&eK[t.s], t.p ^ 1u, abort)) &&
+                  (rr || mbar_wait_ab(&bR[r.s], r.p, abort));
         if (!__all_sync(kFull, ok)) return false;
+        const bool rv = tiles < kCkStages || mbar_test(&eV[t.s], t.p ^ 1u);   // (seen after the keys)
         const unsigned char *rec = sR + (size_t)r.s * g.rec_bytes;
         dequant_keys<D, KB, kCkKeys>(sK + t.s * TB, rec, g.off_ksz, lgG, w);
         fence_proxy_async();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bK[t.s]);
-        ok = tiles < kCkStages || mbar_wait_ab(&eV[t.s], t.p ^ 1u, abort);
+        ok = rv || mbar_wait_ab(&eV[t.s], t.p ^ 1u, abort);
         if (!__all_sync(kFull, ok)) return false;
+        CkRing t1 = t, r1 = r;
+        t1.next(kCkStages);
+        r1.next(rs);
+        rk = x + 1 < n && tiles + 1 >= kCkStages && mbar_test(&eK[t1.s], t1.p ^ 1u);
+        rr = x + 1 < n && mbar_test(&bR[r1.s], r1.p);
         dequant_values<D, VB>(sV + t.s * TB, rec, g.off_vc, g.off_vsz, lgG, w);
         fence_proxy_async();
         __syncwarp();
@@ -107,8 +115,8 @@ __device__ __forceinline__ bool packed_tiles(int n, int &tiles, CkRing &t, CkRin
             mbar_arrive(&bV[t.s]);
             mbar_arrive(&eR[r.s]);
         }
-        t.next(kCkStages);
-        r.next(rs);
+        t = t1;
+        r = r1;
     }
     return true;
 }
