@@ -98,9 +98,6 @@ __device__ __forceinline__ bool packed_tiles(int n, int &tiles, CkRing &t, CkRin
         const bool rv = tiles < kCkStages || mbar_test(&eV[t.s], t.p ^ 1u);   // (seen after the keys)
         const unsigned char *rec = sR + (size_t)r.s * g.rec_bytes;
         dequant_keys<D, KB, kCkKeys>(sK + t.s * TB, rec, g.off_ksz, lgG, w);
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bK[t.s]);
         ok = rv || mbar_wait_ab(&eV[t.s], t.p ^ 1u, abort);
         if (!__all_sync(kFull, ok)) return false;
         CkRing t1 = t, r1 = r;
@@ -109,9 +106,12 @@ __device__ __forceinline__ bool packed_tiles(int n, int &tiles, CkRing &t, CkRin
         rk = x + 1 < n && tiles + 1 >= kCkStages && mbar_test(&eK[t1.s], t1.p ^ 1u);
         rr = x + 1 < n && mbar_test(&bR[r1.s], r1.p);
         dequant_values<D, VB>(sV + t.s * TB, rec, g.off_vc, g.off_vsz, lgG, w);
+        // (one fence for both: telling of K^ before V^ is written takes longer,
+        // 514 against 502 us for 2048 tokens over 16.5k)
         fence_proxy_async();
         __syncwarp();
         if (lane == 0) {
+            mbar_arrive(&bK[t.s]);
             mbar_arrive(&bV[t.s]);
             mbar_arrive(&eR[r.s]);
         }
