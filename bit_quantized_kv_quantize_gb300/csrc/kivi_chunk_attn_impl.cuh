@@ -486,6 +486,8 @@ __global__ void __launch_bounds__(kCkThreads, 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bL[slot]);
+                // this P buffer's last P V has read its weights (polled ahead: most often true)
+                const bool pf = cnt < 2 || mbar_test(&bF[2 * slot + b], (unsigned)((cnt >> 1) + 1) & 1u);
                 if (key0 + kCkKeys - 1 > ps0 || (W > 0 && key0 <= ps1 - W && key0 + kCkKeys > sinks)) {
                     // some row of the slot does not see the whole tile
                     const uint32_t h0 = ck_hidden32(key0, pos, W, sinks), h1 = ck_hidden32(key0 + 32, pos, W, sinks);
@@ -537,8 +539,7 @@ __global__ void __launch_bounds__(kCkThreads, 1)
                         tc_st32(tO + c0, o);
                     }
                 }
-                // this P buffer's last P V has read its weights
-                ok = cnt < 2 || __all_sync(kFull, mbar_wait_ab(&bF[2 * slot + b], (unsigned)((cnt >> 1) + 1) & 1u, abort));
+                ok = __all_sync(kFull, pf || mbar_wait_ab(&bF[2 * slot + b], (unsigned)((cnt >> 1) + 1) & 1u, abort));
                 if (!ok) break;
                 tc_fence_after();
                 tc_st32(tS + 64 + 32 * b, pw);
