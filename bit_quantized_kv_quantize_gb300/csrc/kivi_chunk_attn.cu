@@ -57,9 +57,10 @@ cudaError_t kivi_launch_chunk_attn(const KiviGeom &g, const KiviDev &dv, const _
     // the first positions)
     if (a.vis.window >= end) a.vis = Visible{0, 0};
     // Up to 32 rows a kv head: the transposed kernel, whose work follows the
-    // rows.  Over 32k tokens of 8 sequences of 8 heads, in microseconds, it and
-    // 256-row tiles: 16 rows 149 and 235, 32 rows 190 and 235, 64 rows 270
-    // and 238.  (Over 1000 tokens, 32 rows: 38 and 33.)
+    // rows.  It and 256-row tiles, in microseconds, over 32k tokens of 8
+    // sequences of 8 heads: 16 rows 151 and 208, 32 rows 192 and 209, 64 rows
+    // 270 and 211; of one sequence: 16 rows 48 and 58, 32 rows 56 and 58; over
+    // 1000 tokens of 8 it loses: 16 rows 34 and 32, 32 rows 38 and 32.
     const bool few = maxrows <= 32;
     a.tile_rows = !few ? kCkTileRows : maxrows <= 16 ? 16 : 32;
     a.tile_blocks = few ? 2 : 1;

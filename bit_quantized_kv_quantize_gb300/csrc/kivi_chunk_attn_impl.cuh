@@ -21,6 +21,16 @@
 // up to 1.2e-3 where keys have channels 8 times the others; an fp16 output
 // alone rounds by 2e-4).
 //
+// Bound: the tensor cores, where the rows are many.  A tile's MMAs take 1280
+// cycles (M 128 x N 64 x K 16 from shared memory 49, N 128 from tensor memory
+// 65); the loop takes 2000 without the restoring and 2250 with it: the
+// dequantizing warps' stores and the MMAs' operand reads share shared memory.
+// Measured: 2048 tokens of 32 / 8 heads over 16.5k 2-bit tokens 499 us (1.18
+// PFLOP/s; 303 us at the cuBLAS rate), 200 tokens 89 us, 16 tokens of 8
+// sequences over 32k 211 us; a prompt of 8191 tokens, window 2048, 32 / 8
+// heads, 279 us beside 32 us of packing, one of 4096, window 1024, 32 heads,
+// 116 beside 45.
+//
 // Pipeline.  A slot has one S buffer of 64 columns, two P buffers of 32 and O.
 // The scores are read into registers at once, so S of the next tile runs
 // under the softmax of this one, and P V of the last tile too.  (With P
@@ -55,7 +65,10 @@ constexpr int kCkTileRows = 2 * kCkRows;
 constexpr int kCkKeys = KIVI_KBLK;   // tokens of a tile
 constexpr int kCkStages = 3;     // K^ tiles, and V^ tiles, in flight
 constexpr int kCkMaxRaw = 8;     // records in flight
-constexpr int kCkDq = kCkDqGroup;   // dequantizing warps
+// Dequantizing warps: all that 16 warps of 128 registers leave.  (Eight, at 96
+// to 112 registers for the softmax, took 616 to 660 us where four took 545;
+// two for K^ and two for V^, a tile a warp, 600.)
+constexpr int kCkDq = kCkDqGroup;
 constexpr int kCkOut = 8 * 32 * 64;   // a softmax warp's 32 rows x 32 columns of the output
 constexpr int kCkThreads = 32 * (8 + kCkDq + 4);
 

@@ -3,14 +3,18 @@
 // of the chunk attention (kivi_chunk_attn_impl.cuh has the mathematics).
 //
 // With 128 query rows on the MMA's M side, a few rows leave most of the tensor
-// cores' and the softmax's work padding, and a tile takes about 1800 cycles
-// however few the rows.  Here the tokens are on the M side and the rows on N
+// cores' and the softmax's work padding, and four warps that restore each
+// tile between them set its time however few the rows (211 us where this
+// kernel takes 149).  Here the tokens are on the M side and the rows on N
 // (N = 16 or 32):
 //   S^T [128 tokens x N] = K^ Q^T,   O^T [d x N] += V^^T P^T,
 // so a tile of 128 tokens costs 16 MMAs of N columns, thread t of the softmax
 // owns token t and computes N weights, and what remains is restoring the
 // tile: the kernel is bound by the dequantizing warps' instructions (4.5 a
-// pair of values) and by HBM.
+// pair of values; the SMs issue in 47 % of their cycles, HBM is at 20 %).
+// Measured over 32k 2-bit tokens of 8 sequences of 8 heads (204 MB, 30 us at
+// the copy rate), joining included: 16 rows a kv head 149 us, 32 rows 190 us;
+// 16 rows over 1000 tokens 27 us, over 100 tokens 15 us.
 //
 // The softmax needs a row's maximum over the tile's tokens, which are spread
 // over the threads.  It is not formed a tile: the weights are taken against
