@@ -8,11 +8,13 @@
 // one pass, from the window rows (tokens below T) and the chunk's, bitwise
 // as the one-token appends would.
 //
-// Two launches: the windows' old rows are still read by the first (one CTA a
-// block of max(64, G) tokens: whole key groups and whole 64-token records,
-// so no word has two writers), the second overwrites them and writes the
-// counters.  Bound: memory (a chunk token of a kv head reads 4 d bytes and
-// writes its packed 0.5-1.3 d), with the quantizer's divisions close behind.
+// Two launches: the windows' old rows are still read by the first (one CTA the
+// keys, and one the values, of a block of max(64, G) tokens: whole key groups
+// and whole 64-token records, so no word has two writers), the second
+// overwrites them and writes the counters.  Bound: the quantizer's instructions
+// in a CTA's few passes (bytes: a chunk token of a kv head reads 4 d and writes
+// its packed 0.5-1.3 d).  2048 tokens of 8 heads 23 us, 512 tokens of 8
+// sequences 32 us (a CTA for both: 33 and 51 us).
 #include "kivi_append_impl.cuh"
 #include "kivi_chunk.cuh"
 
@@ -29,30 +31,31 @@ __global__ void __launch_bounds__(kApThreads)
     const int i = blockIdx.z, j = blockIdx.y, d = g.d, R = g.R, CA = span_of(g);
     const int T = a.T[i], Tqk = a.Tqk[i], Tqv = a.Tqv[i], n = a.n[i];
     const int Tqk1 = chunk_tqk(T, Tqk, n, R), Tqv1 = chunk_tqv(T, Tqv, n, R);
-    const int cs = (min(Tqk, Tqv) / CA + blockIdx.x) * CA;   // the CTA's tokens [cs, cs + CA)
+    // the CTA's tokens [cs, cs + CA), their keys or values
+    const int cs = (min(Tqk, Tqv) / CA + (blockIdx.x >> 1)) * CA;
+    const bool keys = !(blockIdx.x & 1);
     const int ka = max(cs, Tqk), kz = min(cs + CA, Tqk1), va = max(cs, Tqv), vz = min(cs + CA, Tqv1);
     __half *xs = reinterpret_cast<__half *>(smem);   // [CA][d]
     float *s_f = reinterpret_cast<float *>(smem + (size_t)CA * d * 2);
-    const int nv = d / 8;
+    const int nv = d / 8, lgv = __ffs(nv) - 1, lgG = __ffs(g.G) - 1;
     // rows of tokens [x, y): below T from the window, the others from the chunk
     auto stage = [&](const __half *win, int ring, const __half *chk, int x, int y) {
         chk += ((size_t)i * g.h + j) * a.n_stride * d;
         for (int e = threadIdx.x; e < (y - x) * nv; e += kApThreads) {
-            const int tau = x + e / nv, c8 = e % nv;
+            const int tau = x + (e >> lgv), c8 = e & (nv - 1);
             const __half *src = tau < T ? win + (size_t)(tau % ring) * d : chk + (size_t)(tau - T) * d;
             reinterpret_cast<uint4 *>(xs + (size_t)(tau - cs) * d)[c8] = reinterpret_cast<const uint4 *>(src)[c8];
         }
         __syncthreads();
     };
-    if (ka < kz) {
+    if (keys && ka < kz) {
         stage(dv.Kf + kf_slice(g, i, j), R, Kn, ka, kz);
         pack_key_round(g, dv, i, j, xs, s_f, cs, CA, ka, kz, Tqk);
-        __syncthreads();   // the rows are reused
     }
-    if (va < vz) {
+    if (!keys && va < vz) {
         stage(dv.Vf + vf_slice(g, i, j), R + 1, Vn, va, vz);
-        const int ngi = d / g.G, lgG = __ffs(g.G) - 1;
-        float *s_s = s_f, *s_z = s_f + CA * ngi;   // [token][group]
+        const int ngi = d >> lgG, lgn = __ffs(ngi) - 1;
+        float *s_s = s_f, *s_z = s_s + CA * ngi, *s_r = s_z + CA * ngi;   // [token][group]
         // value blocks opened here: cleared, so untouched fields read zero
         for (int vb = (va + KIVI_VBLK - 1) / KIVI_VBLK; vb * KIVI_VBLK < vz; ++vb) {
             uint32_t *vc = vc_words(g, dv.blk, i, j, vb);
@@ -61,36 +64,43 @@ __global__ void __launch_bounds__(kApThreads)
             for (int e = threadIdx.x; e < g.vsz_blk; e += kApThreads) vsz[e] = __float2half_rn(0.f);
         }
         __syncthreads();
-        for (int e = threadIdx.x; e < (vz - va) * ngi; e += kApThreads) {
-            const int tau = va + e / ngi, gi = e % ngi;
-            const __half *x = xs + (size_t)(tau - cs) * d + gi * g.G;
-            float mn = __half2float(x[0]), mx = mn;
-            for (int k = 1; k < g.G; ++k) {
-                const float v = __half2float(x[k]);
-                mn = fminf(mn, v);
-                mx = fmaxf(mx, v);
+        for (int e = threadIdx.x; e < (vz - va) << lgn; e += kApThreads) {
+            const int tau = va + (e >> lgn), gi = e & (ngi - 1), nc = g.G / 8;
+            const uint4 *x = reinterpret_cast<const uint4 *>(xs + (size_t)(tau - cs) * d + gi * g.G);
+            float mn = INFINITY, mx = -INFINITY;
+            for (int k = 0; k < nc; ++k) {   // 8 channels, from another one each thread (bank conflicts)
+                const uint4 v = x[(k + 2 * tau + (gi >> 1)) & (nc - 1)];
+                const uint32_t h[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&h[m]));
+                    mn = fminf(mn, fminf(y.x, y.y));
+                    mx = fmaxf(mx, fmaxf(y.x, y.y));
+                }
             }
             const QParams p = qparams(mn, mx, g.vbits);
             __half *vsz = vsz_halves(g, dv.blk, i, j, tau / KIVI_VBLK);
             vsz[vsz_in_block(g, tau, gi, 0)] = p.s16;
             vsz[vsz_in_block(g, tau, gi, 1)] = p.z16;
-            s_s[(tau - cs) * ngi + gi] = p.sf;
-            s_z[(tau - cs) * ngi + gi] = p.zf;
+            const int q = ((tau - cs) << lgn) + gi;
+            s_s[q] = p.sf;
+            s_z[q] = p.zf;
+            s_r[q] = p.sf == 0.0f ? 0.0f : __frcp_rn(p.sf);
         }
         __syncthreads();
         // a token's 16-bit halves: lane class gg (8) x channel words w (d vbits / 128)
-        const int nwv = d * g.vbits / 128, cph = 16 / g.vbits, vcs = v_cs(g);
-        for (int e = threadIdx.x; e < (vz - va) * 8 * nwv; e += kApThreads) {
-            const int tau = va + e / (8 * nwv), gg = e / nwv % 8, w = e % nwv, tt = tau % KIVI_VBLK;
+        const int nwv = d * g.vbits / 128, lgw = __ffs(nwv) - 1, cph = 16 / g.vbits, vcs = v_cs(g), lgc = __ffs(vcs) - 1;
+        for (int e = threadIdx.x; e < (vz - va) << (3 + lgw); e += kApThreads) {
+            const int tau = va + (e >> (3 + lgw)), gg = e & 7, w = (e >> 3) & (nwv - 1), tt = tau % KIVI_VBLK;
             const __half *x = xs + (size_t)(tau - cs) * d;
             uint32_t bits = 0;
             for (int r = 0; r < cph; ++r) {
-                const int c = 8 * (w * cph + r) + gg, gi = (tau - cs) * ngi + (c >> lgG);
-                bits |= qcode(__half2float(x[c]), s_s[gi], s_z[gi], g.vbits) << (r * g.vbits);
+                const int c = 8 * (w * cph + r) + gg, gi = ((tau - cs) << lgn) + (c >> lgG);
+                bits |= qcode_rcp(__half2float(x[c]), s_s[gi], s_z[gi], s_r[gi], g.vbits) << (r * g.vbits);
             }
             const int L = 4 * gg + ((tt & 7) >> 1), u = (tt >> 3) * nwv + w;
             uint32_t *vc = vc_words(g, dv.blk, i, j, tau / KIVI_VBLK);
-            reinterpret_cast<uint16_t *>(vc + (size_t)(u / vcs) * 32 * vcs + (size_t)L * vcs + u % vcs)[tt & 1] =
+            reinterpret_cast<uint16_t *>(vc + (size_t)(u >> lgc) * 32 * vcs + (size_t)L * vcs + (u & (vcs - 1)))[tt & 1] =
                 (uint16_t)bits;
         }
     }
@@ -135,12 +145,12 @@ cudaError_t kivi_launch_append_chunk(const KiviGeom &g, const KiviDev &dv, const
         }
         maxn = a.n[i] > maxn ? a.n[i] : maxn;
     }
-    const size_t par = 3 * (size_t)(CA / g.G) * g.d, val = 2 * (size_t)CA * (g.d / g.G);   // key, value parameters
+    const size_t par = 3 * (size_t)(CA / g.G) * g.d, val = 3 * (size_t)CA * (g.d / g.G);   // key, value parameters
     const size_t smem = (size_t)CA * g.d * 2 + (par > val ? par : val) * 4;
     if (blocks > 0) {
         cudaError_t e = cudaFuncSetAttribute(chunk_pack_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
-        chunk_pack_kernel<<<dim3(blocks, g.h, g.b), kApThreads, smem, st>>>(g, dv, K, V, a);
+        chunk_pack_kernel<<<dim3(2 * blocks, g.h, g.b), kApThreads, smem, st>>>(g, dv, K, V, a);
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
