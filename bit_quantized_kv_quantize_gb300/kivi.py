@@ -307,7 +307,8 @@ class KiviCache:
         """prefill(K, V, t) and the prompt's causal attention: Q CUDA fp16
         [b, h_q, t_stride, d] -> out (same shape; rows past each sequence's
         length untouched).  One launch.  With window > 0 a query sees only the
-        last `window` tokens up to its own and the sequence's first `sinks`."""
+        last `window` tokens up to its own and the sequence's first `sinks`
+        (several launches; calls on one cache must not overlap)."""
         import torch
         t = np.ascontiguousarray(np.broadcast_to(np.asarray(t, np.int32), (self.b,)))
         ts, hq = K.shape[2], Q.shape[1]

@@ -145,7 +145,9 @@ kivi_status kivi_chunk_attn(kivi_cache_t c, const void *q, const void *K, const 
  * n_stride as for kivi_chunk_attn, any d.  The cache afterwards is bitwise
  * the one that n[i] calls of kivi_append for sequence i alone would leave.
  * KIVI_ERR_CAPACITY (and nothing changes) if a sequence would exceed
- * max_tokens.  Two launches at most, on `stream`. */
+ * max_tokens.  K and V lie outside the cache.  Two launches at most, on
+ * `stream`.  A captured call writes, when replayed, the tokens and counts of
+ * the state that it was captured in: replay it only there. */
 kivi_status kivi_append_chunk(kivi_cache_t c, const void *K, const void *V, const int32_t *n, int n_stride,
                               kivi_stream_t stream);
 
