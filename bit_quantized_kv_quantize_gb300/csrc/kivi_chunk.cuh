@@ -25,6 +25,7 @@ struct ChunkArgs {
     int T[KIVI_MAX_BATCH], Tqk[KIVI_MAX_BATCH], Tqv[KIVI_MAX_BATCH], n[KIVI_MAX_BATCH];
 };
 
+constexpr int kFewRows = 16;  // rows of the row tiles for few rows
 constexpr int kCkLead = 4;   // units that stand for a row tile's fixed cost
 
 // x / hg

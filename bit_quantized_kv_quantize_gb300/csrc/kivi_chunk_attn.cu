@@ -47,7 +47,7 @@ cudaError_t kivi_launch_chunk_attn(const KiviGeom &g, const KiviDev &dv, const _
     const int hg = a.hq / g.h;
     a.hg = hg;
     a.hg_mul = (unsigned)(((1ull << 32) + hg - 1) / hg);
-    int maxrows = 0, end = 0;
+    int maxrows = 0, end = 0, seen = 0;   // seen: the most blocks that a sequence sees
     for (int i = 0; i < g.b; ++i) {
         maxrows = a.n[i] * hg > maxrows ? a.n[i] * hg : maxrows;
         end = a.T[i] + a.n[i] > end ? a.T[i] + a.n[i] : end;
@@ -56,13 +56,18 @@ cudaError_t kivi_launch_chunk_attn(const KiviGeom &g, const KiviDev &dv, const _
     // a window that no position reaches is none (and would pass 32 bits below
     // the first positions)
     if (a.vis.window >= end) a.vis = Visible{0, 0};
-    // Up to 32 rows a kv head: the transposed kernel, whose work follows the
-    // rows.  It and 256-row tiles, in microseconds, over 32k tokens of 8
-    // sequences of 8 heads: 16 rows 151 and 208, 32 rows 192 and 209, 64 rows
-    // 270 and 211; of one sequence: 16 rows 48 and 58, 32 rows 56 and 58; over
-    // 1000 tokens of 8 it loses: 16 rows 34 and 32, 32 rows 38 and 32.
-    const bool few = maxrows <= 32;
-    a.tile_rows = !few ? kCkTileRows : maxrows <= 16 ? 16 : 32;
+    for (int i = 0; i < g.b; ++i)
+        if (a.n[i] > 0) {
+            const int x = visible_blocks(a.vis, a.T[i]).virt((a.T[i] + a.n[i] - 1) / KIVI_KBLK + 1);
+            seen = x > seen ? x : seen;
+        }
+    // Up to 16 rows a kv head over 32 blocks or more: the transposed kernel,
+    // whose work follows the rows.  It and 256-row tiles, 16 rows over a cache
+    // of 8 sequences of 8 heads, in microseconds: 32k tokens 151 and 208, 8000
+    // 53 and 62, 2000 30 and 33, 1000 27 and 26, 100 15 and 10.  (32 rows, in a
+    // variant for them: 32k 192 and 209, 4000 49 and 42.)
+    const bool few = maxrows <= kFewRows && seen >= 32;
+    a.tile_rows = few ? kFewRows : kCkTileRows;
     a.tile_blocks = few ? 2 : 1;
     long long items = 0, U = 0;
     for (int i = 0; i < g.b; ++i) {
@@ -73,9 +78,11 @@ cudaError_t kivi_launch_chunk_attn(const KiviGeom &g, const KiviDev &dv, const _
         items += (long long)mt * g.h;
     }
     // One CTA an SM, but no share below 2 kCkLead units unless the row tiles
-    // are that short: cutting them finer costs more than it shortens.
+    // are that short: cutting them finer costs more than it shortens (the
+    // join's launch too: row tiles of up to 3 kCkLead units are not cut while
+    // the SMs suffice for them).
     const long long sms = num_sms < kCkMaxCtas ? num_sms : kCkMaxCtas;
-    const long long want = U / (2 * kCkLead) > items ? U / (2 * kCkLead) : items;
+    const long long want = U > 3 * kCkLead * items && U / (2 * kCkLead) > items ? U / (2 * kCkLead) : items;
     const int ctas = (int)(want < sms ? want : sms);
     // each CTA's first unit, and whether one lies behind the first key tile of
     // a row tile (whose partials are then joined)

@@ -4,17 +4,17 @@
 
 namespace {
 
-template <int D, int N>
+template <int D>
 cudaError_t launch_few(const KiviGeom &g, const KiviDev &dv, const __half *Q, const __half *K, const __half *V,
                        __half *O, ChunkArgs &a, int ctas, cudaStream_t st) {
-    const size_t fixed = (size_t)kFwStages * (fw_kb(D) + fw_vb(D)) + (size_t)N * D * 2 + (size_t)kFwBufs * kFwKeys * N * 2;
+    const size_t fixed = (size_t)kFwStages * (fw_kb(D) + fw_vb(D)) + (size_t)kFwRows * D * 2 + (size_t)kFwBufs * kFwKeys * kFwRows * 2;
     a.rs = (int)((224 * 1024 - fixed) / g.rec_bytes);
     if (a.rs > kFwMaxRaw) a.rs = kFwMaxRaw;
     if (a.rs < 4) return cudaErrorInvalidValue;
     const size_t smem = fixed + (size_t)a.rs * g.rec_bytes;
-    cudaError_t e = cudaFuncSetAttribute(chunk_few_kernel<D, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = cudaFuncSetAttribute(chunk_few_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    chunk_few_kernel<D, N><<<ctas, kFwThreads, smem, st>>>(g, dv, Q, K, V, O, a);
+    chunk_few_kernel<D><<<ctas, kFwThreads, smem, st>>>(g, dv, Q, K, V, O, a);
     return cudaGetLastError();
 }
 
@@ -22,9 +22,5 @@ cudaError_t launch_few(const KiviGeom &g, const KiviDev &dv, const __half *Q, co
 
 cudaError_t kivi_launch_chunk_few(const KiviGeom &g, const KiviDev &dv, const __half *Q, const __half *K,
                                   const __half *V, __half *O, ChunkArgs &a, int ctas, cudaStream_t st) {
-    if (g.d == 64)
-        return a.tile_rows == 16 ? launch_few<64, 16>(g, dv, Q, K, V, O, a, ctas, st)
-                                 : launch_few<64, 32>(g, dv, Q, K, V, O, a, ctas, st);
-    return a.tile_rows == 16 ? launch_few<128, 16>(g, dv, Q, K, V, O, a, ctas, st)
-                             : launch_few<128, 32>(g, dv, Q, K, V, O, a, ctas, st);
+    return g.d == 64 ? launch_few<64>(g, dv, Q, K, V, O, a, ctas, st) : launch_few<128>(g, dv, Q, K, V, O, a, ctas, st);
 }

@@ -5,16 +5,17 @@
 // With 128 query rows on the MMA's M side, a few rows leave most of the tensor
 // cores' and the softmax's work padding, and four warps that restore each
 // tile between them set its time however few the rows (211 us where this
-// kernel takes 149).  Here the tokens are on the M side and the rows on N
-// (N = 16 or 32):
+// kernel takes 149).  Here the tokens are on the M side and up to 16 rows
+// on N:
 //   S^T [128 tokens x N] = K^ Q^T,   O^T [d x N] += V^^T P^T,
 // so a tile of 128 tokens costs 16 MMAs of N columns, thread t of the softmax
 // owns token t and computes N weights, and what remains is restoring the
 // tile: the kernel is bound by the dequantizing warps' instructions (4.5 a
 // pair of values; the SMs issue in 47 % of their cycles, HBM is at 20 %).
 // Measured over 32k 2-bit tokens of 8 sequences of 8 heads (204 MB, 30 us at
-// the copy rate), joining included: 16 rows a kv head 149 us, 32 rows 190 us;
-// 16 rows over 1000 tokens 27 us, over 100 tokens 15 us.
+// the copy rate), joining included: 149 us; over 2000 tokens 30 us.  (N = 32,
+// for 32 rows: 190 us over 32k, 226 where 256-row tiles take 206 over 8k tokens
+// of 32 sequences.)
 //
 // The softmax needs a row's maximum over the tile's tokens, which are spread
 // over the threads.  It is not formed a tile: the weights are taken against
@@ -41,6 +42,7 @@
 
 namespace {
 
+constexpr int kFwRows = kFewRows;
 constexpr int kFwKeys = 128;    // tokens of a tile (two blocks)
 constexpr int kFwStages = 2;    // K^ tiles, and V^ tiles, in flight
 constexpr int kFwMaxRaw = 12;   // records in flight
@@ -312,25 +314,21 @@ __device__ __noinline__ void cold_values(const KiviGeom &g, const KiviDev &dv, c
 // A raise: the rows' maxima over the tile (tS: this warp's scores; hid: does
 // a row miss part of the block), the references of the rows that grew by
 // more than 2^8, and their factors.  Called by every softmax warp.
-template <int N>
 __device__ __noinline__ void raise_refs(uint32_t tS, float sl2, bool cut, int key, int p0, int e0, int hg, int W, int sinks,
-                                        float *s_ref, float *s_al, float (*s_red)[N]) {
+                                        float *s_ref, float *s_al, float (*s_red)[kFwRows]) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-#pragma unroll 1
-    for (int c0 = 0; c0 < N; c0 += 16) {
-        uint32_t r[16];
-        tc_ld16(tS + c0, r);
-        tc_wait_ld();
-        const uint32_t h = cut ? ck_hidden16(key, c0, p0, e0, hg, W, sinks) : 0u;
+    uint32_t r[16];
+    tc_ld16(tS, r);
+    tc_wait_ld();
+    const uint32_t h = cut ? ck_hidden16(key, 0, p0, e0, hg, W, sinks) : 0u;
 #pragma unroll
-        for (int c = 0; c < 16; ++c) {
-            const float m = redux_max((h >> c) & 1u ? -INFINITY : __uint_as_float(r[c]) * sl2);
-            if (lane == 0) s_red[warp][c0 + c] = m;
-        }
+    for (int c = 0; c < kFwRows; ++c) {
+        const float m = redux_max((h >> c) & 1u ? -INFINITY : __uint_as_float(r[c]) * sl2);
+        if (lane == 0) s_red[warp][c] = m;
     }
     fw_sync();
     const int t = threadIdx.x;
-    if (t < N) {
+    if (t < kFwRows) {
         const float m = fmaxf(fmaxf(s_red[0][t], s_red[1][t]), fmaxf(s_red[2][t], s_red[3][t]));
         const float old = s_ref[t];
         const bool grow = m != -INFINITY && m + old > 8.f;
@@ -340,17 +338,13 @@ __device__ __noinline__ void raise_refs(uint32_t tS, float sl2, bool cut, int ke
     fw_sync();
 }
 // O^T times the rows' factors (tO: this warp's lanes)
-template <int N>
 __device__ __noinline__ void rescale_out(uint32_t tO, const float *s_al) {
-#pragma unroll 1
-    for (int c0 = 0; c0 < N; c0 += 16) {
-        uint32_t o[16];
-        tc_ld16(tO + c0, o);
-        tc_wait_ld();
+    uint32_t o[16];
+    tc_ld16(tO, o);
+    tc_wait_ld();
 #pragma unroll
-        for (int c = 0; c < 16; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * s_al[c0 + c]);
-        tc_st16(tO + c0, o);
-    }
+    for (int c = 0; c < kFwRows; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * s_al[c]);
+    tc_st16(tO, o);
     tc_wait_st();
 }
 
@@ -359,15 +353,15 @@ __device__ __noinline__ void rescale_out(uint32_t tO, const float *s_al) {
 // S^T, O^T and the record copies.  Tensor memory: S^T buffers of N
 // columns from 0, then O^T.  Shared memory: K^ and V^ stages, Q [N][D], P^T
 // tiles [128][N], references and sums, records.
-template <int D, int N>
+template <int D>
 __global__ void __launch_bounds__(kFwThreads, 1)
     chunk_few_kernel(KiviGeom g, KiviDev dv, const __half *__restrict__ Q, const __half *__restrict__ Kn,
                      const __half *__restrict__ Vn, __half *__restrict__ O, const __grid_constant__ ChunkArgs a) {
     extern __shared__ __align__(128) unsigned char smem[];
-    constexpr int KB = fw_kb(D), VB = fw_vb(D), KS = kFwStages, PB = kFwKeys * N * 2, QB = N * D * 2;
+    constexpr int N = kFwRows, KB = fw_kb(D), VB = fw_vb(D), KS = kFwStages, PB = kFwKeys * N * 2, QB = N * D * 2;
     constexpr unsigned QLBO = N * 16, KLBO = kFwKS, VLBO = fw_vs(D);
     constexpr int BF = kFwBufs, LB = 2;             // buffers, log2 of them
-    constexpr int TCOLS = N == 16 ? 128 : 256;      // (BF + 1) N columns, a power of two
+    constexpr int TCOLS = 128;                      // (BF + 1) N columns, a power of two
     unsigned char *sK = smem, *sV = sK + KS * KB, *sQ = sV + KS * VB, *sP = sQ + QB, *sR = sP + BF * PB;
     // counts 4 (the softmax warps): Q, P [buffer]; 2 (a tile's two warps, a
     // record's): K and V tiles written, records read; 1: the others
@@ -547,7 +541,6 @@ __global__ void __launch_bounds__(kFwThreads, 1)
         const uint32_t tO = taddr + lane_off + BF * N;
         const float sl2 = 1.4426950408889634f / sqrtf((float)D);   // log2(e) / sqrt(d)
         const int W = a.vis.window, sinks = a.vis.sinks;
-        constexpr int CH = 16;   // columns at a time
         const int kpos = fw_tok(tid);
         int cnt = 0;             // tiles so far
         while (walk.next(g, a, sg)) {
@@ -581,35 +574,33 @@ __global__ void __launch_bounds__(kFwThreads, 1)
                 tc_fence_after();
                 // some row does not see all of this warp's block
                 const bool cut = kb + KIVI_KBLK - 1 > p0 || (W > 0 && kb <= p1 - W && kb + KIVI_KBLK > sinks);
-                // 16 scores of this token as log2 weights against the rows'
+                // the scores of this token as log2 weights against the rows'
                 // references, masked
-                auto scores = [&](int c0, float (&y)[CH]) {
-                    uint32_t r[CH];
-                    tc_ld16(tS + c0, r);
+                auto scores = [&](float (&y)[N]) {
+                    uint32_t r[N];
+                    tc_ld16(tS, r);
                     tc_wait_ld();
 #pragma unroll
-                    for (int c = 0; c < CH; c += 4) {
-                        const float4 ref = *reinterpret_cast<const float4 *>(s_ref + c0 + c);
+                    for (int c = 0; c < N; c += 4) {
+                        const float4 ref = *reinterpret_cast<const float4 *>(s_ref + c);
                         y[c] = fmaf(__uint_as_float(r[c]), sl2, ref.x);
                         y[c + 1] = fmaf(__uint_as_float(r[c + 1]), sl2, ref.y);
                         y[c + 2] = fmaf(__uint_as_float(r[c + 2]), sl2, ref.z);
                         y[c + 3] = fmaf(__uint_as_float(r[c + 3]), sl2, ref.w);
                     }
                     if (cut) {
-                        const uint32_t h = ck_hidden16(key, c0, p0, e0, hg, W, sinks);
+                        const uint32_t h = ck_hidden16(key, 0, p0, e0, hg, W, sinks);
 #pragma unroll
-                        for (int c = 0; c < CH; ++c)
+                        for (int c = 0; c < N; ++c)
                             if ((h >> c) & 1u) y[c] = -INFINITY;
                     }
                 };
-                float s[CH], up = -INFINITY;   // the most that a score lies above its reference
-                if (ok)
+                float s[N], up = -INFINITY;   // the most that a score lies above its reference
+                if (ok) {
+                    scores(s);
 #pragma unroll
-                    for (int c0 = 0; c0 < N; c0 += CH) {
-                        scores(c0, s);
-#pragma unroll
-                        for (int c = 0; c < CH; ++c) up = fmaxf(up, s[c]);
-                    }
+                    for (int c = 0; c < N; ++c) up = fmaxf(up, s[c]);
+                }
                 const bool raise = fw_any(!ok || up > 8.f);
                 if (raise) {
                     // every warp learns whether one has given up
@@ -617,36 +608,33 @@ __global__ void __launch_bounds__(kFwThreads, 1)
                         ok = false;
                         break;
                     }
-                    raise_refs<N>(tS, sl2, cut, key, p0, e0, hg, W, sinks, s_ref, s_al, s_red);
+                    raise_refs(tS, sl2, cut, key, p0, e0, hg, W, sinks, s_ref, s_al, s_red);
 #pragma unroll
                     for (int c = 0; c < N; ++c) lsum[c] *= s_al[c];
                     if (x > 0) {   // O^T, once O^T of tile x - 1 is in
                         ok = __all_sync(kFull, mbar_wait_ab(&bF[(cnt - 1) & (BF - 1)], (unsigned)((cnt - 1) >> LB) & 1u, abort));
                         if (ok) {
                             tc_fence_after();
-                            rescale_out<N>(tO, s_al);
+                            rescale_out(tO, s_al);
                         }
                     }
                 }
                 // P^T: this buffer's last O^T has read its weights
                 if (ok && cnt >= BF) ok = __all_sync(kFull, mbar_wait_ab(&bF[b], (unsigned)((cnt >> LB) + 1) & 1u, abort));
                 if (!ok) continue;   // the next vote ends it for every warp
+                if (raise) scores(s);   // against the new references
+                uint32_t pw[N / 2];
 #pragma unroll
-                for (int c0 = 0; c0 < N; c0 += CH) {
-                    if (N > CH || raise) scores(c0, s);   // (one group of columns: still there)
-                    uint32_t pw[CH / 2];
-#pragma unroll
-                    for (int c = 0; c < CH; c += 2) {
-                        const float y0 = ex2(s[c]), y1 = ex2(s[c + 1]);
-                        lsum[c0 + c] += y0;
-                        lsum[c0 + c + 1] += y1;
-                        pw[c / 2] = ck_pack(y0, y1);
-                    }
-#pragma unroll
-                    for (int k = 0; k < CH / 8; ++k)
-                        *reinterpret_cast<uint4 *>(sP + b * PB + ((c0 / 8 + k) * kFwKeys + kpos) * 16) =
-                            make_uint4(pw[4 * k], pw[4 * k + 1], pw[4 * k + 2], pw[4 * k + 3]);
+                for (int c = 0; c < N; c += 2) {
+                    const float y0 = ex2(s[c]), y1 = ex2(s[c + 1]);
+                    lsum[c] += y0;
+                    lsum[c + 1] += y1;
+                    pw[c / 2] = ck_pack(y0, y1);
                 }
+#pragma unroll
+                for (int k = 0; k < N / 8; ++k)
+                    *reinterpret_cast<uint4 *>(sP + b * PB + (k * kFwKeys + kpos) * 16) =
+                        make_uint4(pw[4 * k], pw[4 * k + 1], pw[4 * k + 2], pw[4 * k + 3]);
                 fence_proxy_async();
                 tc_fence_before();
                 __syncwarp();
@@ -671,15 +659,12 @@ __global__ void __launch_bounds__(kFwThreads, 1)
             // O^T to rows of D floats (the P^T buffers are free), then a row a warp
             float *rows = reinterpret_cast<float *>(sP);
             static_assert((size_t)N * D * 4 <= (size_t)BF * PB, "the rows fit");
+            uint32_t o[N];
+            tc_ld16(tO, o);
+            tc_wait_ld();
+            if (tid < D)
 #pragma unroll
-            for (int c0 = 0; c0 < N; c0 += CH) {
-                uint32_t o[CH];
-                tc_ld16(tO + c0, o);
-                tc_wait_ld();
-                if (tid < D)
-#pragma unroll
-                    for (int c = 0; c < CH; ++c) rows[(c0 + c) * D + tid] = __uint_as_float(o[c]);
-            }
+                for (int c = 0; c < N; ++c) rows[c * D + tid] = __uint_as_float(o[c]);
             fw_sync();
             const bool part = sg.nx < sg.nt;
             const size_t pr = (size_t)(2 * blockIdx.x + (sg.x0 == 0 ? 1 : 0)) * N;

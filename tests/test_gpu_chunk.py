@@ -386,3 +386,50 @@ def test_window_beyond_every_position(n, window):
             c.chunk_attn(q, k, v, n, window=bad)
     assert c.check() == 0
     c.close()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("kb,vb", [(2, 2), (2, 4), (4, 2), (4, 4)])
+@pytest.mark.parametrize("G", [16, 32, 64, 128])
+def test_few_rows_over_long_sequences(d, kb, vb, G):
+    """Few query rows over 32 blocks and more have row tiles of their own:
+    every record format, a short and an empty sequence beside the long one."""
+    if G > d:
+        pytest.skip("needs d % G == 0")
+    _attention_case(3, 4, 1, d, kb, vb, G, max(G, 32), [2413, 90, 0], G // 8, [3, 4, 2], 0, 0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n,hq", [(1, 8), (2, 8), (5, 3), (8, 2), (16, 1), (4, 4)])
+@pytest.mark.parametrize("T", [2040, 2300])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (2035, 0), (2100, 70)])
+def test_few_rows_counts_and_windows(n, hq, T, window, sinks):
+    """Row counts up to a whole tile, at the length from which they have their
+    own row tiles, windows that end inside a block."""
+    _attention_case(2, hq, 1, 128, 2, 4, 32, 32, [T, 10], 1, [n, max(n - 1, 1)], window, sinks)
+
+
+@pytest.mark.gpu
+def test_growing_scores_few_rows():
+    """As test_growing_scores, long enough for few rows' own tiles."""
+    from bit_quantized_kv_quantize_gb300 import kivi as K
+    rng = np.random.default_rng(4)
+    t, d, n = 2600, 64, 2
+    Kh, Vh = (rng.standard_normal((1, 1, t, d)).astype(np.float16) for _ in range(2))
+    Kh[:] = np.abs(Kh) * (np.arange(t) / 260.0).astype(np.float16)[None, None, :, None]
+    Q = np.abs(rng.standard_normal((1, 2, n, d))).astype(np.float16)
+    Kn, Vn = (rng.standard_normal((1, 1, n, d)).astype(np.float16) for _ in range(2))
+    c = K.KiviCache(1, 1, d, 4, 4, 32, 64, t + n)
+    c.prefill(*_cuda(Kh, Vh), t)
+    out = c.chunk_attn(*_cuda(Q, Kn, Vn), n).float().cpu().numpy()
+    k, v = R.restore(Kh[0, 0], Vh[0, 0], *R.counters(t, 64), 4, 4, 32)
+    k, v = np.concatenate([k, Kn[0, 0].astype(np.float64)]), np.concatenate([v, Vn[0, 0].astype(np.float64)])
+    for e in range(2):
+        ref, wabs, mag = R.attend(Q[0, e], k, v, R.visible(t + np.arange(n), t + n, 0, 0))
+        got, h = out[0, e].astype(np.float64), 2.0 ** -11
+        # (the pointwise part of check_rounded: few tokens carry these rows, so
+        # their roundings do not average)
+        bound = wabs * (np.expm1(2 * h * mag)[:, None] + 2 * h + (t + n) * 2.0 ** -23) + np.abs(ref) * h
+        assert np.all(np.abs(got - ref) <= bound + wabs * (t + n) * 2.0 ** -25 + 2.0 ** -24)
+    c.close()
