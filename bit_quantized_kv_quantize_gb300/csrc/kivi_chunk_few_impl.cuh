@@ -320,7 +320,7 @@ __device__ __noinline__ void raise_refs(uint32_t tS, float sl2, bool cut, int ke
     uint32_t r[16];
     tc_ld16(tS, r);
     tc_wait_ld();
-    const uint32_t h = cut ? ck_hidden16(key, 0, p0, e0, hg, W, sinks) : 0u;
+    const uint32_t h = cut ? ck_hidden16(key, p0, e0, hg, W, sinks) : 0u;
 #pragma unroll
     for (int c = 0; c < kFwRows; ++c) {
         const float m = redux_max((h >> c) & 1u ? -INFINITY : __uint_as_float(r[c]) * sl2);
@@ -589,7 +589,7 @@ __global__ void __launch_bounds__(kFwThreads, 1)
                         y[c + 3] = fmaf(__uint_as_float(r[c + 3]), sl2, ref.w);
                     }
                     if (cut) {
-                        const uint32_t h = ck_hidden16(key, 0, p0, e0, hg, W, sinks);
+                        const uint32_t h = ck_hidden16(key, p0, e0, hg, W, sinks);
 #pragma unroll
                         for (int c = 0; c < N; ++c)
                             if ((h >> c) & 1u) y[c] = -INFINITY;

@@ -200,11 +200,11 @@ struct CkWalk {
     }
 };
 
-// Which of the rows (r, e) c0, c0 + 1, ... (16 of them; row 0 at position p0,
-// head e0 of hg) do not see token `key`: bit c for row c0 + c.
-__device__ __noinline__ uint32_t ck_hidden16(int key, int c0, int p0, int e0, int hg, int window, int sinks) {
+// Which of 16 rows (r, e), the first of them head e0 of hg at position p0, do
+// not see token `key`: bit c for row c.
+__device__ __noinline__ uint32_t ck_hidden16(int key, int p0, int e0, int hg, int window, int sinks) {
     uint32_t m = 0;
-    int p = p0 + (e0 + c0) / hg, e = (e0 + c0) % hg;
+    int p = p0, e = e0;
     for (int c = 0; c < 16; ++c) {
         if (key > p || (window > 0 && key <= p - window && key >= sinks)) m |= 1u << c;
         if (++e == hg) {
