@@ -486,7 +486,9 @@ __global__ void __launch_bounds__(kCkThreads, 1)
             }
             const int pos = sg.T + chunk_div(a, row), ps0 = sg.T + chunk_div(a, srow),
                       ps1 = sg.T + chunk_div(a, srow + kCkRows - 1);
-            float mref = -INFINITY, lsum = 0.f;    // the row's reference maximum (raw score units) and weight sum
+            // minus the log2 weight of a score of zero (the row's reference less
+            // the lift; -inf: nothing seen yet), and the weights' sum
+            float ref = -INFINITY, lsum = 0.f;
             for (int x = 0; x < sg.nx; ++x, ++cnt) {
                 const int b = cnt & 1, key0 = sg.key0(x);
                 ok = __all_sync(kFull, mbar_wait_ab(&bS[slot], (unsigned)cnt & 1u, abort));
@@ -518,10 +520,11 @@ __global__ void __launch_bounds__(kCkThreads, 1)
                 const float mx = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])),
                                        fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7])));
                 // lazy rescale: only when the maximum grew by more than 2^8 in weight
-                const bool grow = mx != -INFINITY && (mref == -INFINITY || (mx - mref) * sl2 > 8.f);
-                const float alpha = grow && mref != -INFINITY ? ex2((mref - mx) * sl2) : 1.f;
-                if (grow) mref = mx;
-                const float ms = mref == -INFINITY ? 0.f : mref * sl2;   // (nothing seen yet: weights 0)
+                const bool grow = mx != -INFINITY && (ref == -INFINITY || fmaf(mx, sl2, -ref) > kCkLift + kCkLag);
+                const float up = fmaf(mx, sl2, -kCkLift);
+                const float alpha = grow && ref != -INFINITY ? ex2(ref - up) : 1.f;
+                if (grow) ref = up;
+                const float ms = ref == -INFINITY ? 0.f : ref;   // (nothing seen yet: weights 0)
                 const unsigned long long sc2 = ck_f2(sl2, sl2), ms2 = ck_f2(-ms, -ms);
                 unsigned long long l2[4] = {0ull, 0ull, 0ull, 0ull};
                 uint32_t pw[32];
@@ -568,7 +571,7 @@ __global__ void __launch_bounds__(kCkThreads, 1)
             tc_fence_after();
             if (sg.nx < sg.nt) {   // this CTA's partial of the row
                 const size_t pr = (size_t)(2 * blockIdx.x + (sg.x0 == 0 ? 1 : 0)) * kCkTileRows + slot * kCkRows + rr;
-                if (in) reinterpret_cast<float2 *>(a.ml)[pr] = make_float2(mref * sl2, lsum);
+                if (in) reinterpret_cast<float2 *>(a.ml)[pr] = make_float2(ref, lsum);
 #pragma unroll 1
                 for (int c0 = 0; c0 < D; c0 += 32) {
                     uint32_t o[32];

@@ -64,7 +64,7 @@ constexpr int kFwKS = kFwKeys * 16 + 32;
 __host__ __device__ constexpr int fw_vs(int D) { return D * 16 + 32; }
 __host__ __device__ constexpr int fw_kb(int D) { return D / 8 * kFwKS; }
 __host__ __device__ constexpr int fw_vb(int D) { return kFwKeys / 8 * fw_vs(D); }
-constexpr float kFwUnset = 1e30f;   // minus the reference of a row that has seen nothing
+constexpr float kFwUnset = 1e30f;   // s_ref of a row that has seen nothing
 
 __device__ __forceinline__ float redux_max(float x) {
     float r;
@@ -331,9 +331,9 @@ __device__ __noinline__ void raise_refs(uint32_t tS, float sl2, bool cut, int ke
     if (t < kFwRows) {
         const float m = fmaxf(fmaxf(s_red[0][t], s_red[1][t]), fmaxf(s_red[2][t], s_red[3][t]));
         const float old = s_ref[t];
-        const bool grow = m != -INFINITY && m + old > 8.f;
-        s_al[t] = grow && old != kFwUnset ? ex2(-old - m) : 1.f;
-        if (grow) s_ref[t] = -m;
+        const bool grow = m != -INFINITY && m + old > kCkLift + kCkLag;
+        s_al[t] = grow && old != kFwUnset ? ex2((kCkLift - m) - old) : 1.f;
+        if (grow) s_ref[t] = kCkLift - m;
     }
     fw_sync();
 }
@@ -372,7 +372,7 @@ __global__ void __launch_bounds__(kFwThreads, 1)
                     *const bR = eV + KS;
     __shared__ uint32_t s_taddr;
     __shared__ int s_abort;
-    __shared__ __align__(16) float s_ref[N];       // minus each row's reference (log2 units)
+    __shared__ __align__(16) float s_ref[N];       // the lift less each row's reference (log2 units)
     __shared__ __align__(16) float s_al[N];        // a raise's rescaling factors
     __shared__ float s_red[4][N];                  // per warp: maxima, or sums
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -595,13 +595,13 @@ __global__ void __launch_bounds__(kFwThreads, 1)
                             if ((h >> c) & 1u) y[c] = -INFINITY;
                     }
                 };
-                float s[N], up = -INFINITY;   // the most that a score lies above its reference
+                float s[N], up = -INFINITY;   // the largest lifted log2 weight
                 if (ok) {
                     scores(s);
 #pragma unroll
                     for (int c = 0; c < N; ++c) up = fmaxf(up, s[c]);
                 }
-                const bool raise = fw_any(!ok || up > 8.f);
+                const bool raise = fw_any(!ok || up > kCkLift + kCkLag);
                 if (raise) {
                     // every warp learns whether one has given up
                     if (fw_any(!ok)) {

@@ -15,6 +15,12 @@ namespace {
 constexpr int kCkDqGroup = 4;    // warps that restore a record together
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kJoinRows = 16;    // rows of a row tile that a block joins
+// Weights are taken 2^7 above their row's reference.  In fp16 a weight loses
+// all below 2^-25; lifted, that is 2^-32 of the reference's own weight, and a
+// score 2^8 above the reference (kCkLag: from there on it is raised) still is
+// a finite 2^15.  Many tokens far below one sink then keep their share: 32k of
+// them 17.5 below it came out 8e-4 too small without the lift.
+constexpr float kCkLift = 7.f, kCkLag = 8.f;   // log2
 
 __device__ __forceinline__ uint32_t ck_pack(float lo, float hi) {
     return h2u(__floats2half2_rn(lo, hi));

@@ -130,7 +130,8 @@ kivi_status kivi_prefill_attn_window(kivi_cache_t c, const void *q, const void *
  * out.  Read-only on the cache: kivi_append_chunk appends the tokens, so a
  * rejected draft needs no undoing.  Scores accumulate in fp32; the restored
  * keys and values (scale code + zero) and the softmax weights are rounded to
- * fp16 before the products (|K|, |V| <= 32768, so that they stay finite).
+ * fp16 before the products (|K|, |V| <= 32768, so that they stay finite; a
+ * weight by 2^-11 of itself, or by 2^-32 of the row's largest).
  * out overlaps no input.  One launch, or two when row tiles are split over
  * CTAs and joined (a call's result is repeatable bit for bit).  Uses a buffer of the cache: calls on one cache that overlap on the
  * GPU (two streams, or two captured graphs replayed at once) must not be
