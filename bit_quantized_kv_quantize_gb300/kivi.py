@@ -188,7 +188,8 @@ def rope_frequencies(rot_dim, base=10000.0, scaling=None, factor=1.0, original_l
     if scaling == "yarn":
         at = [rot_dim * math.log(original_length / (r * 2 * math.pi)) / (2 * math.log(base))
               for r in (beta_fast, beta_slow)]
-        lo, hi = max(math.floor(at[0]), 0), min(math.ceil(at[1]), rot_dim // 2 - 1)
+        # (the ramp ends past the last pair where that turns more than beta_slow times)
+        lo, hi = max(math.floor(at[0]), 0), min(math.ceil(at[1]), rot_dim - 1)
         ramp = np.clip((m - lo) / max(hi - lo, 1e-3), 0.0, 1.0)
         return f / factor * ramp + f * (1 - ramp), 0.1 * math.log(factor) + 1.0
     if scaling == "bands":
