@@ -370,6 +370,8 @@ class KiviCache:
         at the positions behind the cached tokens (rope: a Rope, or None),
         attend (chunk_attn; returns its out) and append it (append_chunk)."""
         import torch
+        if torch.cuda.current_device() != self._dev:   # (before the rotation, which runs on the current one)
+            raise KiviError(1, f"the cache belongs to device {self._dev}, which is not current")
         kp, vp, cnt, ns = self._chunk(K, V, n)
         win, snk = _visible(window, sinks)
         T = array.array("i", bytes(4 * self.b))
