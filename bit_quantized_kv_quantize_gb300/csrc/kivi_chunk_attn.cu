@@ -1,5 +1,7 @@
 // kivi_chunk_attn.cu -- plan and launch of the chunk attention
 // (kivi_chunk_attn_impl.cuh).
+#include <climits>
+#include <cstdlib>
 #include <cstring>
 
 #include "kivi_chunk_attn_impl.cuh"
@@ -101,6 +103,8 @@ cudaError_t kivi_launch_chunk_attn(const KiviGeom &g, const KiviDev &dv, const _
             P = end;
         }
     a.cta[ctas] = ChunkPos{U, 0, 0, 0, 0};
+    const char *stop = getenv("KIVI_CHUNK_STOP");   // (tests of a wait that runs out)
+    a.stop = stop ? atoi(stop) : INT_MAX;
     a.acc = partials;
     a.ml = partials + (size_t)2 * num_sms * kCkTileRows * g.d;
     cudaError_t e = few ? kivi_launch_chunk_few(g, dv, Q, K, V, O, a, ctas, st)

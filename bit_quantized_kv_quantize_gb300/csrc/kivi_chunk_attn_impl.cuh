@@ -134,6 +134,23 @@ __device__ __forceinline__ bool packed_tiles(int n, int &tiles, CkRing &t, CkRin
     return true;
 }
 
+// After a wait ran out: the copies of chunk tiles that this thread (the first
+// dequantizing warp's) asked for have landed before shared memory is given up
+// (bounded).  Those of its last KS tiles may not have been waited for; they
+// complete the phases of tiles written, in place of the warps that stopped
+// before them (put: the warps' arrivals at bK, and at bV).
+template <int KS>
+__device__ __noinline__ void drain_tiles(const int (*put)[kCkDq], uint64_t *bK, uint64_t *bV) {
+    for (int k = 0; k < 2; ++k) {
+        uint64_t *const bT = k ? bV : bK;
+        for (int y = max(0, put[k][0] - KS); y < put[k][0]; ++y) {
+            for (int w = 1; w < kCkDq; ++w)
+                if (put[k][w] <= y) mbar_arrive(&bT[y % KS]);
+            mbar_wait(&bT[y % KS], (unsigned)(y / KS) & 1u);
+        }
+    }
+}
+
 // One TMA copy of 128 rows of Q into dst (chunk-major): rows (r, e), e fastest,
 // from token r0 on, of (sequence, kv head) bh.
 __device__ __forceinline__ void tma_rows(void *dst, const CUtensorMap *tm, int r0, int bh, uint64_t *bar,
@@ -173,6 +190,7 @@ __global__ void __launch_bounds__(kCkThreads, 1)
                     *const bF = bS + 2, *const bE = bF + 4, *const eV = bE + 3, *const bR = eV + KS;
     __shared__ uint32_t s_taddr;
     __shared__ int s_abort;   // a wait ran out: every warp stops
+    __shared__ int s_put[2][kCkDq];   // the dequantizing warps' arrivals at K, and V, tiles written
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int hg = a.hg;
     const bool qtma = kCkRows % hg == 0;   // Q's row tiles are boxes of its array
@@ -327,7 +345,7 @@ __global__ void __launch_bounds__(kCkThreads, 1)
         const int w = warp - 8, dt = tid & (32 * kCkDq - 1);
         constexpr int GT = 32 * kCkDq, CPR = D / 8, RPT = kCkKeys * CPR / GT;   // threads, 16-byte chunks a row, a thread's share
         const int lgG = __ffs(g.G) - 1;
-        int tiles = 0, meets = 0;
+        int tiles = 0, kin = 0, meets = 0;   // kin: the current tile's K^ is told of
         CkRing t, r;
         // the dequantizing warps meet (a bounded wait, unlike a named barrier)
         auto meet = [&]() {
@@ -340,6 +358,10 @@ __global__ void __launch_bounds__(kCkThreads, 1)
             const __half *kwin = dv.Kf + kf_slice(g, sg.i, sg.j), *vwin = dv.Vf + vf_slice(g, sg.i, sg.j);
             const size_t chunk0 = ((size_t)sg.i * g.h + sg.j) * a.n_stride;   // the chunk's first row in K and V
             const int npk = max(0, min(sg.nx, sg.bl.virt(min(Tqk, Tqv) / kCkKeys) - sg.x0));   // fully quantized tiles
+            if (tiles >= a.stop && w > 0) {   // (as if a wait had run out)
+                ok = false;
+                break;
+            }
             if (g.kbits == 2)
                 ok = g.vbits == 2 ? packed_tiles<D, 2, 2>(npk, tiles, t, r, sK, sV, sR, g, a.rs, w, bK, eK, bV, eV, bR, eR, abort)
                                   : packed_tiles<D, 2, 4>(npk, tiles, t, r, sK, sV, sR, g, a.rs, w, bK, eK, bV, eV, bR, eR, abort);
@@ -356,7 +378,7 @@ __global__ void __launch_bounds__(kCkThreads, 1)
                 return tau < T + n ? *reinterpret_cast<const uint4 *>(src + 8 * c) : make_uint4(0u, 0u, 0u, 0u);
             };
             // the others: some or all tokens in the window or the chunk
-            for (int x = npk; x < sg.nx && ok; ++x, ++tiles, t.next(KS)) {
+            for (int x = npk; x < sg.nx && ok; ++x, ++tiles, kin = 0, t.next(KS)) {
                 const int tb = sg.key0(x);
                 unsigned char *kt = sK + t.s * TB, *vt = sV + t.s * TB;
                 const bool tma = tb >= T && tb + kCkKeys <= T + n;   // a whole tile of chunk tokens: TMA copies
@@ -370,6 +392,7 @@ __global__ void __launch_bounds__(kCkThreads, 1)
                         tma_tile(sK + t.s * TB, &tmK, (int)chunk0 + tb - T, &bK[t.s], TB);
                     else if (lane == 0)
                         mbar_arrive(&bK[t.s]);
+                    kin = 1;
                     __syncwarp();
                     ok = __all_sync(kFull, tiles < KS || mbar_wait_ab(&eV[t.s], t.p ^ 1u, abort));
                     if (!ok) break;
@@ -402,6 +425,7 @@ __global__ void __launch_bounds__(kCkThreads, 1)
                 fence_proxy_async();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bK[t.s]);
+                kin = 1;
                 ok = __all_sync(kFull, tiles < KS || mbar_wait_ab(&eV[t.s], t.p ^ 1u, abort));
                 if (!ok) break;
                 if (vq) {
@@ -436,14 +460,13 @@ __global__ void __launch_bounds__(kCkThreads, 1)
                 if (raw) r.next(a.rs);
             }
         }
-        if (!ok) {
-            if (lane == 0) {
+        if (lane == 0) {
+            if (!ok) {
                 s_abort = 1;
                 atomicOr(dv.status, KIVI_FLAG_WAIT);
             }
-            // a TMA copy may be in flight: the bounded waits outlast it
-            mbar_wait(&bK[t.s], t.p);
-            mbar_wait(&bV[t.s], t.p);
+            s_put[0][w] = tiles + kin;
+            s_put[1][w] = tiles;
         }
         __syncwarp();
     } else {
@@ -626,6 +649,7 @@ __global__ void __launch_bounds__(kCkThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
+    if (s_abort && tid == 32 * 8) drain_tiles<KS>(s_put, bK, bV);
     if (warp == 0) tc_dealloc(taddr, 512);
 }
 

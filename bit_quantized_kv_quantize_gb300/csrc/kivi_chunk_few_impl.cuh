@@ -503,7 +503,8 @@ __global__ void __launch_bounds__(kFwThreads, 1)
             int blk = (w - 2 * tiles) & (kFwDq - 1);   // the segment's first block of this warp
             CkRing r = seg;
             r.skip(blk, a.rs);
-            for (; blk < 2 * sg.nx; blk += kFwDq, r.skip(kFwDq, a.rs)) {
+            if (tiles >= a.stop && warp > WD) ok = false;   // (as if a wait had run out)
+            for (; ok && blk < 2 * sg.nx; blk += kFwDq, r.skip(kFwDq, a.rs)) {
                 const int y = tiles + (blk >> 1), st = y % KS, half = blk & 1;
                 const bool raw = blk < nraw;
                 const unsigned char *rp = sR + (size_t)r.s * g.rec_bytes;
