@@ -360,6 +360,15 @@ kivi_status launch_fused_step(kivi_cache *c, const void *k, const void *v, const
     return KIVI_OK;
 }
 
+// Plans the attention of the chunk in a.
+kivi_status plan_chunk_attn(const kivi_cache *c, ChunkArgs &a, ChunkPlan *plan) {
+    if (!kivi_plan_chunk_attn(c->g, a, c->num_sms, plan)) {
+        set_err("more than 2^31 key tiles an SM");
+        return KIVI_ERR_UNSUPPORTED;
+    }
+    return KIVI_OK;
+}
+
 // kivi_prefill_attn and kivi_prefill_attn_window
 kivi_status prefill_attn(kivi_cache_t c, const void *q, const void *K, const void *V, const int32_t *t, int t_stride,
                          int h_q, Visible vis, void *out, kivi_stream_t stream) {
@@ -422,10 +431,13 @@ kivi_status prefill_attn(kivi_cache_t c, const void *q, const void *K, const voi
         a.n_stride = t_stride;
         a.hq = h_q;
         a.vis = vis;
+        ChunkPlan plan;
+        s = plan_chunk_attn(c, a, &plan);
+        if (s != KIVI_OK) return s;
         e = kivi_launch_prefill(c->g, c->dv, (const __half *)K, (const __half *)V, lens, t_stride, (cudaStream_t)stream);
         if (e == cudaSuccess)
             e = kivi_launch_chunk_attn(c->g, c->dv, (const __half *)q, (const __half *)K, (const __half *)V,
-                                       (__half *)out, a, c->chunk_part, c->num_sms, (cudaStream_t)stream);
+                                       (__half *)out, a, plan, c->chunk_part, c->num_sms, (cudaStream_t)stream);
     } else {
         e = kivi_launch_prefill_attn(c->g, c->dv, (const __half *)q, (const __half *)K, (const __half *)V,
                                      (__half *)out, lens, t_stride, h_q, (cudaStream_t)stream);
@@ -689,8 +701,11 @@ kivi_status kivi_chunk_attn(kivi_cache_t c, const void *q, const void *K, const 
     }
     a.hq = h_q;
     a.vis = Visible{window, sinks};
+    ChunkPlan plan;
+    s = plan_chunk_attn(c, a, &plan);
+    if (s != KIVI_OK) return s;
     cudaError_t e = kivi_launch_chunk_attn(c->g, c->dv, (const __half *)q, (const __half *)K, (const __half *)V,
-                                           (__half *)out, a, c->chunk_part, c->num_sms, (cudaStream_t)stream);
+                                           (__half *)out, a, plan, c->chunk_part, c->num_sms, (cudaStream_t)stream);
     if (e != cudaSuccess) return fail_cuda(c, e, "chunk_attn");
     return KIVI_OK;
 }

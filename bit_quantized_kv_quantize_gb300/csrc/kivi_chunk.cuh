@@ -63,13 +63,22 @@ __host__ __device__ __forceinline__ int chunk_tqv(int T, int Tqv, int n, int R) 
     return n > 0 && f > Tqv ? f : Tqv;
 }
 
+// How a chunk's attention runs.
+struct ChunkPlan {
+    bool few;   // the kernel for few rows
+    bool join;  // row tiles are cut: partials, and the kernel that joins them
+    int ctas;   // 0: nothing to do
+};
 // floats of the attention's partials buffer of a cache with head dimension d
 size_t kivi_chunk_partial_floats(int d, int num_sms);
-// The attention of the chunk (kivi_chunk_attn.cu).  a: hq, n_stride, vis, T,
-// Tqk, Tqv and n.  d in {64, 128} (cudaErrorInvalidValue otherwise).
+// Plans the attention of the chunk (kivi_chunk_attn.cu).  a: hq, n_stride,
+// vis, T, Tqk, Tqv and n; the work list is added.  False if a CTA's share
+// would pass 32 bits.
+bool kivi_plan_chunk_attn(const KiviGeom &g, ChunkArgs &a, int num_sms, ChunkPlan *plan);
+// ... and launches it.  d in {64, 128} (cudaErrorInvalidValue otherwise).
 cudaError_t kivi_launch_chunk_attn(const KiviGeom &g, const KiviDev &dv, const __half *Q, const __half *K,
-                                   const __half *V, __half *O, ChunkArgs &a, float *partials, int num_sms,
-                                   cudaStream_t st);
+                                   const __half *V, __half *O, ChunkArgs &a, const ChunkPlan &plan, float *partials,
+                                   int num_sms, cudaStream_t st);
 // The append of the chunk (kivi_chunk_append.cu); the counters after it go to
 // nxt ([3][b], the other counter set).
 cudaError_t kivi_launch_append_chunk(const KiviGeom &g, const KiviDev &dv, const __half *K, const __half *V,

@@ -41,11 +41,7 @@ size_t kivi_chunk_partial_floats(int d, int num_sms) {
     return d > 128 ? 0 : (size_t)2 * num_sms * kCkTileRows * (d + 2);
 }
 
-cudaError_t kivi_launch_chunk_attn(const KiviGeom &g, const KiviDev &dv, const __half *Q, const __half *K,
-                                   const __half *V, __half *O, ChunkArgs &a, float *partials, int num_sms,
-                                   cudaStream_t st) {
-    if (g.d != 64 && g.d != 128) return cudaErrorInvalidValue;
-    if ((long long)g.b * g.h * a.n_stride >= (1LL << 31)) return cudaErrorInvalidValue;   // TMA row coordinates
+bool kivi_plan_chunk_attn(const KiviGeom &g, ChunkArgs &a, int num_sms, ChunkPlan *plan) {
     const int hg = a.hq / g.h;
     a.hg = hg;
     a.hg_mul = (unsigned)(((1ull << 32) + hg - 1) / hg);
@@ -54,7 +50,8 @@ cudaError_t kivi_launch_chunk_attn(const KiviGeom &g, const KiviDev &dv, const _
         maxrows = a.n[i] * hg > maxrows ? a.n[i] * hg : maxrows;
         end = a.T[i] + a.n[i] > end ? a.T[i] + a.n[i] : end;
     }
-    if (maxrows == 0) return cudaSuccess;
+    *plan = ChunkPlan{false, false, 0};
+    if (maxrows == 0) return true;
     // a window that no position reaches is none (and would pass 32 bits below
     // the first positions)
     if (a.vis.window >= end) a.vis = Visible{0, 0};
@@ -86,6 +83,7 @@ cudaError_t kivi_launch_chunk_attn(const KiviGeom &g, const KiviDev &dv, const _
     const long long sms = num_sms < kCkMaxCtas ? num_sms : kCkMaxCtas;
     const long long want = U > 3 * kCkLead * items && U / (2 * kCkLead) > items ? U / (2 * kCkLead) : items;
     const int ctas = (int)(want < sms ? want : sms);
+    if (U / ctas >= INT_MAX) return false;   // (CkWalk counts them)
     // each CTA's first unit, and whether one lies behind the first key tile of
     // a row tile (whose partials are then joined)
     bool join = false;
@@ -105,13 +103,23 @@ cudaError_t kivi_launch_chunk_attn(const KiviGeom &g, const KiviDev &dv, const _
     a.cta[ctas] = ChunkPos{U, 0, 0, 0, 0};
     const char *stop = getenv("KIVI_CHUNK_STOP");   // (tests of a wait that runs out)
     a.stop = stop ? atoi(stop) : INT_MAX;
+    *plan = ChunkPlan{few, join, ctas};
+    return true;
+}
+
+cudaError_t kivi_launch_chunk_attn(const KiviGeom &g, const KiviDev &dv, const __half *Q, const __half *K,
+                                   const __half *V, __half *O, ChunkArgs &a, const ChunkPlan &plan, float *partials,
+                                   int num_sms, cudaStream_t st) {
+    if (plan.ctas == 0) return cudaSuccess;
+    if (g.d != 64 && g.d != 128) return cudaErrorInvalidValue;
+    if ((long long)g.b * g.h * a.n_stride >= (1LL << 31)) return cudaErrorInvalidValue;   // TMA row coordinates
     a.acc = partials;
     a.ml = partials + (size_t)2 * num_sms * kCkTileRows * g.d;
-    cudaError_t e = few ? kivi_launch_chunk_few(g, dv, Q, K, V, O, a, ctas, st)
-                    : g.d == 64 ? launch_chunk<64>(g, dv, Q, K, V, O, a, ctas, st)
-                                : launch_chunk<128>(g, dv, Q, K, V, O, a, ctas, st);
-    if (e != cudaSuccess || !join) return e;
-    const unsigned blocks = (unsigned)(ctas - 1) * (a.tile_rows / kJoinRows);
+    cudaError_t e = plan.few ? kivi_launch_chunk_few(g, dv, Q, K, V, O, a, plan.ctas, st)
+                    : g.d == 64 ? launch_chunk<64>(g, dv, Q, K, V, O, a, plan.ctas, st)
+                                : launch_chunk<128>(g, dv, Q, K, V, O, a, plan.ctas, st);
+    if (e != cudaSuccess || !plan.join) return e;
+    const unsigned blocks = (unsigned)(plan.ctas - 1) * (a.tile_rows / kJoinRows);
     if (g.d == 64) chunk_join_kernel<64><<<blocks, 256, 0, st>>>(O, a);
     else chunk_join_kernel<128><<<blocks, 256, 0, st>>>(O, a);
     return cudaGetLastError();
