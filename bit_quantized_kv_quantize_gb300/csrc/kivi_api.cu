@@ -377,8 +377,8 @@ kivi_status prefill_attn(kivi_cache_t c, const void *q, const void *K, const voi
     if (vis.window > 0) {
         s = check_device(c);
         if (s != KIVI_OK) return s;
-        if (t_stride > 0 && (long long)c->g.b * c->g.h * t_stride >= (1LL << 31)) {
-            set_err("b h_kv t_stride must be below 2^31");
+        if (t_stride > (1 << 26) || (t_stride > 0 && (long long)c->g.b * c->g.h * t_stride >= (1LL << 31))) {
+            set_err("t_stride above 2^26, or b h_kv t_stride not below 2^31");
             return KIVI_ERR_UNSUPPORTED;
         }
     }

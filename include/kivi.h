@@ -112,7 +112,8 @@ kivi_status kivi_prefill_attn(kivi_cache_t c, const void *q, const void *K, cons
  * the prompt; the cache afterwards is the same (it takes every token).  Key
  * tiles that no query of a tile sees are neither read nor multiplied.  With
  * window > 0 several launches, which use the cache's buffer as
- * kivi_chunk_attn's do; b h_kv t_stride below 2^31. */
+ * kivi_chunk_attn's do, and its limits: t_stride <= 2^26, b h_kv t_stride
+ * below 2^31. */
 kivi_status kivi_prefill_attn_window(kivi_cache_t c, const void *q, const void *K, const void *V, const int32_t *t,
                                      int t_stride, int h_q, int window, int sinks, void *out,
                                      kivi_stream_t stream);
@@ -136,10 +137,11 @@ kivi_status kivi_prefill_attn_window(kivi_cache_t c, const void *q, const void *
  * CTAs and joined (a call's result is repeatable bit for bit).  Uses a buffer of the cache: calls on one cache that overlap on the
  * GPU (two streams, or two captured graphs replayed at once) must not be
  * issued.  A captured call replays with the counts and positions it was
- * captured with.  Supports d 64 or 128 and n_stride <= 2^26, while an SM's
- * share of the work is below 2^31 key tiles (64 tokens for 256 rows;
- * KIVI_ERR_UNSUPPORTED otherwise); h_q a multiple of h_kv, at most 8 times
- * it; the cache's device must be current (KIVI_ERR_INVALID_ARG). */
+ * captured with.  Supports d 64 or 128, n_stride <= 2^26 and b h_kv n_stride
+ * below 2^31, while an SM's share of the work is below 2^31 key tiles (64
+ * tokens for 256 rows; KIVI_ERR_UNSUPPORTED otherwise); h_q a multiple of
+ * h_kv, at most 8 times it; the cache's device must be current
+ * (KIVI_ERR_INVALID_ARG). */
 kivi_status kivi_chunk_attn(kivi_cache_t c, const void *q, const void *K, const void *V, const int32_t *n,
                             int n_stride, int h_q, int window, int sinks, void *out, kivi_stream_t stream);
 

@@ -25,3 +25,15 @@ def test_work_beyond_32_bits_is_refused():
     assert c.lengths()[0].tolist() == [0] and c.check() == 0
     assert torch.equal(c.chunk_attn(x, x[:, :1].contiguous(), x[:, :1].contiguous(), 4), x)   # still usable
     c.close()
+
+
+@pytest.mark.gpu
+def test_windowed_prompt_beyond_its_stride_is_refused():
+    """Row indices of up to 8 heads a kv head must stay below 2^29."""
+    import torch
+    from bit_quantized_kv_quantize_gb300 import kivi as K
+    c = K.KiviCache(1, 1, 64, 2, 2, 32, 32, 64)
+    x = torch.zeros(1, 8, 4, 64, device="cuda").half()
+    assert _call(K, c, K.lib.kivi_prefill_attn_window, x, 4, (1 << 26) + 1, 8, 7) == 2
+    assert c.lengths()[0].tolist() == [0] and c.check() == 0
+    c.close()
