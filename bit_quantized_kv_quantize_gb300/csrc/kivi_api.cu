@@ -49,7 +49,9 @@ struct kivi_cache {
     // which then becomes current (no CTA of the append waits for another).
     int *cnt;
     int parity;
-    float *chunk_part;   // split partials of the chunk attention
+    // the chunk attention's partials, made by the first call that cuts row
+    // tiles: of 256 rows, of few rows
+    float *chunk_part[2];
     std::vector<int> T, Tqk, Tqv;   // host mirror
     DecodePlan last_plan;
     bool profiling;
@@ -135,12 +137,12 @@ kivi_status check_shape(int b, int h_kv, int d, int k_bits, int v_bits, int G, i
 
 void free_dev(kivi_cache *c) {
     KiviDev &d = c->dv;
-    void *ps[] = {d.blk, d.Kf, d.Vf, c->cnt, d.status, d.part, d.merge_ticket, d.ml, c->chunk_part};
+    void *ps[] = {d.blk, d.Kf, d.Vf, c->cnt, d.status, d.part, d.merge_ticket, d.ml, c->chunk_part[0], c->chunk_part[1]};
     for (void *p : ps)
         if (p) cudaFree(p);
     memset(&d, 0, sizeof d);
     c->cnt = nullptr;
-    c->chunk_part = nullptr;
+    c->chunk_part[0] = c->chunk_part[1] = nullptr;
 }
 
 void point_counters(kivi_cache *c) {
@@ -360,13 +362,26 @@ kivi_status launch_fused_step(kivi_cache *c, const void *k, const void *v, const
     return KIVI_OK;
 }
 
-// Plans the attention of the chunk in a.
-kivi_status plan_chunk_attn(const kivi_cache *c, ChunkArgs &a, ChunkPlan *plan) {
+// Plans the attention of the chunk in a, and makes the buffer for its partials
+// where it needs one and has none yet.  (Relaxed: the allocation is legal, and
+// not part of the graph, while a stream is captured.)
+kivi_status plan_chunk_attn(kivi_cache *c, ChunkArgs &a, ChunkPlan *plan) {
     if (!kivi_plan_chunk_attn(c->g, a, c->num_sms, plan)) {
         set_err("more than 2^31 key tiles an SM");
         return KIVI_ERR_UNSUPPORTED;
     }
-    return KIVI_OK;
+    float **part = &c->chunk_part[plan->few];
+    if (!plan->join || *part) return KIVI_OK;
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    cudaThreadExchangeStreamCaptureMode(&mode);
+    const cudaError_t e = cudaMalloc((void **)part, kivi_chunk_partial_floats(c->g, *plan, c->num_sms) * 4);
+    cudaThreadExchangeStreamCaptureMode(&mode);
+    if (e == cudaSuccess) return KIVI_OK;
+    *part = nullptr;
+    if (e != cudaErrorMemoryAllocation) return fail_cuda(c, e, "partials");
+    cudaGetLastError();
+    set_err("no device memory for the partials");
+    return KIVI_ERR_OOM;
 }
 
 // kivi_prefill_attn and kivi_prefill_attn_window
@@ -437,7 +452,7 @@ kivi_status prefill_attn(kivi_cache_t c, const void *q, const void *K, const voi
         e = kivi_launch_prefill(c->g, c->dv, (const __half *)K, (const __half *)V, lens, t_stride, (cudaStream_t)stream);
         if (e == cudaSuccess)
             e = kivi_launch_chunk_attn(c->g, c->dv, (const __half *)q, (const __half *)K, (const __half *)V,
-                                       (__half *)out, a, plan, c->chunk_part, c->num_sms, (cudaStream_t)stream);
+                                       (__half *)out, a, plan, c->chunk_part[plan.few], c->num_sms, (cudaStream_t)stream);
     } else {
         e = kivi_launch_prefill_attn(c->g, c->dv, (const __half *)q, (const __half *)K, (const __half *)V,
                                      (__half *)out, lens, t_stride, h_q, (cudaStream_t)stream);
@@ -489,7 +504,7 @@ kivi_status kivi_cache_create(int b, int h_kv, int d, int k_bits, int v_bits, in
     }
     c->magic = kMagic;
     c->poisoned = false;
-    c->chunk_part = nullptr;
+    c->chunk_part[0] = c->chunk_part[1] = nullptr;
     c->max_tokens = max_tokens;
     c->profiling = false;
     c->nprof = 0;
@@ -523,10 +538,8 @@ kivi_status kivi_cache_create(int b, int h_kv, int d, int k_bits, int v_bits, in
         {(void **)&dv.part, bh * KIVI_MAX_QPERKV * g.smax * (d + 4) * 4},
         {(void **)&dv.merge_ticket, bh * 4 * 4},
         {(void **)&dv.ml, bh * KIVI_MAX_QPERKV * 2 * 4},
-        {(void **)&c->chunk_part, kivi_chunk_partial_floats(d, c->num_sms) * 4},
     };
     for (auto &r : reqs) {
-        if (r.bytes == 0) continue;
         e = cudaMalloc(r.p, r.bytes);
         if (e == cudaSuccess) e = cudaMemset(*r.p, 0, r.bytes);
         if (e != cudaSuccess) {
@@ -705,7 +718,7 @@ kivi_status kivi_chunk_attn(kivi_cache_t c, const void *q, const void *K, const 
     s = plan_chunk_attn(c, a, &plan);
     if (s != KIVI_OK) return s;
     cudaError_t e = kivi_launch_chunk_attn(c->g, c->dv, (const __half *)q, (const __half *)K, (const __half *)V,
-                                           (__half *)out, a, plan, c->chunk_part, c->num_sms, (cudaStream_t)stream);
+                                           (__half *)out, a, plan, c->chunk_part[plan.few], c->num_sms, (cudaStream_t)stream);
     if (e != cudaSuccess) return fail_cuda(c, e, "chunk_attn");
     return KIVI_OK;
 }

@@ -69,13 +69,14 @@ struct ChunkPlan {
     bool join;  // row tiles are cut: partials, and the kernel that joins them
     int ctas;   // 0: nothing to do
 };
-// floats of the attention's partials buffer of a cache with head dimension d
-size_t kivi_chunk_partial_floats(int d, int num_sms);
+// floats of the partials that a plan's row tiles leave (two a CTA)
+size_t kivi_chunk_partial_floats(const KiviGeom &g, const ChunkPlan &plan, int num_sms);
 // Plans the attention of the chunk (kivi_chunk_attn.cu).  a: hq, n_stride,
 // vis, T, Tqk, Tqv and n; the work list is added.  False if a CTA's share
 // would pass 32 bits.
 bool kivi_plan_chunk_attn(const KiviGeom &g, ChunkArgs &a, int num_sms, ChunkPlan *plan);
-// ... and launches it.  d in {64, 128} (cudaErrorInvalidValue otherwise).
+// ... and launches it.  partials: not used without a join.  d in {64, 128}
+// (cudaErrorInvalidValue otherwise).
 cudaError_t kivi_launch_chunk_attn(const KiviGeom &g, const KiviDev &dv, const __half *Q, const __half *K,
                                    const __half *V, __half *O, ChunkArgs &a, const ChunkPlan &plan, float *partials,
                                    int num_sms, cudaStream_t st);

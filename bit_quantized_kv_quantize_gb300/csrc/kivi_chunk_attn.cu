@@ -37,8 +37,8 @@ cudaError_t launch_chunk(const KiviGeom &g, const KiviDev &dv, const __half *Q, 
 
 }  // namespace
 
-size_t kivi_chunk_partial_floats(int d, int num_sms) {
-    return d > 128 ? 0 : (size_t)2 * num_sms * kCkTileRows * (d + 2);
+size_t kivi_chunk_partial_floats(const KiviGeom &g, const ChunkPlan &plan, int num_sms) {
+    return (size_t)2 * num_sms * (plan.few ? kFewRows : kCkTileRows) * (g.d + 2);
 }
 
 bool kivi_plan_chunk_attn(const KiviGeom &g, ChunkArgs &a, int num_sms, ChunkPlan *plan) {
@@ -114,7 +114,7 @@ cudaError_t kivi_launch_chunk_attn(const KiviGeom &g, const KiviDev &dv, const _
     if (g.d != 64 && g.d != 128) return cudaErrorInvalidValue;
     if ((long long)g.b * g.h * a.n_stride >= (1LL << 31)) return cudaErrorInvalidValue;   // TMA row coordinates
     a.acc = partials;
-    a.ml = partials + (size_t)2 * num_sms * kCkTileRows * g.d;
+    a.ml = partials + (size_t)2 * num_sms * a.tile_rows * g.d;
     cudaError_t e = plan.few ? kivi_launch_chunk_few(g, dv, Q, K, V, O, a, plan.ctas, st)
                     : g.d == 64 ? launch_chunk<64>(g, dv, Q, K, V, O, a, plan.ctas, st)
                                 : launch_chunk<128>(g, dv, Q, K, V, O, a, plan.ctas, st);

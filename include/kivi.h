@@ -29,7 +29,9 @@
  *     KIVI_ERR_STATE (destroy still works).
  *   - calls on one handle are not thread-safe; different handles are
  *     independent.
- *   - no call allocates device memory except kivi_cache_create.
+ *   - no call allocates device memory except kivi_cache_create and, once a
+ *     cache, the first kivi_chunk_attn or kivi_prefill_attn_window that
+ *     splits its work (see there).
  * Supported shapes: k_bits, v_bits in {2, 4}; G in {16, 32, 64, 128};
  * d in {64, 128, 256} with d % G == 0; R % G == 0 (item 4's assertion);
  * 1 <= b <= 1024; h_q a multiple of h_kv with h_q / h_kv <= 8.
@@ -64,9 +66,9 @@ typedef enum {
  * holding up to max_tokens tokens per sequence; k_bits / v_bits per item 1,
  * group size G per items 2-3, residual length R per item 4.  All device
  * memory of the cache is allocated here (packed codes, fp16 scale/zero,
- * fp16 residual windows, counters, decode partials, and with d <= 128 the
- * chunk attention's partials: 2 x SMs x 256 rows of d + 2 floats, 40 MB at
- * d = 128).  *out receives the handle; release it with kivi_cache_destroy. */
+ * fp16 residual windows, counters, decode partials), but for the chunk
+ * attention's partials.  *out receives the handle; release it with
+ * kivi_cache_destroy. */
 kivi_status kivi_cache_create(int b, int h_kv, int d, int k_bits, int v_bits, int G, int R,
                               int max_tokens, kivi_cache_t *out);
 
@@ -134,10 +136,14 @@ kivi_status kivi_prefill_attn_window(kivi_cache_t c, const void *q, const void *
  * fp16 before the products (|K|, |V| <= 32768, so that they stay finite; a
  * weight by 2^-11 of itself, or by 2^-32 of the row's largest).
  * out overlaps no input.  One launch, or two when row tiles are split over
- * CTAs and joined (a call's result is repeatable bit for bit).  Uses a buffer of the cache: calls on one cache that overlap on the
- * GPU (two streams, or two captured graphs replayed at once) must not be
- * issued.  A captured call replays with the counts and positions it was
- * captured with.  Supports d 64 or 128, n_stride <= 2^26 and b h_kv n_stride
+ * CTAs and joined (a call's result is repeatable bit for bit).
+ * Splitting uses a buffer of the cache, which the first such call allocates
+ * (2 x SMs x 256 rows of d + 2 floats, 40 MB at d = 128, or with up to 16 rows
+ * a kv head a sixteenth of that; also while its stream is captured; without
+ * the memory KIVI_ERR_OOM, and nothing changes) and the cache keeps: calls on
+ * one cache that overlap on the GPU (two streams, or two captured graphs
+ * replayed at once) must not be issued.  A captured call replays with the
+ * counts and positions it was captured with.  Supports d 64 or 128, n_stride <= 2^26 and b h_kv n_stride
  * below 2^31, while an SM's share of the work is below 2^31 key tiles (64
  * tokens for 256 rows; KIVI_ERR_UNSUPPORTED otherwise); h_q a multiple of
  * h_kv, at most 8 times it; the cache's device must be current
