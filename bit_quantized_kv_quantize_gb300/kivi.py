@@ -262,7 +262,11 @@ class Rope:
 
 
 class KiviCache:
-    """A KIVI quantized KV cache of b sequences x h_kv heads on the current GPU."""
+    """A KIVI quantized KV cache of b sequences x h_kv heads on the current GPU.
+
+    Calls on one cache must not overlap on the GPU, on two streams or in two
+    captured graphs replayed at once: those that only read it (decode,
+    chunk_attn) share its buffers too."""
 
     def __init__(self, b, h_kv, d, k_bits=2, v_bits=2, G=32, R=128, max_tokens=4096):
         self.b, self.h_kv, self.d = b, h_kv, d
@@ -309,7 +313,7 @@ class KiviCache:
         [b, h_q, t_stride, d] -> out (same shape; rows past each sequence's
         length untouched).  One launch.  With window > 0 a query sees only the
         last `window` tokens up to its own and the sequence's first `sinks`
-        (several launches; calls on one cache must not overlap)."""
+        (several launches)."""
         import torch
         t = np.ascontiguousarray(np.broadcast_to(np.asarray(t, np.int32), (self.b,)))
         ts, hq = K.shape[2], Q.shape[1]

@@ -27,11 +27,13 @@
  *     error nothing is launched and the cache is unchanged.
  *   - a CUDA error inside a call poisons the handle: later calls return
  *     KIVI_ERR_STATE (destroy still works).
- *   - calls on one handle are not thread-safe; different handles are
- *     independent.
- *   - no call allocates device memory except kivi_cache_create and, once a
- *     cache, the first kivi_chunk_attn or kivi_prefill_attn_window that
- *     splits its work (see there).
+ *   - calls on one handle are not thread-safe, and must not overlap on the GPU
+ *     (two streams without an event between them, two captured graphs replayed
+ *     at once): also the read-only ones share the handle's buffers.  Different
+ *     handles are independent.
+ *   - no call allocates device memory except kivi_cache_create and a cache's
+ *     first kivi_chunk_attn or kivi_prefill_attn_window that splits its work
+ *     (see there).
  * Supported shapes: k_bits, v_bits in {2, 4}; G in {16, 32, 64, 128};
  * d in {64, 128, 256} with d % G == 0; R % G == 0 (item 4's assertion);
  * 1 <= b <= 1024; h_q a multiple of h_kv with h_q / h_kv <= 8.
@@ -140,10 +142,9 @@ kivi_status kivi_prefill_attn_window(kivi_cache_t c, const void *q, const void *
  * Splitting uses a buffer of the cache, which the first such call allocates
  * (2 x SMs x 256 rows of d + 2 floats, 40 MB at d = 128, or with up to 16 rows
  * a kv head a sixteenth of that; also while its stream is captured; without
- * the memory KIVI_ERR_OOM, and nothing changes) and the cache keeps: calls on
- * one cache that overlap on the GPU (two streams, or two captured graphs
- * replayed at once) must not be issued.  A captured call replays with the
- * counts and positions it was captured with.  Supports d 64 or 128, n_stride <= 2^26 and b h_kv n_stride
+ * the memory KIVI_ERR_OOM, and nothing changes) and the cache keeps.  A
+ * captured call replays with the counts and positions it was captured with.
+ * Supports d 64 or 128, n_stride <= 2^26 and b h_kv n_stride
  * below 2^31, while an SM's share of the work is below 2^31 key tiles (64
  * tokens for 256 rows; KIVI_ERR_UNSUPPORTED otherwise); h_q a multiple of
  * h_kv, at most 8 times it; the cache's device must be current
