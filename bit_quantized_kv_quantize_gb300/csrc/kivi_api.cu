@@ -397,8 +397,9 @@ kivi_status prefill_attn(kivi_cache_t c, const void *q, const void *K, const voi
             return KIVI_ERR_UNSUPPORTED;
         }
     }
-    if (c->g.G > 64 || (c->g.d != 64 && c->g.d != 128)) {
-        set_err("prefill attention supports d 64 or 128 and G <= 64");
+    // (G: the packing in the attention's own CTAs; with a window the prefill's kernels pack)
+    if ((c->g.G > 64 && vis.window == 0) || (c->g.d != 64 && c->g.d != 128)) {
+        set_err("prefill attention supports d 64 or 128, and G <= 64 without a window");
         return KIVI_ERR_UNSUPPORTED;
     }
     if (h_q < c->g.h || h_q % c->g.h != 0 || h_q / c->g.h > KIVI_MAX_QPERKV) {

@@ -116,8 +116,8 @@ kivi_status kivi_prefill_attn(kivi_cache_t c, const void *q, const void *K, cons
  * the prompt; the cache afterwards is the same (it takes every token).  Key
  * tiles that no query of a tile sees are neither read nor multiplied.  With
  * window > 0 several launches, which use the cache's buffer as
- * kivi_chunk_attn's do, and its limits: t_stride <= 2^26, b h_kv t_stride
- * below 2^31. */
+ * kivi_chunk_attn's do, and its limits: any G; t_stride <= 2^26, b h_kv
+ * t_stride below 2^31. */
 kivi_status kivi_prefill_attn_window(kivi_cache_t c, const void *q, const void *K, const void *V, const int32_t *t,
                                      int t_stride, int h_q, int window, int sinks, void *out,
                                      kivi_stream_t stream);
