@@ -219,15 +219,6 @@ __device__ __forceinline__ void few_values(const KiviGeom &g, unsigned char *til
     if (g.vbits == 2) few_values_g<D, 2>(tile, rec + g.off_vc, rec + g.off_vsz, lgG);
     else few_values_g<D, 4>(tile, rec + g.off_vc, rec + g.off_vsz, lgG);
 }
-// ... out of line, for blocks that also hold fp16 tokens
-template <int D>
-__device__ __noinline__ void few_keys_cold(const KiviGeom &g, unsigned char *tile, const unsigned char *rec, int lgG) {
-    few_keys<D>(g, tile, rec, lgG);
-}
-template <int D>
-__device__ __noinline__ void few_values_cold(const KiviGeom &g, unsigned char *tile, const unsigned char *rec, int lgG) {
-    few_values<D>(g, tile, rec, lgG);
-}
 // 16 bytes of a row (channels 8 c ..) to their positions in row r of a tile
 // whose chunks are STEP bytes apart
 template <int STEP>
