@@ -128,8 +128,12 @@ cudaError_t launch_rope(const RopeArgs &A, int b, bool interleaved, int maxn, cu
     // fewer while that leaves half of the SMs without a block.  40 heads, eight
     // a thread and one, in microseconds: 4 x 8192 tokens 99 and 238, 2048
     // tokens 8.1 and 16.6, 512 tokens 4.3 and 5.8, 64 tokens 4.2 and 2.4.
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
     int per = 8;
-    while (per > 1 && (long long)gx * b * ((rows + per - 1) / per) < 76) per >>= 1;
+    while (per > 1 && (long long)gx * b * ((rows + per - 1) / per) < sms / 2) per >>= 1;
     const dim3 grid(gx, (rows + per - 1) / per, b);
     if (interleaved) rope_kernel<D, true><<<grid, kRopeThreads, 0, st>>>(A, lgTR, lgHY);
     else rope_kernel<D, false><<<grid, kRopeThreads, 0, st>>>(A, lgTR, lgHY);
