@@ -18,9 +18,10 @@ struct ChunkArgs {
     int hq, hg, n_stride;         // hg: query heads a kv head
     unsigned hg_mul;              // ceil(2^32 / hg): x / hg = umulhi(x, hg_mul) for x < 2^29 (hg <= 8)
     int rs;           // record stages
-    int stop;         // tiles after which all dequantizing warps but the first give up (tests; INT_MAX: none)
     int tile_rows, tile_blocks;   // rows of a row tile, 64-token blocks of a key tile
     Visible vis;
+    int quit;         // (tests) a warp gives up: with few rows the copying one after so many records, else
+                      // the dequantizing ones but the first at once; INT_MAX: none does
     float *acc, *ml;  // partials: [2 CTAs][tile_rows][d] and [2 CTAs][tile_rows][2]
     ChunkPos cta[kCkMaxCtas + 1];
     int T[KIVI_MAX_BATCH], Tqk[KIVI_MAX_BATCH], Tqv[KIVI_MAX_BATCH], n[KIVI_MAX_BATCH];

@@ -101,8 +101,8 @@ bool kivi_plan_chunk_attn(const KiviGeom &g, ChunkArgs &a, int num_sms, ChunkPla
             P = end;
         }
     a.cta[ctas] = ChunkPos{U, 0, 0, 0, 0};
-    const char *stop = getenv("KIVI_CHUNK_STOP");   // (tests of a wait that runs out)
-    a.stop = stop ? atoi(stop) : INT_MAX;
+    const char *quit = getenv("KIVI_CHUNK_QUIT");
+    a.quit = quit ? atoi(quit) : INT_MAX;
     *plan = ChunkPlan{few, join, ctas};
     return true;
 }

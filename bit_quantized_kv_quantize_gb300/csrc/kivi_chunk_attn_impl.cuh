@@ -54,6 +54,8 @@
 // CTAs share leaves unnormalized partials (max, sum, O), joined by a second
 // kernel.
 #pragma once
+#include <climits>
+
 #include "kivi_chunk_tiles.cuh"
 #include "kivi_tcgen05.cuh"
 #include "kivi_tma.cuh"
@@ -345,6 +347,7 @@ __global__ void __launch_bounds__(kCkThreads, 1)
         const int w = warp - 8, dt = tid & (32 * kCkDq - 1);
         constexpr int GT = 32 * kCkDq, CPR = D / 8, RPT = kCkKeys * CPR / GT;   // threads, 16-byte chunks a row, a thread's share
         const int lgG = __ffs(g.G) - 1;
+        if (a.quit < INT_MAX && w > 0) ok = false;   // (as if a wait had run out)
         int tiles = 0, kin = 0, meets = 0;   // kin: the current tile's K^ is told of
         CkRing t, r;
         // the dequantizing warps meet (a bounded wait, unlike a named barrier)
@@ -358,10 +361,6 @@ __global__ void __launch_bounds__(kCkThreads, 1)
             const __half *kwin = dv.Kf + kf_slice(g, sg.i, sg.j), *vwin = dv.Vf + vf_slice(g, sg.i, sg.j);
             const size_t chunk0 = ((size_t)sg.i * g.h + sg.j) * a.n_stride;   // the chunk's first row in K and V
             const int npk = max(0, min(sg.nx, sg.bl.virt(min(Tqk, Tqv) / kCkKeys) - sg.x0));   // fully quantized tiles
-            if (tiles >= a.stop && w > 0) {   // (as if a wait had run out)
-                ok = false;
-                break;
-            }
             if (g.kbits == 2)
                 ok = g.vbits == 2 ? packed_tiles<D, 2, 2>(npk, tiles, t, r, sK, sV, sR, g, a.rs, w, bK, eK, bV, eV, bR, eR, abort)
                                   : packed_tiles<D, 2, 4>(npk, tiles, t, r, sK, sV, sR, g, a.rs, w, bK, eK, bV, eV, bR, eR, abort);

@@ -462,7 +462,7 @@ __global__ void __launch_bounds__(kFwThreads, 1)
                 const int n = raw_blocks(max(a.Tqk[sg.i], a.Tqv[sg.i]));
                 const unsigned char *recs = dv.blk + rec_off(g, sg.i, sg.j, 0);
                 for (int y = 0; y < n; ++y, ++issued, r.next(a.rs)) {
-                    ok = issued < a.rs || mbar_wait_ab(&eR[r.s], r.p ^ 1u, abort);
+                    ok = (issued < a.rs || mbar_wait_ab(&eR[r.s], r.p ^ 1u, abort)) && issued < a.quit;
                     if (!ok) break;
                     mbar_expect_tx(&bR[r.s], (unsigned)g.rec_bytes);
                     bulk_g2s(sR + (size_t)r.s * g.rec_bytes, recs + (size_t)sg.bl.phys(2 * sg.x0 + y) * g.rec_bytes,
@@ -494,8 +494,7 @@ __global__ void __launch_bounds__(kFwThreads, 1)
             int blk = (w - 2 * tiles) & (kFwDq - 1);   // the segment's first block of this warp
             CkRing r = seg;
             r.skip(blk, a.rs);
-            if (tiles >= a.stop && warp > WD) ok = false;   // (as if a wait had run out)
-            for (; ok && blk < 2 * sg.nx; blk += kFwDq, r.skip(kFwDq, a.rs)) {
+            for (; blk < 2 * sg.nx; blk += kFwDq, r.skip(kFwDq, a.rs)) {
                 const int y = tiles + (blk >> 1), st = y % KS, half = blk & 1;
                 const bool raw = blk < nraw;
                 const unsigned char *rp = sR + (size_t)r.s * g.rec_bytes;
