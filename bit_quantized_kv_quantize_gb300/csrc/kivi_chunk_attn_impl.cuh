@@ -17,17 +17,17 @@
 // K^ and V^ round once to fp16 (2^-11 relative a value, as the weights P
 // do): the two-term operands that the one-token decode uses would double the
 // MMAs, and the errors of the rounded values are independent, so they
-// average like the values themselves (relative L2 error 3e-4 on even keys,
-// up to 1.2e-3 where keys have channels 8 times the others; an fp16 output
-// alone rounds by 2e-4).
+// average like the values themselves (relative L2 error 3.6e-4 on even keys,
+// 5e-4 to 1.2e-3 where keys have channels 8 times the others; an fp16 output
+// alone rounds by 2.1e-4).
 //
 // Bound: the tensor cores, where the rows are many.  A tile's MMAs take 1280
 // cycles (M 128 x N 64 x K 16 from shared memory 49, N 128 from tensor memory
 // 65); the loop takes 2000 without the restoring and 2250 with it: the
 // dequantizing warps' stores and the MMAs' operand reads share shared memory.
-// Measured: 2048 tokens of 32 / 8 heads over 16.5k 2-bit tokens 499 us (1.18
-// PFLOP/s; 303 us at the cuBLAS rate), 200 tokens 89 us, 16 tokens of 8
-// sequences over 32k 211 us; a prompt of 8191 tokens, window 2048, 32 / 8
+// Measured: 2048 tokens of 32 / 8 heads over 16.5k 2-bit tokens 515 us (1.14
+// PFLOP/s; 303 us at the cuBLAS rate), 200 tokens 93 us, 16 tokens of 8
+// sequences over 32k 215 us; a prompt of 8191 tokens, window 2048, 32 / 8
 // heads, 279 us beside 32 us of packing, one of 4096, window 1024, 32 heads,
 // 116 beside 45.
 //

@@ -4,16 +4,16 @@
 //
 // With 128 query rows on the MMA's M side, a few rows leave most of the tensor
 // cores' and the softmax's work padding, and four warps that restore each
-// tile between them set its time however few the rows (211 us where this
-// kernel takes 149).  Here the tokens are on the M side and up to 16 rows
+// tile between them set its time however few the rows (215 us where this
+// kernel takes 148).  Here the tokens are on the M side and up to 16 rows
 // on N:
 //   S^T [128 tokens x N] = K^ Q^T,   O^T [d x N] += V^^T P^T,
 // so a tile of 128 tokens costs 16 MMAs of N columns, thread t of the softmax
 // owns token t and computes N weights, and what remains is restoring the
 // tile: the kernel is bound by the dequantizing warps' instructions (4.5 a
-// pair of values; the SMs issue in 47 % of their cycles, HBM is at 20 %).
+// pair of values; the SMs issue in 47 % of their cycles, HBM is at 19 %).
 // Measured over 32k 2-bit tokens of 8 sequences of 8 heads (204 MB, 30 us at
-// the copy rate), joining included: 149 us; over 2000 tokens 30 us.  (N = 32,
+// the copy rate), joining included: 148 us; over 2000 tokens 30 us.  (N = 32,
 // for 32 rows: 190 us over 32k, 226 where 256-row tiles take 206 over 8k tokens
 // of 32 sequences.)
 //
