@@ -73,14 +73,7 @@ __device__ __forceinline__ void bulk_g2s(void *dst, const void *src, unsigned by
 __device__ __forceinline__ bool mbar_wait_ab(uint64_t *bar, unsigned phase, const volatile int *abort) {
 #pragma unroll 1   // (short code: the kernels wait in many places)
     for (int it = 0; it < kMaxWaitIters; ++it) {
-        unsigned ok;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(smem_u32(bar)), "r"(phase)
-            : "memory");
-        if (ok) return true;
+        if (mbar_try_wait(bar, phase)) return true;
         if ((it & 255) == 255 && *abort) return false;
     }
     return false;
