@@ -8,7 +8,7 @@ H = 2.0 ** -11   # half a step of fp16, relative
 F = 2.0 ** -25   # ... in its subnormals
 
 
-def attend(q, k, v, see):
+def attend(q, k, v, see, restored=True):
     """Rows q [n, d] over k, v [S, d] in 64 bits: the output [n, d], the error's
     bound of each element and its expected square.
 
@@ -23,7 +23,10 @@ def attend(q, k, v, see):
     Expected square.  The roundings of different keys, weights and values are
     independent, each uniform within half a step at most, so of variance at
     most H^2 / 3 relative: a score's variance is sum (q k)^2 / d times that,
-    and it moves the output by w (v - out)."""
+    and it moves the output by w (v - out).
+
+    restored: False where keys and values are fp16 as they come: they are not
+    rounded then."""
     q, k, v = (x.astype(np.float64) for x in (q, k, v))
     d, S = q.shape[1], k.shape[0]
     x = np.where(see, q @ k.T / np.sqrt(d), -np.inf)
@@ -32,13 +35,15 @@ def attend(q, k, v, see):
     w /= L
     out, wabs = w @ v, w @ np.abs(v)
     e = np.where(see, (H * np.abs(q) @ np.abs(k).T + F * np.abs(q).sum(1, keepdims=True)) / np.sqrt(d), 0).max(1, keepdims=True)
-    bound = (wabs * (np.expm1(2 * e) + 2 * H + 2.0 ** -19 + S * 2.0 ** -23) + H * np.abs(out) +
+    if not restored:
+        e = e * 0
+    bound = (wabs * (np.expm1(2 * e) + (1 + restored) * H + 2.0 ** -19 + S * 2.0 ** -23) + H * np.abs(out) +
              2.0 ** -32 * (see @ np.abs(v)) / L + 2 * F)
     u = H * H / 3
     w2, s2 = w * w, np.where(see, (q * q) @ (k * k).T / d, 0) * u
     ws = w2 * s2   # sum_s w^2 var (v - out)^2, expanded
     moved = ws @ (v * v) - 2 * out * (ws @ v) + out * out * ws.sum(1, keepdims=True)
-    return out, bound, moved + 2 * u * (w2 @ (v * v)) + u * out * out
+    return out, bound, moved * restored + (1 + restored) * u * (w2 @ (v * v)) + u * out * out
 
 
 def check(got, want, what=""):
