@@ -21,10 +21,12 @@ SOURCES = ["kivi_api.cu", "kivi_pack.cu", "kivi_decode.cu", "kivi_decode_d64.cu"
            "kivi_decode_fused_d128.cu", "kivi_decode_fused_d256.cu", "kivi_probs.cu", "kivi_noalloc.cu",
            "kivi_prefill_attn.cu", "kivi_decode_win_d64.cu", "kivi_decode_win_d128.cu",
            "kivi_decode_win_d256.cu", "kivi_chunk_attn.cu", "kivi_chunk_few.cu", "kivi_chunk_append.cu",
-           "kivi_rope.cu"]
+           "kivi_rope.cu", "kivi_verify.cu", "kivi_latent.cu", "kivi_latent_attn.cu", "kivi_head_product.cu",
+           "kivi_latent_prompt.cu"]
 HEADERS = ["kivi_internal.cuh", "kivi_decode_impl.cuh", "kivi_pack_impl.cuh", "kivi_append_impl.cuh",
            "kivi_mma.cuh", "kivi_tcgen05.cuh", "kivi_async.cuh", "kivi_unpack.cuh", "kivi_tma.cuh",
-           "kivi_chunk.cuh", "kivi_chunk_tiles.cuh", "kivi_chunk_attn_impl.cuh", "kivi_chunk_few_impl.cuh"]
+           "kivi_chunk.cuh", "kivi_chunk_tiles.cuh", "kivi_chunk_attn_impl.cuh", "kivi_chunk_few_impl.cuh",
+           "kivi_latent.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 # IEEE division and rounding stay exact: no --use_fast_math anywhere.
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",

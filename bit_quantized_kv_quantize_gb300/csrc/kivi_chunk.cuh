@@ -16,7 +16,7 @@ struct ChunkPos {
 };
 struct ChunkArgs {
     int hq, hg, n_stride;         // hg: query heads a kv head
-    unsigned hg_mul;              // ceil(2^32 / hg): x / hg = umulhi(x, hg_mul) for x < 2^29 (hg <= 8)
+    unsigned hg_mul;              // ceil(2^32 / hg): x / hg = umulhi(x, hg_mul) for x < 2^32 / hg
     int rs;           // record stages
     int tile_rows, tile_blocks;   // rows of a row tile, 64-token blocks of a key tile
     Visible vis;
@@ -64,6 +64,11 @@ __host__ __device__ __forceinline__ int chunk_tqv(int T, int Tqv, int n, int R) 
     return n > 0 && f > Tqv ? f : Tqv;
 }
 
+// Lays out the work list of the row tiles (a: hg, tile_rows, tile_blocks, vis,
+// T and n) of b sequences of h kv heads for up to num_sms CTAs: a.cta, the CTAs,
+// and whether a row tile is cut between them.  least: units below which a share
+// is not cut.  False if a share would pass 32 bits.  (kivi_chunk_attn.cu)
+bool kivi_plan_units(int b, int h, ChunkArgs &a, int num_sms, int least, int *ctas, bool *join);
 // How a chunk's attention runs.
 struct ChunkPlan {
     bool few;   // the kernel for few rows

@@ -1,0 +1,271 @@
+// kivi_head_product.cu -- a matrix of each head times rows of that head (or of
+// all heads alike), on the 5th-generation tensor cores, and the entry point
+// kivi_head_product: what latent attention does before and after itself.
+//
+// Mathematics.  out[i][e][s][:] = W_e x[i][e or 0][s][:] for head e and the
+// tokens s < n[i] of sequence i, W_e [N][K] or, transposed, given as [K][N].
+//   absorbing a query   qn [128] -> Wk_e^T qn [r]     K = 128, N = r, transposed
+//   expanding a latent  c [r] -> Wk_e c, Wv_e c       K = r, N = 128, x of all heads
+//   a head's output     ol [r] -> Wv_e ol             K = r, N = 128
+//
+// The rows of all sequences are one list (prefix sums of n), cut into tiles of
+// 128, so that a step of 64 sequences of one token fills half a tile a head. A
+// CTA makes 128 rows x 128 columns of one head: S = x W^T in tensor memory, 64
+// of K a stage; x by 16-byte asynchronous copies (any row of any sequence), W by
+// TMA as the operand lies in memory, K-major or N-major.  Two CTAs an SM, so
+// that one's first loads and last stores run under the other's products.
+#include <cstring>
+
+#include "../../include/kivi.h"
+#include "kivi_async.cuh"
+#include "kivi_latent.cuh"
+#include "kivi_mma.cuh"
+#include "kivi_tcgen05.cuh"
+#include "kivi_tma.cuh"
+
+namespace {
+
+constexpr int kHpRows = 128, kHpCols = 128, kHpK = 64;
+constexpr int kHpStages = 3;
+constexpr int kHpThreads = 32 * 6;
+constexpr unsigned kHpFull = 0xffffffffu;
+// bytes from a 16-byte chunk of x's tile to the next: 64 more than 128 rows
+// take, so that a store of 4 rows x 2 chunks meets every bank once
+constexpr unsigned kHpAS = kHpRows * 16 + 64;
+constexpr int kHpA = kHpK / 8 * (int)kHpAS, kHpB = kHpK * kHpCols * 2;
+constexpr size_t kHpSmem = (size_t)kHpStages * (kHpA + kHpB) + 128;
+
+struct HeadArgs {
+    const __half *x;
+    __half *out;
+    int b, hx, h, n_stride, K, N;
+    int first[KIVI_MAX_BATCH + 1];   // rows before sequence i
+    unsigned *status;
+};
+
+__device__ __forceinline__ void hp_copy16(void *dst, const void *src, bool in) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(in ? 16 : 0)
+                 : "memory");
+}
+// sequence and token of row `row` of the list
+__device__ __forceinline__ int2 hp_row(const HeadArgs &a, int row) {
+    int lo = 0, hi = a.b;   // first[lo] <= row < first[hi]
+    while (hi - lo > 1) {
+        const int m = (lo + hi) >> 1;
+        if (a.first[m] <= row) lo = m;
+        else hi = m;
+    }
+    return make_int2(lo, row - a.first[lo]);
+}
+
+// Warps 0-3: x's tiles, then the output; 4: W's tiles; 5: the products.
+template <bool MN>
+__global__ void __launch_bounds__(kHpThreads, 2)
+    head_product_kernel(const __grid_constant__ HeadArgs a, const __grid_constant__ CUtensorMap tm) {
+    extern __shared__ unsigned char raw[];
+    unsigned char *sA = raw + ((128u - (smem_u32(raw) & 127u)) & 127u), *sB = sA + kHpStages * kHpA;
+    __shared__ __align__(8) uint64_t bars[3 * kHpStages + 1];
+    uint64_t *const bA = bars, *const bB = bA + kHpStages, *const eS = bB + kHpStages, *const bD = eS + kHpStages;
+    __shared__ uint32_t s_taddr;
+    __shared__ int s_abort;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int row0 = blockIdx.x * kHpRows, col0 = blockIdx.y * kHpCols, e = blockIdx.z;
+    const int rows = a.first[a.b], nk = a.K / kHpK;
+    if (tid < 3 * kHpStages + 1) {
+        mbar_init(&bars[tid], tid < kHpStages ? 4 : 1);
+        fence_mbar_init();
+    }
+    if (tid == 0) s_abort = 0;
+    if (warp == 0) tc_alloc(&s_taddr, kHpCols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t taddr = s_taddr;
+    const volatile int *abort = &s_abort;
+    bool ok = true;
+
+    if (warp < 4) {
+        // x: a thread's two rows, a 16-byte chunk of every two
+        const __half *src[2];
+        bool in[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int row = row0 + (tid >> 1) + 64 * k;
+            in[k] = row < rows;
+            const int2 p = hp_row(a, in[k] ? row : row0);
+            src[k] = a.x + (((size_t)p.x * a.hx + (a.hx > 1 ? e : 0)) * a.n_stride + p.y) * a.K + 8 * (tid & 1);
+        }
+        auto told = [&](int it) {   // the stage's copies of this warp are in
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bA[it % kHpStages]);
+        };
+        for (int it = 0; it < nk && ok; ++it) {
+            const int s = it % kHpStages;
+            ok = __all_sync(kHpFull, it < kHpStages || mbar_wait_ab(&eS[s], (unsigned)(it / kHpStages + 1) & 1u, abort));
+            if (!ok) break;
+            unsigned char *dst = sA + s * kHpA + (tid & 1) * kHpAS + (tid >> 1) * 16;
+#pragma unroll
+            for (int c = 0; c < kHpK / 16; ++c)
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    hp_copy16(dst + 2 * c * kHpAS + k * 64 * 16, src[k] + it * kHpK + 16 * c, in[k]);
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            if (it > 0) {
+                asm volatile("cp.async.wait_group 1;" ::: "memory");
+                told(it - 1);
+            }
+        }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        if (ok) told(nk - 1);
+        ok = ok && __all_sync(kHpFull, mbar_wait_ab(bD, 0u, abort));
+        if (ok) {
+            tc_fence_after();
+            const int row = row0 + tid;
+            const int2 p = hp_row(a, row < rows ? row : row0);
+            __half *dst = a.out + (((size_t)p.x * a.h + e) * a.n_stride + p.y) * a.N + col0;
+#pragma unroll 1
+            for (int c0 = 0; c0 < kHpCols; c0 += 32) {
+                uint32_t o[32];
+                tc_ld32(taddr + ((uint32_t)(32 * warp) << 16) + c0, o);
+                tc_wait_ld();
+                if (row < rows)
+#pragma unroll
+                    for (int c = 0; c < 32; c += 8) {
+                        uint32_t v[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            v[k] = h2u(__floats2half2_rn(__uint_as_float(o[c + 2 * k]), __uint_as_float(o[c + 2 * k + 1])));
+                        *reinterpret_cast<uint4 *>(dst + c0 + c) = make_uint4(v[0], v[1], v[2], v[3]);
+                    }
+            }
+            tc_fence_before();
+        }
+        if (!ok && lane == 0) {
+            s_abort = 1;
+            atomicOr(a.status, KIVI_FLAG_WAIT);
+        }
+        __syncwarp();
+    } else if (warp == 4) {
+        if (lane == 0) {
+            int it = 0;
+            for (; it < nk; ++it) {
+                const int s = it % kHpStages;
+                ok = it < kHpStages || mbar_wait_ab(&eS[s], (unsigned)(it / kHpStages + 1) & 1u, abort);
+                if (!ok) break;
+                mbar_expect_tx(&bB[s], kHpB);
+                const int r = MN ? e * a.K + it * kHpK : e * a.N + col0, c = (MN ? col0 : it * kHpK) / 8;
+                asm volatile(
+                    "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, "
+                    "{%2, %3, %4}], [%5];" ::"r"(smem_u32(sB + s * kHpB)),
+                    "l"(&tm), "r"(0), "r"(r), "r"(c), "r"(smem_u32(&bB[s]))
+                    : "memory");
+            }
+            if (!ok) {
+                s_abort = 1;
+                atomicOr(a.status, KIVI_FLAG_WAIT);
+            }
+            // every copy has landed before shared memory is given up (bounded)
+            for (int y = max(0, it - kHpStages); y < it; ++y) mbar_wait(&bB[y % kHpStages], (unsigned)(y / kHpStages) & 1u);
+        }
+        __syncwarp();
+    } else {
+        constexpr uint32_t ID = tc_idesc_f16(kHpRows, kHpCols, MN ? 1 : 0);
+        const uint64_t da = tc_desc(sA, kHpAS, 128),
+                       db = MN ? tc_desc(sB, 128, kHpK * 16) : tc_desc(sB, kHpCols * 16, 128);
+        int it = 0;
+        for (; it < nk; ++it) {
+            const int s = it % kHpStages;
+            const unsigned ph = (unsigned)(it / kHpStages) & 1u;
+            ok = __all_sync(kHpFull, mbar_wait_ab(&bA[s], ph, abort) && mbar_wait_ab(&bB[s], ph, abort));
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < kHpK / 16; ++c)
+                tc_mma_f16_w(taddr, da + (uint32_t)((s * kHpA + 2 * c * kHpAS) >> 4),
+                             db + (uint32_t)((s * kHpB + (MN ? 256 * c : 2 * c * kHpCols * 16)) >> 4), ID, it > 0 || c > 0);
+            tc_commit_w(&eS[s]);
+        }
+        if (!ok && lane == 0) {
+            s_abort = 1;
+            atomicOr(a.status, KIVI_FLAG_WAIT);
+        }
+        // every product and commit is done before memory is given up (bounded)
+        tc_commit_w(bD);
+        for (int y = max(0, it - kHpStages); y < it; ++y) mbar_wait(&eS[y % kHpStages], (unsigned)(y / kHpStages) & 1u);
+        mbar_wait(bD, 0u);
+        __syncwarp();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) tc_dealloc(taddr, kHpCols);
+}
+
+// Tensor map over fp16 [rows][cols] whose boxes are box_rows rows x box_chunks
+// 16-byte chunks, chunk-major.
+cudaError_t make_box_map(CUtensorMap *tm, const __half *base, long long rows, int cols, int box_rows, int box_chunks) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (!enc) return cudaErrorNotSupported;
+    const cuuint64_t dim[3] = {8, (cuuint64_t)rows, (cuuint64_t)(cols / 8)};
+    const cuuint64_t str[2] = {(cuuint64_t)cols * 2, 16};
+    const cuuint32_t box[3] = {8, (cuuint32_t)box_rows, (cuuint32_t)box_chunks};
+    const cuuint32_t es[3] = {1, 1, 1};
+    const CUresult r = enc(tm, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<__half *>(base), dim, str, box, es,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+kivi_status fail(kivi_status s, const char *msg) {
+    kivi_set_last_error(msg);
+    return s;
+}
+
+}  // namespace
+
+extern "C" kivi_status kivi_head_product(const void *x, const void *w, int b, int h_x, int h, int n_stride,
+                                         const int32_t *n, int K, int N, int transposed, void *out,
+                                         kivi_stream_t stream) {
+    kivi_set_last_error("");
+    if (b < 1 || h < 1 || n_stride < 0 || K < 1 || N < 1) return fail(KIVI_ERR_INVALID_ARG, "sizes must be positive");
+    if (h_x != 1 && h_x != h) return fail(KIVI_ERR_INVALID_ARG, "h_x must be 1 or h");
+    if (b > KIVI_MAX_BATCH) return fail(KIVI_ERR_UNSUPPORTED, "b above 1024");
+    if (h > 1024) return fail(KIVI_ERR_UNSUPPORTED, "more than 1024 heads");
+    if (K % kHpK != 0 || N % kHpCols != 0 || K > 16384 || N > 16384)
+        return fail(KIVI_ERR_UNSUPPORTED, "K must be a multiple of 64 and N of 128, at most 16384");
+    if (!n) return fail(KIVI_ERR_INVALID_ARG, "n is null");
+    HeadArgs a;
+    long long rows = 0;
+    for (int i = 0; i < b; ++i) {
+        if (n[i] < 0 || n[i] > n_stride) return fail(KIVI_ERR_INVALID_ARG, "n[i] outside [0, n_stride]");
+        a.first[i] = (int)rows;
+        rows += n[i];
+        if (rows > (1LL << 30)) return fail(KIVI_ERR_UNSUPPORTED, "more than 2^30 tokens");
+    }
+    a.first[b] = (int)rows;
+    if (rows == 0) return KIVI_OK;
+    if (!x || !w || !out) return fail(KIVI_ERR_INVALID_ARG, "a tensor pointer is null");
+    if (((uintptr_t)x | (uintptr_t)w | (uintptr_t)out) & 15u)
+        return fail(KIVI_ERR_INVALID_ARG, "x, w and out must be 16-byte aligned");
+    a.x = (const __half *)x;
+    a.out = (__half *)out;
+    a.b = b;
+    a.hx = h_x;
+    a.h = h;
+    a.n_stride = n_stride;
+    a.K = K;
+    a.N = N;
+    a.status = kivi_device_status();
+    if (!a.status) return fail(KIVI_ERR_CUDA, "no status word on the current device");
+    const bool mn = transposed != 0;
+    CUtensorMap tm;
+    cudaError_t e = mn ? make_box_map(&tm, (const __half *)w, (long long)h * K, N, kHpK, kHpCols / 8)
+                       : make_box_map(&tm, (const __half *)w, (long long)h * N, K, kHpCols, kHpK / 8);
+    const auto kernel = mn ? head_product_kernel<true> : head_product_kernel<false>;
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kHpSmem);
+    if (e != cudaSuccess) return fail(KIVI_ERR_CUDA, cudaGetErrorString(e));
+    const dim3 grid((unsigned)((rows + kHpRows - 1) / kHpRows), (unsigned)(N / kHpCols), (unsigned)h);
+    kernel<<<grid, kHpThreads, kHpSmem, (cudaStream_t)stream>>>(a, tm);
+    e = cudaGetLastError();
+    return e == cudaSuccess ? KIVI_OK : fail(KIVI_ERR_CUDA, cudaGetErrorString(e));
+}

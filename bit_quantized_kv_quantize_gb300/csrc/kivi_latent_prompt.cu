@@ -1,0 +1,399 @@
+// kivi_latent_prompt.cu -- latent attention in its expanded form: the causal
+// attention of a prompt whose heads' keys and values have been formed, on the
+// 5th-generation tensor cores, and the entry point kivi_latent_prompt_attn.
+//
+// Mathematics.  Token s of head e has the key [k_s ; kr_s] (128 channels of its
+// own, 64 rotary ones that all heads share) and the value v_s [128]:
+//   out_p = sum_{s <= p} softmax_s(scale (qn_p . k_s + qr_p . kr_s)) v_s.
+// 640 operations a (row, token) where the absorbed form takes 2 (2 r + 64):
+// 3.4 times fewer at r = 512, which pays for forming the keys and values as soon
+// as more than a few hundred rows share them.
+//
+// A CTA takes 256 rows (two slots of 128) of one head and walks the 64-token
+// tiles up to its last row; S = Q K^T is 192 deep, the rotary keys' tile beside
+// the head's in shared memory.  S, the weights and O stay in tensor memory, a
+// thread a row; the two slots' softmax and products overlap.  Blocks with the
+// most tiles are launched first.
+#include <climits>
+#include <cstring>
+
+#include "../../include/kivi.h"
+#include "kivi_chunk_tiles.cuh"
+#include "kivi_latent.cuh"
+#include "kivi_tcgen05.cuh"
+#include "kivi_tma.cuh"
+
+namespace {
+
+constexpr int kLpRows = 128, kLpKeys = KIVI_KBLK, kLpStages = 3;
+constexpr int kLpQK = kLatHead + kLatRope;
+constexpr int kLpThreads = 32 * 12;
+constexpr int kLpQ = kLpRows * kLpQK * 2, kLpK = kLpKeys * kLpQK * 2, kLpV = kLpKeys * kLatHead * 2;
+constexpr size_t kLpSmem = (size_t)2 * kLpQ + (size_t)kLpStages * (kLpK + kLpV);
+
+struct PromptArgs {
+    __half *out;
+    int b, h, t_stride, mt;   // mt: row tiles of the longest sequence
+    float sl2;                // scale log2(e)
+    unsigned *status;
+    int t[KIVI_MAX_BATCH];
+};
+
+__device__ __forceinline__ unsigned long long lp_f2(float a, float b) {
+    unsigned long long r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void lp_f2(unsigned long long v, float &a, float &b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ unsigned long long lp_fma2(unsigned long long a, unsigned long long b, unsigned long long c) {
+    unsigned long long r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ unsigned long long lp_add2(unsigned long long a, unsigned long long b) {
+    unsigned long long r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// Warps 0-7: softmax and output (thread tid owns row tid mod 128 of slot tid /
+// 128; tensor-memory columns [256 slot, + 256): S in 0-63, weights from 64 and
+// 96, O from 128); 8, 9: S of a slot; 10: O += P V; 11: copies.
+__global__ void __launch_bounds__(kLpThreads, 1)
+    latent_prompt_kernel(const __grid_constant__ CUtensorMap tmQn, const __grid_constant__ CUtensorMap tmQr,
+                         const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmKr,
+                         const __grid_constant__ CUtensorMap tmV, const __grid_constant__ PromptArgs a) {
+    extern __shared__ __align__(128) unsigned char smem[];
+    constexpr int KS = kLpStages;
+    constexpr unsigned QLBO = kLpRows * 16, KLBO = kLpKeys * 16;
+    const int bh = a.b * a.h, pair = blockIdx.x % bh, m = a.mt - 1 - blockIdx.x / bh, i = pair / a.h;
+    const int n = a.t[i], row0 = m * 2 * kLpRows;
+    if (row0 >= n) return;
+    unsigned char *sQ = smem, *sK = sQ + 2 * kLpQ, *sV = sK + KS * kLpK;
+    // counts 4 (a slot's softmax warps): P [slot][buffer], scores read [slot]; 2
+    // (both slots): K tiles read; 1: the others
+    constexpr int N4 = 6, N2 = N4 + KS, NB = N2 + 2 + 2 + 4 + 3 + 3 * KS + 1;
+    __shared__ __align__(8) uint64_t bars[NB];
+    uint64_t *const bP = bars, *const bL = bars + 4, *const eK = bars + N4, *const bQ = bars + N2, *const bS = bQ + 2,
+                    *const bF = bS + 2, *const bE = bF + 4, *const bK = bE + 3, *const bV = bK + KS, *const eV = bV + KS,
+                    *const bT = eV + KS;
+    __shared__ uint32_t s_taddr;
+    __shared__ int s_abort;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid < NB) {
+        mbar_init(&bars[tid], tid < N4 ? 4 : tid < N2 ? 2 : 1);
+        fence_mbar_init();
+    }
+    if (tid == 0) s_abort = 0;
+    if (warp == 0) tc_alloc(&s_taddr, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t taddr = s_taddr;
+    const volatile int *abort = &s_abort;
+    bool ok = true;
+    // tiles that each slot sees (none: a slot without rows)
+    const int last1 = min(row0 + 2 * kLpRows, n) - 1, last0 = min(row0 + kLpRows, n) - 1;
+    const int nx0 = last0 / kLpKeys + 1, nx1 = n > row0 + kLpRows ? last1 / kLpKeys + 1 : 0;
+    const int nx = max(nx0, nx1);
+
+    if (warp == 8 || warp == 9) {
+        // ---- S = Q K^T of slot e ----
+        const int e = __shfl_sync(kFull, warp - 8, 0), mine = e ? nx1 : nx0;
+        constexpr uint32_t ID = tc_idesc_f16(kLpRows, kLpKeys, 0);
+        CkRing t;
+        const uint64_t dq = tc_desc(sQ + e * kLpQ, QLBO, 128), dk = tc_desc(sK, KLBO, 128);
+        for (int x = 0; x < nx && ok; ++x, t.next(KS)) {
+            ok = __all_sync(kFull, mbar_wait_ab(&bK[t.s], t.p, abort));
+            if (!ok) break;
+            if (x >= mine) {   // this slot sees none of the tile: it releases it, once it is in (a phase an arrival)
+                if (lane == 0) mbar_arrive(&eK[t.s]);
+                continue;
+            }
+            ok = (x > 0 || mbar_wait_ab(&bQ[e], 0u, abort)) && (x == 0 || mbar_wait_ab(&bL[e], (unsigned)(x - 1) & 1u, abort));
+            ok = __all_sync(kFull, ok);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t d = dk + (uint32_t)(t.s * (kLpK >> 4));
+#pragma unroll
+            for (int c = 0; c < kLpQK / 16; ++c)
+                tc_mma_f16_w(taddr + 256 * e, dq + ((2 * c * QLBO) >> 4), d + ((2 * c * KLBO) >> 4), ID, c > 0);
+            tc_commit_w(&bS[e]);
+            tc_commit_w(&eK[t.s]);
+        }
+        if (!ok && lane == 0) {
+            s_abort = 1;
+            atomicOr(a.status, KIVI_FLAG_WAIT);
+        }
+        // every MMA and commit has landed before shared memory is given up (bounded)
+        tc_commit_w(&bE[e]);
+        mbar_wait(&bE[e], 0u);
+        __syncwarp();
+    } else if (warp == 10) {
+        // ---- O += P V ----
+        constexpr uint32_t ID = tc_idesc_f16(kLpRows, kLatHead, 1);
+        CkRing t;
+        const uint64_t dv = tc_desc(sV, 128, KLBO);
+        for (int x = 0; x < nx && ok; ++x, t.next(KS)) {
+            const uint64_t d = dv + (uint32_t)(t.s * (kLpV >> 4));
+            ok = __all_sync(kFull, mbar_wait_ab(&bV[t.s], t.p, abort));
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                if (!ok || x >= (e ? nx1 : nx0)) continue;
+                const int b = x & 1;
+                ok = __all_sync(kFull, mbar_wait_ab(&bP[2 * e + b], (unsigned)(x >> 1) & 1u, abort));
+                if (!ok) continue;
+                tc_fence_after();
+#pragma unroll
+                for (int c = 0; c < kLpKeys / 16; ++c)
+                    tc_mma_f16_ta_w(taddr + 256 * e + 128, taddr + 256 * e + 64 + 32 * b + 8 * c, d + ((256 * c) >> 4), ID,
+                                    x > 0 || c > 0);
+                tc_commit_w(&bF[2 * e + b]);
+            }
+            if (ok) tc_commit_w(&eV[t.s]);
+        }
+        if (!ok && lane == 0) {
+            s_abort = 1;
+            atomicOr(a.status, KIVI_FLAG_WAIT);
+        }
+        tc_commit_w(&bE[2]);
+        mbar_wait(&bE[2], 0u);
+        __syncwarp();
+    } else if (warp == 11) {
+        // ---- copies ----
+        const int q0 = pair * a.t_stride;   // the head's first row
+        if (lane == 0)
+            for (int e = 0; e < 2; ++e) {
+                if (e && nx1 == 0) break;
+                mbar_expect_tx(&bQ[e], kLpQ);
+                tma_box(sQ + e * kLpQ, &tmQn, q0 + row0 + e * kLpRows, &bQ[e]);
+                tma_box(sQ + e * kLpQ + kLatHead / 8 * QLBO, &tmQr, q0 + row0 + e * kLpRows, &bQ[e]);
+            }
+        __syncwarp();
+        CkRing t;
+        int ck = 0, cv = 0;   // tiles asked for
+        for (int x = 0; x < nx && ok; ++x, t.next(KS)) {
+            const int tb = x * kLpKeys;
+            if (lane == 0) {
+                ok = x < KS || mbar_wait_ab(&eK[t.s], t.p ^ 1u, abort);
+                if (ok) {
+                    mbar_expect_tx(&bK[t.s], kLpK);
+                    tma_box(sK + t.s * kLpK, &tmK, q0 + tb, &bK[t.s]);
+                    tma_box(sK + t.s * kLpK + kLatHead / 8 * KLBO, &tmKr, i * a.t_stride + tb, &bK[t.s]);
+                    ++ck;
+                    ok = x < KS || mbar_wait_ab(&eV[t.s], t.p ^ 1u, abort);
+                }
+                if (ok) {
+                    // (the last tile's rows behind the sequence are zeroed first)
+                    uint64_t *const bar = tb + kLpKeys > n ? bT : &bV[t.s];
+                    mbar_expect_tx(bar, kLpV);
+                    tma_box(sV + t.s * kLpV, &tmV, q0 + tb, bar);
+                    ++cv;
+                }
+            }
+            ok = __all_sync(kFull, ok);
+            if (ok && tb + kLpKeys > n) {
+                ok = __all_sync(kFull, mbar_wait_ab(bT, 0u, abort));
+                if (ok) {
+                    const int rows = tb + kLpKeys - n;
+                    for (int y = lane; y < rows * (kLatHead / 8); y += 32)
+                        *reinterpret_cast<uint4 *>(sV + t.s * kLpV + (y / rows) * KLBO + (n - tb + y % rows) * 16) =
+                            make_uint4(0u, 0u, 0u, 0u);
+                    fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bV[t.s]);
+                }
+            }
+        }
+        if (lane == 0) {
+            if (!ok) {
+                s_abort = 1;
+                atomicOr(a.status, KIVI_FLAG_WAIT);
+            }
+            // every copy has landed before shared memory is given up (bounded)
+            mbar_wait(&bQ[0], 0u);
+            if (nx1) mbar_wait(&bQ[1], 0u);
+            for (int y = max(0, ck - KS); y < ck; ++y) mbar_wait(&bK[y % KS], (unsigned)(y / KS) & 1u);
+            for (int y = max(0, cv - KS); y < cv; ++y)
+                mbar_wait(y * kLpKeys + kLpKeys > n ? bT : &bV[y % KS], y * kLpKeys + kLpKeys > n ? 0u : (unsigned)(y / KS) & 1u);
+        }
+        __syncwarp();
+    } else {
+        // ---- softmax ----
+        const int slot = tid / kLpRows, srow = row0 + slot * kLpRows, pos = srow + tid % kLpRows;
+        const int mine = slot ? nx1 : nx0;
+        const uint32_t tS = taddr + 256 * slot + ((uint32_t)(32 * (warp & 3)) << 16), tO = tS + 128;
+        float ref = -INFINITY, lsum = 0.f;   // the row's reference less the lift (log2; -inf: nothing yet), the weights' sum
+        for (int x = 0; x < mine; ++x) {
+            const int b = x & 1, key0 = x * kLpKeys;
+            ok = __all_sync(kFull, mbar_wait_ab(&bS[slot], (unsigned)x & 1u, abort));
+            if (!ok) break;
+            tc_fence_after();
+            uint32_t r[2][32];
+            tc_ld32(tS, r[0]);
+            tc_ld32(tS + 32, r[1]);
+            tc_wait_ld();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bL[slot]);
+            const bool pf = x < 2 || mbar_test(&bF[2 * slot + b], (unsigned)((x >> 1) + 1) & 1u);
+            if (key0 + kLpKeys - 1 > srow) {   // some row of the slot does not see the whole tile
+                const uint32_t h0 = ck_above(pos - key0), h1 = ck_above(pos - key0 - 32);
+#pragma unroll
+                for (int c = 0; c < 32; ++c) {
+                    if ((h0 >> c) & 1u) r[0][c] = 0xff800000u;
+                    if ((h1 >> c) & 1u) r[1][c] = 0xff800000u;
+                }
+            }
+            float m8[8];
+#pragma unroll
+            for (int c = 0; c < 8; ++c) m8[c] = __uint_as_float(r[0][c]);
+#pragma unroll
+            for (int c = 8; c < 64; ++c) m8[c & 7] = fmaxf(m8[c & 7], __uint_as_float(r[c >> 5][c & 31]));
+            const float mx = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])),
+                                   fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7])));
+            // lazy rescale: only when the maximum grew by more than 2^8 in weight
+            const bool grow = mx != -INFINITY && (ref == -INFINITY || fmaf(mx, a.sl2, -ref) > kCkLift + kCkLag);
+            const float up = fmaf(mx, a.sl2, -kCkLift);
+            const float alpha = grow && ref != -INFINITY ? ex2(ref - up) : 1.f;
+            if (grow) ref = up;
+            const float ms = ref == -INFINITY ? 0.f : ref;
+            const unsigned long long sc2 = lp_f2(a.sl2, a.sl2), ms2 = lp_f2(-ms, -ms);
+            unsigned long long l2[4] = {0ull, 0ull, 0ull, 0ull};
+            uint32_t pw[32];
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+                float y0, y1;
+                lp_f2(lp_fma2(lp_f2(__uint_as_float(r[c >> 4][2 * c & 31]), __uint_as_float(r[c >> 4][(2 * c & 31) + 1])), sc2,
+                              ms2), y0, y1);
+                y0 = ex2(y0);
+                y1 = ex2(y1);
+                l2[c & 3] = lp_add2(l2[c & 3], lp_f2(y0, y1));
+                pw[c] = ck_pack(y0, y1);
+            }
+            float l0, l1;
+            lp_f2(lp_add2(lp_add2(l2[0], l2[1]), lp_add2(l2[2], l2[3])), l0, l1);
+            lsum = lsum * alpha + (l0 + l1);
+            if (x > 0 && __any_sync(kFull, alpha != 1.f)) {   // rescale O, once P V of tile x - 1 is in
+                ok = __all_sync(kFull, mbar_wait_ab(&bF[2 * slot + (b ^ 1)], (unsigned)((x - 1) >> 1) & 1u, abort));
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll 1
+                for (int c0 = 0; c0 < kLatHead; c0 += 32) {
+                    uint32_t o[32];
+                    tc_ld32(tO + c0, o);
+                    tc_wait_ld();
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
+                    tc_st32(tO + c0, o);
+                }
+            }
+            ok = __all_sync(kFull, pf || mbar_wait_ab(&bF[2 * slot + b], (unsigned)((x >> 1) + 1) & 1u, abort));
+            if (!ok) break;
+            tc_fence_after();
+            tc_st32(tS + 64 + 32 * b, pw);
+            tc_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bP[2 * slot + b]);
+        }
+        for (int y = max(mine - 2, 0); y < mine && ok; ++y)
+            ok = __all_sync(kFull, mbar_wait_ab(&bF[2 * slot + (y & 1)], (unsigned)(y >> 1) & 1u, abort));
+        if (ok && mine > 0) {
+            tc_fence_after();
+            // 32 columns at a time through shared memory (Q's, which the slot's
+            // products have read; 16-byte chunk c of row r at chunk c ^ (r / 2
+            // mod 4) of it: no bank conflicts): a store covers 64 consecutive
+            // bytes of 8 rows
+            const float inv = 1.f / lsum;
+            unsigned char *st = sQ + slot * kLpQ + (warp & 3) * (32 * 64);
+            const int q8 = lane >> 2, c4 = lane & 3, row32 = srow + 32 * (warp & 3);
+            __half *dst = a.out + ((size_t)pair * a.t_stride + row32) * kLatHead + 8 * c4;
+#pragma unroll 1
+            for (int c0 = 0; c0 < kLatHead; c0 += 32) {
+                uint32_t o[32];
+                tc_ld32(tO + c0, o);
+                tc_wait_ld();
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    *reinterpret_cast<uint4 *>(st + lane * 64 + ((c ^ (lane >> 1)) & 3) * 16) =
+                        make_uint4(ck_pack(__uint_as_float(o[8 * c]) * inv, __uint_as_float(o[8 * c + 1]) * inv),
+                                   ck_pack(__uint_as_float(o[8 * c + 2]) * inv, __uint_as_float(o[8 * c + 3]) * inv),
+                                   ck_pack(__uint_as_float(o[8 * c + 4]) * inv, __uint_as_float(o[8 * c + 5]) * inv),
+                                   ck_pack(__uint_as_float(o[8 * c + 6]) * inv, __uint_as_float(o[8 * c + 7]) * inv));
+                __syncwarp();
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int q = 8 * k + q8;
+                    const uint4 v = *reinterpret_cast<const uint4 *>(st + q * 64 + ((c4 ^ (q >> 1)) & 3) * 16);
+                    if (row32 + q < n) *reinterpret_cast<uint4 *>(dst + (size_t)q * kLatHead + c0) = v;
+                }
+                __syncwarp();
+            }
+        }
+        tc_fence_before();
+        if (!ok && lane == 0) {
+            s_abort = 1;
+            atomicOr(a.status, KIVI_FLAG_WAIT);
+        }
+        __syncwarp();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) tc_dealloc(taddr, 512);
+}
+
+kivi_status fail(kivi_status s, const char *msg) {
+    kivi_set_last_error(msg);
+    return s;
+}
+
+}  // namespace
+
+extern "C" kivi_status kivi_latent_prompt_attn(const void *q, const void *q_rope, const void *K, const void *Kr,
+                                               const void *V, int b, int h, const int32_t *t, int t_stride, float scale,
+                                               void *out, kivi_stream_t stream) {
+    kivi_set_last_error("");
+    if (b < 1 || h < 1 || t_stride < 0) return fail(KIVI_ERR_INVALID_ARG, "sizes must be positive");
+    if (b > KIVI_MAX_BATCH) return fail(KIVI_ERR_UNSUPPORTED, "b above 1024");
+    if (h > 1024) return fail(KIVI_ERR_UNSUPPORTED, "more than 1024 heads");
+    if (t_stride > (1 << 26) || (long long)b * h * t_stride >= (1LL << 31))
+        return fail(KIVI_ERR_UNSUPPORTED, "t_stride above 2^26, or b h t_stride not below 2^31");
+    if (!(scale > 0.f && scale - scale == 0.f)) return fail(KIVI_ERR_INVALID_ARG, "scale must be positive and finite");
+    if (!t) return fail(KIVI_ERR_INVALID_ARG, "t is null");
+    PromptArgs a;
+    int maxt = 0;
+    for (int i = 0; i < b; ++i) {
+        if (t[i] < 0 || t[i] > t_stride) return fail(KIVI_ERR_INVALID_ARG, "t[i] outside [0, t_stride]");
+        a.t[i] = t[i];
+        maxt = t[i] > maxt ? t[i] : maxt;
+    }
+    if (maxt == 0) return KIVI_OK;
+    if (!q || !q_rope || !K || !Kr || !V || !out) return fail(KIVI_ERR_INVALID_ARG, "a tensor pointer is null");
+    if (((uintptr_t)q | (uintptr_t)q_rope | (uintptr_t)K | (uintptr_t)Kr | (uintptr_t)V | (uintptr_t)out) & 15u)
+        return fail(KIVI_ERR_INVALID_ARG, "tensors must be 16-byte aligned");
+    a.out = (__half *)out;
+    a.b = b;
+    a.h = h;
+    a.t_stride = t_stride;
+    a.mt = (maxt + 2 * kLpRows - 1) / (2 * kLpRows);
+    a.sl2 = scale * 1.4426950408889634f;
+    if ((long long)a.mt * b * h > INT_MAX) return fail(KIVI_ERR_UNSUPPORTED, "more than 2^31 row tiles");
+    a.status = kivi_device_status();
+    if (!a.status) return fail(KIVI_ERR_CUDA, "no status word on the current device");
+    const long long rows = (long long)b * h * t_stride;
+    CUtensorMap tq, tqr, tk, tkr, tv;
+    cudaError_t e = make_tile_map(&tq, (const __half *)q, rows, kLatHead, kLpRows);
+    if (e == cudaSuccess) e = make_tile_map(&tqr, (const __half *)q_rope, rows, kLatRope, kLpRows);
+    if (e == cudaSuccess) e = make_tile_map(&tk, (const __half *)K, rows, kLatHead, kLpKeys);
+    if (e == cudaSuccess) e = make_tile_map(&tkr, (const __half *)Kr, (long long)b * t_stride, kLatRope, kLpKeys);
+    if (e == cudaSuccess) e = make_tile_map(&tv, (const __half *)V, rows, kLatHead, kLpKeys);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(latent_prompt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kLpSmem);
+    if (e != cudaSuccess) return fail(KIVI_ERR_CUDA, cudaGetErrorString(e));
+    latent_prompt_kernel<<<(unsigned)(a.mt * b * h), kLpThreads, kLpSmem, (cudaStream_t)stream>>>(tq, tqr, tk, tkr, tv, a);
+    e = cudaGetLastError();
+    return e == cudaSuccess ? KIVI_OK : fail(KIVI_ERR_CUDA, cudaGetErrorString(e));
+}

@@ -1,5 +1,5 @@
-// kivi_rope.cu -- rotary positions of queries and keys, and the entry point
-// kivi_rope.
+// kivi_rope.cu -- rotary positions of queries and keys, and the entry points
+// kivi_rope and kivi_rope_axes.
 //
 // Mathematics.  Channel pair m of a token at position p turns by the angle
 // p w_m:  (x, y) -> f (x cos - y sin, y cos + x sin), with w_m the pair's
@@ -14,6 +14,11 @@
 // by itself (negative positions too), is exact up to the frequency's own
 // rounding (2^-65 turn a position), and its top 32 bits, read as a signed
 // number, are the angle in half turns for sincospi.
+//
+// Several axes (a patch's time, height and width): pair m turns by the token's
+// position on axis[m].  A thread of one axis loads one position, of several
+// eight (from the first-level cache, all in flight at once); the rest is the
+// same.
 //
 // Bound: memory (4 bytes a value moved, 1.5 multiply-adds a value).  A
 // thread keeps the sines and cosines of one token's 8 pairs in registers
@@ -38,9 +43,10 @@ struct RopeArgs {
     int n_stride, rot;
     float factor;
     bool inverse;
-    const int *pos;         // device positions [b][n_stride], or null: pos0[i] + r
+    const int *pos;         // device positions [axes][b][n_stride], or null: pos0[i] + r
     int n[KIVI_MAX_BATCH], pos0[KIVI_MAX_BATCH];
     unsigned long long turns[kRopeMaxPairs];
+    uint8_t axis[kRopeMaxPairs];   // (with several axes)
 };
 
 __device__ __forceinline__ uint32_t rot_pair(float a, float b) {
@@ -50,7 +56,7 @@ __device__ __forceinline__ uint32_t rot_pair(float a, float b) {
 
 // One block: TR tokens x D / 16 units of 16 channels x HY heads; a thread
 // takes heads hy, hy + HY gridDim.y, ... of its unit (q's heads first).
-template <int D, bool INTER>
+template <int D, bool INTER, bool AXES>
 __global__ void __launch_bounds__(kRopeThreads)
     rope_kernel(const __grid_constant__ RopeArgs A, int lgTR, int lgHY) {
     constexpr int U = D / 16;
@@ -62,10 +68,18 @@ __global__ void __launch_bounds__(kRopeThreads)
     const int c1 = turn && !INTER ? A.rot / 2 + 8 * u : c0 + 8;
     float cs[8], sn[8];
     if (turn) {
-        const long long p = A.pos ? A.pos[(size_t)i * A.n_stride + r] : (long long)A.pos0[i] + r;
+        long long p[8];
+        if (AXES) {
+            const size_t plane = (size_t)gridDim.z * A.n_stride;   // (a block of z a sequence)
+            const int *pos = A.pos + (size_t)i * A.n_stride + r;
+#pragma unroll
+            for (int m = 0; m < 8; ++m) p[m] = pos[A.axis[8 * u + m] * plane];
+        } else {
+            p[0] = A.pos ? A.pos[(size_t)i * A.n_stride + r] : (long long)A.pos0[i] + r;
+        }
 #pragma unroll
         for (int m = 0; m < 8; ++m) {
-            const unsigned long long a = (unsigned long long)p * A.turns[8 * u + m];
+            const unsigned long long a = (unsigned long long)p[AXES ? m : 0] * A.turns[8 * u + m];
             sincospif((float)(int)(a >> 32) * 0x1p-31f, &sn[m], &cs[m]);
             cs[m] *= A.factor;
             sn[m] *= A.inverse ? -A.factor : A.factor;
@@ -115,7 +129,7 @@ __global__ void __launch_bounds__(kRopeThreads)
 }
 
 template <int D>
-cudaError_t launch_rope(const RopeArgs &A, int b, bool interleaved, int maxn, cudaStream_t st) {
+cudaError_t launch_rope(const RopeArgs &A, int b, bool interleaved, bool axes, int maxn, cudaStream_t st) {
     constexpr int U = D / 16;
     int lgTR = 0;   // tokens a block: as many as there are, up to the block's threads
     while ((1 << lgTR) < maxn && (U << lgTR) < kRopeThreads) ++lgTR;
@@ -135,8 +149,10 @@ cudaError_t launch_rope(const RopeArgs &A, int b, bool interleaved, int maxn, cu
     int per = 8;
     while (per > 1 && (long long)gx * b * ((rows + per - 1) / per) < sms / 2) per >>= 1;
     const dim3 grid(gx, (rows + per - 1) / per, b);
-    if (interleaved) rope_kernel<D, true><<<grid, kRopeThreads, 0, st>>>(A, lgTR, lgHY);
-    else rope_kernel<D, false><<<grid, kRopeThreads, 0, st>>>(A, lgTR, lgHY);
+    if (interleaved && axes) rope_kernel<D, true, true><<<grid, kRopeThreads, 0, st>>>(A, lgTR, lgHY);
+    else if (interleaved) rope_kernel<D, true, false><<<grid, kRopeThreads, 0, st>>>(A, lgTR, lgHY);
+    else if (axes) rope_kernel<D, false, true><<<grid, kRopeThreads, 0, st>>>(A, lgTR, lgHY);
+    else rope_kernel<D, false, false><<<grid, kRopeThreads, 0, st>>>(A, lgTR, lgHY);
     return cudaGetLastError();
 }
 
@@ -145,13 +161,11 @@ kivi_status fail(kivi_status s, const char *msg) {
     return s;
 }
 
-}  // namespace
-
-extern "C" kivi_status kivi_rope(const void *q, const void *k, int b, int h_q, int h_kv, int n_stride, int d,
-                                 const int32_t *n, const int32_t *pos0, const int32_t *pos, const uint64_t *turns,
-                                 int rot_dim, int interleaved, float factor, int inverse, void *q_out, void *k_out,
-                                 kivi_stream_t stream) {
-    kivi_set_last_error("");
+// kivi_rope, and with axes > 0 kivi_rope_axes (pos then has axes planes)
+kivi_status rope(const void *q, const void *k, int b, int h_q, int h_kv, int n_stride, int d, const int32_t *n,
+                 const int32_t *pos0, const int32_t *pos, int axes, const uint8_t *axis, const uint64_t *turns,
+                 int rot_dim, int interleaved, float factor, int inverse, void *q_out, void *k_out,
+                 kivi_stream_t stream) {
     if (b < 1 || n_stride < 0 || h_q < 0 || h_kv < 0 || h_q + (long long)h_kv < 1)
         return fail(KIVI_ERR_INVALID_ARG, "sizes must be positive");
     if (b > KIVI_MAX_BATCH) return fail(KIVI_ERR_UNSUPPORTED, "b above 1024");
@@ -160,10 +174,14 @@ extern "C" kivi_status kivi_rope(const void *q, const void *k, int b, int h_q, i
         return fail(KIVI_ERR_UNSUPPORTED, "rot_dim must be a multiple of 16, at most d");
     if (h_q > 65536 || h_kv > 65536) return fail(KIVI_ERR_UNSUPPORTED, "more than 65536 heads");
     if (!n || !turns || (pos0 != nullptr) == (pos != nullptr))
-        return fail(KIVI_ERR_INVALID_ARG, "need n, turns and one of pos0 and pos");
+        return fail(KIVI_ERR_INVALID_ARG, axes > 0 ? "need n, turns and pos" : "need n, turns and one of pos0 and pos");
     if (!(factor - factor == 0.f)) return fail(KIVI_ERR_INVALID_ARG, "factor must be finite");
     if ((uintptr_t)pos & 3u) return fail(KIVI_ERR_INVALID_ARG, "pos must be 4-byte aligned");
     RopeArgs A;
+    for (int m = 0; axes > 0 && m < kRopeMaxPairs; ++m) {
+        A.axis[m] = m < rot_dim / 2 ? axis[m] : 0;
+        if (A.axis[m] >= axes) return fail(KIVI_ERR_INVALID_ARG, "a pair's axis is outside [0, axes)");
+    }
     int maxn = 0;
     for (int i = 0; i < b; ++i) {
         if (n[i] < 0 || n[i] > n_stride) return fail(KIVI_ERR_INVALID_ARG, "n[i] outside [0, n_stride]");
@@ -190,9 +208,31 @@ extern "C" kivi_status kivi_rope(const void *q, const void *k, int b, int h_q, i
     A.pos = pos;
     for (int m = 0; m < kRopeMaxPairs; ++m) A.turns[m] = m < rot_dim / 2 ? turns[m] : 0ull;
     const cudaStream_t st = (cudaStream_t)stream;
-    const bool il = interleaved != 0;
-    const cudaError_t e = d == 64 ? launch_rope<64>(A, b, il, maxn, st)
-                                  : d == 128 ? launch_rope<128>(A, b, il, maxn, st)
-                                             : launch_rope<256>(A, b, il, maxn, st);
+    const bool il = interleaved != 0, ax = axes > 0;
+    const cudaError_t e = d == 64 ? launch_rope<64>(A, b, il, ax, maxn, st)
+                                  : d == 128 ? launch_rope<128>(A, b, il, ax, maxn, st)
+                                             : launch_rope<256>(A, b, il, ax, maxn, st);
     return e == cudaSuccess ? KIVI_OK : fail(KIVI_ERR_CUDA, cudaGetErrorString(e));
+}
+
+}  // namespace
+
+extern "C" kivi_status kivi_rope(const void *q, const void *k, int b, int h_q, int h_kv, int n_stride, int d,
+                                 const int32_t *n, const int32_t *pos0, const int32_t *pos, const uint64_t *turns,
+                                 int rot_dim, int interleaved, float factor, int inverse, void *q_out, void *k_out,
+                                 kivi_stream_t stream) {
+    kivi_set_last_error("");
+    return rope(q, k, b, h_q, h_kv, n_stride, d, n, pos0, pos, 0, nullptr, turns, rot_dim, interleaved, factor,
+                inverse, q_out, k_out, stream);
+}
+
+extern "C" kivi_status kivi_rope_axes(const void *q, const void *k, int b, int h_q, int h_kv, int n_stride, int d,
+                                      const int32_t *n, const int32_t *pos, int axes, const uint8_t *axis,
+                                      const uint64_t *turns, int rot_dim, int interleaved, float factor, int inverse,
+                                      void *q_out, void *k_out, kivi_stream_t stream) {
+    kivi_set_last_error("");
+    if (axes < 1 || axes > 255) return fail(KIVI_ERR_INVALID_ARG, "axes outside [1, 255]");
+    if (!axis) return fail(KIVI_ERR_INVALID_ARG, "axis is null");
+    return rope(q, k, b, h_q, h_kv, n_stride, d, n, nullptr, pos, axes, axis, turns, rot_dim, interleaved, factor,
+                inverse, q_out, k_out, stream);
 }

@@ -28,7 +28,10 @@ EXPORTS = ["kivi_cache_create", "kivi_cache_destroy", "kivi_prefill", "kivi_appe
            "kivi_decode_plan", "kivi_status_str", "kivi_last_error", "kivi_abi_version",
            "kivi_decode_attn_noalloc", "kivi_cache_export_records", "kivi_append_decode",
            "kivi_decode_attn_probs", "kivi_plan_preview", "kivi_prefill_attn", "kivi_prefill_attn_window",
-           "kivi_decode_attn_window", "kivi_chunk_attn", "kivi_append_chunk", "kivi_rope"]
+           "kivi_decode_attn_window", "kivi_chunk_attn", "kivi_append_chunk", "kivi_rope",
+           "kivi_rope_axes", "kivi_verify", "kivi_latent_create", "kivi_latent_destroy", "kivi_latent_prefill",
+           "kivi_latent_append", "kivi_latent_attn", "kivi_latent_lengths", "kivi_latent_restore",
+           "kivi_latent_check", "kivi_head_product", "kivi_latent_prompt_attn", "kivi_device_check"]
 
 
 class KiviError(RuntimeError):
@@ -59,6 +62,18 @@ def _load():
     L.kivi_chunk_attn.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i32, vp, vp]
     L.kivi_append_chunk.argtypes = [vp, vp, vp, vp, i32, vp]
     L.kivi_rope.argtypes = [vp, vp] + [i32] * 5 + [vp] * 4 + [i32, i32, ctypes.c_float, i32, vp, vp, vp]
+    L.kivi_rope_axes.argtypes = [vp, vp] + [i32] * 5 + [vp, vp, i32, vp, vp, i32, i32, ctypes.c_float, i32, vp, vp, vp]
+    L.kivi_verify.argtypes = [vp, vp, i32, vp, vp, i32, i32, i32, vp, vp, vp, vp]
+    L.kivi_latent_create.argtypes = [i32] * 6 + [ctypes.POINTER(vp)]
+    L.kivi_latent_destroy.argtypes = [vp]
+    L.kivi_latent_prefill.argtypes = L.kivi_latent_append.argtypes = [vp, vp, vp, vp, i32, vp]
+    L.kivi_latent_attn.argtypes = [vp] * 6 + [i32, i32, ctypes.c_float, vp, vp]
+    L.kivi_latent_lengths.argtypes = [vp, vp, vp]
+    L.kivi_latent_restore.argtypes = [vp, vp, vp, i32, vp]
+    L.kivi_latent_check.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32), vp]
+    L.kivi_head_product.argtypes = [vp, vp, i32, i32, i32, i32, vp, i32, i32, i32, vp, vp]
+    L.kivi_latent_prompt_attn.argtypes = [vp] * 5 + [i32, i32, vp, i32, ctypes.c_float, vp, vp]
+    L.kivi_device_check.argtypes = [ctypes.POINTER(ctypes.c_uint32), vp]
     L.kivi_plan_preview.argtypes = [i32] * 9 + [vp, vp, vp, i32, vp]
     L.kivi_cache_lengths.argtypes = [vp, vp, vp, vp]
     L.kivi_cache_export_sizes.argtypes = [vp, ctypes.POINTER(ctypes.c_size_t)]
@@ -162,6 +177,18 @@ def _rows16(x, shape, dev, name):
     return x.data_ptr()
 
 
+def _rows(x, shape, dtype, dev, name):
+    """Address of a contiguous CUDA tensor of this shape and type on device dev."""
+    import torch
+    if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dtype is not dtype:
+        raise TypeError(f"{name} must be a CUDA {str(dtype)[6:]} tensor")
+    if tuple(x.shape) != tuple(shape) or not x.is_contiguous():
+        raise ValueError(f"{name} must be contiguous with shape {tuple(shape)}, got {tuple(x.shape)}")
+    if x.get_device() != dev:
+        raise ValueError(f"{name} must be on device cuda:{dev}")
+    return x.data_ptr()
+
+
 def rope_frequencies(rot_dim, base=10000.0, scaling=None, factor=1.0, original_length=8192, beta_fast=32.0,
                      beta_slow=1.0, low=1.0, high=4.0):
     """Rotary frequencies (radians a position, float64 [rot_dim / 2]) and the
@@ -200,27 +227,47 @@ def rope_frequencies(rot_dim, base=10000.0, scaling=None, factor=1.0, original_l
     raise ValueError(f"unknown scaling {scaling!r}")
 
 
+def rope_axes(sections, in_turn=False):
+    """The axis of each channel pair for Rope: sections[a] pairs turn by axis a,
+    one section after another, or, in_turn, dealt to the axes in turn while they
+    last (0, 1, 2, 0, 1, 2, ...)."""
+    left = [operator.index(x) for x in sections]
+    if not left or min(left) < 0 or sum(left) < 1:
+        raise ValueError("sections must be numbers of pairs")
+    if not in_turn:
+        return [a for a, k in enumerate(left) for _ in range(k)]
+    return [a for k in range(max(left)) for a, m in enumerate(left) if k < m]
+
+
 class Rope:
     """Rotary positions for heads of dimension d: the first rot_dim channels
     (default all) turn, pairs (m, m + rot_dim / 2) or, interleaved, (2 m,
     2 m + 1), at the frequencies inv_freq (default base ** (-2 m / rot_dim);
-    rope_frequencies has the long-context scalings) times factor."""
+    rope_frequencies has the long-context scalings) times factor.  axes: the
+    axis of each pair's position (rot_dim / 2 numbers from 0 on; rope_axes makes
+    the usual ones), for tokens that stand on several."""
 
-    def __init__(self, d, rot_dim=None, base=10000.0, interleaved=False, inv_freq=None, factor=1.0):
+    def __init__(self, d, rot_dim=None, base=10000.0, interleaved=False, inv_freq=None, factor=1.0, axes=None):
         self.d, self.rot_dim = d, d if rot_dim is None else rot_dim
         self.interleaved, self.factor = int(bool(interleaved)), float(factor)
         f = rope_frequencies(self.rot_dim, base)[0] if inv_freq is None else np.asarray(inv_freq, np.float64)
         if f.shape != (self.rot_dim // 2,) or not np.all(np.isfinite(f)):
             raise ValueError(f"inv_freq must be {self.rot_dim // 2} finite numbers")
         self.inv_freq = f.copy()
+        self.axes = None
+        if axes is not None:
+            a = [operator.index(x) for x in axes]
+            if len(a) != self.rot_dim // 2 or min(a) < 0 or max(a) > 254:
+                raise ValueError(f"axes must be {self.rot_dim // 2} numbers from 0 to 254")
+            self.axes, self._axis = max(a) + 1, array.array("B", a)
         # fractions of a turn, 2^64 = one turn
         self._turns = array.array("Q", [int(round(x / (2 * math.pi) * 2.0**64)) % 2**64 for x in f.tolist()])
 
     def apply(self, q, k, pos, n=None, q_out=None, k_out=None, inverse=False, stream=None):
         """Rotate q (CUDA fp16 [b, h_q, t, d] or [b, h_q, d]) and k (same with
         h_kv heads, or None).  pos: first position of each sequence (an
-        integer or b integers), or every position (CUDA int32 [b, t]).  n:
-        tokens of each sequence (default t; rows past them stay as they are in
+        integer or b integers), or every position (CUDA int32 [b, t], with
+        axes [axes, b, t]; a first position stands on every axis).  n: tokens of each sequence (default t; rows past them stay as they are in
         the outputs, zero in new ones).  inverse: the transposed map.  Returns
         (q_out, k_out), or q_out alone when k is None."""
         import torch
@@ -241,9 +288,7 @@ class Rope:
         cnt = _counts(t if n is None else n, b)
         posp, pos0 = None, None
         if isinstance(pos, torch.Tensor) and pos.is_cuda:
-            if pos.dtype is not torch.int32 or tuple(pos.shape) != (b, t) or not pos.is_contiguous() or pos.get_device() != dev:
-                raise ValueError(f"pos must be a contiguous int32 tensor [{b}, {t}] on device cuda:{dev}")
-            posp = pos.data_ptr()
+            posp = self._pos(pos, b, t, dev)
         else:
             pos0 = _counts(pos, b, "pos")
         if q_out is None or (k_out is None and k is not None):
@@ -255,7 +300,20 @@ class Rope:
                    None if k is None else _rows16(k_out, ks, dev, "k_out"), _stream(stream))
         return q_out if k is None else (q_out, k_out)
 
+    def _pos(self, pos, b, t, dev):
+        """Address of every token's position."""
+        import torch
+        shape = (b, t) if self.axes is None else (self.axes, b, t)
+        if pos.dtype is not torch.int32 or tuple(pos.shape) != shape or not pos.is_contiguous() or pos.get_device() != dev:
+            raise ValueError(f"pos must be a contiguous int32 tensor {list(shape)} on device cuda:{dev}")
+        return pos.data_ptr()
+
     def _call(self, qp, kp, b, hq, hk, t, cnt, pos0, posp, inverse, qo, ko, stream):
+        if posp is not None and self.axes is not None:
+            _check(lib.kivi_rope_axes(qp, kp, b, hq, hk, t, self.d, _addr(cnt), posp, self.axes, _addr(self._axis),
+                                      _addr(self._turns), self.rot_dim, self.interleaved, self.factor,
+                                      1 if inverse else 0, qo, ko, stream))
+            return
         _check(lib.kivi_rope(qp, kp, b, hq, hk, t, self.d, _addr(cnt), None if pos0 is None else _addr(pos0), posp,
                              _addr(self._turns), self.rot_dim, self.interleaved, self.factor, 1 if inverse else 0,
                              qo, ko, stream))
@@ -369,10 +427,11 @@ class KiviCache:
         kp, vp, cnt, ns = self._chunk(K, V, n)
         _check(lib.kivi_append_chunk(self._h, kp, vp, _addr(cnt), ns, _stream(stream)))
 
-    def extend(self, Q, K, V, n, window=0, sinks=0, rope=None, out=None, stream=None):
+    def extend(self, Q, K, V, n, window=0, sinks=0, rope=None, out=None, stream=None, pos=None):
         """Take the next chunk of every sequence: rotate its queries and keys
-        at the positions behind the cached tokens (rope: a Rope, or None),
-        attend (chunk_attn; returns its out) and append it (append_chunk)."""
+        at the positions behind the cached tokens (rope: a Rope, or None; or at
+        pos, as Rope.apply takes every position), attend (chunk_attn; returns
+        its out) and append it (append_chunk)."""
         import torch
         if torch.cuda.current_device() != self._dev:   # (before the rotation, which runs on the current one)
             raise KiviError(1, f"the cache belongs to device {self._dev}, which is not current")
@@ -388,9 +447,11 @@ class KiviCache:
         if rope is not None:
             if rope.d != self.d:
                 raise ValueError(f"rope is for heads of dimension {rope.d}")
+            posp = None if pos is None else rope._pos(pos, self.b, ns, self._dev)
             with _on(stream):   # rows past n are not read
                 rq, rk = torch.empty_like(Q), torch.empty_like(K)
-            rope._call(qp, kp, self.b, hq, self.h_kv, ns, cnt, T, None, False, rq.data_ptr(), rk.data_ptr(), st)
+            rope._call(qp, kp, self.b, hq, self.h_kv, ns, cnt, T if posp is None else None, posp, False, rq.data_ptr(),
+                       rk.data_ptr(), st)
             qp, kp = rq.data_ptr(), rk.data_ptr()
         _check(lib.kivi_chunk_attn(self._h, qp, kp, vp, cp, ns, hq, win, snk, op, st))
         _check(lib.kivi_append_chunk(self._h, kp, vp, cp, ns, st))
@@ -502,3 +563,277 @@ class KiviCache:
         n = ctypes.c_int(0)
         _check(lib.kivi_decode_plan(self._h, ctypes.byref(s), ctypes.byref(n)))
         return int(s.value), int(n.value)
+
+
+def verify(p, q, draft, u, n=None, tokens=None, accepted=None, stream=None):
+    """Verification of drafted tokens (kivi_verify): p CUDA fp32 or fp16 [b, ns +
+    1, vocab], the target's probabilities; q [b, ns, vocab] of the same type, the
+    draft's, or None where each drafted token was certain; draft CUDA int32 [b,
+    ns]; u CUDA fp32 [b, ns + 1], uniform in [0, 1); n: drafted tokens of each
+    sequence (an integer or b of them, default ns).  Returns tokens (int32 [b, ns
+    + 1]: those kept, the one drawn behind them, then -1) and accepted (int32 [b]:
+    how many were kept)."""
+    import torch
+    if not isinstance(p, torch.Tensor) or p.dim() != 3 or p.shape[1] < 1:
+        raise ValueError("p must be a [b, ns + 1, vocab] tensor")
+    if not p.is_cuda or p.dtype not in (torch.float32, torch.float16):
+        raise TypeError("p must be a CUDA float32 or float16 tensor")
+    dev = p.get_device()
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return verify(p, q, draft, u, n, tokens, accepted, stream)
+    b, ns, V = p.shape[0], p.shape[1] - 1, p.shape[2]
+    cnt = _counts(ns if n is None else n, b)
+    args = [_rows(p, p.shape, p.dtype, dev, "p"), None if q is None else _rows(q, (b, ns, V), p.dtype, dev, "q"),
+            p.element_size(), _rows(draft, (b, ns), torch.int32, dev, "draft"),
+            _rows(u, (b, ns + 1), torch.float32, dev, "u")]
+    if tokens is None or accepted is None:
+        with _on(stream):
+            tokens = torch.empty((b, ns + 1), dtype=torch.int32, device=p.device) if tokens is None else tokens
+            accepted = torch.empty((b,), dtype=torch.int32, device=p.device) if accepted is None else accepted
+    _check(lib.kivi_verify(*args, b, ns, V, _addr(cnt), _rows(tokens, (b, ns + 1), torch.int32, dev, "tokens"),
+                           _rows(accepted, (b,), torch.int32, dev, "accepted"), _stream(stream)))
+    return tokens, accepted
+
+
+def device_check(stream=None) -> int:
+    """The current device's status word of the calls without a handle
+    (kivi_device_check)."""
+    f = ctypes.c_uint32(0)
+    _check(lib.kivi_device_check(ctypes.byref(f), _stream(stream)))
+    return int(f.value)
+
+
+LATENT_HEAD, LATENT_ROPE = 128, 64   # channels of a head without positions (and of its values), of the rotary key
+
+
+def head_product(x, w, n=None, transposed=False, out=None, stream=None):
+    """A matrix of each head times its rows (kivi_head_product): x CUDA fp16 [b,
+    h, t, K] or [b, t, K] (rows of all heads alike), w [h, N, K] or, transposed,
+    [h, K, N] -> out [b, h, t, N] (rows past n untouched, zero in a new tensor)."""
+    import torch
+    if not isinstance(x, torch.Tensor) or not isinstance(w, torch.Tensor) or x.dim() not in (3, 4) or w.dim() != 3:
+        raise ValueError("x must be [b, h, t, K] or [b, t, K], w [h, N, K]")
+    if not x.is_cuda:
+        raise TypeError("x must be a CUDA float16 tensor")
+    dev = x.get_device()
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return head_product(x, w, n, transposed, out, stream)
+    b, t, K, h = x.shape[0], x.shape[-2], x.shape[-1], w.shape[0]
+    N = w.shape[2] if transposed else w.shape[1]
+    hx = 1 if x.dim() == 3 else h
+    xp = _rows16(x, (b, t, K) if x.dim() == 3 else (b, h, t, K), dev, "x")
+    wp = _rows16(w, (h, K, N) if transposed else (h, N, K), dev, "w")
+    cnt = _counts(t if n is None else n, b)
+    if out is None:
+        with _on(stream):
+            out = (torch.empty if n is None or min(cnt) == t else torch.zeros)((b, h, t, N), dtype=x.dtype, device=x.device)
+    _check(lib.kivi_head_product(xp, wp, b, hx, h, t, _addr(cnt), K, N, 1 if transposed else 0,
+                                 _rows16(out, (b, h, t, N), dev, "out"), _stream(stream)))
+    return out
+
+
+def _latent_args(qn, qr, c, kr, wk, wv, out, stream, dev):
+    """Checks of a latent call's tensors: (b, h, t, r) and their addresses."""
+    import torch
+    if any(not isinstance(x, torch.Tensor) for x in (qn, qr, c, kr, wk, wv)):
+        raise TypeError("queries, latent vectors and weights must be tensors")
+    if qn.dim() != 4 or c.dim() != 3:
+        raise ValueError("qn must be [b, h, t, 128] and c [b, t, r]")
+    (b, h, t, _), r = qn.shape, c.shape[2]
+    qnp, qrp = _rows16(qn, (b, h, t, LATENT_HEAD), dev, "qn"), _rows16(qr, (b, h, t, LATENT_ROPE), dev, "qr")
+    cp, krp = _rows16(c, (b, t, r), dev, "c"), _rows16(kr, (b, t, LATENT_ROPE), dev, "kr")
+    wkp, wvp = _rows16(wk, (h, LATENT_HEAD, r), dev, "wk"), _rows16(wv, (h, LATENT_HEAD, r), dev, "wv")
+    if out is None:
+        with _on(stream):
+            out = torch.zeros_like(qn)
+    return (b, h, t, r), (qnp, qrp, cp, krp, wkp, wvp, _rows16(out, (b, h, t, LATENT_HEAD), dev, "out")), out
+
+
+def _latent_scale(scale):
+    return 1.0 / math.sqrt(LATENT_HEAD + LATENT_ROPE) if scale is None else float(scale)
+
+
+def latent_prompt_attn(qn, qr, c, kr, t, wk, wv, scale=None, out=None, stream=None):
+    """Latent attention of prompts, expanded: every head's keys and values are
+    formed (head_product) and attended to causally (kivi_latent_prompt_attn).  qn
+    CUDA fp16 [b, h, ts, 128], qr [b, h, ts, 64] (rotated), c [b, ts, r], kr [b,
+    ts, 64] (rotated), wk and wv [h, 128, r], t tokens of each sequence -> out [b,
+    h, ts, 128] (rows past t untouched, zero in a new tensor).  scale: default 1 /
+    sqrt(192)."""
+    import torch
+    if not isinstance(qn, torch.Tensor) or not qn.is_cuda:
+        raise TypeError("qn must be a CUDA float16 tensor")
+    dev = qn.get_device()
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return latent_prompt_attn(qn, qr, c, kr, t, wk, wv, scale, out, stream)
+    (b, h, ts, r), (qnp, qrp, cp, krp, wkp, wvp, op), out = _latent_args(qn, qr, c, kr, wk, wv, out, stream, dev)
+    cnt, st = _counts(t, b, "t"), _stream(stream)
+    with _on(stream):   # (rows past t are not read)
+        K, V = torch.empty_like(qn), torch.empty_like(qn)
+    for w, x in ((wkp, K), (wvp, V)):
+        _check(lib.kivi_head_product(cp, w, b, 1, h, ts, _addr(cnt), r, LATENT_HEAD, 0, x.data_ptr(), st))
+    _check(lib.kivi_latent_prompt_attn(qnp, qrp, K.data_ptr(), krp, V.data_ptr(), b, h, _addr(cnt), ts,
+                                       _latent_scale(scale), op, st))
+    return out
+
+
+class LatentCache:
+    """A quantized cache of latent vectors for b sequences on the current GPU:
+    one vector c [r] a token (r 256 or 512), from which every head's keys and
+    values are products, and one rotary key kr [64].  The newest R tokens (a
+    multiple of 64) are fp16, older ones quantized to `bits` in groups of G
+    channels of a token.
+
+    Calls on one cache must not overlap on the GPU, as for KiviCache."""
+
+    def __init__(self, b, r, bits=4, G=32, R=128, max_tokens=4096):
+        self.b, self.r, self.bits, self.G, self.R, self.max_tokens = b, r, bits, G, R, max_tokens
+        self._h = ctypes.c_void_p()
+        _check(lib.kivi_latent_create(b, r, bits, G, R, max_tokens, ctypes.byref(self._h)))
+        import torch
+        self._dev = torch.cuda.current_device()   # the handle's memory is there
+
+    def close(self):
+        if self._h:
+            h, self._h = self._h, ctypes.c_void_p()
+            _check(lib.kivi_latent_destroy(h))
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    @property
+    def handle(self):
+        return self._h
+
+    def _tokens(self, c, kr, n, name="n"):
+        """Addresses of new tokens' rows, their counts and stride."""
+        import torch
+        if not isinstance(c, torch.Tensor) or c.dim() != 3:
+            raise ValueError(f"c must be a [b, {name}, r] tensor")
+        ns = c.shape[1]
+        return (_rows16(c, (self.b, ns, self.r), self._dev, "c"),
+                _rows16(kr, (self.b, ns, LATENT_ROPE), self._dev, "kr"), _counts(n, self.b, name), ns)
+
+    def _here(self):
+        import torch
+        if torch.cuda.current_device() != self._dev:   # (before anything is launched)
+            raise KiviError(1, f"the latent cache belongs to device {self._dev}, which is not current")
+
+    def prefill(self, c, kr, t, stream=None):
+        """Every sequence anew, with its first t tokens (an integer or b of them):
+        c CUDA fp16 [b, ts, r], kr [b, ts, 64]."""
+        cp, krp, cnt, ts = self._tokens(c, kr, t, "t")
+        _check(lib.kivi_latent_prefill(self._h, cp, krp, _addr(cnt), ts, _stream(stream)))
+
+    def append(self, c, kr, n, stream=None):
+        """n more tokens of each sequence (an integer or b of them)."""
+        cp, krp, cnt, ns = self._tokens(c, kr, n)
+        _check(lib.kivi_latent_append(self._h, cp, krp, _addr(cnt), ns, _stream(stream)))
+
+    def attn_latent(self, ql, qr, c, kr, n, scale=None, out=None, stream=None):
+        """The absorbed attention itself (kivi_latent_attn): ql CUDA fp16 [b, h,
+        ns, r], qr [b, h, ns, 64] -> out [b, h, ns, r] (rows past n untouched,
+        zero in a new tensor)."""
+        import torch
+        if not isinstance(ql, torch.Tensor) or ql.dim() != 4:
+            raise ValueError("ql must be a [b, h, ns, r] tensor")
+        cp, krp, cnt, ns = self._tokens(c, kr, n)
+        h = ql.shape[1]
+        shape = (self.b, h, ns, self.r)
+        qlp, qrp = _rows16(ql, shape, self._dev, "ql"), _rows16(qr, (self.b, h, ns, LATENT_ROPE), self._dev, "qr")
+        if out is None:
+            with _on(stream):
+                out = torch.zeros_like(ql)
+        _check(lib.kivi_latent_attn(self._h, qlp, qrp, cp, krp, _addr(cnt), ns, h, _latent_scale(scale),
+                                    _rows16(out, shape, self._dev, "out"), _stream(stream)))
+        return out
+
+    def _attn(self, dims, ptrs, qrp, krp, cnt, scale, stream, st):
+        import torch
+        (b, h, ns, r), (qnp, _, cp, _, wkp, wvp, op) = dims, ptrs
+        with _on(stream):   # (rows past n are not read)
+            ql = torch.empty((b, h, ns, r), dtype=torch.float16, device=f"cuda:{self._dev}")
+            ol = torch.empty_like(ql)
+        _check(lib.kivi_head_product(qnp, wkp, b, h, h, ns, _addr(cnt), LATENT_HEAD, r, 1, ql.data_ptr(), st))
+        _check(lib.kivi_latent_attn(self._h, ql.data_ptr(), qrp, cp, krp, _addr(cnt), ns, h, scale, ol.data_ptr(), st))
+        _check(lib.kivi_head_product(ol.data_ptr(), wvp, b, h, h, ns, _addr(cnt), r, LATENT_HEAD, 0, op, st))
+
+    def _args(self, qn, qr, c, kr, wk, wv, out, stream):
+        dims, ptrs, out = _latent_args(qn, qr, c, kr, wk, wv, out, stream, self._dev)
+        if dims[0] != self.b or dims[3] != self.r:
+            raise ValueError(f"the latent cache holds {self.b} sequences of vectors of {self.r}")
+        return dims, ptrs, out
+
+    def attn(self, qn, qr, c, kr, n, wk, wv, scale=None, out=None, stream=None):
+        """Latent attention of n new tokens of each sequence (an integer or b of
+        them) over the cache and over themselves, absorbed: qn CUDA fp16 [b, h, ns,
+        128], qr [b, h, ns, 64], c [b, ns, r], kr [b, ns, 64], wk and wv [h, 128,
+        r] -> out [b, h, ns, 128] (rows past n untouched, zero in a new tensor).
+        Queries and keys rotated.  Does not append (append, extend)."""
+        self._here()
+        dims, ptrs, out = self._args(qn, qr, c, kr, wk, wv, out, stream)
+        self._attn(dims, ptrs, ptrs[1], ptrs[3], _counts(n, self.b), _latent_scale(scale), stream, _stream(stream))
+        return out
+
+    def prefill_attn(self, qn, qr, c, kr, t, wk, wv, scale=None, out=None, stream=None):
+        """prefill(c, kr, t) and the prompt's attention (latent_prompt_attn)."""
+        self._here()
+        _, _, out = self._args(qn, qr, c, kr, wk, wv, out, stream)
+        self.prefill(c, kr, t, stream)
+        return latent_prompt_attn(qn, qr, c, kr, t, wk, wv, scale, out, stream)
+
+    def extend(self, qn, qr, c, kr, n, wk, wv, rope=None, pos=None, scale=None, out=None, stream=None):
+        """Take the next n tokens of every sequence (a chunk, or one): rotate qr
+        and kr at the positions behind the cached tokens (rope: a Rope of 64
+        channels, or None; or at pos, as Rope.apply takes every position), attend
+        (attn; returns its out) and append them."""
+        import torch
+        self._here()
+        dims, ptrs, out = self._args(qn, qr, c, kr, wk, wv, out, stream)
+        (b, h, ns, _), cnt, st = dims, _counts(n, self.b), _stream(stream)
+        qrp, krp = ptrs[1], ptrs[3]
+        T = array.array("i", bytes(4 * b))
+        _check(lib.kivi_latent_lengths(self._h, _addr(T), None))
+        for i in range(b):
+            if cnt[i] > self.max_tokens - T[i]:
+                raise CapacityError(3, f"sequence {i} would exceed max_tokens")
+        if rope is not None:
+            if rope.d != LATENT_ROPE:
+                raise ValueError(f"rope is for heads of dimension {rope.d}")
+            posp = None if pos is None else rope._pos(pos, b, ns, self._dev)
+            with _on(stream):   # (rows past n are not read)
+                rq, rk = torch.empty_like(qr), torch.empty_like(kr)
+            rope._call(qrp, krp, b, h, 1, ns, cnt, T if posp is None else None, posp, False, rq.data_ptr(), rk.data_ptr(), st)
+            qrp, krp = rq.data_ptr(), rk.data_ptr()
+        self._attn(dims, ptrs, qrp, krp, cnt, _latent_scale(scale), stream, st)
+        _check(lib.kivi_latent_append(self._h, ptrs[2], krp, _addr(cnt), ns, st))
+        return out
+
+    # -- inspection ----------------------------------------------------------
+    def lengths(self):
+        """Tokens of each sequence, and how many of them are quantized."""
+        T, Tq = np.zeros(self.b, np.int32), np.zeros(self.b, np.int32)
+        _check(lib.kivi_latent_lengths(self._h, T.ctypes.data, Tq.ctypes.data))
+        return T, Tq
+
+    def restore(self, stream=None):
+        """The cached latent vectors and rotary keys as attention sees them: CUDA
+        fp16 [b, t, r] and [b, t, 64] (t: the longest sequence; zero past each)."""
+        import torch
+        t = max(1, int(self.lengths()[0].max()))
+        with _on(stream):
+            c = torch.zeros((self.b, t, self.r), dtype=torch.float16, device=f"cuda:{self._dev}")
+            kr = torch.zeros((self.b, t, LATENT_ROPE), dtype=torch.float16, device=f"cuda:{self._dev}")
+        _check(lib.kivi_latent_restore(self._h, c.data_ptr(), kr.data_ptr(), t, _stream(stream)))
+        return c, kr
+
+    def check(self, stream=None) -> int:
+        f = ctypes.c_uint32(0)
+        _check(lib.kivi_latent_check(self._h, ctypes.byref(f), _stream(stream)))
+        return int(f.value)

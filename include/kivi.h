@@ -31,9 +31,10 @@
  *     (two streams without an event between them, two captured graphs replayed
  *     at once): also the read-only ones share the handle's buffers.  Different
  *     handles are independent.
- *   - no call allocates device memory except kivi_cache_create and a cache's
- *     first kivi_chunk_attn or kivi_prefill_attn_window that splits its work
- *     (see there).
+ *   - no call allocates device memory except kivi_cache_create,
+ *     kivi_latent_create and a cache's first kivi_chunk_attn,
+ *     kivi_prefill_attn_window or kivi_latent_attn that splits its work (see
+ *     there).
  * Supported shapes: k_bits, v_bits in {2, 4}; G in {16, 32, 64, 128};
  * d in {64, 128, 256} with d % G == 0; R % G == 0 (item 4's assertion);
  * 1 <= b <= 1024; h_q a multiple of h_kv with h_q / h_kv <= 8.
@@ -52,6 +53,7 @@ extern "C" {
 #define KIVI_ABI_VERSION 6
 
 typedef struct kivi_cache *kivi_cache_t;   /* opaque, library-owned */
+typedef struct kivi_latent *kivi_latent_t; /* the same: a latent cache */
 typedef struct CUstream_st *kivi_stream_t; /* the same type as cudaStream_t */
 
 typedef enum {
@@ -187,6 +189,131 @@ kivi_status kivi_append_chunk(kivi_cache_t c, const void *K, const void *V, cons
 kivi_status kivi_rope(const void *q, const void *k, int b, int h_q, int h_kv, int n_stride, int d, const int32_t *n,
                       const int32_t *pos0, const int32_t *pos, const uint64_t *turns, int rot_dim, int interleaved,
                       float factor, int inverse, void *q_out, void *k_out, kivi_stream_t stream);
+
+/* kivi_rope with several axes (an image's or a film's tokens: time, height,
+ * width): channel pair m turns by the angle p w_m with p the token's position on
+ * axis[m] (axis: HOST, rot_dim / 2 entries below axes).  pos: DEVICE int32
+ * [axes][b][n_stride]; any int32 position is valid.  1 <= axes <= 255; the rest
+ * as there, inverse (the gradient) included.  Tokens that stand at the same
+ * position on every axis (text) may go through kivi_rope. */
+kivi_status kivi_rope_axes(const void *q, const void *k, int b, int h_q, int h_kv, int n_stride, int d,
+                           const int32_t *n, const int32_t *pos, int axes, const uint8_t *axis, const uint64_t *turns,
+                           int rot_dim, int interleaved, float factor, int inverse, void *q_out, void *k_out,
+                           kivi_stream_t stream);
+
+/* Verification of drafted tokens against the target's probabilities, after the
+ * attention of a speculative step (kivi_chunk_attn, kivi_latent_attn) and before
+ * the kept tokens are appended.  Sequence i drafted n[i] tokens (n: HOST array of
+ * b int32, 0 <= n[i] <= n_stride), draft[i][r], from its own probabilities
+ * q[i][r][:]; p[i][r][:] are the target's at the same place, p[i][n[i]][:] those
+ * after the whole draft.  p: DEVICE [b][n_stride + 1][vocab], q: DEVICE
+ * [b][n_stride][vocab], fp32 or fp16 (bytes = 4 or 2); q == NULL: a draft without
+ * probabilities, each token certain.  u: DEVICE fp32 [b][n_stride + 1], uniform
+ * numbers in [0, 1).
+ *   Token r is kept while u[i][r] q[i][r][x] < p[i][r][x] (x = draft[i][r];
+ *   exact; never for a token outside the vocabulary).  At the first that is not,
+ *   one token is drawn from the weights max(p[i][r] - q[i][r], 0), or after n[i]
+ *   kept ones from p[i][n[i]], by u[i][n_stride].  Probabilities count in units
+ *   of 2^-40, rounded down (negative ones and NaN as 0, above 1 as 1); with W the
+ *   sum of the weights the token is the lowest whose weights up to and with it
+ *   exceed floor(floor(2^30 u) W / 2^30).  No weight left: drawn from p; none
+ *   there either: no token, -1.
+ * accepted[i] (DEVICE int32 [b]) is the number of kept tokens; tokens[i] (DEVICE
+ * int32 [b][n_stride + 1]) they, the drawn one behind them, then -1.  Only the
+ * row that is drawn from is read whole.  Outputs overlap no input.  One launch on
+ * the current device, no state.  vocab and n_stride up to 2^20. */
+kivi_status kivi_verify(const void *p, const void *q, int bytes, const int32_t *draft, const float *u, int b,
+                        int n_stride, int vocab, const int32_t *n, int32_t *tokens, int32_t *accepted,
+                        kivi_stream_t stream);
+
+/* Latent attention: keys and values of every head are products of one latent
+ * vector c_s [r] a token, and a rotary key kr_s [64] is shared by the heads.  Head
+ * e has Wk_e, Wv_e [128][r]; a query is qn [128] and qr [64]:
+ *   out_p = Wv_e sum_{s <= p} softmax_s(scale (qn . Wk_e c_s + qr . kr_s)) c_s.
+ * The cache holds c and kr; the newest R tokens' c in fp16, older ones' quantized
+ * as the KIVI values are (items 1 and 3: per token in groups of G channels), kr in
+ * fp16.  Two forms, the same sums:
+ *   absorbed (steps and chunks over the cache):
+ *     ql = kivi_head_product(qn, Wk, transposed), kivi_latent_attn(ql, qr) -> ol,
+ *     out = kivi_head_product(ol, Wv);
+ *   expanded (whole prompts): K, V = kivi_head_product(c of all heads, Wk, Wv),
+ *     kivi_latent_prompt_attn(qn, qr, K, kr, V), and kivi_latent_prefill.
+ * Handles are as kivi_cache_t: not thread-safe, no two calls on one at once on the
+ * GPU, poisoned by a CUDA error; the cache's device must be current
+ * (KIVI_ERR_INVALID_ARG).
+ *
+ * kivi_latent_create: an empty cache for b sequences of up to max_tokens tokens.
+ * r 256 or 512; bits 2 or 4; G 32, 64 or 128; R a positive multiple of 64 (R >=
+ * max_tokens: nothing is quantized); b <= 1024 (KIVI_ERR_UNSUPPORTED
+ * otherwise).  All device memory is allocated here but for kivi_latent_attn's
+ * partials. */
+kivi_status kivi_latent_create(int b, int r, int bits, int G, int R, int max_tokens, kivi_latent_t *out);
+kivi_status kivi_latent_destroy(kivi_latent_t c);
+
+/* Fill (every sequence starts anew with t[i] tokens) and append (n[i] more, 0
+ * leaves a sequence as it is): C fp16 [b][stride][r], Kr fp16 [b][stride][64]
+ * (device, 16-byte aligned), t and n HOST arrays of b int32 in [0, stride].
+ * Afterwards tokens [0, T - R) are quantized, whatever calls brought them.  Inputs
+ * finite.  KIVI_ERR_CAPACITY (and nothing changes) if a sequence would exceed
+ * max_tokens; stride <= 2^26.  One launch.  A captured append writes, when
+ * replayed, at the positions of the state that it was captured in: replay it only
+ * there. */
+kivi_status kivi_latent_prefill(kivi_latent_t c, const void *C, const void *Kr, const int32_t *t, int t_stride,
+                                kivi_stream_t stream);
+kivi_status kivi_latent_append(kivi_latent_t c, const void *C, const void *Kr, const int32_t *n, int n_stride,
+                               kivi_stream_t stream);
+
+/* The absorbed attention of n[i] new tokens of each sequence (positions T_i,
+ * T_i + 1, ...) over the cache as it stands and over themselves; read-only on the
+ * cache.  q fp16 [b][h][n_stride][r] (absorbed), q_rope fp16 [b][h][n_stride][64],
+ * C, Kr, n as for kivi_latent_append; out fp16 [b][h][n_stride][r] = sum of the
+ * weights times c, rows past n[i] not written; out overlaps no input.  scale is
+ * positive.  Restored latent vectors and weights are rounded to fp16 before the
+ * products (2^-11 of themselves, a weight or 2^-32 of the row's largest), sums in
+ * fp32, |restored c| below 65504.  One launch, or two where row tiles are cut and
+ * joined (repeatable bit for bit): the first such call allocates a buffer that the
+ * cache keeps (2 x SMs x 64 rows of r + 2 floats, 40 MB at r = 512; also while its
+ * stream is captured; without the memory KIVI_ERR_OOM).  A captured call replays
+ * with the counts it was captured with.  1 <= h <= 128, n_stride h < 2^24,
+ * b n_stride < 2^31 (KIVI_ERR_UNSUPPORTED otherwise). */
+kivi_status kivi_latent_attn(kivi_latent_t c, const void *q, const void *q_rope, const void *C, const void *Kr,
+                             const int32_t *n, int n_stride, int h, float scale, void *out, kivi_stream_t stream);
+
+/* Tokens of each sequence, and how many of them are quantized (HOST arrays of b
+ * int32; either may be NULL); the cache's rows as attention sees them, into C fp16
+ * [b][t_stride][r] and Kr fp16 [b][t_stride][64] (device; either may be NULL; rows
+ * past T_i not written); the status word, as kivi_cache_check. */
+kivi_status kivi_latent_lengths(kivi_latent_t c, int32_t *T, int32_t *Tq);
+kivi_status kivi_latent_restore(kivi_latent_t c, void *C, void *Kr, int t_stride, kivi_stream_t stream);
+kivi_status kivi_latent_check(kivi_latent_t c, uint32_t *flags, kivi_stream_t stream);
+
+/* A matrix of each head times rows of its own (h_x = h) or of all heads alike
+ * (h_x = 1): x fp16 [b][h_x][n_stride][K], out fp16 [b][h][n_stride][N], for the
+ * tokens s < n[i] (n: HOST array of b int32):
+ *   out[i][e][s] = W_e x[i][e or 0][s],
+ * w fp16 [h][N][K], or with transposed != 0 [h][K][N] (device, all 16-byte
+ * aligned).  Sums in fp32, rounded once.  Rows past n[i] are neither read nor
+ * written; out overlaps no input.  One launch on the current device, no state.  K a
+ * multiple of 64, N of 128, up to 16384; h <= 1024, b <= 1024, up to 2^30 tokens in
+ * all (KIVI_ERR_UNSUPPORTED otherwise). */
+kivi_status kivi_head_product(const void *x, const void *w, int b, int h_x, int h, int n_stride, const int32_t *n,
+                              int K, int N, int transposed, void *out, kivi_stream_t stream);
+
+/* The expanded attention of prompts: q fp16 [b][h][t_stride][128], q_rope fp16
+ * [b][h][t_stride][64], K and V fp16 [b][h][t_stride][128], Kr fp16
+ * [b][t_stride][64], out fp16 [b][h][t_stride][128]; for token p < t[i] (t: HOST
+ * array of b int32) causal over the tokens s <= p, scale as above.  Rows past t[i]
+ * of out are not written, of the inputs may hold anything.  Weights are rounded to
+ * fp16 (2^-11, or 2^-32 of the row's largest), sums in fp32.  out overlaps no input.
+ * One launch on the current device, no state.  h <= 1024, t_stride <= 2^26, b h
+ * t_stride < 2^31 (KIVI_ERR_UNSUPPORTED otherwise). */
+kivi_status kivi_latent_prompt_attn(const void *q, const void *q_rope, const void *K, const void *Kr, const void *V,
+                                    int b, int h, const int32_t *t, int t_stride, float scale, void *out,
+                                    kivi_stream_t stream);
+
+/* As kivi_cache_check, for the current device's calls that have no handle
+ * (kivi_head_product, kivi_latent_prompt_attn). */
+kivi_status kivi_device_check(uint32_t *flags, kivi_stream_t stream);
 
 /* Append one token to every sequence: k and v fp16 [b][h_kv][d] (device).
  * First, per sequence, the maintenance of item 4 left over from the previous
