@@ -10,10 +10,11 @@
 //
 // The rows of all sequences are one list (prefix sums of n), cut into tiles of
 // 128, so that a step of 64 sequences of one token fills half a tile a head. A
-// CTA makes 128 rows x 128 columns of one head: S = x W^T in tensor memory, 64
-// of K a stage; x by 16-byte asynchronous copies (any row of any sequence), W by
-// TMA as the operand lies in memory, K-major or N-major.  Two CTAs an SM, so
-// that one's first loads and last stores run under the other's products.
+// CTA makes 128 rows x 128 columns of one head: x W^T in tensor memory, 64 of K a
+// stage; x by 16-byte asynchronous copies (any row of any sequence), W by TMA as
+// the operand lies in memory, K-major or N-major, both in the 128-byte swizzle.
+// Two CTAs an SM, so that one's first loads and last stores run under the other's
+// products.
 #include <cstring>
 
 #include "../../include/kivi.h"
@@ -29,11 +30,8 @@ constexpr int kHpRows = 128, kHpCols = 128, kHpK = 64;
 constexpr int kHpStages = 3;
 constexpr int kHpThreads = 32 * 6;
 constexpr unsigned kHpFull = 0xffffffffu;
-// bytes from a 16-byte chunk of x's tile to the next: 64 more than 128 rows
-// take, so that a store of 4 rows x 2 chunks meets every bank once
-constexpr unsigned kHpAS = kHpRows * 16 + 64;
-constexpr int kHpA = kHpK / 8 * (int)kHpAS, kHpB = kHpK * kHpCols * 2;
-constexpr size_t kHpSmem = (size_t)kHpStages * (kHpA + kHpB) + 128;
+constexpr int kHpA = kHpK * kHpRows * 2, kHpB = kHpK * kHpCols * 2;
+constexpr size_t kHpSmem = (size_t)kHpStages * (kHpA + kHpB) + 1024;
 
 struct HeadArgs {
     const __half *x;
@@ -63,7 +61,7 @@ template <bool MN>
 __global__ void __launch_bounds__(kHpThreads, 2)
     head_product_kernel(const __grid_constant__ HeadArgs a, const __grid_constant__ CUtensorMap tm) {
     extern __shared__ unsigned char raw[];
-    unsigned char *sA = raw + ((128u - (smem_u32(raw) & 127u)) & 127u), *sB = sA + kHpStages * kHpA;
+    unsigned char *sA = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u), *sB = sA + kHpStages * kHpA;
     __shared__ __align__(8) uint64_t bars[3 * kHpStages + 1];
     uint64_t *const bA = bars, *const bB = bA + kHpStages, *const eS = bB + kHpStages, *const bD = eS + kHpStages;
     __shared__ uint32_t s_taddr;
@@ -85,16 +83,18 @@ __global__ void __launch_bounds__(kHpThreads, 2)
     bool ok = true;
 
     if (warp < 4) {
-        // x: a thread's two rows, a 16-byte chunk of every two
-        const __half *src[2];
-        bool in[2];
+        // x: a thread's 16-byte chunk of every 16th row
+        constexpr int NR = kHpRows / 16;
+        const __half *src[NR];
+        unsigned in = 0;
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const int row = row0 + (tid >> 1) + 64 * k;
-            in[k] = row < rows;
-            const int2 p = hp_row(a, in[k] ? row : row0);
-            src[k] = a.x + (((size_t)p.x * a.hx + (a.hx > 1 ? e : 0)) * a.n_stride + p.y) * a.K + 8 * (tid & 1);
+        for (int k = 0; k < NR; ++k) {
+            const int row = row0 + (tid >> 3) + 16 * k;
+            if (row < rows) in |= 1u << k;
+            const int2 p = hp_row(a, row < rows ? row : row0);
+            src[k] = a.x + (((size_t)p.x * a.hx + (a.hx > 1 ? e : 0)) * a.n_stride + p.y) * a.K + 8 * (tid & 7);
         }
+        const unsigned at = (tid >> 3) * 128 + (((tid & 7) ^ ((tid >> 3) & 7)) * 16);   // (16 rows further: the same chunk)
         auto told = [&](int it) {   // the stage's copies of this warp are in
             fence_proxy_async();
             __syncwarp();
@@ -104,12 +104,9 @@ __global__ void __launch_bounds__(kHpThreads, 2)
             const int s = it % kHpStages;
             ok = __all_sync(kHpFull, it < kHpStages || mbar_wait_ab(&eS[s], (unsigned)(it / kHpStages + 1) & 1u, abort));
             if (!ok) break;
-            unsigned char *dst = sA + s * kHpA + (tid & 1) * kHpAS + (tid >> 1) * 16;
+            unsigned char *dst = sA + s * kHpA + at;
 #pragma unroll
-            for (int c = 0; c < kHpK / 16; ++c)
-#pragma unroll
-                for (int k = 0; k < 2; ++k)
-                    hp_copy16(dst + 2 * c * kHpAS + k * 64 * 16, src[k] + it * kHpK + 16 * c, in[k]);
+            for (int k = 0; k < NR; ++k) hp_copy16(dst + k * 16 * 128, src[k] + it * kHpK, (in >> k) & 1u);
             asm volatile("cp.async.commit_group;" ::: "memory");
             if (it > 0) {
                 asm volatile("cp.async.wait_group 1;" ::: "memory");
@@ -154,12 +151,13 @@ __global__ void __launch_bounds__(kHpThreads, 2)
                 ok = it < kHpStages || mbar_wait_ab(&eS[s], (unsigned)(it / kHpStages + 1) & 1u, abort);
                 if (!ok) break;
                 mbar_expect_tx(&bB[s], kHpB);
-                const int r = MN ? e * a.K + it * kHpK : e * a.N + col0, c = (MN ? col0 : it * kHpK) / 8;
-                asm volatile(
-                    "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, "
-                    "{%2, %3, %4}], [%5];" ::"r"(smem_u32(sB + s * kHpB)),
-                    "l"(&tm), "r"(0), "r"(r), "r"(c), "r"(smem_u32(&bB[s]))
-                    : "memory");
+                unsigned char *dst = sB + s * kHpB;
+                if (MN) {   // 64 of K x 64 columns, twice
+                    tma_sw(dst, &tm, col0, e * a.K + it * kHpK, &bB[s]);
+                    tma_sw(dst + kHpB / 2, &tm, col0 + 64, e * a.K + it * kHpK, &bB[s]);
+                } else {
+                    tma_sw(dst, &tm, it * kHpK, e * a.N + col0, &bB[s]);
+                }
             }
             if (!ok) {
                 s_abort = 1;
@@ -171,8 +169,7 @@ __global__ void __launch_bounds__(kHpThreads, 2)
         __syncwarp();
     } else {
         constexpr uint32_t ID = tc_idesc_f16(kHpRows, kHpCols, MN ? 1 : 0);
-        const uint64_t da = tc_desc(sA, kHpAS, 128),
-                       db = MN ? tc_desc(sB, 128, kHpK * 16) : tc_desc(sB, kHpCols * 16, 128);
+        const uint64_t da = tc_desc_sw(sA, 16, 1024), db = MN ? tc_desc_sw(sB, kHpB / 2, 1024) : tc_desc_sw(sB, 16, 1024);
         int it = 0;
         for (; it < nk; ++it) {
             const int s = it % kHpStages;
@@ -182,8 +179,8 @@ __global__ void __launch_bounds__(kHpThreads, 2)
             tc_fence_after();
 #pragma unroll
             for (int c = 0; c < kHpK / 16; ++c)
-                tc_mma_f16_w(taddr, da + (uint32_t)((s * kHpA + 2 * c * kHpAS) >> 4),
-                             db + (uint32_t)((s * kHpB + (MN ? 256 * c : 2 * c * kHpCols * 16)) >> 4), ID, it > 0 || c > 0);
+                tc_mma_f16_w(taddr, da + (uint32_t)((s * kHpA + 32 * c) >> 4),
+                             db + (uint32_t)((s * kHpB + (MN ? 2048 : 32) * c) >> 4), ID, it > 0 || c > 0);
             tc_commit_w(&eS[s]);
         }
         if (!ok && lane == 0) {
@@ -199,21 +196,6 @@ __global__ void __launch_bounds__(kHpThreads, 2)
     tc_fence_before();
     __syncthreads();
     if (warp == 0) tc_dealloc(taddr, kHpCols);
-}
-
-// Tensor map over fp16 [rows][cols] whose boxes are box_rows rows x box_chunks
-// 16-byte chunks, chunk-major.
-cudaError_t make_box_map(CUtensorMap *tm, const __half *base, long long rows, int cols, int box_rows, int box_chunks) {
-    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
-    if (!enc) return cudaErrorNotSupported;
-    const cuuint64_t dim[3] = {8, (cuuint64_t)rows, (cuuint64_t)(cols / 8)};
-    const cuuint64_t str[2] = {(cuuint64_t)cols * 2, 16};
-    const cuuint32_t box[3] = {8, (cuuint32_t)box_rows, (cuuint32_t)box_chunks};
-    const cuuint32_t es[3] = {1, 1, 1};
-    const CUresult r = enc(tm, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<__half *>(base), dim, str, box, es,
-                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
-                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
 kivi_status fail(kivi_status s, const char *msg) {
@@ -259,8 +241,8 @@ extern "C" kivi_status kivi_head_product(const void *x, const void *w, int b, in
     if (!a.status) return fail(KIVI_ERR_CUDA, "no status word on the current device");
     const bool mn = transposed != 0;
     CUtensorMap tm;
-    cudaError_t e = mn ? make_box_map(&tm, (const __half *)w, (long long)h * K, N, kHpK, kHpCols / 8)
-                       : make_box_map(&tm, (const __half *)w, (long long)h * N, K, kHpCols, kHpK / 8);
+    cudaError_t e = mn ? make_sw_map(&tm, (const __half *)w, (long long)h * K, N, kHpK)
+                       : make_sw_map(&tm, (const __half *)w, (long long)h * N, K, kHpCols);
     const auto kernel = mn ? head_product_kernel<true> : head_product_kernel<false>;
     if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kHpSmem);
     if (e != cudaSuccess) return fail(KIVI_ERR_CUDA, cudaGetErrorString(e));

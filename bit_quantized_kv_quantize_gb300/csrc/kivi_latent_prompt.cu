@@ -29,7 +29,8 @@ constexpr int kLpRows = 128, kLpKeys = KIVI_KBLK, kLpStages = 3;
 constexpr int kLpQK = kLatHead + kLatRope;
 constexpr int kLpThreads = 32 * 12;
 constexpr int kLpQ = kLpRows * kLpQK * 2, kLpK = kLpKeys * kLpQK * 2, kLpV = kLpKeys * kLatHead * 2;
-constexpr size_t kLpSmem = (size_t)2 * kLpQ + (size_t)kLpStages * (kLpK + kLpV);
+constexpr size_t kLpSmem = (size_t)2 * kLpQ + (size_t)kLpStages * (kLpK + kLpV) + 1024;
+constexpr int kLpQs = kLpRows * 128, kLpKs = kLpKeys * 128;   // a tile of 64 channels (bytes)
 
 struct PromptArgs {
     __half *out;
@@ -65,9 +66,9 @@ __global__ void __launch_bounds__(kLpThreads, 1)
     latent_prompt_kernel(const __grid_constant__ CUtensorMap tmQn, const __grid_constant__ CUtensorMap tmQr,
                          const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmKr,
                          const __grid_constant__ CUtensorMap tmV, const __grid_constant__ PromptArgs a) {
-    extern __shared__ __align__(128) unsigned char smem[];
+    extern __shared__ unsigned char raw[];
+    unsigned char *const smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
     constexpr int KS = kLpStages;
-    constexpr unsigned QLBO = kLpRows * 16, KLBO = kLpKeys * 16;
     const int bh = a.b * a.h, pair = blockIdx.x % bh, m = a.mt - 1 - blockIdx.x / bh, i = pair / a.h;
     const int n = a.t[i], row0 = m * 2 * kLpRows;
     if (row0 >= n) return;
@@ -104,7 +105,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
         const int e = __shfl_sync(kFull, warp - 8, 0), mine = e ? nx1 : nx0;
         constexpr uint32_t ID = tc_idesc_f16(kLpRows, kLpKeys, 0);
         CkRing t;
-        const uint64_t dq = tc_desc(sQ + e * kLpQ, QLBO, 128), dk = tc_desc(sK, KLBO, 128);
+        const uint64_t dq = tc_desc_sw(sQ + e * kLpQ, 16, 1024), dk = tc_desc_sw(sK, 16, 1024);
         for (int x = 0; x < nx && ok; ++x, t.next(KS)) {
             ok = __all_sync(kFull, mbar_wait_ab(&bK[t.s], t.p, abort));
             if (!ok) break;
@@ -119,7 +120,8 @@ __global__ void __launch_bounds__(kLpThreads, 1)
             const uint64_t d = dk + (uint32_t)(t.s * (kLpK >> 4));
 #pragma unroll
             for (int c = 0; c < kLpQK / 16; ++c)
-                tc_mma_f16_w(taddr + 256 * e, dq + ((2 * c * QLBO) >> 4), d + ((2 * c * KLBO) >> 4), ID, c > 0);
+                tc_mma_f16_w(taddr + 256 * e, dq + (((c >> 2) * kLpQs + (c & 3) * 32) >> 4),
+                             d + (((c >> 2) * kLpKs + (c & 3) * 32) >> 4), ID, c > 0);
             tc_commit_w(&bS[e]);
             tc_commit_w(&eK[t.s]);
         }
@@ -135,7 +137,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
         // ---- O += P V ----
         constexpr uint32_t ID = tc_idesc_f16(kLpRows, kLatHead, 1);
         CkRing t;
-        const uint64_t dv = tc_desc(sV, 128, KLBO);
+        const uint64_t dv = tc_desc_sw(sV, kLpKs, 1024);
         for (int x = 0; x < nx && ok; ++x, t.next(KS)) {
             const uint64_t d = dv + (uint32_t)(t.s * (kLpV >> 4));
             ok = __all_sync(kFull, mbar_wait_ab(&bV[t.s], t.p, abort));
@@ -148,7 +150,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
                 tc_fence_after();
 #pragma unroll
                 for (int c = 0; c < kLpKeys / 16; ++c)
-                    tc_mma_f16_ta_w(taddr + 256 * e + 128, taddr + 256 * e + 64 + 32 * b + 8 * c, d + ((256 * c) >> 4), ID,
+                    tc_mma_f16_ta_w(taddr + 256 * e + 128, taddr + 256 * e + 64 + 32 * b + 8 * c, d + ((2048 * c) >> 4), ID,
                                     x > 0 || c > 0);
                 tc_commit_w(&bF[2 * e + b]);
             }
@@ -168,8 +170,8 @@ __global__ void __launch_bounds__(kLpThreads, 1)
             for (int e = 0; e < 2; ++e) {
                 if (e && nx1 == 0) break;
                 mbar_expect_tx(&bQ[e], kLpQ);
-                tma_box(sQ + e * kLpQ, &tmQn, q0 + row0 + e * kLpRows, &bQ[e]);
-                tma_box(sQ + e * kLpQ + kLatHead / 8 * QLBO, &tmQr, q0 + row0 + e * kLpRows, &bQ[e]);
+                for (int c = 0; c < 3; ++c)
+                    tma_sw(sQ + e * kLpQ + c * kLpQs, c < 2 ? &tmQn : &tmQr, c < 2 ? 64 * c : 0, q0 + row0 + e * kLpRows, &bQ[e]);
             }
         __syncwarp();
         CkRing t;
@@ -180,8 +182,8 @@ __global__ void __launch_bounds__(kLpThreads, 1)
                 ok = x < KS || mbar_wait_ab(&eK[t.s], t.p ^ 1u, abort);
                 if (ok) {
                     mbar_expect_tx(&bK[t.s], kLpK);
-                    tma_box(sK + t.s * kLpK, &tmK, q0 + tb, &bK[t.s]);
-                    tma_box(sK + t.s * kLpK + kLatHead / 8 * KLBO, &tmKr, i * a.t_stride + tb, &bK[t.s]);
+                    for (int c = 0; c < 2; ++c) tma_sw(sK + t.s * kLpK + c * kLpKs, &tmK, 64 * c, q0 + tb, &bK[t.s]);
+                    tma_sw(sK + t.s * kLpK + 2 * kLpKs, &tmKr, 0, i * a.t_stride + tb, &bK[t.s]);
                     ++ck;
                     ok = x < KS || mbar_wait_ab(&eV[t.s], t.p ^ 1u, abort);
                 }
@@ -189,7 +191,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
                     // (the last tile's rows behind the sequence are zeroed first)
                     uint64_t *const bar = tb + kLpKeys > n ? bT : &bV[t.s];
                     mbar_expect_tx(bar, kLpV);
-                    tma_box(sV + t.s * kLpV, &tmV, q0 + tb, bar);
+                    for (int c = 0; c < 2; ++c) tma_sw(sV + t.s * kLpV + c * kLpKs, &tmV, 64 * c, q0 + tb, bar);
                     ++cv;
                 }
             }
@@ -197,9 +199,9 @@ __global__ void __launch_bounds__(kLpThreads, 1)
             if (ok && tb + kLpKeys > n) {
                 ok = __all_sync(kFull, mbar_wait_ab(bT, 0u, abort));
                 if (ok) {
-                    const int rows = tb + kLpKeys - n;
-                    for (int y = lane; y < rows * (kLatHead / 8); y += 32)
-                        *reinterpret_cast<uint4 *>(sV + t.s * kLpV + (y / rows) * KLBO + (n - tb + y % rows) * 16) =
+                    const int c16 = (tb + kLpKeys - n) * 8;   // 16-byte chunks of 64 channels
+                    for (int y = lane; y < 2 * c16; y += 32)
+                        *reinterpret_cast<uint4 *>(sV + t.s * kLpV + (y / c16) * kLpKs + (n - tb) * 128 + y % c16 * 16) =
                             make_uint4(0u, 0u, 0u, 0u);
                     fence_proxy_async();
                     __syncwarp();
@@ -385,11 +387,11 @@ extern "C" kivi_status kivi_latent_prompt_attn(const void *q, const void *q_rope
     if (!a.status) return fail(KIVI_ERR_CUDA, "no status word on the current device");
     const long long rows = (long long)b * h * t_stride;
     CUtensorMap tq, tqr, tk, tkr, tv;
-    cudaError_t e = make_tile_map(&tq, (const __half *)q, rows, kLatHead, kLpRows);
-    if (e == cudaSuccess) e = make_tile_map(&tqr, (const __half *)q_rope, rows, kLatRope, kLpRows);
-    if (e == cudaSuccess) e = make_tile_map(&tk, (const __half *)K, rows, kLatHead, kLpKeys);
-    if (e == cudaSuccess) e = make_tile_map(&tkr, (const __half *)Kr, (long long)b * t_stride, kLatRope, kLpKeys);
-    if (e == cudaSuccess) e = make_tile_map(&tv, (const __half *)V, rows, kLatHead, kLpKeys);
+    cudaError_t e = make_sw_map(&tq, (const __half *)q, rows, kLatHead, kLpRows);
+    if (e == cudaSuccess) e = make_sw_map(&tqr, (const __half *)q_rope, rows, kLatRope, kLpRows);
+    if (e == cudaSuccess) e = make_sw_map(&tk, (const __half *)K, rows, kLatHead, kLpKeys);
+    if (e == cudaSuccess) e = make_sw_map(&tkr, (const __half *)Kr, (long long)b * t_stride, kLatRope, kLpKeys);
+    if (e == cudaSuccess) e = make_sw_map(&tv, (const __half *)V, rows, kLatHead, kLpKeys);
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(latent_prompt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kLpSmem);
     if (e != cudaSuccess) return fail(KIVI_ERR_CUDA, cudaGetErrorString(e));

@@ -23,6 +23,15 @@ __device__ __forceinline__ uint64_t tc_desc(const void *base, unsigned lbo, unsi
     return (uint64_t)((a >> 4) & 0x3FFFu) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
            ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | ((uint64_t)1 << 46);
 }
+// ... of tiles in the 128-byte swizzle: rows of 128 bytes (64 fp16), 8 of them an
+// atom of 1024 bytes (to which the tile is aligned), 16-byte chunk c of row r at
+// chunk c ^ (r mod 8), as TMA writes them.  K-major: rows along M / N, sbo from 8
+// rows to the next 8, lbo not used; 32 bytes further is the next 16 of K.
+// MN-major: rows along K, sbo from 8 of K to the next 8, lbo from 64 of M / N to the
+// next.  (TMA takes a 16-byte row of the no-swizzle layout as long as one of 128.)
+__device__ __forceinline__ uint64_t tc_desc_sw(const void *base, unsigned lbo, unsigned sbo) {
+    return tc_desc(base, lbo, sbo) | ((uint64_t)2 << 61);
+}
 // instruction descriptor of kind::f16: fp16 A and B, fp32 accumulator, A
 // K-major, B K-major (b_mn = 0) or MN-major (1), M x N
 __host__ __device__ constexpr uint32_t tc_idesc_f16(int M, int N, int b_mn) {

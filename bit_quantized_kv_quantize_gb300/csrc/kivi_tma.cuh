@@ -64,6 +64,29 @@ cudaError_t make_tile_map(CUtensorMap *tm, const __half *base, long long rows, i
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// Tensor map over an fp16 [rows][cols] array giving tiles of box_rows rows x 64
+// columns in the 128-byte swizzle.
+cudaError_t make_sw_map(CUtensorMap *tm, const __half *base, long long rows, int cols, int box_rows) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (!enc) return cudaErrorNotSupported;
+    const cuuint64_t dim[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    const cuuint64_t str[1] = {(cuuint64_t)cols * 2};
+    const cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
+    const cuuint32_t es[2] = {1, 1};
+    const CUresult r = enc(tm, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<__half *>(base), dim, str, box, es,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+// one such tile, from row row0 and column col0 (a multiple of 8) on
+__device__ __forceinline__ void tma_sw(void *dst, const CUtensorMap *tm, int col0, int row0, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+        "[%4];" ::"r"(smem_u32(dst)),
+        "l"(tm), "r"(col0), "r"(row0), "r"(smem_u32(bar))
+        : "memory");
+}
+
 // Tensor map over queries [heads / hg][hg][n][D] whose boxes are 128 rows
 // (token r, head e of a group), e fastest, in chunk-major order: dimensions
 // (8, hg, n, D / 8, heads / hg), box (8, hg, 128 / hg, D / 8, 1).
