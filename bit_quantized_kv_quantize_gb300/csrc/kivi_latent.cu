@@ -15,12 +15,12 @@ namespace {
 __device__ unsigned g_status;   // of the calls without a handle
 
 // ---------------------------------------------------------------------------
-// Append.  A warp takes new token tau = T + x.  Where R newer ones follow, tau
-// goes straight to codes; otherwise it goes into the ring, and the cached token
-// whose place it takes (a multiple of R before it: n may be above R) leaves the
-// window and is quantized first.  The R last tokens take every place that a
-// cached one leaves, and no warp reads a place that another writes.  Lane l holds
-// channels [r / 32 l, ..); a group's bounds by exchanges among its lanes.
+// Append.  Warp x takes new token tau = T + x: straight to codes where R newer
+// ones follow, else into the ring.  The cached tokens that leave the window,
+// [Tq, Tq1) below T, are quantized from the ring: one whose place a new token
+// takes (it is a multiple of the ring's size before it; n may be larger than
+// that) by that token's warp, before it is overwritten; of the others the x-th by
+// warp x.  So no warp reads a place that another writes.
 //
 // Bound: memory (2 r + 128 bytes read a token, its codes or 16-bit rows
 // written), for single tokens the latency of one round trip.
@@ -40,18 +40,18 @@ struct LatRow {
     __device__ __forceinline__ void load_block(const __half *blk, int t, int lane) {
 #pragma unroll
         for (int k = 0; k < CH / 8; ++k)
-            v[k] = *reinterpret_cast<const uint4 *>(blk + ((size_t)(CH / 8 * lane + k) * KIVI_KBLK + t) * 8);
+            v[k] = *reinterpret_cast<const uint4 *>((const char *)blk + lat_at(CH / 8 * lane + k, t, kLatTok));
     }
     __device__ __forceinline__ void store_block(__half *blk, int t, int lane) const {
 #pragma unroll
         for (int k = 0; k < CH / 8; ++k)
-            *reinterpret_cast<uint4 *>(blk + ((size_t)(CH / 8 * lane + k) * KIVI_KBLK + t) * 8) = v[k];
+            *reinterpret_cast<uint4 *>((char *)blk + lat_at(CH / 8 * lane + k, t, kLatTok)) = v[k];
     }
 };
 
-// the row as codes, scales and zeros of token t of a record
+// the row as codes, scales and zeros of token t of a record; row: as they restore it
 template <int CH, int BITS>
-__device__ __forceinline__ void lat_quantize(const LatentGeom &g, unsigned char *rec, int t, const LatRow<CH> &row) {
+__device__ __forceinline__ void lat_quantize(const LatentGeom &g, unsigned char *rec, int t, LatRow<CH> &row) {
     const int lane = threadIdx.x & 31, gl = g.G / CH;   // lanes a group
     float x[CH];
 #pragma unroll
@@ -74,14 +74,18 @@ __device__ __forceinline__ void lat_quantize(const LatentGeom &g, unsigned char 
     const QParams p = qparams(mn, mx, BITS);
     const float rs = __fdiv_rn(1.f, p.sf);
     if (lane % gl == 0)
-        *reinterpret_cast<__half2 *>(rec + g.off_sz + ((lane / gl) * KIVI_KBLK + t) * 4) = __halves2half2(p.s16, p.z16);
+        *reinterpret_cast<__half2 *>(rec + g.off_sz + ((lane / gl) * kLatTok + t) * 4) = __halves2half2(p.s16, p.z16);
     constexpr int PW = 32 / BITS, NW = (CH + PW - 1) / PW;   // channels a 32-bit word, words a lane (of 2 bits and 8 channels: half a word)
     uint32_t w[NW];
 #pragma unroll
     for (int k = 0; k < NW; ++k) w[k] = 0;
 #pragma unroll
-    for (int k = 0; k < CH; ++k)
-        w[k / PW] |= qcode_rcp(x[k], p.sf, p.zf, rs, BITS) << (16 * (k & 1) + BITS * ((k % PW) >> 1));
+    for (int k = 0; k < CH; k += 2) {
+        const uint32_t q0 = qcode_rcp(x[k], p.sf, p.zf, rs, BITS), q1 = qcode_rcp(x[k + 1], p.sf, p.zf, rs, BITS);
+        w[k / PW] |= (q0 | q1 << 16) << (BITS * ((k % PW) >> 1));
+        const __half2 y = __hfma2(__halves2half2(__uint2half_rn(q0), __uint2half_rn(q1)), __half2half2(p.s16), __half2half2(p.z16));
+        reinterpret_cast<uint32_t *>(row.v)[k / 2] = *reinterpret_cast<const uint32_t *>(&y);
+    }
     if (CH < PW) {   // two lanes share a word
         w[0] <<= BITS * (CH / 2) * (lane & 1);
         w[0] |= __shfl_xor_sync(0xffffffffu, w[0], 1);
@@ -90,7 +94,7 @@ __device__ __forceinline__ void lat_quantize(const LatentGeom &g, unsigned char 
 #pragma unroll
     for (int k = 0; k < NW; ++k) {
         const int wi = CH * lane / PW + k;   // 32-bit word of the token
-        *reinterpret_cast<uint32_t *>(rec + ((wi >> 2) * KIVI_KBLK + t) * 16 + (wi & 3) * 4) = w[k];
+        *reinterpret_cast<uint32_t *>(rec + ((wi >> 2) * kLatTok + t) * 16 + (wi & 3) * 4) = w[k];
     }
 }
 
@@ -101,20 +105,30 @@ __global__ void __launch_bounds__(32 * kApWarps)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int i = blockIdx.y, x = blockIdx.x * kApWarps + warp, n = a.n[i], T = a.T[i];
     if (x >= n) return;
-    const int tau = T + x, Tq1 = lat_tq(T + n, g.R);
-    const int out = tau - (tau - T + g.R) / g.R * g.R;   // the last of tau - R, tau - 2 R, .. that is cached
+    const int tau = T + x, Tq = lat_tq(T, g.R), Tq1 = lat_tq(T + n, g.R), W = g.ring * kLatTok;
     const size_t src = (size_t)i * a.n_stride + x;
-    LatRow<CH> row, old;
+    LatRow<CH> row;
     row.load(C + src * g.r, lane);
     const uint32_t key = *reinterpret_cast<const uint32_t *>(Kr + src * kLatRope + 2 * lane);
-    if (tau >= Tq1 && out >= 0) {   // (in [T - R, T): it was in the window)
-        old.load_block(dv.ring + lat_ring(g, i, out / KIVI_KBLK), out % KIVI_KBLK, lane);
-        lat_quantize<CH, BITS>(g, dv.rec + lat_rec(g, i, out / KIVI_KBLK), out % KIVI_KBLK, old);
-    }
-    if (tau >= Tq1) row.store_block(dv.ring + lat_ring(g, i, tau / KIVI_KBLK), tau % KIVI_KBLK, lane);
-    else lat_quantize<CH, BITS>(g, dv.rec + lat_rec(g, i, tau / KIVI_KBLK), tau % KIVI_KBLK, row);
-    *reinterpret_cast<uint32_t *>(dv.kr + lat_kr(g, i, tau / KIVI_KBLK) + ((lane >> 2) * KIVI_KBLK + tau % KIVI_KBLK) * 8 +
-                                  (lane & 3) * 2) = key;
+    // token o to codes; in the block of Tq1 the ring keeps it, as they restore it
+    // (no new token's place: the ring is long enough)
+    auto quantize = [&](int o, LatRow<CH> &r) {
+        lat_quantize<CH, BITS>(g, dv.rec + lat_rec(g, i, o / kLatTok), o % kLatTok, r);
+        if (o / kLatTok == Tq1 / kLatTok) r.store_block(dv.ring + lat_ring(g, i, o / kLatTok), o % kLatTok, lane);
+    };
+    auto leave = [&](int o) {   // cached token o leaves the window
+        LatRow<CH> old;
+        old.load_block(dv.ring + lat_ring(g, i, o / kLatTok), o % kLatTok, lane);
+        quantize(o, old);
+    };
+    const int own = Tq + x, first = max(T, Tq1);   // the x-th to leave; the first that goes into the ring
+    if (own < min(T, Tq1) && own + (first - own + W - 1) / W * W >= T + n) leave(own);
+    const int under = tau - (x + W) / W * W;       // the last token before T in tau's place
+    if (tau >= Tq1 && under >= Tq) leave(under);
+    if (tau >= Tq1) row.store_block(dv.ring + lat_ring(g, i, tau / kLatTok), tau % kLatTok, lane);
+    else quantize(tau, row);
+    *reinterpret_cast<uint32_t *>((char *)(dv.kr + lat_kr(g, i, tau / kLatTok)) + lat_at(lane >> 2, tau % kLatTok, kLatTok) +
+                                  (lane & 3) * 4) = key;
 }
 
 // The cache as attention sees it: 8 channels a thread.
@@ -124,24 +138,24 @@ __global__ void latent_restore_kernel(LatentGeom g, LatentDev dv, __half *__rest
     const long long e = (long long)blockIdx.x * blockDim.x + threadIdx.x;
     const int tau = (int)(e / per), c = (int)(e % per);
     if (tau >= a.T[i]) return;
-    const int kb = tau / KIVI_KBLK, t = tau % KIVI_KBLK;
+    const int kb = tau / kLatTok, t = tau % kLatTok;
     const size_t row = (size_t)i * a.n_stride + tau;
     if (c >= g.r / 8) {
         const int k = c - g.r / 8;
         if (Kr)
             *reinterpret_cast<uint4 *>(Kr + row * kLatRope + 8 * k) =
-                *reinterpret_cast<const uint4 *>(dv.kr + lat_kr(g, i, kb) + (k * KIVI_KBLK + t) * 8);
+                *reinterpret_cast<const uint4 *>((const char *)(dv.kr + lat_kr(g, i, kb)) + lat_at(k, t, kLatTok));
         return;
     }
     if (!C) return;
     uint4 v;
     if (tau >= lat_tq(a.T[i], g.R)) {
-        v = *reinterpret_cast<const uint4 *>(dv.ring + lat_ring(g, i, kb) + ((size_t)c * KIVI_KBLK + t) * 8);
+        v = *reinterpret_cast<const uint4 *>((const char *)(dv.ring + lat_ring(g, i, kb)) + lat_at(c, t, kLatTok));
     } else {
         const unsigned char *rec = dv.rec + lat_rec(g, i, kb);
-        const __half2 sz = *reinterpret_cast<const __half2 *>(rec + g.off_sz + ((8 * c / g.G) * KIVI_KBLK + t) * 4);
+        const __half2 sz = *reinterpret_cast<const __half2 *>(rec + g.off_sz + ((8 * c / g.G) * kLatTok + t) * 4);
         const int PW = 32 / g.bits, wi = 8 * c / PW, f0 = (8 * c % PW) >> 1, m = (1 << g.bits) - 1;
-        const uint32_t w = *reinterpret_cast<const uint32_t *>(rec + ((wi >> 2) * KIVI_KBLK + t) * 16 + (wi & 3) * 4);
+        const uint32_t w = *reinterpret_cast<const uint32_t *>(rec + ((wi >> 2) * kLatTok + t) * 16 + (wi & 3) * 4);
         uint32_t *h = reinterpret_cast<uint32_t *>(&v);
         for (int k = 0; k < 4; ++k) {
             const int lo = (w >> (g.bits * (f0 + k))) & m, hi = (w >> (16 + g.bits * (f0 + k))) & m;
@@ -278,7 +292,7 @@ kivi_status kivi_latent_create(int b, int r, int bits, int G, int R, int max_tok
     if (r != 256 && r != 512) return fail(KIVI_ERR_UNSUPPORTED, "r must be 256 or 512");
     if (bits != 2 && bits != 4) return fail(KIVI_ERR_UNSUPPORTED, "bits must be 2 or 4");
     if (G != 32 && G != 64 && G != 128) return fail(KIVI_ERR_UNSUPPORTED, "G must be 32, 64 or 128");
-    if (R % KIVI_KBLK != 0) return fail(KIVI_ERR_UNSUPPORTED, "R must be a multiple of 64");
+    if (R % 64 != 0) return fail(KIVI_ERR_UNSUPPORTED, "R must be a multiple of 64");
     if (max_tokens > (1 << 30)) return fail(KIVI_ERR_UNSUPPORTED, "max_tokens above 2^30");
     kivi_latent *c = new (std::nothrow) kivi_latent();
     if (!c) return fail(KIVI_ERR_OOM, "host allocation failed");
@@ -294,10 +308,11 @@ kivi_status kivi_latent_create(int b, int r, int bits, int G, int R, int max_tok
     g.r = r;
     g.bits = bits;
     g.G = G;
-    g.blocks = (max_tokens + KIVI_KBLK - 1) / KIVI_KBLK;
-    g.R = R < g.blocks * KIVI_KBLK ? R : g.blocks * KIVI_KBLK;   // (a window that holds every token)
-    g.off_sz = KIVI_KBLK * r * bits / 8;
-    g.rec_bytes = g.off_sz + r / G * KIVI_KBLK * 4;
+    g.blocks = (max_tokens + kLatTok - 1) / kLatTok;
+    g.R = R < g.blocks * kLatTok ? R : g.blocks * kLatTok;   // (a window that holds every token)
+    g.ring = (g.R + kLatTok - 1) / kLatTok + 1;   // (a window's tokens and those before them in their first block)
+    g.off_sz = kLatTok * r * bits / 8;
+    g.rec_bytes = g.off_sz + r / G * kLatTok * 4;
     cudaError_t e = cudaGetDevice(&c->device);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&c->num_sms, cudaDevAttrMultiProcessorCount, c->device);
     if (e != cudaSuccess) {
@@ -306,8 +321,8 @@ kivi_status kivi_latent_create(int b, int r, int bits, int G, int R, int max_tok
     }
     struct Req { void **p; size_t bytes; } reqs[] = {
         {(void **)&c->dv.rec, (size_t)b * g.blocks * g.rec_bytes},
-        {(void **)&c->dv.ring, (size_t)b * g.R * r * 2},
-        {(void **)&c->dv.kr, (size_t)b * g.blocks * KIVI_KBLK * kLatRope * 2},
+        {(void **)&c->dv.ring, (size_t)b * g.ring * kLatTok * r * 2},
+        {(void **)&c->dv.kr, (size_t)b * g.blocks * kLatTok * kLatRope * 2},
         {(void **)&c->dv.status, 4},
     };
     for (auto &q : reqs) {
@@ -376,8 +391,8 @@ kivi_status kivi_latent_attn(kivi_latent_t c, const void *q, const void *q_rope,
     if (!q || !q_rope || !out) return fail(KIVI_ERR_INVALID_ARG, "q, q_rope or out is null");
     if (!aligned16(q) || !aligned16(q_rope) || !aligned16(out))
         return fail(KIVI_ERR_INVALID_ARG, "q, q_rope and out must be 16-byte aligned");
-    if ((long long)n_stride * h >= (1LL << 24)) return fail(KIVI_ERR_UNSUPPORTED, "n_stride h must be below 2^24");
     if ((long long)c->g.b * n_stride >= (1LL << 31)) return fail(KIVI_ERR_UNSUPPORTED, "b n_stride must be below 2^31");
+    if ((long long)n_stride * h >= (1LL << 24)) return fail(KIVI_ERR_UNSUPPORTED, "n_stride h must be below 2^24");
     ChunkArgs a;
     for (int i = 0; i < c->g.b; ++i) {
         a.T[i] = c->T[i];

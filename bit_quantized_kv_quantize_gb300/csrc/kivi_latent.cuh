@@ -4,27 +4,31 @@
 // Per sequence the cache holds each token's latent vector c [r] and rotary key
 // kr [64].  Tokens [0, Tq) are quantized, a token's groups of G channels with an
 // fp16 scale and zero each (the value side of the KIVI quantizer); the newest
-// R, [Tq, T), are fp16.  Device memory, tokens in blocks of 64 (R and the
-// capacity are multiples of 64, so a block of tokens is a block of memory):
+// R, [Tq, T), are fp16.  Device memory, tokens in blocks of 128 (an attention
+// tile):
 //   records  [b][blocks]: codes, then scales and zeros.  16-byte words of codes
-//            [r bits / 128][64 tokens]: word x of a token covers channels
+//            [r bits / 128][128 tokens]: word x of a token covers channels
 //            (128 / bits) x ..  In each 32-bit word (16-bit half h, field f of
 //            `bits` bits) is the code of channel 2 f + h of the word's 32 /
-//            bits.  Scale and zero, a half2, [r / G][64 tokens].
-//   ring     [b][R / 64] and rotary keys [b][blocks]: fp16 blocks in the tensor
-//            cores' core-matrix layout, [channels / 8][64 tokens][8 channels]:
-//            a block is copied into an attention tile as it is.  Token tau of
-//            the ring is at block (tau / 64) mod (R / 64).
+//            bits.  Scale and zero, a half2, [r / G][128 tokens].
+//   ring     [b][ring blocks] and rotary keys [b][blocks]: fp16 blocks as an
+//            attention tile holds them (lat_at), so that a block is copied into
+//            one as it is.  Token tau of the window is in the ring's block
+//            (tau / 128) mod (ring blocks).  The block of Tq holds its quantized
+//            tokens too, as their codes restore them: every block from Tq / 128 on
+//            is there whole.
 #pragma once
 #include "kivi_chunk.cuh"
 #include "kivi_internal.cuh"
 
+constexpr int kLatTok = 128;    // tokens of a block
 constexpr int kLatRope = 64;    // channels of the rotary key
 constexpr int kLatHead = 128;   // channels of a head's other keys, and of its values
 
 struct LatentGeom {
     int b, r, bits, G, R;
-    int blocks;      // of 64 tokens, a sequence
+    int blocks;      // of a sequence
+    int ring;        // blocks of its ring
     int off_sz;      // scales and zeros in a record (bytes)
     int rec_bytes;
 };
@@ -39,11 +43,16 @@ __host__ __device__ __forceinline__ size_t lat_rec(const LatentGeom &g, int i, i
 }
 // a block of the ring, of the rotary keys (halves)
 __host__ __device__ __forceinline__ size_t lat_ring(const LatentGeom &g, int i, int kb) {
-    const int nr = g.R / KIVI_KBLK;
-    return ((size_t)i * nr + kb % nr) * KIVI_KBLK * g.r;
+    return ((size_t)i * g.ring + kb % g.ring) * kLatTok * g.r;
 }
 __host__ __device__ __forceinline__ size_t lat_kr(const LatentGeom &g, int i, int kb) {
-    return ((size_t)i * g.blocks + kb) * KIVI_KBLK * kLatRope;
+    return ((size_t)i * g.blocks + kb) * kLatTok * kLatRope;
+}
+// Byte of 16-byte chunk c (8 channels) of row t of a block: 64 channels of every
+// row together, a row 128 bytes, its chunks in the 128-byte swizzle (which the
+// tensor cores read along either axis at their full rate).
+__host__ __device__ __forceinline__ unsigned lat_at(int c, int t, int rows) {
+    return (unsigned)((c >> 3) * rows * 128 + t * 128 + (((c ^ t) & 7) << 4));
 }
 // quantized tokens of T
 __host__ __device__ __forceinline__ int lat_tq(int T, int R) { return T > R ? T - R : 0; }

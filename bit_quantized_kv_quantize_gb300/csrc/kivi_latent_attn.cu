@@ -6,26 +6,30 @@
 // row t_s = [c_s ; kr_s], head h of the token at position p has
 //   out = sum_s softmax_s(scale q . t_s) c_s   over s <= p:
 // one key and value row a token for every head.  So the rows (token, head) of a
-// sequence are one list, cut into row tiles of 64, and a tile of 64 tokens,
-// restored once to fp16 in shared memory, is the B operand of
-//   S [64 rows x 64 tokens] = Q T^T   (r + 64 deep)
-// and, read along its other axis, the A operand of
-//   O^T [r x 64 rows] += C^T P^T      (64 deep, r / 128 MMAs of 128 rows).
-// O is held transposed because 128 channels fill the tensor memory's lanes
-// where 64 rows would fill half of them: r x 64 sums take r / 2 columns.
+// sequence are one list, cut into row tiles of 64, and a tile of 128 tokens,
+// restored once to fp16 in shared memory, is the A operand of both
+//   S^T [128 tokens x 64 rows] = T Q^T      (r + 64 deep)
+// and, read along its other axis,
+//   O^T [r x 64 rows] += C^T P^T            (128 deep, r / 128 MMAs of 128 rows).
 //
-// The softmax has one row in the four threads of a quad (each holds 16 of its
-// 64 scores), weights against a lifted reference as in the chunk attention;
-// the reference is raised, and O^T's columns rescaled, only when a score lies
-// more than 2^8 above it.
+// Bound: the MMAs' operand reads.  One of 128 x 64 x 16 reads 6 KB of shared
+// memory (48 cycles of its bandwidth, 32 of the tensor cores'), so a tile costs
+// 48 (r / 8 + r / 16 + 4) cycles and the restoring's stores.  (S with the 64 rows
+// on the M side and tiles of 64 tokens takes as long an MMA, 49 measured, for half
+// of the tokens: 220 us where this form takes NEW over 8 x 32k tokens of 128 heads.)
+// 64 rows are what tensor memory holds: r x 64 sums take r / 2 of its 512 columns.
+//
+// A thread of the softmax has one token and 32 of the rows, so a row's maximum over
+// the tile is spread over threads.  It is not formed a tile: weights are taken
+// against the row's reference, and only when some score lies more than 2^8 above
+// it (one vote a tile) are the maxima formed, the references raised, O^T's columns
+// and the sums rescaled, as in the chunk attention's kernel for few rows.
 //
 // Rounding.  A restored latent vector (scale code + zero), the weights and the
 // query enter the products in fp16 (2^-11 relative each); sums in fp32.
 //
-// Work split (as the chunk attention's): the 64-token tiles of all row tiles
-// end to end, each CTA an equal share, cut row tiles joined from partials.
-#include <cstring>
-
+// Work split (as the chunk attention's): the tiles of all row tiles end to end,
+// each CTA an equal share, cut row tiles joined from partials.
 #include "kivi_chunk_tiles.cuh"
 #include "kivi_latent.cuh"
 #include "kivi_tcgen05.cuh"
@@ -33,31 +37,44 @@
 
 namespace {
 
-constexpr int kLaDq = 8;   // warps that restore tiles
-constexpr int kLaThreads = 32 * (4 + kLaDq + 3);
-constexpr unsigned kLaCS = KIVI_KBLK * 16;   // bytes from a 16-byte chunk of a tile to the next along its rows
-__host__ __device__ constexpr int la_stages(int r) { return r == 512 ? 2 : 4; }
-__host__ __device__ constexpr int la_tile(int r) { return (r + kLatRope) / 8 * (int)kLaCS; }   // bytes: of Q too
-__host__ __device__ constexpr size_t la_smem(int r) { return (size_t)(la_stages(r) + 1) * la_tile(r) + kLatRows * KIVI_KBLK * 2; }
+// Warps that restore tiles and take their softmax: with two more for the MMAs and
+// copies, 10 warps of 168 registers.  (16 of 96 spilled, and spills go to L2 where
+// shared memory takes all of the first-level cache: 300 us against NEW.)
+constexpr int kLaWork = 8;
+constexpr int kLaThreads = 32 * (kLaWork + 2);
+constexpr int kLaCols = 32;   // rows of a thread in the softmax
+constexpr unsigned kLaCS = kLatTok * 128;    // bytes of 64 channels of a tile
+constexpr unsigned kLaQS = kLatRows * 128;   // of Q
+// tiles in shared memory (of r = 512 one fits; it is refilled in parts)
+__host__ __device__ constexpr int la_stages(int r) { return r == 512 ? 1 : 2; }
+__host__ __device__ constexpr int la_tile(int r) { return (r + kLatRope) / 64 * (int)kLaCS; }
+__host__ __device__ constexpr size_t la_smem(int r) { return (size_t)la_stages(r) * la_tile(r) + (r + kLatRope) / 64 * kLaQS + 1024; }
+constexpr float kLaUnset = 1e30f;   // s_ref of a row that has seen nothing
 
-// whether any of the four softmax warps says v (all come here every tile)
+// whether any of the working warps says v (all come here every tile)
 __device__ __forceinline__ bool la_any(bool v) {
     unsigned r;
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 1, 128, p;\n\t"
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 1, 256, p;\n\t"
         "selp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(r)
         : "r"(v ? 1u : 0u)
         : "memory");
     return r != 0;
 }
-__device__ __forceinline__ void la_sync() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ void la_sync() { asm volatile("barrier.cta.sync 1, 256;" ::: "memory"); }
+__device__ __forceinline__ float la_redux_max(float x) {
+    float r;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+    return r;
+}
 
-// 16 bytes of codes of a token (word x) to 128 / BITS channels of it: sz the
-// scales and zeros of the groups they span (GW channels of the word each).
-template <int BITS, int NG>
-__device__ __forceinline__ void la_restore(unsigned char *dst, const uint4 &v, const uint32_t (&sz)[NG]) {
-    constexpr int PW = 32 / BITS, CW = 4 * PW;   // channels a 32-bit word, the 16 bytes
+// 16 bytes of codes of a token (128 / BITS channels) to their chunks of its row
+// (at: the first one's place): sz the scales and zeros of their halves (4 bits: of
+// all).
+template <int BITS>
+__device__ __forceinline__ void la_restore(unsigned char *tile, unsigned at, const uint4 &v, const uint32_t *sz) {
+    constexpr int PW = 32 / BITS, CW = 4 * PW, NG = CW / 32;   // channels a 32-bit word, the 16 bytes
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int c = 0; c < CW / 8; ++c) {   // 8 channels: one 16-byte chunk
@@ -69,152 +86,173 @@ __device__ __forceinline__ void la_restore(unsigned char *dst, const uint4 &v, c
             const int f = (8 * c % PW) / 2 + k;   // field of the word's halves
             o[k] = ck_affine(unpack<BITS, false>(w[8 * c / PW], f), slot_offset<BITS, false>(f), s, z);
         }
-        *reinterpret_cast<uint4 *>(dst + c * kLaCS) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4 *>(tile + (at ^ (c << 4))) = make_uint4(o[0], o[1], o[2], o[3]);
     }
 }
 
-// A warp's part of a fully quantized tile in registers: its units are half a
-// block's tokens (a lane each) of one 16-byte word.
-template <int RD, int BITS, int GL>   // GL: log2 of the group size
-struct LaPacked {
-    static constexpr int CW = 128 / BITS, NU = 2 * RD / CW / kLaDq;   // channels a word, units a warp
-    static constexpr int NG = CW >> GL > 1 ? CW >> GL : 1;            // groups a word spans
+// A warp's part of a tile: units of one 16-byte word of codes (CW channels) of 32
+// tokens, a lane each.  Unit k is word x0 + 2 k (x0: warp / 4); PU of them are of a
+// part of 128 channels.
+template <int RD, int BITS>
+struct LaUnits {
+    static constexpr int CW = 128 / BITS, NU = 4 * RD / CW / kLaWork, NG = CW / 32, PU = 64 / CW;
     uint4 w[NU];
     uint32_t sz[NU][NG];
-    __device__ __forceinline__ void load(const unsigned char *rec, int off_sz, int warp, int lane) {
+    // p: unit 0's codes in the record; z: the record's scales and zeros of the
+    // warp's token; ch: unit 0's first channel
+    __device__ __forceinline__ void load(const unsigned char *p, const unsigned char *z, int ch, int lgG) {
 #pragma unroll
         for (int k = 0; k < NU; ++k) {
-            const int u = warp + kLaDq * k, x = u >> 1, t = 32 * (u & 1) + lane;
-            w[k] = __ldg(reinterpret_cast<const uint4 *>(rec + (x * KIVI_KBLK + t) * 16));
+            w[k] = __ldg(reinterpret_cast<const uint4 *>(p + k * (2 * kLatTok * 16)));
 #pragma unroll
             for (int q = 0; q < NG; ++q)
-                sz[k][q] = __ldg(reinterpret_cast<const uint32_t *>(rec + off_sz + ((((x * CW) >> GL) + q) * KIVI_KBLK + t) * 4));
-        }
-    }
-    __device__ __forceinline__ void restore(unsigned char *tile, int warp, int lane) const {
-#pragma unroll
-        for (int k = 0; k < NU; ++k) {
-            const int u = warp + kLaDq * k, x = u >> 1, t = 32 * (u & 1) + lane;
-            la_restore<BITS, NG>(tile + x * (CW / 8) * kLaCS + t * 16, w[k], sz[k]);
+                sz[k][q] = __ldg(reinterpret_cast<const uint32_t *>(z + ((ch + 2 * CW * k + 32 * q) >> lgG) * (kLatTok * 4)));
         }
     }
 };
 
-// 16 bytes (8 channels, chunk c) of token tau's row: from the codes, the ring or
-// the new tokens; zero past them.
-__device__ __forceinline__ uint4 la_row16(const LatentGeom &g, const LatentDev &dv, const __half *Cn, const __half *Kn,
-                                          int i, int T, int Tq, int n, size_t new0, int tau, int c) {
-    const int kb = tau / KIVI_KBLK, t = tau % KIVI_KBLK, nc = g.r / 8;
-    if (tau >= T + n) return make_uint4(0u, 0u, 0u, 0u);
-    if (tau >= T)
-        return *reinterpret_cast<const uint4 *>(c < nc ? Cn + (new0 + (tau - T)) * g.r + 8 * c
-                                                       : Kn + (new0 + (tau - T)) * kLatRope + 8 * (c - nc));
-    if (c >= nc) return *reinterpret_cast<const uint4 *>(dv.kr + lat_kr(g, i, kb) + ((c - nc) * KIVI_KBLK + t) * 8);
-    if (tau >= Tq) return *reinterpret_cast<const uint4 *>(dv.ring + lat_ring(g, i, kb) + ((size_t)c * KIVI_KBLK + t) * 8);
-    const unsigned char *rec = dv.rec + lat_rec(g, i, kb);
-    const __half2 sz = *reinterpret_cast<const __half2 *>(rec + g.off_sz + ((8 * c / g.G) * KIVI_KBLK + t) * 4);
-    const int PW = 32 / g.bits, wi = 8 * c / PW, f0 = (8 * c % PW) >> 1, m = (1 << g.bits) - 1;
-    const uint32_t w = *reinterpret_cast<const uint32_t *>(rec + ((wi >> 2) * KIVI_KBLK + t) * 16 + (wi & 3) * 4);
-    uint32_t h[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const int lo = (w >> (g.bits * (f0 + k))) & m, hi = (w >> (16 + g.bits * (f0 + k))) & m;
-        h[k] = h2u(__hfma2(__halves2half2(__int2half_rn(lo), __int2half_rn(hi)), __low2half2(sz), __high2half2(sz)));
-    }
-    return make_uint4(h[0], h[1], h[2], h[3]);
-}
-
-// What a tile holds, and who fills it.
+// What a tile holds, and who fills it: codes only (restored by the working warps),
+// or fp16 rows (copied).
 struct LaTile {
     int tb;
     bool packed;   // codes only
-    bool ring;     // a whole block of the ring: copied
-    bool fresh;    // new tokens only: copied
-    bool keys;     // the rotary keys are a whole block of the cache: copied
-    __device__ __forceinline__ LaTile(int tb, int T, int Tq, int n)
-        : tb(tb), packed(tb + KIVI_KBLK <= Tq), ring(tb >= Tq && tb + KIVI_KBLK <= T),
-          fresh(tb >= T && tb + KIVI_KBLK <= T + n), keys(tb + KIVI_KBLK <= T) {}
+    bool block;    // a whole block of the ring
+    bool keys;     // the rotary keys are a whole block of the cache
+    __device__ __forceinline__ LaTile(int tb, int T, int Tq)
+        : tb(tb), packed(tb + kLatTok <= Tq), block(!packed && tb + kLatTok <= T), keys(tb + kLatTok <= T) {}
 };
 
-// A tile that is neither: chunk by chunk, by all restoring warps.
-__device__ __noinline__ void la_mixed(const LatentGeom &g, const LatentDev &dv, const __half *Cn, const __half *Kn,
-                                      unsigned char *tile, const LaTile &lt, int i, int T, int Tq, int n, size_t new0) {
-    constexpr int U = 4;
-    const int e0 = threadIdx.x - 128;   // (the restoring warps follow the four of the softmax)
-    const int total = (lt.keys ? g.r / 8 : (g.r + kLatRope) / 8) * KIVI_KBLK;
-    for (int e = e0; e < total; e += U * 32 * kLaDq) {
-        uint4 x[U];
+// A raise: the rows' maxima over the tile (tS: this warp's scores of 32 rows, of
+// which those c < lim do not see the token), the references of the rows that grew by
+// more than 2^8, and their factors.  Called by every working warp.
+__device__ __forceinline__ void la_raise(uint32_t tS, float sl2, int lim, float *s_ref, float *s_al, float (*s_red)[kLatRows]) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint32_t r[kLaCols];
+    tc_ld32(tS, r);
+    tc_wait_ld();
 #pragma unroll
-        for (int k = 0; k < U; ++k) {
-            const int y = min(e + k * 32 * kLaDq, total - 1);
-            x[k] = la_row16(g, dv, Cn, Kn, i, T, Tq, n, new0, lt.tb + y % KIVI_KBLK, y / KIVI_KBLK);
-        }
-#pragma unroll
-        for (int k = 0; k < U; ++k) {
-            const int y = e + k * 32 * kLaDq;
-            if (y < total) *reinterpret_cast<uint4 *>(tile + y * 16) = x[k];
-        }
+    for (int c = 0; c < kLaCols; ++c) {
+        const float m = la_redux_max(c < lim ? -INFINITY : __uint_as_float(r[c]) * sl2);
+        if (lane == 0) s_red[warp & 3][kLaCols * (warp >> 2) + c] = m;
     }
+    la_sync();
+    const int t = threadIdx.x;
+    if (t < kLatRows) {
+        const float m = fmaxf(fmaxf(s_red[0][t], s_red[1][t]), fmaxf(s_red[2][t], s_red[3][t]));
+        const float old = s_ref[t];
+        const bool grow = m != -INFINITY && m + old > kCkLift + kCkLag;
+        s_al[t] = grow && old != kLaUnset ? ex2((kCkLift - m) - old) : 1.f;
+        if (grow) s_ref[t] = kCkLift - m;
+    }
+    la_sync();
 }
-
-// One restoring warp's share of a segment's nx tiles from first token tb0 on.
-// False if a wait ran out.
-template <int RD, int BITS, int GL>
-__device__ __forceinline__ bool la_tiles(const LatentGeom &g, const LatentDev &dv, const __half *Cn, const __half *Kn,
-                                         int i, int T, int Tq, int n, size_t new0, int tb0, int nx, int &tiles, CkRing &t,
-                                         unsigned char *sC, uint64_t *bC, uint64_t *eC, const volatile int *abort) {
-    constexpr int KS = la_stages(RD), TB = la_tile(RD);
-    const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - 4;
-    LaPacked<RD, BITS, GL> cur, nxt;
-    const unsigned char *rec = dv.rec + lat_rec(g, i, tb0 / KIVI_KBLK);
-    if (tb0 + KIVI_KBLK <= Tq) cur.load(rec, g.off_sz, warp, lane);
+// 32 columns of O^T times the rows' factors, NM times (tO: this warp's lanes)
+template <int NM>
+__device__ __forceinline__ void la_rescale(uint32_t tO, const float *al) {
 #pragma unroll 1
-    for (int x = 0; x < nx; ++x, ++tiles, t.next(KS)) {
-        const LaTile lt(tb0 + KIVI_KBLK * x, T, Tq, n);
-        unsigned char *tile = sC + t.s * TB;
-        if (lt.packed && lt.tb + 2 * KIVI_KBLK <= Tq && x + 1 < nx)
-            nxt.load(rec + (size_t)(x + 1) * g.rec_bytes, g.off_sz, warp, lane);
-        const bool ok = tiles < KS || mbar_wait_ab(&eC[t.s], t.p ^ 1u, abort);
-        if (!__all_sync(kFull, ok)) return false;
-        if (lt.packed) {
-            cur.restore(tile, warp, lane);
-            cur = nxt;
-        } else if (!lt.ring && !lt.fresh) {
-            la_mixed(g, dv, Cn, Kn, tile, lt, i, T, Tq, n, new0);
-        }
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bC[t.s]);
+    for (int m = 0; m < NM; ++m) {
+        uint32_t o[kLaCols];
+        tc_ld32(tO + kLatRows * m, o);
+        tc_wait_ld();
+#pragma unroll
+        for (int c = 0; c < kLaCols; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * al[c]);
+        tc_st32(tO + kLatRows * m, o);
     }
-    return true;
+    tc_wait_st();
 }
 
-// Warps 0-3: softmax and output; 4-11: restoring tiles; 12: S; 13: O^T; 14:
-// copies (rotary keys, whole fp16 tiles).  They meet on mbarriers only (bounded
-// waits).  Tensor memory: two S buffers of 64 columns, then O^T.  Shared
-// memory: tiles [r + 64 channels in chunks of 8][64 tokens], Q alike, P.
-template <int RD>
+// One thread's weights of its token against the references of its 32 rows, from
+// the scores at tS: into its row of P (sP: the shared-memory address of its first
+// chunk), their sums from tL0 (first: none yet) to tL1.  Rows c < lim do not see the
+// token.  The largest log2 weight.
+__device__ __forceinline__ float la_weights(uint32_t tS, uint32_t tL0, uint32_t tL1, bool first, unsigned sP,
+                                            const float *refs, float sl2, int lim) {
+    float up = -INFINITY;
+    uint32_t r[kLaCols];
+    tc_ld32(tS, r);
+#pragma unroll
+    for (int c0 = 0; c0 < kLaCols; c0 += 16) {
+        uint32_t l[16];
+        if (!first) tc_ld16(tL0 + c0, l);
+        tc_wait_ld();
+        if (first)
+#pragma unroll
+            for (int c = 0; c < 16; ++c) l[c] = 0u;
+#pragma unroll
+        for (int c = 0; c < 16; c += 8) {
+            float y[8];
+#pragma unroll
+            for (int k = 0; k < 8; k += 4) {
+                const float4 ref = *reinterpret_cast<const float4 *>(refs + c0 + c + k);
+                y[k] = fmaf(__uint_as_float(r[c0 + c + k]), sl2, ref.x);
+                y[k + 1] = fmaf(__uint_as_float(r[c0 + c + k + 1]), sl2, ref.y);
+                y[k + 2] = fmaf(__uint_as_float(r[c0 + c + k + 2]), sl2, ref.z);
+                y[k + 3] = fmaf(__uint_as_float(r[c0 + c + k + 3]), sl2, ref.w);
+            }
+            if (lim > c0 + c)
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (c0 + c + k < lim) y[k] = -INFINITY;
+            uint32_t pw[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                up = fmaxf(up, fmaxf(y[2 * k], y[2 * k + 1]));
+                const float y0 = ex2(y[2 * k]), y1 = ex2(y[2 * k + 1]);
+                l[c + 2 * k] = __float_as_uint(__uint_as_float(l[c + 2 * k]) + y0);
+                l[c + 2 * k + 1] = __float_as_uint(__uint_as_float(l[c + 2 * k + 1]) + y1);
+                pw[k] = ck_pack(y0, y1);
+            }
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(sP ^ (((c0 + c) / 8) << 4)), "r"(pw[0]), "r"(pw[1]),
+                         "r"(pw[2]), "r"(pw[3])
+                         : "memory");
+        }
+        tc_st16(tL1 + c0, l);
+    }
+    tc_wait_st();
+    fence_proxy_async();
+    tc_fence_before();
+    return up;
+}
+
+// Warps 0-7: restoring tiles, softmax and output (of r = 512 one tile fits, so that
+// the two never run at once); 8: S^T and O^T; 9: copies (rotary keys, whole fp16
+// tiles).  They meet on mbarriers only (bounded
+// waits).  A tile is filled, and given back, in parts of 128 channels: S^T of the
+// next tile begins with its first part while O^T still reads the others.  Tensor
+// memory: two S^T buffers of 64 columns, O^T, two buffers of the weights' sums.  Shared memory: tiles, then Q,
+// both in lat_at's layout.  The weights (a row of 64 a token) take the place of the
+// tile's rotary keys, which only S^T reads.
+template <int RD, int BITS>
 __global__ void __launch_bounds__(kLaThreads, 1)
-    latent_attn_kernel(const __grid_constant__ LatentGeom g, const __grid_constant__ LatentDev dv, const __half *__restrict__ Q, const __half *__restrict__ Qr,
-                       const __half *__restrict__ Cn, const __half *__restrict__ Kn, __half *__restrict__ O,
-                       const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmK, float sl2,
-                       const __grid_constant__ ChunkArgs a) {
-    extern __shared__ __align__(128) unsigned char smem[];
+    latent_attn_kernel(const __grid_constant__ LatentGeom g, const __grid_constant__ LatentDev dv,
+                       const __half *__restrict__ Q, const __half *__restrict__ Qr, const __half *__restrict__ Cn,
+                       const __half *__restrict__ Kn, __half *__restrict__ O, const __grid_constant__ CUtensorMap tmC,
+                       const __grid_constant__ CUtensorMap tmK, float sl2, const __grid_constant__ ChunkArgs a) {
+    extern __shared__ unsigned char raw[];
+    unsigned char *const smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
     constexpr int KS = la_stages(RD), TB = la_tile(RD), NM = RD / 128;
-    constexpr int OC = 2 * KIVI_KBLK;   // first column of O^T
-    unsigned char *sC = smem, *sQ = sC + KS * TB, *sP = sQ + TB;
-    // counts 4 (the softmax warps): Q, P [buffer of S]; 8: tiles restored; 1: the others
-    constexpr int NB = 3 + 3 * KS + 3;
+    constexpr unsigned CB = RD / 64 * kLaCS, RB = kLatRope / 64 * kLaCS;   // bytes of a tile's c, and kr
+    static_assert(RB == kLatRows * kLatTok * 2, "the weights fit in the rotary keys' place");
+    constexpr int OC = 2 * kLatRows;   // first column of O^T
+    unsigned char *sC = smem, *sQ = sC + KS * TB;
+    using Units = LaUnits<RD, BITS>;
+    // counts the working warps: Q, parts of a tile restored [stage][part]; 1: the
+    // others (bR, bK: parts and rotary keys copied; each part waits for both.  bF: O^T
+    // done, two in turn, as it may be two tiles behind the softmax)
+    constexpr int N8 = 1 + KS * NM, NB = N8 + 2 * KS * NM + KS + 8;
     __shared__ __align__(8) uint64_t bars[NB];
-    uint64_t *const bQ = bars, *const bP = bars + 1, *const bC = bars + 3, *const bB = bC + KS, *const eC = bB + KS,
-                    *const bS = eC + KS, *const bF = bS + 2;
+    uint64_t *const bQ = bars, *const bC = bars + 1, *const eC = bars + N8, *const bR = eC + KS * NM,
+                    *const bK = bR + KS * NM, *const bP = bK + KS, *const bS = bP + 2, *const bF = bS + 2, *const bE = bF + 2, *const bX = bE + 1;
     __shared__ uint32_t s_taddr;
     __shared__ int s_abort;
-    __shared__ __align__(16) float s_al[kLatRows];   // a raise's factors; 1 / sum of each row
+    __shared__ __align__(16) float s_ref[kLatRows];   // the lift less each row's reference (log2 units)
+    __shared__ __align__(16) float s_al[kLatRows];    // a raise's factors; 1 / sum of each row
+    __shared__ float s_red[4][kLatRows];              // per 32 tokens: maxima, or sums
+    __shared__ CkSeg s_seg;                           // for the segment's end (out of the tile loop's registers)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int h = a.hg;
     if (tid < NB) {
-        mbar_init(&bars[tid], tid < 3 ? 4 : tid < 3 + KS ? kLaDq : 1);
+        mbar_init(&bars[tid], tid < N8 ? kLaWork : 1);
         fence_mbar_init();
     }
     if (tid == 0) s_abort = 0;
@@ -231,31 +269,65 @@ __global__ void __launch_bounds__(kLaThreads, 1)
     CkWalk walk;
     walk.start(a, blockIdx.x);
     CkSeg sg = {};
-    constexpr int WS = 4 + kLaDq;
+    constexpr int WS = kLaWork;
 
     if (warp == WS) {
-        // ---- S = Q T^T ----
-        constexpr uint32_t ID = tc_idesc_f16(kLatRows, KIVI_KBLK, 0);
-        CkRing t;
-        int cnt = 0;
+        // ---- S^T = T Q^T of tile x, then O^T += C^T P^T of tile x - (KS - 1) ----
+        constexpr uint32_t IDS = tc_idesc_f16(kLatTok, kLatRows, 0);
+        constexpr uint32_t IDO = tc_idesc_f16_at(128, kLatRows) | (1u << 16);   // both MN-major
+        CkRing t, u;
+        int cs = 0, co = 0;   // S^T, O^T so far
         unsigned qph = 0;
-        const uint64_t dq = tc_desc(sQ, kLaCS, 128), dc = tc_desc(sC, kLaCS, 128);
+        const uint64_t dq = tc_desc_sw(sQ, 16, 1024), ds = tc_desc_sw(sC, 16, 1024);
+        const uint64_t dc = tc_desc_sw(sC, kLaCS, 1024), dp = tc_desc_sw(sC + CB, 16, 1024);
         while (ok && walk.next(kg, a, sg)) {
             const int nx = __reduce_max_sync(kFull, sg.nx);
-            for (int x = 0; x < nx; ++x, ++cnt, t.next(KS)) {
-                const int b = cnt & 1;
-                // Q and the tile in, the buffer's last scores read (their weights written)
-                ok = (x > 0 || mbar_wait_ab(bQ, qph, abort)) && mbar_wait_ab(&bB[t.s], t.p, abort) &&
-                     mbar_wait_ab(&bC[t.s], t.p, abort) &&
-                     (cnt < 2 || mbar_wait_ab(&bP[b], (unsigned)((cnt >> 1) + 1) & 1u, abort));
-                ok = __all_sync(kFull, ok);
+            for (int x = 0; x < nx + KS - 1; ++x) {
+                if (x < nx) {
+                    const int b = cs & 1;
+                    // (the buffer's last scores are read: with one tile O^T waited for their
+                    // weights, with two that of the last but one did)
+                    ok = x > 0 || mbar_wait_ab(bQ, qph, abort);
+                    const uint64_t d = ds + (uint32_t)(t.s * (TB >> 4));
+                    auto part_in = [&](int m, auto wait) {
+                        return m < NM ? wait(&bC[t.s * NM + m]) && wait(&bR[t.s * NM + m]) : wait(&bK[t.s]);
+                    };
+                    bool in = false;   // the part is in (polled while the last one's products are issued)
+#pragma unroll
+                    for (int m = 0; m <= NM; ++m) {   // its parts, then the rotary keys
+                        ok = __all_sync(kFull, ok && (in || part_in(m, [&](uint64_t *bar) { return mbar_wait_ab(bar, t.p, abort); })));
+                        if (!ok) break;
+                        in = m < NM && part_in(m + 1, [&](uint64_t *bar) { return mbar_test(bar, t.p); });
+                        tc_fence_after();
+                        const uint64_t qm = dq + (uint32_t)((2 * m * kLaQS) >> 4), cm = d + (uint32_t)((2 * m * kLaCS) >> 4);
+#pragma unroll
+                        for (int c = 0; c < 8; ++c)
+                            if (c < 4 || m < NM)
+                                tc_mma_f16_w(taddr + kLatRows * b, cm + (((c >> 2) * kLaCS + 32 * (c & 3)) >> 4),
+                                             qm + (((c >> 2) * kLaQS + 32 * (c & 3)) >> 4), IDS, m > 0 || c > 0);
+                    }
+                    if (!ok) break;
+                    tc_commit_w(&bS[b]);
+                    ++cs;
+                    t.next(KS);
+                }
+                const int y = x - (KS - 1);
+                if (y < 0) continue;
+                ok = __all_sync(kFull, mbar_wait_ab(&bP[co & 1], (unsigned)(co >> 1) & 1u, abort));
                 if (!ok) break;
                 tc_fence_after();
-                const uint64_t d = dc + (uint32_t)(t.s * (TB >> 4));
-#pragma unroll 4
-                for (int c = 0; c < (RD + kLatRope) / 16; ++c)
-                    tc_mma_f16_w(taddr + KIVI_KBLK * b, dq + ((2 * c * kLaCS) >> 4), d + ((2 * c * kLaCS) >> 4), ID, c > 0);
-                tc_commit_w(&bS[b]);
+                const uint64_t st = (uint32_t)(u.s * (TB >> 4));
+#pragma unroll
+                for (int m = 0; m < NM; ++m) {
+#pragma unroll
+                    for (int c = 0; c < kLatTok / 16; ++c)
+                        tc_mma_f16_w(taddr + OC + kLatRows * m, dc + st + ((2 * m * kLaCS + 2048 * c) >> 4),
+                                     dp + st + ((2048 * c) >> 4), IDO, y > 0 || c > 0);
+                    tc_commit_w(&eC[u.s * NM + m]);
+                }
+                tc_commit_w(&bF[co & 1]);
+                ++co;
+                u.next(KS);
             }
             qph ^= 1u;
         }
@@ -263,67 +335,111 @@ __global__ void __launch_bounds__(kLaThreads, 1)
             s_abort = 1;
             atomicOr(dv.status, KIVI_FLAG_WAIT);
         }
-        // every commit has landed before shared memory is given up (bounded)
-        for (int y = max(0, cnt - 2); y < cnt; ++y) mbar_wait(&bS[y & 1], (unsigned)(y >> 1) & 1u);
+        // every MMA and commit has landed before memory is given up (bounded)
+        tc_commit_w(bE);
+        mbar_wait(bE, 0u);
         __syncwarp();
     } else if (warp == WS + 1) {
-        // ---- O^T += C^T P^T ----
-        constexpr uint32_t ID = tc_idesc_f16_at(128, kLatRows);
+        // ---- copies ----
         CkRing t;
-        int cnt = 0;
-        const uint64_t dc = tc_desc(sC, 128, kLaCS), dp = tc_desc(sP, kLaCS, 128);
+        int cnt = 0, parts = 0, meets = 0;   // tiles; parts told of; copies waited for here
         while (ok && walk.next(kg, a, sg)) {
-            const int nx = __reduce_max_sync(kFull, sg.nx);
-            for (int x = 0; x < nx; ++x, ++cnt, t.next(KS)) {
-                ok = __all_sync(kFull, mbar_wait_ab(&bP[cnt & 1], (unsigned)(cnt >> 1) & 1u, abort));
-                if (!ok) break;
-                tc_fence_after();
-                const uint64_t d = dc + (uint32_t)(t.s * (TB >> 4));
-#pragma unroll
-                for (int m = 0; m < NM; ++m)
-#pragma unroll
-                    for (int c = 0; c < KIVI_KBLK / 16; ++c)
-                        tc_mma_f16_w(taddr + OC + kLatRows * m, d + ((16 * m * kLaCS + 256 * c) >> 4),
-                                     dp + ((2 * c * kLaCS) >> 4), ID, x > 0 || c > 0);
-                tc_commit_w(bF);
-                tc_commit_w(&eC[t.s]);
-            }
-        }
-        if (!ok && lane == 0) {
-            s_abort = 1;
-            atomicOr(dv.status, KIVI_FLAG_WAIT);
-        }
-        if (cnt > 0) mbar_wait(bF, (unsigned)(cnt - 1) & 1u);
-        for (int y = max(0, cnt - KS); y < cnt; ++y) mbar_wait(&eC[y % KS], (unsigned)(y / KS) & 1u);
-        __syncwarp();
-    } else if (warp == WS + 2) {
-        // ---- copies (lane 0 issues) ----
-        CkRing t;
-        int cnt = 0;
-        while (ok && walk.next(kg, a, sg)) {
-            if (lane == 0) {
-                const int T = sg.T, Tq = a.Tqk[sg.i];
-                for (int x = 0; x < sg.nx; ++x, ++cnt, t.next(KS)) {
-                    ok = cnt < KS || mbar_wait_ab(&eC[t.s], t.p ^ 1u, abort);
+            const int T = sg.T, Tq = a.Tqk[sg.i], n = sg.n;
+            const long long new0 = (long long)sg.i * a.n_stride;
+            for (int x = 0; x < sg.nx; ++x, ++cnt, t.next(KS)) {
+                const LaTile lt(kLatTok * (sg.x0 + x), T, Tq);
+                const int kb = lt.tb / kLatTok;
+                unsigned char *tile = sC + t.s * TB;
+                const unsigned char *ring = (const unsigned char *)(dv.ring + lat_ring(g, sg.i, kb)),
+                                    *keys = (const unsigned char *)(dv.kr + lat_kr(g, sg.i, kb));
+                // the record after next into L2 (the first two at the start)
+                if (lane == 0)
+                    for (int e = x ? 2 : 0; e < 3; ++e)
+                        if (lt.tb + (e + 1) * kLatTok <= Tq && x + e < sg.nx)
+                            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(dv.rec + lat_rec(g, sg.i, kb + e)),
+                                         "r"(g.rec_bytes)
+                                         : "memory");
+                // New tokens: a full tile of them (and of cached ones before them) by
+                // TMA; then, over what it brought of the rows before them, the cached
+                // ones.  A short one: the cached block, or zeros (what lies behind the
+                // last token has no weight, but must be finite), and row by row.
+                const int old = min(max(T - lt.tb, 0), kLatTok), rows = T + n - lt.tb;   // cached rows, rows in all
+                const bool fresh = !lt.keys, full = rows >= kLatTok;
+                if (fresh) {
+                    ok = __all_sync(kFull, cnt < KS || mbar_wait_ab(&eC[t.s * NM + NM - 1], t.p ^ 1u, abort));
                     if (!ok) break;
-                    const LaTile lt(sg.key0(x), T, Tq, sg.n);
-                    unsigned char *tile = sC + t.s * TB;
-                    constexpr unsigned CB = RD / 8 * kLaCS, RB = kLatRope / 8 * kLaCS;
-                    const int kb = lt.tb / KIVI_KBLK;
-                    const unsigned bytes = (lt.ring || lt.fresh ? CB : 0u) + (lt.keys || lt.fresh ? RB : 0u);
-                    if (bytes) mbar_expect_tx(&bB[t.s], bytes);
-                    else mbar_arrive(&bB[t.s]);
-                    if (lt.fresh) {
-                        const int row = (int)((size_t)sg.i * a.n_stride + (lt.tb - T));
-                        tma_box(tile, &tmC, row, &bB[t.s]);
-                        tma_box(tile + CB, &tmK, row, &bB[t.s]);
-                    } else {
-                        if (lt.ring) bulk_g2s(tile, dv.ring + lat_ring(g, sg.i, kb), CB, &bB[t.s]);
-                        if (lt.keys) bulk_g2s(tile + CB, dv.kr + lat_kr(g, sg.i, kb), RB, &bB[t.s]);
+                    if (old > 0 && lane == 0) {
+                        mbar_expect_tx(bX, CB + RB);
+                        if (full) {
+                            for (int c = 0; c < 2 * NM; ++c)
+                                tma_sw(tile + c * kLaCS, &tmC, 64 * c, (int)(new0 + lt.tb - T), bX);
+                            tma_sw(tile + CB, &tmK, 0, (int)(new0 + lt.tb - T), bX);
+                        } else {
+                            bulk_g2s(tile, ring, CB, bX);
+                            bulk_g2s(tile + CB, keys, RB, bX);
+                        }
+                    }
+                    if (old > 0) {
+                        ok = __all_sync(kFull, mbar_wait_ab(bX, (unsigned)meets++ & 1u, abort));
+                        if (!ok) break;
+                    }
+                    if (!full) {
+                        constexpr int CR = (RD + kLatRope) / 8;   // 16-byte chunks of a row
+                        constexpr int U = 4;
+#pragma unroll 1
+                        for (int e0 = old * CR + lane; e0 < (old > 0 ? rows : kLatTok) * CR; e0 += 32 * U) {
+                            uint4 v[U];
+#pragma unroll
+                            for (int k = 0; k < U; ++k) {
+                                const int e = e0 + 32 * k, r = e / CR, c = e - r * CR;
+                                const size_t row = (size_t)(new0 + lt.tb - T + r);
+                                v[k] = make_uint4(0u, 0u, 0u, 0u);
+                                if (r < rows)
+                                    v[k] = *reinterpret_cast<const uint4 *>(c < RD / 8 ? Cn + row * RD + 8 * c
+                                                                                       : Kn + row * kLatRope + 8 * (c - RD / 8));
+                            }
+#pragma unroll
+                            for (int k = 0; k < U; ++k) {
+                                const int e = e0 + 32 * k, r = e / CR, c = e - r * CR;
+                                if (r < kLatTok) *reinterpret_cast<uint4 *>(tile + lat_at(c, r, kLatTok)) = v[k];
+                            }
+                        }
+                        fence_proxy_async();
+                        __syncwarp();
                     }
                 }
+                for (int m = 0; m < NM; ++m, ++parts) {
+                    ok = __all_sync(kFull, ok && (cnt < KS || mbar_wait_ab(&eC[t.s * NM + m], t.p ^ 1u, abort)));
+                    if (!ok) break;
+                    if (lane == 0) {
+                        uint64_t *const bar = &bR[t.s * NM + m];
+                        unsigned char *dst = tile + 2 * m * kLaCS;
+                        if (lt.block) {
+                            mbar_expect_tx(bar, 2 * kLaCS);
+                            bulk_g2s(dst, ring + 2 * m * kLaCS, 2 * kLaCS, bar);
+                        } else if (fresh && full) {
+                            mbar_expect_tx(bar, 2 * (old > 0 ? old * 128 : kLaCS));
+                            for (int c = 0; c < 2; ++c)
+                                if (old > 0) bulk_g2s(dst + c * kLaCS, ring + (2 * m + c) * kLaCS, old * 128, bar);
+                                else tma_sw(dst + c * kLaCS, &tmC, 128 * m + 64 * c, (int)(new0 + lt.tb - T), bar);
+                        } else {
+                            mbar_arrive(bar);
+                        }
+                    }
+                }
+                if (!ok) break;
+                // (the last part given back: the weights too, O^T's MMAs end in order)
+                if (lane == 0) {
+                    if (lt.keys || (fresh && full)) {
+                        mbar_expect_tx(&bK[t.s], lt.keys || old == 0 ? RB : old * 128);
+                        if (lt.keys || old > 0) bulk_g2s(tile + CB, keys, lt.keys ? RB : old * 128, &bK[t.s]);
+                        else tma_sw(tile + CB, &tmK, 0, (int)(new0 + lt.tb - T), &bK[t.s]);
+                    } else {
+                        mbar_arrive(&bK[t.s]);
+                    }
+                }
+                __syncwarp();
             }
-            ok = __all_sync(kFull, ok);
         }
         if (lane == 0) {
             if (!ok) {
@@ -331,188 +447,181 @@ __global__ void __launch_bounds__(kLaThreads, 1)
                 atomicOr(dv.status, KIVI_FLAG_WAIT);
             }
             // every copy has landed before shared memory is given up (bounded)
-            for (int y = max(0, cnt - KS); y < cnt; ++y) mbar_wait(&bB[y % KS], (unsigned)(y / KS) & 1u);
-        }
-        __syncwarp();
-    } else if (warp >= 4) {
-        // ---- tiles ----
-        int tiles = 0;
-        CkRing t;
-        while (ok && walk.next(kg, a, sg)) {
-            const int T = sg.T, Tq = a.Tqk[sg.i], n = sg.n, tb0 = sg.key0(0), nx = sg.nx;
-            const size_t new0 = (size_t)sg.i * a.n_stride;
-#define LA_TILES(B, L) la_tiles<RD, B, L>(g, dv, Cn, Kn, sg.i, T, Tq, n, new0, tb0, nx, tiles, t, sC, bC, eC, abort)
-            if (g.bits == 4)
-                ok = g.G == 32 ? LA_TILES(4, 5) : g.G == 64 ? LA_TILES(4, 6) : LA_TILES(4, 7);
-            else
-                ok = g.G == 32 ? LA_TILES(2, 5) : g.G == 64 ? LA_TILES(2, 6) : LA_TILES(2, 7);
-#undef LA_TILES
-        }
-        if (!ok && lane == 0) {
-            s_abort = 1;
-            atomicOr(dv.status, KIVI_FLAG_WAIT);
+            for (int y = max(0, parts - KS * NM); y < parts; ++y)
+                mbar_wait(&bR[y % (KS * NM)], (unsigned)(y / (KS * NM)) & 1u);
+            for (int y = max(0, cnt - KS); y < cnt; ++y) mbar_wait(&bK[y % KS], (unsigned)(y / KS) & 1u);
         }
         __syncwarp();
     } else {
-        // ---- softmax ----
-        const uint32_t lane_off = (uint32_t)(32 * warp) << 16;
-        const int rq = 16 * warp + (lane >> 2), tq = lane & 3;   // this quad's rows: rq, rq + 8
-        int cnt = 0;
+        // ---- tiles, softmax, output ----
+        const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
+        const int x0 = warp >> 2, r0 = kLaCols * x0, t0 = 32 * (warp & 3), tok = t0 + lane;   // word, rows, token
+        const uint32_t tO = taddr + lane_off + OC + r0, tL = tO + kLatRows * NM;   // O^T, two buffers of each thread's sums
+        int cnt = 0, tiles = 0;   // softmax, restored
+        CkRing t, u;
         while (walk.next(kg, a, sg)) {
-            // Q: row (token, head); rows past the last are zero (the last
-            // segment's scores are all read)
-            for (int e = tid; e < kLatRows * (RD + kLatRope) / 8; e += 128) {
-                const int c = e / (2 * kLatRows) * 2 + (e & 1), q = (e >> 1) % kLatRows, rw = sg.row0 + q;
-                uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                if (rw < sg.nrows) {
-                    const int tok = chunk_div(a, rw);
-                    const size_t row = ((size_t)sg.i * h + rw - tok * h) * a.n_stride + tok;
-                    v = *reinterpret_cast<const uint4 *>(c < RD / 8 ? Q + row * RD + 8 * c : Qr + row * kLatRope + 8 * (c - RD / 8));
+            const int T = sg.T, Tq = a.Tqk[sg.i], nx = sg.nx, first = sg.x0, row0 = sg.row0;
+            const unsigned char *rec = dv.rec + lat_rec(g, sg.i, first);
+            // Q: row (token, head), 8 rows x 4 chunks at a time; rows past the last
+            // are zero (the last segment's scores are all read)
+            constexpr int QN = kLatRows * (RD + kLatRope) / 8 / (32 * kLaWork), QB = QN % 6 == 0 ? 6 : 5;
+#pragma unroll 1
+            for (int k0 = 0; k0 < QN; k0 += QB) {
+                uint4 v[QB];
+#pragma unroll
+                for (int k = 0; k < QB; ++k) {
+                    const int blk = (k0 + k) * kLaWork + warp, q = 8 * (blk & 7) + (lane & 7), c = 4 * (blk >> 3) + (lane >> 3);
+                    const int rw = min(sg.row0 + q, sg.nrows - 1), tk = chunk_div(a, rw);
+                    const size_t row = ((size_t)sg.i * h + rw - tk * h) * a.n_stride + tk;
+                    v[k] = *reinterpret_cast<const uint4 *>(c < RD / 8 ? Q + row * RD + 8 * c : Qr + row * kLatRope + 8 * (c - RD / 8));
                 }
-                *reinterpret_cast<uint4 *>(sQ + c * kLaCS + q * 16) = v;
+#pragma unroll
+                for (int k = 0; k < QB; ++k) {
+                    const int blk = (k0 + k) * kLaWork + warp, q = 8 * (blk & 7) + (lane & 7), c = 4 * (blk >> 3) + (lane >> 3);
+                    if (sg.row0 + q >= sg.nrows) v[k] = make_uint4(0u, 0u, 0u, 0u);
+                    *reinterpret_cast<uint4 *>(sQ + lat_at(c, q, kLatRows)) = v[k];
+                }
             }
+            if (tid < kLatRows) s_ref[tid] = kLaUnset;
+            if (tid == 0) s_seg = sg;
             fence_proxy_async();
             __syncwarp();
             if (lane == 0) mbar_arrive(bQ);
-            const int p0 = sg.T + chunk_div(a, sg.row0);   // the first row's position
-            const int pos[2] = {sg.T + chunk_div(a, sg.row0 + rq), sg.T + chunk_div(a, sg.row0 + rq + 8)};
-            float ref[2] = {-INFINITY, -INFINITY}, lsum[2] = {0.f, 0.f};
-            for (int x = 0; x < sg.nx; ++x, ++cnt) {
-                const int b = cnt & 1, key0 = sg.key0(x);
+            la_sync();   // the references are set
+            const int p0 = T + chunk_div(a, sg.row0);   // the first row's position
+            // step x: tile x restored, then the softmax of tile x - (KS - 1)
+#pragma unroll 1
+            for (int x = 0; x < nx + KS - 1; ++x) {
+                // (what follows from the thread's number is formed anew every tile: kept, it
+                // would be spilled)
+                int th = threadIdx.x;
+                asm volatile("" : "+r"(th));
+                const int x0 = th >> 7, r0 = kLaCols * x0, tok = th & 127, t0 = tok & ~31, lane = th & 31;
+                const unsigned out = lat_at(x0 * (Units::CW / 8), tok, kLatTok);   // unit 0's place in a tile
+                if (x < nx) {
+                    const LaTile lt(kLatTok * (first + x), T, Tq);
+                    unsigned char *tile = sC + t.s * TB;
+                    Units cur;   // (from L2; on their way while the parts' places are waited for)
+                    if (lt.packed)
+                        cur.load(rec + tok * 16 + x0 * (kLatTok * 16), rec + g.off_sz + tok * 4, x0 * Units::CW, __ffs(g.G) - 1);
+                    rec += g.rec_bytes;
+#pragma unroll
+                    for (int m = 0; m < NM; ++m) {
+                        if (lt.packed) {
+                            // the part's place is free
+                            ok = ok && __all_sync(kFull, tiles < KS || mbar_wait_ab(&eC[t.s * NM + m], t.p ^ 1u, abort));
+                            if (ok)
+#pragma unroll
+                                for (int k = Units::PU * m; k < Units::PU * (m + 1); ++k)
+                                    la_restore<BITS>(tile + (2 * k * Units::CW / 64) * kLaCS, out, cur.w[k], cur.sz[k]);
+                            fence_proxy_async();
+                            __syncwarp();
+                        }
+                        if (ok && lane == 0) mbar_arrive(&bC[t.s * NM + m]);
+                    }
+                    ++tiles;
+                    t.next(KS);
+                }
+                const int xs = x - (KS - 1);
+                if (xs < 0) continue;
+                const int b = cnt & 1, key0 = kLatTok * (first + xs);
+                const uint32_t tW = taddr + ((uint32_t)t0 << 16) + r0, tS = tW + kLatRows * b;
+                const uint32_t tO = tW + OC, tL = tO + kLatRows * NM;
+                // the sums so far, and with this tile (kept apart until the tile stands)
+                const uint32_t tL0 = tL + kLatRows * (xs & 1), tL1 = tL + kLatRows * (~xs & 1);
+                // rows c < lim do not see this token: those of a token before it
+                int lim = 0;
+                if (key0 + kLatTok - 1 > p0) {
+                    const int l = (key0 + tok - T) * h - row0 - r0;   // (below 2^24 + 2^16)
+                    lim = l < 0 ? 0 : l > kLaCols ? kLaCols : l;
+                }
+                const unsigned sP = smem_u32(sC + u.s * TB + CB) + lat_at(r0 / 8, tok, kLatTok);   // (the tile's rotary keys are read once S^T is in)
                 ok = ok && __all_sync(kFull, mbar_wait_ab(&bS[b], (unsigned)(cnt >> 1) & 1u, abort));
                 tc_fence_after();
-                uint32_t r[32];   // r[4 k + 2 e + c]: row rq + 8 e, token 8 k + 2 tq + c
-                float alpha[2] = {1.f, 1.f};
-                bool grow = false;
-                if (ok) {
-                    tc_ld_16x64(taddr + lane_off + KIVI_KBLK * b, r);
-                    tc_wait_ld();
-                    if (key0 + KIVI_KBLK - 1 > p0) {   // some row does not see the whole tile
-#pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            if (key0 + 8 * (k >> 2) + 2 * tq + (k & 1) > pos[(k >> 1) & 1]) r[k] = 0xff800000u;
+                float up = -INFINITY;
+                if (ok) up = la_weights(tS, tL0, tL1, xs == 0, sP, s_ref + r0, sl2, lim);
+                if (la_any(!ok || up > kCkLift + kCkLag)) {   // a raise: then this tile's weights anew
+                    if (la_any(!ok)) {   // every warp learns whether one has given up
+                        ok = false;
+                        break;
                     }
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float m = __uint_as_float(r[2 * e]);
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            m = fmaxf(m, fmaxf(__uint_as_float(r[4 * k + 2 * e]), __uint_as_float(r[4 * k + 2 * e + 1])));
-                        m = fmaxf(m, __shfl_xor_sync(kFull, m, 1));
-                        m = fmaxf(m, __shfl_xor_sync(kFull, m, 2));
-                        if (m != -INFINITY && (ref[e] == -INFINITY || fmaf(m, sl2, -ref[e]) > kCkLift + kCkLag)) {
-                            const float up = fmaf(m, sl2, -kCkLift);
-                            if (ref[e] != -INFINITY) {
-                                alpha[e] = ex2(ref[e] - up);
-                                grow = true;
-                            }
-                            ref[e] = up;
+                    la_raise(tS, sl2, lim, s_ref, s_al, s_red);
+                    if (xs > 0) {   // O^T, once that of the last tile is in, and the sums
+                        ok = __all_sync(kFull, mbar_wait_ab(&bF[~cnt & 1], (unsigned)((cnt - 1) >> 1) & 1u, abort));
+                        if (ok) {
+                            tc_fence_after();
+                            la_rescale<NM>(tO, s_al + r0);
+                            la_rescale<1>(tL0, s_al + r0);
                         }
                     }
-                }
-                const bool raise = la_any(!ok || grow);
-                if (raise && la_any(!ok)) {   // every warp learns whether one has given up
-                    ok = false;
-                    break;
-                }
-                uint32_t pw[16];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float ms = ref[e] == -INFINITY ? 0.f : ref[e];   // (nothing seen yet: weights 0)
-                    float l = 0.f;
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const float y0 = ex2(fmaf(__uint_as_float(r[4 * k + 2 * e]), sl2, -ms)),
-                                    y1 = ex2(fmaf(__uint_as_float(r[4 * k + 2 * e + 1]), sl2, -ms));
-                        l += y0 + y1;
-                        pw[2 * k + e] = ck_pack(y0, y1);
-                    }
-                    lsum[e] = lsum[e] * alpha[e] + l;
-                }
-                // the last tile's O^T is in: its weights are read, and it may be rescaled
-                if (x > 0) ok = __all_sync(kFull, mbar_wait_ab(bF, (unsigned)(cnt - 1) & 1u, abort));
-                if (raise) {
+                    if (ok) la_weights(tS, tL0, tL1, xs == 0, sP, s_ref + r0, sl2, lim);
                     if (la_any(!ok)) {
                         ok = false;
                         break;
                     }
-                    if (tq == 0) {
-                        s_al[rq] = alpha[0];
-                        s_al[rq + 8] = alpha[1];
-                    }
-                    la_sync();
-                    if (x > 0) {
-                        tc_fence_after();
-#pragma unroll 1
-                        for (int m = 0; m < 2 * NM; ++m) {
-                            const uint32_t tO = taddr + lane_off + OC + 32 * m;
-                            uint32_t o[32];
-                            tc_ld32(tO, o);
-                            tc_wait_ld();
-#pragma unroll
-                            for (int c = 0; c < 32; ++c)
-                                o[c] = __float_as_uint(__uint_as_float(o[c]) * s_al[(32 * m & 32) + c]);
-                            tc_st32(tO, o);
-                        }
-                        tc_wait_st();
-                    }
-                    la_sync();   // the factors are read
                 }
-                if (!ok) continue;   // the next vote ends it for every warp
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    *reinterpret_cast<uint32_t *>(sP + k * kLaCS + rq * 16 + tq * 4) = pw[2 * k];
-                    *reinterpret_cast<uint32_t *>(sP + k * kLaCS + (rq + 8) * 16 + tq * 4) = pw[2 * k + 1];
-                }
-                fence_proxy_async();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bP[b]);
+                if (th == 0) mbar_arrive(&bP[b]);   // (after the vote: every warp's weights are in)
+                ++cnt;
+                u.next(KS);
             }
-            ok = ok && __all_sync(kFull, mbar_wait_ab(bF, (unsigned)(cnt - 1) & 1u, abort));
+            if (!ok) break;
+            ok = __all_sync(kFull, mbar_wait_ab(&bF[~cnt & 1], (unsigned)((cnt - 1) >> 1) & 1u, abort));
             if (la_any(!ok)) {
                 ok = false;
                 break;
             }
             tc_fence_after();
-            // the rows' sums, and the output: thread = channel, a row at a time
-            const bool part = sg.nx < sg.nt;
-            const size_t pr = (size_t)(2 * blockIdx.x + (sg.x0 == 0 ? 1 : 0)) * kLatRows;
+            // the rows' sums over the threads: halves exchanged, lane c ends with row c
+            float lsum[kLaCols];
+            {
+                uint32_t l[kLaCols];
+                tc_ld32(tL + kLatRows * (nx & 1), l);
+                tc_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                lsum[e] += __shfl_xor_sync(kFull, lsum[e], 1);
-                lsum[e] += __shfl_xor_sync(kFull, lsum[e], 2);
-                if (tq == 0) {
-                    s_al[rq + 8 * e] = 1.f / lsum[e];
-                    if (part && sg.row0 + rq + 8 * e < sg.nrows)
-                        reinterpret_cast<float2 *>(a.ml)[pr + rq + 8 * e] = make_float2(ref[e], lsum[e]);
+                for (int c = 0; c < kLaCols; ++c) lsum[c] = __uint_as_float(l[c]);
+            }
+#pragma unroll
+            for (int o = kLaCols / 2; o; o >>= 1)
+#pragma unroll
+                for (int c = 0; c < o; ++c) {
+                    const bool hi = lane & o;
+                    const float give = hi ? lsum[c] : lsum[c + o], keep = hi ? lsum[c + o] : lsum[c];
+                    lsum[c] = keep + __shfl_xor_sync(kFull, give, o);
                 }
+            s_red[warp & 3][r0 + lane] = lsum[0];
+            la_sync();
+            const bool part = nx < s_seg.nt;
+            const size_t pr = (size_t)(2 * blockIdx.x + (first == 0 ? 1 : 0)) * kLatRows;
+            if (tid < kLatRows) {
+                const float l = s_red[0][tid] + s_red[1][tid] + s_red[2][tid] + s_red[3][tid];
+                s_al[tid] = 1.f / l;
+                if (part && s_seg.row0 + tid < s_seg.nrows)
+                    reinterpret_cast<float2 *>(a.ml)[pr + tid] = make_float2(s_ref[tid] == kLaUnset ? -INFINITY : -s_ref[tid], l);
             }
             la_sync();
-            const int rows = min(sg.nrows - sg.row0, kLatRows), chan = 32 * warp + lane;
+            // the output: thread = channel, a row at a time
+            const int rows = min(s_seg.nrows - s_seg.row0 - r0, kLaCols);
 #pragma unroll 1
-            for (int m = 0; m < 2 * NM; ++m) {
-                const int q0 = 32 * (m & 1);
-                if (q0 >= rows) continue;
-                uint32_t o[32];
-                tc_ld32(taddr + lane_off + OC + 32 * m, o);
+            for (int m = 0; m < NM && rows > 0; ++m) {
+                uint32_t o[kLaCols];
+                tc_ld32(tO + kLatRows * m, o);
                 tc_wait_ld();
-                const int ch = 128 * (m >> 1) + chan;
+                const int ch = 128 * m + tok;
 #pragma unroll
-                for (int c = 0; c < 32; ++c) {
-                    const int q = q0 + c;
-                    if (q >= rows) break;
+                for (int c = 0; c < kLaCols; ++c) {
+                    if (c >= rows) break;
+                    const int q = r0 + c;
                     if (part) {
                         a.acc[(pr + q) * RD + ch] = __uint_as_float(o[c]);
                     } else {
-                        const int rw = sg.row0 + q, tok = chunk_div(a, rw);
-                        O[(((size_t)sg.i * h + rw - tok * h) * a.n_stride + tok) * RD + ch] =
+                        const int rw = s_seg.row0 + q, tk = chunk_div(a, rw);
+                        O[(((size_t)s_seg.i * h + rw - tk * h) * a.n_stride + tk) * RD + ch] =
                             __float2half_rn(__uint_as_float(o[c]) * s_al[q]);
                     }
                 }
             }
             tc_fence_before();
-            la_sync();   // the factors are read
+            la_sync();   // the sums and references are read
         }
         if (!ok && lane == 0) {
             s_abort = 1;
@@ -524,22 +633,96 @@ __global__ void __launch_bounds__(kLaThreads, 1)
     if (warp == 0) tc_dealloc(taddr, 512);
 }
 
-template <int RD>
+// Joins the partials of the row tiles that CTA boundaries cut (a block per
+// boundary and RB rows, 8 / RB warps a row that take every so-manieth partial):
+// weights 2^(m_k - M), M the largest m.
+template <int RD, int RB>
+__global__ void __launch_bounds__(256) latent_join_kernel(__half *__restrict__ O, const __grid_constant__ ChunkArgs a) {
+    constexpr int W = 8 / RB, V = RD / 128;   // warps a row, 16-byte pieces a lane
+    __shared__ __align__(16) float s_acc[RB][W][RD];
+    __shared__ float s_l[RB][W];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rr = warp / W, w = warp % W;
+    const int c = blockIdx.x / (kLatRows / RB) + 1, r = blockIdx.x % (kLatRows / RB) * RB + rr;
+    const ChunkPos &p = a.cta[c];
+    if (p.o <= kCkLead) return;   // CTA c starts with a row tile of its own
+    const int i = p.i, m = p.m;
+    const long long first = p.u - p.o + kCkLead;                         // the unit of its first tile
+    if (a.cta[c - 1].u > first) return;                                  // an earlier boundary owns it
+    const int nrows = min(a.n[i] * a.hg - m * kLatRows, kLatRows);
+    if (blockIdx.x % (kLatRows / RB) * RB >= nrows) return;
+    const long long end = first + chunk_tiles(a, i, m);
+    int c1 = c;                                                          // the last CTA with its tiles
+    while (a.cta[c1 + 1].u < end) ++c1;
+    const int c0 = c - 1;   // (holds the first tile, slot 2 c + 1; the others start in it, slot 2 c)
+    const float2 *ml = reinterpret_cast<const float2 *>(a.ml);
+    float4 acc[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+    float L = 0.f;
+    if (r < nrows) {
+        auto part = [&](int k) { return (size_t)(2 * k + (k == c0 ? 1 : 0)) * kLatRows + r; };
+        float M = -INFINITY;
+        for (int k = c0 + lane; k <= c1; k += 32) M = fmaxf(M, ml[part(k)].x);
+        M = la_redux_max(M);
+#pragma unroll 4
+        for (int k = c0 + w; k <= c1; k += W) {
+            const float2 x = ml[part(k)];
+            const float wt = x.x == -INFINITY ? 0.f : ex2(x.x - M);   // (sees nothing of this share)
+            const float4 *src = reinterpret_cast<const float4 *>(a.acc + part(k) * RD) + lane;
+            L = fmaf(wt, x.y, L);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const float4 y = src[32 * v];
+                acc[v].x = fmaf(wt, y.x, acc[v].x);
+                acc[v].y = fmaf(wt, y.y, acc[v].y);
+                acc[v].z = fmaf(wt, y.z, acc[v].z);
+                acc[v].w = fmaf(wt, y.w, acc[v].w);
+            }
+        }
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) reinterpret_cast<float4 *>(s_acc[rr][w])[lane + 32 * v] = acc[v];
+    if (lane == 0) s_l[rr][w] = L;
+    __syncthreads();
+    if (r >= nrows) return;
+    // the row's warps share its channels, two a thread and turn
+    float l = 0.f;
+#pragma unroll
+    for (int k = 0; k < W; ++k) l += s_l[rr][k];
+    const float inv = 1.f / l;
+    const int row = m * kLatRows + r, tok = chunk_div(a, row);
+    __half *dst = O + (((size_t)i * a.hq + row - tok * a.hg) * a.n_stride + tok) * RD;
+    for (int e = 2 * (32 * w + lane); e < RD; e += 64 * W) {
+        float2 y = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < W; ++k) {
+            const float2 z = *reinterpret_cast<const float2 *>(&s_acc[rr][k][e]);
+            y.x += z.x;
+            y.y += z.y;
+        }
+        *reinterpret_cast<uint32_t *>(dst + e) = ck_pack(y.x * inv, y.y * inv);
+    }
+}
+
+template <int RD, int BITS>
 cudaError_t launch(const LatentGeom &g, const LatentDev &dv, const __half *Q, const __half *Qr, const __half *C,
                    const __half *Kr, __half *O, const ChunkArgs &a, const ChunkPlan &plan, float scale, cudaStream_t st) {
     CUtensorMap tc, tk;
     const long long rows = (long long)g.b * a.n_stride;
-    cudaError_t e = make_tile_map(&tc, C, rows, RD, KIVI_KBLK);
-    if (e == cudaSuccess) e = make_tile_map(&tk, Kr, rows, kLatRope, KIVI_KBLK);
+    cudaError_t e = make_sw_map(&tc, C, rows, RD, kLatTok);
+    if (e == cudaSuccess) e = make_sw_map(&tk, Kr, rows, kLatRope, kLatTok);
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(latent_attn_kernel<RD>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)la_smem(RD));
+        e = cudaFuncSetAttribute(latent_attn_kernel<RD, BITS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)la_smem(RD));
     if (e != cudaSuccess) return e;
-    latent_attn_kernel<RD><<<plan.ctas, kLaThreads, la_smem(RD), st>>>(g, dv, Q, Qr, C, Kr, O, tc, tk,
-                                                                      scale * 1.4426950408889634f, a);
+    latent_attn_kernel<RD, BITS><<<plan.ctas, kLaThreads, la_smem(RD), st>>>(g, dv, Q, Qr, C, Kr, O, tc, tk,
+                                                                            scale * 1.4426950408889634f, a);
     e = cudaGetLastError();
     if (e != cudaSuccess || !plan.join) return e;
-    const unsigned blocks = (unsigned)(plan.ctas - 1) * (kLatRows / kJoinRows);
-    chunk_join_kernel<RD><<<blocks, 256, 0, st>>>(O, a);
+    long long tiles = 0;
+    for (int i = 0; i < g.b; ++i) tiles += chunk_row_tiles(a, i);
+    // many partials a row tile: all of a block's warps at one row
+    if (plan.ctas > 8 * tiles) latent_join_kernel<RD, 1><<<(plan.ctas - 1) * kLatRows, 256, 0, st>>>(O, a);
+    else latent_join_kernel<RD, 4><<<(plan.ctas - 1) * (kLatRows / 4), 256, 0, st>>>(O, a);
     return cudaGetLastError();
 }
 
@@ -550,9 +733,9 @@ bool kivi_plan_latent(const LatentGeom &g, int h, ChunkArgs &a, int num_sms, Chu
     a.hg_mul = (unsigned)(((1ull << 32) + h - 1) / h);
     a.vis = Visible{0, 0};
     a.tile_rows = kLatRows;
-    a.tile_blocks = 1;
+    a.tile_blocks = kLatTok / KIVI_KBLK;
     *plan = ChunkPlan{false, false, 0};
-    return kivi_plan_units(g.b, 1, a, num_sms, 2 * kCkLead, &plan->ctas, &plan->join);
+    return kivi_plan_units(g.b, 1, a, num_sms, kCkLead, &plan->ctas, &plan->join);
 }
 
 size_t kivi_latent_partial_floats(const LatentGeom &g, int num_sms) {
@@ -564,6 +747,9 @@ cudaError_t kivi_launch_latent_attn(const LatentGeom &g, const LatentDev &dv, co
                                     float scale, float *partials, int num_sms, cudaStream_t st) {
     a.acc = partials;
     a.ml = partials + (size_t)2 * num_sms * kLatRows * g.r;
-    return g.r == 256 ? launch<256>(g, dv, Q, Qr, C, Kr, O, a, plan, scale, st)
-                      : launch<512>(g, dv, Q, Qr, C, Kr, O, a, plan, scale, st);
+    if (g.r == 256)
+        return g.bits == 2 ? launch<256, 2>(g, dv, Q, Qr, C, Kr, O, a, plan, scale, st)
+                           : launch<256, 4>(g, dv, Q, Qr, C, Kr, O, a, plan, scale, st);
+    return g.bits == 2 ? launch<512, 2>(g, dv, Q, Qr, C, Kr, O, a, plan, scale, st)
+                       : launch<512, 4>(g, dv, Q, Qr, C, Kr, O, a, plan, scale, st);
 }

@@ -23,15 +23,6 @@ __device__ __forceinline__ void tma_tile(void *dst, const CUtensorMap *tm, int r
         : "memory");
 }
 
-// the same without telling the barrier of its bytes (the caller has)
-__device__ __forceinline__ void tma_box(void *dst, const CUtensorMap *tm, int row0, uint64_t *bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, "
-        "%4}], [%5];" ::"r"(smem_u32(dst)),
-        "l"(tm), "r"(0), "r"(row0), "r"(0), "r"(smem_u32(bar))
-        : "memory");
-}
-
 // The encoder of TMA tensor maps, from the driver (through the runtime, no
 // link to the driver library); null if unavailable.
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {

@@ -45,9 +45,12 @@ struct VerifyArgs {
 
 __device__ __forceinline__ float vf_float(float x) { return x; }
 __device__ __forceinline__ float vf_float(__half x) { return __half2float(x); }
-// units of a probability; not a number and below zero: none, above one: one
+// units of a probability: its 24 bits, shifted (conversions to 64-bit integers
+// are slow here); not a number and below zero: none, above one: one
 __device__ __forceinline__ u64 vf_units(float p) {
-    return p > 0.f ? __float2ull_rz(fminf(p, 1.f) * 0x1p40f) : 0ull;
+    const unsigned b = min(__float_as_uint(p), 0x3f800000u);   // (for p > 0)
+    const u64 v = (u64)((b & 0x7fffffu) | 0x800000u) << 17 >> min(127u - (b >> 23), 63u);
+    return p > 0.f ? v : 0ull;
 }
 __device__ __forceinline__ u64 vf_warp_sum(u64 x) {
 #pragma unroll
@@ -161,7 +164,7 @@ __global__ void __launch_bounds__(kVfThreads) verify_kernel(const __grid_constan
     const u64 total = plain ? tp : tw;
     // floor(U total / 2^30)
     const float uu = u[a.n_stride];
-    const u64 U = uu > 0.f ? __float2ull_rz(fminf(uu, 1.f - 0x1p-24f) * 0x1p30f) : 0ull;
+    const u64 U = uu > 0.f ? __float2uint_rz(fminf(uu, 1.f - 0x1p-24f) * 0x1p30f) : 0u;
     const u64 mark = U * (total >> 30) + ((U * (total & ((1ull << 30) - 1))) >> 30);
     if (rank == 0) {
         for (int r = tid; r <= a.n_stride; r += kVfThreads)
