@@ -14,7 +14,8 @@
 // stage; x by 16-byte asynchronous copies (any row of any sequence), W by TMA as
 // the operand lies in memory, K-major or N-major, both in the 128-byte swizzle.
 // Two CTAs an SM, so that one's first loads and last stores run under the other's
-// products.
+// products; with fewer CTAs than SMs one an SM and twice the stages, so that most
+// of W is on its way at once.
 #include <cstring>
 
 #include "../../include/kivi.h"
@@ -27,11 +28,10 @@
 namespace {
 
 constexpr int kHpRows = 128, kHpCols = 128, kHpK = 64;
-constexpr int kHpStages = 3;
 constexpr int kHpThreads = 32 * 6;
 constexpr unsigned kHpFull = 0xffffffffu;
 constexpr int kHpA = kHpK * kHpRows * 2, kHpB = kHpK * kHpCols * 2;
-constexpr size_t kHpSmem = (size_t)kHpStages * (kHpA + kHpB) + 1024;
+__host__ __device__ constexpr size_t hp_smem(int stages) { return (size_t)stages * (kHpA + kHpB) + 1024; }
 
 struct HeadArgs {
     const __half *x;
@@ -57,20 +57,20 @@ __device__ __forceinline__ int2 hp_row(const HeadArgs &a, int row) {
 }
 
 // Warps 0-3: x's tiles, then the output; 4: W's tiles; 5: the products.
-template <bool MN>
-__global__ void __launch_bounds__(kHpThreads, 2)
+template <bool MN, int S>   // S: stages
+__global__ void __launch_bounds__(kHpThreads, S > 3 ? 1 : 2)
     head_product_kernel(const __grid_constant__ HeadArgs a, const __grid_constant__ CUtensorMap tm) {
     extern __shared__ unsigned char raw[];
-    unsigned char *sA = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u), *sB = sA + kHpStages * kHpA;
-    __shared__ __align__(8) uint64_t bars[3 * kHpStages + 1];
-    uint64_t *const bA = bars, *const bB = bA + kHpStages, *const eS = bB + kHpStages, *const bD = eS + kHpStages;
+    unsigned char *sA = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u), *sB = sA + S * kHpA;
+    __shared__ __align__(8) uint64_t bars[3 * S + 1];
+    uint64_t *const bA = bars, *const bB = bA + S, *const eS = bB + S, *const bD = eS + S;
     __shared__ uint32_t s_taddr;
     __shared__ int s_abort;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int row0 = blockIdx.x * kHpRows, col0 = blockIdx.y * kHpCols, e = blockIdx.z;
     const int rows = a.first[a.b], nk = a.K / kHpK;
-    if (tid < 3 * kHpStages + 1) {
-        mbar_init(&bars[tid], tid < kHpStages ? 4 : 1);
+    if (tid < 3 * S + 1) {
+        mbar_init(&bars[tid], tid < S ? 4 : 1);
         fence_mbar_init();
     }
     if (tid == 0) s_abort = 0;
@@ -98,23 +98,23 @@ __global__ void __launch_bounds__(kHpThreads, 2)
         auto told = [&](int it) {   // the stage's copies of this warp are in
             fence_proxy_async();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bA[it % kHpStages]);
+            if (lane == 0) mbar_arrive(&bA[it % S]);
         };
         for (int it = 0; it < nk && ok; ++it) {
-            const int s = it % kHpStages;
-            ok = __all_sync(kHpFull, it < kHpStages || mbar_wait_ab(&eS[s], (unsigned)(it / kHpStages + 1) & 1u, abort));
+            const int s = it % S;
+            ok = __all_sync(kHpFull, it < S || mbar_wait_ab(&eS[s], (unsigned)(it / S + 1) & 1u, abort));
             if (!ok) break;
             unsigned char *dst = sA + s * kHpA + at;
 #pragma unroll
             for (int k = 0; k < NR; ++k) hp_copy16(dst + k * 16 * 128, src[k] + it * kHpK, (in >> k) & 1u);
             asm volatile("cp.async.commit_group;" ::: "memory");
-            if (it > 0) {
-                asm volatile("cp.async.wait_group 1;" ::: "memory");
-                told(it - 1);
+            if (it >= S - 2) {
+                asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
+                told(it - (S - 2));
             }
         }
         asm volatile("cp.async.wait_group 0;" ::: "memory");
-        if (ok) told(nk - 1);
+        for (int it = max(0, nk - (S - 2)); it < nk && ok; ++it) told(it);
         ok = ok && __all_sync(kHpFull, mbar_wait_ab(bD, 0u, abort));
         if (ok) {
             tc_fence_after();
@@ -147,8 +147,8 @@ __global__ void __launch_bounds__(kHpThreads, 2)
         if (lane == 0) {
             int it = 0;
             for (; it < nk; ++it) {
-                const int s = it % kHpStages;
-                ok = it < kHpStages || mbar_wait_ab(&eS[s], (unsigned)(it / kHpStages + 1) & 1u, abort);
+                const int s = it % S;
+                ok = it < S || mbar_wait_ab(&eS[s], (unsigned)(it / S + 1) & 1u, abort);
                 if (!ok) break;
                 mbar_expect_tx(&bB[s], kHpB);
                 unsigned char *dst = sB + s * kHpB;
@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(kHpThreads, 2)
                 atomicOr(a.status, KIVI_FLAG_WAIT);
             }
             // every copy has landed before shared memory is given up (bounded)
-            for (int y = max(0, it - kHpStages); y < it; ++y) mbar_wait(&bB[y % kHpStages], (unsigned)(y / kHpStages) & 1u);
+            for (int y = max(0, it - S); y < it; ++y) mbar_wait(&bB[y % S], (unsigned)(y / S) & 1u);
         }
         __syncwarp();
     } else {
@@ -172,8 +172,8 @@ __global__ void __launch_bounds__(kHpThreads, 2)
         const uint64_t da = tc_desc_sw(sA, 16, 1024), db = MN ? tc_desc_sw(sB, kHpB / 2, 1024) : tc_desc_sw(sB, 16, 1024);
         int it = 0;
         for (; it < nk; ++it) {
-            const int s = it % kHpStages;
-            const unsigned ph = (unsigned)(it / kHpStages) & 1u;
+            const int s = it % S;
+            const unsigned ph = (unsigned)(it / S) & 1u;
             ok = __all_sync(kHpFull, mbar_wait_ab(&bA[s], ph, abort) && mbar_wait_ab(&bB[s], ph, abort));
             if (!ok) break;
             tc_fence_after();
@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(kHpThreads, 2)
         }
         // every product and commit is done before memory is given up (bounded)
         tc_commit_w(bD);
-        for (int y = max(0, it - kHpStages); y < it; ++y) mbar_wait(&eS[y % kHpStages], (unsigned)(y / kHpStages) & 1u);
+        for (int y = max(0, it - S); y < it; ++y) mbar_wait(&eS[y % S], (unsigned)(y / S) & 1u);
         mbar_wait(bD, 0u);
         __syncwarp();
     }
@@ -237,17 +237,22 @@ extern "C" kivi_status kivi_head_product(const void *x, const void *w, int b, in
     a.n_stride = n_stride;
     a.K = K;
     a.N = N;
-    a.status = kivi_device_status();
-    if (!a.status) return fail(KIVI_ERR_CUDA, "no status word on the current device");
+    KiviDeviceInfo info;
+    if (!kivi_device_info(&info)) return fail(KIVI_ERR_CUDA, "no status word on the current device");
+    a.status = info.status;
     const bool mn = transposed != 0;
     CUtensorMap tm;
     cudaError_t e = mn ? make_sw_map(&tm, (const __half *)w, (long long)h * K, N, kHpK)
                        : make_sw_map(&tm, (const __half *)w, (long long)h * N, K, kHpCols);
-    const auto kernel = mn ? head_product_kernel<true> : head_product_kernel<false>;
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kHpSmem);
-    if (e != cudaSuccess) return fail(KIVI_ERR_CUDA, cudaGetErrorString(e));
     const dim3 grid((unsigned)((rows + kHpRows - 1) / kHpRows), (unsigned)(N / kHpCols), (unsigned)h);
-    kernel<<<grid, kHpThreads, kHpSmem, (cudaStream_t)stream>>>(a, tm);
+    const bool deep = K > 2 * kHpK && (long long)grid.x * grid.y * grid.z <= info.sms;
+    const auto kernel = deep ? (mn ? head_product_kernel<true, 6> : head_product_kernel<false, 6>)
+                             : (mn ? head_product_kernel<true, 3> : head_product_kernel<false, 3>);
+    const size_t smem = hp_smem(deep ? 6 : 3);
+    static std::atomic<uint64_t> done[4];
+    if (e == cudaSuccess) e = kivi_allow_smem(kernel, smem, info.device, done[2 * deep + mn]);
+    if (e != cudaSuccess) return fail(KIVI_ERR_CUDA, cudaGetErrorString(e));
+    kernel<<<grid, kHpThreads, smem, (cudaStream_t)stream>>>(a, tm);
     e = cudaGetLastError();
     return e == cudaSuccess ? KIVI_OK : fail(KIVI_ERR_CUDA, cudaGetErrorString(e));
 }

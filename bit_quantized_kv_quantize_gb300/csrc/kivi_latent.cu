@@ -185,9 +185,25 @@ cudaError_t kivi_launch_latent_restore(const LatentGeom &g, const LatentDev &dv,
     return cudaGetLastError();
 }
 
-unsigned *kivi_device_status() {
+bool kivi_device_info(KiviDeviceInfo *info) {
+    constexpr int N = 64;
+    static std::mutex mu;
+    static KiviDeviceInfo known[N];   // (status null: not asked for yet)
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return false;
+    std::lock_guard<std::mutex> lk(mu);
+    if (dev < N && known[dev].status) {
+        *info = known[dev];
+        return true;
+    }
     void *p = nullptr;
-    return cudaGetSymbolAddress(&p, g_status) == cudaSuccess ? (unsigned *)p : nullptr;
+    info->device = dev;
+    if (cudaDeviceGetAttribute(&info->sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+        cudaGetSymbolAddress(&p, g_status) != cudaSuccess)
+        return false;
+    info->status = (unsigned *)p;
+    if (dev < N) known[dev] = *info;
+    return true;
 }
 
 // ---------------------------------------------------------------------------
@@ -418,7 +434,7 @@ kivi_status kivi_latent_attn(kivi_latent_t c, const void *q, const void *q_rope,
     }
     const cudaError_t e = kivi_launch_latent_attn(c->g, c->dv, (const __half *)q, (const __half *)q_rope,
                                                   (const __half *)C, (const __half *)Kr, (__half *)out, a, plan, scale,
-                                                  c->part, c->num_sms, (cudaStream_t)stream);
+                                                  c->part, c->device, c->num_sms, (cudaStream_t)stream);
     if (e != cudaSuccess) return fail_cuda(c, e, "latent_attn");
     return KIVI_OK;
 }
@@ -473,11 +489,12 @@ kivi_status kivi_latent_check(kivi_latent_t c, uint32_t *flags, kivi_stream_t st
 kivi_status kivi_device_check(uint32_t *flags, kivi_stream_t stream) {
     kivi_set_last_error("");
     if (!flags) return fail(KIVI_ERR_INVALID_ARG, "flags is null");
-    unsigned *p = kivi_device_status();
+    KiviDeviceInfo info;
+    if (!kivi_device_info(&info)) return fail(KIVI_ERR_CUDA, "no status word on the current device");
     const cudaStream_t st = (cudaStream_t)stream;
-    cudaError_t e = p ? cudaMemcpyAsync(flags, p, 4, cudaMemcpyDeviceToHost, st) : cudaErrorInvalidValue;
+    cudaError_t e = cudaMemcpyAsync(flags, info.status, 4, cudaMemcpyDeviceToHost, st);
     if (e == cudaSuccess) e = cudaStreamSynchronize(st);
-    if (e == cudaSuccess) e = cudaMemsetAsync(p, 0, 4, st);
+    if (e == cudaSuccess) e = cudaMemsetAsync(info.status, 0, 4, st);
     if (e == cudaSuccess) e = cudaStreamSynchronize(st);
     return e == cudaSuccess ? KIVI_OK : fail_cuda(nullptr, e, "device_check");
 }

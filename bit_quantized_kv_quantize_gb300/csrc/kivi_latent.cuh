@@ -18,6 +18,8 @@
 //            tokens too, as their codes restore them: every block from Tq / 128 on
 //            is there whole.
 #pragma once
+#include <atomic>
+
 #include "kivi_chunk.cuh"
 #include "kivi_internal.cuh"
 
@@ -74,7 +76,20 @@ bool kivi_plan_latent(const LatentGeom &g, int h, ChunkArgs &a, int num_sms, Chu
 size_t kivi_latent_partial_floats(const LatentGeom &g, int num_sms);
 cudaError_t kivi_launch_latent_attn(const LatentGeom &g, const LatentDev &dv, const __half *Q, const __half *Qr,
                                     const __half *C, const __half *Kr, __half *O, ChunkArgs &a, const ChunkPlan &plan,
-                                    float scale, float *partials, int num_sms, cudaStream_t st);
-// The status word of the calls without a handle, on the current device
-// (kivi_latent.cu); null: not available.
-unsigned *kivi_device_status();
+                                    float scale, float *partials, int device, int num_sms, cudaStream_t st);
+// What the calls without a handle need of the current device: its number, SMs, and
+// their status word (kivi_latent.cu; asked for once a device).  False: not available.
+struct KiviDeviceInfo {
+    int device, sms;
+    unsigned *status;
+};
+bool kivi_device_info(KiviDeviceInfo *info);
+// Shared memory that a kernel may take, set once a device (done: a bit each).
+template <typename K>
+cudaError_t kivi_allow_smem(K *kernel, size_t bytes, int device, std::atomic<uint64_t> &done) {
+    const uint64_t bit = 1ull << (device & 63);
+    if (device < 64 && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess && device < 64) done.fetch_or(bit, std::memory_order_release);
+    return e;
+}

@@ -464,20 +464,19 @@ __global__ void __launch_bounds__(kLaThreads, 1)
             const unsigned char *rec = dv.rec + lat_rec(g, sg.i, first);
             // Q: row (token, head), 8 rows x 4 chunks at a time; rows past the last
             // are zero (the last segment's scores are all read)
-            constexpr int QN = kLatRows * (RD + kLatRope) / 8 / (32 * kLaWork), QB = QN % 6 == 0 ? 6 : 5;
-#pragma unroll 1
-            for (int k0 = 0; k0 < QN; k0 += QB) {
-                uint4 v[QB];
+            constexpr int QN = kLatRows * (RD + kLatRope) / 8 / (32 * kLaWork);
+            {
+                uint4 v[QN];
 #pragma unroll
-                for (int k = 0; k < QB; ++k) {
-                    const int blk = (k0 + k) * kLaWork + warp, q = 8 * (blk & 7) + (lane & 7), c = 4 * (blk >> 3) + (lane >> 3);
+                for (int k = 0; k < QN; ++k) {
+                    const int q = 8 * warp + (lane & 7), c = 4 * k + (lane >> 3);   // (warp w: rows 8 w ..)
                     const int rw = min(sg.row0 + q, sg.nrows - 1), tk = chunk_div(a, rw);
                     const size_t row = ((size_t)sg.i * h + rw - tk * h) * a.n_stride + tk;
                     v[k] = *reinterpret_cast<const uint4 *>(c < RD / 8 ? Q + row * RD + 8 * c : Qr + row * kLatRope + 8 * (c - RD / 8));
                 }
 #pragma unroll
-                for (int k = 0; k < QB; ++k) {
-                    const int blk = (k0 + k) * kLaWork + warp, q = 8 * (blk & 7) + (lane & 7), c = 4 * (blk >> 3) + (lane >> 3);
+                for (int k = 0; k < QN; ++k) {
+                    const int q = 8 * warp + (lane & 7), c = 4 * k + (lane >> 3);
                     if (sg.row0 + q >= sg.nrows) v[k] = make_uint4(0u, 0u, 0u, 0u);
                     *reinterpret_cast<uint4 *>(sQ + lat_at(c, q, kLatRows)) = v[k];
                 }
@@ -706,13 +705,14 @@ __global__ void __launch_bounds__(256) latent_join_kernel(__half *__restrict__ O
 
 template <int RD, int BITS>
 cudaError_t launch(const LatentGeom &g, const LatentDev &dv, const __half *Q, const __half *Qr, const __half *C,
-                   const __half *Kr, __half *O, const ChunkArgs &a, const ChunkPlan &plan, float scale, cudaStream_t st) {
+                   const __half *Kr, __half *O, const ChunkArgs &a, const ChunkPlan &plan, float scale, int device,
+                   cudaStream_t st) {
+    static std::atomic<uint64_t> done;
     CUtensorMap tc, tk;
     const long long rows = (long long)g.b * a.n_stride;
     cudaError_t e = make_sw_map(&tc, C, rows, RD, kLatTok);
     if (e == cudaSuccess) e = make_sw_map(&tk, Kr, rows, kLatRope, kLatTok);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(latent_attn_kernel<RD, BITS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)la_smem(RD));
+    if (e == cudaSuccess) e = kivi_allow_smem(latent_attn_kernel<RD, BITS>, la_smem(RD), device, done);
     if (e != cudaSuccess) return e;
     latent_attn_kernel<RD, BITS><<<plan.ctas, kLaThreads, la_smem(RD), st>>>(g, dv, Q, Qr, C, Kr, O, tc, tk,
                                                                             scale * 1.4426950408889634f, a);
@@ -744,12 +744,12 @@ size_t kivi_latent_partial_floats(const LatentGeom &g, int num_sms) {
 
 cudaError_t kivi_launch_latent_attn(const LatentGeom &g, const LatentDev &dv, const __half *Q, const __half *Qr,
                                     const __half *C, const __half *Kr, __half *O, ChunkArgs &a, const ChunkPlan &plan,
-                                    float scale, float *partials, int num_sms, cudaStream_t st) {
+                                    float scale, float *partials, int device, int num_sms, cudaStream_t st) {
     a.acc = partials;
     a.ml = partials + (size_t)2 * num_sms * kLatRows * g.r;
     if (g.r == 256)
-        return g.bits == 2 ? launch<256, 2>(g, dv, Q, Qr, C, Kr, O, a, plan, scale, st)
-                           : launch<256, 4>(g, dv, Q, Qr, C, Kr, O, a, plan, scale, st);
-    return g.bits == 2 ? launch<512, 2>(g, dv, Q, Qr, C, Kr, O, a, plan, scale, st)
-                       : launch<512, 4>(g, dv, Q, Qr, C, Kr, O, a, plan, scale, st);
+        return g.bits == 2 ? launch<256, 2>(g, dv, Q, Qr, C, Kr, O, a, plan, scale, device, st)
+                           : launch<256, 4>(g, dv, Q, Qr, C, Kr, O, a, plan, scale, device, st);
+    return g.bits == 2 ? launch<512, 2>(g, dv, Q, Qr, C, Kr, O, a, plan, scale, device, st)
+                       : launch<512, 4>(g, dv, Q, Qr, C, Kr, O, a, plan, scale, device, st);
 }

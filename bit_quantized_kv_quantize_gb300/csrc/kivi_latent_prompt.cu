@@ -383,8 +383,9 @@ extern "C" kivi_status kivi_latent_prompt_attn(const void *q, const void *q_rope
     a.mt = (maxt + 2 * kLpRows - 1) / (2 * kLpRows);
     a.sl2 = scale * 1.4426950408889634f;
     if ((long long)a.mt * b * h > INT_MAX) return fail(KIVI_ERR_UNSUPPORTED, "more than 2^31 row tiles");
-    a.status = kivi_device_status();
-    if (!a.status) return fail(KIVI_ERR_CUDA, "no status word on the current device");
+    KiviDeviceInfo info;
+    if (!kivi_device_info(&info)) return fail(KIVI_ERR_CUDA, "no status word on the current device");
+    a.status = info.status;
     const long long rows = (long long)b * h * t_stride;
     CUtensorMap tq, tqr, tk, tkr, tv;
     cudaError_t e = make_sw_map(&tq, (const __half *)q, rows, kLatHead, kLpRows);
@@ -392,8 +393,8 @@ extern "C" kivi_status kivi_latent_prompt_attn(const void *q, const void *q_rope
     if (e == cudaSuccess) e = make_sw_map(&tk, (const __half *)K, rows, kLatHead, kLpKeys);
     if (e == cudaSuccess) e = make_sw_map(&tkr, (const __half *)Kr, (long long)b * t_stride, kLatRope, kLpKeys);
     if (e == cudaSuccess) e = make_sw_map(&tv, (const __half *)V, rows, kLatHead, kLpKeys);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(latent_prompt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kLpSmem);
+    static std::atomic<uint64_t> done;
+    if (e == cudaSuccess) e = kivi_allow_smem(latent_prompt_kernel, kLpSmem, info.device, done);
     if (e != cudaSuccess) return fail(KIVI_ERR_CUDA, cudaGetErrorString(e));
     latent_prompt_kernel<<<(unsigned)(a.mt * b * h), kLpThreads, kLpSmem, (cudaStream_t)stream>>>(tq, tqr, tk, tkr, tv, a);
     e = cudaGetLastError();

@@ -21,7 +21,7 @@
 #include <cooperative_groups.h>
 
 #include "../../include/kivi.h"
-#include "kivi_internal.cuh"
+#include "kivi_latent.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -48,9 +48,10 @@ __device__ __forceinline__ float vf_float(__half x) { return __half2float(x); }
 // units of a probability: its 24 bits, shifted (conversions to 64-bit integers
 // are slow here); not a number and below zero: none, above one: one
 __device__ __forceinline__ u64 vf_units(float p) {
-    const unsigned b = min(__float_as_uint(p), 0x3f800000u);   // (for p > 0)
-    const u64 v = (u64)((b & 0x7fffffu) | 0x800000u) << 17 >> min(127u - (b >> 23), 63u);
-    return p > 0.f ? v : 0ull;
+    const unsigned b = p > 0.f ? min(__float_as_uint(p), 0x3f800000u) : 0u;
+    const int d = (int)(b >> 23) - 110;   // 2^40 p = m 2^d
+    const unsigned m = ((b & 0x7fffffu) | 0x800000u) >> min(max(-d, 0), 31);
+    return (u64)m << max(d, 0);
 }
 __device__ __forceinline__ u64 vf_warp_sum(u64 x) {
 #pragma unroll
@@ -74,9 +75,11 @@ struct VfRow {
 template <typename T>
 __global__ void __launch_bounds__(kVfThreads) verify_kernel(const __grid_constant__ VerifyArgs a) {
     cg::cluster_group cl = cg::this_cluster();
-    __shared__ u64 s_sum[2][kVfWarps];   // each warp's weights, and units of p
+    __shared__ u64 s_sum[2][kVfMaxCluster][kVfWarps];   // the warps' weights, and units of p, of every CTA
     __shared__ u64 s_scan[kVfWarps];
-    __shared__ int s_first;
+    __shared__ u64 s_mark, s_before;
+    __shared__ int s_first, s_which;
+    __shared__ bool s_plain;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int i = blockIdx.y, rank = blockIdx.x, C = gridDim.x, n = a.n[i];
     const T *P = (const T *)a.p + (size_t)i * (a.n_stride + 1) * a.V;
@@ -84,6 +87,8 @@ __global__ void __launch_bounds__(kVfThreads) verify_kernel(const __grid_constan
     const int *draft = a.draft + (size_t)i * a.n_stride;
     const float *u = a.u + (size_t)i * (a.n_stride + 1);
 
+    const float uu = u[a.n_stride];
+    cl.barrier_arrive();   // (waited for before the first store to another CTA: it has started)
     // the first token that is not kept (every CTA finds it for itself)
     if (warp == 0) {
         int first = n;
@@ -133,68 +138,74 @@ __global__ void __launch_bounds__(kVfThreads) verify_kernel(const __grid_constan
     }
     sw = vf_warp_sum(sw);
     sp = vf_warp_sum(sp);
-    if (lane == 0) {
-        s_sum[0][warp] = sw;
-        s_sum[1][warp] = sp;
+    cl.barrier_wait();
+    // to every CTA (then none reads another's shared memory, which may be given up)
+    if (lane < C) {
+        u64 *s = cl.map_shared_rank(&s_sum[0][rank][warp], lane);
+        s[0] = sw;
+        s[kVfMaxCluster * kVfWarps] = sp;
     }
     cl.sync();
-    // every warp: the sums of all CTAs' warps, lane by lane
-    u64 w[kVfMaxCluster * kVfWarps / 32], tw = 0, tp = 0;
+    // the stretch that holds the mark (every CTA finds it for itself: the first warp,
+    // the sums of all CTAs' warps lane by lane)
+    if (warp == 0) {
+        constexpr int NK = kVfMaxCluster * kVfWarps / 32;
+        const u64 *sums = &s_sum[0][0][0];
+        u64 w[NK], tw = 0;
+        auto take = [&]() {
+            tw = 0;
 #pragma unroll
-    for (int k = 0; k < kVfMaxCluster * kVfWarps / 32; ++k) {
-        const int e = 32 * k + lane;
-        w[k] = 0;
-        if (e < C * kVfWarps) {
-            const u64 *s = cl.map_shared_rank(&s_sum[0][0], e / kVfWarps);
-            w[k] = s[e % kVfWarps];
-            tp += s[kVfWarps + e % kVfWarps];
+            for (int k = 0; k < NK; ++k) {
+                w[k] = 32 * k + lane < C * kVfWarps ? sums[32 * k + lane] : 0ull;
+                tw += w[k];
+            }
+            tw = vf_warp_sum(tw);
+        };
+        take();
+        const bool plain = tw == 0;   // nothing left of the difference: p itself
+        if (plain) {
+            sums += kVfMaxCluster * kVfWarps;
+            take();
         }
-        tw += w[k];
-    }
-    tw = vf_warp_sum(tw);
-    tp = vf_warp_sum(tp);
-    const bool plain = tw == 0;   // nothing left of the difference: p itself
-    if (plain)
+        // floor(U W / 2^30)
+        const u64 U = uu > 0.f ? __float2uint_rz(fminf(uu, 1.f - 0x1p-24f) * 0x1p30f) : 0u;
+        const u64 mark = U * (tw >> 30) + ((U * (tw & ((1ull << 30) - 1))) >> 30);
+        u64 before = 0;
+        int which = -1;   // (none: no weight at all)
 #pragma unroll
-        for (int k = 0; k < kVfMaxCluster * kVfWarps / 32; ++k) {
-            const int e = 32 * k + lane;
-            if (e < C * kVfWarps) w[k] = cl.map_shared_rank(&s_sum[1][0], e / kVfWarps)[e % kVfWarps];
-        }
-    cl.sync();   // the other CTAs' shared memory is not read any more
-    const u64 total = plain ? tp : tw;
-    // floor(U total / 2^30)
-    const float uu = u[a.n_stride];
-    const u64 U = uu > 0.f ? __float2uint_rz(fminf(uu, 1.f - 0x1p-24f) * 0x1p30f) : 0u;
-    const u64 mark = U * (total >> 30) + ((U * (total & ((1ull << 30) - 1))) >> 30);
-    if (rank == 0) {
-        for (int r = tid; r <= a.n_stride; r += kVfThreads)
-            if (r != first || total == 0) a.tokens[(size_t)i * (a.n_stride + 1) + r] = r < first ? draft[r] : -1;
-        if (tid == 0) a.accepted[i] = first;
-    }
-    if (total == 0) return;
-    // the stretch that holds the mark, and the weights before it
-    u64 before = 0;
-    int which = -1;
+        for (int k = 0; k < NK; ++k) {
+            if (32 * k >= C * kVfWarps || which >= 0 || tw == 0) break;
+            u64 c = w[k];
 #pragma unroll
-    for (int k = 0; k < kVfMaxCluster * kVfWarps / 32; ++k) {
-        u64 c = w[k];
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const u64 v = __shfl_up_sync(0xffffffffu, c, o);
-            if (lane >= o) c += v;
-        }
-        const unsigned m = __ballot_sync(0xffffffffu, which < 0 && before + c > mark);
-        if (which < 0) {
+            for (int o = 1; o < 32; o <<= 1) {
+                const u64 v = __shfl_up_sync(0xffffffffu, c, o);
+                if (lane >= o) c += v;
+            }
+            const unsigned m = __ballot_sync(0xffffffffu, before + c > mark);
             if (m) {
-                const int l = __ffs(m) - 1;
-                which = 32 * k + l;
-                before += __shfl_sync(0xffffffffu, c - w[k], l);
+                which = 32 * k + __ffs(m) - 1;
+                before += __shfl_sync(0xffffffffu, c - w[k], __ffs(m) - 1);
             } else {
                 before += __shfl_sync(0xffffffffu, c, 31);
             }
         }
+        if (lane == 0) {
+            s_mark = mark;
+            s_before = before;
+            s_which = which;
+            s_plain = plain;
+        }
+    }
+    __syncthreads();
+    const int which = s_which;
+    if (rank == 0) {
+        for (int r = tid; r <= a.n_stride; r += kVfThreads)
+            if (r != first || which < 0) a.tokens[(size_t)i * (a.n_stride + 1) + r] = r < first ? draft[r] : -1;
+        if (tid == 0) a.accepted[i] = first;
     }
     if (which < 0 || which / kVfWarps != rank) return;
+    const u64 mark = s_mark, before = s_before;
+    const bool plain = s_plain;
     // this CTA's threads share that stretch
     const int l0 = which * a.per, l1 = min(l0 + a.per, a.V), share = (l1 - l0 + kVfThreads - 1) / kVfThreads;
     const int t0 = min(l0 + tid * share, l1), t1 = min(t0 + share, l1);
@@ -259,8 +270,12 @@ extern "C" kivi_status kivi_verify(const void *p, const void *q, int bytes, cons
     A.accepted = accepted;
     A.n_stride = n_stride;
     A.V = vocab;
+    // CTAs a sequence: eight, fewer where the vocabulary is small, or where they
+    // would not all run at once (two an SM)
+    KiviDeviceInfo info;
+    if (!kivi_device_info(&info)) return fail(KIVI_ERR_CUDA, "no current device");
     int C = kVfMaxCluster;
-    while (C > 1 && vocab < 2048 * C) C >>= 1;
+    while (C > 1 && (vocab < 2048 * C || (long long)b * C > 2 * info.sms)) C >>= 1;
     A.per = (vocab + C * kVfWarps - 1) / (C * kVfWarps);
     A.per = (A.per + 31) / 32 * 32;
     cudaLaunchConfig_t cfg = {};
