@@ -537,8 +537,8 @@ __global__ void __launch_bounds__(kLaThreads, 1)
                 const unsigned sP = smem_u32(sC + u.s * TB + CB) + lat_at(r0 / 8, tok, kLatTok);   // (the tile's rotary keys are read once S^T is in)
                 ok = ok && __all_sync(kFull, mbar_wait_ab(&bS[b], (unsigned)(cnt >> 1) & 1u, abort));
                 tc_fence_after();
-                float up = -INFINITY;
-                if (ok) up = la_weights(tS, tL0, tL1, xs == 0, sP, s_ref + r0, sl2, lim);
+                float up = INFINITY;   // (the segment's first tile: a raise at once)
+                if (ok && xs > 0) up = la_weights(tS, tL0, tL1, false, sP, s_ref + r0, sl2, lim);
                 if (la_any(!ok || up > kCkLift + kCkLag)) {   // a raise: then this tile's weights anew
                     if (la_any(!ok)) {   // every warp learns whether one has given up
                         ok = false;
@@ -598,24 +598,34 @@ __global__ void __launch_bounds__(kLaThreads, 1)
                     reinterpret_cast<float2 *>(a.ml)[pr + tid] = make_float2(s_ref[tid] == kLaUnset ? -INFINITY : -s_ref[tid], l);
             }
             la_sync();
-            // the output: thread = channel, a row at a time
-            const int rows = min(s_seg.nrows - s_seg.row0 - r0, kLaCols);
+            // the output: thread = channel, a row at a time; lane c knows where row c
+            // begins
+            const CkSeg se = s_seg;
+            const int rows = min(se.nrows - se.row0 - r0, kLaCols);
+            long long off;
+            {
+                const int q = r0 + lane, rw = min(se.row0 + q, se.nrows - 1), tk = chunk_div(a, rw);
+                off = part ? (long long)(pr + q) * RD : (((long long)se.i * h + rw - tk * h) * a.n_stride + tk) * RD;
+            }
+            const float inv = s_al[r0 + lane];
 #pragma unroll 1
             for (int m = 0; m < NM && rows > 0; ++m) {
                 uint32_t o[kLaCols];
                 tc_ld32(tO + kLatRows * m, o);
                 tc_wait_ld();
                 const int ch = 128 * m + tok;
+                if (part) {
 #pragma unroll
-                for (int c = 0; c < kLaCols; ++c) {
-                    if (c >= rows) break;
-                    const int q = r0 + c;
-                    if (part) {
-                        a.acc[(pr + q) * RD + ch] = __uint_as_float(o[c]);
-                    } else {
-                        const int rw = s_seg.row0 + q, tk = chunk_div(a, rw);
-                        O[(((size_t)s_seg.i * h + rw - tk * h) * a.n_stride + tk) * RD + ch] =
-                            __float2half_rn(__uint_as_float(o[c]) * s_al[q]);
+                    for (int c = 0; c < kLaCols; ++c) {
+                        const long long at = __shfl_sync(kFull, off, c) + ch;
+                        if (c < rows) a.acc[at] = __uint_as_float(o[c]);
+                    }
+                } else {
+#pragma unroll
+                    for (int c = 0; c < kLaCols; ++c) {
+                        const long long at = __shfl_sync(kFull, off, c) + ch;
+                        const float w = __shfl_sync(kFull, inv, c);
+                        if (c < rows) O[at] = __float2half_rn(__uint_as_float(o[c]) * w);
                     }
                 }
             }
@@ -735,7 +745,8 @@ bool kivi_plan_latent(const LatentGeom &g, int h, ChunkArgs &a, int num_sms, Chu
     a.tile_rows = kLatRows;
     a.tile_blocks = kLatTok / KIVI_KBLK;
     *plan = ChunkPlan{false, false, 0};
-    return kivi_plan_units(g.b, 1, a, num_sms, kCkLead, &plan->ctas, &plan->join);
+    // (shares of two units and more: a tile takes as long as 8 of the chunk attention's)
+    return kivi_plan_units(g.b, 1, a, num_sms, 2, &plan->ctas, &plan->join);
 }
 
 size_t kivi_latent_partial_floats(const LatentGeom &g, int num_sms) {
