@@ -16,8 +16,13 @@
 // Two CTAs an SM, so that one's first loads and last stores run under the other's
 // products; with fewer CTAs than SMs one an SM and twice the stages, so that most
 // of W is on its way at once.
-#include <cstring>
-
+//
+// Rows that all heads share (a prompt's expansion) stay in shared memory, 128 of
+// them up to 512 deep, while a CTA goes through several heads: W alone streams, the
+// accumulator has two buffers, and one head's output is written under the next
+// one's products.  (4096 tokens, 512 deep, 32 heads: 23 us, 0.73 PFLOP/s, where a CTA
+// a tile, with twice the traffic from L2 and its own prologue, took 27.  Each CTA
+// waits for W from L2: 131 MB in all, 80 KB on their way an SM.)
 #include "../../include/kivi.h"
 #include "kivi_async.cuh"
 #include "kivi_latent.cuh"
@@ -54,6 +59,29 @@ __device__ __forceinline__ int2 hp_row(const HeadArgs &a, int row) {
         else hi = m;
     }
     return make_int2(lo, row - a.first[lo]);
+}
+
+// A row's 128 columns of the output (dst; null: no row) from the accumulator, a lane
+// a row; read: called once they are read.  (Through shared memory, 64 consecutive
+// bytes of 8 rows a store: no faster with many rows, 0.7 us slower with few.)
+template <typename F>
+__device__ __forceinline__ void hp_store(__half *dst, uint32_t acc, F read) {
+#pragma unroll 1
+    for (int c0 = 0; c0 < kHpCols; c0 += 32) {
+        uint32_t o[32];
+        tc_ld32(acc + c0, o);
+        tc_wait_ld();
+        if (c0 + 32 == kHpCols) read();
+        if (dst)
+#pragma unroll
+            for (int c = 0; c < 32; c += 8) {
+                uint32_t v[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    v[k] = h2u(__floats2half2_rn(__uint_as_float(o[c + 2 * k]), __uint_as_float(o[c + 2 * k + 1])));
+                *reinterpret_cast<uint4 *>(dst + c0 + c) = make_uint4(v[0], v[1], v[2], v[3]);
+            }
+    }
 }
 
 // Warps 0-3: x's tiles, then the output; 4: W's tiles; 5: the products.
@@ -115,27 +143,13 @@ __global__ void __launch_bounds__(kHpThreads, S > 3 ? 1 : 2)
         }
         asm volatile("cp.async.wait_group 0;" ::: "memory");
         for (int it = max(0, nk - (S - 2)); it < nk && ok; ++it) told(it);
+        const int row = row0 + tid;
+        const int2 p = hp_row(a, row < rows ? row : row0);
         ok = ok && __all_sync(kHpFull, mbar_wait_ab(bD, 0u, abort));
         if (ok) {
             tc_fence_after();
-            const int row = row0 + tid;
-            const int2 p = hp_row(a, row < rows ? row : row0);
-            __half *dst = a.out + (((size_t)p.x * a.h + e) * a.n_stride + p.y) * a.N + col0;
-#pragma unroll 1
-            for (int c0 = 0; c0 < kHpCols; c0 += 32) {
-                uint32_t o[32];
-                tc_ld32(taddr + ((uint32_t)(32 * warp) << 16) + c0, o);
-                tc_wait_ld();
-                if (row < rows)
-#pragma unroll
-                    for (int c = 0; c < 32; c += 8) {
-                        uint32_t v[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            v[k] = h2u(__floats2half2_rn(__uint_as_float(o[c + 2 * k]), __uint_as_float(o[c + 2 * k + 1])));
-                        *reinterpret_cast<uint4 *>(dst + c0 + c) = make_uint4(v[0], v[1], v[2], v[3]);
-                    }
-            }
+            hp_store(row < rows ? a.out + (((size_t)p.x * a.h + e) * a.n_stride + p.y) * a.N + col0 : nullptr,
+                     taddr + ((uint32_t)(32 * warp) << 16), [] {});
             tc_fence_before();
         }
         if (!ok && lane == 0) {
@@ -198,6 +212,130 @@ __global__ void __launch_bounds__(kHpThreads, S > 3 ? 1 : 2)
     if (warp == 0) tc_dealloc(taddr, kHpCols);
 }
 
+constexpr int kHsStages = 5, kHsMaxK = 512;
+__host__ __device__ constexpr size_t hs_smem(int K) { return (size_t)kHpRows * K * 2 + (size_t)kHsStages * kHpB + 1024; }
+
+// The rows of all heads alike: CTA (row tile, group) makes tiles [per y, per (y +
+// 1)) of the heads' 128-column tiles.  Warps as above.
+__global__ void __launch_bounds__(kHpThreads, 1)
+    head_product_shared_kernel(const __grid_constant__ HeadArgs a, const __grid_constant__ CUtensorMap tm, int per) {
+    extern __shared__ unsigned char raw[];
+    constexpr int S = kHsStages;
+    const int nk = a.K / kHpK, nc = a.N / kHpCols;
+    unsigned char *sA = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u), *sB = sA + nk * kHpA;
+    // counts 4: x in, buffer read [buffer]; 1: the others
+    __shared__ __align__(8) uint64_t bars[3 + 2 * S + 3];
+    uint64_t *const bA = bars, *const eD = bars + 1, *const bB = bars + 3, *const eS = bB + S, *const bD = eS + S, *const bE = bD + 2;
+    __shared__ uint32_t s_taddr;
+    __shared__ int s_abort;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int row0 = blockIdx.x * kHpRows, rows = a.first[a.b];
+    const int j0 = blockIdx.y * per, j1 = min(j0 + per, a.h * nc);
+    if (tid < 3 + 2 * S + 3) {
+        mbar_init(&bars[tid], tid < 3 ? 4 : 1);
+        fence_mbar_init();
+    }
+    if (tid == 0) s_abort = 0;
+    if (warp == 0) tc_alloc(&s_taddr, 2 * kHpCols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t taddr = s_taddr;
+    const volatile int *abort = &s_abort;
+    bool ok = true;
+
+    if (warp < 4) {
+        constexpr int NR = kHpRows / 16;
+        const unsigned at = (tid >> 3) * 128 + (((tid & 7) ^ ((tid >> 3) & 7)) * 16);
+#pragma unroll
+        for (int k = 0; k < NR; ++k) {
+            const int row = row0 + (tid >> 3) + 16 * k;
+            const int2 p = hp_row(a, row < rows ? row : row0);
+            const __half *src = a.x + ((size_t)p.x * a.n_stride + p.y) * a.K + 8 * (tid & 7);
+            for (int it = 0; it < nk; ++it) hp_copy16(sA + it * kHpA + at + k * 16 * 128, src + it * kHpK, row < rows);
+        }
+        asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bA);
+        const int row = row0 + tid;
+        const int2 p = hp_row(a, row < rows ? row : row0);
+        for (int j = j0; j < j1 && ok; ++j) {
+            const int y = j - j0, b = y & 1, e = j / nc, col0 = (j - e * nc) * kHpCols;
+            ok = __all_sync(kHpFull, mbar_wait_ab(&bD[b], (unsigned)(y >> 1) & 1u, abort));
+            if (!ok) break;
+            tc_fence_after();
+            hp_store(row < rows ? a.out + (((size_t)p.x * a.h + e) * a.n_stride + p.y) * a.N + col0 : nullptr,
+                     taddr + ((uint32_t)(32 * warp) << 16) + kHpCols * b, [&] {   // the buffer is read
+                         tc_fence_before();
+                         __syncwarp();
+                         if (lane == 0) mbar_arrive(&eD[b]);
+                     });
+        }
+        if (!ok && lane == 0) {
+            s_abort = 1;
+            atomicOr(a.status, KIVI_FLAG_WAIT);
+        }
+        __syncwarp();
+    } else if (warp == 4) {
+        if (lane == 0) {
+            int it = 0;
+            const int end = (j1 - j0) * nk;
+            for (; it < end; ++it) {
+                const int s = it % S, j = j0 + it / nk, e = j / nc;
+                ok = it < S || mbar_wait_ab(&eS[s], (unsigned)(it / S + 1) & 1u, abort);
+                if (!ok) break;
+                mbar_expect_tx(&bB[s], kHpB);
+                tma_sw(sB + s * kHpB, &tm, it % nk * kHpK, e * a.N + (j - e * nc) * kHpCols, &bB[s]);
+            }
+            if (!ok) {
+                s_abort = 1;
+                atomicOr(a.status, KIVI_FLAG_WAIT);
+            }
+            // every copy has landed before shared memory is given up (bounded)
+            for (int y = max(0, it - S); y < it; ++y) mbar_wait(&bB[y % S], (unsigned)(y / S) & 1u);
+        }
+        __syncwarp();
+    } else {
+        constexpr uint32_t ID = tc_idesc_f16(kHpRows, kHpCols, 0);
+        const uint64_t da = tc_desc_sw(sA, 16, 1024), db = tc_desc_sw(sB, 16, 1024);
+        ok = __all_sync(kHpFull, mbar_wait_ab(bA, 0u, abort));
+        int s = 0, it = 0;
+        unsigned ph = 0;
+        for (int j = j0; j < j1 && ok; ++j) {
+            const int y = j - j0, b = y & 1;
+            // the buffer's last output is read
+            ok = __all_sync(kHpFull, y < 2 || mbar_wait_ab(&eD[b], (unsigned)((y >> 1) + 1) & 1u, abort));
+            for (int k = 0; k < nk && ok; ++k, ++it) {
+                ok = __all_sync(kHpFull, mbar_wait_ab(&bB[s], ph, abort));
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int c = 0; c < kHpK / 16; ++c)
+                    tc_mma_f16_w(taddr + kHpCols * b, da + (uint32_t)((k * kHpA + 32 * c) >> 4),
+                                 db + (uint32_t)((s * kHpB + 32 * c) >> 4), ID, k > 0 || c > 0);
+                tc_commit_w(&eS[s]);
+                if (++s == S) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+            }
+            if (ok) tc_commit_w(&bD[b]);
+        }
+        if (!ok && lane == 0) {
+            s_abort = 1;
+            atomicOr(a.status, KIVI_FLAG_WAIT);
+        }
+        // every product and commit is done before memory is given up (bounded)
+        tc_commit_w(bE);
+        mbar_wait(bE, 0u);
+        __syncwarp();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) tc_dealloc(taddr, 2 * kHpCols);
+}
+
 kivi_status fail(kivi_status s, const char *msg) {
     kivi_set_last_error(msg);
     return s;
@@ -245,6 +383,22 @@ extern "C" kivi_status kivi_head_product(const void *x, const void *w, int b, in
     cudaError_t e = mn ? make_sw_map(&tm, (const __half *)w, (long long)h * K, N, kHpK)
                        : make_sw_map(&tm, (const __half *)w, (long long)h * N, K, kHpCols);
     const dim3 grid((unsigned)((rows + kHpRows - 1) / kHpRows), (unsigned)(N / kHpCols), (unsigned)h);
+    const int cols = h * (N / kHpCols);   // column tiles of all heads
+    if (e == cudaSuccess && h_x == 1 && h > 1 && !mn && K <= kHsMaxK && (long long)grid.x * cols > info.sms) {
+        // a CTA an SM: as many groups of heads as leave every row tile one
+        long long groups = info.sms / (long long)grid.x;
+        if (groups < 1) groups = 1;
+        if (groups > cols) groups = cols;
+        const int per = (int)((cols + groups - 1) / groups);
+        static std::atomic<uint64_t> done;
+        e = kivi_allow_smem(head_product_shared_kernel, hs_smem(kHsMaxK), info.device, done);
+        if (e == cudaSuccess) {
+            head_product_shared_kernel<<<dim3(grid.x, (unsigned)((cols + per - 1) / per)), kHpThreads, hs_smem(K),
+                                         (cudaStream_t)stream>>>(a, tm, per);
+            e = cudaGetLastError();
+        }
+        return e == cudaSuccess ? KIVI_OK : fail(KIVI_ERR_CUDA, cudaGetErrorString(e));
+    }
     const bool deep = K > 2 * kHpK && (long long)grid.x * grid.y * grid.z <= info.sms;
     const auto kernel = deep ? (mn ? head_product_kernel<true, 6> : head_product_kernel<false, 6>)
                              : (mn ? head_product_kernel<true, 3> : head_product_kernel<false, 3>);

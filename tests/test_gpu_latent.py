@@ -140,6 +140,8 @@ def test_cache_holds_its_tokens(r, bits, G, R):
     (1, 1, 1, 128, 512, True, False), (64, 3, 1, 128, 256, True, False), (3, 2, 130, 512, 128, False, False),
     (2, 5, 301, 512, 128, False, True), (1, 2, 128, 64, 128, False, False), (2, 1, 77, 192, 384, True, True),
     (5, 128, 2, 256, 128, False, False),
+    # rows of all heads alike over several heads a CTA: an odd number of heads, two column tiles, ragged ends
+    (3, 61, 260, 512, 128, False, True), (1, 7, 5000, 192, 256, False, True), (1, 200, 127, 64, 128, False, True),
 ])
 def test_head_product(b, h, n, K_, N, transposed, shared):
     torch = pytest.importorskip("torch")
