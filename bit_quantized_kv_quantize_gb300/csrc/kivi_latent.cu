@@ -131,15 +131,27 @@ __global__ void __launch_bounds__(32 * kApWarps)
                                   (lane & 3) * 4) = key;
 }
 
-// The cache as attention sees it: 8 channels a thread.
-__global__ void latent_restore_kernel(LatentGeom g, LatentDev dv, __half *__restrict__ C, __half *__restrict__ Kr,
-                                      const __grid_constant__ LatentTokens a) {
+// The cache as attention sees it, and new tokens behind it: 8 channels a thread.
+__global__ void latent_rows_kernel(LatentGeom g, LatentDev dv, const __half *__restrict__ Cn, const __half *__restrict__ Krn,
+                                   __half *__restrict__ C, __half *__restrict__ Kr, int stride,
+                                   const __grid_constant__ LatentTokens a) {
     const int i = blockIdx.y, per = (g.r + kLatRope) / 8;
     const long long e = (long long)blockIdx.x * blockDim.x + threadIdx.x;
     const int tau = (int)(e / per), c = (int)(e % per);
-    if (tau >= a.T[i]) return;
+    const int T = a.T[i];
+    if (tau >= T + a.n[i]) return;
     const int kb = tau / kLatTok, t = tau % kLatTok;
-    const size_t row = (size_t)i * a.n_stride + tau;
+    const size_t row = (size_t)i * stride + tau;
+    if (tau >= T) {
+        const size_t src = (size_t)i * a.n_stride + (tau - T);
+        if (c >= g.r / 8) {
+            const int k = c - g.r / 8;
+            if (Kr) *reinterpret_cast<uint4 *>(Kr + row * kLatRope + 8 * k) = *reinterpret_cast<const uint4 *>(Krn + src * kLatRope + 8 * k);
+        } else if (C) {
+            *reinterpret_cast<uint4 *>(C + row * g.r + 8 * c) = *reinterpret_cast<const uint4 *>(Cn + src * g.r + 8 * c);
+        }
+        return;
+    }
     if (c >= g.r / 8) {
         const int k = c - g.r / 8;
         if (Kr)
@@ -149,7 +161,7 @@ __global__ void latent_restore_kernel(LatentGeom g, LatentDev dv, __half *__rest
     }
     if (!C) return;
     uint4 v;
-    if (tau >= lat_tq(a.T[i], g.R)) {
+    if (tau >= lat_tq(T, g.R)) {
         v = *reinterpret_cast<const uint4 *>((const char *)(dv.ring + lat_ring(g, i, kb)) + lat_at(c, t, kLatTok));
     } else {
         const unsigned char *rec = dv.rec + lat_rec(g, i, kb);
@@ -178,10 +190,10 @@ cudaError_t kivi_launch_latent_append(const LatentGeom &g, const LatentDev &dv, 
     return cudaGetLastError();
 }
 
-cudaError_t kivi_launch_latent_restore(const LatentGeom &g, const LatentDev &dv, __half *C, __half *Kr,
-                                       const LatentTokens &a, int maxT, cudaStream_t st) {
-    const long long items = (long long)maxT * ((g.r + kLatRope) / 8);
-    latent_restore_kernel<<<dim3((unsigned)((items + 255) / 256), (unsigned)g.b), 256, 0, st>>>(g, dv, C, Kr, a);
+cudaError_t kivi_launch_latent_rows(const LatentGeom &g, const LatentDev &dv, const __half *Cn, const __half *Krn,
+                                    __half *C, __half *Kr, const LatentTokens &a, int stride, int maxS, cudaStream_t st) {
+    const long long items = (long long)maxS * ((g.r + kLatRope) / 8);
+    latent_rows_kernel<<<dim3((unsigned)((items + 255) / 256), (unsigned)g.b), 256, 0, st>>>(g, dv, Cn, Krn, C, Kr, stride, a);
     return cudaGetLastError();
 }
 
@@ -293,6 +305,29 @@ kivi_status put(kivi_latent *c, const void *C, const void *Kr, const int32_t *n,
     }
     for (int i = 0; i < c->g.b; ++i) c->T[i] = T[i] + n[i];
     return KIVI_OK;
+}
+
+// kivi_latent_restore (n null: every sequence, no new tokens) and kivi_latent_rows
+// (sequences with new tokens)
+kivi_status rows(kivi_latent *c, const void *Cn, const void *Krn, const int32_t *n, int n_stride, void *C, void *Kr,
+                 int stride, const char *what, cudaStream_t st) {
+    if (stride < 0) return fail(KIVI_ERR_INVALID_ARG, "the output's stride is negative");
+    if ((C && !aligned16(C)) || (Kr && !aligned16(Kr)))
+        return fail(KIVI_ERR_INVALID_ARG, "tensors must be 16-byte aligned");
+    LatentTokens a;
+    a.n_stride = n_stride;
+    int maxS = 0;
+    for (int i = 0; i < c->g.b; ++i) {
+        a.n[i] = n ? n[i] : 0;
+        a.T[i] = !n || n[i] > 0 ? c->T[i] : 0;
+        if (a.n[i] > stride - a.T[i])
+            return fail(KIVI_ERR_INVALID_ARG, "sequence %ld has more tokens than the output's stride", i);
+        maxS = a.T[i] + a.n[i] > maxS ? a.T[i] + a.n[i] : maxS;
+    }
+    if (maxS == 0 || (!C && !Kr)) return KIVI_OK;
+    const cudaError_t e = kivi_launch_latent_rows(c->g, c->dv, (const __half *)Cn, (const __half *)Krn, (__half *)C,
+                                                  (__half *)Kr, a, stride, maxS, st);
+    return e == cudaSuccess ? KIVI_OK : fail_cuda(c, e, what);
 }
 
 }  // namespace
@@ -454,22 +489,18 @@ kivi_status kivi_latent_restore(kivi_latent_t c, void *C, void *Kr, int t_stride
     kivi_set_last_error("");
     kivi_status s = check(c, true);
     if (s != KIVI_OK) return s;
-    if (t_stride < 0) return fail(KIVI_ERR_INVALID_ARG, "t_stride negative");
-    if ((C && !aligned16(C)) || (Kr && !aligned16(Kr)))
-        return fail(KIVI_ERR_INVALID_ARG, "tensors must be 16-byte aligned");
-    LatentTokens a;
-    a.n_stride = t_stride;
-    int maxT = 0;
-    for (int i = 0; i < c->g.b; ++i) {
-        a.T[i] = c->T[i];
-        a.n[i] = 0;
-        if (c->T[i] > t_stride) return fail(KIVI_ERR_INVALID_ARG, "sequence %ld has more than t_stride tokens", i);
-        maxT = c->T[i] > maxT ? c->T[i] : maxT;
-    }
-    if (maxT == 0 || (!C && !Kr)) return KIVI_OK;
-    const cudaError_t e = kivi_launch_latent_restore(c->g, c->dv, (__half *)C, (__half *)Kr, a, maxT, (cudaStream_t)stream);
-    if (e != cudaSuccess) return fail_cuda(c, e, "latent_restore");
-    return KIVI_OK;
+    return rows(c, nullptr, nullptr, nullptr, 0, C, Kr, t_stride, "latent_restore", (cudaStream_t)stream);
+}
+
+kivi_status kivi_latent_rows(kivi_latent_t c, const void *C, const void *Kr, const int32_t *n, int n_stride, void *C_out,
+                             void *Kr_out, int s_stride, kivi_stream_t stream) {
+    kivi_set_last_error("");
+    kivi_status s = check(c, true);
+    if (s != KIVI_OK) return s;
+    int maxn = 0;
+    s = check_tokens(c->g.b, C, Kr, n, n_stride, &maxn);
+    if (s != KIVI_OK) return s;
+    return maxn == 0 ? KIVI_OK : rows(c, C, Kr, n, n_stride, C_out, Kr_out, s_stride, "latent_rows", (cudaStream_t)stream);
 }
 
 kivi_status kivi_latent_check(kivi_latent_t c, uint32_t *flags, kivi_stream_t stream) {

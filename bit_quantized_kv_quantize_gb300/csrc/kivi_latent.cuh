@@ -67,8 +67,9 @@ struct LatentTokens {
 
 cudaError_t kivi_launch_latent_append(const LatentGeom &g, const LatentDev &dv, const __half *C, const __half *Kr,
                                       const LatentTokens &a, int maxn, cudaStream_t st);
-cudaError_t kivi_launch_latent_restore(const LatentGeom &g, const LatentDev &dv, __half *C, __half *Kr,
-                                       const LatentTokens &a, int maxT, cudaStream_t st);
+// a: T and n[i] new tokens behind them (of Cn, Krn, [b][a.n_stride]); into [b][stride]
+cudaError_t kivi_launch_latent_rows(const LatentGeom &g, const LatentDev &dv, const __half *Cn, const __half *Krn,
+                                    __half *C, __half *Kr, const LatentTokens &a, int stride, int maxS, cudaStream_t st);
 // The absorbed attention (kivi_latent_attn.cu); a: hq = hg = h, T, Tqk = Tqv =
 // the quantized tokens, n, n_stride, and the work list of kivi_plan_latent.
 constexpr int kLatRows = 64;   // rows of a row tile

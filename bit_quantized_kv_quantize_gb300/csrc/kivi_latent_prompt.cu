@@ -1,6 +1,7 @@
 // kivi_latent_prompt.cu -- latent attention in its expanded form: the causal
-// attention of a prompt whose heads' keys and values have been formed, on the
-// 5th-generation tensor cores, and the entry point kivi_latent_prompt_attn.
+// attention of a prompt, or of a long chunk behind cached tokens, whose heads' keys
+// and values have been formed, on the 5th-generation tensor cores, and the entry
+// points kivi_latent_prompt_attn and kivi_latent_expanded_attn.
 //
 // Mathematics.  Token s of head e has the key [k_s ; kr_s] (128 channels of its
 // own, 64 rotary ones that all heads share) and the value v_s [128]:
@@ -34,10 +35,10 @@ constexpr int kLpQs = kLpRows * 128, kLpKs = kLpKeys * 128;   // a tile of 64 ch
 
 struct PromptArgs {
     __half *out;
-    int b, h, t_stride, mt;   // mt: row tiles of the longest sequence
-    float sl2;                // scale log2(e)
+    int b, h, n_stride, s_stride, mt;   // strides of queries and of keys; row tiles of the longest sequence
+    float sl2;                          // scale log2(e)
     unsigned *status;
-    int t[KIVI_MAX_BATCH];
+    int n[KIVI_MAX_BATCH], T[KIVI_MAX_BATCH];   // queries of a sequence; tokens before them
 };
 
 __device__ __forceinline__ unsigned long long lp_f2(float a, float b) {
@@ -70,7 +71,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
     unsigned char *const smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
     constexpr int KS = kLpStages;
     const int bh = a.b * a.h, pair = blockIdx.x % bh, m = a.mt - 1 - blockIdx.x / bh, i = pair / a.h;
-    const int n = a.t[i], row0 = m * 2 * kLpRows;
+    const int n = a.n[i], T = a.T[i], row0 = m * 2 * kLpRows;
     if (row0 >= n) return;
     unsigned char *sQ = smem, *sK = sQ + 2 * kLpQ, *sV = sK + KS * kLpK;
     // counts 4 (a slot's softmax warps): P [slot][buffer], scores read [slot]; 2
@@ -97,7 +98,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
     bool ok = true;
     // tiles that each slot sees (none: a slot without rows)
     const int last1 = min(row0 + 2 * kLpRows, n) - 1, last0 = min(row0 + kLpRows, n) - 1;
-    const int nx0 = last0 / kLpKeys + 1, nx1 = n > row0 + kLpRows ? last1 / kLpKeys + 1 : 0;
+    const int nx0 = (T + last0) / kLpKeys + 1, nx1 = n > row0 + kLpRows ? (T + last1) / kLpKeys + 1 : 0;
     const int nx = max(nx0, nx1);
 
     if (warp == 8 || warp == 9) {
@@ -165,7 +166,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
         __syncwarp();
     } else if (warp == 11) {
         // ---- copies ----
-        const int q0 = pair * a.t_stride;   // the head's first row
+        const int q0 = pair * a.n_stride, k0 = pair * a.s_stride, S = T + n;   // the head's first rows; tokens
         if (lane == 0)
             for (int e = 0; e < 2; ++e) {
                 if (e && nx1 == 0) break;
@@ -182,26 +183,26 @@ __global__ void __launch_bounds__(kLpThreads, 1)
                 ok = x < KS || mbar_wait_ab(&eK[t.s], t.p ^ 1u, abort);
                 if (ok) {
                     mbar_expect_tx(&bK[t.s], kLpK);
-                    for (int c = 0; c < 2; ++c) tma_sw(sK + t.s * kLpK + c * kLpKs, &tmK, 64 * c, q0 + tb, &bK[t.s]);
-                    tma_sw(sK + t.s * kLpK + 2 * kLpKs, &tmKr, 0, i * a.t_stride + tb, &bK[t.s]);
+                    for (int c = 0; c < 2; ++c) tma_sw(sK + t.s * kLpK + c * kLpKs, &tmK, 64 * c, k0 + tb, &bK[t.s]);
+                    tma_sw(sK + t.s * kLpK + 2 * kLpKs, &tmKr, 0, i * a.s_stride + tb, &bK[t.s]);
                     ++ck;
                     ok = x < KS || mbar_wait_ab(&eV[t.s], t.p ^ 1u, abort);
                 }
                 if (ok) {
                     // (the last tile's rows behind the sequence are zeroed first)
-                    uint64_t *const bar = tb + kLpKeys > n ? bT : &bV[t.s];
+                    uint64_t *const bar = tb + kLpKeys > S ? bT : &bV[t.s];
                     mbar_expect_tx(bar, kLpV);
-                    for (int c = 0; c < 2; ++c) tma_sw(sV + t.s * kLpV + c * kLpKs, &tmV, 64 * c, q0 + tb, bar);
+                    for (int c = 0; c < 2; ++c) tma_sw(sV + t.s * kLpV + c * kLpKs, &tmV, 64 * c, k0 + tb, bar);
                     ++cv;
                 }
             }
             ok = __all_sync(kFull, ok);
-            if (ok && tb + kLpKeys > n) {
+            if (ok && tb + kLpKeys > S) {
                 ok = __all_sync(kFull, mbar_wait_ab(bT, 0u, abort));
                 if (ok) {
-                    const int c16 = (tb + kLpKeys - n) * 8;   // 16-byte chunks of 64 channels
+                    const int c16 = (tb + kLpKeys - S) * 8;   // 16-byte chunks of 64 channels
                     for (int y = lane; y < 2 * c16; y += 32)
-                        *reinterpret_cast<uint4 *>(sV + t.s * kLpV + (y / c16) * kLpKs + (n - tb) * 128 + y % c16 * 16) =
+                        *reinterpret_cast<uint4 *>(sV + t.s * kLpV + (y / c16) * kLpKs + (S - tb) * 128 + y % c16 * 16) =
                             make_uint4(0u, 0u, 0u, 0u);
                     fence_proxy_async();
                     __syncwarp();
@@ -219,12 +220,12 @@ __global__ void __launch_bounds__(kLpThreads, 1)
             if (nx1) mbar_wait(&bQ[1], 0u);
             for (int y = max(0, ck - KS); y < ck; ++y) mbar_wait(&bK[y % KS], (unsigned)(y / KS) & 1u);
             for (int y = max(0, cv - KS); y < cv; ++y)
-                mbar_wait(y * kLpKeys + kLpKeys > n ? bT : &bV[y % KS], y * kLpKeys + kLpKeys > n ? 0u : (unsigned)(y / KS) & 1u);
+                mbar_wait(y * kLpKeys + kLpKeys > S ? bT : &bV[y % KS], y * kLpKeys + kLpKeys > S ? 0u : (unsigned)(y / KS) & 1u);
         }
         __syncwarp();
     } else {
         // ---- softmax ----
-        const int slot = tid / kLpRows, srow = row0 + slot * kLpRows, pos = srow + tid % kLpRows;
+        const int slot = tid / kLpRows, srow = row0 + slot * kLpRows, pos = T + srow + tid % kLpRows;
         const int mine = slot ? nx1 : nx0;
         const uint32_t tS = taddr + 256 * slot + ((uint32_t)(32 * (warp & 3)) << 16), tO = tS + 128;
         float ref = -INFINITY, lsum = 0.f;   // the row's reference less the lift (log2; -inf: nothing yet), the weights' sum
@@ -241,7 +242,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&bL[slot]);
             const bool pf = x < 2 || mbar_test(&bF[2 * slot + b], (unsigned)((x >> 1) + 1) & 1u);
-            if (key0 + kLpKeys - 1 > srow) {   // some row of the slot does not see the whole tile
+            if (key0 + kLpKeys - 1 > T + srow) {   // some row of the slot does not see the whole tile
                 const uint32_t h0 = ck_above(pos - key0), h1 = ck_above(pos - key0 - 32);
 #pragma unroll
                 for (int c = 0; c < 32; ++c) {
@@ -312,7 +313,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
             const float inv = 1.f / lsum;
             unsigned char *st = sQ + slot * kLpQ + (warp & 3) * (32 * 64);
             const int q8 = lane >> 2, c4 = lane & 3, row32 = srow + 32 * (warp & 3);
-            __half *dst = a.out + ((size_t)pair * a.t_stride + row32) * kLatHead + 8 * c4;
+            __half *dst = a.out + ((size_t)pair * a.n_stride + row32) * kLatHead + 8 * c4;
 #pragma unroll 1
             for (int c0 = 0; c0 < kLatHead; c0 += 32) {
                 uint32_t o[32];
@@ -352,51 +353,72 @@ kivi_status fail(kivi_status s, const char *msg) {
     return s;
 }
 
-}  // namespace
-
-extern "C" kivi_status kivi_latent_prompt_attn(const void *q, const void *q_rope, const void *K, const void *Kr,
-                                               const void *V, int b, int h, const int32_t *t, int t_stride, float scale,
-                                               void *out, kivi_stream_t stream) {
-    kivi_set_last_error("");
-    if (b < 1 || h < 1 || t_stride < 0) return fail(KIVI_ERR_INVALID_ARG, "sizes must be positive");
+// Both entry points: n[i] queries behind T[i] tokens (T null: none).
+kivi_status expanded(const void *q, const void *q_rope, const void *K, const void *Kr, const void *V, int b, int h,
+                     const int32_t *T, const int32_t *n, int n_stride, int s_stride, float scale, void *out,
+                     kivi_stream_t stream) {
+    if (b < 1 || h < 1 || n_stride < 0 || s_stride < 0) return fail(KIVI_ERR_INVALID_ARG, "sizes must be positive");
     if (b > KIVI_MAX_BATCH) return fail(KIVI_ERR_UNSUPPORTED, "b above 1024");
     if (h > 1024) return fail(KIVI_ERR_UNSUPPORTED, "more than 1024 heads");
-    if (t_stride > (1 << 26) || (long long)b * h * t_stride >= (1LL << 31))
-        return fail(KIVI_ERR_UNSUPPORTED, "t_stride above 2^26, or b h t_stride not below 2^31");
+    if (n_stride > (1 << 26) || s_stride > (1 << 26) || (long long)b * h * n_stride >= (1LL << 31) ||
+        (long long)b * h * s_stride >= (1LL << 31))
+        return fail(KIVI_ERR_UNSUPPORTED, "a stride above 2^26, or b h times it not below 2^31");
     if (!(scale > 0.f && scale - scale == 0.f)) return fail(KIVI_ERR_INVALID_ARG, "scale must be positive and finite");
-    if (!t) return fail(KIVI_ERR_INVALID_ARG, "t is null");
+    if (!n) return fail(KIVI_ERR_INVALID_ARG, "the counts are null");
     PromptArgs a;
-    int maxt = 0;
+    int maxn = 0;
     for (int i = 0; i < b; ++i) {
-        if (t[i] < 0 || t[i] > t_stride) return fail(KIVI_ERR_INVALID_ARG, "t[i] outside [0, t_stride]");
-        a.t[i] = t[i];
-        maxt = t[i] > maxt ? t[i] : maxt;
+        a.n[i] = n[i];
+        a.T[i] = T ? T[i] : 0;
+        if (n[i] < 0 || n[i] > n_stride) return fail(KIVI_ERR_INVALID_ARG, "a count outside its stride");
+        if (n[i] > 0 && (a.T[i] < 0 || a.T[i] > s_stride - n[i]))
+            return fail(KIVI_ERR_INVALID_ARG, "tokens before the queries negative, or past the keys' stride");
+        maxn = n[i] > maxn ? n[i] : maxn;
     }
-    if (maxt == 0) return KIVI_OK;
+    if (maxn == 0) return KIVI_OK;
     if (!q || !q_rope || !K || !Kr || !V || !out) return fail(KIVI_ERR_INVALID_ARG, "a tensor pointer is null");
     if (((uintptr_t)q | (uintptr_t)q_rope | (uintptr_t)K | (uintptr_t)Kr | (uintptr_t)V | (uintptr_t)out) & 15u)
         return fail(KIVI_ERR_INVALID_ARG, "tensors must be 16-byte aligned");
     a.out = (__half *)out;
     a.b = b;
     a.h = h;
-    a.t_stride = t_stride;
-    a.mt = (maxt + 2 * kLpRows - 1) / (2 * kLpRows);
+    a.n_stride = n_stride;
+    a.s_stride = s_stride;
+    a.mt = (maxn + 2 * kLpRows - 1) / (2 * kLpRows);
     a.sl2 = scale * 1.4426950408889634f;
     if ((long long)a.mt * b * h > INT_MAX) return fail(KIVI_ERR_UNSUPPORTED, "more than 2^31 row tiles");
     KiviDeviceInfo info;
     if (!kivi_device_info(&info)) return fail(KIVI_ERR_CUDA, "no status word on the current device");
     a.status = info.status;
-    const long long rows = (long long)b * h * t_stride;
+    const long long rows = (long long)b * h * n_stride, keys = (long long)b * h * s_stride;
     CUtensorMap tq, tqr, tk, tkr, tv;
     cudaError_t e = make_sw_map(&tq, (const __half *)q, rows, kLatHead, kLpRows);
     if (e == cudaSuccess) e = make_sw_map(&tqr, (const __half *)q_rope, rows, kLatRope, kLpRows);
-    if (e == cudaSuccess) e = make_sw_map(&tk, (const __half *)K, rows, kLatHead, kLpKeys);
-    if (e == cudaSuccess) e = make_sw_map(&tkr, (const __half *)Kr, (long long)b * t_stride, kLatRope, kLpKeys);
-    if (e == cudaSuccess) e = make_sw_map(&tv, (const __half *)V, rows, kLatHead, kLpKeys);
+    if (e == cudaSuccess) e = make_sw_map(&tk, (const __half *)K, keys, kLatHead, kLpKeys);
+    if (e == cudaSuccess) e = make_sw_map(&tkr, (const __half *)Kr, (long long)b * s_stride, kLatRope, kLpKeys);
+    if (e == cudaSuccess) e = make_sw_map(&tv, (const __half *)V, keys, kLatHead, kLpKeys);
     static std::atomic<uint64_t> done;
     if (e == cudaSuccess) e = kivi_allow_smem(latent_prompt_kernel, kLpSmem, info.device, done);
     if (e != cudaSuccess) return fail(KIVI_ERR_CUDA, cudaGetErrorString(e));
     latent_prompt_kernel<<<(unsigned)(a.mt * b * h), kLpThreads, kLpSmem, (cudaStream_t)stream>>>(tq, tqr, tk, tkr, tv, a);
     e = cudaGetLastError();
     return e == cudaSuccess ? KIVI_OK : fail(KIVI_ERR_CUDA, cudaGetErrorString(e));
+}
+
+}  // namespace
+
+extern "C" kivi_status kivi_latent_prompt_attn(const void *q, const void *q_rope, const void *K, const void *Kr,
+                                               const void *V, int b, int h, const int32_t *t, int t_stride, float scale,
+                                               void *out, kivi_stream_t stream) {
+    kivi_set_last_error("");
+    return expanded(q, q_rope, K, Kr, V, b, h, nullptr, t, t_stride, t_stride, scale, out, stream);
+}
+
+extern "C" kivi_status kivi_latent_expanded_attn(const void *q, const void *q_rope, const void *K, const void *Kr,
+                                                 const void *V, int b, int h, const int32_t *T, const int32_t *n,
+                                                 int n_stride, int s_stride, float scale, void *out,
+                                                 kivi_stream_t stream) {
+    kivi_set_last_error("");
+    if (!T) return fail(KIVI_ERR_INVALID_ARG, "T is null");
+    return expanded(q, q_rope, K, Kr, V, b, h, T, n, n_stride, s_stride, scale, out, stream);
 }

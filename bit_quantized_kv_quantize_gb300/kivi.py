@@ -31,7 +31,7 @@ EXPORTS = ["kivi_cache_create", "kivi_cache_destroy", "kivi_prefill", "kivi_appe
            "kivi_decode_attn_window", "kivi_chunk_attn", "kivi_append_chunk", "kivi_rope",
            "kivi_rope_axes", "kivi_verify", "kivi_latent_create", "kivi_latent_destroy", "kivi_latent_prefill",
            "kivi_latent_append", "kivi_latent_attn", "kivi_latent_lengths", "kivi_latent_restore",
-           "kivi_latent_check", "kivi_head_product", "kivi_latent_prompt_attn", "kivi_device_check"]
+           "kivi_latent_check", "kivi_latent_rows", "kivi_latent_expanded_attn", "kivi_head_product", "kivi_latent_prompt_attn", "kivi_device_check"]
 
 
 class KiviError(RuntimeError):
@@ -73,6 +73,8 @@ def _load():
     L.kivi_latent_check.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32), vp]
     L.kivi_head_product.argtypes = [vp, vp, i32, i32, i32, i32, vp, i32, i32, i32, vp, vp]
     L.kivi_latent_prompt_attn.argtypes = [vp] * 5 + [i32, i32, vp, i32, ctypes.c_float, vp, vp]
+    L.kivi_latent_rows.argtypes = [vp, vp, vp, vp, i32, vp, vp, i32, vp]
+    L.kivi_latent_expanded_attn.argtypes = [vp] * 5 + [i32, i32, vp, vp, i32, i32, ctypes.c_float, vp, vp]
     L.kivi_device_check.argtypes = [ctypes.POINTER(ctypes.c_uint32), vp]
     L.kivi_plan_preview.argtypes = [i32] * 9 + [vp, vp, vp, i32, vp]
     L.kivi_cache_lengths.argtypes = [vp, vp, vp, vp]
@@ -695,6 +697,7 @@ class LatentCache:
         _check(lib.kivi_latent_create(b, r, bits, G, R, max_tokens, ctypes.byref(self._h)))
         import torch
         self._dev = torch.cuda.current_device()   # the handle's memory is there
+        self._sms = torch.cuda.get_device_properties(self._dev).multi_processor_count
 
     def close(self):
         if self._h:
@@ -754,9 +757,56 @@ class LatentCache:
                                     _rows16(out, shape, self._dev, "out"), _stream(stream)))
         return out
 
-    def _attn(self, dims, ptrs, qrp, krp, cnt, scale, stream, st):
+    def _form(self, form, cnt, T, h):
+        """Whether attn forms every head's keys and values (expanded) rather than
+        absorbing them, and the longest sequence with its new tokens.
+
+        None, the faster by these times on a GB300 (r = 512): absorbed 30 us and one
+        for 205,000 (query, head, token); expanded 10 us, one for 3,000 (token, head),
+        and 0.8 us for 64 tokens while every SM has a row tile of 256 queries of a
+        head.  16 heads over 8000 tokens: 128 queries 114 and 134 us, 256 180 and 168,
+        512 326 and 173; 128 heads over 4000: 64 queries 196 and 226, 256 675 and 243.
+        Expanded from 16 queries on, where keys and values take up to 4 GB."""
+        S = [t + n if n > 0 else 0 for t, n in zip(T, cnt)]
+        if form not in (None, "absorbed", "expanded"):
+            raise ValueError('form must be None, "absorbed" or "expanded"')
+        if form is not None:
+            return form == "expanded", max(S)
+        if max(cnt) < 16 or 4 * self.b * max(S) * h * LATENT_HEAD > 1 << 32:
+            return False, max(S)
+        absorbed = 30 + h * sum(n * s for n, s in zip(cnt, S)) / 205e3
+        turns = -(-h * sum((n + 255) // 256 for n in cnt) // self._sms)
+        return 10 + h * sum(S) / 3e3 + turns * max(S) / 80 < absorbed, max(S)
+
+    def _expanded(self, dims, ptrs, qrp, krp, cnt, T, S, scale, stream, st):
         import torch
         (b, h, ns, r), (qnp, _, cp, _, wkp, wvp, op) = dims, ptrs
+        dev = f"cuda:{self._dev}"
+        with _on(stream):   # (rows past a sequence's tokens are not read)
+            c_all = torch.empty((b, S, r), dtype=torch.float16, device=dev)
+            kr_all = torch.empty((b, S, LATENT_ROPE), dtype=torch.float16, device=dev)
+            K = torch.empty((b, h, S, LATENT_HEAD), dtype=torch.float16, device=dev)
+            V = torch.empty_like(K)
+        _check(lib.kivi_latent_rows(self._h, cp, krp, _addr(cnt), ns, c_all.data_ptr(), kr_all.data_ptr(), S, st))
+        tok = array.array("i", [t + n if n else 0 for t, n in zip(T, cnt)])
+        for w, x in ((wkp, K), (wvp, V)):
+            _check(lib.kivi_head_product(c_all.data_ptr(), w, b, 1, h, S, _addr(tok), r, LATENT_HEAD, 0, x.data_ptr(), st))
+        _check(lib.kivi_latent_expanded_attn(qnp, qrp, K.data_ptr(), kr_all.data_ptr(), V.data_ptr(), b, h, _addr(T),
+                                             _addr(cnt), ns, S, scale, op, st))
+
+    def _lengths(self):
+        T = array.array("i", bytes(4 * self.b))
+        _check(lib.kivi_latent_lengths(self._h, _addr(T), None))
+        return T
+
+    def _attn(self, dims, ptrs, qrp, krp, cnt, scale, form, stream, st):
+        import torch
+        (b, h, ns, r), (qnp, _, cp, _, wkp, wvp, op) = dims, ptrs
+        if form is not None or max(cnt) >= 16:
+            T = self._lengths()
+            expanded, S = self._form(form, cnt, T, h)
+            if expanded:
+                return self._expanded(dims, ptrs, qrp, krp, cnt, T, S, scale, stream, st)
         with _on(stream):   # (rows past n are not read)
             ql = torch.empty((b, h, ns, r), dtype=torch.float16, device=f"cuda:{self._dev}")
             ol = torch.empty_like(ql)
@@ -770,15 +820,16 @@ class LatentCache:
             raise ValueError(f"the latent cache holds {self.b} sequences of vectors of {self.r}")
         return dims, ptrs, out
 
-    def attn(self, qn, qr, c, kr, n, wk, wv, scale=None, out=None, stream=None):
+    def attn(self, qn, qr, c, kr, n, wk, wv, scale=None, out=None, stream=None, form=None):
         """Latent attention of n new tokens of each sequence (an integer or b of
-        them) over the cache and over themselves, absorbed: qn CUDA fp16 [b, h, ns,
+        them) over the cache and over themselves, absorbed or expanded (form;
+        default the faster, which for long chunks is the latter): qn CUDA fp16 [b, h, ns,
         128], qr [b, h, ns, 64], c [b, ns, r], kr [b, ns, 64], wk and wv [h, 128,
         r] -> out [b, h, ns, 128] (rows past n untouched, zero in a new tensor).
         Queries and keys rotated.  Does not append (append, extend)."""
         self._here()
         dims, ptrs, out = self._args(qn, qr, c, kr, wk, wv, out, stream)
-        self._attn(dims, ptrs, ptrs[1], ptrs[3], _counts(n, self.b), _latent_scale(scale), stream, _stream(stream))
+        self._attn(dims, ptrs, ptrs[1], ptrs[3], _counts(n, self.b), _latent_scale(scale), form, stream, _stream(stream))
         return out
 
     def prefill_attn(self, qn, qr, c, kr, t, wk, wv, scale=None, out=None, stream=None):
@@ -788,7 +839,7 @@ class LatentCache:
         self.prefill(c, kr, t, stream)
         return latent_prompt_attn(qn, qr, c, kr, t, wk, wv, scale, out, stream)
 
-    def extend(self, qn, qr, c, kr, n, wk, wv, rope=None, pos=None, scale=None, out=None, stream=None):
+    def extend(self, qn, qr, c, kr, n, wk, wv, rope=None, pos=None, scale=None, out=None, stream=None, form=None):
         """Take the next n tokens of every sequence (a chunk, or one): rotate qr
         and kr at the positions behind the cached tokens (rope: a Rope of 64
         channels, or None; or at pos, as Rope.apply takes every position), attend
@@ -798,8 +849,7 @@ class LatentCache:
         dims, ptrs, out = self._args(qn, qr, c, kr, wk, wv, out, stream)
         (b, h, ns, _), cnt, st = dims, _counts(n, self.b), _stream(stream)
         qrp, krp = ptrs[1], ptrs[3]
-        T = array.array("i", bytes(4 * b))
-        _check(lib.kivi_latent_lengths(self._h, _addr(T), None))
+        T = self._lengths()
         for i in range(b):
             if cnt[i] > self.max_tokens - T[i]:
                 raise CapacityError(3, f"sequence {i} would exceed max_tokens")
@@ -811,7 +861,7 @@ class LatentCache:
                 rq, rk = torch.empty_like(qr), torch.empty_like(kr)
             rope._call(qrp, krp, b, h, 1, ns, cnt, T if posp is None else None, posp, False, rq.data_ptr(), rk.data_ptr(), st)
             qrp, krp = rq.data_ptr(), rk.data_ptr()
-        self._attn(dims, ptrs, qrp, krp, cnt, _latent_scale(scale), stream, st)
+        self._attn(dims, ptrs, qrp, krp, cnt, _latent_scale(scale), form, stream, st)
         _check(lib.kivi_latent_append(self._h, ptrs[2], krp, _addr(cnt), ns, st))
         return out
 

@@ -279,6 +279,15 @@ kivi_status kivi_latent_append(kivi_latent_t c, const void *C, const void *Kr, c
 kivi_status kivi_latent_attn(kivi_latent_t c, const void *q, const void *q_rope, const void *C, const void *Kr,
                              const int32_t *n, int n_stride, int h, float scale, void *out, kivi_stream_t stream);
 
+/* The expanded form over a cache, for long chunks: kivi_latent_rows writes, of each
+ * sequence with new tokens (n[i] > 0), the cached rows as attention sees them and the
+ * new ones behind them, into C_out fp16 [b][s_stride][r] and Kr_out fp16
+ * [b][s_stride][64] (device; either may be NULL; T_i + n[i] <= s_stride; other rows
+ * not written); heads' keys and values are then formed of C_out, and
+ * kivi_latent_expanded_attn attends to them.  C, Kr, n as for kivi_latent_append. */
+kivi_status kivi_latent_rows(kivi_latent_t c, const void *C, const void *Kr, const int32_t *n, int n_stride, void *C_out,
+                             void *Kr_out, int s_stride, kivi_stream_t stream);
+
 /* Tokens of each sequence, and how many of them are quantized (HOST arrays of b
  * int32; either may be NULL); the cache's rows as attention sees them, into C fp16
  * [b][t_stride][r] and Kr fp16 [b][t_stride][64] (device; either may be NULL; rows
@@ -311,8 +320,16 @@ kivi_status kivi_latent_prompt_attn(const void *q, const void *q_rope, const voi
                                     int b, int h, const int32_t *t, int t_stride, float scale, void *out,
                                     kivi_stream_t stream);
 
+/* The same for n[i] queries of each sequence behind T[i] tokens (T, n: HOST arrays of
+ * b int32): q, q_rope and out [b][h][n_stride][..], K and V [b][h][s_stride][128], Kr
+ * [b][s_stride][64]; the query r < n[i] stands at position T[i] + r, T[i] + n[i] <=
+ * s_stride.  Limits as above, for both strides. */
+kivi_status kivi_latent_expanded_attn(const void *q, const void *q_rope, const void *K, const void *Kr, const void *V,
+                                      int b, int h, const int32_t *T, const int32_t *n, int n_stride, int s_stride,
+                                      float scale, void *out, kivi_stream_t stream);
+
 /* As kivi_cache_check, for the current device's calls that have no handle
- * (kivi_head_product, kivi_latent_prompt_attn). */
+ * (kivi_head_product, kivi_latent_prompt_attn, kivi_latent_expanded_attn). */
 kivi_status kivi_device_check(uint32_t *flags, kivi_stream_t stream);
 
 /* Append one token to every sequence: k and v fp16 [b][h_kv][d] (device).

@@ -74,12 +74,12 @@ def check(got, ref, bound, what=""):
         assert rel <= 1.5e-3, f"{what}: relative L2 error {rel:.3e}"
 
 
-def latent(qn, qr, c, kr, wk, wv, first, scale, absorbed):
+def latent(qn, qr, c, kr, wk, wv, first, scale, absorbed, restored=False):
     """One head's rows over tokens c (64 bits), kr: the output [n, 128] and what it
     may be off by before its last rounding.  Absorbed: q Wk, the restored c (as
     key and as value), the weights and the sums ol round to fp16; expanded: Wk c
     and Wv c (products of r terms in fp32: r 2^-23 of their size each), the
-    weights."""
+    weights, and with restored c too (H of every product's size)."""
     qn, qr, kr, wk, wv, c = (x.to(F64) for x in (qn, qr, kr, wk, wv, c))
     S, r = c.shape
     if absorbed:
@@ -95,8 +95,9 @@ def latent(qn, qr, c, kr, wk, wv, first, scale, absorbed):
     k, v = c @ wk.t(), c @ wv.t()
     ka, va = c.abs() @ wk.abs().t(), c.abs() @ wv.abs().t()
     o, wabs, mag = attend(torch.cat((qn, qr), 1), torch.cat((k, kr), 1), v, first, scale)
-    mag = mag + r * 2.0 ** -12 * scale * (qn.abs() @ ka.t()).amax(1)
-    return o, attn_bound(wabs + r * 2.0 ** -12 * va.amax(0), mag, S, 192)
+    own = r * 2.0 ** -12 + (1 if restored else 0)
+    mag = mag + own * scale * (qn.abs() @ ka.t()).amax(1)
+    return o, attn_bound(wabs + own * va.amax(0), mag, S, 192)
 
 
 def verify(p, q, draft, u, n):

@@ -48,6 +48,7 @@ def test_handles_and_calls_without_one_refuse():
         assert K.lib.kivi_latent_attn(h, p, p, p, p, n.ctypes.data, 1, 1, 1.0, p, None) == 1
         assert K.lib.kivi_latent_lengths(h, None, None) == 1
         assert K.lib.kivi_latent_restore(h, None, None, 0, None) == 1
+        assert K.lib.kivi_latent_rows(h, p, p, n.ctypes.data, 1, p, p, 1, None) == 1
 
     def product(x=p, w=p, b=1, hx=1, h=4, ns=1, n=n, k=128, nn=128, out=p):
         return K.lib.kivi_head_product(x, w, b, hx, h, ns, None if n is None else n.ctypes.data, k, nn, 0, out, None)
@@ -63,6 +64,14 @@ def test_handles_and_calls_without_one_refuse():
     assert prompt(b=0) == 1 and prompt(h=0) == 1 and prompt(t=None) == 1 and prompt(ts=-1) == 1 and prompt(q=None) == 1
     assert prompt(scale=0.0) == 1 and prompt(scale=float("nan")) == 1 and prompt(scale=float("inf")) == 1
     assert prompt(v=odd) == 1 and prompt(t=np.array([2], np.int32)) == 1
+    T = np.array([0], np.int32)
+
+    def expanded(T=T, n=n, ns=1, ss=1):
+        a = lambda x: None if x is None else x.ctypes.data   # noqa: E731
+        return K.lib.kivi_latent_expanded_attn(p, p, p, p, odd, 1, 1, a(T), a(n), ns, ss, 1.0, p, None)
+
+    assert expanded(T=None) == 1 and expanded(n=None) == 1 and expanded(ss=0) == 1 and expanded(T=np.array([-1], np.int32)) == 1
+    assert expanded(T=np.array([1], np.int32)) == 1 and expanded(ss=2 ** 26 + 1) == 2 and expanded() == 1
     assert prompt(b=1025) == 2 and prompt(ts=2 ** 26 + 1) == 2 and prompt(h=1025) == 2 and prompt(h=1024, ts=2 ** 21) == 2
 
 
@@ -176,6 +185,8 @@ def test_head_product(b, h, n, K_, N, transposed, shared):
     (2, 12, 256, 2, 64, 192, [700, 190], [40, 33]),
     (1, 3, 256, 4, 32, 1024, [900], [150]),           # fp16 tiles, whole tiles of new tokens
     (2, 8, 512, 4, 64, 64, [0, 100], [200, 3]),
+    (3, 2, 256, 4, 32, 128, [61, 700, 0], [300, 0, 129]),   # several row tiles behind cached tokens that end inside a tile
+    (1, 2, 512, 2, 64, 64, [127], [257]),
     (1, 64, 256, 2, 128, 64, [5000], [2]),            # cut into shares
     (4, 16, 512, 4, 32, 128, [4000, 3, 2500, 64], [1, 1, 1, 1]),
     (1, 1, 512, 2, 128, 64, [3000], [5]),
@@ -200,11 +211,13 @@ def test_attention_over_the_cache(b, h, r, bits, G, R, t, n):
     cache.attn_latent(ql, qr, c1, kr1, n, out=lat)
     again = cache.attn_latent(ql, qr, c1, kr1, n, out=torch.full_like(lat, 7.0))
     out = torch.full((b, h, ns, 128), 7.0, dtype=torch.float16, device="cuda")
-    cache.attn(qn, qr, c1, kr1, n, m.wk, m.wv, out=out)
+    cache.attn(qn, qr, c1, kr1, n, m.wk, m.wv, out=out, form="absorbed")
+    exp = cache.attn(qn, qr, c1, kr1, n, m.wk, m.wv, out=torch.full_like(out, 7.0), form="expanded")
+    pick = cache.attn(qn, qr, c1, kr1, n, m.wk, m.wv, out=torch.full_like(out, 7.0))
     assert cache.check() == 0 and K.device_check() == 0
-    assert torch.equal(lat, again)
+    assert torch.equal(lat, again) and (torch.equal(pick, out) or torch.equal(pick, exp))
     for i in range(b):
-        assert bool((lat[i, :, n[i]:] == 7.0).all()) and bool((out[i, :, n[i]:] == 7.0).all())
+        assert all(bool((x[i, :, n[i]:] == 7.0).all()) for x in (lat, out, exp))
         if n[i] == 0:
             continue
         cs = torch.cat((L.cached(c[i], t[i], R, bits, G), c1[i, :n[i]].double()))
@@ -218,6 +231,8 @@ def test_attention_over_the_cache(b, h, r, bits, G, R, t, n):
         L.check(torch.stack(got), torch.stack(ref), torch.stack(err), f"latent {i}")
         full = [L.latent(qn[i, e, :n[i]], qr[i, e, :n[i]], cs, ks, m.wk[e], m.wv[e], t[i], SCALE, True) for e in range(h)]
         L.check(out[i, :, :n[i]], torch.stack([x for x, _ in full]), torch.stack([x for _, x in full]), f"out {i}")
+        full = [L.latent(qn[i, e, :n[i]], qr[i, e, :n[i]], cs, ks, m.wk[e], m.wv[e], t[i], SCALE, False, True) for e in range(h)]
+        L.check(exp[i, :, :n[i]], torch.stack([x for x, _ in full]), torch.stack([x for _, x in full]), f"expanded {i}")
     cache.close()
 
 
@@ -357,7 +372,8 @@ def test_a_prompt_pieces_drafts_and_steps(r, bits, G, R, axes):
         for i in range(b):
             cs = torch.cat((L.cached(seen[i], T[i], R, bits, G), c[i, :n[i]].double()))
             ks = torch.cat((keys[i], krot[i, :n[i]]))
-            full = [L.latent(qn[i, e, :n[i]], qrot[i, e, :n[i]], cs, ks, m.wk[e], m.wv[e], T[i], SCALE, what != "prompt")
+            absorbed = what in ("draft", "step")          # (the piece expands: 16 queries and more over a short cache)
+            full = [L.latent(qn[i, e, :n[i]], qrot[i, e, :n[i]], cs, ks, m.wk[e], m.wv[e], T[i], SCALE, absorbed, what == "piece")
                     for e in range(h)]
             L.check(out[i, :, :n[i]], torch.stack([x for x, _ in full]), torch.stack([x for _, x in full]), f"{what} {i}")
             seen[i], keys[i] = torch.cat((seen[i], c[i, :keep[i]])), torch.cat((keys[i], krot[i, :keep[i]]))
@@ -417,6 +433,13 @@ def test_binding_refuses():
         cache.extend(qn, qr, c, kr, 3, m.wk, m.wv, rope=K.Rope(128))
     with pytest.raises(K.KiviError):
         cache.attn(qn, qr, c, kr, 4, m.wk, m.wv)
+    for form in ("absorbed", "expanded"):
+        with pytest.raises(K.KiviError):
+            cache.attn(qn, qr, c, kr, 4, m.wk, m.wv, form=form)
+        with pytest.raises(K.KiviError):
+            cache.attn(qn, qr, c, kr, -1, m.wk, m.wv, form=form)
+    with pytest.raises(ValueError):
+        cache.attn(qn, qr, c, kr, 3, m.wk, m.wv, form="other")
     with pytest.raises(K.KiviError):
         cache.attn(qn, qr, c, kr, 3, m.wk, m.wv, scale=-1.0)
     cache.prefill(c, kr, 3)
