@@ -653,6 +653,20 @@ def _latent_args(qn, qr, c, kr, wk, wv, out, stream, dev):
     return (b, h, t, r), (qnp, qrp, cp, krp, wkp, wvp, _rows16(out, (b, h, t, LATENT_HEAD), dev, "out")), out
 
 
+def _space(stream, dev, *halves):
+    """A workspace of several fp16 arrays: the tensor that holds it (kept until the
+    calls that use it are issued) and their addresses.  (One allocation: each takes
+    longer than a call's checks.)"""
+    import torch
+    at = [0]
+    for n in halves:
+        at.append(at[-1] + (n + 127) // 128 * 128)
+    with _on(stream):
+        t = torch.empty(at[-1], dtype=torch.float16, device=dev)
+    p = t.data_ptr()
+    return t, [p + 2 * a for a in at[:-1]]
+
+
 def _latent_scale(scale):
     return 1.0 / math.sqrt(LATENT_HEAD + LATENT_ROPE) if scale is None else float(scale)
 
@@ -673,12 +687,10 @@ def latent_prompt_attn(qn, qr, c, kr, t, wk, wv, scale=None, out=None, stream=No
             return latent_prompt_attn(qn, qr, c, kr, t, wk, wv, scale, out, stream)
     (b, h, ts, r), (qnp, qrp, cp, krp, wkp, wvp, op), out = _latent_args(qn, qr, c, kr, wk, wv, out, stream, dev)
     cnt, st = _counts(t, b, "t"), _stream(stream)
-    with _on(stream):   # (rows past t are not read)
-        K, V = torch.empty_like(qn), torch.empty_like(qn)
+    keep, (K, V) = _space(stream, qn.device, *[b * h * ts * LATENT_HEAD] * 2)   # (rows past t are not read)
     for w, x in ((wkp, K), (wvp, V)):
-        _check(lib.kivi_head_product(cp, w, b, 1, h, ts, _addr(cnt), r, LATENT_HEAD, 0, x.data_ptr(), st))
-    _check(lib.kivi_latent_prompt_attn(qnp, qrp, K.data_ptr(), krp, V.data_ptr(), b, h, _addr(cnt), ts,
-                                       _latent_scale(scale), op, st))
+        _check(lib.kivi_head_product(cp, w, b, 1, h, ts, _addr(cnt), r, LATENT_HEAD, 0, x, st))
+    _check(lib.kivi_latent_prompt_attn(qnp, qrp, K, krp, V, b, h, _addr(cnt), ts, _latent_scale(scale), op, st))
     return out
 
 
@@ -697,6 +709,7 @@ class LatentCache:
         _check(lib.kivi_latent_create(b, r, bits, G, R, max_tokens, ctypes.byref(self._h)))
         import torch
         self._dev = torch.cuda.current_device()   # the handle's memory is there
+        self._device = torch.device("cuda", self._dev)
         self._sms = torch.cuda.get_device_properties(self._dev).multi_processor_count
 
     def close(self):
@@ -779,20 +792,14 @@ class LatentCache:
         return 10 + h * sum(S) / 3e3 + turns * max(S) / 80 < absorbed, max(S)
 
     def _expanded(self, dims, ptrs, qrp, krp, cnt, T, S, scale, stream, st):
-        import torch
         (b, h, ns, r), (qnp, _, cp, _, wkp, wvp, op) = dims, ptrs
-        dev = f"cuda:{self._dev}"
-        with _on(stream):   # (rows past a sequence's tokens are not read)
-            c_all = torch.empty((b, S, r), dtype=torch.float16, device=dev)
-            kr_all = torch.empty((b, S, LATENT_ROPE), dtype=torch.float16, device=dev)
-            K = torch.empty((b, h, S, LATENT_HEAD), dtype=torch.float16, device=dev)
-            V = torch.empty_like(K)
-        _check(lib.kivi_latent_rows(self._h, cp, krp, _addr(cnt), ns, c_all.data_ptr(), kr_all.data_ptr(), S, st))
+        keep, (c_all, kr_all, K, V) = _space(stream, self._device, b * S * r, b * S * LATENT_ROPE,
+                                             *[b * h * S * LATENT_HEAD] * 2)   # (rows past a sequence's tokens are not read)
+        _check(lib.kivi_latent_rows(self._h, cp, krp, _addr(cnt), ns, c_all, kr_all, S, st))
         tok = array.array("i", [t + n if n else 0 for t, n in zip(T, cnt)])
         for w, x in ((wkp, K), (wvp, V)):
-            _check(lib.kivi_head_product(c_all.data_ptr(), w, b, 1, h, S, _addr(tok), r, LATENT_HEAD, 0, x.data_ptr(), st))
-        _check(lib.kivi_latent_expanded_attn(qnp, qrp, K.data_ptr(), kr_all.data_ptr(), V.data_ptr(), b, h, _addr(T),
-                                             _addr(cnt), ns, S, scale, op, st))
+            _check(lib.kivi_head_product(c_all, w, b, 1, h, S, _addr(tok), r, LATENT_HEAD, 0, x, st))
+        _check(lib.kivi_latent_expanded_attn(qnp, qrp, K, kr_all, V, b, h, _addr(T), _addr(cnt), ns, S, scale, op, st))
 
     def _lengths(self):
         T = array.array("i", bytes(4 * self.b))
@@ -800,19 +807,16 @@ class LatentCache:
         return T
 
     def _attn(self, dims, ptrs, qrp, krp, cnt, scale, form, stream, st):
-        import torch
         (b, h, ns, r), (qnp, _, cp, _, wkp, wvp, op) = dims, ptrs
         if form is not None or max(cnt) >= 16:
             T = self._lengths()
             expanded, S = self._form(form, cnt, T, h)
             if expanded:
                 return self._expanded(dims, ptrs, qrp, krp, cnt, T, S, scale, stream, st)
-        with _on(stream):   # (rows past n are not read)
-            ql = torch.empty((b, h, ns, r), dtype=torch.float16, device=f"cuda:{self._dev}")
-            ol = torch.empty_like(ql)
-        _check(lib.kivi_head_product(qnp, wkp, b, h, h, ns, _addr(cnt), LATENT_HEAD, r, 1, ql.data_ptr(), st))
-        _check(lib.kivi_latent_attn(self._h, ql.data_ptr(), qrp, cp, krp, _addr(cnt), ns, h, scale, ol.data_ptr(), st))
-        _check(lib.kivi_head_product(ol.data_ptr(), wvp, b, h, h, ns, _addr(cnt), r, LATENT_HEAD, 0, op, st))
+        keep, (ql, ol) = _space(stream, self._device, b * h * ns * r, b * h * ns * r)   # (rows past n are not read)
+        _check(lib.kivi_head_product(qnp, wkp, b, h, h, ns, _addr(cnt), LATENT_HEAD, r, 1, ql, st))
+        _check(lib.kivi_latent_attn(self._h, ql, qrp, cp, krp, _addr(cnt), ns, h, scale, ol, st))
+        _check(lib.kivi_head_product(ol, wvp, b, h, h, ns, _addr(cnt), r, LATENT_HEAD, 0, op, st))
 
     def _args(self, qn, qr, c, kr, wk, wv, out, stream):
         dims, ptrs, out = _latent_args(qn, qr, c, kr, wk, wv, out, stream, self._dev)
@@ -857,10 +861,9 @@ class LatentCache:
             if rope.d != LATENT_ROPE:
                 raise ValueError(f"rope is for heads of dimension {rope.d}")
             posp = None if pos is None else rope._pos(pos, b, ns, self._dev)
-            with _on(stream):   # (rows past n are not read)
-                rq, rk = torch.empty_like(qr), torch.empty_like(kr)
-            rope._call(qrp, krp, b, h, 1, ns, cnt, T if posp is None else None, posp, False, rq.data_ptr(), rk.data_ptr(), st)
-            qrp, krp = rq.data_ptr(), rk.data_ptr()
+            keep, (rq, rk) = _space(stream, self._device, b * h * ns * LATENT_ROPE, b * ns * LATENT_ROPE)   # (rows past n are not read)
+            rope._call(qrp, krp, b, h, 1, ns, cnt, T if posp is None else None, posp, False, rq, rk, st)
+            qrp, krp = rq, rk
         self._attn(dims, ptrs, qrp, krp, cnt, _latent_scale(scale), form, stream, st)
         _check(lib.kivi_latent_append(self._h, ptrs[2], krp, _addr(cnt), ns, st))
         return out
