@@ -12,12 +12,16 @@
 // and, read along its other axis,
 //   O^T [r x 64 rows] += C^T P^T            (128 deep, r / 128 MMAs of 128 rows).
 //
-// Bound: the MMAs' operand reads.  One of 128 x 64 x 16 reads 6 KB of shared
-// memory (48 cycles of its bandwidth, 32 of the tensor cores'), so a tile costs
-// 48 (r / 8 + r / 16 + 4) cycles and the restoring's stores.  (S with the 64 rows
-// on the M side and tiles of 64 tokens takes as long an MMA, 49 measured, for half
-// of the tokens: 220 us where this form takes NEW over 8 x 32k tokens of 128 heads.)
+// Bound: shared memory's bandwidth.  An MMA of 128 x 64 x 16 reads 6 KB of it (48
+// cycles, for 32 of the tensor cores'); with the restoring's stores a tile of r =
+// 512 moves 570 KB, 4450 cycles of it, and takes 7000: with one tile in shared
+// memory its steps follow one another (S^T 1700 cycles and the waits for the last
+// parts, softmax 1500, O^T's first part 900), and only the restoring runs beside
+// them.  8 x 32k 4-bit tokens of 128 heads (73 GFLOP): 158 us and 8 for the join; 64
+// ragged sequences of 4k, 16 heads: 42; 1024 tokens of 16 heads over 8000: 495.
 // 64 rows are what tensor memory holds: r x 64 sums take r / 2 of its 512 columns.
+// (S with the 64 rows on the M side and tiles of 64 tokens, two of which fit, took as
+// long an MMA, 49 cycles measured, for half of the tokens: 220 us over the 32k.)
 //
 // A thread of the softmax has one token and 32 of the rows, so a row's maximum over
 // the tile is spread over threads.  It is not formed a tile: weights are taken
@@ -39,7 +43,8 @@ namespace {
 
 // Warps that restore tiles and take their softmax: with two more for the MMAs and
 // copies, 10 warps of 168 registers.  (16 of 96 spilled, and spills go to L2 where
-// shared memory takes all of the first-level cache: 300 us against NEW.)
+// shared memory takes all of the first-level cache: 180 to 275 us where this takes
+// 158; so did calls of other functions in the loop.)
 constexpr int kLaWork = 8;
 constexpr int kLaThreads = 32 * (kLaWork + 2);
 constexpr int kLaCols = 32;   // rows of a thread in the softmax

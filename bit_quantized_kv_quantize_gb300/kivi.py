@@ -137,6 +137,8 @@ def _on(stream):
 
 def _counts(n, b, name="n"):
     """Per-sequence counts (an integer or b of them) as an array of C ints."""
+    if isinstance(n, array.array):
+        n = n.tolist()
     if not isinstance(n, (int, list, tuple)) or isinstance(n, bool):
         a = np.asarray(n)
         if a.dtype.kind not in "iu" or a.ndim > 1:
@@ -840,8 +842,12 @@ class LatentCache:
         """prefill(c, kr, t) and the prompt's attention (latent_prompt_attn)."""
         self._here()
         _, _, out = self._args(qn, qr, c, kr, wk, wv, out, stream)
-        self.prefill(c, kr, t, stream)
-        return latent_prompt_attn(qn, qr, c, kr, t, wk, wv, scale, out, stream)
+        cnt = _counts(t, self.b, "t")
+        if max(cnt) > self.max_tokens:
+            raise CapacityError(3, "a prompt exceeds max_tokens")
+        out = latent_prompt_attn(qn, qr, c, kr, cnt, wk, wv, scale, out, stream)   # (refuses before the cache changes)
+        self.prefill(c, kr, cnt, stream)
+        return out
 
     def extend(self, qn, qr, c, kr, n, wk, wv, rope=None, pos=None, scale=None, out=None, stream=None, form=None):
         """Take the next n tokens of every sequence (a chunk, or one): rotate qr

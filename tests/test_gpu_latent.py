@@ -443,6 +443,11 @@ def test_binding_refuses():
     with pytest.raises(K.KiviError):
         cache.attn(qn, qr, c, kr, 3, m.wk, m.wv, scale=-1.0)
     cache.prefill(c, kr, 3)
+    with pytest.raises(K.KiviError):                  # refused before the cache changes
+        cache.prefill_attn(qn, qr, c, kr, 2, m.wk, m.wv, scale=0.0)
+    with pytest.raises(K.CapacityError):
+        cache.prefill_attn(*m.queries(65), *m.tokens(65), 65, m.wk, m.wv)
+    assert list(cache.lengths()[0]) == [3, 3]
     big = m.tokens(62)
     with pytest.raises(K.CapacityError):
         cache.extend(*m.queries(62), *big, 62, m.wk, m.wv)
