@@ -106,6 +106,7 @@ __global__ void __launch_bounds__(kHpThreads, S > 3 ? 1 : 2)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    kivi_after_previous();
     const uint32_t taddr = s_taddr;
     const volatile int *abort = &s_abort;
     bool ok = true;
@@ -240,6 +241,7 @@ __global__ void __launch_bounds__(kHpThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    kivi_after_previous();
     const uint32_t taddr = s_taddr;
     const volatile int *abort = &s_abort;
     bool ok = true;
@@ -392,11 +394,9 @@ extern "C" kivi_status kivi_head_product(const void *x, const void *w, int b, in
         const int per = (int)((cols + groups - 1) / groups);
         static std::atomic<uint64_t> done;
         e = kivi_allow_smem(head_product_shared_kernel, hs_smem(kHsMaxK), info.device, done);
-        if (e == cudaSuccess) {
-            head_product_shared_kernel<<<dim3(grid.x, (unsigned)((cols + per - 1) / per)), kHpThreads, hs_smem(K),
-                                         (cudaStream_t)stream>>>(a, tm, per);
-            e = cudaGetLastError();
-        }
+        if (e == cudaSuccess)
+            e = kivi_launch_after(head_product_shared_kernel, dim3(grid.x, (unsigned)((cols + per - 1) / per)), kHpThreads,
+                                  hs_smem(K), (cudaStream_t)stream, a, tm, per);
         return e == cudaSuccess ? KIVI_OK : fail(KIVI_ERR_CUDA, cudaGetErrorString(e));
     }
     const bool deep = K > 2 * kHpK && (long long)grid.x * grid.y * grid.z <= info.sms;
@@ -406,7 +406,6 @@ extern "C" kivi_status kivi_head_product(const void *x, const void *w, int b, in
     static std::atomic<uint64_t> done[4];
     if (e == cudaSuccess) e = kivi_allow_smem(kernel, smem, info.device, done[2 * deep + mn]);
     if (e != cudaSuccess) return fail(KIVI_ERR_CUDA, cudaGetErrorString(e));
-    kernel<<<grid, kHpThreads, smem, (cudaStream_t)stream>>>(a, tm);
-    e = cudaGetLastError();
+    e = kivi_launch_after(kernel, grid, kHpThreads, smem, (cudaStream_t)stream, a, tm);
     return e == cudaSuccess ? KIVI_OK : fail(KIVI_ERR_CUDA, cudaGetErrorString(e));
 }

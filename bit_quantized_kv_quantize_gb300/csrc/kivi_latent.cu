@@ -104,6 +104,7 @@ __global__ void __launch_bounds__(32 * kApWarps)
                          const __grid_constant__ LatentTokens a) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int i = blockIdx.y, x = blockIdx.x * kApWarps + warp, n = a.n[i], T = a.T[i];
+    kivi_after_previous();
     if (x >= n) return;
     const int tau = T + x, Tq = lat_tq(T, g.R), Tq1 = lat_tq(T + n, g.R), W = g.ring * kLatTok;
     const size_t src = (size_t)i * a.n_stride + x;
@@ -139,6 +140,7 @@ __global__ void latent_rows_kernel(LatentGeom g, LatentDev dv, const __half *__r
     const long long e = (long long)blockIdx.x * blockDim.x + threadIdx.x;
     const int tau = (int)(e / per), c = (int)(e % per);
     const int T = a.T[i];
+    kivi_after_previous();
     if (tau >= T + a.n[i]) return;
     const int kb = tau / kLatTok, t = tau % kLatTok;
     const size_t row = (size_t)i * stride + tau;
@@ -183,18 +185,16 @@ __global__ void latent_rows_kernel(LatentGeom g, LatentDev dv, const __half *__r
 cudaError_t kivi_launch_latent_append(const LatentGeom &g, const LatentDev &dv, const __half *C, const __half *Kr,
                                       const LatentTokens &a, int maxn, cudaStream_t st) {
     const dim3 grid((unsigned)((maxn + kApWarps - 1) / kApWarps), (unsigned)g.b);
-    if (g.r == 512 && g.bits == 4) latent_append_kernel<16, 4><<<grid, 32 * kApWarps, 0, st>>>(g, dv, C, Kr, a);
-    else if (g.r == 512) latent_append_kernel<16, 2><<<grid, 32 * kApWarps, 0, st>>>(g, dv, C, Kr, a);
-    else if (g.bits == 4) latent_append_kernel<8, 4><<<grid, 32 * kApWarps, 0, st>>>(g, dv, C, Kr, a);
-    else latent_append_kernel<8, 2><<<grid, 32 * kApWarps, 0, st>>>(g, dv, C, Kr, a);
-    return cudaGetLastError();
+    const auto kernel = g.r == 512 ? (g.bits == 4 ? latent_append_kernel<16, 4> : latent_append_kernel<16, 2>)
+                                   : (g.bits == 4 ? latent_append_kernel<8, 4> : latent_append_kernel<8, 2>);
+    return kivi_launch_after(kernel, grid, 32 * kApWarps, 0, st, g, dv, C, Kr, a);
 }
 
 cudaError_t kivi_launch_latent_rows(const LatentGeom &g, const LatentDev &dv, const __half *Cn, const __half *Krn,
                                     __half *C, __half *Kr, const LatentTokens &a, int stride, int maxS, cudaStream_t st) {
     const long long items = (long long)maxS * ((g.r + kLatRope) / 8);
-    latent_rows_kernel<<<dim3((unsigned)((items + 255) / 256), (unsigned)g.b), 256, 0, st>>>(g, dv, Cn, Krn, C, Kr, stride, a);
-    return cudaGetLastError();
+    return kivi_launch_after(latent_rows_kernel, dim3((unsigned)((items + 255) / 256), (unsigned)g.b), 256, 0, st, g, dv, Cn,
+                             Krn, C, Kr, stride, a);
 }
 
 bool kivi_device_info(KiviDeviceInfo *info) {

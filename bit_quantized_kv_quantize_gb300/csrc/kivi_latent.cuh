@@ -94,3 +94,27 @@ cudaError_t kivi_allow_smem(K *kernel, size_t bytes, int device, std::atomic<uin
     if (e == cudaSuccess && device < 64) done.fetch_or(bit, std::memory_order_release);
     return e;
 }
+
+// A launch as a programmatic dependent of the kernel before it on the stream: its
+// CTAs are placed and set up while that one's last writes land, and wait
+// (kivi_after_previous, every CTA, before any access to global memory and before it
+// may return) until it is done.  The four kernels of a step
+// for 64 sequences take 56 us for 57, the expanded form of short prompts 42 for 44.
+template <typename... P, typename... A>
+cudaError_t kivi_launch_after(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t st, A &&...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+    return e == cudaSuccess ? cudaGetLastError() : e;
+}
+#ifdef __CUDACC__
+__device__ __forceinline__ void kivi_after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+#endif

@@ -265,6 +265,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    kivi_after_previous();
     const uint32_t taddr = s_taddr;
     const volatile int *abort = &s_abort;
     bool ok = true;
@@ -658,6 +659,7 @@ __global__ void __launch_bounds__(256) latent_join_kernel(__half *__restrict__ O
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rr = warp / W, w = warp % W;
     const int c = blockIdx.x / (kLatRows / RB) + 1, r = blockIdx.x % (kLatRows / RB) * RB + rr;
     const ChunkPos &p = a.cta[c];
+    kivi_after_previous();
     if (p.o <= kCkLead) return;   // CTA c starts with a row tile of its own
     const int i = p.i, m = p.m;
     const long long first = p.u - p.o + kCkLead;                         // the unit of its first tile
@@ -729,16 +731,15 @@ cudaError_t launch(const LatentGeom &g, const LatentDev &dv, const __half *Q, co
     if (e == cudaSuccess) e = make_sw_map(&tk, Kr, rows, kLatRope, kLatTok);
     if (e == cudaSuccess) e = kivi_allow_smem(latent_attn_kernel<RD, BITS>, la_smem(RD), device, done);
     if (e != cudaSuccess) return e;
-    latent_attn_kernel<RD, BITS><<<plan.ctas, kLaThreads, la_smem(RD), st>>>(g, dv, Q, Qr, C, Kr, O, tc, tk,
-                                                                            scale * 1.4426950408889634f, a);
-    e = cudaGetLastError();
+    e = kivi_launch_after(latent_attn_kernel<RD, BITS>, dim3((unsigned)plan.ctas), kLaThreads, la_smem(RD), st, g, dv, Q, Qr, C,
+                          Kr, O, tc, tk, scale * 1.4426950408889634f, a);
     if (e != cudaSuccess || !plan.join) return e;
     long long tiles = 0;
     for (int i = 0; i < g.b; ++i) tiles += chunk_row_tiles(a, i);
     // many partials a row tile: all of a block's warps at one row
-    if (plan.ctas > 8 * tiles) latent_join_kernel<RD, 1><<<(plan.ctas - 1) * kLatRows, 256, 0, st>>>(O, a);
-    else latent_join_kernel<RD, 4><<<(plan.ctas - 1) * (kLatRows / 4), 256, 0, st>>>(O, a);
-    return cudaGetLastError();
+    const bool one = plan.ctas > 8 * tiles;
+    return kivi_launch_after(one ? latent_join_kernel<RD, 1> : latent_join_kernel<RD, 4>,
+                             dim3((unsigned)((plan.ctas - 1) * (one ? kLatRows : kLatRows / 4))), 256, 0, st, O, a);
 }
 
 }  // namespace

@@ -72,6 +72,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
     constexpr int KS = kLpStages;
     const int bh = a.b * a.h, pair = blockIdx.x % bh, m = a.mt - 1 - blockIdx.x / bh, i = pair / a.h;
     const int n = a.n[i], T = a.T[i], row0 = m * 2 * kLpRows;
+    kivi_after_previous();
     if (row0 >= n) return;
     unsigned char *sQ = smem, *sK = sQ + 2 * kLpQ, *sV = sK + KS * kLpK;
     // counts 4 (a slot's softmax warps): P [slot][buffer], scores read [slot]; 2
@@ -400,8 +401,8 @@ kivi_status expanded(const void *q, const void *q_rope, const void *K, const voi
     static std::atomic<uint64_t> done;
     if (e == cudaSuccess) e = kivi_allow_smem(latent_prompt_kernel, kLpSmem, info.device, done);
     if (e != cudaSuccess) return fail(KIVI_ERR_CUDA, cudaGetErrorString(e));
-    latent_prompt_kernel<<<(unsigned)(a.mt * b * h), kLpThreads, kLpSmem, (cudaStream_t)stream>>>(tq, tqr, tk, tkr, tv, a);
-    e = cudaGetLastError();
+    e = kivi_launch_after(latent_prompt_kernel, dim3((unsigned)(a.mt * b * h)), kLpThreads, kLpSmem, (cudaStream_t)stream, tq,
+                          tqr, tk, tkr, tv, a);
     return e == cudaSuccess ? KIVI_OK : fail(KIVI_ERR_CUDA, cudaGetErrorString(e));
 }
 
