@@ -73,6 +73,7 @@ cudaError_t kivi_launch_latent_rows(const LatentGeom &g, const LatentDev &dv, co
 // The absorbed attention (kivi_latent_attn.cu); a: hq = hg = h, T, Tqk = Tqv =
 // the quantized tokens, n, n_stride, and the work list of kivi_plan_latent.
 constexpr int kLatRows = 64;   // rows of a row tile
+constexpr int kLatFew = 32;    // ... where there are few
 bool kivi_plan_latent(const LatentGeom &g, int h, ChunkArgs &a, int num_sms, ChunkPlan *plan);
 size_t kivi_latent_partial_floats(const LatentGeom &g, int num_sms);
 cudaError_t kivi_launch_latent_attn(const LatentGeom &g, const LatentDev &dv, const __half *Q, const __half *Qr,

@@ -47,13 +47,14 @@ namespace {
 // 158; so did calls of other functions in the loop.)
 constexpr int kLaWork = 8;
 constexpr int kLaThreads = 32 * (kLaWork + 2);
-constexpr int kLaCols = 32;   // rows of a thread in the softmax
+__host__ __device__ constexpr int la_cols(int rows) { return rows / 2; }   // rows of a thread in the softmax
 constexpr unsigned kLaCS = kLatTok * 128;    // bytes of 64 channels of a tile
-constexpr unsigned kLaQS = kLatRows * 128;   // of Q
 // tiles in shared memory (of r = 512 one fits; it is refilled in parts)
 __host__ __device__ constexpr int la_stages(int r) { return r == 512 ? 1 : 2; }
 __host__ __device__ constexpr int la_tile(int r) { return (r + kLatRope) / 64 * (int)kLaCS; }
-__host__ __device__ constexpr size_t la_smem(int r) { return (size_t)la_stages(r) * la_tile(r) + (r + kLatRope) / 64 * kLaQS + 1024; }
+__host__ __device__ constexpr size_t la_smem(int r, int rows) {
+    return (size_t)la_stages(r) * la_tile(r) + (r + kLatRope) / 64 * rows * 128 + 1024;
+}
 constexpr float kLaUnset = 1e30f;   // s_ref of a row that has seen nothing
 
 // whether any of the working warps says v (all come here every tile)
@@ -127,22 +128,30 @@ struct LaTile {
         : tb(tb), packed(tb + kLatTok <= Tq), block(!packed && tb + kLatTok <= T), keys(tb + kLatTok <= T) {}
 };
 
+// a thread's columns of a row tile
+__device__ __forceinline__ void la_ld(uint32_t t, uint32_t (&r)[32]) { tc_ld32(t, r); }
+__device__ __forceinline__ void la_ld(uint32_t t, uint32_t (&r)[16]) { tc_ld16(t, r); }
+__device__ __forceinline__ void la_st(uint32_t t, const uint32_t (&r)[32]) { tc_st32(t, r); }
+__device__ __forceinline__ void la_st(uint32_t t, const uint32_t (&r)[16]) { tc_st16(t, r); }
+
 // A raise: the rows' maxima over the tile (tS: this warp's scores of 32 rows, of
 // which those c < lim do not see the token), the references of the rows that grew by
 // more than 2^8, and their factors.  Called by every working warp.
+template <int RN>
 __device__ __forceinline__ void la_raise(uint32_t tS, float sl2, int lim, float *s_ref, float *s_al, float (*s_red)[kLatRows]) {
+    constexpr int CN = la_cols(RN);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    uint32_t r[kLaCols];
-    tc_ld32(tS, r);
+    uint32_t r[CN];
+    la_ld(tS, r);
     tc_wait_ld();
 #pragma unroll
-    for (int c = 0; c < kLaCols; ++c) {
+    for (int c = 0; c < CN; ++c) {
         const float m = la_redux_max(c < lim ? -INFINITY : __uint_as_float(r[c]) * sl2);
-        if (lane == 0) s_red[warp & 3][kLaCols * (warp >> 2) + c] = m;
+        if (lane == 0) s_red[warp & 3][CN * (warp >> 2) + c] = m;
     }
     la_sync();
     const int t = threadIdx.x;
-    if (t < kLatRows) {
+    if (t < RN) {
         const float m = fmaxf(fmaxf(s_red[0][t], s_red[1][t]), fmaxf(s_red[2][t], s_red[3][t]));
         const float old = s_ref[t];
         const bool grow = m != -INFINITY && m + old > kCkLift + kCkLag;
@@ -152,16 +161,17 @@ __device__ __forceinline__ void la_raise(uint32_t tS, float sl2, int lim, float 
     la_sync();
 }
 // 32 columns of O^T times the rows' factors, NM times (tO: this warp's lanes)
-template <int NM>
+template <int RN, int NM>
 __device__ __forceinline__ void la_rescale(uint32_t tO, const float *al) {
+    constexpr int CN = la_cols(RN);
 #pragma unroll 1
     for (int m = 0; m < NM; ++m) {
-        uint32_t o[kLaCols];
-        tc_ld32(tO + kLatRows * m, o);
+        uint32_t o[CN];
+        la_ld(tO + RN * m, o);
         tc_wait_ld();
 #pragma unroll
-        for (int c = 0; c < kLaCols; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * al[c]);
-        tc_st32(tO + kLatRows * m, o);
+        for (int c = 0; c < CN; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * al[c]);
+        la_st(tO + RN * m, o);
     }
     tc_wait_st();
 }
@@ -170,13 +180,15 @@ __device__ __forceinline__ void la_rescale(uint32_t tO, const float *al) {
 // the scores at tS: into its row of P (sP: the shared-memory address of its first
 // chunk), their sums from tL0 (first: none yet) to tL1.  Rows c < lim do not see the
 // token.  The largest log2 weight.
+template <int RN>
 __device__ __forceinline__ float la_weights(uint32_t tS, uint32_t tL0, uint32_t tL1, bool first, unsigned sP,
                                             const float *refs, float sl2, int lim) {
+    constexpr int CN = la_cols(RN);
     float up = -INFINITY;
-    uint32_t r[kLaCols];
-    tc_ld32(tS, r);
+    uint32_t r[CN];
+    la_ld(tS, r);
 #pragma unroll
-    for (int c0 = 0; c0 < kLaCols; c0 += 16) {
+    for (int c0 = 0; c0 < CN; c0 += 16) {
         uint32_t l[16];
         if (!first) tc_ld16(tL0 + c0, l);
         tc_wait_ld();
@@ -227,7 +239,7 @@ __device__ __forceinline__ float la_weights(uint32_t tS, uint32_t tL0, uint32_t 
 // memory: two S^T buffers of 64 columns, O^T, two buffers of the weights' sums.  Shared memory: tiles, then Q,
 // both in lat_at's layout.  The weights (a row of 64 a token) take the place of the
 // tile's rotary keys, which only S^T reads.
-template <int RD, int BITS>
+template <int RD, int BITS, int RN>
 __global__ void __launch_bounds__(kLaThreads, 1)
     latent_attn_kernel(const __grid_constant__ LatentGeom g, const __grid_constant__ LatentDev dv,
                        const __half *__restrict__ Q, const __half *__restrict__ Qr, const __half *__restrict__ Cn,
@@ -237,8 +249,10 @@ __global__ void __launch_bounds__(kLaThreads, 1)
     unsigned char *const smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
     constexpr int KS = la_stages(RD), TB = la_tile(RD), NM = RD / 128;
     constexpr unsigned CB = RD / 64 * kLaCS, RB = kLatRope / 64 * kLaCS;   // bytes of a tile's c, and kr
-    static_assert(RB == kLatRows * kLatTok * 2, "the weights fit in the rotary keys' place");
-    constexpr int OC = 2 * kLatRows;   // first column of O^T
+    static_assert(RB >= RN * kLatTok * 2, "the weights fit in the rotary keys' place");
+    constexpr int CN = la_cols(RN);
+    constexpr unsigned QS = RN * 128;   // bytes of 64 channels of Q
+    constexpr int OC = 2 * RN;   // first column of O^T
     unsigned char *sC = smem, *sQ = sC + KS * TB;
     using Units = LaUnits<RD, BITS>;
     // counts the working warps: Q, parts of a tile restored [stage][part]; 1: the
@@ -279,8 +293,8 @@ __global__ void __launch_bounds__(kLaThreads, 1)
 
     if (warp == WS) {
         // ---- S^T = T Q^T of tile x, then O^T += C^T P^T of tile x - (KS - 1) ----
-        constexpr uint32_t IDS = tc_idesc_f16(kLatTok, kLatRows, 0);
-        constexpr uint32_t IDO = tc_idesc_f16_at(128, kLatRows) | (1u << 16);   // both MN-major
+        constexpr uint32_t IDS = tc_idesc_f16(kLatTok, RN, 0);
+        constexpr uint32_t IDO = tc_idesc_f16_at(128, RN) | (1u << 16);   // both MN-major
         CkRing t, u;
         int cs = 0, co = 0;   // S^T, O^T so far
         unsigned qph = 0;
@@ -305,12 +319,12 @@ __global__ void __launch_bounds__(kLaThreads, 1)
                         if (!ok) break;
                         in = m < NM && part_in(m + 1, [&](uint64_t *bar) { return mbar_test(bar, t.p); });
                         tc_fence_after();
-                        const uint64_t qm = dq + (uint32_t)((2 * m * kLaQS) >> 4), cm = d + (uint32_t)((2 * m * kLaCS) >> 4);
+                        const uint64_t qm = dq + (uint32_t)((2 * m * QS) >> 4), cm = d + (uint32_t)((2 * m * kLaCS) >> 4);
 #pragma unroll
                         for (int c = 0; c < 8; ++c)
                             if (c < 4 || m < NM)
-                                tc_mma_f16_w(taddr + kLatRows * b, cm + (((c >> 2) * kLaCS + 32 * (c & 3)) >> 4),
-                                             qm + (((c >> 2) * kLaQS + 32 * (c & 3)) >> 4), IDS, m > 0 || c > 0);
+                                tc_mma_f16_w(taddr + RN * b, cm + (((c >> 2) * kLaCS + 32 * (c & 3)) >> 4),
+                                             qm + (((c >> 2) * QS + 32 * (c & 3)) >> 4), IDS, m > 0 || c > 0);
                     }
                     if (!ok) break;
                     tc_commit_w(&bS[b]);
@@ -327,7 +341,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
                 for (int m = 0; m < NM; ++m) {
 #pragma unroll
                     for (int c = 0; c < kLatTok / 16; ++c)
-                        tc_mma_f16_w(taddr + OC + kLatRows * m, dc + st + ((2 * m * kLaCS + 2048 * c) >> 4),
+                        tc_mma_f16_w(taddr + OC + RN * m, dc + st + ((2 * m * kLaCS + 2048 * c) >> 4),
                                      dp + st + ((2048 * c) >> 4), IDO, y > 0 || c > 0);
                     tc_commit_w(&eC[u.s * NM + m]);
                 }
@@ -461,8 +475,8 @@ __global__ void __launch_bounds__(kLaThreads, 1)
     } else {
         // ---- tiles, softmax, output ----
         const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
-        const int x0 = warp >> 2, r0 = kLaCols * x0, t0 = 32 * (warp & 3), tok = t0 + lane;   // word, rows, token
-        const uint32_t tO = taddr + lane_off + OC + r0, tL = tO + kLatRows * NM;   // O^T, two buffers of each thread's sums
+        const int x0 = warp >> 2, r0 = CN * x0, t0 = 32 * (warp & 3), tok = t0 + lane;   // word, rows, token
+        const uint32_t tO = taddr + lane_off + OC + r0, tL = tO + RN * NM;   // O^T, two buffers of each thread's sums
         int cnt = 0, tiles = 0;   // softmax, restored
         CkRing t, u;
         while (walk.next(kg, a, sg)) {
@@ -470,24 +484,26 @@ __global__ void __launch_bounds__(kLaThreads, 1)
             const unsigned char *rec = dv.rec + lat_rec(g, sg.i, first);
             // Q: row (token, head), 8 rows x 4 chunks at a time; rows past the last
             // are zero (the last segment's scores are all read)
-            constexpr int QN = kLatRows * (RD + kLatRope) / 8 / (32 * kLaWork);
+            constexpr int QC = (RD + kLatRope) / 8, QW = kLaWork * 8 / RN, QN = QC / 4 / QW;   // chunks of a row; warps and turns of 8 rows
+            static_assert(QC == QN * 4 * QW, "whole turns");
             {
                 uint4 v[QN];
+                const int q = 8 * (warp / QW) + (lane & 7), c0 = 4 * (warp % QW) + (lane >> 3);
 #pragma unroll
                 for (int k = 0; k < QN; ++k) {
-                    const int q = 8 * warp + (lane & 7), c = 4 * k + (lane >> 3);   // (warp w: rows 8 w ..)
+                    const int c = 4 * QW * k + c0;
                     const int rw = min(sg.row0 + q, sg.nrows - 1), tk = chunk_div(a, rw);
                     const size_t row = ((size_t)sg.i * h + rw - tk * h) * a.n_stride + tk;
                     v[k] = *reinterpret_cast<const uint4 *>(c < RD / 8 ? Q + row * RD + 8 * c : Qr + row * kLatRope + 8 * (c - RD / 8));
                 }
 #pragma unroll
                 for (int k = 0; k < QN; ++k) {
-                    const int q = 8 * warp + (lane & 7), c = 4 * k + (lane >> 3);
+                    const int c = 4 * QW * k + c0;
                     if (sg.row0 + q >= sg.nrows) v[k] = make_uint4(0u, 0u, 0u, 0u);
-                    *reinterpret_cast<uint4 *>(sQ + lat_at(c, q, kLatRows)) = v[k];
+                    *reinterpret_cast<uint4 *>(sQ + lat_at(c, q, RN)) = v[k];
                 }
             }
-            if (tid < kLatRows) s_ref[tid] = kLaUnset;
+            if (tid < RN) s_ref[tid] = kLaUnset;
             if (tid == 0) s_seg = sg;
             fence_proxy_async();
             __syncwarp();
@@ -501,7 +517,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
                 // would be spilled)
                 int th = threadIdx.x;
                 asm volatile("" : "+r"(th));
-                const int x0 = th >> 7, r0 = kLaCols * x0, tok = th & 127, t0 = tok & ~31, lane = th & 31;
+                const int x0 = th >> 7, r0 = CN * x0, tok = th & 127, t0 = tok & ~31, lane = th & 31;
                 const unsigned out = lat_at(x0 * (Units::CW / 8), tok, kLatTok);   // unit 0's place in a tile
                 if (x < nx) {
                     const LaTile lt(kLatTok * (first + x), T, Tq);
@@ -530,36 +546,36 @@ __global__ void __launch_bounds__(kLaThreads, 1)
                 const int xs = x - (KS - 1);
                 if (xs < 0) continue;
                 const int b = cnt & 1, key0 = kLatTok * (first + xs);
-                const uint32_t tW = taddr + ((uint32_t)t0 << 16) + r0, tS = tW + kLatRows * b;
-                const uint32_t tO = tW + OC, tL = tO + kLatRows * NM;
+                const uint32_t tW = taddr + ((uint32_t)t0 << 16) + r0, tS = tW + RN * b;
+                const uint32_t tO = tW + OC, tL = tO + RN * NM;
                 // the sums so far, and with this tile (kept apart until the tile stands)
-                const uint32_t tL0 = tL + kLatRows * (xs & 1), tL1 = tL + kLatRows * (~xs & 1);
+                const uint32_t tL0 = tL + RN * (xs & 1), tL1 = tL + RN * (~xs & 1);
                 // rows c < lim do not see this token: those of a token before it
                 int lim = 0;
                 if (key0 + kLatTok - 1 > p0) {
                     const int l = (key0 + tok - T) * h - row0 - r0;   // (below 2^24 + 2^16)
-                    lim = l < 0 ? 0 : l > kLaCols ? kLaCols : l;
+                    lim = l < 0 ? 0 : l > CN ? CN : l;
                 }
                 const unsigned sP = smem_u32(sC + u.s * TB + CB) + lat_at(r0 / 8, tok, kLatTok);   // (the tile's rotary keys are read once S^T is in)
                 ok = ok && __all_sync(kFull, mbar_wait_ab(&bS[b], (unsigned)(cnt >> 1) & 1u, abort));
                 tc_fence_after();
                 float up = INFINITY;   // (the segment's first tile: a raise at once)
-                if (ok && xs > 0) up = la_weights(tS, tL0, tL1, false, sP, s_ref + r0, sl2, lim);
+                if (ok && xs > 0) up = la_weights<RN>(tS, tL0, tL1, false, sP, s_ref + r0, sl2, lim);
                 if (la_any(!ok || up > kCkLift + kCkLag)) {   // a raise: then this tile's weights anew
                     if (la_any(!ok)) {   // every warp learns whether one has given up
                         ok = false;
                         break;
                     }
-                    la_raise(tS, sl2, lim, s_ref, s_al, s_red);
+                    la_raise<RN>(tS, sl2, lim, s_ref, s_al, s_red);
                     if (xs > 0) {   // O^T, once that of the last tile is in, and the sums
                         ok = __all_sync(kFull, mbar_wait_ab(&bF[~cnt & 1], (unsigned)((cnt - 1) >> 1) & 1u, abort));
                         if (ok) {
                             tc_fence_after();
-                            la_rescale<NM>(tO, s_al + r0);
-                            la_rescale<1>(tL0, s_al + r0);
+                            la_rescale<RN, NM>(tO, s_al + r0);
+                            la_rescale<RN, 1>(tL0, s_al + r0);
                         }
                     }
-                    if (ok) la_weights(tS, tL0, tL1, xs == 0, sP, s_ref + r0, sl2, lim);
+                    if (ok) la_weights<RN>(tS, tL0, tL1, xs == 0, sP, s_ref + r0, sl2, lim);
                     if (la_any(!ok)) {
                         ok = false;
                         break;
@@ -577,27 +593,28 @@ __global__ void __launch_bounds__(kLaThreads, 1)
             }
             tc_fence_after();
             // the rows' sums over the threads: halves exchanged, lane c ends with row c
-            float lsum[kLaCols];
+            float lsum[CN];
             {
-                uint32_t l[kLaCols];
-                tc_ld32(tL + kLatRows * (nx & 1), l);
+                uint32_t l[CN];
+                la_ld(tL + RN * (nx & 1), l);
                 tc_wait_ld();
 #pragma unroll
-                for (int c = 0; c < kLaCols; ++c) lsum[c] = __uint_as_float(l[c]);
+                for (int c = 0; c < CN; ++c) lsum[c] = __uint_as_float(l[c]);
             }
 #pragma unroll
-            for (int o = kLaCols / 2; o; o >>= 1)
+            for (int o = CN / 2; o; o >>= 1)
 #pragma unroll
                 for (int c = 0; c < o; ++c) {
                     const bool hi = lane & o;
                     const float give = hi ? lsum[c] : lsum[c + o], keep = hi ? lsum[c + o] : lsum[c];
                     lsum[c] = keep + __shfl_xor_sync(kFull, give, o);
                 }
-            s_red[warp & 3][r0 + lane] = lsum[0];
+            if (CN < 32) lsum[0] += __shfl_xor_sync(kFull, lsum[0], 16);
+            if (lane < CN) s_red[warp & 3][r0 + lane] = lsum[0];
             la_sync();
             const bool part = nx < s_seg.nt;
-            const size_t pr = (size_t)(2 * blockIdx.x + (first == 0 ? 1 : 0)) * kLatRows;
-            if (tid < kLatRows) {
+            const size_t pr = (size_t)(2 * blockIdx.x + (first == 0 ? 1 : 0)) * RN;
+            if (tid < RN) {
                 const float l = s_red[0][tid] + s_red[1][tid] + s_red[2][tid] + s_red[3][tid];
                 s_al[tid] = 1.f / l;
                 if (part && s_seg.row0 + tid < s_seg.nrows)
@@ -607,7 +624,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
             // the output: thread = channel, a row at a time; lane c knows where row c
             // begins
             const CkSeg se = s_seg;
-            const int rows = min(se.nrows - se.row0 - r0, kLaCols);
+            const int rows = min(se.nrows - se.row0 - r0, CN);
             long long off;
             {
                 const int q = r0 + lane, rw = min(se.row0 + q, se.nrows - 1), tk = chunk_div(a, rw);
@@ -616,19 +633,19 @@ __global__ void __launch_bounds__(kLaThreads, 1)
             const float inv = s_al[r0 + lane];
 #pragma unroll 1
             for (int m = 0; m < NM && rows > 0; ++m) {
-                uint32_t o[kLaCols];
-                tc_ld32(tO + kLatRows * m, o);
+                uint32_t o[CN];
+                la_ld(tO + RN * m, o);
                 tc_wait_ld();
                 const int ch = 128 * m + tok;
                 if (part) {
 #pragma unroll
-                    for (int c = 0; c < kLaCols; ++c) {
+                    for (int c = 0; c < CN; ++c) {
                         const long long at = __shfl_sync(kFull, off, c) + ch;
                         if (c < rows) a.acc[at] = __uint_as_float(o[c]);
                     }
                 } else {
 #pragma unroll
-                    for (int c = 0; c < kLaCols; ++c) {
+                    for (int c = 0; c < CN; ++c) {
                         const long long at = __shfl_sync(kFull, off, c) + ch;
                         const float w = __shfl_sync(kFull, inv, c);
                         if (c < rows) O[at] = __float2half_rn(__uint_as_float(o[c]) * w);
@@ -657,15 +674,15 @@ __global__ void __launch_bounds__(256) latent_join_kernel(__half *__restrict__ O
     __shared__ __align__(16) float s_acc[RB][W][RD];
     __shared__ float s_l[RB][W];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rr = warp / W, w = warp % W;
-    const int c = blockIdx.x / (kLatRows / RB) + 1, r = blockIdx.x % (kLatRows / RB) * RB + rr;
+    const int RN = a.tile_rows, c = blockIdx.x / (RN / RB) + 1, r = blockIdx.x % (RN / RB) * RB + rr;
     const ChunkPos &p = a.cta[c];
     kivi_after_previous();
     if (p.o <= kCkLead) return;   // CTA c starts with a row tile of its own
     const int i = p.i, m = p.m;
     const long long first = p.u - p.o + kCkLead;                         // the unit of its first tile
     if (a.cta[c - 1].u > first) return;                                  // an earlier boundary owns it
-    const int nrows = min(a.n[i] * a.hg - m * kLatRows, kLatRows);
-    if (blockIdx.x % (kLatRows / RB) * RB >= nrows) return;
+    const int nrows = min(a.n[i] * a.hg - m * RN, RN);
+    if (blockIdx.x % (RN / RB) * RB >= nrows) return;
     const long long end = first + chunk_tiles(a, i, m);
     int c1 = c;                                                          // the last CTA with its tiles
     while (a.cta[c1 + 1].u < end) ++c1;
@@ -676,7 +693,7 @@ __global__ void __launch_bounds__(256) latent_join_kernel(__half *__restrict__ O
     for (int v = 0; v < V; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
     float L = 0.f;
     if (r < nrows) {
-        auto part = [&](int k) { return (size_t)(2 * k + (k == c0 ? 1 : 0)) * kLatRows + r; };
+        auto part = [&](int k) { return (size_t)(2 * k + (k == c0 ? 1 : 0)) * RN + r; };
         float M = -INFINITY;
         for (int k = c0 + lane; k <= c1; k += 32) M = fmaxf(M, ml[part(k)].x);
         M = la_redux_max(M);
@@ -706,7 +723,7 @@ __global__ void __launch_bounds__(256) latent_join_kernel(__half *__restrict__ O
 #pragma unroll
     for (int k = 0; k < W; ++k) l += s_l[rr][k];
     const float inv = 1.f / l;
-    const int row = m * kLatRows + r, tok = chunk_div(a, row);
+    const int row = m * RN + r, tok = chunk_div(a, row);
     __half *dst = O + (((size_t)i * a.hq + row - tok * a.hg) * a.n_stride + tok) * RD;
     for (int e = 2 * (32 * w + lane); e < RD; e += 64 * W) {
         float2 y = make_float2(0.f, 0.f);
@@ -720,7 +737,7 @@ __global__ void __launch_bounds__(256) latent_join_kernel(__half *__restrict__ O
     }
 }
 
-template <int RD, int BITS>
+template <int RD, int BITS, int RN>
 cudaError_t launch(const LatentGeom &g, const LatentDev &dv, const __half *Q, const __half *Qr, const __half *C,
                    const __half *Kr, __half *O, const ChunkArgs &a, const ChunkPlan &plan, float scale, int device,
                    cudaStream_t st) {
@@ -729,9 +746,9 @@ cudaError_t launch(const LatentGeom &g, const LatentDev &dv, const __half *Q, co
     const long long rows = (long long)g.b * a.n_stride;
     cudaError_t e = make_sw_map(&tc, C, rows, RD, kLatTok);
     if (e == cudaSuccess) e = make_sw_map(&tk, Kr, rows, kLatRope, kLatTok);
-    if (e == cudaSuccess) e = kivi_allow_smem(latent_attn_kernel<RD, BITS>, la_smem(RD), device, done);
+    if (e == cudaSuccess) e = kivi_allow_smem(latent_attn_kernel<RD, BITS, RN>, la_smem(RD, RN), device, done);
     if (e != cudaSuccess) return e;
-    e = kivi_launch_after(latent_attn_kernel<RD, BITS>, dim3((unsigned)plan.ctas), kLaThreads, la_smem(RD), st, g, dv, Q, Qr, C,
+    e = kivi_launch_after(latent_attn_kernel<RD, BITS, RN>, dim3((unsigned)plan.ctas), kLaThreads, la_smem(RD, RN), st, g, dv, Q, Qr, C,
                           Kr, O, tc, tk, scale * 1.4426950408889634f, a);
     if (e != cudaSuccess || !plan.join) return e;
     long long tiles = 0;
@@ -739,7 +756,7 @@ cudaError_t launch(const LatentGeom &g, const LatentDev &dv, const __half *Q, co
     // many partials a row tile: all of a block's warps at one row
     const bool one = plan.ctas > 8 * tiles;
     return kivi_launch_after(one ? latent_join_kernel<RD, 1> : latent_join_kernel<RD, 4>,
-                             dim3((unsigned)((plan.ctas - 1) * (one ? kLatRows : kLatRows / 4))), 256, 0, st, O, a);
+                             dim3((unsigned)((plan.ctas - 1) * (one ? RN : RN / 4))), 256, 0, st, O, a);
 }
 
 }  // namespace
@@ -748,8 +765,15 @@ bool kivi_plan_latent(const LatentGeom &g, int h, ChunkArgs &a, int num_sms, Chu
     a.hq = a.hg = h;
     a.hg_mul = (unsigned)(((1ull << 32) + h - 1) / h);
     a.vis = Visible{0, 0};
-    a.tile_rows = kLatRows;
     a.tile_blocks = kLatTok / KIVI_KBLK;
+    // Row tiles of 32 where they are no more: a tile then takes 3/4 of the time.
+    long long few = 0, many = 0;   // tiles
+    for (int i = 0; i < g.b; ++i) {
+        const long long rows = (long long)a.n[i] * h, tiles = (a.T[i] + a.n[i] + kLatTok - 1) / kLatTok;
+        few += (rows + kLatFew - 1) / kLatFew * tiles;
+        many += (rows + kLatRows - 1) / kLatRows * tiles;
+    }
+    a.tile_rows = 3 * few < 4 * many ? kLatFew : kLatRows;
     *plan = ChunkPlan{false, false, 0};
     // (shares of two units and more: a tile takes as long as 8 of the chunk attention's)
     return kivi_plan_units(g.b, 1, a, num_sms, 2, &plan->ctas, &plan->join);
@@ -764,9 +788,15 @@ cudaError_t kivi_launch_latent_attn(const LatentGeom &g, const LatentDev &dv, co
                                     float scale, float *partials, int device, int num_sms, cudaStream_t st) {
     a.acc = partials;
     a.ml = partials + (size_t)2 * num_sms * kLatRows * g.r;
-    if (g.r == 256)
-        return g.bits == 2 ? launch<256, 2>(g, dv, Q, Qr, C, Kr, O, a, plan, scale, device, st)
-                           : launch<256, 4>(g, dv, Q, Qr, C, Kr, O, a, plan, scale, device, st);
-    return g.bits == 2 ? launch<512, 2>(g, dv, Q, Qr, C, Kr, O, a, plan, scale, device, st)
-                       : launch<512, 4>(g, dv, Q, Qr, C, Kr, O, a, plan, scale, device, st);
+    const auto pick = [&](auto rd, auto bits) {
+        return a.tile_rows == kLatRows
+                   ? launch<rd(), bits(), kLatRows>(g, dv, Q, Qr, C, Kr, O, a, plan, scale, device, st)
+                   : launch<rd(), bits(), kLatFew>(g, dv, Q, Qr, C, Kr, O, a, plan, scale, device, st);
+    };
+    using I2 = std::integral_constant<int, 2>;
+    using I4 = std::integral_constant<int, 4>;
+    using I256 = std::integral_constant<int, 256>;
+    using I512 = std::integral_constant<int, 512>;
+    if (g.r == 256) return g.bits == 2 ? pick(I256(), I2()) : pick(I256(), I4());
+    return g.bits == 2 ? pick(I512(), I2()) : pick(I512(), I4());
 }
