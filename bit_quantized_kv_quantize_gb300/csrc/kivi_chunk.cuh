@@ -66,9 +66,9 @@ __host__ __device__ __forceinline__ int chunk_tqv(int T, int Tqv, int n, int R) 
 
 // Lays out the work list of the row tiles (a: hg, tile_rows, tile_blocks, vis,
 // T and n) of b sequences of h kv heads for up to num_sms CTAs: a.cta, the CTAs,
-// and whether a row tile is cut between them.  least: units below which a share
-// is not cut.  False if a share would pass 32 bits.  (kivi_chunk_attn.cu)
-bool kivi_plan_units(int b, int h, ChunkArgs &a, int num_sms, int least, int *ctas, bool *join);
+// and whether a row tile is cut between them.  lead: the units of a row tile's
+// fixed cost; least: units below which a share is not cut.  False if a share would pass 32 bits.  (kivi_chunk_attn.cu)
+bool kivi_plan_units(int b, int h, ChunkArgs &a, int num_sms, int lead, int least, int *ctas, bool *join);
 // How a chunk's attention runs.
 struct ChunkPlan {
     bool few;   // the kernel for few rows

@@ -41,21 +41,21 @@ size_t kivi_chunk_partial_floats(const KiviGeom &g, const ChunkPlan &plan, int n
     return (size_t)2 * num_sms * (plan.few ? kFewRows : kCkTileRows) * (g.d + 2);
 }
 
-bool kivi_plan_units(int b, int h, ChunkArgs &a, int num_sms, int least, int *ctas, bool *join) {
+bool kivi_plan_units(int b, int h, ChunkArgs &a, int num_sms, int lead, int least, int *ctas, bool *join) {
     long long items = 0, U = 0;
     for (int i = 0; i < b; ++i) {
         const int mt = chunk_row_tiles(a, i);
         long long u = 0;
-        for (int m = 0; m < mt; ++m) u += kCkLead + chunk_tiles(a, i, m);
+        for (int m = 0; m < mt; ++m) u += lead + chunk_tiles(a, i, m);
         U += u * h;
         items += (long long)mt * h;
     }
     // One CTA an SM, but no share below `least` units unless the row tiles
     // are that short: cutting them finer costs more than it shortens (the
-    // join's launch too: row tiles of up to 3 kCkLead units are not cut while
+    // join's launch too: row tiles of up to 3 lead units are not cut while
     // the SMs suffice for them).
     const long long sms = num_sms < kCkMaxCtas ? num_sms : kCkMaxCtas;
-    const long long want = U > 3 * kCkLead * items && U / least > items ? U / least : items;
+    const long long want = U > 3 * lead * items && U / least > items ? U / least : items;
     *ctas = (int)(want < sms ? want : sms);
     if (U / *ctas >= INT_MAX) return false;   // (CkWalk counts them)
     // each CTA's first unit, and whether one lies behind the first key tile of
@@ -65,12 +65,12 @@ bool kivi_plan_units(int b, int h, ChunkArgs &a, int num_sms, int least, int *ct
     int c = 0;
     for (int i = 0; i < b; ++i)
         for (int m = 0; m < chunk_row_tiles(a, i); ++m) {
-            const int w = kCkLead + chunk_tiles(a, i, m);
+            const int w = lead + chunk_tiles(a, i, m);
             const long long end = P + (long long)h * w;
             for (; c < *ctas && (long long)c * U / *ctas < end; ++c) {
                 const long long u = (long long)c * U / *ctas;
                 a.cta[c] = ChunkPos{u, i, m, (int)((u - P) / w), (int)((u - P) % w)};
-                *join |= a.cta[c].o > kCkLead;
+                *join |= a.cta[c].o > lead;
             }
             P = end;
         }
@@ -107,7 +107,7 @@ bool kivi_plan_chunk_attn(const KiviGeom &g, ChunkArgs &a, int num_sms, ChunkPla
     a.tile_blocks = few ? 2 : 1;
     int ctas = 0;
     bool join = false;
-    if (!kivi_plan_units(g.b, g.h, a, num_sms, 2 * kCkLead, &ctas, &join)) return false;
+    if (!kivi_plan_units(g.b, g.h, a, num_sms, kCkLead, 2 * kCkLead, &ctas, &join)) return false;
     const char *quit = getenv("KIVI_CHUNK_QUIT");
     a.quit = quit ? atoi(quit) : INT_MAX;
     *plan = ChunkPlan{few, join, ctas};

@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(kCkThreads, 1)
     const uint32_t taddr = s_taddr;
     const volatile int *abort = &s_abort;
     bool ok = true;
-    CkWalk walk;
+    CkWalk<> walk;
     walk.start(a, blockIdx.x);
     CkSeg sg = {};
     // the segment's first tiles have a record: how many

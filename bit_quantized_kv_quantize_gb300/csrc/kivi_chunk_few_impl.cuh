@@ -380,7 +380,7 @@ __global__ void __launch_bounds__(kFwThreads, 1)
     const uint32_t taddr = s_taddr;
     const volatile int *abort = &s_abort;
     bool ok = true;
-    CkWalk walk;
+    CkWalk<> walk;
     walk.start(a, blockIdx.x);
     CkSeg sg = {};
     constexpr int WD = 4, WS = WD + 2 * kFwDq;   // first dequantizing warp, the S^T warp

@@ -161,7 +161,9 @@ struct CkSeg {
     __device__ __forceinline__ int key0(int x) const { return bl.phys(x0 + x) * KIVI_KBLK; }
 };
 
-// Walks a CTA's units: every warp runs the same walk.
+// Walks a CTA's units: every warp runs the same walk.  LEAD: the units of a row
+// tile's fixed cost.
+template <int LEAD = kCkLead>
 struct CkWalk {
     int left;        // units left
     int i, m, j, o;  // where they begin
@@ -177,8 +179,8 @@ struct CkWalk {
     __device__ __forceinline__ bool next(const KiviGeom &g, const ChunkArgs &a, CkSeg &s) {
         while (left > 0) {
             const int nb = chunk_blocks(a, i, m), nt = a.tile_blocks == 2 ? (nb + 1) >> 1 : nb;
-            const int w = kCkLead + nt, o1 = min(w, o + left);
-            const int x0 = max(o - kCkLead, 0), x1 = max(o1 - kCkLead, 0);
+            const int w = LEAD + nt, o1 = min(w, o + left);
+            const int x0 = max(o - LEAD, 0), x1 = max(o1 - LEAD, 0);
             s.i = i;
             s.j = j;
             s.m = m;

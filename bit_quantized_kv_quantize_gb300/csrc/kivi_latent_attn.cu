@@ -6,24 +6,28 @@
 // row t_s = [c_s ; kr_s], head h of the token at position p has
 //   out = sum_s softmax_s(scale q . t_s) c_s   over s <= p:
 // one key and value row a token for every head.  So the rows (token, head) of a
-// sequence are one list, cut into row tiles of 64, and a tile of 128 tokens,
-// restored once to fp16 in shared memory, is the A operand of both
-//   S^T [128 tokens x 64 rows] = T Q^T      (r + 64 deep)
+// sequence are one list, cut into row tiles of RN = 64 or 32, and a tile of 128
+// tokens, restored once to fp16 in shared memory, is the A operand of both
+//   S^T [128 tokens x RN rows] = T Q^T      (r + 64 deep)
 // and, read along its other axis,
-//   O^T [r x 64 rows] += C^T P^T            (128 deep, r / 128 MMAs of 128 rows).
+//   O^T [r x RN rows] += C^T P^T            (128 deep, r / 128 MMAs of 128 rows).
 //
 // Bound: shared memory's bandwidth.  An MMA of 128 x 64 x 16 reads 6 KB of it (48
 // cycles, for 32 of the tensor cores'); with the restoring's stores a tile of r =
-// 512 moves 570 KB, 4450 cycles of it, and takes 7000: with one tile in shared
-// memory its steps follow one another (S^T 1700 cycles and the waits for the last
-// parts, softmax 1500, O^T's first part 900), and only the restoring runs beside
-// them.  8 x 32k 4-bit tokens of 128 heads (73 GFLOP): 158 us and 8 for the join; 64
-// ragged sequences of 4k, 16 heads: 42; 1024 tokens of 16 heads over 8000: 495.
+// 512 moves 570 KB, 4450 cycles of it, and takes 6500: with one tile in shared
+// memory its steps follow one another (waits for the last parts and the end of S^T
+// 1800 cycles, softmax 1200, O^T's first part 1000), and only the restoring, 2500,
+// runs beside the products.  8 x 32k 4-bit tokens of 128 heads (73 GFLOP): 142 us
+// and 8 for the join; 64 ragged sequences of 4k, 16 heads: 35 in all; 1024 tokens of
+// 16 heads over 8000: 515.
 // 64 rows are what tensor memory holds: r x 64 sums take r / 2 of its 512 columns.
 // (S with the 64 rows on the M side and tiles of 64 tokens, two of which fit, took as
 // long an MMA, 49 cycles measured, for half of the tokens: 220 us over the 32k.)
+// Where row tiles of 32 are no more than those of 64, as in a step of up to 32
+// heads, an MMA takes 40 cycles and a softmax 700: the 64 ragged sequences' attention
+// 35 us for 39.
 //
-// A thread of the softmax has one token and 32 of the rows, so a row's maximum over
+// A thread of the softmax has one token and a quarter of the rows, so a row's maximum over
 // the tile is spread over threads.  It is not formed a tile: weights are taken
 // against the row's reference, and only when some score lies more than 2^8 above
 // it (one vote a tile) are the maxima formed, the references raised, O^T's columns
@@ -42,12 +46,15 @@
 namespace {
 
 // Warps that restore tiles and take their softmax: with two more for the MMAs and
-// copies, 10 warps of 168 registers.  (16 of 96 spilled, and spills go to L2 where
-// shared memory takes all of the first-level cache: 180 to 275 us where this takes
-// 158; so did calls of other functions in the loop.)
-constexpr int kLaWork = 8;
+// copies, 18 warps of 96 registers.  (8 of 168: 160 us over the 32k for 150.  What is
+// live over a tile has to fit: spills go to L2 where shared memory takes all of the
+// first-level cache, and calls of other functions in the loop spill, 180 to 275 us.)
+constexpr int kLaWork = 16;
 constexpr int kLaThreads = 32 * (kLaWork + 2);
-__host__ __device__ constexpr int la_cols(int rows) { return rows / 2; }   // rows of a thread in the softmax
+// Tiles that stand for a row tile's fixed cost, 14,000 cycles and a cut one's partials
+// (2: as long; 1 and 4: 3 % longer).
+constexpr int kLaLead = 3;
+__host__ __device__ constexpr int la_cols(int rows) { return rows / (kLaWork / 4); }   // rows of a thread in the softmax
 constexpr unsigned kLaCS = kLatTok * 128;    // bytes of 64 channels of a tile
 // tiles in shared memory (of r = 512 one fits; it is refilled in parts)
 __host__ __device__ constexpr int la_stages(int r) { return r == 512 ? 1 : 2; }
@@ -61,14 +68,14 @@ constexpr float kLaUnset = 1e30f;   // s_ref of a row that has seen nothing
 __device__ __forceinline__ bool la_any(bool v) {
     unsigned r;
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 1, 256, p;\n\t"
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 1, 512, p;\n\t"
         "selp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(r)
         : "r"(v ? 1u : 0u)
         : "memory");
     return r != 0;
 }
-__device__ __forceinline__ void la_sync() { asm volatile("barrier.cta.sync 1, 256;" ::: "memory"); }
+__device__ __forceinline__ void la_sync() { asm volatile("barrier.cta.sync 1, 512;" ::: "memory"); }
 __device__ __forceinline__ float la_redux_max(float x) {
     float r;
     asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
@@ -97,11 +104,13 @@ __device__ __forceinline__ void la_restore(unsigned char *tile, unsigned at, con
 }
 
 // A warp's part of a tile: units of one 16-byte word of codes (CW channels) of 32
-// tokens, a lane each.  Unit k is word x0 + 2 k (x0: warp / 4); PU of them are of a
-// part of 128 channels.
+// tokens, a lane each.  Unit k is word x0 + WX k (x0: warp / 4); PU of them are of a
+// part of 128 channels, or the words that the warps have at a time span SPAN parts.
 template <int RD, int BITS>
 struct LaUnits {
-    static constexpr int CW = 128 / BITS, NU = 4 * RD / CW / kLaWork, NG = CW / 32, PU = 64 / CW;
+    static constexpr int WX = kLaWork / 4;   // words at a time
+    static constexpr int CW = 128 / BITS, NU = RD / CW / WX, NG = CW / 32, SPAN = WX * CW > 128 ? WX * CW / 128 : 1;
+    static constexpr int PU = WX * CW > 128 ? 1 : 128 / CW / WX;
     uint4 w[NU];
     uint32_t sz[NU][NG];
     // p: unit 0's codes in the record; z: the record's scales and zeros of the
@@ -109,10 +118,10 @@ struct LaUnits {
     __device__ __forceinline__ void load(const unsigned char *p, const unsigned char *z, int ch, int lgG) {
 #pragma unroll
         for (int k = 0; k < NU; ++k) {
-            w[k] = __ldg(reinterpret_cast<const uint4 *>(p + k * (2 * kLatTok * 16)));
+            w[k] = __ldg(reinterpret_cast<const uint4 *>(p + k * (WX * kLatTok * 16)));
 #pragma unroll
             for (int q = 0; q < NG; ++q)
-                sz[k][q] = __ldg(reinterpret_cast<const uint32_t *>(z + ((ch + 2 * CW * k + 32 * q) >> lgG) * (kLatTok * 4)));
+                sz[k][q] = __ldg(reinterpret_cast<const uint32_t *>(z + ((ch + WX * CW * k + 32 * q) >> lgG) * (kLatTok * 4)));
         }
     }
 };
@@ -129,12 +138,12 @@ struct LaTile {
 };
 
 // a thread's columns of a row tile
-__device__ __forceinline__ void la_ld(uint32_t t, uint32_t (&r)[32]) { tc_ld32(t, r); }
+__device__ __forceinline__ void la_ld(uint32_t t, uint32_t (&r)[8]) { tc_ld8(t, r); }
 __device__ __forceinline__ void la_ld(uint32_t t, uint32_t (&r)[16]) { tc_ld16(t, r); }
-__device__ __forceinline__ void la_st(uint32_t t, const uint32_t (&r)[32]) { tc_st32(t, r); }
 __device__ __forceinline__ void la_st(uint32_t t, const uint32_t (&r)[16]) { tc_st16(t, r); }
+__device__ __forceinline__ void la_st(uint32_t t, const uint32_t (&r)[8]) { tc_st8(t, r); }
 
-// A raise: the rows' maxima over the tile (tS: this warp's scores of 32 rows, of
+// A raise: the rows' maxima over the tile (tS: this warp's scores of its rows, of
 // which those c < lim do not see the token), the references of the rows that grew by
 // more than 2^8, and their factors.  Called by every working warp.
 template <int RN>
@@ -160,7 +169,7 @@ __device__ __forceinline__ void la_raise(uint32_t tS, float sl2, int lim, float 
     }
     la_sync();
 }
-// 32 columns of O^T times the rows' factors, NM times (tO: this warp's lanes)
+// A warp's columns of O^T times the rows' factors, NM times (tO: this warp's lanes)
 template <int RN, int NM>
 __device__ __forceinline__ void la_rescale(uint32_t tO, const float *al) {
     constexpr int CN = la_cols(RN);
@@ -176,7 +185,7 @@ __device__ __forceinline__ void la_rescale(uint32_t tO, const float *al) {
     tc_wait_st();
 }
 
-// One thread's weights of its token against the references of its 32 rows, from
+// One thread's weights of its token against the references of its rows, from
 // the scores at tS: into its row of P (sP: the shared-memory address of its first
 // chunk), their sums from tL0 (first: none yet) to tL1.  Rows c < lim do not see the
 // token.  The largest log2 weight.
@@ -185,60 +194,56 @@ __device__ __forceinline__ float la_weights(uint32_t tS, uint32_t tL0, uint32_t 
                                             const float *refs, float sl2, int lim) {
     constexpr int CN = la_cols(RN);
     float up = -INFINITY;
-    uint32_t r[CN];
+    uint32_t r[CN], l[CN];
     la_ld(tS, r);
+    if (!first) la_ld(tL0, l);
+    tc_wait_ld();
+    if (first)
 #pragma unroll
-    for (int c0 = 0; c0 < CN; c0 += 16) {
-        uint32_t l[16];
-        if (!first) tc_ld16(tL0 + c0, l);
-        tc_wait_ld();
-        if (first)
+        for (int c = 0; c < CN; ++c) l[c] = 0u;
 #pragma unroll
-            for (int c = 0; c < 16; ++c) l[c] = 0u;
+    for (int c = 0; c < CN; c += 8) {
+        float y[8];
 #pragma unroll
-        for (int c = 0; c < 16; c += 8) {
-            float y[8];
-#pragma unroll
-            for (int k = 0; k < 8; k += 4) {
-                const float4 ref = *reinterpret_cast<const float4 *>(refs + c0 + c + k);
-                y[k] = fmaf(__uint_as_float(r[c0 + c + k]), sl2, ref.x);
-                y[k + 1] = fmaf(__uint_as_float(r[c0 + c + k + 1]), sl2, ref.y);
-                y[k + 2] = fmaf(__uint_as_float(r[c0 + c + k + 2]), sl2, ref.z);
-                y[k + 3] = fmaf(__uint_as_float(r[c0 + c + k + 3]), sl2, ref.w);
-            }
-            if (lim > c0 + c)
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    if (c0 + c + k < lim) y[k] = -INFINITY;
-            uint32_t pw[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                up = fmaxf(up, fmaxf(y[2 * k], y[2 * k + 1]));
-                const float y0 = ex2(y[2 * k]), y1 = ex2(y[2 * k + 1]);
-                l[c + 2 * k] = __float_as_uint(__uint_as_float(l[c + 2 * k]) + y0);
-                l[c + 2 * k + 1] = __float_as_uint(__uint_as_float(l[c + 2 * k + 1]) + y1);
-                pw[k] = ck_pack(y0, y1);
-            }
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(sP ^ (((c0 + c) / 8) << 4)), "r"(pw[0]), "r"(pw[1]),
-                         "r"(pw[2]), "r"(pw[3])
-                         : "memory");
+        for (int k = 0; k < 8; k += 4) {
+            const float4 ref = *reinterpret_cast<const float4 *>(refs + c + k);
+            y[k] = fmaf(__uint_as_float(r[c + k]), sl2, ref.x);
+            y[k + 1] = fmaf(__uint_as_float(r[c + k + 1]), sl2, ref.y);
+            y[k + 2] = fmaf(__uint_as_float(r[c + k + 2]), sl2, ref.z);
+            y[k + 3] = fmaf(__uint_as_float(r[c + k + 3]), sl2, ref.w);
         }
-        tc_st16(tL1 + c0, l);
+        if (lim > c)
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (c + k < lim) y[k] = -INFINITY;
+        uint32_t pw[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            up = fmaxf(up, fmaxf(y[2 * k], y[2 * k + 1]));
+            const float y0 = ex2(y[2 * k]), y1 = ex2(y[2 * k + 1]);
+            l[c + 2 * k] = __float_as_uint(__uint_as_float(l[c + 2 * k]) + y0);
+            l[c + 2 * k + 1] = __float_as_uint(__uint_as_float(l[c + 2 * k + 1]) + y1);
+            pw[k] = ck_pack(y0, y1);
+        }
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(sP ^ ((c / 8) << 4)), "r"(pw[0]), "r"(pw[1]), "r"(pw[2]),
+                     "r"(pw[3])
+                     : "memory");
     }
+    la_st(tL1, l);
     tc_wait_st();
     fence_proxy_async();
     tc_fence_before();
     return up;
 }
 
-// Warps 0-7: restoring tiles, softmax and output (of r = 512 one tile fits, so that
-// the two never run at once); 8: S^T and O^T; 9: copies (rotary keys, whole fp16
+// Warps 0-15: restoring tiles, softmax and output (of r = 512 one tile fits, so that
+// the two never run at once); 16: S^T and O^T; 17: copies (rotary keys, whole fp16
 // tiles).  They meet on mbarriers only (bounded
 // waits).  A tile is filled, and given back, in parts of 128 channels: S^T of the
 // next tile begins with its first part while O^T still reads the others.  Tensor
-// memory: two S^T buffers of 64 columns, O^T, two buffers of the weights' sums.  Shared memory: tiles, then Q,
-// both in lat_at's layout.  The weights (a row of 64 a token) take the place of the
-// tile's rotary keys, which only S^T reads.
+// memory: two S^T buffers of RN columns, O^T, two buffers of the weights' sums.
+// Shared memory: tiles, then Q, both in lat_at's layout.  The weights (a row of RN a
+// token) take the place of the tile's rotary keys, which only S^T reads.
 template <int RD, int BITS, int RN>
 __global__ void __launch_bounds__(kLaThreads, 1)
     latent_attn_kernel(const __grid_constant__ LatentGeom g, const __grid_constant__ LatentDev dv,
@@ -271,7 +276,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int h = a.hg;
     if (tid < NB) {
-        mbar_init(&bars[tid], tid < N8 ? kLaWork : 1);
+        mbar_init(&bars[tid], tid == 0 ? kLaWork : tid < N8 ? kLaWork / Units::SPAN : 1);
         fence_mbar_init();
     }
     if (tid == 0) s_abort = 0;
@@ -286,7 +291,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
     KiviGeom kg;   // (the walk reads b and h)
     kg.b = g.b;
     kg.h = 1;
-    CkWalk walk;
+    CkWalk<kLaLead> walk;
     walk.start(a, blockIdx.x);
     CkSeg sg = {};
     constexpr int WS = kLaWork;
@@ -484,14 +489,14 @@ __global__ void __launch_bounds__(kLaThreads, 1)
             const unsigned char *rec = dv.rec + lat_rec(g, sg.i, first);
             // Q: row (token, head), 8 rows x 4 chunks at a time; rows past the last
             // are zero (the last segment's scores are all read)
-            constexpr int QC = (RD + kLatRope) / 8, QW = kLaWork * 8 / RN, QN = QC / 4 / QW;   // chunks of a row; warps and turns of 8 rows
-            static_assert(QC == QN * 4 * QW, "whole turns");
+            constexpr int QC = (RD + kLatRope) / 8, QW = kLaWork * 8 / RN, QN = (QC / 4 + QW - 1) / QW;   // chunks of a row; warps and turns of 8 rows
             {
                 uint4 v[QN];
                 const int q = 8 * (warp / QW) + (lane & 7), c0 = 4 * (warp % QW) + (lane >> 3);
 #pragma unroll
                 for (int k = 0; k < QN; ++k) {
                     const int c = 4 * QW * k + c0;
+                    if (c >= QC) continue;
                     const int rw = min(sg.row0 + q, sg.nrows - 1), tk = chunk_div(a, rw);
                     const size_t row = ((size_t)sg.i * h + rw - tk * h) * a.n_stride + tk;
                     v[k] = *reinterpret_cast<const uint4 *>(c < RD / 8 ? Q + row * RD + 8 * c : Qr + row * kLatRope + 8 * (c - RD / 8));
@@ -499,6 +504,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
 #pragma unroll
                 for (int k = 0; k < QN; ++k) {
                     const int c = 4 * QW * k + c0;
+                    if (c >= QC) continue;
                     if (sg.row0 + q >= sg.nrows) v[k] = make_uint4(0u, 0u, 0u, 0u);
                     *reinterpret_cast<uint4 *>(sQ + lat_at(c, q, RN)) = v[k];
                 }
@@ -528,13 +534,15 @@ __global__ void __launch_bounds__(kLaThreads, 1)
                     rec += g.rec_bytes;
 #pragma unroll
                     for (int m = 0; m < NM; ++m) {
+                        constexpr int SP = Units::SPAN;
+                        if (SP > 1 && x0 * Units::CW / 128 != m % SP) continue;   // other warps'
                         if (lt.packed) {
                             // the part's place is free
                             ok = ok && __all_sync(kFull, tiles < KS || mbar_wait_ab(&eC[t.s * NM + m], t.p ^ 1u, abort));
                             if (ok)
 #pragma unroll
-                                for (int k = Units::PU * m; k < Units::PU * (m + 1); ++k)
-                                    la_restore<BITS>(tile + (2 * k * Units::CW / 64) * kLaCS, out, cur.w[k], cur.sz[k]);
+                                for (int k = Units::PU * (m / SP); k < Units::PU * (m / SP + 1); ++k)
+                                    la_restore<BITS>(tile + (Units::WX * k * Units::CW / 64) * kLaCS, out, cur.w[k], cur.sz[k]);
                             fence_proxy_async();
                             __syncwarp();
                         }
@@ -609,7 +617,8 @@ __global__ void __launch_bounds__(kLaThreads, 1)
                     const float give = hi ? lsum[c] : lsum[c + o], keep = hi ? lsum[c + o] : lsum[c];
                     lsum[c] = keep + __shfl_xor_sync(kFull, give, o);
                 }
-            if (CN < 32) lsum[0] += __shfl_xor_sync(kFull, lsum[0], 16);
+#pragma unroll
+            for (int o = CN; o < 32; o <<= 1) lsum[0] += __shfl_xor_sync(kFull, lsum[0], o);
             if (lane < CN) s_red[warp & 3][r0 + lane] = lsum[0];
             la_sync();
             const bool part = nx < s_seg.nt;
@@ -677,9 +686,9 @@ __global__ void __launch_bounds__(256) latent_join_kernel(__half *__restrict__ O
     const int RN = a.tile_rows, c = blockIdx.x / (RN / RB) + 1, r = blockIdx.x % (RN / RB) * RB + rr;
     const ChunkPos &p = a.cta[c];
     kivi_after_previous();
-    if (p.o <= kCkLead) return;   // CTA c starts with a row tile of its own
+    if (p.o <= kLaLead) return;   // CTA c starts with a row tile of its own
     const int i = p.i, m = p.m;
-    const long long first = p.u - p.o + kCkLead;                         // the unit of its first tile
+    const long long first = p.u - p.o + kLaLead;                         // the unit of its first tile
     if (a.cta[c - 1].u > first) return;                                  // an earlier boundary owns it
     const int nrows = min(a.n[i] * a.hg - m * RN, RN);
     if (blockIdx.x % (RN / RB) * RB >= nrows) return;
@@ -766,7 +775,8 @@ bool kivi_plan_latent(const LatentGeom &g, int h, ChunkArgs &a, int num_sms, Chu
     a.hg_mul = (unsigned)(((1ull << 32) + h - 1) / h);
     a.vis = Visible{0, 0};
     a.tile_blocks = kLatTok / KIVI_KBLK;
-    // Row tiles of 32 where they are no more: a tile then takes 3/4 of the time.
+    // Row tiles of 32 where they are hardly more: a tile then takes 0.8 of the time (r =
+    // 512; 128 heads over 32k, in twice the tiles, 238 us for 151) or 0.6 (r = 256).
     long long few = 0, many = 0;   // tiles
     for (int i = 0; i < g.b; ++i) {
         const long long rows = (long long)a.n[i] * h, tiles = (a.T[i] + a.n[i] + kLatTok - 1) / kLatTok;
@@ -776,7 +786,7 @@ bool kivi_plan_latent(const LatentGeom &g, int h, ChunkArgs &a, int num_sms, Chu
     a.tile_rows = 3 * few < 4 * many ? kLatFew : kLatRows;
     *plan = ChunkPlan{false, false, 0};
     // (shares of two units and more: a tile takes as long as 8 of the chunk attention's)
-    return kivi_plan_units(g.b, 1, a, num_sms, 2, &plan->ctas, &plan->join);
+    return kivi_plan_units(g.b, 1, a, num_sms, kLaLead, 2, &plan->ctas, &plan->join);
 }
 
 size_t kivi_latent_partial_floats(const LatentGeom &g, int num_sms) {
