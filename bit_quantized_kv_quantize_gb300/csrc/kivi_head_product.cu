@@ -396,7 +396,7 @@ extern "C" kivi_status kivi_head_product(const void *x, const void *w, int b, in
         e = kivi_allow_smem(head_product_shared_kernel, hs_smem(kHsMaxK), info.device, done);
         if (e == cudaSuccess)
             e = kivi_launch_after(head_product_shared_kernel, dim3(grid.x, (unsigned)((cols + per - 1) / per)), kHpThreads,
-                                  hs_smem(K), (cudaStream_t)stream, a, tm, per);
+                                  hs_smem(K), (cudaStream_t)stream, 1, a, tm, per);
         return e == cudaSuccess ? KIVI_OK : fail(KIVI_ERR_CUDA, cudaGetErrorString(e));
     }
     const bool deep = K > 2 * kHpK && (long long)grid.x * grid.y * grid.z <= info.sms;
@@ -406,6 +406,6 @@ extern "C" kivi_status kivi_head_product(const void *x, const void *w, int b, in
     static std::atomic<uint64_t> done[4];
     if (e == cudaSuccess) e = kivi_allow_smem(kernel, smem, info.device, done[2 * deep + mn]);
     if (e != cudaSuccess) return fail(KIVI_ERR_CUDA, cudaGetErrorString(e));
-    e = kivi_launch_after(kernel, grid, kHpThreads, smem, (cudaStream_t)stream, a, tm);
+    e = kivi_launch_after(kernel, grid, kHpThreads, smem, (cudaStream_t)stream, 1, a, tm);
     return e == cudaSuccess ? KIVI_OK : fail(KIVI_ERR_CUDA, cudaGetErrorString(e));
 }

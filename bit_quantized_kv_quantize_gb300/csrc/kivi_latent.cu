@@ -187,13 +187,13 @@ cudaError_t kivi_launch_latent_append(const LatentGeom &g, const LatentDev &dv, 
     const dim3 grid((unsigned)((maxn + kApWarps - 1) / kApWarps), (unsigned)g.b);
     const auto kernel = g.r == 512 ? (g.bits == 4 ? latent_append_kernel<16, 4> : latent_append_kernel<16, 2>)
                                    : (g.bits == 4 ? latent_append_kernel<8, 4> : latent_append_kernel<8, 2>);
-    return kivi_launch_after(kernel, grid, 32 * kApWarps, 0, st, g, dv, C, Kr, a);
+    return kivi_launch_after(kernel, grid, 32 * kApWarps, 0, st, 1, g, dv, C, Kr, a);
 }
 
 cudaError_t kivi_launch_latent_rows(const LatentGeom &g, const LatentDev &dv, const __half *Cn, const __half *Krn,
                                     __half *C, __half *Kr, const LatentTokens &a, int stride, int maxS, cudaStream_t st) {
     const long long items = (long long)maxS * ((g.r + kLatRope) / 8);
-    return kivi_launch_after(latent_rows_kernel, dim3((unsigned)((items + 255) / 256), (unsigned)g.b), 256, 0, st, g, dv, Cn,
+    return kivi_launch_after(latent_rows_kernel, dim3((unsigned)((items + 255) / 256), (unsigned)g.b), 256, 0, st, 1, g, dv, Cn,
                              Krn, C, Kr, stride, a);
 }
 

@@ -99,20 +99,24 @@ cudaError_t kivi_allow_smem(K *kernel, size_t bytes, int device, std::atomic<uin
 // A launch as a programmatic dependent of the kernel before it on the stream: its
 // CTAs are placed and set up while that one's last writes land, and wait
 // (kivi_after_previous, every CTA, before any access to global memory and before it
-// may return) until it is done.  The four kernels of a step
-// for 64 sequences take 56 us for 57, the expanded form of short prompts 42 for 44.
+// may return) until it is done.  The four kernels of a step for 64 sequences take
+// 56 us for 57, the expanded form of short prompts 42 for 44.  cluster: CTAs of one.
 template <typename... P, typename... A>
-cudaError_t kivi_launch_after(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t st, A &&...args) {
+cudaError_t kivi_launch_after(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t st, int cluster,
+                              A &&...args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cudaLaunchAttribute at;
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = (unsigned)cluster;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
     return e == cudaSuccess ? cudaGetLastError() : e;
 }

@@ -757,7 +757,7 @@ cudaError_t launch(const LatentGeom &g, const LatentDev &dv, const __half *Q, co
     if (e == cudaSuccess) e = make_sw_map(&tk, Kr, rows, kLatRope, kLatTok);
     if (e == cudaSuccess) e = kivi_allow_smem(latent_attn_kernel<RD, BITS, RN>, la_smem(RD, RN), device, done);
     if (e != cudaSuccess) return e;
-    e = kivi_launch_after(latent_attn_kernel<RD, BITS, RN>, dim3((unsigned)plan.ctas), kLaThreads, la_smem(RD, RN), st, g, dv, Q, Qr, C,
+    e = kivi_launch_after(latent_attn_kernel<RD, BITS, RN>, dim3((unsigned)plan.ctas), kLaThreads, la_smem(RD, RN), st, 1, g, dv, Q, Qr, C,
                           Kr, O, tc, tk, scale * 1.4426950408889634f, a);
     if (e != cudaSuccess || !plan.join) return e;
     long long tiles = 0;
@@ -765,7 +765,7 @@ cudaError_t launch(const LatentGeom &g, const LatentDev &dv, const __half *Q, co
     // many partials a row tile: all of a block's warps at one row
     const bool one = plan.ctas > 8 * tiles;
     return kivi_launch_after(one ? latent_join_kernel<RD, 1> : latent_join_kernel<RD, 4>,
-                             dim3((unsigned)((plan.ctas - 1) * (one ? RN : RN / 4))), 256, 0, st, O, a);
+                             dim3((unsigned)((plan.ctas - 1) * (one ? RN : RN / 4))), 256, 0, st, 1, O, a);
 }
 
 }  // namespace

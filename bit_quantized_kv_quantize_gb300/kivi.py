@@ -776,11 +776,12 @@ class LatentCache:
         """Whether attn forms every head's keys and values (expanded) rather than
         absorbing them, and the longest sequence with its new tokens.
 
-        None, the faster by these times on a GB300 (r = 512): absorbed 30 us and one
-        for 205,000 (query, head, token); expanded 10 us, one for 3,000 (token, head),
-        and 0.8 us for 64 tokens while every SM has a row tile of 256 queries of a
-        head.  16 heads over 8000 tokens: 128 queries 114 and 134 us, 256 180 and 168,
-        512 326 and 173; 128 heads over 4000: 64 queries 196 and 226, 256 675 and 243.
+        None, the faster by these times on a GB300 (us; r = 512, at 256 0.55 and 0.67
+        of the second terms): absorbed 35 and one for 250,000 (query, head, token);
+        expanded 10, one for 2,800 (token, head), and 0.8 for 64 tokens while every SM
+        has a row tile of 256 queries of a head, or a share of one, with 3 to join
+        them.  16 heads over 8000 tokens: 64 queries 64 and 76, 128 108 and 77, 512 305
+        and 96; 128 heads over 4000: 64 queries 184 and 223, 256 636 and 240.
         Expanded from 16 queries on, where keys and values take up to 4 GB."""
         S = [t + n if n > 0 else 0 for t, n in zip(T, cnt)]
         if form not in (None, "absorbed", "expanded"):
@@ -789,9 +790,11 @@ class LatentCache:
             return form == "expanded", max(S)
         if max(cnt) < 16 or 4 * self.b * max(S) * h * LATENT_HEAD > 1 << 32:
             return False, max(S)
-        absorbed = 30 + h * sum(n * s for n, s in zip(cnt, S)) / 205e3
-        turns = -(-h * sum((n + 255) // 256 for n in cnt) // self._sms)
-        return 10 + h * sum(S) / 3e3 + turns * max(S) / 80 < absorbed, max(S)
+        absorbed = 35 + h * sum(n * s for n, s in zip(cnt, S)) * (self.r + 64) / 144e6
+        rt = h * sum((n + 255) // 256 for n in cnt)
+        c = max(1, min(6, self._sms * 9 // 10 // rt))
+        expanded = 10 + h * sum(S) * (self.r + 256) / 2.15e6 + -(-rt // self._sms) * max(S) / (80 * c) + 3 * (c > 1)
+        return expanded < absorbed, max(S)
 
     def _expanded(self, dims, ptrs, qrp, krp, cnt, T, S, scale, stream, st):
         (b, h, ns, r), (qnp, _, cp, _, wkp, wvp, op) = dims, ptrs

@@ -332,6 +332,54 @@ def test_prompt_growing_scores_and_dead_values():
 # ---- together ------------------------------------------------------------------------------
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("b,h,r,t,n", [
+    (1, 1, 256, [4100], [300]),             # two row tiles, eight shares each
+    (2, 3, 512, [5000, 0], [130, 700]),     # shares without tiles; rows that see nothing of a share
+    (3, 7, 256, [1500, 900, 1100], [1, 0, 257]),
+    (1, 20, 512, [2600], [17]),
+])
+def test_row_tiles_that_ctas_share(b, h, r, t, n):
+    """The expanded form of few row tiles over many tokens, in shares that are
+    joined; scores that rise along the tokens for some rows and fall for others.
+    (The joined factors' roundings, 2^-22 relative a share, are within the bound's
+    S 2^-24.)"""
+    torch = pytest.importorskip("torch")
+    K, L = _K(), _L()
+    m = _Made(47, b, h, r)
+    bits, G, R, ns = 4, 32, 64, max(n)
+    cache = K.LatentCache(b, r, bits, G, R, max_tokens=max(t))
+    c, kr = m.tokens(max(t))
+    kr[:, :, 0] = torch.linspace(-8, 8, max(t), device="cuda").half()
+    cache.prefill(c, kr, t)
+    c1, kr1 = m.tokens(ns)
+    qn, qr = m.queries(ns)
+    qr[:, :, :, 0] = torch.linspace(-12, 12, ns, device="cuda").half()
+    out = cache.attn(qn, qr, c1, kr1, n, m.wk, m.wv, out=torch.full_like(qn, 7.0), form="expanded")
+    again = cache.attn(qn, qr, c1, kr1, n, m.wk, m.wv, out=torch.full_like(qn, 7.0), form="expanded")
+    assert cache.check() == 0 and K.device_check() == 0 and torch.equal(out, again)
+    for i in range(b):
+        assert bool((out[i, :, n[i]:] == 7.0).all())
+        if n[i] == 0:
+            continue
+        cs = torch.cat((L.cached(c[i], t[i], R, bits, G), c1[i, :n[i]].double()))
+        ks = torch.cat((kr[i, :t[i]], kr1[i, :n[i]])).double()
+        full = [L.latent(qn[i, e, :n[i]], qr[i, e, :n[i]], cs, ks, m.wk[e], m.wv[e], t[i], SCALE, False, True) for e in range(h)]
+        L.check(out[i, :, :n[i]], torch.stack([x for x, _ in full]), torch.stack([x for _, x in full]), f"{i}")
+    cache.close()
+    # a prompt alone
+    t = [x + y for x, y in zip(t, n)]
+    c, kr = m.tokens(max(t))
+    qn, qr = m.queries(max(t))
+    out = K.latent_prompt_attn(qn, qr, c, kr, t, m.wk, m.wv, out=torch.full_like(qn, 7.0))
+    assert K.device_check() == 0
+    i = t.index(max(t))
+    first = t[i] - 300
+    for e in (0, h - 1):
+        o, w = L.latent(qn[i, e, first:t[i]], qr[i, e, first:t[i]], c[i, :t[i]], kr[i, :t[i]], m.wk[e], m.wv[e], first, SCALE, False)
+        L.check(out[i, e, first:t[i]], o, w, f"prompt {e}")
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("r,bits,G,R,axes", [(512, 4, 32, 64, False), (256, 2, 64, 128, True)])
 def test_a_prompt_pieces_drafts_and_steps(r, bits, G, R, axes):
     """As a program serves: a rotated prompt, a piece, a draft that is verified and
