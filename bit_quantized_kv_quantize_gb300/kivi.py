@@ -687,13 +687,17 @@ def latent_prompt_attn(qn, qr, c, kr, t, wk, wv, scale=None, out=None, stream=No
     if dev != torch.cuda.current_device():
         with torch.cuda.device(dev):
             return latent_prompt_attn(qn, qr, c, kr, t, wk, wv, scale, out, stream)
-    (b, h, ts, r), (qnp, qrp, cp, krp, wkp, wvp, op), out = _latent_args(qn, qr, c, kr, wk, wv, out, stream, dev)
-    cnt, st = _counts(t, b, "t"), _stream(stream)
-    keep, (K, V) = _space(stream, qn.device, *[b * h * ts * LATENT_HEAD] * 2)   # (rows past t are not read)
+    dims, ptrs, out = _latent_args(qn, qr, c, kr, wk, wv, out, stream, dev)
+    _prompt(dims, ptrs, _counts(t, dims[0], "t"), _latent_scale(scale), stream, _stream(stream), qn.device)
+    return out
+
+
+def _prompt(dims, ptrs, cnt, scale, stream, st, device):
+    (b, h, ts, r), (qnp, qrp, cp, krp, wkp, wvp, op) = dims, ptrs
+    keep, (K, V) = _space(stream, device, *[b * h * ts * LATENT_HEAD] * 2)   # (rows past t are not read)
     for w, x in ((wkp, K), (wvp, V)):
         _check(lib.kivi_head_product(cp, w, b, 1, h, ts, _addr(cnt), r, LATENT_HEAD, 0, x, st))
-    _check(lib.kivi_latent_prompt_attn(qnp, qrp, K, krp, V, b, h, _addr(cnt), ts, _latent_scale(scale), op, st))
-    return out
+    _check(lib.kivi_latent_prompt_attn(qnp, qrp, K, krp, V, b, h, _addr(cnt), ts, scale, op, st))
 
 
 class LatentCache:
@@ -844,12 +848,12 @@ class LatentCache:
     def prefill_attn(self, qn, qr, c, kr, t, wk, wv, scale=None, out=None, stream=None):
         """prefill(c, kr, t) and the prompt's attention (latent_prompt_attn)."""
         self._here()
-        _, _, out = self._args(qn, qr, c, kr, wk, wv, out, stream)
-        cnt = _counts(t, self.b, "t")
+        dims, ptrs, out = self._args(qn, qr, c, kr, wk, wv, out, stream)
+        cnt, st = _counts(t, self.b, "t"), _stream(stream)
         if max(cnt) > self.max_tokens:
             raise CapacityError(3, "a prompt exceeds max_tokens")
-        out = latent_prompt_attn(qn, qr, c, kr, cnt, wk, wv, scale, out, stream)   # (refuses before the cache changes)
-        self.prefill(c, kr, cnt, stream)
+        _prompt(dims, ptrs, cnt, _latent_scale(scale), stream, st, self._device)   # (refuses before the cache changes)
+        _check(lib.kivi_latent_prefill(self._h, ptrs[2], ptrs[3], _addr(cnt), dims[2], st))
         return out
 
     def extend(self, qn, qr, c, kr, n, wk, wv, rope=None, pos=None, scale=None, out=None, stream=None, form=None):

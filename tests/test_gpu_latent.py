@@ -379,6 +379,48 @@ def test_row_tiles_that_ctas_share(b, h, r, t, n):
         L.check(out[i, e, first:t[i]], o, w, f"prompt {e}")
 
 
+def _outputs(torch, m, cache, qn, qr, c, kr, c1, kr1, t, n, R, bits, G, rows):
+    """Both forms against the reference: the given (sequence, head) pairs."""
+    K, L = _K(), _L()
+    for form in ("absorbed", "expanded"):
+        out = cache.attn(qn, qr, c1, kr1, n, m.wk, m.wv, out=torch.full_like(qn, 7.0), form=form)
+        assert cache.check() == 0 and K.device_check() == 0
+        assert all(bool((out[i, :, k:] == 7.0).all()) for i, k in enumerate(n) if k < out.shape[2])
+        for i, e in rows:
+            cs = torch.cat((L.cached(c[i, :t[i]], t[i], R, bits, G), c1[i, :n[i]].double()))
+            ks = torch.cat((kr[i, :t[i]], kr1[i, :n[i]])).double()
+            o, w = L.latent(qn[i, e, :n[i]], qr[i, e, :n[i]], cs, ks, m.wk[e], m.wv[e], t[i], SCALE, form == "absorbed",
+                            form == "expanded")
+            L.check(out[i, e, :n[i]], o, w, f"{form} {i} {e}")
+
+
+@pytest.mark.gpu
+def test_offsets_past_32_bits():
+    """A cache of 5 GB of records, most of it empty, and its last sequences; keys
+    and values of more than 4 GB."""
+    torch = pytest.importorskip("torch")
+    K = _K()
+    b, h, r, R = 1024, 2, 512, 64
+    m = _Made(3, b, h, r)
+    cache = K.LatentCache(b, r, 4, 32, R, max_tokens=16384)
+    t, n = [0] * b, [0] * b
+    t[1000], t[1023], n[1000], n[1022], n[1023] = 129, 300, 1, 2, 3
+    c, kr = m.tokens(300)
+    cache.prefill(c, kr, t)
+    c1, kr1 = m.tokens(3)
+    _outputs(torch, m, cache, *m.queries(3), c, kr, c1, kr1, t, n, R, 4, 32, [(1000, 1), (1022, 0), (1023, 0), (1023, 1)])
+    cache.close()
+    del cache, c, kr
+    b, h, t, n = 1, 128, [140000], [2]
+    m = _Made(4, b, h, r)
+    cache = K.LatentCache(b, r, 4, 32, R, max_tokens=t[0])
+    c, kr = m.tokens(t[0])
+    cache.prefill(c, kr, t)
+    c1, kr1 = m.tokens(2)
+    _outputs(torch, m, cache, *m.queries(2), c, kr, c1, kr1, t, n, R, 4, 32, [(0, 0), (0, 127)])
+    cache.close()
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("r,bits,G,R,axes", [(512, 4, 32, 64, False), (256, 2, 64, 128, True)])
 def test_a_prompt_pieces_drafts_and_steps(r, bits, G, R, axes):
