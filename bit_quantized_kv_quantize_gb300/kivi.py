@@ -448,6 +448,8 @@ class KiviCache:
                 raise CapacityError(3, f"sequence {i} would exceed max_tokens")
         qp, out, op = self._chunk_out(Q, ns, out, stream)
         hq, st, cp = Q.shape[1], _stream(stream), _addr(cnt)
+        if rope is None and pos is not None:
+            raise ValueError("positions without a rope")
         if rope is not None:
             if rope.d != self.d:
                 raise ValueError(f"rope is for heads of dimension {rope.d}")
@@ -866,6 +868,8 @@ class LatentCache:
         dims, ptrs, out = self._args(qn, qr, c, kr, wk, wv, out, stream)
         (b, h, ns, _), cnt, st = dims, _counts(n, self.b), _stream(stream)
         qrp, krp = ptrs[1], ptrs[3]
+        if rope is None and pos is not None:
+            raise ValueError("positions without a rope")
         T = self._lengths()
         for i in range(b):
             if cnt[i] > self.max_tokens - T[i]:

@@ -505,6 +505,41 @@ def test_streams_and_graphs():
 
 
 @pytest.mark.gpu
+def test_shared_row_tiles_on_streams_and_in_graphs():
+    """A chunk whose row tiles CTAs share, on another stream and captured twice,
+    the graphs replayed in turn; and a step behind it in the same graph."""
+    torch = pytest.importorskip("torch")
+    K = _K()
+    b, h, r, t, n = 1, 3, 256, 2100, 40
+    m = _Made(9, b, h, r)
+    cache = K.LatentCache(b, r, 4, 32, 64, max_tokens=t)
+    c, kr = m.tokens(t)
+    cache.prefill(c, kr, t)
+    c1, kr1 = m.tokens(n)
+    qn, qr = m.queries(n)
+    want = [cache.attn(qn, qr, c1, kr1, k, m.wk, m.wv, out=torch.full_like(qn, 7.0)) for k in (n, 1)]
+    st, outs, graphs = torch.cuda.Stream(), [], []
+    st.wait_stream(torch.cuda.current_stream())
+    for _ in range(2):
+        o = [torch.full_like(qn, 7.0) for _ in want]
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=st):
+            for k, x in zip((n, 1), o):
+                cache.attn(qn, qr, c1, kr1, k, m.wk, m.wv, out=x)
+        outs.append(o)
+        graphs.append(g)
+    for g in graphs + graphs:
+        g.replay()
+    side = torch.full_like(qn, 7.0)
+    st.wait_stream(torch.cuda.current_stream())
+    cache.attn(qn, qr, c1, kr1, n, m.wk, m.wv, out=side, stream=st)
+    torch.cuda.synchronize()
+    assert cache.check() == 0 and K.device_check() == 0
+    assert all(torch.equal(x, y) for o in outs for x, y in zip(o, want)) and torch.equal(side, want[0])
+    cache.close()
+
+
+@pytest.mark.gpu
 def test_binding_refuses():
     torch = pytest.importorskip("torch")
     K = _K()

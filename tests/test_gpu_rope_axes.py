@@ -158,3 +158,19 @@ def test_extend_at_given_positions():
     with pytest.raises(ValueError):
         a.extend(Q, Kn, V, 9, rope=rope, pos=pos[:2].contiguous())
     assert a.check() == 0 and [int(x) for x in a.lengths()[0]] == [9, 4]
+
+
+@pytest.mark.gpu
+def test_positions_without_a_rope_are_refused():
+    torch = pytest.importorskip("torch")
+    K = _K()
+    half = lambda *s: torch.zeros(*s, device="cuda", dtype=torch.float16)   # noqa: E731
+    pos = torch.zeros(1, 3, dtype=torch.int32, device="cuda")
+    cache = K.KiviCache(1, 2, 64, max_tokens=100)
+    with pytest.raises(ValueError):
+        cache.extend(half(1, 4, 3, 64), half(1, 2, 3, 64), half(1, 2, 3, 64), 3, pos=pos)
+    latent = K.LatentCache(1, 256, max_tokens=100)
+    with pytest.raises(ValueError):
+        latent.extend(half(1, 2, 3, 128), half(1, 2, 3, 64), half(1, 3, 256), half(1, 3, 64), 3, half(2, 128, 256), half(2, 128, 256),
+                      pos=pos)
+    assert int(cache.lengths()[0][0]) == 0 and int(latent.lengths()[0][0]) == 0
