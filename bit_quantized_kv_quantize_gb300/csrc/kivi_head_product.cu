@@ -20,9 +20,10 @@
 // Rows that all heads share (a prompt's expansion) stay in shared memory, 128 of
 // them up to 512 deep, while a CTA goes through several heads: W alone streams, the
 // accumulator has two buffers, and one head's output is written under the next
-// one's products.  (4096 tokens, 512 deep, 32 heads: 23 us, 0.73 PFLOP/s, where a CTA
-// a tile, with twice the traffic from L2 and its own prologue, took 27.  Each CTA
-// waits for W from L2: 131 MB in all, 80 KB on their way an SM.)
+// one's products.  (4096 tokens, 512 deep, 32 heads: 21.3 us, 0.81 PFLOP/s, where a
+// CTA a tile, with twice the traffic from L2 and its own prologue, took 27.  A CTA
+// takes in 128 KB of W for 128 columns; sent to two row tiles at once by multicast it
+// took 24.4.)
 #include "../../include/kivi.h"
 #include "kivi_async.cuh"
 #include "kivi_latent.cuh"
@@ -213,31 +214,37 @@ __global__ void __launch_bounds__(kHpThreads, S > 3 ? 1 : 2)
     if (warp == 0) tc_dealloc(taddr, kHpCols);
 }
 
-constexpr int kHsStages = 5, kHsMaxK = 512;
-__host__ __device__ constexpr size_t hs_smem(int K) { return (size_t)kHpRows * K * 2 + (size_t)kHsStages * kHpB + 1024; }
+constexpr int kHsMaxK = 512;
+__host__ __device__ constexpr int hs_stages(int C) { return C == 2 ? 3 : 5; }
+__host__ __device__ constexpr size_t hs_smem(int C, int K) {
+    return (size_t)kHpRows * K * 2 + (size_t)hs_stages(C) * C * kHpB + 1024;
+}
 
 // The rows of all heads alike: CTA (row tile, group) makes tiles [per y, per (y +
-// 1)) of the heads' 128-column tiles.  Warps as above.
+// 1)) of all heads' columns, 128 C a tile.  (128 make an MMA's operands 8 KB for 32
+// cycles' work, 256 12 KB for 64.)  Warps as above.
+template <int C>
 __global__ void __launch_bounds__(kHpThreads, 1)
     head_product_shared_kernel(const __grid_constant__ HeadArgs a, const __grid_constant__ CUtensorMap tm, int per) {
     extern __shared__ unsigned char raw[];
-    constexpr int S = kHsStages;
-    const int nk = a.K / kHpK, nc = a.N / kHpCols;
+    constexpr int S = hs_stages(C), NX = kHsMaxK / kHpK, Cols = C * kHpCols, B = C * kHpB;
+    const int nk = a.K / kHpK, nc = a.N / kHpCols, cols = a.h * nc;
     unsigned char *sA = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u), *sB = sA + nk * kHpA;
-    // counts 4: x in, buffer read [buffer]; 1: the others
-    __shared__ __align__(8) uint64_t bars[3 + 2 * S + 3];
-    uint64_t *const bA = bars, *const eD = bars + 1, *const bB = bars + 3, *const eS = bB + S, *const bD = eS + S, *const bE = bD + 2;
+    // counts 4: x in [64 of K], buffer read [buffer]; 1: the others
+    constexpr int N4 = NX + 2, NB = N4 + 2 * S + 3;
+    __shared__ __align__(8) uint64_t bars[NB];
+    uint64_t *const bA = bars, *const eD = bars + NX, *const bB = bars + N4, *const eS = bB + S, *const bD = eS + S, *const bE = bD + 2;
     __shared__ uint32_t s_taddr;
     __shared__ int s_abort;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int row0 = blockIdx.x * kHpRows, rows = a.first[a.b];
-    const int j0 = blockIdx.y * per, j1 = min(j0 + per, a.h * nc);
-    if (tid < 3 + 2 * S + 3) {
-        mbar_init(&bars[tid], tid < 3 ? 4 : 1);
+    const int j0 = blockIdx.y * per, j1 = min(j0 + per, (cols + C - 1) / C);
+    if (tid < NB) {
+        mbar_init(&bars[tid], tid < N4 ? 4 : 1);
         fence_mbar_init();
     }
     if (tid == 0) s_abort = 0;
-    if (warp == 0) tc_alloc(&s_taddr, 2 * kHpCols);
+    if (warp == 0) tc_alloc(&s_taddr, 2 * Cols);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -249,30 +256,53 @@ __global__ void __launch_bounds__(kHpThreads, 1)
     if (warp < 4) {
         constexpr int NR = kHpRows / 16;
         const unsigned at = (tid >> 3) * 128 + (((tid & 7) ^ ((tid >> 3) & 7)) * 16);
+        const __half *src[NR];
+        unsigned in = 0;
 #pragma unroll
         for (int k = 0; k < NR; ++k) {
             const int row = row0 + (tid >> 3) + 16 * k;
+            if (row < rows) in |= 1u << k;
             const int2 p = hp_row(a, row < rows ? row : row0);
-            const __half *src = a.x + ((size_t)p.x * a.n_stride + p.y) * a.K + 8 * (tid & 7);
-            for (int it = 0; it < nk; ++it) hp_copy16(sA + it * kHpA + at + k * 16 * 128, src + it * kHpK, row < rows);
+            src[k] = a.x + ((size_t)p.x * a.n_stride + p.y) * a.K + 8 * (tid & 7);
         }
-        asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bA);
+        for (int it = 0; it < NX; ++it) {   // (past K: empty groups)
+#pragma unroll
+            for (int k = 0; k < NR; ++k)
+                if (it < nk) hp_copy16(sA + it * kHpA + at + k * 16 * 128, src[k] + it * kHpK, (in >> k) & 1u);
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        }
+        auto told = [&](int it) {
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0 && it < nk) mbar_arrive(&bA[it]);
+        };
+        static_assert(NX == 8, "a wait for each group");
+        asm volatile("cp.async.wait_group 7;" ::: "memory"); told(0);
+        asm volatile("cp.async.wait_group 6;" ::: "memory"); told(1);
+        asm volatile("cp.async.wait_group 5;" ::: "memory"); told(2);
+        asm volatile("cp.async.wait_group 4;" ::: "memory"); told(3);
+        asm volatile("cp.async.wait_group 3;" ::: "memory"); told(4);
+        asm volatile("cp.async.wait_group 2;" ::: "memory"); told(5);
+        asm volatile("cp.async.wait_group 1;" ::: "memory"); told(6);
+        asm volatile("cp.async.wait_group 0;" ::: "memory"); told(7);
         const int row = row0 + tid;
         const int2 p = hp_row(a, row < rows ? row : row0);
         for (int j = j0; j < j1 && ok; ++j) {
-            const int y = j - j0, b = y & 1, e = j / nc, col0 = (j - e * nc) * kHpCols;
+            const int y = j - j0, b = y & 1;
             ok = __all_sync(kHpFull, mbar_wait_ab(&bD[b], (unsigned)(y >> 1) & 1u, abort));
             if (!ok) break;
             tc_fence_after();
-            hp_store(row < rows ? a.out + (((size_t)p.x * a.h + e) * a.n_stride + p.y) * a.N + col0 : nullptr,
-                     taddr + ((uint32_t)(32 * warp) << 16) + kHpCols * b, [&] {   // the buffer is read
-                         tc_fence_before();
-                         __syncwarp();
-                         if (lane == 0) mbar_arrive(&eD[b]);
-                     });
+#pragma unroll
+            for (int k = 0; k < C; ++k) {
+                const int e = (C * j + k) / nc, col0 = (C * j + k - e * nc) * kHpCols;
+                hp_store(row < rows && C * j + k < cols ? a.out + (((size_t)p.x * a.h + e) * a.n_stride + p.y) * a.N + col0 : nullptr,
+                         taddr + ((uint32_t)(32 * warp) << 16) + Cols * b + kHpCols * k, [&] {   // the buffer is read
+                             if (k < C - 1) return;
+                             tc_fence_before();
+                             __syncwarp();
+                             if (lane == 0) mbar_arrive(&eD[b]);
+                         });
+            }
         }
         if (!ok && lane == 0) {
             s_abort = 1;
@@ -284,11 +314,11 @@ __global__ void __launch_bounds__(kHpThreads, 1)
             int it = 0;
             const int end = (j1 - j0) * nk;
             for (; it < end; ++it) {
-                const int s = it % S, j = j0 + it / nk, e = j / nc;
+                const int s = it % S, j = j0 + it / nk;
                 ok = it < S || mbar_wait_ab(&eS[s], (unsigned)(it / S + 1) & 1u, abort);
                 if (!ok) break;
-                mbar_expect_tx(&bB[s], kHpB);
-                tma_sw(sB + s * kHpB, &tm, it % nk * kHpK, e * a.N + (j - e * nc) * kHpCols, &bB[s]);
+                mbar_expect_tx(&bB[s], B);
+                tma_sw(sB + s * B, &tm, it % nk * kHpK, j * Cols, &bB[s]);
             }
             if (!ok) {
                 s_abort = 1;
@@ -299,9 +329,8 @@ __global__ void __launch_bounds__(kHpThreads, 1)
         }
         __syncwarp();
     } else {
-        constexpr uint32_t ID = tc_idesc_f16(kHpRows, kHpCols, 0);
+        constexpr uint32_t ID = tc_idesc_f16(kHpRows, Cols, 0);
         const uint64_t da = tc_desc_sw(sA, 16, 1024), db = tc_desc_sw(sB, 16, 1024);
-        ok = __all_sync(kHpFull, mbar_wait_ab(bA, 0u, abort));
         int s = 0, it = 0;
         unsigned ph = 0;
         for (int j = j0; j < j1 && ok; ++j) {
@@ -309,13 +338,13 @@ __global__ void __launch_bounds__(kHpThreads, 1)
             // the buffer's last output is read
             ok = __all_sync(kHpFull, y < 2 || mbar_wait_ab(&eD[b], (unsigned)((y >> 1) + 1) & 1u, abort));
             for (int k = 0; k < nk && ok; ++k, ++it) {
-                ok = __all_sync(kHpFull, mbar_wait_ab(&bB[s], ph, abort));
+                ok = __all_sync(kHpFull, (y > 0 || mbar_wait_ab(&bA[k], 0u, abort)) && mbar_wait_ab(&bB[s], ph, abort));
                 if (!ok) break;
                 tc_fence_after();
 #pragma unroll
                 for (int c = 0; c < kHpK / 16; ++c)
-                    tc_mma_f16_w(taddr + kHpCols * b, da + (uint32_t)((k * kHpA + 32 * c) >> 4),
-                                 db + (uint32_t)((s * kHpB + 32 * c) >> 4), ID, k > 0 || c > 0);
+                    tc_mma_f16_w(taddr + Cols * b, da + (uint32_t)((k * kHpA + 32 * c) >> 4),
+                                 db + (uint32_t)((s * B + 32 * c) >> 4), ID, k > 0 || c > 0);
                 tc_commit_w(&eS[s]);
                 if (++s == S) {
                     s = 0;
@@ -335,7 +364,7 @@ __global__ void __launch_bounds__(kHpThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 0) tc_dealloc(taddr, 2 * kHpCols);
+    if (warp == 0) tc_dealloc(taddr, 2 * Cols);
 }
 
 kivi_status fail(kivi_status s, const char *msg) {
@@ -381,22 +410,32 @@ extern "C" kivi_status kivi_head_product(const void *x, const void *w, int b, in
     if (!kivi_device_info(&info)) return fail(KIVI_ERR_CUDA, "no status word on the current device");
     a.status = info.status;
     const bool mn = transposed != 0;
-    CUtensorMap tm;
-    cudaError_t e = mn ? make_sw_map(&tm, (const __half *)w, (long long)h * K, N, kHpK)
-                       : make_sw_map(&tm, (const __half *)w, (long long)h * N, K, kHpCols);
     const dim3 grid((unsigned)((rows + kHpRows - 1) / kHpRows), (unsigned)(N / kHpCols), (unsigned)h);
     const int cols = h * (N / kHpCols);   // column tiles of all heads
-    if (e == cudaSuccess && h_x == 1 && h > 1 && !mn && K <= kHsMaxK && (long long)grid.x * cols > info.sms) {
-        // a CTA an SM: as many groups of heads as leave every row tile one
+    const bool shared = h_x == 1 && h > 1 && !mn && K <= kHsMaxK && (long long)grid.x * cols > info.sms;
+    // (shared) a CTA an SM: as many groups of heads as leave every row tile one, and
+    // the tiles of C column tiles that each then has.  C = 2 where that leaves no CTA
+    // more columns, and several tiles (4096 tokens, 32 heads: 21.3 us for 22.7; 3000, 11
+    // heads, 256 deep, in tiles of one 8.8 for 9.8)
+    const auto share = [&](int C) {
+        const long long tiles = (cols + C - 1) / C;
         long long groups = info.sms / (long long)grid.x;
         if (groups < 1) groups = 1;
-        if (groups > cols) groups = cols;
-        const int per = (int)((cols + groups - 1) / groups);
-        static std::atomic<uint64_t> done;
-        e = kivi_allow_smem(head_product_shared_kernel, hs_smem(kHsMaxK), info.device, done);
+        if (groups > tiles) groups = tiles;
+        return (int)((tiles + groups - 1) / groups);
+    };
+    const int C = share(1) >= 4 && 2 * share(2) <= share(1) ? 2 : 1;
+    CUtensorMap tm;
+    cudaError_t e = mn ? make_sw_map(&tm, (const __half *)w, (long long)h * K, N, kHpK)
+                       : make_sw_map(&tm, (const __half *)w, (long long)h * N, K, shared ? C * kHpCols : kHpCols);
+    if (e == cudaSuccess && shared) {
+        const int tiles = (cols + C - 1) / C, per = share(C);
+        static std::atomic<uint64_t> done[2];
+        const auto kernel = C == 2 ? head_product_shared_kernel<2> : head_product_shared_kernel<1>;
+        e = kivi_allow_smem(kernel, hs_smem(C, kHsMaxK), info.device, done[C - 1]);
         if (e == cudaSuccess)
-            e = kivi_launch_after(head_product_shared_kernel, dim3(grid.x, (unsigned)((cols + per - 1) / per)), kHpThreads,
-                                  hs_smem(K), (cudaStream_t)stream, 1, a, tm, per);
+            e = kivi_launch_after(kernel, dim3(grid.x, (unsigned)((tiles + per - 1) / per)), kHpThreads, hs_smem(C, K),
+                                  (cudaStream_t)stream, 1, a, tm, per);
         return e == cudaSuccess ? KIVI_OK : fail(KIVI_ERR_CUDA, cudaGetErrorString(e));
     }
     const bool deep = K > 2 * kHpK && (long long)grid.x * grid.y * grid.z <= info.sms;

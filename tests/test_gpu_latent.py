@@ -151,6 +151,8 @@ def test_cache_holds_its_tokens(r, bits, G, R):
     (5, 128, 2, 256, 128, False, False),
     # rows of all heads alike over several heads a CTA: an odd number of heads, two column tiles, ragged ends
     (3, 61, 260, 512, 128, False, True), (1, 7, 5000, 192, 256, False, True), (1, 200, 127, 64, 128, False, True),
+    # ... in tiles of two column tiles, of which the last has one
+    (1, 24, 5000, 512, 128, False, True), (2, 23, 4999, 320, 128, False, True), (1, 8, 5000, 64, 384, False, True),
 ])
 def test_head_product(b, h, n, K_, N, transposed, shared):
     torch = pytest.importorskip("torch")
