@@ -121,5 +121,13 @@ cudaError_t kivi_launch_after(void (*kernel)(P...), dim3 grid, unsigned threads,
     return e == cudaSuccess ? cudaGetLastError() : e;
 }
 #ifdef __CUDACC__
-__device__ __forceinline__ void kivi_after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// EARLY: the kernel after this one may be placed as soon as all of this one's CTAs
+// run, not only as they end (1024 tokens of 16 heads over 8000: 125.6 -> 123.1 us).
+// Not after the attention over the cache and its join, whose successors would take
+// places that they need (8 drafts of 5 over 16k: 45.3 us for 42.6).
+template <bool EARLY = true>
+__device__ __forceinline__ void kivi_after_previous() {
+    if (EARLY) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
 #endif

@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    kivi_after_previous();
+    kivi_after_previous<false>();
     const uint32_t taddr = s_taddr;
     const volatile int *abort = &s_abort;
     bool ok = true;
@@ -685,7 +685,7 @@ __global__ void __launch_bounds__(256) latent_join_kernel(__half *__restrict__ O
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rr = warp / W, w = warp % W;
     const int RN = a.tile_rows, c = blockIdx.x / (RN / RB) + 1, r = blockIdx.x % (RN / RB) * RB + rr;
     const ChunkPos &p = a.cta[c];
-    kivi_after_previous();
+    kivi_after_previous<false>();
     if (p.o <= kLaLead) return;   // CTA c starts with a row tile of its own
     const int i = p.i, m = p.m;
     const long long first = p.u - p.o + kLaLead;                         // the unit of its first tile
