@@ -86,8 +86,10 @@ __global__ void __launch_bounds__(kLpThreads, 1)
     const int bh = a.b * a.h, blk = blockIdx.x / a.split, rank = blockIdx.x % a.split;
     const int pair = blk % bh, m = a.mt - 1 - blk / bh, i = pair / a.h;
     const int n = a.n[i], T = a.T[i], row0 = m * 2 * kLpRows;
-    kivi_after_previous();
-    if (row0 >= n) return;
+    if (row0 >= n) {
+        kivi_after_previous();
+        return;
+    }
     unsigned char *sQ = smem, *sK = sQ + 2 * kLpQ, *sV = sK + KS * kLpK;
     // counts 4 (a slot's softmax warps): P [slot][buffer], scores read [slot]; 2
     // (both slots): K tiles read; 1: the others
@@ -109,6 +111,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    kivi_after_previous();
     const uint32_t taddr = s_taddr;
     const volatile int *abort = &s_abort;
     bool ok = true;
