@@ -26,7 +26,7 @@ SOURCES = ["kivi_api.cu", "kivi_pack.cu", "kivi_decode.cu", "kivi_decode_d64.cu"
 HEADERS = ["kivi_internal.cuh", "kivi_decode_impl.cuh", "kivi_pack_impl.cuh", "kivi_append_impl.cuh",
            "kivi_mma.cuh", "kivi_tcgen05.cuh", "kivi_async.cuh", "kivi_unpack.cuh", "kivi_tma.cuh",
            "kivi_chunk.cuh", "kivi_chunk_tiles.cuh", "kivi_chunk_attn_impl.cuh", "kivi_chunk_few_impl.cuh",
-           "kivi_latent.cuh"]
+           "kivi_latent.cuh", "kivi_latent_places.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 # IEEE division and rounding stay exact: no --use_fast_math anywhere.
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",

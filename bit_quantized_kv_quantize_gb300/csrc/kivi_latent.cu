@@ -15,12 +15,11 @@ namespace {
 __device__ unsigned g_status;   // of the calls without a handle
 
 // ---------------------------------------------------------------------------
-// Append.  Warp x takes new token tau = T + x: straight to codes where R newer
-// ones follow, else into the ring.  The cached tokens that leave the window,
-// [Tq, Tq1) below T, are quantized from the ring: one whose place a new token
-// takes (it is a multiple of the ring's size before it; n may be larger than
-// that) by that token's warp, before it is overwritten; of the others the x-th by
-// warp x.  So no warp reads a place that another writes.
+// Append.  Warp x takes new token tau = T + x: to codes where R newer ones follow,
+// else into the ring as it is.  The cached tokens that leave the window, [Tq, Tq1)
+// below T, are quantized from the ring, each by one warp: that of the new token which
+// takes its place, before that is overwritten, or one that has no part in the place
+// otherwise (kivi_latent_places.h).
 //
 // Bound: memory (2 r + 128 bytes read a token, its codes or 16-bit rows
 // written), for single tokens the latency of one round trip.
@@ -106,28 +105,26 @@ __global__ void __launch_bounds__(32 * kApWarps)
     const int i = blockIdx.y, x = blockIdx.x * kApWarps + warp, n = a.n[i], T = a.T[i];
     kivi_after_previous();
     if (x >= n) return;
-    const int tau = T + x, Tq = lat_tq(T, g.R), Tq1 = lat_tq(T + n, g.R), W = g.ring * kLatTok;
+    const int tau = T + x;
+    const LatMoves mv = lat_moves(T, n, g.R, g.ring * kLatTok, x);
     const size_t src = (size_t)i * a.n_stride + x;
     LatRow<CH> row;
     row.load(C + src * g.r, lane);
     const uint32_t key = *reinterpret_cast<const uint32_t *>(Kr + src * kLatRope + 2 * lane);
     // token o to codes; in the block of Tq1 the ring keeps it, as they restore it
-    // (no new token's place: the ring is long enough)
     auto quantize = [&](int o, LatRow<CH> &r) {
         lat_quantize<CH, BITS>(g, dv.rec + lat_rec(g, i, o / kLatTok), o % kLatTok, r);
-        if (o / kLatTok == Tq1 / kLatTok) r.store_block(dv.ring + lat_ring(g, i, o / kLatTok), o % kLatTok, lane);
+        if (lat_restored(T, n, g.R, o)) r.store_block(dv.ring + lat_ring(g, i, o / kLatTok), o % kLatTok, lane);
     };
     auto leave = [&](int o) {   // cached token o leaves the window
         LatRow<CH> old;
         old.load_block(dv.ring + lat_ring(g, i, o / kLatTok), o % kLatTok, lane);
         quantize(o, old);
     };
-    const int own = Tq + x, first = max(T, Tq1);   // the x-th to leave; the first that goes into the ring
-    if (own < min(T, Tq1) && own + (first - own + W - 1) / W * W >= T + n) leave(own);
-    const int under = tau - (x + W) / W * W;       // the last token before T in tau's place
-    if (tau >= Tq1 && under >= Tq) leave(under);
-    if (tau >= Tq1) row.store_block(dv.ring + lat_ring(g, i, tau / kLatTok), tau % kLatTok, lane);
-    else quantize(tau, row);
+    if (mv.own >= 0) leave(mv.own);
+    if (mv.under >= 0) leave(mv.under);
+    if (mv.codes) quantize(tau, row);
+    else row.store_block(dv.ring + lat_ring(g, i, tau / kLatTok), tau % kLatTok, lane);
     *reinterpret_cast<uint32_t *>((char *)(dv.kr + lat_kr(g, i, tau / kLatTok)) + lat_at(lane >> 2, tau % kLatTok, kLatTok) +
                                   (lane & 3) * 4) = key;
 }

@@ -22,8 +22,8 @@
 
 #include "kivi_chunk.cuh"
 #include "kivi_internal.cuh"
+#include "kivi_latent_places.h"
 
-constexpr int kLatTok = 128;    // tokens of a block
 constexpr int kLatRope = 64;    // channels of the rotary key
 constexpr int kLatHead = 128;   // channels of a head's other keys, and of its values
 
@@ -56,8 +56,6 @@ __host__ __device__ __forceinline__ size_t lat_kr(const LatentGeom &g, int i, in
 __host__ __device__ __forceinline__ unsigned lat_at(int c, int t, int rows) {
     return (unsigned)((c >> 3) * rows * 128 + t * 128 + (((c ^ t) & 7) << 4));
 }
-// quantized tokens of T
-__host__ __device__ __forceinline__ int lat_tq(int T, int R) { return T > R ? T - R : 0; }
 
 // n[i] tokens at positions T[i].. (counts from the host mirror)
 struct LatentTokens {
