@@ -16,7 +16,7 @@
 //            one as it is.  Token tau of the window is in the ring's block
 //            (tau / 128) mod (ring blocks).  The block of Tq holds its quantized
 //            tokens too, as their codes restore them: every block from Tq / 128 on
-//            is there whole.
+//            is there whole, the places behind the last token zero.
 #pragma once
 #include <atomic>
 
@@ -64,7 +64,7 @@ struct LatentTokens {
 };
 
 cudaError_t kivi_launch_latent_append(const LatentGeom &g, const LatentDev &dv, const __half *C, const __half *Kr,
-                                      const LatentTokens &a, int maxn, cudaStream_t st);
+                                      const LatentTokens &a, cudaStream_t st);
 // a: T and n[i] new tokens behind them (of Cn, Krn, [b][a.n_stride]); into [b][stride]
 cudaError_t kivi_launch_latent_rows(const LatentGeom &g, const LatentDev &dv, const __half *Cn, const __half *Krn,
                                     __half *C, __half *Kr, const LatentTokens &a, int stride, int maxS, cudaStream_t st);

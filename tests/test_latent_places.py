@@ -1,7 +1,7 @@
 """Which warp of a latent cache's append reads and writes which place of the ring
 (csrc/kivi_latent_places.h, the kernel's own lines, compiled for the host): a place
 is one warp's, and every token that leaves the window is quantized once, from its
-own place."""
+own place; the places of a new block that hold no tokens yet are zeroed."""
 import ctypes
 import os
 import random
@@ -12,13 +12,15 @@ import pytest
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "bit_quantized_kv_quantize_gb300", "csrc")
 SHIM = """
 #include "kivi_latent_places.h"
-extern "C" void moves(int T, int n, int R, int W, int *out) {   // [n][3]
-    for (int x = 0; x < n; ++x) {
+extern "C" int moves(int T, int n, int R, int W, int *out) {   // [warps][3]
+    const int warps = lat_end(T, n) - T;
+    for (int x = 0; x < warps; ++x) {
         const LatMoves m = lat_moves(T, n, R, W, x);
         out[3 * x] = m.own;
         out[3 * x + 1] = m.under;
         out[3 * x + 2] = m.codes;
     }
+    return warps;
 }
 extern "C" int restored(int T, int n, int R, int o) { return lat_restored(T, n, R, o); }
 """
@@ -41,8 +43,8 @@ def _walk(lib, T, n, R):
     """The append of n tokens to T: who touches each place, what is quantized from
     where, and the ring as it is afterwards (place -> token)."""
     W = _ring(R)
-    out = (ctypes.c_int * (3 * n))()
-    lib.moves(T, n, R, W, out)
+    out = (ctypes.c_int * (3 * (n + 128)))()
+    warps = lib.moves(T, n, R, W, out)
     Tq, Tq1, B = max(0, T - R), max(0, T + n - R), max(0, T + n - R) // 128 * 128
     reads, writes, coded = {}, {}, []
     ring = {o % W: o for o in range(Tq // 128 * 128, T)}
@@ -59,7 +61,7 @@ def _walk(lib, T, n, R):
         writes.setdefault(o % W, set()).add(x)
         assert stored.setdefault(o % W, o) == o       # (no two tokens into one place)
 
-    for x in range(n):
+    for x in range(warps):
         own, under, codes = out[3 * x:3 * x + 3]
         if own >= 0:
             leave(x, own)
@@ -76,6 +78,8 @@ def _walk(lib, T, n, R):
     assert sorted(coded) == list(range(Tq, Tq1)), f"T {T}, n {n}, R {R}: quantized {len(coded)} of {Tq1 - Tq}"
     ring.update(stored)
     assert all(ring[o % W] == o for o in range(B, T + n)), f"T {T}, n {n}, R {R}: a block is not whole"
+    last = (T + n - 1) // 128 * 128                   # (a block begun before: by the append that did)
+    assert all(stored.get(f % W) == f for f in range(T + n, last + 128)) == (last >= T or (T + n) % 128 == 0)
 
 
 @pytest.mark.parametrize("R", [64, 128, 192, 256, 1024])
