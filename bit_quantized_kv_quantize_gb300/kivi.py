@@ -778,7 +778,7 @@ class LatentCache:
                                     _rows16(out, shape, self._dev, "out"), _stream(stream)))
         return out
 
-    def _form(self, form, cnt, T, h):
+    def _form(self, form, cnt, T, h, ns):
         """Whether attn forms every head's keys and values (expanded) rather than
         absorbing them, and the longest sequence with its new tokens.
 
@@ -788,12 +788,15 @@ class LatentCache:
         has a row tile of 256 queries of a head, or a share of one, with 3 to join
         them.  16 heads over 8000 tokens: 64 queries 64 and 76, 128 108 and 77, 512 305
         and 96; 128 heads over 4000: 64 queries 184 and 223, 256 636 and 240.
-        Expanded from 16 queries on, where keys and values take up to 4 GB."""
+        Expanded from 16 queries on, where keys and values take up to 4 GB; and
+        whatever they take where the absorbed attention refuses the call."""
         S = [t + n if n > 0 else 0 for t, n in zip(T, cnt)]
         if form not in (None, "absorbed", "expanded"):
             raise ValueError('form must be None, "absorbed" or "expanded"')
         if form is not None:
             return form == "expanded", max(S)
+        if not self._absorbs(h, ns):
+            return True, max(S)
         if max(cnt) < 16 or 4 * self.b * max(S) * h * LATENT_HEAD > 1 << 32:
             return False, max(S)
         absorbed = 35 + h * sum(n * s for n, s in zip(cnt, S)) * (self.r + 64) / 144e6
@@ -801,6 +804,11 @@ class LatentCache:
         c = max(1, min(6, self._sms * 9 // 10 // rt))
         expanded = 10 + h * sum(S) * (self.r + 256) / 2.15e6 + -(-rt // self._sms) * max(S) / (80 * c) + 3 * (c > 1)
         return expanded < absorbed, max(S)
+
+    @staticmethod
+    def _absorbs(h, ns):
+        """Whether kivi_latent_attn takes h heads of a stride of ns tokens."""
+        return h <= 128 and h * ns < 1 << 24
 
     def _expanded(self, dims, ptrs, qrp, krp, cnt, T, S, scale, stream, st):
         (b, h, ns, r), (qnp, _, cp, _, wkp, wvp, op) = dims, ptrs
@@ -819,9 +827,9 @@ class LatentCache:
 
     def _attn(self, dims, ptrs, qrp, krp, cnt, scale, form, stream, st):
         (b, h, ns, r), (qnp, _, cp, _, wkp, wvp, op) = dims, ptrs
-        if form is not None or max(cnt) >= 16:
+        if form is not None or max(cnt) >= 16 or not self._absorbs(h, ns):
             T = self._lengths()
-            expanded, S = self._form(form, cnt, T, h)
+            expanded, S = self._form(form, cnt, T, h, ns)
             if expanded:
                 return self._expanded(dims, ptrs, qrp, krp, cnt, T, S, scale, stream, st)
         keep, (ql, ol) = _space(stream, self._device, b * h * ns * r, b * h * ns * r)   # (rows past n are not read)
@@ -838,9 +846,10 @@ class LatentCache:
     def attn(self, qn, qr, c, kr, n, wk, wv, scale=None, out=None, stream=None, form=None):
         """Latent attention of n new tokens of each sequence (an integer or b of
         them) over the cache and over themselves, absorbed or expanded (form;
-        default the faster, which for long chunks is the latter): qn CUDA fp16 [b, h, ns,
-        128], qr [b, h, ns, 64], c [b, ns, r], kr [b, ns, 64], wk and wv [h, 128,
-        r] -> out [b, h, ns, 128] (rows past n untouched, zero in a new tensor).
+        default the faster, which for long chunks is the latter, and expanded where
+        the other is refused: more than 128 heads, h ns of 2^24 and more): qn CUDA fp16
+        [b, h, ns, 128], qr [b, h, ns, 64], c [b, ns, r], kr [b, ns, 64], wk and wv [h,
+        128, r] -> out [b, h, ns, 128] (rows past n untouched, zero in a new tensor).
         Queries and keys rotated.  Does not append (append, extend)."""
         self._here()
         dims, ptrs, out = self._args(qn, qr, c, kr, wk, wv, out, stream)
