@@ -374,10 +374,8 @@ kivi_status fail(kivi_status s, const char *msg) {
 
 }  // namespace
 
-extern "C" kivi_status kivi_head_product(const void *x, const void *w, int b, int h_x, int h, int n_stride,
-                                         const int32_t *n, int K, int N, int transposed, void *out,
-                                         kivi_stream_t stream) {
-    kivi_set_last_error("");
+kivi_status kivi_head_product_to(unsigned *status, const void *x, const void *w, int b, int h_x, int h, int n_stride,
+                                 const int32_t *n, int K, int N, int transposed, void *out, kivi_stream_t stream) {
     if (b < 1 || h < 1 || n_stride < 0 || K < 1 || N < 1) return fail(KIVI_ERR_INVALID_ARG, "sizes must be positive");
     if (h_x != 1 && h_x != h) return fail(KIVI_ERR_INVALID_ARG, "h_x must be 1 or h");
     if (b > KIVI_MAX_BATCH) return fail(KIVI_ERR_UNSUPPORTED, "b above 1024");
@@ -408,7 +406,7 @@ extern "C" kivi_status kivi_head_product(const void *x, const void *w, int b, in
     a.N = N;
     KiviDeviceInfo info;
     if (!kivi_device_info(&info)) return fail(KIVI_ERR_CUDA, "no status word on the current device");
-    a.status = info.status;
+    a.status = status ? status : info.status;
     const bool mn = transposed != 0;
     const dim3 grid((unsigned)((rows + kHpRows - 1) / kHpRows), (unsigned)(N / kHpCols), (unsigned)h);
     const int cols = h * (N / kHpCols);   // column tiles of all heads
@@ -447,4 +445,11 @@ extern "C" kivi_status kivi_head_product(const void *x, const void *w, int b, in
     if (e != cudaSuccess) return fail(KIVI_ERR_CUDA, cudaGetErrorString(e));
     e = kivi_launch_after(kernel, grid, kHpThreads, smem, (cudaStream_t)stream, 1, a, tm);
     return e == cudaSuccess ? KIVI_OK : fail(KIVI_ERR_CUDA, cudaGetErrorString(e));
+}
+
+extern "C" kivi_status kivi_head_product(const void *x, const void *w, int b, int h_x, int h, int n_stride,
+                                         const int32_t *n, int K, int N, int transposed, void *out,
+                                         kivi_stream_t stream) {
+    kivi_set_last_error("");
+    return kivi_head_product_to(nullptr, x, w, b, h_x, h, n_stride, n, K, N, transposed, out, stream);
 }

@@ -518,6 +518,27 @@ kivi_status kivi_latent_rows(kivi_latent_t c, const void *C, const void *Kr, con
     return maxn == 0 ? KIVI_OK : rows(c, C, Kr, n, n_stride, C_out, Kr_out, s_stride, "latent_rows", (cudaStream_t)stream);
 }
 
+kivi_status kivi_latent_product(kivi_latent_t c, const void *x, const void *w, int h_x, int h, int n_stride,
+                                const int32_t *n, int K, int N, int transposed, void *out, kivi_stream_t stream) {
+    kivi_set_last_error("");
+    kivi_status s = check(c, true);
+    if (s != KIVI_OK) return s;
+    s = kivi_head_product_to(c->dv.status, x, w, c->g.b, h_x, h, n_stride, n, K, N, transposed, out, stream);
+    c->poisoned |= s == KIVI_ERR_CUDA;
+    return s;
+}
+
+kivi_status kivi_latent_expanded(kivi_latent_t c, const void *q, const void *q_rope, const void *K, const void *Kr,
+                                 const void *V, int h, const int32_t *T, const int32_t *n, int n_stride, int s_stride,
+                                 float scale, void *out, kivi_stream_t stream) {
+    kivi_set_last_error("");
+    kivi_status s = check(c, true);
+    if (s != KIVI_OK) return s;
+    s = kivi_latent_expanded_to(c->dv.status, q, q_rope, K, Kr, V, c->g.b, h, T, n, n_stride, s_stride, scale, out, stream);
+    c->poisoned |= s == KIVI_ERR_CUDA;
+    return s;
+}
+
 kivi_status kivi_latent_check(kivi_latent_t c, uint32_t *flags, kivi_stream_t stream) {
     kivi_set_last_error("");
     kivi_status s = check(c, true);

@@ -20,6 +20,7 @@
 #pragma once
 #include <atomic>
 
+#include "../../include/kivi.h"
 #include "kivi_chunk.cuh"
 #include "kivi_internal.cuh"
 #include "kivi_latent_places.h"
@@ -84,6 +85,13 @@ struct KiviDeviceInfo {
     unsigned *status;
 };
 bool kivi_device_info(KiviDeviceInfo *info);
+// kivi_head_product, and kivi_latent_expanded_attn (T null: prompts), whose waits that
+// run out show in *status (device; null: the device's word for calls without a handle)
+kivi_status kivi_head_product_to(unsigned *status, const void *x, const void *w, int b, int h_x, int h, int n_stride,
+                                 const int32_t *n, int K, int N, int transposed, void *out, kivi_stream_t stream);
+kivi_status kivi_latent_expanded_to(unsigned *status, const void *q, const void *q_rope, const void *K, const void *Kr,
+                                    const void *V, int b, int h, const int32_t *T, const int32_t *n, int n_stride,
+                                    int s_stride, float scale, void *out, kivi_stream_t stream);
 // Shared memory that a kernel may take, set once a device (done: a bit each).
 template <typename K>
 cudaError_t kivi_allow_smem(K *kernel, size_t bytes, int device, std::atomic<uint64_t> &done) {

@@ -464,10 +464,12 @@ kivi_status fail(kivi_status s, const char *msg) {
     return s;
 }
 
-// Both entry points: n[i] queries behind T[i] tokens (T null: none).
-kivi_status expanded(const void *q, const void *q_rope, const void *K, const void *Kr, const void *V, int b, int h,
-                     const int32_t *T, const int32_t *n, int n_stride, int s_stride, float scale, void *out,
-                     kivi_stream_t stream) {
+}  // namespace
+
+// n[i] queries behind T[i] tokens (T null: none)
+kivi_status kivi_latent_expanded_to(unsigned *status, const void *q, const void *q_rope, const void *K, const void *Kr,
+                                    const void *V, int b, int h, const int32_t *T, const int32_t *n, int n_stride,
+                                    int s_stride, float scale, void *out, kivi_stream_t stream) {
     if (b < 1 || h < 1 || n_stride < 0 || s_stride < 0) return fail(KIVI_ERR_INVALID_ARG, "sizes must be positive");
     if (b > KIVI_MAX_BATCH) return fail(KIVI_ERR_UNSUPPORTED, "b above 1024");
     if (h > 1024) return fail(KIVI_ERR_UNSUPPORTED, "more than 1024 heads");
@@ -507,7 +509,7 @@ kivi_status expanded(const void *q, const void *q_rope, const void *K, const voi
     if ((long long)a.mt * b * h > INT_MAX / kLpMaxSplit) return fail(KIVI_ERR_UNSUPPORTED, "more than 2^28 row tiles");
     KiviDeviceInfo info;
     if (!kivi_device_info(&info)) return fail(KIVI_ERR_CUDA, "no status word on the current device");
-    a.status = info.status;
+    a.status = status ? status : info.status;
     const long long rows = (long long)b * h * n_stride, keys = (long long)b * h * s_stride;
     CUtensorMap tq, tqr, tk, tkr, tv;
     cudaError_t e = make_sw_map(&tq, (const __half *)q, rows, kLatHead, kLpRows);
@@ -524,13 +526,11 @@ kivi_status expanded(const void *q, const void *q_rope, const void *K, const voi
     return e == cudaSuccess ? KIVI_OK : fail(KIVI_ERR_CUDA, cudaGetErrorString(e));
 }
 
-}  // namespace
-
 extern "C" kivi_status kivi_latent_prompt_attn(const void *q, const void *q_rope, const void *K, const void *Kr,
                                                const void *V, int b, int h, const int32_t *t, int t_stride, float scale,
                                                void *out, kivi_stream_t stream) {
     kivi_set_last_error("");
-    return expanded(q, q_rope, K, Kr, V, b, h, nullptr, t, t_stride, t_stride, scale, out, stream);
+    return kivi_latent_expanded_to(nullptr, q, q_rope, K, Kr, V, b, h, nullptr, t, t_stride, t_stride, scale, out, stream);
 }
 
 extern "C" kivi_status kivi_latent_expanded_attn(const void *q, const void *q_rope, const void *K, const void *Kr,
@@ -539,5 +539,5 @@ extern "C" kivi_status kivi_latent_expanded_attn(const void *q, const void *q_ro
                                                  kivi_stream_t stream) {
     kivi_set_last_error("");
     if (!T) return fail(KIVI_ERR_INVALID_ARG, "T is null");
-    return expanded(q, q_rope, K, Kr, V, b, h, T, n, n_stride, s_stride, scale, out, stream);
+    return kivi_latent_expanded_to(nullptr, q, q_rope, K, Kr, V, b, h, T, n, n_stride, s_stride, scale, out, stream);
 }

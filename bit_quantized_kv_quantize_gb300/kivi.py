@@ -31,7 +31,8 @@ EXPORTS = ["kivi_cache_create", "kivi_cache_destroy", "kivi_prefill", "kivi_appe
            "kivi_decode_attn_window", "kivi_chunk_attn", "kivi_append_chunk", "kivi_rope",
            "kivi_rope_axes", "kivi_verify", "kivi_latent_create", "kivi_latent_destroy", "kivi_latent_prefill",
            "kivi_latent_append", "kivi_latent_attn", "kivi_latent_lengths", "kivi_latent_restore",
-           "kivi_latent_check", "kivi_latent_rows", "kivi_latent_expanded_attn", "kivi_head_product", "kivi_latent_prompt_attn", "kivi_device_check"]
+           "kivi_latent_check", "kivi_latent_rows", "kivi_latent_expanded_attn", "kivi_head_product",
+           "kivi_latent_prompt_attn", "kivi_latent_product", "kivi_latent_expanded", "kivi_device_check"]
 
 
 class KiviError(RuntimeError):
@@ -75,6 +76,8 @@ def _load():
     L.kivi_latent_prompt_attn.argtypes = [vp] * 5 + [i32, i32, vp, i32, ctypes.c_float, vp, vp]
     L.kivi_latent_rows.argtypes = [vp, vp, vp, vp, i32, vp, vp, i32, vp]
     L.kivi_latent_expanded_attn.argtypes = [vp] * 5 + [i32, i32, vp, vp, i32, i32, ctypes.c_float, vp, vp]
+    L.kivi_latent_product.argtypes = [vp, vp, vp, i32, i32, i32, vp, i32, i32, i32, vp, vp]
+    L.kivi_latent_expanded.argtypes = [vp] * 6 + [i32, vp, vp, i32, i32, ctypes.c_float, vp, vp]
     L.kivi_device_check.argtypes = [ctypes.POINTER(ctypes.c_uint32), vp]
     L.kivi_plan_preview.argtypes = [i32] * 9 + [vp, vp, vp, i32, vp]
     L.kivi_cache_lengths.argtypes = [vp, vp, vp, vp]
@@ -604,7 +607,7 @@ def verify(p, q, draft, u, n=None, tokens=None, accepted=None, stream=None):
 
 def device_check(stream=None) -> int:
     """The current device's status word of the calls without a handle
-    (kivi_device_check)."""
+    (kivi_device_check): head_product, latent_prompt_attn."""
     f = ctypes.c_uint32(0)
     _check(lib.kivi_device_check(ctypes.byref(f), _stream(stream)))
     return int(f.value)
@@ -690,16 +693,13 @@ def latent_prompt_attn(qn, qr, c, kr, t, wk, wv, scale=None, out=None, stream=No
         with torch.cuda.device(dev):
             return latent_prompt_attn(qn, qr, c, kr, t, wk, wv, scale, out, stream)
     dims, ptrs, out = _latent_args(qn, qr, c, kr, wk, wv, out, stream, dev)
-    _prompt(dims, ptrs, _counts(t, dims[0], "t"), _latent_scale(scale), stream, _stream(stream), qn.device)
-    return out
-
-
-def _prompt(dims, ptrs, cnt, scale, stream, st, device):
     (b, h, ts, r), (qnp, qrp, cp, krp, wkp, wvp, op) = dims, ptrs
-    keep, (K, V) = _space(stream, device, *[b * h * ts * LATENT_HEAD] * 2)   # (rows past t are not read)
+    cnt, scale, st = _counts(t, b, "t"), _latent_scale(scale), _stream(stream)
+    keep, (K, V) = _space(stream, qn.device, *[b * h * ts * LATENT_HEAD] * 2)   # (rows past t are not read)
     for w, x in ((wkp, K), (wvp, V)):
         _check(lib.kivi_head_product(cp, w, b, 1, h, ts, _addr(cnt), r, LATENT_HEAD, 0, x, st))
     _check(lib.kivi_latent_prompt_attn(qnp, qrp, K, krp, V, b, h, _addr(cnt), ts, scale, op, st))
+    return out
 
 
 class LatentCache:
@@ -810,15 +810,21 @@ class LatentCache:
         """Whether kivi_latent_attn takes h heads of a stride of ns tokens."""
         return h <= 128 and h * ns < 1 << 24
 
+    def _expand(self, dims, ptrs, qrp, c, kr, K, V, T, cnt, tok, S, scale, st):
+        """Every head's keys K and values V of tok tokens c, and the attention to them."""
+        (_, h, ns, r), (qnp, _, _, _, wkp, wvp, op) = dims, ptrs
+        for w, x in ((wkp, K), (wvp, V)):
+            _check(lib.kivi_latent_product(self._h, c, w, 1, h, S, _addr(tok), r, LATENT_HEAD, 0, x, st))
+        _check(lib.kivi_latent_expanded(self._h, qnp, qrp, K, kr, V, h, None if T is None else _addr(T), _addr(cnt), ns, S,
+                                        scale, op, st))
+
     def _expanded(self, dims, ptrs, qrp, krp, cnt, T, S, scale, stream, st):
-        (b, h, ns, r), (qnp, _, cp, _, wkp, wvp, op) = dims, ptrs
+        (b, h, ns, r), cp = dims, ptrs[2]
         keep, (c_all, kr_all, K, V) = _space(stream, self._device, b * S * r, b * S * LATENT_ROPE,
                                              *[b * h * S * LATENT_HEAD] * 2)   # (rows past a sequence's tokens are not read)
         _check(lib.kivi_latent_rows(self._h, cp, krp, _addr(cnt), ns, c_all, kr_all, S, st))
         tok = array.array("i", [t + n if n else 0 for t, n in zip(T, cnt)])
-        for w, x in ((wkp, K), (wvp, V)):
-            _check(lib.kivi_head_product(c_all, w, b, 1, h, S, _addr(tok), r, LATENT_HEAD, 0, x, st))
-        _check(lib.kivi_latent_expanded_attn(qnp, qrp, K, kr_all, V, b, h, _addr(T), _addr(cnt), ns, S, scale, op, st))
+        self._expand(dims, ptrs, qrp, c_all, kr_all, K, V, T, cnt, tok, S, scale, st)
 
     def _lengths(self):
         T = array.array("i", bytes(4 * self.b))
@@ -833,9 +839,9 @@ class LatentCache:
             if expanded:
                 return self._expanded(dims, ptrs, qrp, krp, cnt, T, S, scale, stream, st)
         keep, (ql, ol) = _space(stream, self._device, b * h * ns * r, b * h * ns * r)   # (rows past n are not read)
-        _check(lib.kivi_head_product(qnp, wkp, b, h, h, ns, _addr(cnt), LATENT_HEAD, r, 1, ql, st))
+        _check(lib.kivi_latent_product(self._h, qnp, wkp, h, h, ns, _addr(cnt), LATENT_HEAD, r, 1, ql, st))
         _check(lib.kivi_latent_attn(self._h, ql, qrp, cp, krp, _addr(cnt), ns, h, scale, ol, st))
-        _check(lib.kivi_head_product(ol, wvp, b, h, h, ns, _addr(cnt), r, LATENT_HEAD, 0, op, st))
+        _check(lib.kivi_latent_product(self._h, ol, wvp, h, h, ns, _addr(cnt), r, LATENT_HEAD, 0, op, st))
 
     def _args(self, qn, qr, c, kr, wk, wv, out, stream):
         dims, ptrs, out = _latent_args(qn, qr, c, kr, wk, wv, out, stream, self._dev)
@@ -863,7 +869,10 @@ class LatentCache:
         cnt, st = _counts(t, self.b, "t"), _stream(stream)
         if max(cnt) > self.max_tokens:
             raise CapacityError(3, "a prompt exceeds max_tokens")
-        _prompt(dims, ptrs, cnt, _latent_scale(scale), stream, st, self._device)   # (refuses before the cache changes)
+        b, h, ts, _ = dims
+        keep, (K, V) = _space(stream, self._device, *[b * h * ts * LATENT_HEAD] * 2)   # (rows past t are not read)
+        # (refuses before the cache changes)
+        self._expand(dims, ptrs, ptrs[1], ptrs[2], ptrs[3], K, V, None, cnt, cnt, ts, _latent_scale(scale), st)
         _check(lib.kivi_latent_prefill(self._h, ptrs[2], ptrs[3], _addr(cnt), dims[2], st))
         return out
 
@@ -913,6 +922,7 @@ class LatentCache:
         return c, kr
 
     def check(self, stream=None) -> int:
+        """The status word of every call of this cache's methods (kivi_latent_check)."""
         f = ctypes.c_uint32(0)
         _check(lib.kivi_latent_check(self._h, ctypes.byref(f), _stream(stream)))
         return int(f.value)

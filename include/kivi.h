@@ -238,6 +238,7 @@ kivi_status kivi_verify(const void *p, const void *q, int bytes, const int32_t *
  *     out = kivi_head_product(ol, Wv);
  *   expanded (whole prompts): K, V = kivi_head_product(c of all heads, Wk, Wv),
  *     kivi_latent_prompt_attn(qn, qr, K, kr, V), and kivi_latent_prefill.
+ * (Or kivi_latent_product and kivi_latent_expanded, which kivi_latent_check covers.)
  * Handles are as kivi_cache_t: not thread-safe, no two calls on one at once on the
  * GPU, poisoned by a CUDA error; the cache's device must be current
  * (KIVI_ERR_INVALID_ARG).
@@ -327,6 +328,16 @@ kivi_status kivi_latent_prompt_attn(const void *q, const void *q_rope, const voi
 kivi_status kivi_latent_expanded_attn(const void *q, const void *q_rope, const void *K, const void *Kr, const void *V,
                                       int b, int h, const int32_t *T, const int32_t *n, int n_stride, int s_stride,
                                       float scale, void *out, kivi_stream_t stream);
+
+/* kivi_head_product and kivi_latent_expanded_attn (T NULL: none, as
+ * kivi_latent_prompt_attn with t = n) for the b sequences of a cache: the same, but a
+ * wait that runs out shows in kivi_latent_check of the cache, not in kivi_device_check,
+ * and the cache's device must be current. */
+kivi_status kivi_latent_product(kivi_latent_t c, const void *x, const void *w, int h_x, int h, int n_stride,
+                                const int32_t *n, int K, int N, int transposed, void *out, kivi_stream_t stream);
+kivi_status kivi_latent_expanded(kivi_latent_t c, const void *q, const void *q_rope, const void *K, const void *Kr,
+                                 const void *V, int h, const int32_t *T, const int32_t *n, int n_stride, int s_stride,
+                                 float scale, void *out, kivi_stream_t stream);
 
 /* As kivi_cache_check, for the current device's calls that have no handle
  * (kivi_head_product, kivi_latent_prompt_attn, kivi_latent_expanded_attn). */

@@ -69,3 +69,42 @@ def test_the_form_that_takes_the_call(cache):
     assert _absorbed(attn(128, 40, ns=(1 << 17) - 1)) and _expanded(attn(128, 40, ns=1 << 17))
     assert _expanded(attn(128, 1, ns=1 << 17))
     assert _absorbed(attn(129, 1, form="absorbed"))   # (asked for: the library refuses it)
+
+
+def test_every_call_of_a_cache_reports_to_it(cache):
+    """Products and expanded attention too: kivi_latent_check tells of a wait that ran
+    out in any of them."""
+    c, lib, attn = cache
+    import torch
+    c._h = object()
+    rows = lambda *s: torch.empty(s, device="meta", dtype=torch.float16)   # noqa: E731
+    w = rows(8, 128, 512)
+
+    def all_of_it(names):
+        assert all(a[0] is c._h for _, a in lib.calls), [n for n, a in lib.calls if a[0] is not c._h]
+        return names
+
+    for form in ("absorbed", "expanded"):
+        names = all_of_it(attn(8, 20, form=form))
+        assert len(names) == (3 if form == "absorbed" else 4)
+    lib.calls.clear()
+    q = rows(1, 8, 30, 128)
+    c.prefill_attn(q, rows(1, 8, 30, 64), rows(1, 30, 512), rows(1, 30, 64), 30, w, w, out=q)
+    assert len(all_of_it(lib.names())) == 4
+    lib.calls.clear()
+    c.extend(q, rows(1, 8, 30, 64), rows(1, 30, 512), rows(1, 30, 64), 30, w, w, out=q)
+    assert all_of_it(lib.names())[-1] == "kivi_latent_append"
+
+
+def test_a_caches_products_and_expanded_attention_refuse():
+    import ctypes
+
+    import numpy as np
+    from bit_quantized_kv_quantize_gb300 import kivi as K
+    p, n = ctypes.c_void_p(4096), np.array([1], np.int32)   # never dereferenced: every call below is refused
+    bogus = ctypes.cast(ctypes.create_string_buffer(64), ctypes.c_void_p)
+    for h in (None, bogus):
+        assert K.lib.kivi_latent_product(h, p, p, 1, 4, 1, n.ctypes.data, 128, 128, 0, p, None) == 1
+        for T in (None, n.ctypes.data):
+            assert K.lib.kivi_latent_expanded(h, p, p, p, p, p, 4, T, n.ctypes.data, 1, 2, 1.0, p, None) == 1
+        assert b"latent cache handle" in K.lib.kivi_last_error()
