@@ -475,6 +475,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
             for (int y = max(0, parts - KS * NM); y < parts; ++y)
                 mbar_wait(&bR[y % (KS * NM)], (unsigned)(y / (KS * NM)) & 1u);
             for (int y = max(0, cnt - KS); y < cnt; ++y) mbar_wait(&bK[y % KS], (unsigned)(y / KS) & 1u);
+            if (meets > 0) mbar_wait(bX, (unsigned)(meets - 1) & 1u);   // (the one whose wait was given up)
         }
         __syncwarp();
     } else {
