@@ -684,7 +684,7 @@ def latent_prompt_attn(qn, qr, c, kr, t, wk, wv, scale=None, out=None, stream=No
     CUDA fp16 [b, h, ts, 128], qr [b, h, ts, 64] (rotated), c [b, ts, r], kr [b,
     ts, 64] (rotated), wk and wv [h, 128, r], t tokens of each sequence -> out [b,
     h, ts, 128] (rows past t untouched, zero in a new tensor).  scale: default 1 /
-    sqrt(192)."""
+    sqrt(192).  Keys and values are fp16: wk c and wv c must stay below 65504."""
     import torch
     if not isinstance(qn, torch.Tensor) or not qn.is_cuda:
         raise TypeError("qn must be a CUDA float16 tensor")
@@ -856,7 +856,10 @@ class LatentCache:
         the other is refused: more than 128 heads, h ns of 2^24 and more): qn CUDA fp16
         [b, h, ns, 128], qr [b, h, ns, 64], c [b, ns, r], kr [b, ns, 64], wk and wv [h,
         128, r] -> out [b, h, ns, 128] (rows past n untouched, zero in a new tensor).
-        Queries and keys rotated.  Does not append (append, extend)."""
+        Queries and keys rotated.  Does not append (append, extend).
+
+        What lies between the products is fp16: wk^T qn (absorbed) or wk c and wv c of
+        every token (expanded) must stay below 65504, or out is not finite."""
         self._here()
         dims, ptrs, out = self._args(qn, qr, c, kr, wk, wv, out, stream)
         self._attn(dims, ptrs, ptrs[1], ptrs[3], _counts(n, self.b), _latent_scale(scale), form, stream, _stream(stream))

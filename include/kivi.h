@@ -239,6 +239,8 @@ kivi_status kivi_verify(const void *p, const void *q, int bytes, const int32_t *
  *   expanded (whole prompts): K, V = kivi_head_product(c of all heads, Wk, Wv),
  *     kivi_latent_prompt_attn(qn, qr, K, kr, V), and kivi_latent_prefill.
  * (Or kivi_latent_product and kivi_latent_expanded, which kivi_latent_check covers.)
+ * ql, ol, K and V are fp16: a query's Wk_e^T qn, or a token's Wk_e c_s and Wv_e c_s,
+ * must stay below 65504, or the output is not finite (no flag tells).
  * Handles are as kivi_cache_t: not thread-safe, no two calls on one at once on the
  * GPU, poisoned by a CUDA error; the cache's device must be current
  * (KIVI_ERR_INVALID_ARG).
@@ -302,10 +304,10 @@ kivi_status kivi_latent_check(kivi_latent_t c, uint32_t *flags, kivi_stream_t st
  * tokens s < n[i] (n: HOST array of b int32):
  *   out[i][e][s] = W_e x[i][e or 0][s],
  * w fp16 [h][N][K], or with transposed != 0 [h][K][N] (device, all 16-byte
- * aligned).  Sums in fp32, rounded once.  Rows past n[i] are neither read nor
- * written; out overlaps no input.  One launch on the current device, no state.  K a
- * multiple of 64, N of 128, up to 16384; h <= 1024, b <= 1024, up to 2^30 tokens in
- * all (KIVI_ERR_UNSUPPORTED otherwise). */
+ * aligned).  Sums in fp32, rounded once (beyond 65504: infinite).  Rows past n[i] are
+ * neither read nor written; out overlaps no input.  One launch on the current device, no
+ * state.  K a multiple of 64, N of 128, up to 16384; h <= 1024, b <= 1024, up to 2^30
+ * tokens in all (KIVI_ERR_UNSUPPORTED otherwise). */
 kivi_status kivi_head_product(const void *x, const void *w, int b, int h_x, int h, int n_stride, const int32_t *n,
                               int K, int N, int transposed, void *out, kivi_stream_t stream);
 
