@@ -68,14 +68,14 @@ constexpr float kLaUnset = 1e30f;   // s_ref of a row that has seen nothing
 __device__ __forceinline__ bool la_any(bool v) {
     unsigned r;
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 1, 512, p;\n\t"
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 1, %2, p;\n\t"
         "selp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(r)
-        : "r"(v ? 1u : 0u)
+        : "r"(v ? 1u : 0u), "n"(32 * kLaWork)
         : "memory");
     return r != 0;
 }
-__device__ __forceinline__ void la_sync() { asm volatile("barrier.cta.sync 1, 512;" ::: "memory"); }
+__device__ __forceinline__ void la_sync() { asm volatile("barrier.cta.sync 1, %0;" ::"n"(32 * kLaWork) : "memory"); }
 __device__ __forceinline__ float la_redux_max(float x) {
     float r;
     asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
@@ -520,23 +520,23 @@ __global__ void __launch_bounds__(kLaThreads, 1)
             // step x: tile x restored, then the softmax of tile x - (KS - 1)
 #pragma unroll 1
             for (int x = 0; x < nx + KS - 1; ++x) {
-                // (what follows from the thread's number is formed anew every tile: kept, it
-                // would be spilled)
+                // (what follows from the thread's number is formed anew every tile, under names
+                // of its own: kept, it would be spilled)
                 int th = threadIdx.x;
                 asm volatile("" : "+r"(th));
-                const int x0 = th >> 7, r0 = CN * x0, tok = th & 127, t0 = tok & ~31, lane = th & 31;
-                const unsigned out = lat_at(x0 * (Units::CW / 8), tok, kLatTok);   // unit 0's place in a tile
+                const int wx = th >> 7, wr = CN * wx, wt = th & 127, w0 = wt & ~31, ln = th & 31;
+                const unsigned out = lat_at(wx * (Units::CW / 8), wt, kLatTok);   // unit 0's place in a tile
                 if (x < nx) {
                     const LaTile lt(kLatTok * (first + x), T, Tq);
                     unsigned char *tile = sC + t.s * TB;
                     Units cur;   // (from L2; on their way while the parts' places are waited for)
                     if (lt.packed)
-                        cur.load(rec + tok * 16 + x0 * (kLatTok * 16), rec + g.off_sz + tok * 4, x0 * Units::CW, __ffs(g.G) - 1);
+                        cur.load(rec + wt * 16 + wx * (kLatTok * 16), rec + g.off_sz + wt * 4, wx * Units::CW, __ffs(g.G) - 1);
                     rec += g.rec_bytes;
 #pragma unroll
                     for (int m = 0; m < NM; ++m) {
                         constexpr int SP = Units::SPAN;
-                        if (SP > 1 && x0 * Units::CW / 128 != m % SP) continue;   // other warps'
+                        if (SP > 1 && wx * Units::CW / 128 != m % SP) continue;   // other warps'
                         if (lt.packed) {
                             // the part's place is free
                             ok = ok && __all_sync(kFull, tiles < KS || mbar_wait_ab(&eC[t.s * NM + m], t.p ^ 1u, abort));
@@ -547,7 +547,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
                             fence_proxy_async();
                             __syncwarp();
                         }
-                        if (ok && lane == 0) mbar_arrive(&bC[t.s * NM + m]);
+                        if (ok && ln == 0) mbar_arrive(&bC[t.s * NM + m]);
                     }
                     ++tiles;
                     t.next(KS);
@@ -555,36 +555,36 @@ __global__ void __launch_bounds__(kLaThreads, 1)
                 const int xs = x - (KS - 1);
                 if (xs < 0) continue;
                 const int b = cnt & 1, key0 = kLatTok * (first + xs);
-                const uint32_t tW = taddr + ((uint32_t)t0 << 16) + r0, tS = tW + RN * b;
-                const uint32_t tO = tW + OC, tL = tO + RN * NM;
+                const uint32_t tW = taddr + ((uint32_t)w0 << 16) + wr, wS = tW + RN * b;
+                const uint32_t wO = tW + OC, wL = wO + RN * NM;
                 // the sums so far, and with this tile (kept apart until the tile stands)
-                const uint32_t tL0 = tL + RN * (xs & 1), tL1 = tL + RN * (~xs & 1);
+                const uint32_t tL0 = wL + RN * (xs & 1), tL1 = wL + RN * (~xs & 1);
                 // rows c < lim do not see this token: those of a token before it
                 int lim = 0;
                 if (key0 + kLatTok - 1 > p0) {
-                    const int l = (key0 + tok - T) * h - row0 - r0;   // (below 2^24 + 2^16)
+                    const int l = (key0 + wt - T) * h - row0 - wr;   // (below 2^24 + 2^16)
                     lim = l < 0 ? 0 : l > CN ? CN : l;
                 }
-                const unsigned sP = smem_u32(sC + u.s * TB + CB) + lat_at(r0 / 8, tok, kLatTok);   // (the tile's rotary keys are read once S^T is in)
+                const unsigned sP = smem_u32(sC + u.s * TB + CB) + lat_at(wr / 8, wt, kLatTok);   // (the tile's rotary keys are read once S^T is in)
                 ok = ok && __all_sync(kFull, mbar_wait_ab(&bS[b], (unsigned)(cnt >> 1) & 1u, abort));
                 tc_fence_after();
                 float up = INFINITY;   // (the segment's first tile: a raise at once)
-                if (ok && xs > 0) up = la_weights<RN>(tS, tL0, tL1, false, sP, s_ref + r0, sl2, lim);
+                if (ok && xs > 0) up = la_weights<RN>(wS, tL0, tL1, false, sP, s_ref + wr, sl2, lim);
                 if (la_any(!ok || up > kCkLift + kCkLag)) {   // a raise: then this tile's weights anew
                     if (la_any(!ok)) {   // every warp learns whether one has given up
                         ok = false;
                         break;
                     }
-                    la_raise<RN>(tS, sl2, lim, s_ref, s_al, s_red);
+                    la_raise<RN>(wS, sl2, lim, s_ref, s_al, s_red);
                     if (xs > 0) {   // O^T, once that of the last tile is in, and the sums
                         ok = __all_sync(kFull, mbar_wait_ab(&bF[~cnt & 1], (unsigned)((cnt - 1) >> 1) & 1u, abort));
                         if (ok) {
                             tc_fence_after();
-                            la_rescale<RN, NM>(tO, s_al + r0);
-                            la_rescale<RN, 1>(tL0, s_al + r0);
+                            la_rescale<RN, NM>(wO, s_al + wr);
+                            la_rescale<RN, 1>(tL0, s_al + wr);
                         }
                     }
-                    if (ok) la_weights<RN>(tS, tL0, tL1, xs == 0, sP, s_ref + r0, sl2, lim);
+                    if (ok) la_weights<RN>(wS, tL0, tL1, xs == 0, sP, s_ref + wr, sl2, lim);
                     if (la_any(!ok)) {
                         ok = false;
                         break;
@@ -776,8 +776,9 @@ bool kivi_plan_latent(const LatentGeom &g, int h, ChunkArgs &a, int num_sms, Chu
     a.hg_mul = (unsigned)(((1ull << 32) + h - 1) / h);
     a.vis = Visible{0, 0};
     a.tile_blocks = kLatTok / KIVI_KBLK;
-    // Row tiles of 32 where they are hardly more: a tile then takes 0.8 of the time (r =
-    // 512; 128 heads over 32k, in twice the tiles, 238 us for 151) or 0.6 (r = 256).
+    // Row tiles of 32 where they are hardly more: a tile then takes 0.7 to 0.9 of the time
+    // (8 x 16k 4-bit tokens: 32 rows a sequence 43.6 us for 49.9 with r = 512, 24.5 for
+    // 28.2 with 256; 96 rows, three tiles for two, 98 for 87 and 49 for 44).
     long long few = 0, many = 0;   // tiles
     for (int i = 0; i < g.b; ++i) {
         const long long rows = (long long)a.n[i] * h, tiles = (a.T[i] + a.n[i] + kLatTok - 1) / kLatTok;
