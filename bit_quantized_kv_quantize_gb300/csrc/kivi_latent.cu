@@ -107,7 +107,7 @@ __device__ __forceinline__ void lat_quantize(const LatentGeom &g, unsigned char 
 
 template <int CH, int BITS>
 __global__ void __launch_bounds__(32 * kApWarps)
-    latent_append_kernel(LatentGeom g, LatentDev dv, const __half *__restrict__ C, const __half *__restrict__ Kr,
+    latent_append_kernel(LatentGeom g, LatentDev dv, const __half *C, const __half *Kr,
                          const __grid_constant__ LatentTokens a) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int i = blockIdx.y, x = blockIdx.x * kApWarps + warp, n = a.n[i], T = a.T[i];
@@ -145,8 +145,7 @@ __global__ void __launch_bounds__(32 * kApWarps)
 }
 
 // The cache as attention sees it, and new tokens behind it: 8 channels a thread.
-__global__ void latent_rows_kernel(LatentGeom g, LatentDev dv, const __half *__restrict__ Cn, const __half *__restrict__ Krn,
-                                   __half *__restrict__ C, __half *__restrict__ Kr, int stride,
+__global__ void latent_rows_kernel(LatentGeom g, LatentDev dv, const __half *Cn, const __half *Krn, __half *C, __half *Kr, int stride,
                                    const __grid_constant__ LatentTokens a) {
     const int i = blockIdx.y, per = (g.r + kLatRope) / 8;
     const long long e = (long long)blockIdx.x * blockDim.x + threadIdx.x;

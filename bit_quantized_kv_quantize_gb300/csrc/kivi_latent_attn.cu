@@ -118,10 +118,10 @@ struct LaUnits {
     __device__ __forceinline__ void load(const unsigned char *p, const unsigned char *z, int ch, int lgG) {
 #pragma unroll
         for (int k = 0; k < NU; ++k) {
-            w[k] = __ldg(reinterpret_cast<const uint4 *>(p + k * (WX * kLatTok * 16)));
+            w[k] = *reinterpret_cast<const uint4 *>(p + k * (WX * kLatTok * 16));
 #pragma unroll
             for (int q = 0; q < NG; ++q)
-                sz[k][q] = __ldg(reinterpret_cast<const uint32_t *>(z + ((ch + WX * CW * k + 32 * q) >> lgG) * (kLatTok * 4)));
+                sz[k][q] = *reinterpret_cast<const uint32_t *>(z + ((ch + WX * CW * k + 32 * q) >> lgG) * (kLatTok * 4));
         }
     }
 };
@@ -247,8 +247,7 @@ __device__ __forceinline__ float la_weights(uint32_t tS, uint32_t tL0, uint32_t 
 template <int RD, int BITS, int RN>
 __global__ void __launch_bounds__(kLaThreads, 1)
     latent_attn_kernel(const __grid_constant__ LatentGeom g, const __grid_constant__ LatentDev dv,
-                       const __half *__restrict__ Q, const __half *__restrict__ Qr, const __half *__restrict__ Cn,
-                       const __half *__restrict__ Kn, __half *__restrict__ O, const __grid_constant__ CUtensorMap tmC,
+                       const __half *Q, const __half *Qr, const __half *Cn, const __half *Kn, __half *O, const __grid_constant__ CUtensorMap tmC,
                        const __grid_constant__ CUtensorMap tmK, float sl2, const __grid_constant__ ChunkArgs a) {
     extern __shared__ unsigned char raw[];
     unsigned char *const smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
@@ -679,7 +678,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
 // boundary and RB rows, 8 / RB warps a row that take every so-manieth partial):
 // weights 2^(m_k - M), M the largest m.
 template <int RD, int RB>
-__global__ void __launch_bounds__(256) latent_join_kernel(__half *__restrict__ O, const __grid_constant__ ChunkArgs a) {
+__global__ void __launch_bounds__(256) latent_join_kernel(__half *O, const __grid_constant__ ChunkArgs a) {
     constexpr int W = 8 / RB, V = RD / 128;   // warps a row, 16-byte pieces a lane
     __shared__ __align__(16) float s_acc[RB][W][RD];
     __shared__ float s_l[RB][W];
