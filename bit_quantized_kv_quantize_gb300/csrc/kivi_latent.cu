@@ -375,6 +375,7 @@ kivi_status kivi_latent_create(int b, int r, int bits, int G, int R, int max_tok
     g.G = G;
     g.blocks = (max_tokens + kLatTok - 1) / kLatTok;
     g.R = R < g.blocks * kLatTok ? R : g.blocks * kLatTok;   // (a window that holds every token)
+    g.recs = (lat_tq(max_tokens, g.R) + kLatTok - 1) / kLatTok;
     g.ring = (g.R + kLatTok - 1) / kLatTok + 1;   // (a window's tokens and those before them in their first block)
     g.off_sz = kLatTok * r * bits / 8;
     g.rec_bytes = g.off_sz + r / G * kLatTok * 4;
@@ -385,12 +386,13 @@ kivi_status kivi_latent_create(int b, int r, int bits, int G, int R, int max_tok
         return fail_cuda(nullptr, e, "no CUDA device");
     }
     struct Req { void **p; size_t bytes; } reqs[] = {
-        {(void **)&c->dv.rec, (size_t)b * g.blocks * g.rec_bytes},
+        {(void **)&c->dv.rec, (size_t)b * g.recs * g.rec_bytes},
         {(void **)&c->dv.ring, (size_t)b * g.ring * kLatTok * r * 2},
         {(void **)&c->dv.kr, (size_t)b * g.blocks * kLatTok * kLatRope * 2},
         {(void **)&c->dv.status, 4},
     };
     for (auto &q : reqs) {
+        if (q.bytes == 0) continue;   // (no records: a window that holds every token)
         e = cudaMalloc(q.p, q.bytes);
         if (e == cudaSuccess) e = cudaMemset(*q.p, 0, q.bytes);
         if (e != cudaSuccess) break;

@@ -6,10 +6,10 @@
 // fp16 scale and zero each (the value side of the KIVI quantizer); the newest
 // R, [Tq, T), are fp16.  Device memory, tokens in blocks of 128 (an attention
 // tile):
-//   records  [b][blocks]: codes, then scales and zeros.  16-byte words of codes
-//            [r bits / 128][128 tokens]: word x of a token covers channels
-//            (128 / bits) x ..  In each 32-bit word (16-bit half h, field f of
-//            `bits` bits) is the code of channel 2 f + h of the word's 32 /
+//   records  [b][blocks that codes can reach]: codes, then scales and zeros.
+//            16-byte words of codes [r bits / 128][128 tokens]: word x of a token
+//            covers channels (128 / bits) x ..  In each 32-bit word (16-bit half h,
+//            field f of `bits` bits) is the code of channel 2 f + h of the word's 32 /
 //            bits.  Scale and zero, a half2, [r / G][128 tokens].
 //   ring     [b][ring blocks] and rotary keys [b][blocks]: fp16 blocks as an
 //            attention tile holds them (lat_at), so that a block is copied into
@@ -31,6 +31,7 @@ constexpr int kLatHead = 128;   // channels of a head's other keys, and of its v
 struct LatentGeom {
     int b, r, bits, G, R;
     int blocks;      // of a sequence
+    int recs;        // its records: blocks up to the last that can hold a quantized token
     int ring;        // blocks of its ring
     int off_sz;      // scales and zeros in a record (bytes)
     int rec_bytes;
@@ -42,7 +43,7 @@ struct LatentDev {
 };
 
 __host__ __device__ __forceinline__ size_t lat_rec(const LatentGeom &g, int i, int kb) {
-    return ((size_t)i * g.blocks + kb) * g.rec_bytes;
+    return ((size_t)i * g.recs + kb) * g.rec_bytes;
 }
 // a block of the ring, of the rotary keys (halves)
 __host__ __device__ __forceinline__ size_t lat_ring(const LatentGeom &g, int i, int kb) {
