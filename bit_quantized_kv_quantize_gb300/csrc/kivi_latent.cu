@@ -299,25 +299,25 @@ void free_latent(kivi_latent *c) {
         if (p) cudaFree(p);
 }
 
-// kivi_latent_append and kivi_latent_prefill (T: the counts before it)
-kivi_status put(kivi_latent *c, const void *C, const void *Kr, const int32_t *n, int n_stride, const std::vector<int> &T,
-                const char *what, cudaStream_t st) {
+// kivi_latent_append, and kivi_latent_prefill (anew: every sequence is empty before it)
+kivi_status put(kivi_latent *c, const void *C, const void *Kr, const int32_t *n, int n_stride, bool anew, const char *what,
+                cudaStream_t st) {
     int maxn = 0;
     kivi_status s = check_tokens(c->g.b, C, Kr, n, n_stride, &maxn);
     if (s != KIVI_OK) return s;
     LatentTokens a;
     a.n_stride = n_stride;
     for (int i = 0; i < c->g.b; ++i) {
-        if (n[i] > c->max_tokens - T[i]) return fail(KIVI_ERR_CAPACITY, "sequence %ld would exceed max_tokens", i);
-        a.T[i] = T[i];
+        a.T[i] = anew ? 0 : c->T[i];
         a.n[i] = n[i];
+        if (n[i] > c->max_tokens - a.T[i]) return fail(KIVI_ERR_CAPACITY, "sequence %ld would exceed max_tokens", i);
     }
     if (maxn > 0) {
         const cudaError_t e =
             kivi_launch_latent_append(c->g, c->dv, (const __half *)C, (const __half *)Kr, a, st);
         if (e != cudaSuccess) return fail_cuda(c, e, what);
     }
-    for (int i = 0; i < c->g.b; ++i) c->T[i] = T[i] + n[i];
+    for (int i = 0; i < c->g.b; ++i) c->T[i] = a.T[i] + n[i];
     return KIVI_OK;
 }
 
@@ -405,9 +405,13 @@ kivi_status kivi_latent_create(int b, int r, int bits, int G, int R, int max_tok
         fail_cuda(nullptr, e, "device allocation failed");
         return e == cudaErrorMemoryAllocation ? KIVI_ERR_OOM : KIVI_ERR_CUDA;
     }
-    {
+    try {
         std::lock_guard<std::mutex> lk(g_mu);
         g_handles.insert(c);
+    } catch (...) {
+        free_latent(c);
+        delete c;
+        return fail(KIVI_ERR_OOM, "host allocation failed");
     }
     *out = c;
     return KIVI_OK;
@@ -432,7 +436,7 @@ kivi_status kivi_latent_prefill(kivi_latent_t c, const void *C, const void *Kr, 
     kivi_set_last_error("");
     kivi_status s = check(c, true);
     if (s != KIVI_OK) return s;
-    return put(c, C, Kr, t, t_stride, std::vector<int>(c->T.size(), 0), "latent_prefill", (cudaStream_t)stream);
+    return put(c, C, Kr, t, t_stride, true, "latent_prefill", (cudaStream_t)stream);
 }
 
 kivi_status kivi_latent_append(kivi_latent_t c, const void *C, const void *Kr, const int32_t *n, int n_stride,
@@ -440,7 +444,7 @@ kivi_status kivi_latent_append(kivi_latent_t c, const void *C, const void *Kr, c
     kivi_set_last_error("");
     kivi_status s = check(c, true);
     if (s != KIVI_OK) return s;
-    return put(c, C, Kr, n, n_stride, c->T, "latent_append", (cudaStream_t)stream);
+    return put(c, C, Kr, n, n_stride, false, "latent_append", (cudaStream_t)stream);
 }
 
 kivi_status kivi_latent_attn(kivi_latent_t c, const void *q, const void *q_rope, const void *C, const void *Kr,
