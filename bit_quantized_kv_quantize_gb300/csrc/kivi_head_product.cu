@@ -221,8 +221,9 @@ __host__ __device__ constexpr size_t hs_smem(int C, int K) {
 }
 
 // The rows of all heads alike: CTA (row tile, group) makes tiles [per y, per (y +
-// 1)) of all heads' columns, 128 C a tile.  (128 make an MMA's operands 8 KB for 32
-// cycles' work, 256 12 KB for 64.)  Warps as above.
+// 1)) of all heads' columns, 128 C a tile.  (Of 128 columns an MMA reads 8 KB of
+// operands, 64 cycles of shared memory's bandwidth, for 64 cycles of work; of 256 12
+// KB, 96 cycles, for 128.)  Warps as above.
 template <int C>
 __global__ void __launch_bounds__(kHpThreads, 1)
     head_product_shared_kernel(const __grid_constant__ HeadArgs a, const __grid_constant__ CUtensorMap tm, int per) {

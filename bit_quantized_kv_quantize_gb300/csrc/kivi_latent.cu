@@ -23,10 +23,11 @@ __device__ unsigned g_status;   // of the calls without a handle
 // otherwise.  Where a block is begun, its places behind the last token are set to zero
 // (kivi_latent_places.h).
 //
-// Bound: memory (2 r + 128 bytes read a token, its codes or 16-bit rows
-// written), for single tokens the latency of one round trip.  r = 512, 4 bits, R =
-// 128, in a captured graph: a token of 64 sequences 3.1 us (3.9 where every one begins a
-// block), 1024 tokens 3.5, a fill of 4096 5.1, of 8 x 32767 180 (2.3 TB/s).
+// Bound: of single tokens the latency of one round trip, of long fills instructions
+// (quantizing r values a token: issue 76 %, HBM 27 %; 2 r + 128 bytes are read a token,
+// its codes or 16-bit rows written).  r = 512, 4 bits, R = 128, in a captured graph: a
+// token of 64 sequences 3.1 us (3.9 where every one begins a block), 1024 tokens 3.5, a
+// fill of 4096 5.1, of 8 x 32767 180 (2.3 TB/s).
 // ---------------------------------------------------------------------------
 constexpr int kApWarps = 4;
 

@@ -13,7 +13,10 @@
 // floor(2^30 u).  Sums of whole numbers do not depend on their order, so the
 // split over threads and CTAs does not show in the result.
 //
-// Bound: memory, two rows of the vocabulary a sequence, then latency.  A
+// Bound: latency, for all that two rows of the vocabulary a sequence have to come from
+// memory: draft -> its probabilities -> the row, 8 values a lane at a time, each time
+// waiting for the last (64 x 32000: 2, 16 x 150001: 5) -> the cluster's sums -> the
+// stretch again.  A
 // cluster of CTAs shares a sequence: each warp sums a stretch of the row (the
 // units are never stored), the CTAs exchange their warps' sums through
 // distributed shared memory, and the CTA whose stretch holds the mark reads
