@@ -342,7 +342,8 @@ kivi_status kivi_latent_expanded(kivi_latent_t c, const void *q, const void *q_r
                                  float scale, void *out, kivi_stream_t stream);
 
 /* As kivi_cache_check, for the current device's calls that have no handle
- * (kivi_head_product, kivi_latent_prompt_attn, kivi_latent_expanded_attn). */
+ * (kivi_head_product, kivi_latent_prompt_attn, kivi_latent_expanded_attn): one word
+ * for all streams and threads, cleared by the call that reads it. */
 kivi_status kivi_device_check(uint32_t *flags, kivi_stream_t stream);
 
 /* Append one token to every sequence: k and v fp16 [b][h_kv][d] (device).
